@@ -245,6 +245,138 @@ const char* moe_strerror(moe_status s);
 moe_status moe_route_noalloc(const uint16_t* x_bf16, const float* W, int T, int H, int E, int k, int router,
                              int* idx, float* w, void* stream);
 
+/* ---------------------------------------------------------------- a batch of tokens in 16-bit weights
+ * The routed layer's parts as calls of their own, for a batch of tokens (a prompt, the verify
+ * pass of drafted tokens, a training step) and experts kept in bf16 or fp16: the router's
+ * selection with the rows grouped by expert, the products of those ragged groups with their
+ * experts' weights and the products' gradients, and the verification of drafted tokens
+ * ("WISP - streaming what can't run", section "Speculative decoding": several drafted
+ * tokens are verified in one parallel forward).
+ *
+ * Shared by these calls: no context; device pointers, on the current device; `stream` as
+ * everywhere; nothing is allocated, nothing blocks the host, every call can be recorded
+ * into a CUDA graph.  The first call on a device sets that device up (kernel attributes):
+ * make it before any stream capture.  Calls on different streams or threads are
+ * independent as long as their outputs and workspaces are.  Sizes, types and pointers are
+ * checked on the host (MOE_EINVAL); what stands in device memory (offsets, row numbers,
+ * lengths, token ids) cannot be, so the kernels check it: each call says what a bad value
+ * does, and none reads or writes outside the arrays.  A device wait that runs out makes
+ * the next call on that device return MOE_ETIMEOUT (sticky).
+ * Same inputs, same bits: no atomics order a sum. */
+typedef enum { MOE_T_BF16 = 0, MOE_T_FP16 = 1, MOE_T_FP32 = 2 } moe_dtype;
+typedef enum {
+    MOE_GROUP_NK = 0,   /* expert weights [n][k]: k (the contracted dimension) contiguous */
+    MOE_GROUP_KN = 1    /* expert weights [k][n]: n contiguous */
+} moe_group_layout;
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_group_act;
+
+/* Router selection of T tokens from their logits, and the selected (token, rank) pairs
+ * grouped by expert.  logits [T][E] of `dtype` (any moe_dtype), token rows ld elements
+ * apart (ld >= E).  Per token the k largest logits (equal ones: the lower expert id
+ * first; NaN counts as -inf, +inf as the largest finite float) and their weights as the
+ * layer's router defines them (moe_router; sigmoid weights are formed from log sigmoid, so
+ * scores that would all underflow still give weights that sum to 1).  A logit of -inf
+ * masks: it is never selected, so a token with fewer than k others has idx -1 and weight 0 in
+ * the ranks left, and a token masked whole (padding) has only those.
+ *   idx [T][k] int32, weights [T][k] fp32: the selection in rank order;
+ *   offsets [E+1] int32: expert e's pairs stand at [offsets[e], offsets[e+1]);
+ *   pairs [T k] int32: the pair ids t k + j, by expert, ascending within one;
+ *   rows [T k] int32: their tokens t;  both -1 from offsets[E] on.
+ * idx, offsets, rows and pairs feed moe_grouped_matmul.  E 1..1024, k 1..min(E, 32), T >= 1 and
+ * T k < 2^31.  workspace: moe_group_route_workspace(T, E, k) bytes of device memory, 16-byte
+ * aligned (NULL where that is 0); calls that can overlap, replays of graphs among them, need one each. */
+moe_status moe_group_route(const void* logits, long long ld, int dtype, int T, int E, int k, int router, int* idx,
+                           float* weights, int* offsets, int* rows, int* pairs, void* workspace,
+                           size_t workspace_bytes, void* stream);
+size_t moe_group_route_workspace(int T, int E, int k);
+
+/* out row of i = act(W_e x_i) for every sorted row i of [offsets[e], offsets[e+1]), e < groups.
+ *   x [x_rows][k] bf16 or fp16, rows ldx apart; row i reads x row rows[i], or x row i with
+ *   rows NULL (then m <= x_rows);
+ *   w [groups] matrices of the same type, w_stride elements apart, rows ldw apart:
+ *   [n][k] (MOE_GROUP_NK) or [k][n] (MOE_GROUP_KN);
+ *   out [out_rows_n][n_out] bf16, fp16 or fp32 (out_dtype), rows ldo apart; row i is written to
+ *   out row out_rows[i], or i with out_rows NULL (then m <= out_rows_n).
+ * MOE_ACT_SWIGLU (MOE_GROUP_NK only, n even): W_e's first n/2 rows are gate, the others up,
+ * out = silu(gate x) * (up x), n_out = n/2; otherwise n_out = n.
+ * The inputs' gradient of a product is the same call with the other layout:
+ * dx = grouped(dy, w as [k'][n']), n' = k, k' = n.
+ * offsets [groups + 1] int32, non-decreasing, offsets[0] >= 0, offsets[groups] <= m: groups may be empty, and
+ * out rows that no sorted row writes are left as they were.  Offsets outside [0, m] are taken
+ * as the nearer end and a group that ends before it starts as empty; a rows[i] outside [0, x_rows) is a row
+ * of zeros; an out_rows[i] outside [0, out_rows_n) writes nothing.  Two sorted rows must not name one
+ * out row.  groups 1..1024; m 0..2^30 (0: nothing to do); n, k 1..2^24.  Any strides that keep
+ * rows apart (ldx >= k, ldw >= the row's length, ldo >= n_out; w_stride any) and any
+ * 2-byte (fp32: 4-byte) alignment; pointers and strides of x and w that are multiples of 16 bytes
+ * (and for SwiGLU n/2 a multiple of 16) take the fast kernels.
+ * Sums are fp32, rounded once at the store. */
+typedef struct {
+    const void* x;
+    const void* w;
+    const int* offsets;
+    const int* rows;      /* [m] or NULL */
+    const int* out_rows;  /* [m] or NULL */
+    void* out;
+    long long x_rows, ldx, ldw, w_stride, out_rows_n, ldo;
+    long long m;          /* sorted rows that offsets may name */
+    int groups, n, k;
+    int dtype, out_dtype; /* moe_dtype */
+    int layout;           /* moe_group_layout */
+    int act;              /* moe_group_act */
+} moe_grouped_args;
+moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream);
+
+/* dw[e][n][k] = sum over the sorted rows i of expert e of dy_i[n] x_i[k]: the weights' gradient
+ * of moe_grouped_matmul (MOE_GROUP_NK; for MOE_GROUP_KN exchange dy and x).  Every element of dw is written,
+ * zeros where a group is empty.
+ *   dy [dy_rows_n][n] and x [x_rows_n][k] bf16 or fp16, rows lddy and ldx apart; row i reads
+ *   dy row dy_rows[i] and x row x_rows[i], or row i where that is NULL;
+ *   dw [groups] matrices [n][k] bf16, fp16 or fp32, dw_stride elements apart, rows lddw apart.
+ * Offsets, row numbers, limits and alignment as moe_grouped_matmul; with m = 0 (dy and x may be
+ * NULL then) dw is all zeros. */
+typedef struct {
+    const void* dy;
+    const void* x;
+    const int* offsets;
+    const int* dy_rows;   /* [m] or NULL */
+    const int* x_rows;    /* [m] or NULL */
+    void* dw;
+    long long dy_rows_n, lddy, x_rows_n, ldx, lddw, dw_stride;
+    long long m;
+    int groups, n, k;
+    int dtype, out_dtype;
+} moe_grouped_wgrad_args;
+moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* stream);
+
+/* Which of a sequence's drafted tokens stand, and the token after them, so that what comes
+ * out is distributed as the target's own samples.  For sequence b with L = lengths[b] drafts
+ * (lengths NULL: D):
+ *   draft i < L with token t stands iff u[b][i] q[b][i][t] < p[b][i][t] and every draft before it does;
+ *   accepted[b] = r, the number that stand;
+ *   the next token is drawn from the weights max(p[b][r] - q[b][r], 0) if r < L (a draft was
+ *   rejected), else p[b][L]: the least v whose running sum exceeds u[b][D] times the total;
+ *   tokens[b] = the r drafts, the drawn token, then -1 up to D + 1 entries.
+ * p [B][D+1][V], q [B][D][V]: probabilities of `dtype` (any moe_dtype), each row summing to about one (8 at
+ * most); rows p_row / q_row and sequences p_seq / q_seq elements apart.  q NULL: the drafts came
+ * without probabilities (one-hot).  Probabilities and u (meant in [0, 1)) are read as clamped to [0, 1],
+ * NaN as 0; u = 1 draws the last v that has any weight.  Products and sums are exact (running sums in 2^-60 steps), so the
+ * order of summation decides nothing.  Where the residual is all zero the token is drawn from
+ * p[b][r]; where that is too, it is -1.  lengths outside [0, D] are taken as the nearer end; a token
+ * outside [0, V) is rejected.  draft [B][D] int32, u [B][D+1] fp32, tokens [B][D+1] int32, all
+ * contiguous; rows and drafts past a sequence's length are not read.  B >= 1, D 0..31, V 1..2^30. */
+typedef struct {
+    const void* p;
+    const void* q;        /* NULL: one-hot drafts */
+    const int* draft;     /* may be NULL with D = 0 */
+    const int* lengths;   /* [B] or NULL */
+    const float* u;
+    int* accepted;
+    int* tokens;
+    long long p_seq, p_row, q_seq, q_row;
+    int B, D, V, dtype;
+} moe_verify_args;
+moe_status moe_verify_draft(const moe_verify_args* a, void* stream);
+
 /* ---- measurement (no counterpart in the pages) ---- */
 
 /* Per-kernel timing: when enabled, moe_forward records CUDA events (timing enabled) on its

@@ -1,0 +1,142 @@
+// batch.cu - entry points of the batch operators (moe_group_route, moe_grouped_matmul,
+// moe_grouped_wgrad, moe_verify_draft): argument checks, then one launcher each.
+#include "../../include/moe.h"
+#include "group_route.h"
+#include "grouped.h"
+#include "verify.h"
+
+namespace {
+
+bool is_dtype(int t, bool fp32) { return t == MOE_T_BF16 || t == MOE_T_FP16 || (fp32 && t == MOE_T_FP32); }
+size_t dtype_bytes(int t) { return t == MOE_T_FP32 ? 4 : 2; }
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// rows of `len` elements `ld` apart; at most 2^24 long, and `rows` of them within 2^62 bytes
+bool rows_fit(long long rows, long long ld, long long len) {
+  return rows >= 0 && ld >= len && ld < (1ll << 40) && (rows == 0 || ld <= (1ll << 60) / rows);
+}
+
+moe_status done(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return MOE_ECUDA;
+}
+
+constexpr long long kMaxRows = 1ll << 30;
+constexpr int kMaxDim = 1 << 24;
+
+bool product_ok(int groups, long long m, int n, int k, int dtype, int out_dtype) {
+  return groups >= 1 && groups <= 1024 && m >= 0 && m <= kMaxRows && n >= 1 && n <= kMaxDim && k >= 1 && k <= kMaxDim &&
+         is_dtype(dtype, false) && is_dtype(out_dtype, true);
+}
+
+}  // namespace
+
+extern "C" size_t moe_group_route_workspace(int T, int E, int k) {
+  if (T < 1 || E < 1 || E > 1024 || k < 1 || k > E || k > 32 || (long long)T * k > 0x7fffffffLL) return 0;
+  return moe::group_route_plan(T, E, k).workspace;
+}
+
+extern "C" moe_status moe_group_route(const void* logits, long long ld, int dtype, int T, int E, int k, int router,
+                                      int* idx, float* weights, int* offsets, int* rows, int* pairs, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  if (!logits || !idx || !weights || !offsets || !rows || !pairs) return MOE_EINVAL;
+  if (!is_dtype(dtype, true) || T < 1 || E < 1 || E > 1024 || k < 1 || k > E || k > 32) return MOE_EINVAL;
+  if ((long long)T * k > 0x7fffffffLL || !rows_fit(T, ld, E)) return MOE_EINVAL;
+  if (router != MOE_ROUTER_SOFTMAX_TOPK_RENORM && router != MOE_ROUTER_SIGMOID_TOPK_NORM) return MOE_EINVAL;
+  if (!aligned(logits, dtype_bytes(dtype)) || !aligned(idx, 4) || !aligned(weights, 4) || !aligned(offsets, 4) ||
+      !aligned(rows, 4) || !aligned(pairs, 4) || !aligned(workspace, 16))
+    return MOE_EINVAL;
+  const moe::GroupRoutePlan plan = moe::group_route_plan(T, E, k);
+  if (plan.workspace && (!workspace || workspace_bytes < plan.workspace)) return MOE_EINVAL;
+  moe::GroupRouteArgs a{logits, ld, dtype, T, E, k, router, idx, weights, offsets, rows, pairs,
+                        static_cast<int*>(workspace), plan.blocks, plan.per_block};
+  return done(moe::launch_group_route(a, (cudaStream_t)stream));
+}
+
+extern "C" moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream) {
+  if (!a || !a->x || !a->w || !a->offsets || !a->out) return MOE_EINVAL;
+  if (!product_ok(a->groups, a->m, a->n, a->k, a->dtype, a->out_dtype)) return MOE_EINVAL;
+  if (a->layout != MOE_GROUP_NK && a->layout != MOE_GROUP_KN) return MOE_EINVAL;
+  if (a->act != MOE_ACT_NONE && a->act != MOE_ACT_SWIGLU) return MOE_EINVAL;
+  const bool sw = a->act == MOE_ACT_SWIGLU, kn = a->layout == MOE_GROUP_KN;
+  if (sw && (kn || a->n % 2)) return MOE_EINVAL;
+  if (!rows_fit(a->x_rows, a->ldx, a->k) || !rows_fit(kn ? a->k : a->n, a->ldw, kn ? a->n : a->k) ||
+      !rows_fit(a->out_rows_n, a->ldo, sw ? a->n / 2 : a->n) || a->w_stride < 0 || a->w_stride >= (1ll << 50))
+    return MOE_EINVAL;
+  if ((!a->rows && a->m > a->x_rows) || (!a->out_rows && a->m > a->out_rows_n)) return MOE_EINVAL;
+  if (!aligned(a->x, 2) || !aligned(a->w, 2) || !aligned(a->out, dtype_bytes(a->out_dtype)) || !aligned(a->offsets, 4) ||
+      !aligned(a->rows, 4) || !aligned(a->out_rows, 4))
+    return MOE_EINVAL;
+  if (a->m == 0) return MOE_OK;
+  moe::GroupedProblem p{};
+  p.a = static_cast<const uint16_t*>(a->x);
+  p.b = static_cast<const uint16_t*>(a->w);
+  p.d = a->out;
+  p.offsets = a->offsets;
+  p.a_rows = a->rows;
+  p.d_rows = a->out_rows;
+  p.a_nrows = a->x_rows;
+  p.lda = a->ldx;
+  p.ldb = a->ldw;
+  p.b_stride = a->w_stride;
+  p.d_nrows = a->out_rows_n;
+  p.ldd = a->ldo;
+  p.m = a->m;
+  p.groups = a->groups;
+  p.n = a->n;
+  p.k = a->k;
+  p.dtype = a->dtype;
+  p.out_dtype = a->out_dtype;
+  p.kn = kn;
+  p.swiglu = sw;
+  return done(moe::launch_grouped_any(p, false, (cudaStream_t)stream));
+}
+
+extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* stream) {
+  if (!a || !a->offsets || !a->dw || (a->m != 0 && (!a->dy || !a->x))) return MOE_EINVAL;
+  if (!product_ok(a->groups, a->m, a->n, a->k, a->dtype, a->out_dtype)) return MOE_EINVAL;
+  if (!rows_fit(a->dy_rows_n, a->lddy, a->n) || !rows_fit(a->x_rows_n, a->ldx, a->k) || !rows_fit(a->n, a->lddw, a->k) ||
+      a->dw_stride < (a->n - 1) * a->lddw + a->k || a->dw_stride >= (1ll << 50))
+    return MOE_EINVAL;
+  if ((!a->dy_rows && a->m > a->dy_rows_n) || (!a->x_rows && a->m > a->x_rows_n)) return MOE_EINVAL;
+  if (!aligned(a->dy, 2) || !aligned(a->x, 2) || !aligned(a->dw, dtype_bytes(a->out_dtype)) || !aligned(a->offsets, 4) ||
+      !aligned(a->dy_rows, 4) || !aligned(a->x_rows, 4))
+    return MOE_EINVAL;
+  moe::GroupedProblem p{};
+  p.a = static_cast<const uint16_t*>(a->dy);
+  p.b = static_cast<const uint16_t*>(a->x);
+  p.d = a->dw;
+  p.offsets = a->offsets;
+  p.a_rows = a->dy_rows;
+  p.b_rows = a->x_rows;
+  p.a_nrows = a->dy_rows_n;
+  p.lda = a->lddy;
+  p.b_nrows = a->x_rows_n;
+  p.ldb = a->ldx;
+  p.ldd = a->lddw;
+  p.d_stride = a->dw_stride;
+  p.m = a->m;
+  p.groups = a->groups;
+  p.n = a->n;
+  p.k = a->k;
+  p.dtype = a->dtype;
+  p.out_dtype = a->out_dtype;
+  return done(moe::launch_grouped_any(p, true, (cudaStream_t)stream));
+}
+
+extern "C" moe_status moe_verify_draft(const moe_verify_args* a, void* stream) {
+  if (!a || !a->p || !a->u || !a->accepted || !a->tokens) return MOE_EINVAL;
+  if (a->B < 1 || a->D < 0 || a->D > 31 || (a->D && !a->draft) || a->V < 1 || a->V > (1 << 30) || !is_dtype(a->dtype, true))
+    return MOE_EINVAL;
+  if (!rows_fit(a->D + 1, a->p_row, a->V) || !rows_fit(a->B, a->p_seq, a->D * a->p_row + a->V)) return MOE_EINVAL;
+  if (a->q && a->D && (!rows_fit(a->D, a->q_row, a->V) || !rows_fit(a->B, a->q_seq, (a->D - 1) * a->q_row + a->V)))
+    return MOE_EINVAL;
+  const size_t el = dtype_bytes(a->dtype);
+  if (!aligned(a->p, el) || !aligned(a->q, el) || !aligned(a->draft, 4) || !aligned(a->lengths, 4) || !aligned(a->u, 4) ||
+      !aligned(a->accepted, 4) || !aligned(a->tokens, 4))
+    return MOE_EINVAL;
+  moe::VerifyArgs v{a->p, a->q, a->draft, a->lengths, a->u, a->accepted, a->tokens,
+                    a->p_seq, a->p_row, a->q_seq, a->q_row, a->B, a->D, a->V, a->dtype};
+  return done(moe::launch_verify(v, (cudaStream_t)stream));
+}
