@@ -5,7 +5,58 @@
 #include "grouped.h"
 #include "verify.h"
 
+#include <atomic>
+#include <mutex>
+#include <new>
+
 namespace {
+
+// What a device needs once: kernel attributes, its SM count, and the host-visible word that a kernel whose wait ran
+// out sets.  Made by the first call on the device, kept for the life of the process.
+struct Device {
+  int num_sms;
+  uint32_t* status;
+};
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+std::atomic<Device*> g_device[kMaxDevices];
+
+moe_status device_setup(int dev, Device** out) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if ((*out = g_device[dev].load())) return MOE_OK;
+  Device d{0, nullptr};
+  void* word = nullptr;
+  if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      moe::grouped_pair_set_attributes() != cudaSuccess ||
+      cudaHostAlloc(&word, sizeof(uint32_t), cudaHostAllocMapped | cudaHostAllocPortable) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ECUDA;
+  }
+  d.status = static_cast<uint32_t*>(word);   // unified addressing: the same address on the device
+  *d.status = 0;
+  *out = new (std::nothrow) Device(d);
+  if (!*out) {
+    cudaFreeHost(word);
+    return MOE_ENOMEM;
+  }
+  g_device[dev].store(*out);
+  return MOE_OK;
+}
+
+// the current device, set up; MOE_ETIMEOUT once a wait ran out there
+moe_status current_device(Device** out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return MOE_ECUDA;
+  }
+  *out = g_device[dev].load(std::memory_order_acquire);
+  if (!*out) {
+    const moe_status st = device_setup(dev, out);
+    if (st != MOE_OK) return st;
+  }
+  return *static_cast<volatile uint32_t*>((*out)->status) ? MOE_ETIMEOUT : MOE_OK;
+}
 
 bool is_dtype(int t, bool fp32) { return t == MOE_T_BF16 || t == MOE_T_FP16 || (fp32 && t == MOE_T_FP32); }
 size_t dtype_bytes(int t) { return t == MOE_T_FP32 ? 4 : 2; }
@@ -30,6 +81,16 @@ bool product_ok(int groups, long long m, int n, int k, int dtype, int out_dtype)
          is_dtype(dtype, false) && is_dtype(out_dtype, true);
 }
 
+// The kernel of a product, by what the operands allow: TMA wants 16-byte aligned addresses and strides.
+moe_status run_product(const moe::GroupedProblem& p, bool wgrad, cudaStream_t s) {
+  Device* d;
+  const moe_status st = current_device(&d);
+  if (st != MOE_OK) return st;
+  cudaError_t e = cudaSuccess;
+  if (p.m > 0 && moe::launch_grouped_pair(p, wgrad, d->num_sms, d->status, s, &e)) return done(e);
+  return done(moe::launch_grouped_any(p, wgrad, s));
+}
+
 }  // namespace
 
 extern "C" size_t moe_group_route_workspace(int T, int E, int k) {
@@ -51,6 +112,9 @@ extern "C" moe_status moe_group_route(const void* logits, long long ld, int dtyp
   if (plan.workspace && (!workspace || workspace_bytes < plan.workspace)) return MOE_EINVAL;
   moe::GroupRouteArgs a{logits, ld, dtype, T, E, k, router, idx, weights, offsets, rows, pairs,
                         static_cast<int*>(workspace), plan.blocks, plan.per_block};
+  Device* d;
+  const moe_status st = current_device(&d);
+  if (st != MOE_OK) return st;
   return done(moe::launch_group_route(a, (cudaStream_t)stream));
 }
 
@@ -90,7 +154,7 @@ extern "C" moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream
   p.out_dtype = a->out_dtype;
   p.kn = kn;
   p.swiglu = sw;
-  return done(moe::launch_grouped_any(p, false, (cudaStream_t)stream));
+  return run_product(p, false, (cudaStream_t)stream);
 }
 
 extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* stream) {
@@ -122,7 +186,7 @@ extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* s
   p.k = a->k;
   p.dtype = a->dtype;
   p.out_dtype = a->out_dtype;
-  return done(moe::launch_grouped_any(p, true, (cudaStream_t)stream));
+  return run_product(p, true, (cudaStream_t)stream);
 }
 
 extern "C" moe_status moe_verify_draft(const moe_verify_args* a, void* stream) {
@@ -138,5 +202,8 @@ extern "C" moe_status moe_verify_draft(const moe_verify_args* a, void* stream) {
     return MOE_EINVAL;
   moe::VerifyArgs v{a->p, a->q, a->draft, a->lengths, a->u, a->accepted, a->tokens,
                     a->p_seq, a->p_row, a->q_seq, a->q_row, a->B, a->D, a->V, a->dtype};
+  Device* d;
+  const moe_status st = current_device(&d);
+  if (st != MOE_OK) return st;
   return done(moe::launch_verify(v, (cudaStream_t)stream));
 }

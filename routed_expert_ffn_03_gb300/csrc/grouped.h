@@ -1,5 +1,6 @@
 // grouped.h - device arguments and launchers of the 16-bit grouped products (internal).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -29,6 +30,7 @@ struct GroupedProblem {
   int swiglu;
 };
 
+#ifdef __CUDACC__
 // Row range of group g, with offsets outside [0, m] taken as the nearer end and an end
 // before its start as an empty group.
 __device__ __forceinline__ void group_range(const int* offsets, int g, long long m, int& r0, int& r1) {
@@ -36,7 +38,23 @@ __device__ __forceinline__ void group_range(const int* offsets, int g, long long
   r0 = min(max(__ldg(offsets + g), 0), hi);
   r1 = min(max(__ldg(offsets + g + 1), r0), hi);
 }
+#endif
 
 cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, cudaStream_t s);
+
+// A tensor map over 16-bit elements, 128-byte swizzled, zeros outside: dims and box in elements, innermost
+// first; strides (of dims 1 ..) in bytes.  False where the hardware cannot address the tensor so (a base, stride or
+// size it does not take).
+bool tensor_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box);
+// The maps of a product: [0] the first factor in tiles (forward: w_rows rows of W_e), [1] the second (forward: tile_rows
+// rows of x), [2], [3] both row by row.  False where TMA cannot take the operands as they lie.
+bool grouped_maps(const GroupedProblem& p, bool wgrad, int tile_rows, int w_rows, CUtensorMap (&m)[4]);
+
+// The tensor-core kernel over pairs of SMs; false (nothing launched) where TMA cannot take the operands.
+// status: host-visible word that a wait which ran out sets.
+bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, uint32_t* status, cudaStream_t s,
+                         cudaError_t* err);
+cudaError_t grouped_pair_set_attributes();
 
 }  // namespace moe

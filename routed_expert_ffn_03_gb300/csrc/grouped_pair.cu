@@ -1,0 +1,528 @@
+// grouped_pair.cu - grouped 16-bit products on the tensor cores, one tile per pair of SMs.
+//
+//   forward:          D^T[f][t] = sum_k W_e[f][k] x[t][k]      f: 256 features, t: up to 256 of a group's rows
+//   weight gradient:  dW_e[n][k] = sum_i dy[i][n] x[i][k]      n: 256, k: 256, i: a group's rows
+//
+// Both are one tcgen05 product of a pair of blocks (cta_group::2, M = 256): each block stages its
+// 128 rows of the first factor and its half of the second in shared memory, and holds its
+// 128 rows of the result in tensor memory.  The weights are the first factor of the forward
+// product, so that a group's rows are the N of the instruction, which takes any multiple
+// of 32: a group of 40 rows costs 64 columns and not a tile of 128 or 256 (with the rows as M it would).
+// The pair halves what each SM fetches: 64 contracted elements take 32 KB for 512
+// tensor cycles, where single blocks of 128 x 256 would take 48 KB, more than L2 delivers.
+//
+// Persistent pairs walk the tiles; the warps of a block have fixed roles:
+//   warp 0      copies operands by TMA into a ring of 6 stages (64 contracted elements each);
+//   warp 1      of the first block issues the products for both;
+//   warps 2..9  read finished results from tensor memory and store them, while the next
+//               tile's products run into the other half of the 512 columns.
+// Tiles of a group go rows first within bands of 8 row tiles, so the pairs at work share
+// weights and rows in L2.  Rows are copied as tiles where they are consecutive, and row by row (gather) where
+// row numbers are given or a group of the weight gradient ends inside a step: rows
+// outside the group are then zeros in both factors, so nothing of a neighbour enters a sum.
+#include <cstring>
+
+#include "grouped.h"
+#include "grouped_mma.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int GP_STAGES = 6;
+constexpr int GP_OP = 128 * 128;                 // bytes of one factor's half stage: 128 rows x 64 elements
+constexpr int GP_STAGE = 2 * GP_OP;
+constexpr int GP_EPI_WARPS = 8;
+constexpr int GP_THREADS = (2 + GP_EPI_WARPS) * 32;
+constexpr int GP_MAX_GROUPS = 1024;
+constexpr int GP_BAND = 8;                       // row tiles of a band
+constexpr int GP_OFF_BAR = GP_STAGES * GP_STAGE;
+constexpr int GP_OFF_TAB = GP_OFF_BAR + 256;     // first tile of each group [groups + 1]
+constexpr int GP_OFF_SCAN = GP_OFF_TAB + (GP_MAX_GROUPS + 1) * 4 + 12;
+constexpr int GP_SMEM = GP_OFF_SCAN + 64 + 1024; // and 1024 to align the stages
+
+enum : int { GP_NK = 0, GP_KN = 1, GP_SWIGLU = 2, GP_WGRAD = 3 };
+
+struct PairArgs {
+  GroupedProblem p;
+  int nft, nkt;        // forward: feature tiles; weight gradient: n tiles and k tiles
+  uint32_t* status;
+  bool wide;           // results can be stored in words: 4-byte pairs (forward), 16 bytes (weight gradient)
+};
+
+struct Tile {
+  int e, f0;           // group; first feature (forward), first n (weight gradient)
+  int r0, rows;        // forward: the tile's rows; weight gradient: the group's rows
+  int n;               // columns of the product: rows rounded up to 32, or 256
+  int c0;              // weight gradient: first k
+  int nkb;             // steps of 64
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int t) {
+  if (t == GT_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void store1(void* d, long long at, float v, int t) {
+  if (t == GT_FP32) static_cast<float*>(d)[at] = v;
+  else if (t == GT_BF16) static_cast<__nv_bfloat16*>(d)[at] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(d)[at] = __float2half_rn(v);
+}
+
+// the tile with number `t` (first[g] = first tile of group g)
+template <int MODE>
+__device__ __forceinline__ Tile decode(const PairArgs& a, const int* first, int t) {
+  Tile T;
+  const GroupedProblem& p = a.p;
+  if (MODE == GP_WGRAD) {
+    const int per = a.nft * a.nkt;
+    T.e = t / per;
+    int i = t - T.e * per;
+    const int band = i / (GP_BAND * a.nkt), in = i - band * GP_BAND * a.nkt;
+    const int h = min(GP_BAND, a.nft - band * GP_BAND);
+    T.f0 = (band * GP_BAND + in % h) * 256;
+    T.c0 = in / h * 256;
+    int r1;
+    group_range(p.offsets, T.e, p.m, T.r0, r1);
+    T.rows = r1 - T.r0;
+    T.n = 256;
+    T.nkb = (T.rows + 63) / 64;
+    return T;
+  }
+  int lo = 0, hi = p.groups;   // last group whose first tile is <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  T.e = lo;
+  int r1;
+  group_range(p.offsets, lo, p.m, T.r0, r1);
+  const int R = r1 - T.r0, nt = (R + 255) / 256;
+  const int each = ((R + nt - 1) / nt + 31) & ~31;      // rows of a tile: the group in even parts
+  const int i = t - first[lo];
+  const int band = i / (GP_BAND * a.nft), in = i - band * GP_BAND * a.nft;
+  const int h = min(GP_BAND, nt - band * GP_BAND);
+  const int rt = band * GP_BAND + in % h;
+  T.f0 = in / h * (MODE == GP_SWIGLU ? 128 : 256);
+  T.r0 += rt * each;
+  T.rows = min(R - rt * each, each);                    // 0 or less where the even parts end early
+  T.n = (max(T.rows, 0) + 31) & ~31;
+  T.c0 = 0;
+  T.nkb = T.rows > 0 ? (p.k + 63) / 64 : 0;
+  return T;
+}
+
+// row number of sorted row i for a gather; `none` outside [.., end) or outside the tensor
+__device__ __forceinline__ int row_of(const int* rows, long long i, long long end, int none) {
+  if (i >= end) return none;
+  if (!rows) return (int)i;
+  const int r = __ldg(rows + i);
+  return r >= 0 && r < none ? r : none;
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
+    grouped_pair_kernel(const __grid_constant__ PairArgs a, const __grid_constant__ CUtensorMap map_a,
+                        const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap gat_a,
+                        const __grid_constant__ CUtensorMap gat_b) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const GroupedProblem& p = a.p;
+  constexpr bool WG = MODE == GP_WGRAD, SW = MODE == GP_SWIGLU;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + GP_OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + GP_OFF_BAR + 240);
+  volatile int* s_abort = reinterpret_cast<int*>(smem + GP_OFF_BAR + 244);
+  int* first = reinterpret_cast<int*>(smem + GP_OFF_TAB);
+  int* scan = reinterpret_cast<int*>(smem + GP_OFF_SCAN);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * GP_STAGES;
+  const uint32_t tfull0 = empty0 + 8 * GP_STAGES, tempty0 = tfull0 + 16;
+
+  if (tid == 0) {
+    for (int s = 0; s < GP_STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);     // first block's: its own arrival, both blocks' bytes
+      mbar_init(empty0 + 8 * s, 1);    // the products that read the stage
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tempty0 + 8 * b, 2 * GP_EPI_WARPS);   // first block's: the storing warps of both
+    }
+    *s_abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) tmem_alloc<2>(smem_u32(tmem_slot), 512);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_b);
+  }
+  // first tile of each group: thread i scans groups 4 i .. 4 i + 3
+  int total;
+  if (WG) {
+    total = p.groups * a.nft * a.nkt;
+  } else {
+    int nt[4], mine = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int g = 4 * tid + q;
+      int r0 = 0, r1 = 0;
+      if (g < p.groups) group_range(p.offsets, g, p.m, r0, r1);
+      nt[q] = (r1 - r0 + 255) / 256 * a.nft;
+      mine += nt[q];
+    }
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int off = inc - mine;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < GP_THREADS / 32; ++w) {
+      if (w < warp) off += scan[w];
+      total += scan[w];
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (4 * tid + q < p.groups) first[4 * tid + q] = off;
+      off += nt[q];
+    }
+  }
+  umma_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // barriers of both blocks exist before either signals the other
+  umma_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int pair = blockIdx.x >> 1, npair = gridDim.x >> 1;
+  const uint32_t s0 = smem_u32(smem);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- copies
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int t = pair; t < total && ok; t += npair) {
+      const Tile T = decode<MODE>(a, first, t);
+      const int half = T.n / 2;                            // rows of the second factor in each block
+      const uint32_t bytes = 2 * GP_OP + (WG ? 2 * GP_OP : T.n * 128);
+      int4 gr = make_int4(0, 0, 0, 0);
+      if (!WG && p.a_rows && T.nkb > 0 && lane < half / 4) {   // this block's rows: lane i gathers 4 i .. 4 i + 3
+        const long long i = T.r0 + (long long)rank * half + 4 * lane, end = (long long)T.r0 + T.rows;
+        const int none = (int)p.a_nrows;
+        gr = make_int4(row_of(p.a_rows, i, end, none), row_of(p.a_rows, i + 1, end, none),
+                       row_of(p.a_rows, i + 2, end, none), row_of(p.a_rows, i + 3, end, none));
+      }
+      for (int kb = 0; kb < T.nkb; ++kb) {
+        ok = wait_cluster(empty0 + 8 * s, ph ^ 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = map_rank(full0 + 8 * s, 0);
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(full0 + 8 * s, bytes);
+        __syncwarp();
+        const uint32_t da = s0 + s * GP_STAGE, db = da + GP_OP;
+        if (!WG) {
+          if (lane == 0) {
+            const int f = T.f0 + (int)rank * (SW ? 64 : 128);
+            if (MODE == GP_NK) tma_3d<2>(da, &map_a, kb * 64, f, T.e, bar);
+            if (SW) tma_5d<2>(da, &map_a, kb * 64, 0, 0, f / 16, T.e, bar);
+            if (MODE == GP_KN) {
+              tma_3d<2>(da, &map_a, f, kb * 64, T.e, bar);
+              tma_3d<2>(da + SLAB_BYTES, &map_a, f + 64, kb * 64, T.e, bar);
+            }
+          }
+          if (p.a_rows) {
+            if (lane < half / 4) tma_gather4<2>(db + lane * 512, &gat_b, kb * 64, gr, bar);
+          } else if (lane < half / 16) {
+            tma_2d<2>(db + lane * 2048, &map_b, kb * 64, T.r0 + (int)rank * half + lane * 16, bar);
+          }
+        } else {
+          const int fa = T.f0 + (int)rank * 128, fb = T.c0 + (int)rank * 128;
+          const long long i = T.r0 + kb * 64, end = (long long)T.r0 + T.rows;
+          const bool tail = i + 64 > end;
+          const int sl = lane >> 4, q = (lane & 15) * 4;    // lane: slab, first of its four rows
+          if (p.a_rows || tail) {
+            const int none = (int)p.a_nrows;
+            const int4 r = make_int4(row_of(p.a_rows, i + q, end, none), row_of(p.a_rows, i + q + 1, end, none),
+                                     row_of(p.a_rows, i + q + 2, end, none), row_of(p.a_rows, i + q + 3, end, none));
+            tma_gather4<2>(da + sl * SLAB_BYTES + q * 128, &gat_a, fa + sl * 64, r, bar);
+          } else if (lane < 2) {
+            tma_2d<2>(da + lane * SLAB_BYTES, &map_a, fa + lane * 64, (int)i, bar);
+          }
+          if (p.b_rows || tail) {
+            const int none = (int)p.b_nrows;
+            const int4 r = make_int4(row_of(p.b_rows, i + q, end, none), row_of(p.b_rows, i + q + 1, end, none),
+                                     row_of(p.b_rows, i + q + 2, end, none), row_of(p.b_rows, i + q + 3, end, none));
+            tma_gather4<2>(db + sl * SLAB_BYTES + q * 128, &gat_b, fb + sl * 64, r, bar);
+          } else if (lane < 2) {
+            tma_2d<2>(db + lane * SLAB_BYTES, &map_b, fb + lane * 64, (int)i, bar);
+          }
+        }
+        if (++s == GP_STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    // the first block's products signal this block's barriers: they have all done so before it may exit
+    for (int i = 0; i < GP_STAGES && ok; ++i) {
+      ok = __all_sync(0xffffffffu, wait_cluster(empty0 + 8 * s, ph ^ 1));
+      if (++s == GP_STAGES) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+    if (!ok && lane == 0) *s_abort = 1;
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- products
+    if (rank == 0 && lane == 0) {
+      int s = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      const bool bf = p.dtype == GT_BF16;
+      constexpr bool a_mn = MODE == GP_KN || WG, b_mn = WG;
+      constexpr uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
+      for (int t = pair; t < total && ok; t += npair) {
+        const Tile T = decode<MODE>(a, first, t);
+        if (T.nkb == 0) continue;
+        ok = wait_cluster(tempty0 + 8 * acc, aph ^ 1);
+        umma_fence_after();
+        const uint32_t idesc = idesc_16(bf, a_mn, b_mn, 256, T.n);
+        for (int kb = 0; kb < T.nkb && ok; ++kb) {
+          ok = wait_cluster(full0 + 8 * s, ph);
+          if (!ok) break;
+          umma_fence_after();
+          const uint32_t sa = s0 + s * GP_STAGE, sb = sa + GP_OP;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma<2>(tmem + acc * 256, sw128_desc(sa + kk * a_step, a_mn), sw128_desc(sb + kk * b_step, b_mn), idesc,
+                    kb > 0 || kk > 0);
+          umma_commit_pair(empty0 + 8 * s);
+          if (++s == GP_STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) umma_commit_pair(tfull0 + 8 * acc);
+        if (++acc == 2) {
+          acc = 0;
+          aph ^= 1;
+        }
+      }
+      if (!ok) *s_abort = 1;
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- results
+    const int quarter = warp & 3, part = (warp - 2) >> 2;   // TMEM lanes this warp may read; which half of the columns
+    int acc = 0;
+    uint32_t aph = 0;
+    bool ok = true;
+    const int n_out = SW ? p.n / 2 : p.n;
+    for (int t = pair; t < total; t += npair) {
+      const Tile T = decode<MODE>(a, first, t);
+      if (T.nkb == 0 && !WG) continue;
+      if (T.nkb > 0) {
+        ok = wait_cluster(tfull0 + 8 * acc, aph);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        umma_fence_after();
+      }
+      const uint32_t td = tmem + acc * 256 + ((uint32_t)(quarter * 32) << 16);
+      for (int c = part * 32; c < T.n; c += 64) {
+        float v[32];
+        if (WG && T.nkb == 0) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        } else {
+          tmem_ld32(td + c, v);
+        }
+        if (WG) {
+          // lane: row n of dw; columns: k
+          const int n = T.f0 + (int)rank * 128 + quarter * 32 + lane, k = T.c0 + c;
+          if (n < p.n && k < p.k) {
+            const long long at = (long long)T.e * p.d_stride + (long long)n * p.ldd + k;
+            if (a.wide && k + 32 <= p.k) {
+              if (p.out_dtype == GT_FP32) {
+                float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.d) + at);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              } else {
+                uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + at);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  d[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1], p.out_dtype), pack2(v[8 * i + 2], v[8 * i + 3], p.out_dtype),
+                                    pack2(v[8 * i + 4], v[8 * i + 5], p.out_dtype), pack2(v[8 * i + 6], v[8 * i + 7], p.out_dtype));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (k + i < p.k) store1(p.d, at + i, v[i], p.out_dtype);
+            }
+          }
+        } else {
+          // lane: feature; columns: rows c .. c + 31 of the tile.  Lane i finds the out row of column c + i.
+          long long my_row = -1;
+          if (c + lane < T.rows) {
+            const long long i = (long long)T.r0 + c + lane;
+            const long long r = p.d_rows ? __ldg(p.d_rows + i) : i;
+            if (r >= 0 && r < p.d_nrows) my_row = r;
+          }
+          if (SW) {
+            // lanes 0..15 hold gate, 16..31 up of the same 16 features: columns i and i + 1 are
+            // exchanged so that the lower lanes finish column i and the upper ones column i + 1
+            const int f = T.f0 + (int)rank * 64 + quarter * 16 + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float mine = lane < 16 ? v[i] : v[i + 1];
+              const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? v[i + 1] : v[i], 16);
+              const float g = lane < 16 ? mine : other, u = lane < 16 ? other : mine;
+              const float h = g / (1.f + expf(-g)) * u;
+              const long long row = __shfl_sync(0xffffffffu, my_row, i + (lane >> 4));
+              if (row >= 0 && f < n_out) store1(p.d, row * p.ldd + f, h, p.out_dtype);
+            }
+          } else {
+            const int f = T.f0 + (int)rank * 128 + quarter * 32 + lane;
+            if (a.wide && p.out_dtype != GT_FP32) {
+              // lanes 2 j and 2 j + 1 exchange columns i and i + 1: the even lane stores column i of both
+              // features in one word, the odd lane column i + 1
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const bool odd = lane & 1;
+                const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+                const uint32_t w = odd ? pack2(other, v[i + 1], p.out_dtype) : pack2(v[i], other, p.out_dtype);
+                const long long row = __shfl_sync(0xffffffffu, my_row, i + (lane & 1));
+                if (row >= 0 && f < n_out)   // n even: both features or neither
+                  *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.d) + row * p.ldd + (f & ~1)) = w;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const long long row = __shfl_sync(0xffffffffu, my_row, i);
+                if (row >= 0 && f < n_out) store1(p.d, row * p.ldd + f, v[i], p.out_dtype);
+              }
+            }
+          }
+        }
+      }
+      if (T.nkb > 0) {
+        umma_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_rank(tempty0 + 8 * acc, 0));
+        if (++acc == 2) {
+          acc = 0;
+          aph ^= 1;
+        }
+      }
+    }
+    if (!ok && lane == 0) *s_abort = 1;
+  }
+  umma_fence_before();
+  __syncthreads();
+  if (*s_abort) {   // a wait ran out: report, and let what is in flight end before the memory goes
+    if (tid == 0) {
+      *reinterpret_cast<volatile uint32_t*>(a.status) = ST_TIMEOUT;
+      __threadfence_system();
+    }
+    drain_time();
+  }
+  cluster_sync_all();   // the peer reads and signals this block's memory until here
+  umma_fence_after();
+  if (warp == 1) tmem_dealloc<2>(tmem, 512);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const PairArgs& a, const CUtensorMap (&m)[4], unsigned pairs, cudaStream_t s) {
+  grouped_pair_kernel<MODE><<<2 * pairs, GP_THREADS, GP_SMEM, s>>>(a, m[0], m[1], m[2], m[3]);
+  return cudaGetLastError();
+}
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+cudaError_t grouped_pair_set_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(grouped_pair_kernel<GP_NK>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(grouped_pair_kernel<GP_KN>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(grouped_pair_kernel<GP_SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(grouped_pair_kernel<GP_WGRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
+  return e;
+}
+
+bool grouped_maps(const GroupedProblem& p, bool wgrad, int tile_rows, int w_rows, CUtensorMap (&m)[4]) {
+  const uint64_t lda = p.lda * 2, ldb = p.ldb * 2;
+  if (p.a_nrows < 1 || p.a_nrows > 0x7fffffffLL) return false;
+  if (wgrad) {
+    if (p.b_nrows < 1 || p.b_nrows > 0x7fffffffLL) return false;
+    const uint64_t da[] = {(uint64_t)p.n, (uint64_t)p.a_nrows}, db[] = {(uint64_t)p.k, (uint64_t)p.b_nrows};
+    const uint32_t tile[] = {64, 64}, one[] = {64, 1};
+    return tensor_map(&m[0], p.a, 2, da, &lda, tile) && tensor_map(&m[1], p.b, 2, db, &ldb, tile) &&
+           tensor_map(&m[2], p.a, 2, da, &lda, one) && tensor_map(&m[3], p.b, 2, db, &ldb, one);
+  }
+  const uint64_t n = p.n, k = p.k, E = p.groups;
+  // one expert: any step to the next; several on top of one another are not a tensor
+  const uint64_t rows = p.kn ? k : n, step = p.groups > 1 ? p.b_stride * 2 : rows * ldb;
+  if (step == 0) return false;
+  bool ok;
+  if (p.swiglu) {
+    const uint64_t h = n / 2, d[] = {k, 16, 2, h / 16, E}, st[] = {ldb, h * ldb, 16 * ldb, step};
+    const uint32_t box[] = {64, 16, 2, (uint32_t)w_rows / 32, 1};
+    ok = h % 16 == 0 && tensor_map(&m[0], p.b, 5, d, st, box);
+  } else if (p.kn) {
+    const uint64_t d[] = {n, k, E}, st[] = {ldb, step};
+    const uint32_t box[] = {64, 64, 1};
+    ok = tensor_map(&m[0], p.b, 3, d, st, box);
+  } else {
+    const uint64_t d[] = {k, n, E}, st[] = {ldb, step};
+    const uint32_t box[] = {64, (uint32_t)w_rows, 1};
+    ok = tensor_map(&m[0], p.b, 3, d, st, box);
+  }
+  const uint64_t dx[] = {k, (uint64_t)p.a_nrows};
+  const uint32_t tile[] = {64, (uint32_t)tile_rows}, one[] = {64, 1};
+  ok = ok && tensor_map(&m[1], p.a, 2, dx, &lda, tile) && tensor_map(&m[3], p.a, 2, dx, &lda, one);
+  m[2] = m[0];
+  return ok;
+}
+
+bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, uint32_t* status, cudaStream_t s,
+                         cudaError_t* err) {
+  CUtensorMap m[4];
+  if (!grouped_maps(p, wgrad, 16, 128, m)) return false;
+  PairArgs a;
+  a.p = p;
+  a.status = status;
+  const int n_out = p.swiglu ? p.n / 2 : p.n;
+  const size_t el = p.out_dtype == GT_FP32 ? 4 : 2;
+  long long tiles;
+  if (wgrad) {
+    a.nft = (int)ceil_div(p.n, 256);
+    a.nkt = (int)ceil_div(p.k, 256);
+    tiles = (long long)p.groups * a.nft * a.nkt;
+    a.wide = (uintptr_t)p.d % 16 == 0 && p.ldd * el % 16 == 0 && p.d_stride * el % 16 == 0;
+  } else {
+    a.nft = (int)ceil_div(n_out, p.swiglu ? 128 : 256);
+    a.nkt = 1;
+    tiles = (p.m / 256 + (p.m < p.groups ? p.m : p.groups)) * a.nft;   // the most that m rows in groups can make
+    a.wide = (uintptr_t)p.d % 4 == 0 && p.ldd % 2 == 0 && n_out % 2 == 0;
+  }
+  if (tiles > 0x3fffffff) return false;
+  const unsigned pairs = (unsigned)(tiles < num_sms / 2 ? tiles : num_sms / 2);
+  if (wgrad) *err = launch_mode<GP_WGRAD>(a, m, pairs, s);
+  else if (p.swiglu) *err = launch_mode<GP_SWIGLU>(a, m, pairs, s);
+  else *err = p.kn ? launch_mode<GP_KN>(a, m, pairs, s) : launch_mode<GP_NK>(a, m, pairs, s);
+  return true;
+}
+
+}  // namespace moe

@@ -54,7 +54,7 @@ def run_matmul(M, sizes, n, k, dtype, kn=False, swiglu=False, gather=False, scat
     rows = rng.integers(0, R, m).astype(np.int32) if gather else None
     out_rows = rng.permutation(m + 3)[:m].astype(np.int32) if scatter else None
     val, tol = B.grouped_ref(xd, wd, offsets, rows, kn, swiglu)
-    full = torch.full((m + 3, n + 5), 7.0, dtype=B.torch_type(out), device="cuda")
+    full = torch.full((m + 3, n + (5 if seed % 2 else 8)), 7.0, dtype=B.torch_type(out), device="cuda")
     got = M.grouped_matmul(x, w, dev(offsets), rows=None if rows is None else dev(rows),
                            out_rows=None if out_rows is None else dev(out_rows), w_layout="kn" if kn else "nk",
                            act="swiglu" if swiglu else None, out=full[:, :n])
@@ -225,7 +225,7 @@ def test_wgrad(M, case, dtype, out):
     dy, dyd = values((m, n), case + 1, dtype)
     x, xd = values((m, k), case + 2, dtype)
     val, tol = B.wgrad_ref(dyd, xd, off, dr, xr)
-    full = torch.full((len(sizes), n + 1, k + 3), 7.0, dtype=B.torch_type(out), device="cuda")
+    full = torch.full((len(sizes), n + 1, k + (3 if case % 3 else 8)), 7.0, dtype=B.torch_type(out), device="cuda")
     M.grouped_wgrad(dy, x, dev(off), dy_rows=None if dr is None else dev(dr), x_rows=None if xr is None else dev(xr),
                     out=full[:, :n, :k])
     B.check_close(full[:, :n, :k], val, tol, out)
