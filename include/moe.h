@@ -309,6 +309,9 @@ size_t moe_group_route_workspace(int T, int E, int k);
  * rows apart (ldx >= k, ldw >= the row's length, ldo >= n_out; w_stride any) and any
  * 2-byte (fp32: 4-byte) alignment; pointers and strides of x and w that are multiples of 16 bytes
  * (and for SwiGLU n/2 a multiple of 16) take the fast kernels.
+ * Rows named by `rows` are copied side by side into the workspace first, as the fast kernel for many rows takes
+ * them; with a workspace that is NULL or too small a slower kernel reads them where they are.  Calls that can overlap,
+ * replays of graphs among them, need a workspace each.
  * Sums are fp32, rounded once at the store. */
 typedef struct {
     const void* x;
@@ -323,8 +326,12 @@ typedef struct {
     int dtype, out_dtype; /* moe_dtype */
     int layout;           /* moe_group_layout */
     int act;              /* moe_group_act */
+    void* workspace;      /* with rows: moe_grouped_workspace(m, k) bytes, 16-byte aligned, or NULL */
+    size_t workspace_bytes;
 } moe_grouped_args;
 moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream);
+/* Bytes of workspace for m rows of length k named by number (0 for sizes that are refused). */
+size_t moe_grouped_workspace(long long m, int k);
 
 /* dw[e][n][k] = sum over the sorted rows i of expert e of dy_i[n] x_i[k]: the weights' gradient
  * of moe_grouped_matmul (MOE_GROUP_NK; for MOE_GROUP_KN exchange dy and x).  Every element of dw is written,
@@ -345,6 +352,8 @@ typedef struct {
     long long m;
     int groups, n, k;
     int dtype, out_dtype;
+    void* workspace;      /* moe_grouped_workspace(m, n) bytes with dy_rows and (m, k) with x_rows, or NULL */
+    size_t workspace_bytes;
 } moe_grouped_wgrad_args;
 moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* stream);
 

@@ -23,13 +23,15 @@ _vp, _i, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
 class GroupedArgs(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("x", "w", "offsets", "rows", "out_rows", "out")] + \
         [(n, _ll) for n in ("x_rows", "ldx", "ldw", "w_stride", "out_rows_n", "ldo", "m")] + \
-        [(n, _i) for n in ("groups", "n", "k", "dtype", "out_dtype", "layout", "act")]
+        [(n, _i) for n in ("groups", "n", "k", "dtype", "out_dtype", "layout", "act")] + \
+        [("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class GroupedWgradArgs(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("dy", "x", "offsets", "dy_rows", "x_rows", "dw")] + \
         [(n, _ll) for n in ("dy_rows_n", "lddy", "x_rows_n", "ldx", "lddw", "dw_stride", "m")] + \
-        [(n, _i) for n in ("groups", "n", "k", "dtype", "out_dtype")]
+        [(n, _i) for n in ("groups", "n", "k", "dtype", "out_dtype")] + \
+        [("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class VerifyArgs(ctypes.Structure):
@@ -47,6 +49,8 @@ def _lib():
         L.moe_group_route.argtypes = [_vp, _ll, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
         L.moe_group_route_workspace.argtypes = [_i, _i, _i]
         L.moe_group_route_workspace.restype = ctypes.c_size_t
+        L.moe_grouped_workspace.argtypes = [_ll, _i]
+        L.moe_grouped_workspace.restype = ctypes.c_size_t
         L.moe_grouped_matmul.argtypes = [ctypes.POINTER(GroupedArgs), _vp]
         L.moe_grouped_wgrad.argtypes = [ctypes.POINTER(GroupedWgradArgs), _vp]
         L.moe_verify_draft.argtypes = [ctypes.POINTER(VerifyArgs), _vp]
@@ -162,14 +166,32 @@ def group_route_workspace(T, E, k):
     return int(_lib().moe_group_route_workspace(T, E, k))
 
 
-def grouped_matmul(x, w, offsets, rows=None, out_rows=None, w_layout="nk", act=None, out=None, out_dtype=None, stream=None):
+def _row_space(workspace, need, dev):
+    """The workspace of a call that names rows by number: what is given, or new memory of `need` bytes."""
+    if workspace is None and need:
+        workspace = _torch.empty(need, dtype=_torch.uint8, device=dev)
+    if workspace is None:
+        return None, 0
+    if workspace.device != dev:
+        raise ValueError("workspace: on %s, wanted on %s" % (workspace.device, dev))
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def grouped_workspace(m, k):
+    """Bytes of workspace for m rows of length k that a grouped product names by number."""
+    return int(_lib().moe_grouped_workspace(m, k))
+
+
+def grouped_matmul(x, w, offsets, rows=None, out_rows=None, w_layout="nk", act=None, out=None, out_dtype=None, stream=None,
+                   workspace=None):
     """The products of ragged groups of rows with their experts' weights (moe_grouped_matmul).
 
     x [R, k] bf16 or fp16; w [E, n, k] ("nk") or [E, k, n] ("kn") of the same type; offsets [E + 1] int32: sorted
     row i of [offsets[e], offsets[e + 1]) gives out = W_e x[rows[i]] (x[i] without rows), written to
     out[out_rows[i]] (out[i] without out_rows).  act="swiglu" ("nk" only): the first n / 2 rows of W_e are gate, the others
     up, and out = silu(gate x) * (up x) has n / 2 columns.  Rows of out that no sorted row names are left as they
-    were (undefined in a new tensor).  The gradient of x is the same call on dy with the other w_layout."""
+    were (undefined in a new tensor).  The gradient of x is the same call on dy with the other w_layout.
+    workspace (with rows): uint8 device memory of grouped_workspace(m, k) bytes; new memory without it."""
     torch = _dtypes()
     dev = _device(x)
     dt = _type(_dense(x, "x", 2, dev), "x", fp32=False)
@@ -190,8 +212,9 @@ def grouped_matmul(x, w, offsets, rows=None, out_rows=None, w_layout="nk", act=N
         raise ValueError("act: None or 'swiglu', got %r" % (act,))
     n_out = n // 2 if act else n
     m = rows.shape[0] if rows is not None else out_rows.shape[0] if out_rows is not None else R
-    ctx = _on(dev, stream, out is None)
+    ctx = _on(dev, stream, out is None or (rows is not None and workspace is None))
     with ctx if ctx is not None else contextlib.nullcontext():
+        space = (None, 0) if rows is None else _row_space(workspace, _lib().moe_grouped_workspace(m, k), dev)
         if out is None:
             out = torch.empty(m, n_out, dtype=out_dtype or x.dtype, device=dev)
         _dense(out, "out", 2, dev)
@@ -202,17 +225,19 @@ def grouped_matmul(x, w, offsets, rows=None, out_rows=None, w_layout="nk", act=N
             None if rows is None else _ints(rows, "rows", (m,), dev),
             None if out_rows is None else _ints(out_rows, "out_rows", (m,), dev), out.data_ptr(),
             R, _pitch(x, 0, k), _pitch(w, 1, w.shape[2]), w.stride(0) if E > 1 else 0, out.shape[0], _pitch(out, 0, n_out), m,
-            E, n, k, dt, _type(out, "out"), layout, ACT_SWIGLU if act else ACT_NONE)
+            E, n, k, dt, _type(out, "out"), layout, ACT_SWIGLU if act else ACT_NONE, *space)
         if m:
             _check(_lib().moe_grouped_matmul(ctypes.byref(a), _stream(stream)), "moe_grouped_matmul")
     return out
 
 
-def grouped_wgrad(dy, x, offsets, dy_rows=None, x_rows=None, out=None, out_dtype=None, stream=None):
+def grouped_wgrad(dy, x, offsets, dy_rows=None, x_rows=None, out=None, out_dtype=None, stream=None, workspace=None):
     """The weights' gradient of grouped_matmul (moe_grouped_wgrad): out[e] = sum over the sorted rows i of
     expert e of dy[dy_rows[i]]^T x[x_rows[i]], [E, n, k] (zeros where a group is empty).
 
-    dy [R, n] and x [S, k] bf16 or fp16 of one type; offsets [E + 1] int32.  For "kn" weights exchange dy and x."""
+    dy [R, n] and x [S, k] bf16 or fp16 of one type; offsets [E + 1] int32.  For "kn" weights exchange dy and x.
+    workspace (with row numbers): uint8 device memory of grouped_workspace(m, n) bytes for dy_rows and
+    grouped_workspace(m, k) for x_rows; new memory without it."""
     torch = _dtypes()
     dev = _device(dy)
     dt = _type(_dense(dy, "dy", 2, dev), "dy", fp32=False)
@@ -226,8 +251,12 @@ def grouped_wgrad(dy, x, offsets, dy_rows=None, x_rows=None, out=None, out_dtype
         m = x_rows.shape[0]
     else:
         m = min(dy.shape[0], x.shape[0])
-    ctx = _on(dev, stream, out is None)
+    L = _lib()
+    need = (L.moe_grouped_workspace(m, n) if dy_rows is not None else 0) + \
+        (L.moe_grouped_workspace(m, k) if x_rows is not None else 0)
+    ctx = _on(dev, stream, out is None or (need and workspace is None))
     with ctx if ctx is not None else contextlib.nullcontext():
+        space = _row_space(workspace, need, dev)
         if out is None:
             out = torch.empty(E, n, k, dtype=out_dtype or dy.dtype, device=dev)
         _dense(out, "out", 3, dev)
@@ -240,8 +269,8 @@ def grouped_wgrad(dy, x, offsets, dy_rows=None, x_rows=None, out=None, out_dtype
             None if dy_rows is None else _ints(dy_rows, "dy_rows", (m,), dev),
             None if x_rows is None else _ints(x_rows, "x_rows", (m,), dev), out.data_ptr(),
             dy.shape[0], _pitch(dy, 0, n), x.shape[0], _pitch(x, 0, k), ldw,
-            out.stride(0) if E > 1 else max(out.stride(0), (n - 1) * ldw + k), m, E, n, k, dt, _type(out, "out"))
-        _check(_lib().moe_grouped_wgrad(ctypes.byref(a), _stream(stream)), "moe_grouped_wgrad")
+            out.stride(0) if E > 1 else max(out.stride(0), (n - 1) * ldw + k), m, E, n, k, dt, _type(out, "out"), *space)
+        _check(L.moe_grouped_wgrad(ctypes.byref(a), _stream(stream)), "moe_grouped_wgrad")
     return out
 
 

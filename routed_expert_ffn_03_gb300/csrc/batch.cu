@@ -81,13 +81,44 @@ bool product_ok(int groups, long long m, int n, int k, int dtype, int out_dtype)
          is_dtype(dtype, false) && is_dtype(out_dtype, true);
 }
 
-// The kernel of a product, by what the operands allow: TMA wants 16-byte aligned addresses and strides.
-moe_status run_product(const moe::GroupedProblem& p, bool wgrad, cudaStream_t s) {
+size_t row_copy_bytes(long long m, int len) { return (size_t)m * ((len + 7) / 8 * 8) * 2; }
+
+// Where an operand's rows are named by number: copies them into ws (m rows), and makes the operand the copy.
+struct Operand {
+  const uint16_t** base;
+  const int** rows;
+  long long *nrows, *ld;
+  int len;
+};
+cudaError_t copy_operand(const Operand& o, const moe::GroupedProblem& p, uint16_t* ws, int num_sms, cudaStream_t s) {
+  const int ld = (o.len + 7) / 8 * 8;
+  const moe::RowCopy c{*o.base, ws, *o.rows, p.offsets, *o.nrows, *o.ld, p.m, p.groups, o.len, ld};
+  *o.base = ws;
+  *o.rows = nullptr;
+  *o.nrows = p.m;
+  *o.ld = ld;
+  return moe::launch_copy_rows(c, num_sms, s);
+}
+
+// The kernels of a product, by what the operands allow: TMA wants 16-byte aligned addresses and strides, and rows side
+// by side, so named rows are copied into the workspace first.
+moe_status run_product(moe::GroupedProblem p, bool wgrad, void* workspace, size_t workspace_bytes, cudaStream_t s) {
   Device* d;
   const moe_status st = current_device(&d);
   if (st != MOE_OK) return st;
+  const Operand a{&p.a, &p.a_rows, &p.a_nrows, &p.lda, wgrad ? p.n : p.k};
+  const Operand b{&p.b, &p.b_rows, &p.b_nrows, &p.ldb, p.k};
+  const size_t need_a = p.a_rows ? row_copy_bytes(p.m, a.len) : 0, need_b = p.b_rows ? row_copy_bytes(p.m, b.len) : 0;
   cudaError_t e = cudaSuccess;
-  if (p.m > 0 && moe::launch_grouped_pair(p, wgrad, d->num_sms, d->status, s, &e)) return done(e);
+  // the maps are made once without the copies, which lie no worse, to see that the fast kernel takes the product
+  moe::GroupedMaps maps;
+  if (p.m > 0 && workspace_bytes >= need_a + need_b && moe::grouped_maps(p, wgrad, &maps)) {
+    uint16_t* ws = static_cast<uint16_t*>(workspace);
+    if (need_a) e = copy_operand(a, p, ws, d->num_sms, s);
+    if (need_b && e == cudaSuccess) e = copy_operand(b, p, ws + need_a / 2, d->num_sms, s);
+    if (e != cudaSuccess) return done(e);
+    if (moe::launch_grouped_pair(p, wgrad, d->num_sms, d->status, s, &e)) return done(e);
+  }
   return done(moe::launch_grouped_any(p, wgrad, s));
 }
 
@@ -118,6 +149,10 @@ extern "C" moe_status moe_group_route(const void* logits, long long ld, int dtyp
   return done(moe::launch_group_route(a, (cudaStream_t)stream));
 }
 
+extern "C" size_t moe_grouped_workspace(long long m, int k) {
+  return m < 0 || m > kMaxRows || k < 1 || k > kMaxDim ? 0 : row_copy_bytes(m, k);
+}
+
 extern "C" moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream) {
   if (!a || !a->x || !a->w || !a->offsets || !a->out) return MOE_EINVAL;
   if (!product_ok(a->groups, a->m, a->n, a->k, a->dtype, a->out_dtype)) return MOE_EINVAL;
@@ -130,7 +165,8 @@ extern "C" moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream
     return MOE_EINVAL;
   if ((!a->rows && a->m > a->x_rows) || (!a->out_rows && a->m > a->out_rows_n)) return MOE_EINVAL;
   if (!aligned(a->x, 2) || !aligned(a->w, 2) || !aligned(a->out, dtype_bytes(a->out_dtype)) || !aligned(a->offsets, 4) ||
-      !aligned(a->rows, 4) || !aligned(a->out_rows, 4))
+      !aligned(a->rows, 4) || !aligned(a->out_rows, 4) || !aligned(a->workspace, 16) ||
+      (!a->workspace && a->workspace_bytes))
     return MOE_EINVAL;
   if (a->m == 0) return MOE_OK;
   moe::GroupedProblem p{};
@@ -154,7 +190,7 @@ extern "C" moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream
   p.out_dtype = a->out_dtype;
   p.kn = kn;
   p.swiglu = sw;
-  return run_product(p, false, (cudaStream_t)stream);
+  return run_product(p, false, a->workspace, a->workspace_bytes, (cudaStream_t)stream);
 }
 
 extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* stream) {
@@ -165,7 +201,8 @@ extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* s
     return MOE_EINVAL;
   if ((!a->dy_rows && a->m > a->dy_rows_n) || (!a->x_rows && a->m > a->x_rows_n)) return MOE_EINVAL;
   if (!aligned(a->dy, 2) || !aligned(a->x, 2) || !aligned(a->dw, dtype_bytes(a->out_dtype)) || !aligned(a->offsets, 4) ||
-      !aligned(a->dy_rows, 4) || !aligned(a->x_rows, 4))
+      !aligned(a->dy_rows, 4) || !aligned(a->x_rows, 4) || !aligned(a->workspace, 16) ||
+      (!a->workspace && a->workspace_bytes))
     return MOE_EINVAL;
   moe::GroupedProblem p{};
   p.a = static_cast<const uint16_t*>(a->dy);
@@ -186,7 +223,7 @@ extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* s
   p.k = a->k;
   p.dtype = a->dtype;
   p.out_dtype = a->out_dtype;
-  return run_product(p, true, (cudaStream_t)stream);
+  return run_product(p, true, a->workspace, a->workspace_bytes, (cudaStream_t)stream);
 }
 
 extern "C" moe_status moe_verify_draft(const moe_verify_args* a, void* stream) {

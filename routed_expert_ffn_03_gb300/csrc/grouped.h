@@ -47,9 +47,25 @@ cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, cudaStream_t
 // size it does not take).
 bool tensor_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box);
-// The maps of a product: [0] the first factor in tiles (forward: w_rows rows of W_e), [1] the second (forward: tile_rows
-// rows of x), [2], [3] both row by row.  False where TMA cannot take the operands as they lie.
-bool grouped_maps(const GroupedProblem& p, bool wgrad, int tile_rows, int w_rows, CUtensorMap (&m)[4]);
+// The maps of a product, 64 elements wide: a: the first factor in tiles; b: the second, forward in boxes of 16, 32,
+// 64 and 128 rows, weight gradient [0] in tiles of 64 rows.
+struct GroupedMaps {
+  CUtensorMap a, b[4];
+};
+// False where TMA cannot take the operands as they lie.
+bool grouped_maps(const GroupedProblem& p, bool wgrad, GroupedMaps* m);
+
+// Copy of the rows named by number: dst[i][0 .. ld_dst) = src[rows[i]][0 .. len), zeros behind len and for a number
+// outside [0, nrows), for the sorted rows i that offsets cover.  src and dst 16-byte aligned, ld_src and ld_dst
+// multiples of 8 elements, ld_dst >= len.
+struct RowCopy {
+  const uint16_t* src;
+  uint16_t* dst;
+  const int *rows, *offsets;
+  long long nrows, ld_src, m;
+  int groups, len, ld_dst;
+};
+cudaError_t launch_copy_rows(const RowCopy& c, int num_sms, cudaStream_t s);
 
 // The tensor-core kernel over pairs of SMs; false (nothing launched) where TMA cannot take the operands.
 // status: host-visible word that a wait which ran out sets.

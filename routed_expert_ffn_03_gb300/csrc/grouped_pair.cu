@@ -15,11 +15,16 @@
 //   warp 0      copies operands by TMA into a ring of 6 stages (64 contracted elements each);
 //   warp 1      of the first block issues the products for both;
 //   warps 2..9  read finished results from tensor memory and store them, while the next
-//               tile's products run into the other half of the 512 columns.
+//               tile's products run into the other half of the 512 columns;
+//   warp 10     where a weight gradient's group ends inside a step, clears the rows behind it in both
+//               factors, so that nothing of a neighbour enters a sum (zeros in one factor alone
+//               would let the other's NaN through).
+// Rows named by number are copied side by side by a kernel of their own first (memory bound; 2% of a
+// Mixtral-shaped gate/up product's time) and then come as tiles.  Measured against that, for the Mixtral-shaped down
+// product of 8192 tokens (1160 us from tiles): TMA gather 4014 us (~76 cycles an instruction of 4 rows), cp.async by
+// 4 warps into the same stages 1379 to 2072 us (its shared-memory writes wait behind the tensor core's reads).
 // Tiles of a group go rows first within bands of 8 row tiles, so the pairs at work share
-// weights and rows in L2.  Rows are copied as tiles where they are consecutive, and row by row (gather) where
-// row numbers are given or a group of the weight gradient ends inside a step: rows
-// outside the group are then zeros in both factors, so nothing of a neighbour enters a sum.
+// weights and rows in L2.
 #include <cstring>
 
 #include "grouped.h"
@@ -33,11 +38,13 @@ constexpr int GP_STAGES = 6;
 constexpr int GP_OP = 128 * 128;                 // bytes of one factor's half stage: 128 rows x 64 elements
 constexpr int GP_STAGE = 2 * GP_OP;
 constexpr int GP_EPI_WARPS = 8;
-constexpr int GP_THREADS = (2 + GP_EPI_WARPS) * 32;
+constexpr int GP_CLEAR_WARP = 2 + GP_EPI_WARPS;
+constexpr int GP_THREADS = (GP_CLEAR_WARP + 1) * 32;
 constexpr int GP_MAX_GROUPS = 1024;
 constexpr int GP_BAND = 8;                       // row tiles of a band
 constexpr int GP_OFF_BAR = GP_STAGES * GP_STAGE;
-constexpr int GP_OFF_TAB = GP_OFF_BAR + 256;     // first tile of each group [groups + 1]
+constexpr int GP_BARS = 4 * GP_STAGES + 4;
+constexpr int GP_OFF_TAB = GP_OFF_BAR + GP_BARS * 8 + 16;     // first tile of each group [groups + 1]
 constexpr int GP_OFF_SCAN = GP_OFF_TAB + (GP_MAX_GROUPS + 1) * 4 + 12;
 constexpr int GP_SMEM = GP_OFF_SCAN + 64 + 1024; // and 1024 to align the stages
 
@@ -116,19 +123,9 @@ __device__ __forceinline__ Tile decode(const PairArgs& a, const int* first, int 
   return T;
 }
 
-// row number of sorted row i for a gather; `none` outside [.., end) or outside the tensor
-__device__ __forceinline__ int row_of(const int* rows, long long i, long long end, int none) {
-  if (i >= end) return none;
-  if (!rows) return (int)i;
-  const int r = __ldg(rows + i);
-  return r >= 0 && r < none ? r : none;
-}
-
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
-    grouped_pair_kernel(const __grid_constant__ PairArgs a, const __grid_constant__ CUtensorMap map_a,
-                        const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap gat_a,
-                        const __grid_constant__ CUtensorMap gat_b) {
+    grouped_pair_kernel(const __grid_constant__ PairArgs a, const __grid_constant__ GroupedMaps maps) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -137,17 +134,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   constexpr bool WG = MODE == GP_WGRAD, SW = MODE == GP_SWIGLU;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + GP_OFF_BAR);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + GP_OFF_BAR + 240);
-  volatile int* s_abort = reinterpret_cast<int*>(smem + GP_OFF_BAR + 244);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + GP_OFF_BAR + GP_BARS * 8);
+  volatile int* s_abort = reinterpret_cast<int*>(smem + GP_OFF_BAR + GP_BARS * 8 + 4);
   int* first = reinterpret_cast<int*>(smem + GP_OFF_TAB);
   int* scan = reinterpret_cast<int*>(smem + GP_OFF_SCAN);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * GP_STAGES;
-  const uint32_t tfull0 = empty0 + 8 * GP_STAGES, tempty0 = tfull0 + 16;
+  const uint32_t land0 = empty0 + 8 * GP_STAGES, ready0 = land0 + 8 * GP_STAGES;
+  const uint32_t tfull0 = ready0 + 8 * GP_STAGES, tempty0 = tfull0 + 16;
 
   if (tid == 0) {
     for (int s = 0; s < GP_STAGES; ++s) {
       mbar_init(full0 + 8 * s, 1);     // first block's: its own arrival, both blocks' bytes
       mbar_init(empty0 + 8 * s, 1);    // the products that read the stage
+      mbar_init(land0 + 8 * s, 1);     // this block's tiles of a step that has rows to clear
+      mbar_init(ready0 + 8 * s, 2);    // first block's: both blocks have cleared theirs
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
@@ -158,9 +158,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   }
   if (warp == 1) tmem_alloc<2>(smem_u32(tmem_slot), 512);
   if (warp == 0 && lane == 0) {
-    tma_prefetch_map(&map_a);
-    tma_prefetch_map(&map_b);
+    tma_prefetch_map(&maps.a);
+    tma_prefetch_map(&maps.b[0]);
   }
+  pdl_wait();   // the copy of named rows, where there is one (and through it all work before)
   // first tile of each group: thread i scans groups 4 i .. 4 i + 3
   int total;
   if (WG) {
@@ -201,6 +202,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   cluster_sync_all();   // barriers of both blocks exist before either signals the other
   umma_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // whether the group ends inside step kb
+  auto clears = [&](const Tile& T, int kb) { return WG && T.rows - kb * 64 < 64; };
   const int pair = blockIdx.x >> 1, npair = gridDim.x >> 1;
   const uint32_t s0 = smem_u32(smem);
 
@@ -212,60 +215,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
     for (int t = pair; t < total && ok; t += npair) {
       const Tile T = decode<MODE>(a, first, t);
       const int half = T.n / 2;                            // rows of the second factor in each block
-      const uint32_t bytes = 2 * GP_OP + (WG ? 2 * GP_OP : T.n * 128);
-      int4 gr = make_int4(0, 0, 0, 0);
-      if (!WG && p.a_rows && T.nkb > 0 && lane < half / 4) {   // this block's rows: lane i gathers 4 i .. 4 i + 3
-        const long long i = T.r0 + (long long)rank * half + 4 * lane, end = (long long)T.r0 + T.rows;
-        const int none = (int)p.a_nrows;
-        gr = make_int4(row_of(p.a_rows, i, end, none), row_of(p.a_rows, i + 1, end, none),
-                       row_of(p.a_rows, i + 2, end, none), row_of(p.a_rows, i + 3, end, none));
-      }
+      // consecutive rows come as one box of 16, 32, 64 or 128: what is past the half is not multiplied
+      const int box = half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
       for (int kb = 0; kb < T.nkb; ++kb) {
-        ok = wait_cluster(empty0 + 8 * s, ph ^ 1);
+        ok = wait_bar(empty0 + 8 * s, ph ^ 1);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
-        const uint32_t bar = map_rank(full0 + 8 * s, 0);
-        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(full0 + 8 * s, bytes);
-        __syncwarp();
+        const uint32_t bytes = GP_OP + (WG ? GP_OP : 2048 << box);   // in each block
+        uint32_t bar = map_rank(full0 + 8 * s, 0);
+        if (lane == 0) {
+          if (clears(T, kb)) {   // the step is ready when both blocks' rows behind the group are cleared
+            bar = land0 + 8 * s;
+            mbar_arrive_expect_tx(bar, bytes);
+            if (rank == 0) mbar_arrive(full0 + 8 * s);
+          } else if (rank == 0) {
+            mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
+          }
+        }
+        bar = __shfl_sync(0xffffffffu, bar, 0);
         const uint32_t da = s0 + s * GP_STAGE, db = da + GP_OP;
         if (!WG) {
           if (lane == 0) {
             const int f = T.f0 + (int)rank * (SW ? 64 : 128);
-            if (MODE == GP_NK) tma_3d<2>(da, &map_a, kb * 64, f, T.e, bar);
-            if (SW) tma_5d<2>(da, &map_a, kb * 64, 0, 0, f / 16, T.e, bar);
+            if (MODE == GP_NK) tma_3d<2>(da, &maps.a, kb * 64, f, T.e, bar);
+            if (SW) tma_5d<2>(da, &maps.a, kb * 64, 0, 0, f / 16, T.e, bar);
             if (MODE == GP_KN) {
-              tma_3d<2>(da, &map_a, f, kb * 64, T.e, bar);
-              tma_3d<2>(da + SLAB_BYTES, &map_a, f + 64, kb * 64, T.e, bar);
+              tma_3d<2>(da, &maps.a, f, kb * 64, T.e, bar);
+              tma_3d<2>(da + SLAB_BYTES, &maps.a, f + 64, kb * 64, T.e, bar);
             }
+            tma_2d<2>(db, &maps.b[box], kb * 64, T.r0 + (int)rank * half, bar);
           }
-          if (p.a_rows) {
-            if (lane < half / 4) tma_gather4<2>(db + lane * 512, &gat_b, kb * 64, gr, bar);
-          } else if (lane < half / 16) {
-            tma_2d<2>(db + lane * 2048, &map_b, kb * 64, T.r0 + (int)rank * half + lane * 16, bar);
-          }
-        } else {
+        } else if (lane < 2) {
           const int fa = T.f0 + (int)rank * 128, fb = T.c0 + (int)rank * 128;
-          const long long i = T.r0 + kb * 64, end = (long long)T.r0 + T.rows;
-          const bool tail = i + 64 > end;
-          const int sl = lane >> 4, q = (lane & 15) * 4;    // lane: slab, first of its four rows
-          if (p.a_rows || tail) {
-            const int none = (int)p.a_nrows;
-            const int4 r = make_int4(row_of(p.a_rows, i + q, end, none), row_of(p.a_rows, i + q + 1, end, none),
-                                     row_of(p.a_rows, i + q + 2, end, none), row_of(p.a_rows, i + q + 3, end, none));
-            tma_gather4<2>(da + sl * SLAB_BYTES + q * 128, &gat_a, fa + sl * 64, r, bar);
-          } else if (lane < 2) {
-            tma_2d<2>(da + lane * SLAB_BYTES, &map_a, fa + lane * 64, (int)i, bar);
-          }
-          if (p.b_rows || tail) {
-            const int none = (int)p.b_nrows;
-            const int4 r = make_int4(row_of(p.b_rows, i + q, end, none), row_of(p.b_rows, i + q + 1, end, none),
-                                     row_of(p.b_rows, i + q + 2, end, none), row_of(p.b_rows, i + q + 3, end, none));
-            tma_gather4<2>(db + sl * SLAB_BYTES + q * 128, &gat_b, fb + sl * 64, r, bar);
-          } else if (lane < 2) {
-            tma_2d<2>(db + lane * SLAB_BYTES, &map_b, fb + lane * 64, (int)i, bar);
-          }
+          tma_2d<2>(da + lane * SLAB_BYTES, &maps.a, fa + lane * 64, T.r0 + kb * 64, bar);
+          tma_2d<2>(db + lane * SLAB_BYTES, &maps.b[0], fb + lane * 64, T.r0 + kb * 64, bar);
         }
         if (++s == GP_STAGES) {
           s = 0;
@@ -275,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
     }
     // the first block's products signal this block's barriers: they have all done so before it may exit
     for (int i = 0; i < GP_STAGES && ok; ++i) {
-      ok = __all_sync(0xffffffffu, wait_cluster(empty0 + 8 * s, ph ^ 1));
+      ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1));
       if (++s == GP_STAGES) {
         s = 0;
         ph ^= 1;
@@ -286,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
     // ---------------------------------------------------------------- products
     if (rank == 0 && lane == 0) {
       int s = 0, acc = 0;
-      uint32_t ph = 0, aph = 0;
+      uint32_t ph = 0, aph = 0, ready_ph = 0;   // ready_ph: a bit per stage, as not every step uses its barrier
       bool ok = true;
       const bool bf = p.dtype == GT_BF16;
       constexpr bool a_mn = MODE == GP_KN || WG, b_mn = WG;
@@ -294,11 +279,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
       for (int t = pair; t < total && ok; t += npair) {
         const Tile T = decode<MODE>(a, first, t);
         if (T.nkb == 0) continue;
-        ok = wait_cluster(tempty0 + 8 * acc, aph ^ 1);
+        ok = wait_bar(tempty0 + 8 * acc, aph ^ 1);
         umma_fence_after();
         const uint32_t idesc = idesc_16(bf, a_mn, b_mn, 256, T.n);
         for (int kb = 0; kb < T.nkb && ok; ++kb) {
-          ok = wait_cluster(full0 + 8 * s, ph);
+          ok = wait_bar(full0 + 8 * s, ph);
+          if (ok && clears(T, kb)) {
+            ok = wait_bar(ready0 + 8 * s, (ready_ph >> s) & 1);
+            ready_ph ^= 1u << s;
+          }
           if (!ok) break;
           umma_fence_after();
           const uint32_t sa = s0 + s * GP_STAGE, sb = sa + GP_OP;
@@ -321,6 +310,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
       if (!ok) *s_abort = 1;
     }
     __syncwarp();
+  } else if (warp == GP_CLEAR_WARP) {
+    // ---------------------------------------------------------------- rows behind a group
+    if (WG) {
+      int s = 0;
+      uint32_t land_ph = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += npair) {
+        const Tile T = decode<MODE>(a, first, t);
+        if (T.nkb == 0) continue;
+        s = (s + T.nkb - 1) % GP_STAGES;   // the tile's last step
+        if (clears(T, T.nkb - 1)) {
+          ok = __all_sync(0xffffffffu, wait_bar(land0 + 8 * s, (land_ph >> s) & 1));
+          land_ph ^= 1u << s;
+          if (!ok) break;
+          uint8_t* st = smem + s * GP_STAGE;
+          const uint4 z = make_uint4(0, 0, 0, 0);
+          for (int r = T.rows - (T.nkb - 1) * 64 + (lane >> 3); r < 64; r += 4) {   // 8 lanes a row, 4 slabs
+            uint4* d = reinterpret_cast<uint4*>(st + r * 128 + (lane & 7) * 16);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) d[q * SLAB_BYTES / 16] = z;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_rank(ready0 + 8 * s, 0));
+        }
+        s = (s + 1) % GP_STAGES;
+      }
+      if (!ok && lane == 0) *s_abort = 1;
+    }
   } else {
     // ---------------------------------------------------------------- results
     const int quarter = warp & 3, part = (warp - 2) >> 2;   // TMEM lanes this warp may read; which half of the columns
@@ -332,7 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
       const Tile T = decode<MODE>(a, first, t);
       if (T.nkb == 0 && !WG) continue;
       if (T.nkb > 0) {
-        ok = wait_cluster(tfull0 + 8 * acc, aph);
+        ok = wait_bar(tfull0 + 8 * acc, aph);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         umma_fence_after();
@@ -441,9 +459,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
 }
 
 template <int MODE>
-cudaError_t launch_mode(const PairArgs& a, const CUtensorMap (&m)[4], unsigned pairs, cudaStream_t s) {
-  grouped_pair_kernel<MODE><<<2 * pairs, GP_THREADS, GP_SMEM, s>>>(a, m[0], m[1], m[2], m[3]);
-  return cudaGetLastError();
+cudaError_t launch_mode(const PairArgs& a, const GroupedMaps& m, unsigned pairs, cudaStream_t s) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(2 * pairs);
+  c.blockDim = dim3(GP_THREADS);
+  c.dynamicSmemBytes = GP_SMEM;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, grouped_pair_kernel<MODE>, a, m);
 }
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -461,15 +488,14 @@ cudaError_t grouped_pair_set_attributes() {
   return e;
 }
 
-bool grouped_maps(const GroupedProblem& p, bool wgrad, int tile_rows, int w_rows, CUtensorMap (&m)[4]) {
+bool grouped_maps(const GroupedProblem& p, bool wgrad, GroupedMaps* m) {
   const uint64_t lda = p.lda * 2, ldb = p.ldb * 2;
   if (p.a_nrows < 1 || p.a_nrows > 0x7fffffffLL) return false;
   if (wgrad) {
     if (p.b_nrows < 1 || p.b_nrows > 0x7fffffffLL) return false;
     const uint64_t da[] = {(uint64_t)p.n, (uint64_t)p.a_nrows}, db[] = {(uint64_t)p.k, (uint64_t)p.b_nrows};
-    const uint32_t tile[] = {64, 64}, one[] = {64, 1};
-    return tensor_map(&m[0], p.a, 2, da, &lda, tile) && tensor_map(&m[1], p.b, 2, db, &ldb, tile) &&
-           tensor_map(&m[2], p.a, 2, da, &lda, one) && tensor_map(&m[3], p.b, 2, db, &ldb, one);
+    const uint32_t tile[] = {64, 64};
+    return tensor_map(&m->a, p.a, 2, da, &lda, tile) && tensor_map(&m->b[0], p.b, 2, db, &ldb, tile);
   }
   const uint64_t n = p.n, k = p.k, E = p.groups;
   // one expert: any step to the next; several on top of one another are not a tensor
@@ -478,28 +504,25 @@ bool grouped_maps(const GroupedProblem& p, bool wgrad, int tile_rows, int w_rows
   bool ok;
   if (p.swiglu) {
     const uint64_t h = n / 2, d[] = {k, 16, 2, h / 16, E}, st[] = {ldb, h * ldb, 16 * ldb, step};
-    const uint32_t box[] = {64, 16, 2, (uint32_t)w_rows / 32, 1};
-    ok = h % 16 == 0 && tensor_map(&m[0], p.b, 5, d, st, box);
-  } else if (p.kn) {
-    const uint64_t d[] = {n, k, E}, st[] = {ldb, step};
-    const uint32_t box[] = {64, 64, 1};
-    ok = tensor_map(&m[0], p.b, 3, d, st, box);
+    const uint32_t box[] = {64, 16, 2, 4, 1};
+    ok = h % 16 == 0 && tensor_map(&m->a, p.b, 5, d, st, box);
   } else {
-    const uint64_t d[] = {k, n, E}, st[] = {ldb, step};
-    const uint32_t box[] = {64, (uint32_t)w_rows, 1};
-    ok = tensor_map(&m[0], p.b, 3, d, st, box);
+    const uint64_t d[] = {p.kn ? n : k, p.kn ? k : n, E}, st[] = {ldb, step};
+    const uint32_t box[] = {64, p.kn ? 64u : 128u, 1};
+    ok = tensor_map(&m->a, p.b, 3, d, st, box);
   }
   const uint64_t dx[] = {k, (uint64_t)p.a_nrows};
-  const uint32_t tile[] = {64, (uint32_t)tile_rows}, one[] = {64, 1};
-  ok = ok && tensor_map(&m[1], p.a, 2, dx, &lda, tile) && tensor_map(&m[3], p.a, 2, dx, &lda, one);
-  m[2] = m[0];
+  for (int i = 0; i < 4 && ok; ++i) {
+    const uint32_t tile[] = {64, 16u << i};
+    ok = tensor_map(&m->b[i], p.a, 2, dx, &lda, tile);
+  }
   return ok;
 }
 
 bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, uint32_t* status, cudaStream_t s,
                          cudaError_t* err) {
-  CUtensorMap m[4];
-  if (!grouped_maps(p, wgrad, 16, 128, m)) return false;
+  GroupedMaps m;
+  if (p.a_rows || p.b_rows || !grouped_maps(p, wgrad, &m)) return false;
   PairArgs a;
   a.p = p;
   a.status = status;
