@@ -42,15 +42,16 @@ __device__ __forceinline__ void group_range(const int* offsets, int g, long long
 
 cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, cudaStream_t s);
 
-// A tensor map over 16-bit elements, 128-byte swizzled, zeros outside: dims and box in elements, innermost
+// A tensor map over elements of 2 or 4 bytes, 128-byte swizzled, zeros outside: dims and box in elements, innermost
 // first; strides (of dims 1 ..) in bytes.  False where the hardware cannot address the tensor so (a base, stride or
 // size it does not take).
-bool tensor_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+bool tensor_map(CUtensorMap* m, const void* base, size_t elem, int rank, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box);
 // The maps of a product, 64 elements wide: a: the first factor in tiles; b: the second, forward in boxes of 16, 32,
 // 64 and 128 rows, weight gradient [0] in tiles of 64 rows.
 struct GroupedMaps {
   CUtensorMap a, b[4];
+  CUtensorMap d;   // weight gradient: the result, in boxes of 32 rows of 128 bytes (made by the launcher)
 };
 // False where TMA cannot take the operands as they lie.
 bool grouped_maps(const GroupedProblem& p, bool wgrad, GroupedMaps* m);

@@ -34,7 +34,10 @@ namespace moe {
 
 namespace {
 
-constexpr int GP_STAGES = 6;
+enum : int { GP_NK = 0, GP_KN = 1, GP_SWIGLU = 2, GP_WGRAD = 3 };
+
+// stages of the ring: the weight gradient gives one up for the results on their way out
+constexpr int GP_MAX_STAGES = 6, GP_WGRAD_STAGES = 5;
 constexpr int GP_OP = 128 * 128;                 // bytes of one factor's half stage: 128 rows x 64 elements
 constexpr int GP_STAGE = 2 * GP_OP;
 constexpr int GP_EPI_WARPS = 8;
@@ -42,19 +45,20 @@ constexpr int GP_CLEAR_WARP = 2 + GP_EPI_WARPS;
 constexpr int GP_THREADS = (GP_CLEAR_WARP + 1) * 32;
 constexpr int GP_MAX_GROUPS = 1024;
 constexpr int GP_BAND = 8;                       // row tiles of a band
-constexpr int GP_OFF_BAR = GP_STAGES * GP_STAGE;
-constexpr int GP_BARS = 4 * GP_STAGES + 4;
-constexpr int GP_OFF_TAB = GP_OFF_BAR + GP_BARS * 8 + 16;     // first tile of each group [groups + 1]
+constexpr int GP_OUT = 4096;                     // a warp's box of results: 32 rows of 128 bytes
+constexpr int GP_OFF_OUT = GP_WGRAD_STAGES * GP_STAGE;   // weight gradient: two boxes a storing warp
+constexpr int GP_OFF_TAB = GP_MAX_STAGES * GP_STAGE;      // forward: first tile of each group [groups + 1]
 constexpr int GP_OFF_SCAN = GP_OFF_TAB + (GP_MAX_GROUPS + 1) * 4 + 12;
-constexpr int GP_SMEM = GP_OFF_SCAN + 64 + 1024; // and 1024 to align the stages
-
-enum : int { GP_NK = 0, GP_KN = 1, GP_SWIGLU = 2, GP_WGRAD = 3 };
+constexpr int GP_OFF_BAR = GP_OFF_OUT + 2 * GP_EPI_WARPS * GP_OUT;
+constexpr int GP_BARS = 4 * GP_MAX_STAGES + 4;
+constexpr int GP_SMEM = GP_OFF_BAR + GP_BARS * 8 + 16 + 1024;   // and 1024 to align the stages
+static_assert(GP_OFF_SCAN + 64 <= GP_OFF_BAR && GP_SMEM <= 227 * 1024, "shared memory");
 
 struct PairArgs {
   GroupedProblem p;
   int nft, nkt;        // forward: feature tiles; weight gradient: n tiles and k tiles
   uint32_t* status;
-  bool wide;           // results can be stored in words: 4-byte pairs (forward), 16 bytes (weight gradient)
+  bool wide;           // results can be stored as 4-byte pairs (forward) or by TMA (weight gradient)
 };
 
 struct Tile {
@@ -132,6 +136,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   const uint32_t rank = cluster_rank();
   const GroupedProblem& p = a.p;
   constexpr bool WG = MODE == GP_WGRAD, SW = MODE == GP_SWIGLU;
+  constexpr int GP_STAGES = WG ? GP_WGRAD_STAGES : GP_MAX_STAGES;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + GP_OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + GP_OFF_BAR + GP_BARS * 8);
@@ -342,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   } else {
     // ---------------------------------------------------------------- results
     const int quarter = warp & 3, part = (warp - 2) >> 2;   // TMEM lanes this warp may read; which half of the columns
-    int acc = 0;
+    int acc = 0, buf = 0;
     uint32_t aph = 0;
     bool ok = true;
     const int n_out = SW ? p.n / 2 : p.n;
@@ -356,6 +361,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         umma_fence_after();
       }
       const uint32_t td = tmem + acc * 256 + ((uint32_t)(quarter * 32) << 16);
+      if (WG && a.wide) {
+        // boxes of 32 rows x 128 bytes, by way of shared memory (128-byte swizzled, so that 8 lanes' 16-byte
+        // stores meet 32 banks): each goes out as full lines, where a thread's own row would be written in
+        // 16-byte pieces.  TMA leaves out what lies behind n and k.
+        const bool f32 = p.out_dtype == GT_FP32;
+        const int cols = f32 ? 32 : 64, n0 = T.f0 + (int)rank * 128 + quarter * 32;
+        uint8_t* out = smem + GP_OFF_OUT + (warp - 2) * 2 * GP_OUT;
+        for (int c = part * cols; c < 256; c += 2 * cols) {
+          if (n0 >= p.n || T.c0 + c >= p.k) break;
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // the box before last has left
+          __syncwarp();
+          uint8_t* row = out + buf * GP_OUT + lane * 128;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (f32 && h) break;
+            float v[32];
+            if (T.nkb > 0) {
+              tmem_ld32(td + c + 32 * h, v);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            }
+            if (f32) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4*>(row + ((i ^ (lane & 7)) << 4)) =
+                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(row + (((4 * h + i) ^ (lane & 7)) << 4)) =
+                    make_uint4(pack2(v[8 * i], v[8 * i + 1], p.out_dtype), pack2(v[8 * i + 2], v[8 * i + 3], p.out_dtype),
+                               pack2(v[8 * i + 4], v[8 * i + 5], p.out_dtype), pack2(v[8 * i + 6], v[8 * i + 7], p.out_dtype));
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) tma_store_3d(smem_u32(out + buf * GP_OUT), &maps.d, T.c0 + c, n0, T.e);
+          buf ^= 1;
+        }
+      } else
       for (int c = part * 32; c < T.n; c += 64) {
         float v[32];
         if (WG && T.nkb == 0) {
@@ -367,25 +413,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         if (WG) {
           // lane: row n of dw; columns: k
           const int n = T.f0 + (int)rank * 128 + quarter * 32 + lane, k = T.c0 + c;
-          if (n < p.n && k < p.k) {
+          if (n < p.n) {
             const long long at = (long long)T.e * p.d_stride + (long long)n * p.ldd + k;
-            if (a.wide && k + 32 <= p.k) {
-              if (p.out_dtype == GT_FP32) {
-                float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.d) + at);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-              } else {
-                uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + at);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  d[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1], p.out_dtype), pack2(v[8 * i + 2], v[8 * i + 3], p.out_dtype),
-                                    pack2(v[8 * i + 4], v[8 * i + 5], p.out_dtype), pack2(v[8 * i + 6], v[8 * i + 7], p.out_dtype));
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (k + i < p.k) store1(p.d, at + i, v[i], p.out_dtype);
-            }
+            for (int i = 0; i < 32; ++i)
+              if (k + i < p.k) store1(p.d, at + i, v[i], p.out_dtype);
           }
         } else {
           // lane: feature; columns: rows c .. c + 31 of the tile.  Lane i finds the out row of column c + i.
@@ -442,6 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         }
       }
     }
+    if (WG && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok && lane == 0) *s_abort = 1;
   }
   umma_fence_before();
@@ -495,7 +528,7 @@ bool grouped_maps(const GroupedProblem& p, bool wgrad, GroupedMaps* m) {
     if (p.b_nrows < 1 || p.b_nrows > 0x7fffffffLL) return false;
     const uint64_t da[] = {(uint64_t)p.n, (uint64_t)p.a_nrows}, db[] = {(uint64_t)p.k, (uint64_t)p.b_nrows};
     const uint32_t tile[] = {64, 64};
-    return tensor_map(&m->a, p.a, 2, da, &lda, tile) && tensor_map(&m->b[0], p.b, 2, db, &ldb, tile);
+    return tensor_map(&m->a, p.a, 2, 2, da, &lda, tile) && tensor_map(&m->b[0], p.b, 2, 2, db, &ldb, tile);
   }
   const uint64_t n = p.n, k = p.k, E = p.groups;
   // one expert: any step to the next; several on top of one another are not a tensor
@@ -505,16 +538,16 @@ bool grouped_maps(const GroupedProblem& p, bool wgrad, GroupedMaps* m) {
   if (p.swiglu) {
     const uint64_t h = n / 2, d[] = {k, 16, 2, h / 16, E}, st[] = {ldb, h * ldb, 16 * ldb, step};
     const uint32_t box[] = {64, 16, 2, 4, 1};
-    ok = h % 16 == 0 && tensor_map(&m->a, p.b, 5, d, st, box);
+    ok = h % 16 == 0 && tensor_map(&m->a, p.b, 2, 5, d, st, box);
   } else {
     const uint64_t d[] = {p.kn ? n : k, p.kn ? k : n, E}, st[] = {ldb, step};
     const uint32_t box[] = {64, p.kn ? 64u : 128u, 1};
-    ok = tensor_map(&m->a, p.b, 3, d, st, box);
+    ok = tensor_map(&m->a, p.b, 2, 3, d, st, box);
   }
   const uint64_t dx[] = {k, (uint64_t)p.a_nrows};
   for (int i = 0; i < 4 && ok; ++i) {
     const uint32_t tile[] = {64, 16u << i};
-    ok = tensor_map(&m->b[i], p.a, 2, dx, &lda, tile);
+    ok = tensor_map(&m->b[i], p.a, 2, 2, dx, &lda, tile);
   }
   return ok;
 }
@@ -533,7 +566,10 @@ bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, uint3
     a.nft = (int)ceil_div(p.n, 256);
     a.nkt = (int)ceil_div(p.k, 256);
     tiles = (long long)p.groups * a.nft * a.nkt;
-    a.wide = (uintptr_t)p.d % 16 == 0 && p.ldd * el % 16 == 0 && p.d_stride * el % 16 == 0;
+    const uint64_t d[] = {(uint64_t)p.k, (uint64_t)p.n, (uint64_t)p.groups};
+    const uint64_t st[] = {p.ldd * el, p.groups > 1 ? p.d_stride * el : p.n * p.ldd * el};
+    const uint32_t box[] = {128u / (uint32_t)el, 32, 1};
+    a.wide = tensor_map(&m.d, p.d, el, 3, d, st, box);
   } else {
     a.nft = (int)ceil_div(n_out, p.swiglu ? 128 : 256);
     a.nkt = 1;
