@@ -44,6 +44,11 @@ constexpr int GP_EPI_WARPS = 8;
 constexpr int GP_CLEAR_WARP = 2 + GP_EPI_WARPS;
 constexpr int GP_THREADS = (GP_CLEAR_WARP + 1) * 32;
 constexpr int GP_MAX_GROUPS = 1024;
+// The tensor core's running sum drops bits at every step (K = 16) instead of rounding, which costs about
+// 2e-8 of the result a step: nothing in a 16-bit result, but 1.3e-6 after 1024 elements, where fp32 sums rounded
+// at every step are off by 3e-7.  fp32 results are therefore summed in parts of 8 stages (512 elements), which
+// the storing warps add up in registers, rounding to nearest, while the next part's products run.
+constexpr int GP_PART = 8;
 constexpr int GP_BAND = 8;                       // row tiles of a band
 constexpr int GP_OUT = 4096;                     // a warp's box of results: 32 rows of 128 bytes
 constexpr int GP_OFF_OUT = GP_WGRAD_STAGES * GP_STAGE;   // weight gradient: two boxes a storing warp
@@ -127,7 +132,7 @@ __device__ __forceinline__ Tile decode(const PairArgs& a, const int* first, int 
   return T;
 }
 
-template <int MODE>
+template <int MODE, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
     grouped_pair_kernel(const __grid_constant__ PairArgs a, const __grid_constant__ GroupedMaps maps) {
   extern __shared__ uint8_t smem_raw[];
@@ -274,42 +279,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
     if (!ok && lane == 0) *s_abort = 1;
   } else if (warp == 1) {
     // ---------------------------------------------------------------- products
+    // One thread, whose instructions are its time: descriptors are a base and a 32-bit offset, and the next tile
+    // is found while this one's products are queued.  (Descriptors made anew for each of the 8 operands
+    // of a step: 690 cycles a step instead of the tensor core's 512.)
     if (rank == 0 && lane == 0) {
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0, ready_ph = 0;   // ready_ph: a bit per stage, as not every step uses its barrier
       bool ok = true;
-      const bool bf = p.dtype == GT_BF16;
       constexpr bool a_mn = MODE == GP_KN || WG, b_mn = WG;
-      constexpr uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
+      constexpr uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+      const uint64_t da0 = sw128_desc(s0, a_mn), db0 = sw128_desc(s0 + GP_OP, b_mn);
+      const uint32_t hi_a = (uint32_t)(da0 >> 32), hi_b = (uint32_t)(db0 >> 32);
+      const uint32_t idesc0 = idesc_16(p.dtype == GT_BF16, a_mn, b_mn, 256, 0);
+      Tile T;
+      if (pair < total) T = decode<MODE>(a, first, pair);
       for (int t = pair; t < total && ok; t += npair) {
-        const Tile T = decode<MODE>(a, first, t);
-        if (T.nkb == 0) continue;
-        ok = wait_bar(tempty0 + 8 * acc, aph ^ 1);
-        umma_fence_after();
-        const uint32_t idesc = idesc_16(bf, a_mn, b_mn, 256, T.n);
-        for (int kb = 0; kb < T.nkb && ok; ++kb) {
-          ok = wait_bar(full0 + 8 * s, ph);
-          if (ok && clears(T, kb)) {
-            ok = wait_bar(ready0 + 8 * s, (ready_ph >> s) & 1);
-            ready_ph ^= 1u << s;
+        const int nkb = T.nkb, last_rows = T.rows - (nkb - 1) * 64;
+        const uint32_t idesc = idesc0 | ((uint32_t)(T.n >> 3) << 17);
+        if (t + npair < total) T = decode<MODE>(a, first, t + npair);
+        for (int kb0 = 0; kb0 < nkb && ok; kb0 += F32 ? GP_PART : nkb) {
+          const int kb1 = F32 ? min(kb0 + GP_PART, nkb) : nkb;
+          ok = wait_bar(tempty0 + 8 * acc, aph ^ 1);
+          umma_fence_after();
+          const uint32_t dst = tmem + acc * 256;
+          for (int kb = kb0; kb < kb1 && ok; ++kb) {
+            ok = wait_bar(full0 + 8 * s, ph);
+            if (WG && kb == nkb - 1 && last_rows < 64) {   // rows behind the group are being cleared
+              ok = ok && wait_bar(ready0 + 8 * s, (ready_ph >> s) & 1);
+              ready_ph ^= 1u << s;
+            }
+            if (!ok) break;
+            umma_fence_after();
+            const uint32_t off = s * (GP_STAGE >> 4), la = (uint32_t)da0 + off, lb = (uint32_t)db0 + off;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma<2>(dst, (uint64_t)hi_a << 32 | (la + kk * a_step), (uint64_t)hi_b << 32 | (lb + kk * b_step), idesc,
+                      kb > kb0 || kk > 0);
+            umma_commit_pair(empty0 + 8 * s);
+            if (++s == GP_STAGES) {
+              s = 0;
+              ph ^= 1;
+            }
           }
           if (!ok) break;
-          umma_fence_after();
-          const uint32_t sa = s0 + s * GP_STAGE, sb = sa + GP_OP;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma<2>(tmem + acc * 256, sw128_desc(sa + kk * a_step, a_mn), sw128_desc(sb + kk * b_step, b_mn), idesc,
-                    kb > 0 || kk > 0);
-          umma_commit_pair(empty0 + 8 * s);
-          if (++s == GP_STAGES) {
-            s = 0;
-            ph ^= 1;
+          umma_commit_pair(tfull0 + 8 * acc);
+          if (++acc == 2) {
+            acc = 0;
+            aph ^= 1;
           }
-        }
-        if (ok) umma_commit_pair(tfull0 + 8 * acc);
-        if (++acc == 2) {
-          acc = 0;
-          aph ^= 1;
         }
       }
       if (!ok) *s_abort = 1;
@@ -351,44 +368,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
     uint32_t aph = 0;
     bool ok = true;
     const int n_out = SW ? p.n / 2 : p.n;
+    auto release = [&]() {   // this warp has read result `acc`
+      umma_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_rank(tempty0 + 8 * acc, 0));
+      if (++acc == 2) {
+        acc = 0;
+        aph ^= 1;
+      }
+    };
     for (int t = pair; t < total; t += npair) {
       const Tile T = decode<MODE>(a, first, t);
       if (T.nkb == 0 && !WG) continue;
-      if (T.nkb > 0) {
-        ok = wait_bar(tfull0 + 8 * acc, aph);
-        ok = __all_sync(0xffffffffu, ok);
+      // column c of this warp's q-th run of 32: its runs alternate with the other warp's of the same lanes
+      float sum[F32 ? 4 : 1][32];
+      uint32_t td = 0;
+      if (F32) {
+#pragma unroll
+        for (int q = 0; q < (F32 ? 4 : 1); ++q)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[q][i] = 0.f;
+        for (int kb = 0; kb < T.nkb && ok; kb += GP_PART) {
+          ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, aph));
+          if (!ok) break;
+          umma_fence_after();
+#pragma unroll
+          for (int q = 0; q < (F32 ? 4 : 1); ++q) {
+            const int c = part * 32 + 64 * q;
+            if (c < T.n) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {   // by 16: the sums fill the registers
+                float v[16];
+                tmem_ld16(tmem + acc * 256 + ((uint32_t)(quarter * 32) << 16) + c + 16 * h, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[q][16 * h + i] += v[i];
+              }
+            }
+          }
+          release();
+        }
+        if (!ok) break;
+      } else if (T.nkb > 0) {
+        ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, aph));
         if (!ok) break;
         umma_fence_after();
+        td = tmem + acc * 256 + ((uint32_t)(quarter * 32) << 16);
       }
-      const uint32_t td = tmem + acc * 256 + ((uint32_t)(quarter * 32) << 16);
       if (WG && a.wide) {
         // boxes of 32 rows x 128 bytes, by way of shared memory (128-byte swizzled, so that 8 lanes' 16-byte
         // stores meet 32 banks): each goes out as full lines, where a thread's own row would be written in
         // 16-byte pieces.  TMA leaves out what lies behind n and k.
-        const bool f32 = p.out_dtype == GT_FP32;
-        const int cols = f32 ? 32 : 64, n0 = T.f0 + (int)rank * 128 + quarter * 32;
+        constexpr int cols = F32 ? 32 : 64;
+        const int n0 = T.f0 + (int)rank * 128 + quarter * 32;
         uint8_t* out = smem + GP_OFF_OUT + (warp - 2) * 2 * GP_OUT;
-        for (int c = part * cols; c < 256; c += 2 * cols) {
+#pragma unroll
+        for (int q = 0; q < 128 / cols; ++q) {
+          const int c = (2 * q + part) * cols;
           if (n0 >= p.n || T.c0 + c >= p.k) break;
           if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // the box before last has left
           __syncwarp();
           uint8_t* row = out + buf * GP_OUT + lane * 128;
+          if (F32) {
+            const float(&v)[32] = sum[F32 ? q : 0];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (f32 && h) break;
-            float v[32];
-            if (T.nkb > 0) {
-              tmem_ld32(td + c + 32 * h, v);
-            } else {
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(row + ((i ^ (lane & 7)) << 4)) =
+                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0.f;
-            }
-            if (f32) {
+            for (int h = 0; h < 2; ++h) {
+              float v[32];
+              if (T.nkb > 0) {
+                tmem_ld32(td + c + 32 * h, v);
+              } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float4*>(row + ((i ^ (lane & 7)) << 4)) =
-                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            } else {
+                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+              }
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<uint4*>(row + (((4 * h + i) ^ (lane & 7)) << 4)) =
@@ -402,9 +457,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
           buf ^= 1;
         }
       } else
-      for (int c = part * 32; c < T.n; c += 64) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = part * 32 + 64 * q;
+        if (c >= T.n) break;
         float v[32];
-        if (WG && T.nkb == 0) {
+        if (F32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = sum[F32 ? q : 0][i];
+        } else if (WG && T.nkb == 0) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
         } else {
@@ -420,59 +481,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
               if (k + i < p.k) store1(p.d, at + i, v[i], p.out_dtype);
           }
         } else {
-          // lane: feature; columns: rows c .. c + 31 of the tile.  Lane i finds the out row of column c + i.
-          long long my_row = -1;
-          if (c + lane < T.rows) {
-            const long long i = (long long)T.r0 + c + lane;
-            const long long r = p.d_rows ? __ldg(p.d_rows + i) : i;
-            if (r >= 0 && r < p.d_nrows) my_row = r;
+          // lane: feature; columns: rows c .. c + 31 of the tile
+          constexpr int el = F32 ? 4 : 2;
+          const long long pitch = p.ldd * el;
+          long long my_off = -1;   // out rows by number: lane i finds that of column c + i
+          if (p.d_rows && c + lane < T.rows) {
+            const long long r = __ldg(p.d_rows + T.r0 + c + lane);
+            if (r >= 0 && r < p.d_nrows) my_off = r * pitch;
           }
+          // feature f of columns i + sub, i = 0 .. 31 in steps: where it goes, or null
+          const int sub = SW ? lane >> 4 : !F32 && a.wide ? lane & 1 : 0;
+          const int f = SW ? T.f0 + (int)rank * 64 + quarter * 16 + (lane & 15) : T.f0 + (int)rank * 128 + quarter * 32 + lane;
+          char* d = static_cast<char*>(p.d) + (long long)(!SW && !F32 && a.wide ? f & ~1 : f) * el;
+          char* first_col = d + ((long long)T.r0 + c + sub) * pitch;
+          const int cols = f < n_out ? T.rows - c - sub : 0;
+          auto place = [&](int i) -> void* {
+            if (!p.d_rows) return i < cols ? first_col + i * pitch : nullptr;
+            const long long off = __shfl_sync(0xffffffffu, my_off, i + sub);
+            return off >= 0 && f < n_out ? d + off : nullptr;
+          };
           if (SW) {
             // lanes 0..15 hold gate, 16..31 up of the same 16 features: columns i and i + 1 are
             // exchanged so that the lower lanes finish column i and the upper ones column i + 1
-            const int f = T.f0 + (int)rank * 64 + quarter * 16 + (lane & 15);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float mine = lane < 16 ? v[i] : v[i + 1];
               const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? v[i + 1] : v[i], 16);
               const float g = lane < 16 ? mine : other, u = lane < 16 ? other : mine;
-              const float h = g / (1.f + expf(-g)) * u;
-              const long long row = __shfl_sync(0xffffffffu, my_row, i + (lane >> 4));
-              if (row >= 0 && f < n_out) store1(p.d, row * p.ldd + f, h, p.out_dtype);
+              const float h = __fdividef(g, 1.f + expf(-g)) * u;
+              if (void* at = place(i)) store1(at, 0, h, p.out_dtype);
+            }
+          } else if (!F32 && a.wide) {
+            // lanes 2 j and 2 j + 1 exchange columns i and i + 1: the even lane stores column i of both
+            // features in one word, the odd lane column i + 1 (n is even: both features or neither)
+            const bool odd = lane & 1;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+              const uint32_t w = odd ? pack2(other, v[i + 1], p.out_dtype) : pack2(v[i], other, p.out_dtype);
+              if (void* at = place(i)) *static_cast<uint32_t*>(at) = w;
             }
           } else {
-            const int f = T.f0 + (int)rank * 128 + quarter * 32 + lane;
-            if (a.wide && p.out_dtype != GT_FP32) {
-              // lanes 2 j and 2 j + 1 exchange columns i and i + 1: the even lane stores column i of both
-              // features in one word, the odd lane column i + 1
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const bool odd = lane & 1;
-                const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-                const uint32_t w = odd ? pack2(other, v[i + 1], p.out_dtype) : pack2(v[i], other, p.out_dtype);
-                const long long row = __shfl_sync(0xffffffffu, my_row, i + (lane & 1));
-                if (row >= 0 && f < n_out)   // n even: both features or neither
-                  *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.d) + row * p.ldd + (f & ~1)) = w;
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const long long row = __shfl_sync(0xffffffffu, my_row, i);
-                if (row >= 0 && f < n_out) store1(p.d, row * p.ldd + f, v[i], p.out_dtype);
-              }
-            }
+            for (int i = 0; i < 32; ++i)
+              if (void* at = place(i)) store1(at, 0, v[i], p.out_dtype);
           }
         }
       }
-      if (T.nkb > 0) {
-        umma_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_rank(tempty0 + 8 * acc, 0));
-        if (++acc == 2) {
-          acc = 0;
-          aph ^= 1;
-        }
-      }
+      if (!F32 && T.nkb > 0) release();
     }
     if (WG && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok && lane == 0) *s_abort = 1;
@@ -491,8 +547,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   if (warp == 1) tmem_dealloc<2>(tmem, 512);
 }
 
-template <int MODE>
-cudaError_t launch_mode(const PairArgs& a, const GroupedMaps& m, unsigned pairs, cudaStream_t s) {
+template <int MODE, bool F32>
+cudaError_t launch_as(const PairArgs& a, const GroupedMaps& m, unsigned pairs, cudaStream_t s) {
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(2 * pairs);
   c.blockDim = dim3(GP_THREADS);
@@ -503,7 +559,19 @@ cudaError_t launch_mode(const PairArgs& a, const GroupedMaps& m, unsigned pairs,
   at[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, grouped_pair_kernel<MODE>, a, m);
+  return cudaLaunchKernelEx(&c, grouped_pair_kernel<MODE, F32>, a, m);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const PairArgs& a, const GroupedMaps& m, unsigned pairs, cudaStream_t s) {
+  return a.p.out_dtype == GT_FP32 ? launch_as<MODE, true>(a, m, pairs, s) : launch_as<MODE, false>(a, m, pairs, s);
+}
+
+template <int MODE>
+cudaError_t set_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(grouped_pair_kernel<MODE, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(grouped_pair_kernel<MODE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
 }
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -511,13 +579,10 @@ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 }  // namespace
 
 cudaError_t grouped_pair_set_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(grouped_pair_kernel<GP_NK>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(grouped_pair_kernel<GP_KN>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(grouped_pair_kernel<GP_SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(grouped_pair_kernel<GP_WGRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
+  cudaError_t e = set_attributes<GP_NK>();
+  if (e == cudaSuccess) e = set_attributes<GP_KN>();
+  if (e == cudaSuccess) e = set_attributes<GP_SWIGLU>();
+  if (e == cudaSuccess) e = set_attributes<GP_WGRAD>();
   return e;
 }
 
