@@ -219,32 +219,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- copies
+    const uint32_t pair_full0 = map_rank(full0, 0);
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
     for (int t = pair; t < total && ok; t += npair) {
       const Tile T = decode<MODE>(a, first, t);
       const int half = T.n / 2;                            // rows of the second factor in each block
-      // consecutive rows come as one box of 16, 32, 64 or 128: what is past the half is not multiplied
-      const int box = half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
       for (int kb = 0; kb < T.nkb; ++kb) {
-        ok = wait_bar(empty0 + 8 * s, ph ^ 1);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        const uint32_t bytes = GP_OP + (WG ? GP_OP : 2048 << box);   // in each block
-        uint32_t bar = map_rank(full0 + 8 * s, 0);
+        ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1));
+        if (!ok) break;
+        const uint32_t bytes = GP_OP + (WG ? GP_OP : half * 128);   // in each block
+        // a step whose rows behind the group are to be cleared is announced to the block's own warp 10
+        const bool clear = clears(T, kb);
+        const uint32_t bar = (clear ? land0 : pair_full0) + 8 * s;
         if (lane == 0) {
-          if (clears(T, kb)) {   // the step is ready when both blocks' rows behind the group are cleared
-            bar = land0 + 8 * s;
-            mbar_arrive_expect_tx(bar, bytes);
-            if (rank == 0) mbar_arrive(full0 + 8 * s);
-          } else if (rank == 0) {
-            mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
+          if (clear) mbar_arrive_expect_tx(bar, bytes);
+          if (rank == 0) {
+            if (clear) mbar_arrive(full0 + 8 * s);
+            else mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
           }
         }
-        bar = __shfl_sync(0xffffffffu, bar, 0);
+        __syncwarp();
         const uint32_t da = s0 + s * GP_STAGE, db = da + GP_OP;
         if (!WG) {
           if (lane == 0) {
@@ -255,7 +251,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
               tma_3d<2>(da, &maps.a, f, kb * 64, T.e, bar);
               tma_3d<2>(da + SLAB_BYTES, &maps.a, f + 64, kb * 64, T.e, bar);
             }
-            tma_2d<2>(db, &maps.b[box], kb * 64, T.r0 + (int)rank * half, bar);
+          }
+          // the half's rows, a multiple of 16, in boxes of 128, 64, 32 and 16: lane i those of bit i
+          const int box = 16 << lane;
+          if (lane < 4 && (half & box)) {
+            const int before = half & ~(2 * box - 1);
+            tma_2d<2>(db + before * 128, &maps.b[lane], kb * 64, T.r0 + (int)rank * half + before, bar);
           }
         } else if (lane < 2) {
           const int fa = T.f0 + (int)rank * 128, fb = T.c0 + (int)rank * 128;
@@ -279,59 +280,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
     if (!ok && lane == 0) *s_abort = 1;
   } else if (warp == 1) {
     // ---------------------------------------------------------------- products
-    // One thread, whose instructions are its time: descriptors are a base and a 32-bit offset, and the next tile
-    // is found while this one's products are queued.  (Descriptors made anew for each of the 8 operands
-    // of a step: 690 cycles a step instead of the tensor core's 512.)
-    if (rank == 0 && lane == 0) {
+    // One elected thread issues, but the warp walks the loop together: the operands of the instructions then
+    // sit in uniform registers.  Issued inside a lane's own branch each of them is moved there first, some 90 cycles
+    // an instruction, and a step takes 650 cycles instead of the tensor core's 512.
+    if (rank == 0) {
+      const bool leader = elect_one();
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0, ready_ph = 0;   // ready_ph: a bit per stage, as not every step uses its barrier
       bool ok = true;
       constexpr bool a_mn = MODE == GP_KN || WG, b_mn = WG;
       constexpr uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
-      const uint64_t da0 = sw128_desc(s0, a_mn), db0 = sw128_desc(s0 + GP_OP, b_mn);
-      const uint32_t hi_a = (uint32_t)(da0 >> 32), hi_b = (uint32_t)(db0 >> 32);
+      const uint32_t base = __shfl_sync(0xffffffffu, s0, 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t da0 = sw128_desc(base, a_mn), db0 = sw128_desc(base + GP_OP, b_mn);
       const uint32_t idesc0 = idesc_16(p.dtype == GT_BF16, a_mn, b_mn, 256, 0);
-      Tile T;
+      Tile T{};
       if (pair < total) T = decode<MODE>(a, first, pair);
       for (int t = pair; t < total && ok; t += npair) {
-        const int nkb = T.nkb, last_rows = T.rows - (nkb - 1) * 64;
-        const uint32_t idesc = idesc0 | ((uint32_t)(T.n >> 3) << 17);
-        if (t + npair < total) T = decode<MODE>(a, first, t + npair);
+        const int nkb = __shfl_sync(0xffffffffu, T.nkb, 0), n = __shfl_sync(0xffffffffu, T.n, 0);
+        const int last_rows = __shfl_sync(0xffffffffu, T.rows, 0) - (nkb - 1) * 64;
+        const uint32_t idesc = idesc0 | ((uint32_t)(n >> 3) << 17);
+        if (t + npair < total) T = decode<MODE>(a, first, t + npair);   // while this tile's products are queued
         for (int kb0 = 0; kb0 < nkb && ok; kb0 += F32 ? GP_PART : nkb) {
           const int kb1 = F32 ? min(kb0 + GP_PART, nkb) : nkb;
-          ok = wait_bar(tempty0 + 8 * acc, aph ^ 1);
+          ok = __all_sync(0xffffffffu, wait_bar(tempty0 + 8 * acc, aph ^ 1));
           umma_fence_after();
-          const uint32_t dst = tmem + acc * 256;
+          const uint32_t dst = tm + acc * 256;
           for (int kb = kb0; kb < kb1 && ok; ++kb) {
-            ok = wait_bar(full0 + 8 * s, ph);
+            ok = __all_sync(0xffffffffu, wait_bar(full0 + 8 * s, ph));
             if (WG && kb == nkb - 1 && last_rows < 64) {   // rows behind the group are being cleared
-              ok = ok && wait_bar(ready0 + 8 * s, (ready_ph >> s) & 1);
+              ok = __all_sync(0xffffffffu, ok && wait_bar(ready0 + 8 * s, (ready_ph >> s) & 1));
               ready_ph ^= 1u << s;
             }
             if (!ok) break;
             umma_fence_after();
-            const uint32_t off = s * (GP_STAGE >> 4), la = (uint32_t)da0 + off, lb = (uint32_t)db0 + off;
+            const uint64_t da = da0 + (uint32_t)(s * (GP_STAGE >> 4)), db = db0 + (uint32_t)(s * (GP_STAGE >> 4));
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma<2>(dst, (uint64_t)hi_a << 32 | (la + kk * a_step), (uint64_t)hi_b << 32 | (lb + kk * b_step), idesc,
-                      kb > kb0 || kk > 0);
-            umma_commit_pair(empty0 + 8 * s);
+              for (int kk = 0; kk < 4; ++kk)
+                umma<2>(dst, da + kk * a_step, db + kk * b_step, idesc, kb > kb0 || kk > 0);
+              umma_commit_pair(empty0 + 8 * s);
+            }
+            __syncwarp();
             if (++s == GP_STAGES) {
               s = 0;
               ph ^= 1;
             }
           }
           if (!ok) break;
-          umma_commit_pair(tfull0 + 8 * acc);
+          if (leader) umma_commit_pair(tfull0 + 8 * acc);
+          __syncwarp();
           if (++acc == 2) {
             acc = 0;
             aph ^= 1;
           }
         }
       }
-      if (!ok) *s_abort = 1;
+      if (!ok && lane == 0) *s_abort = 1;
     }
-    __syncwarp();
   } else if (warp == GP_CLEAR_WARP) {
     // ---------------------------------------------------------------- rows behind a group
     if (WG) {
