@@ -88,6 +88,18 @@ __device__ __forceinline__ void store1(void* d, long long at, float v, int t) {
   else static_cast<__half*>(d)[at] = __float2half_rn(v);
 }
 
+// stores without a branch around each
+__device__ __forceinline__ void store32_if(bool live, void* at, uint32_t v) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n @p st.global.b32 [%0], %1;\n}\n" ::"l"(at), "r"(v),
+               "r"((uint32_t)live)
+               : "memory");
+}
+__device__ __forceinline__ void store16_if(bool live, void* at, uint32_t v) {
+  asm volatile("{\n .reg .pred p;\n .reg .b16 l, h;\n setp.ne.u32 p, %2, 0;\n mov.b32 {l, h}, %1;\n @p st.global.b16 [%0], l;\n}\n" ::"l"(at),
+               "r"(v), "r"((uint32_t)live)
+               : "memory");
+}
+
 // the tile with number `t` (first[g] = first tile of group g)
 template <int MODE>
 __device__ __forceinline__ Tile decode(const PairArgs& a, const int* first, int t) {
@@ -500,10 +512,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
           char* d = static_cast<char*>(p.d) + (long long)(!SW && !F32 && a.wide ? f & ~1 : f) * el;
           char* first_col = d + ((long long)T.r0 + c + sub) * pitch;
           const int cols = f < n_out ? T.rows - c - sub : 0;
-          auto place = [&](int i) -> void* {
-            if (!p.d_rows) return i < cols ? first_col + i * pitch : nullptr;
+          auto place = [&](int i, bool& live) -> char* {
+            if (!p.d_rows) {
+              live = i < cols;
+              return first_col + i * pitch;
+            }
             const long long off = __shfl_sync(0xffffffffu, my_off, i + sub);
-            return off >= 0 && f < n_out ? d + off : nullptr;
+            live = off >= 0 && f < n_out;
+            return d + off;
           };
           if (SW) {
             // lanes 0..15 hold gate, 16..31 up of the same 16 features: columns i and i + 1 are
@@ -514,7 +530,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
               const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? v[i + 1] : v[i], 16);
               const float g = lane < 16 ? mine : other, u = lane < 16 ? other : mine;
               const float h = __fdividef(g, 1.f + expf(-g)) * u;
-              if (void* at = place(i)) store1(at, 0, h, p.out_dtype);
+              bool live;
+              char* at = place(i, live);
+              if (F32) store32_if(live, at, __float_as_uint(h));
+              else store16_if(live, at, pack2(h, h, p.out_dtype));
             }
           } else if (!F32 && a.wide) {
             // lanes 2 j and 2 j + 1 exchange columns i and i + 1: the even lane stores column i of both
@@ -523,13 +542,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-              const uint32_t w = odd ? pack2(other, v[i + 1], p.out_dtype) : pack2(v[i], other, p.out_dtype);
-              if (void* at = place(i)) *static_cast<uint32_t*>(at) = w;
+              bool live;
+              char* at = place(i, live);
+              store32_if(live, at, odd ? pack2(other, v[i + 1], p.out_dtype) : pack2(v[i], other, p.out_dtype));
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (void* at = place(i)) store1(at, 0, v[i], p.out_dtype);
+            for (int i = 0; i < 32; ++i) {
+              bool live;
+              char* at = place(i, live);
+              if (F32) store32_if(live, at, __float_as_uint(v[i]));
+              else store16_if(live, at, pack2(v[i], v[i], p.out_dtype));
+            }
           }
         }
       }
