@@ -192,11 +192,15 @@ __device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* m, int a
         "l"(m), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(bar)
         : "memory");
 }
-// a box of shared memory to global memory, as a bulk group of this thread
+// a box of shared memory to global memory, as a bulk group of this thread; the first to leave L2, which the
+// operands need (3% of a weight gradient bound by its results)
 __device__ __forceinline__ void tma_store_3d(uint32_t src, const CUtensorMap* m, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m), "r"(x),
-               "r"(y), "r"(z), "r"(src)
-               : "memory");
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2, %3}], [%4], %5;" ::"l"(m),
+      "r"(x), "r"(y), "r"(z), "r"(src), "l"(policy)
+      : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* m) {

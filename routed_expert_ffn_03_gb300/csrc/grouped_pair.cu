@@ -36,8 +36,9 @@ namespace {
 
 enum : int { GP_NK = 0, GP_KN = 1, GP_SWIGLU = 2, GP_WGRAD = 3 };
 
-// stages of the ring: the weight gradient gives one up for the results on their way out
-constexpr int GP_MAX_STAGES = 6, GP_WGRAD_STAGES = 5;
+// stages of the ring, and per storing warp one box of results on its way out (weight gradient).  5 stages and two boxes
+// were 8% slower (Mixtral-shaped, fp32 results: 765 and 711 us).
+constexpr int GP_STAGES = 6;
 constexpr int GP_OP = 128 * 128;                 // bytes of one factor's half stage: 128 rows x 64 elements
 constexpr int GP_STAGE = 2 * GP_OP;
 constexpr int GP_EPI_WARPS = 8;
@@ -51,11 +52,11 @@ constexpr int GP_MAX_GROUPS = 1024;
 constexpr int GP_PART = 8;
 constexpr int GP_BAND = 8;                       // row tiles of a band
 constexpr int GP_OUT = 4096;                     // a warp's box of results: 32 rows of 128 bytes
-constexpr int GP_OFF_OUT = GP_WGRAD_STAGES * GP_STAGE;   // weight gradient: two boxes a storing warp
-constexpr int GP_OFF_TAB = GP_MAX_STAGES * GP_STAGE;      // forward: first tile of each group [groups + 1]
+constexpr int GP_OFF_OUT = GP_STAGES * GP_STAGE;      // weight gradient
+constexpr int GP_OFF_TAB = GP_OFF_OUT;           // forward: first tile of each group [groups + 1]
 constexpr int GP_OFF_SCAN = GP_OFF_TAB + (GP_MAX_GROUPS + 1) * 4 + 12;
-constexpr int GP_OFF_BAR = GP_OFF_OUT + 2 * GP_EPI_WARPS * GP_OUT;
-constexpr int GP_BARS = 4 * GP_MAX_STAGES + 4;
+constexpr int GP_OFF_BAR = GP_OFF_OUT + GP_EPI_WARPS * GP_OUT;
+constexpr int GP_BARS = 4 * GP_STAGES + 4;
 constexpr int GP_SMEM = GP_OFF_BAR + GP_BARS * 8 + 16 + 1024;   // and 1024 to align the stages
 static_assert(GP_OFF_SCAN + 64 <= GP_OFF_BAR && GP_SMEM <= 227 * 1024, "shared memory");
 
@@ -153,7 +154,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   const uint32_t rank = cluster_rank();
   const GroupedProblem& p = a.p;
   constexpr bool WG = MODE == GP_WGRAD, SW = MODE == GP_SWIGLU;
-  constexpr int GP_STAGES = WG ? GP_WGRAD_STAGES : GP_MAX_STAGES;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + GP_OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + GP_OFF_BAR + GP_BARS * 8);
@@ -381,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   } else {
     // ---------------------------------------------------------------- results
     const int quarter = warp & 3, part = (warp - 2) >> 2;   // TMEM lanes this warp may read; which half of the columns
-    int acc = 0, buf = 0;
+    int acc = 0;
     uint32_t aph = 0;
     bool ok = true;
     const int n_out = SW ? p.n / 2 : p.n;
@@ -437,14 +437,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         // 16-byte pieces.  TMA leaves out what lies behind n and k.
         constexpr int cols = F32 ? 32 : 64;
         const int n0 = T.f0 + (int)rank * 128 + quarter * 32;
-        uint8_t* out = smem + GP_OFF_OUT + (warp - 2) * 2 * GP_OUT;
+        uint8_t* out = smem + GP_OFF_OUT + (warp - 2) * GP_OUT;
 #pragma unroll
         for (int q = 0; q < 128 / cols; ++q) {
           const int c = (2 * q + part) * cols;
           if (n0 >= p.n || T.c0 + c >= p.k) break;
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // the box before last has left
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the box before has left
           __syncwarp();
-          uint8_t* row = out + buf * GP_OUT + lane * 128;
+          uint8_t* row = out + lane * 128;
           if (F32) {
             const float(&v)[32] = sum[F32 ? q : 0];
 #pragma unroll
@@ -470,8 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) tma_store_3d(smem_u32(out + buf * GP_OUT), &maps.d, T.c0 + c, n0, T.e);
-          buf ^= 1;
+          if (lane == 0) tma_store_3d(smem_u32(out), &maps.d, T.c0 + c, n0, T.e);
         }
       } else
 #pragma unroll
