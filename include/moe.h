@@ -326,12 +326,13 @@ typedef struct {
     int dtype, out_dtype; /* moe_dtype */
     int layout;           /* moe_group_layout */
     int act;              /* moe_group_act */
-    void* workspace;      /* with rows: moe_grouped_workspace(m, k) bytes, 16-byte aligned, or NULL */
+    void* workspace;      /* with rows: moe_grouped_workspace(m, k, groups) bytes, 16-byte aligned, or NULL */
     size_t workspace_bytes;
 } moe_grouped_args;
 moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream);
-/* Bytes of workspace for m rows of length k named by number (0 for sizes that are refused). */
-size_t moe_grouped_workspace(long long m, int k);
+/* Bytes of workspace for m rows of length k named by number, over that many groups (0 where the rows are so few that the
+ * kernel for them reads them where they are, and for sizes that are refused). */
+size_t moe_grouped_workspace(long long m, int k, int groups);
 
 /* dw[e][n][k] = sum over the sorted rows i of expert e of dy_i[n] x_i[k]: the weights' gradient
  * of moe_grouped_matmul (MOE_GROUP_NK; for MOE_GROUP_KN exchange dy and x).  Every element of dw is written,
@@ -352,10 +353,12 @@ typedef struct {
     long long m;
     int groups, n, k;
     int dtype, out_dtype;
-    void* workspace;      /* moe_grouped_workspace(m, n) bytes with dy_rows and (m, k) with x_rows, or NULL */
+    void* workspace;      /* moe_grouped_wgrad_workspace(m, n) bytes with dy_rows, (m, k) with x_rows, or NULL */
     size_t workspace_bytes;
 } moe_grouped_wgrad_args;
 moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* stream);
+/* Bytes of workspace for m rows of length `len` named by number (the sum of both for dy_rows and x_rows). */
+size_t moe_grouped_wgrad_workspace(long long m, int len);
 
 /* Which of a sequence's drafted tokens stand, and the token after them, so that what comes
  * out is distributed as the target's own samples.  For sequence b with L = lengths[b] drafts

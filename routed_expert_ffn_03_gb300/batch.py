@@ -2,16 +2,17 @@
 expert, the 16-bit grouped products and their gradients, the verification of drafted tokens.
 
 Argument marshalling only: shapes, types and devices of the tensors are checked here (ValueError),
-everything else by the library (MoeError).  Outputs are allocated where ``out`` is not given; with
-``stream`` they then belong to that stream.  The launch goes to the tensors' device, whichever is
-current.
+everything else by the library (MoeError).  Outputs and workspaces are allocated where they are not
+given; with ``stream`` they then belong to that stream.  The launch goes to the tensors' device,
+whichever is current.  The calls take a few microseconds of host time, which decides what the smallest
+products take, so the checks are kept lean.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import struct
 
-from .moe import OK, ROUTER_SOFTMAX, MoeError, _stream, lib
+from .moe import OK, ROUTER_SOFTMAX, MoeError, lib
 
 T_BF16, T_FP16, T_FP32 = 0, 1, 2
 GROUP_NK, GROUP_KN = 0, 1
@@ -39,6 +40,14 @@ class VerifyArgs(ctypes.Structure):
         [(n, _ll) for n in ("p_seq", "p_row", "q_seq", "q_row")] + [(n, _i) for n in ("B", "D", "V", "dtype")]
 
 
+def _packer(cls):
+    """The structure's packed form: the same bytes as the ctypes structure, made in one call (pointers and sizes as
+    unsigned numbers)."""
+    code = {_vp: "Q", _ll: "q", _i: "i", ctypes.c_size_t: "Q"}
+    return struct.Struct("@" + "".join(code[t] for _, t in cls._fields_)).pack
+
+
+_pack_matmul, _pack_wgrad, _pack_verify = _packer(GroupedArgs), _packer(GroupedWgradArgs), _packer(VerifyArgs)
 _calls = None
 
 
@@ -48,12 +57,12 @@ def _lib():
         L = lib()
         L.moe_group_route.argtypes = [_vp, _ll, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
         L.moe_group_route_workspace.argtypes = [_i, _i, _i]
-        L.moe_group_route_workspace.restype = ctypes.c_size_t
-        L.moe_grouped_workspace.argtypes = [_ll, _i]
-        L.moe_grouped_workspace.restype = ctypes.c_size_t
-        L.moe_grouped_matmul.argtypes = [ctypes.POINTER(GroupedArgs), _vp]
-        L.moe_grouped_wgrad.argtypes = [ctypes.POINTER(GroupedWgradArgs), _vp]
-        L.moe_verify_draft.argtypes = [ctypes.POINTER(VerifyArgs), _vp]
+        L.moe_grouped_workspace.argtypes = [_ll, _i, _i]
+        L.moe_grouped_wgrad_workspace.argtypes = [_ll, _i]
+        for n in ("moe_group_route_workspace", "moe_grouped_workspace", "moe_grouped_wgrad_workspace"):
+            getattr(L, n).restype = ctypes.c_size_t
+        for n in ("moe_grouped_matmul", "moe_grouped_wgrad", "moe_verify_draft"):
+            getattr(L, n).argtypes = [_vp, _vp]
         for n in ("moe_group_route", "moe_grouped_matmul", "moe_grouped_wgrad", "moe_verify_draft"):
             getattr(L, n).restype = _i
         _calls = L
@@ -64,13 +73,14 @@ _torch = None
 _types = {}
 
 
-def _dtypes():
+def _start():
+    """(torch, the library)"""
     global _torch
     if _torch is None:
         import torch
         _types.update({torch.bfloat16: T_BF16, torch.float16: T_FP16, torch.float32: T_FP32})
         _torch = torch
-    return _torch
+    return _torch, _calls or _lib()
 
 
 def _type(t, what, fp32=True):
@@ -81,18 +91,19 @@ def _type(t, what, fp32=True):
 
 
 def _dense(t, what, dims, device):
-    """A tensor of `dims` dimensions on `device`, its last dimension contiguous."""
-    if t.dim() != dims or t.device != device or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    """The shape of a tensor of `dims` dimensions on `device`, its last dimension contiguous."""
+    shape = t.shape
+    if len(shape) != dims or t.device != device or (shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError("%s: a %d-dimensional tensor on %s with a contiguous last dimension is wanted, got %s on %s" %
-                         (what, dims, device, tuple(t.shape), t.device))
-    return t
+                         (what, dims, device, tuple(shape), t.device))
+    return shape
 
 
-def _ints(t, what, shape, device):
-    """A contiguous int32 tensor of the shape on the device."""
-    if t.dtype != _torch.int32 or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
-        raise ValueError("%s: a contiguous int32 tensor of shape %s on %s is wanted, got %s %s on %s" %
-                         (what, shape, device, t.dtype, tuple(t.shape), t.device))
+def _flat(t, what, dtype, shape, device):
+    """The address of a contiguous tensor of that type and shape on the device."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError("%s: a contiguous %s tensor of shape %s on %s is wanted, got %s %s on %s" %
+                         (what, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
     return t.data_ptr()
 
 
@@ -102,23 +113,46 @@ def _pitch(t, dim, least):
 
 
 def _device(t):
-    if t.device.type != "cuda":
-        raise ValueError("the tensors must be on a CUDA device, got %s" % t.device)
-    return t.device
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device, got %s" % dev)
+    return dev
 
 
-def _on(device, stream, allocates):
-    """The context a call runs in: its device current, and its stream too where it allocates."""
+def _new(stream, dev, *wanted):
+    """New tensors of the given (shape, dtype), belonging to the stream that will use them."""
     torch = _torch
-    if allocates and stream is not None:
-        s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-        return torch.cuda.stream(s)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return None
+    if stream is None:
+        return [torch.empty(s, dtype=t, device=dev) for s, t in wanted]
+    s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):
+        return [torch.empty(s, dtype=t, device=dev) for s, t in wanted]
 
 
-def _check(st, what):
+def _space(workspace, need, stream, dev):
+    """(address, bytes) of a call's workspace: what is given, or new memory; and the tensor, to be held until the
+    launch."""
+    if workspace is None:
+        if not need:
+            return 0, 0, None
+        workspace, = _new(stream, dev, ((need,), _torch.uint8))
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on %s is wanted, got one on %s" % (dev, workspace.device))
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _run(what, call, dev, stream, *args):
+    """The call on the tensors' device, on `stream` or that device's current one."""
+    torch = _torch
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev.index == torch.cuda.current_device():
+        st = call(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, stream)
     if st != OK:
         raise MoeError(st, what)
 
@@ -131,33 +165,22 @@ def group_route(logits, k, router=ROUTER_SOFTMAX, out=None, workspace=None, stre
     the (token, rank) slots t k + j that its output is scattered to.  A logit of -inf is never selected: idx -1,
     weight 0, in no group.  out: the five tensors to write instead of new ones.  workspace: uint8 device
     memory of group_route_workspace(T, E, k) bytes; calls that may overlap on the GPU need one each."""
-    torch = _dtypes()
+    torch, L = _start()
     dev = _device(logits)
-    _dense(logits, "logits", 2, dev)
+    T, E = _dense(logits, "logits", 2, dev)
     dt = _type(logits, "logits")
-    T, E = logits.shape
-    L = _lib()
-    ctx = _on(dev, stream, out is None or workspace is None)
-    with ctx if ctx is not None else contextlib.nullcontext():
-        if out is None:
-            i32 = torch.empty(2 * T * k + T * k + E + 1, dtype=torch.int32, device=dev)
-            idx, rows, pairs, offsets = i32[:T * k].view(T, k), i32[T * k:2 * T * k], i32[2 * T * k:3 * T * k], i32[3 * T * k:]
-            out = (idx, torch.empty(T, k, dtype=torch.float32, device=dev), offsets, rows, pairs)
+    i32, P = torch.int32, T * k
+    if out is None:
+        idx, weights, offsets, rows, pairs = out = _new(
+            stream, dev, ((T, max(k, 0)), i32), ((T, max(k, 0)), torch.float32), ((E + 1,), i32), ((max(P, 0),), i32), ((max(P, 0),), i32))
+        out = tuple(out)
+    else:
         idx, weights, offsets, rows, pairs = out
-        if weights.dtype != torch.float32 or tuple(weights.shape) != (T, k) or weights.device != dev or \
-                not weights.is_contiguous():
-            raise ValueError("out: weights must be a contiguous float32 tensor of shape %s" % ((T, k),))
-        need = L.moe_group_route_workspace(T, E, k)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if workspace is not None and workspace.device != dev:
-            raise ValueError("workspace: on %s, wanted on %s" % (workspace.device, dev))
-        _check(L.moe_group_route(
-            logits.data_ptr(), _pitch(logits, 0, E), dt, T, E, k, router, _ints(idx, "out: idx", (T, k), dev),
-            weights.data_ptr(), _ints(offsets, "out: offsets", (E + 1,), dev), _ints(rows, "out: rows", (T * k,), dev),
-            _ints(pairs, "out: pairs", (T * k,), dev), workspace.data_ptr() if workspace is not None else None,
-            workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)),
-            "moe_group_route")
+    ws, ws_bytes, _held = _space(workspace, L.moe_group_route_workspace(T, E, k), stream, dev)
+    _run("moe_group_route", L.moe_group_route, dev, stream, logits.data_ptr(), _pitch(logits, 0, E), dt, T, E, k, router,
+         _flat(idx, "out: idx", i32, (T, k), dev), _flat(weights, "out: weights", torch.float32, (T, k), dev),
+         _flat(offsets, "out: offsets", i32, (E + 1,), dev), _flat(rows, "out: rows", i32, (P,), dev),
+         _flat(pairs, "out: pairs", i32, (P,), dev), ws, ws_bytes)
     return out
 
 
@@ -166,20 +189,14 @@ def group_route_workspace(T, E, k):
     return int(_lib().moe_group_route_workspace(T, E, k))
 
 
-def _row_space(workspace, need, dev):
-    """The workspace of a call that names rows by number: what is given, or new memory of `need` bytes."""
-    if workspace is None and need:
-        workspace = _torch.empty(need, dtype=_torch.uint8, device=dev)
-    if workspace is None:
-        return None, 0
-    if workspace.device != dev:
-        raise ValueError("workspace: on %s, wanted on %s" % (workspace.device, dev))
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+def grouped_workspace(m, k, groups):
+    """Bytes of workspace that grouped_matmul needs for m rows of length k named by number (0 where it needs none)."""
+    return int(_lib().moe_grouped_workspace(m, k, groups))
 
 
-def grouped_workspace(m, k):
-    """Bytes of workspace for m rows of length k that a grouped product names by number."""
-    return int(_lib().moe_grouped_workspace(m, k))
+def grouped_wgrad_workspace(m, length):
+    """Bytes of workspace that grouped_wgrad needs for m rows of that length named by number."""
+    return int(_lib().moe_grouped_wgrad_workspace(m, length))
 
 
 def grouped_matmul(x, w, offsets, rows=None, out_rows=None, w_layout="nk", act=None, out=None, out_dtype=None, stream=None,
@@ -191,43 +208,46 @@ def grouped_matmul(x, w, offsets, rows=None, out_rows=None, w_layout="nk", act=N
     out[out_rows[i]] (out[i] without out_rows).  act="swiglu" ("nk" only): the first n / 2 rows of W_e are gate, the others
     up, and out = silu(gate x) * (up x) has n / 2 columns.  Rows of out that no sorted row names are left as they
     were (undefined in a new tensor).  The gradient of x is the same call on dy with the other w_layout.
-    workspace (with rows): uint8 device memory of grouped_workspace(m, k) bytes; new memory without it."""
-    torch = _dtypes()
+    workspace (with rows): uint8 device memory of grouped_workspace(m, k, E) bytes; new memory without it."""
+    torch, L = _start()
     dev = _device(x)
-    dt = _type(_dense(x, "x", 2, dev), "x", fp32=False)
-    _dense(w, "w", 3, dev)
+    R, k = _dense(x, "x", 2, dev)
+    dt = _type(x, "x", fp32=False)
+    E, n, kw = _dense(w, "w", 3, dev)
     if w.dtype != x.dtype:
         raise ValueError("w: dtype %s, x has %s" % (w.dtype, x.dtype))
-    E = w.shape[0]
-    R, k = x.shape
     if w_layout == "nk":
-        layout, n, kw = GROUP_NK, w.shape[1], w.shape[2]
+        layout = GROUP_NK
     elif w_layout == "kn":
-        layout, n, kw = GROUP_KN, w.shape[2], w.shape[1]
+        layout, n, kw = GROUP_KN, kw, n
     else:
         raise ValueError("w_layout: 'nk' or 'kn', got %r" % (w_layout,))
     if kw != k:
         raise ValueError("x has %d columns, w takes %d" % (k, kw))
-    if act not in (None, "swiglu"):
+    if act is None:
+        n_out, act = n, ACT_NONE
+    elif act == "swiglu":
+        n_out, act = n // 2, ACT_SWIGLU
+    else:
         raise ValueError("act: None or 'swiglu', got %r" % (act,))
-    n_out = n // 2 if act else n
+    i32 = torch.int32
     m = rows.shape[0] if rows is not None else out_rows.shape[0] if out_rows is not None else R
-    ctx = _on(dev, stream, out is None or (rows is not None and workspace is None))
-    with ctx if ctx is not None else contextlib.nullcontext():
-        space = (None, 0) if rows is None else _row_space(workspace, _lib().moe_grouped_workspace(m, k), dev)
-        if out is None:
-            out = torch.empty(m, n_out, dtype=out_dtype or x.dtype, device=dev)
-        _dense(out, "out", 2, dev)
-        if out.shape[1] != n_out or (out_dtype is not None and out.dtype != out_dtype):
-            raise ValueError("out: %s %s, wanted %d columns" % (tuple(out.shape), out.dtype, n_out))
-        a = GroupedArgs(
-            x.data_ptr(), w.data_ptr(), _ints(offsets, "offsets", (E + 1,), dev),
-            None if rows is None else _ints(rows, "rows", (m,), dev),
-            None if out_rows is None else _ints(out_rows, "out_rows", (m,), dev), out.data_ptr(),
-            R, _pitch(x, 0, k), _pitch(w, 1, w.shape[2]), w.stride(0) if E > 1 else 0, out.shape[0], _pitch(out, 0, n_out), m,
-            E, n, k, dt, _type(out, "out"), layout, ACT_SWIGLU if act else ACT_NONE, *space)
-        if m:
-            _check(_lib().moe_grouped_matmul(ctypes.byref(a), _stream(stream)), "moe_grouped_matmul")
+    if out is None:
+        out, = _new(stream, dev, ((m, n_out), out_dtype or x.dtype))
+    N, cols = _dense(out, "out", 2, dev)
+    if cols != n_out or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out: %s %s, wanted %d columns" % (tuple(out.shape), out.dtype, n_out))
+    ws = ws_bytes = rows_at = 0
+    if rows is not None:
+        rows_at = _flat(rows, "rows", i32, (m,), dev)
+        ws, ws_bytes, _held = _space(workspace, L.moe_grouped_workspace(m, k, E), stream, dev)
+    if m:
+        a = _pack_matmul(
+            x.data_ptr(), w.data_ptr(), _flat(offsets, "offsets", i32, (E + 1,), dev), rows_at,
+            0 if out_rows is None else _flat(out_rows, "out_rows", i32, (m,), dev), out.data_ptr(), R, _pitch(x, 0, k),
+            _pitch(w, 1, w.shape[2]), w.stride(0) if E > 1 else 0, N, _pitch(out, 0, n_out), m, E, n, k, dt, _type(out, "out"), layout,
+            act, ws, ws_bytes)
+        _run("moe_grouped_matmul", L.moe_grouped_matmul, dev, stream, a)
     return out
 
 
@@ -236,41 +256,35 @@ def grouped_wgrad(dy, x, offsets, dy_rows=None, x_rows=None, out=None, out_dtype
     expert e of dy[dy_rows[i]]^T x[x_rows[i]], [E, n, k] (zeros where a group is empty).
 
     dy [R, n] and x [S, k] bf16 or fp16 of one type; offsets [E + 1] int32.  For "kn" weights exchange dy and x.
-    workspace (with row numbers): uint8 device memory of grouped_workspace(m, n) bytes for dy_rows and
-    grouped_workspace(m, k) for x_rows; new memory without it."""
-    torch = _dtypes()
+    workspace (with row numbers): uint8 device memory of grouped_wgrad_workspace(m, n) bytes for dy_rows and
+    grouped_wgrad_workspace(m, k) for x_rows; new memory without it."""
+    torch, L = _start()
     dev = _device(dy)
-    dt = _type(_dense(dy, "dy", 2, dev), "dy", fp32=False)
-    _dense(x, "x", 2, dev)
+    R, n = _dense(dy, "dy", 2, dev)
+    dt = _type(dy, "dy", fp32=False)
+    S, k = _dense(x, "x", 2, dev)
     if x.dtype != dy.dtype:
         raise ValueError("x: dtype %s, dy has %s" % (x.dtype, dy.dtype))
-    n, k, E = dy.shape[1], x.shape[1], offsets.shape[0] - 1
+    E, i32 = offsets.shape[0] - 1, torch.int32
+    m = dy_rows.shape[0] if dy_rows is not None else x_rows.shape[0] if x_rows is not None else min(R, S)
+    if out is None:
+        out, = _new(stream, dev, ((E, n, k), out_dtype or dy.dtype))
+    if _dense(out, "out", 3, dev) != (E, n, k) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out: %s %s, wanted %s" % (tuple(out.shape), out.dtype, (E, n, k)))
+    ldw = _pitch(out, 1, k)
+    dy_at = x_at = need = 0
     if dy_rows is not None:
-        m = dy_rows.shape[0]
-    elif x_rows is not None:
-        m = x_rows.shape[0]
-    else:
-        m = min(dy.shape[0], x.shape[0])
-    L = _lib()
-    need = (L.moe_grouped_workspace(m, n) if dy_rows is not None else 0) + \
-        (L.moe_grouped_workspace(m, k) if x_rows is not None else 0)
-    ctx = _on(dev, stream, out is None or (need and workspace is None))
-    with ctx if ctx is not None else contextlib.nullcontext():
-        space = _row_space(workspace, need, dev)
-        if out is None:
-            out = torch.empty(E, n, k, dtype=out_dtype or dy.dtype, device=dev)
-        _dense(out, "out", 3, dev)
-        if tuple(out.shape) != (E, n, k) or (out_dtype is not None and out.dtype != out_dtype):
-            raise ValueError("out: %s %s, wanted %s" % (tuple(out.shape), out.dtype, (E, n, k)))
-        ldw = _pitch(out, 1, k)
-        a = GroupedWgradArgs(
-            dy.data_ptr() if dy.shape[0] else None, x.data_ptr() if x.shape[0] else None,
-            _ints(offsets, "offsets", (E + 1,), dev),
-            None if dy_rows is None else _ints(dy_rows, "dy_rows", (m,), dev),
-            None if x_rows is None else _ints(x_rows, "x_rows", (m,), dev), out.data_ptr(),
-            dy.shape[0], _pitch(dy, 0, n), x.shape[0], _pitch(x, 0, k), ldw,
-            out.stride(0) if E > 1 else max(out.stride(0), (n - 1) * ldw + k), m, E, n, k, dt, _type(out, "out"), *space)
-        _check(L.moe_grouped_wgrad(ctypes.byref(a), _stream(stream)), "moe_grouped_wgrad")
+        dy_at = _flat(dy_rows, "dy_rows", i32, (m,), dev)
+        need = L.moe_grouped_wgrad_workspace(m, n)
+    if x_rows is not None:
+        x_at = _flat(x_rows, "x_rows", i32, (m,), dev)
+        need += L.moe_grouped_wgrad_workspace(m, k)
+    ws, ws_bytes, _held = _space(workspace, need, stream, dev) if need else (0, 0, None)
+    a = _pack_wgrad(
+        dy.data_ptr(), x.data_ptr(), _flat(offsets, "offsets", i32, (E + 1,), dev), dy_at, x_at, out.data_ptr(), R, _pitch(dy, 0, n),
+        S, _pitch(x, 0, k), ldw, out.stride(0) if E > 1 else max(out.stride(0), (n - 1) * ldw + k), m, E, n, k, dt, _type(out, "out"),
+        ws, ws_bytes)
+    _run("moe_grouped_wgrad", L.moe_grouped_wgrad, dev, stream, a)
     return out
 
 
@@ -281,27 +295,23 @@ def verify_draft(p, draft, u, q=None, lengths=None, out=None, stream=None):
     q [B, D, V]: the draft's probabilities, of p's type, or None for drafts given without; lengths [B] int32:
     drafts per sequence (D without it).  Returns (accepted [B] int32, tokens [B, D + 1] int32): the accepted drafts,
     the drawn token, then -1."""
-    torch = _dtypes()
+    torch, L = _start()
     dev = _device(p)
-    dt = _type(_dense(p, "p", 3, dev), "p")
-    B, D1, V = p.shape
-    D = D1 - 1
+    B, D1, V = _dense(p, "p", 3, dev)
+    dt = _type(p, "p")
+    D, i32 = D1 - 1, torch.int32
+    q_at = q_seq = q_row = 0
     if q is not None:
-        _dense(q, "q", 3, dev)
-        if q.dtype != p.dtype or tuple(q.shape) != (B, D, V):
+        if _dense(q, "q", 3, dev) != (B, D, V) or q.dtype != p.dtype:
             raise ValueError("q: %s %s, wanted %s %s" % (tuple(q.shape), q.dtype, (B, D, V), p.dtype))
-    if u.dtype != torch.float32 or tuple(u.shape) != (B, D1) or u.device != dev or not u.is_contiguous():
-        raise ValueError("u: a contiguous float32 tensor of shape %s on %s is wanted" % ((B, D1), dev))
-    ctx = _on(dev, stream, out is None)
-    with ctx if ctx is not None else contextlib.nullcontext():
-        if out is None:
-            out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B, D1, dtype=torch.int32, device=dev))
-        has_q = q is not None and D > 0
-        a = VerifyArgs(
-            p.data_ptr(), q.data_ptr() if has_q else None, _ints(draft, "draft", (B, D), dev) if D else None,
-            None if lengths is None else _ints(lengths, "lengths", (B,), dev), u.data_ptr(),
-            _ints(out[0], "out: accepted", (B,), dev), _ints(out[1], "out: tokens", (B, D1), dev),
-            _pitch(p, 0, D1 * V), _pitch(p, 1, V), _pitch(q, 0, D * V) if has_q else 0, _pitch(q, 1, V) if has_q else 0,
-            B, D, V, dt)
-        _check(_lib().moe_verify_draft(ctypes.byref(a), _stream(stream)), "moe_verify_draft")
+        if D:
+            q_at, q_seq, q_row = q.data_ptr(), _pitch(q, 0, D * V), _pitch(q, 1, V)
+    if out is None:
+        out = tuple(_new(stream, dev, ((B,), i32), ((B, D1), i32)))
+    a = _pack_verify(
+        p.data_ptr(), q_at, _flat(draft, "draft", i32, (B, D), dev) if D else 0,
+        0 if lengths is None else _flat(lengths, "lengths", i32, (B,), dev), _flat(u, "u", torch.float32, (B, D1), dev),
+        _flat(out[0], "out: accepted", i32, (B,), dev), _flat(out[1], "out: tokens", i32, (B, D1), dev),
+        _pitch(p, 0, D1 * V), _pitch(p, 1, V), q_seq, q_row, B, D, V, dt)
+    _run("moe_verify_draft", L.moe_verify_draft, dev, stream, a)
     return out

@@ -6,6 +6,7 @@
 #include "verify.h"
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 #include <new>
 
@@ -27,7 +28,7 @@ moe_status device_setup(int dev, Device** out) {
   Device d{0, nullptr};
   void* word = nullptr;
   if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      moe::grouped_pair_set_attributes() != cudaSuccess ||
+      moe::grouped_pair_set_attributes() != cudaSuccess || moe::grouped_few_set_attributes() != cudaSuccess ||
       cudaHostAlloc(&word, sizeof(uint32_t), cudaHostAllocMapped | cudaHostAllocPortable) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ECUDA;
@@ -81,6 +82,27 @@ bool product_ok(int groups, long long m, int n, int k, int dtype, int out_dtype)
          is_dtype(dtype, false) && is_dtype(out_dtype, true);
 }
 
+// Whether the kernel for few rows a group takes a forward product, by the mean over the groups that m rows can reach, as
+// the groups' sizes are not known here: tiles of nt rows, four times the mean, so that uneven groups fit too.  Measured
+// (DeepSeek-V3- and Mixtral-shaped layers, us for nt 16 / 32 / 64 / the pair kernel): mean 1: 75 / 74 / 75 / 83; mean 8:
+// 2038 / 2016 / 2054 / 2144; mean 16: 386 / 284 / 274 / 281; mean 32: 610 / 410 / 310 / 285.
+int few_rows_tile(long long m, int groups) {
+  const long long reach = m < groups ? m : groups;
+  return m < 1 ? 0 : m <= 4 * reach ? 16 : m <= 8 * reach ? 32 : m <= 16 * reach ? 64 : 0;
+}
+// And the blocks that share a tile's k: as many as bring 1.5 blocks an SM from the tiles that m rows spread evenly make,
+// 512 elements each at least.  Measured (down product, k = 14336, 64 tiles, cluster 1 / 2 / 4 / 8): 57 / 42 / 39 / 42 us;
+// 450 tiles of k = 2048: 40 / 45 / 53 / 82 us.
+bool few_rows(const moe::GroupedProblem& p, int num_sms, int* nt, int* cluster) {
+  *nt = few_rows_tile(p.m, p.groups);
+  if (!*nt) return false;
+  const double reached = p.groups * (1 - std::pow(1 - 1.0 / p.groups, (double)p.m));
+  const double tiles = (reached + p.m / *nt) * ((p.swiglu ? p.n / 2 : p.n) / (p.swiglu ? 64.0 : 128.0));
+  *cluster = 1;
+  while (*cluster < 8 && tiles * *cluster < 1.5 * num_sms && p.k / (2 * *cluster) >= 512) *cluster *= 2;
+  return true;
+}
+
 size_t row_copy_bytes(long long m, int len) { return (size_t)m * ((len + 7) / 8 * 8) * 2; }
 
 // Where an operand's rows are named by number: copies them into ws (m rows), and makes the operand the copy.
@@ -110,6 +132,10 @@ moe_status run_product(moe::GroupedProblem p, bool wgrad, void* workspace, size_
   const Operand b{&p.b, &p.b_rows, &p.b_nrows, &p.ldb, p.k};
   const size_t need_a = p.a_rows ? row_copy_bytes(p.m, a.len) : 0, need_b = p.b_rows ? row_copy_bytes(p.m, b.len) : 0;
   cudaError_t e = cudaSuccess;
+  int nt, cluster;
+  if (!wgrad && few_rows(p, d->num_sms, &nt, &cluster) &&
+      moe::launch_grouped_few(p, nt, cluster, d->status, s, &e))
+    return done(e);
   // the maps are made once without the copies, which lie no worse, to see that the fast kernel takes the product
   moe::GroupedMaps maps;
   if (p.m > 0 && workspace_bytes >= need_a + need_b && moe::grouped_maps(p, wgrad, &maps)) {
@@ -149,8 +175,13 @@ extern "C" moe_status moe_group_route(const void* logits, long long ld, int dtyp
   return done(moe::launch_group_route(a, (cudaStream_t)stream));
 }
 
-extern "C" size_t moe_grouped_workspace(long long m, int k) {
-  return m < 0 || m > kMaxRows || k < 1 || k > kMaxDim ? 0 : row_copy_bytes(m, k);
+extern "C" size_t moe_grouped_workspace(long long m, int k, int groups) {
+  if (m < 0 || m > kMaxRows || k < 1 || k > kMaxDim || groups < 1 || groups > 1024) return 0;
+  return few_rows_tile(m, groups) ? 0 : row_copy_bytes(m, k);
+}
+
+extern "C" size_t moe_grouped_wgrad_workspace(long long m, int len) {
+  return m < 0 || m > kMaxRows || len < 1 || len > kMaxDim ? 0 : row_copy_bytes(m, len);
 }
 
 extern "C" moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream) {

@@ -51,6 +51,7 @@ bool tensor_map(CUtensorMap* m, const void* base, size_t elem, int rank, const u
 // 64 and 128 rows, weight gradient [0] in tiles of 64 rows.
 struct GroupedMaps {
   CUtensorMap a, b[4];
+  CUtensorMap b_row;   // forward: one row
   CUtensorMap d;   // weight gradient: the result, in boxes of 32 rows of 128 bytes (made by the launcher)
 };
 // False where TMA cannot take the operands as they lie.
@@ -73,5 +74,10 @@ cudaError_t launch_copy_rows(const RowCopy& c, int num_sms, cudaStream_t s);
 bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, uint32_t* status, cudaStream_t s,
                          cudaError_t* err);
 cudaError_t grouped_pair_set_attributes();
+
+// The kernel for few rows a group, in tiles of nt = 16, 32 or 64 rows, `cluster` (1, 2, 4, 8) blocks to a tile; forward
+// products only; reads rows by number where they are.  Otherwise as launch_grouped_pair.
+bool launch_grouped_few(const GroupedProblem& p, int nt, int cluster, uint32_t* status, cudaStream_t s, cudaError_t* err);
+cudaError_t grouped_few_set_attributes();
 
 }  // namespace moe

@@ -3,6 +3,7 @@
 #include <cuda.h>
 
 #include "common.cuh"
+#include "grouped.h"
 
 namespace moe {
 
@@ -110,6 +111,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// two results rounded to a 16-bit type
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi, int dtype) {
+  if (dtype == GT_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // ---------------------------------------------------------------- cluster
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -191,6 +202,14 @@ __device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* m, int a
         "%6}], [%7];" ::"r"(dst),
         "l"(m), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(bar)
         : "memory");
+}
+// four rows named by number (a tensor map of one-row boxes; a number outside the tensor gives zeros)
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* m, int x, int4 r, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+      "%5, %6}], [%7];" ::"r"(dst),
+      "l"(m), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
+      : "memory");
 }
 // a box of shared memory to global memory, as a bulk group of this thread; the first to leave L2, which the
 // operands need (3% of a weight gradient bound by its results)

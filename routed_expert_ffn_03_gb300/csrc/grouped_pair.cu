@@ -75,14 +75,6 @@ struct Tile {
   int nkb;             // steps of 64
 };
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, int t) {
-  if (t == GT_BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ void store1(void* d, long long at, float v, int t) {
   if (t == GT_FP32) static_cast<float*>(d)[at] = v;
   else if (t == GT_BF16) static_cast<__nv_bfloat16*>(d)[at] = __float2bfloat16_rn(v);
@@ -464,8 +456,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<uint4*>(row + (((4 * h + i) ^ (lane & 7)) << 4)) =
-                    make_uint4(pack2(v[8 * i], v[8 * i + 1], p.out_dtype), pack2(v[8 * i + 2], v[8 * i + 3], p.out_dtype),
-                               pack2(v[8 * i + 4], v[8 * i + 5], p.out_dtype), pack2(v[8 * i + 6], v[8 * i + 7], p.out_dtype));
+                    make_uint4(pack_out(v[8 * i], v[8 * i + 1], p.out_dtype), pack_out(v[8 * i + 2], v[8 * i + 3], p.out_dtype),
+                               pack_out(v[8 * i + 4], v[8 * i + 5], p.out_dtype), pack_out(v[8 * i + 6], v[8 * i + 7], p.out_dtype));
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -532,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
               bool live;
               char* at = place(i, live);
               if (F32) store32_if(live, at, __float_as_uint(h));
-              else store16_if(live, at, pack2(h, h, p.out_dtype));
+              else store16_if(live, at, pack_out(h, h, p.out_dtype));
             }
           } else if (!F32 && a.wide) {
             // lanes 2 j and 2 j + 1 exchange columns i and i + 1: the even lane stores column i of both
@@ -543,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
               const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
               bool live;
               char* at = place(i, live);
-              store32_if(live, at, odd ? pack2(other, v[i + 1], p.out_dtype) : pack2(v[i], other, p.out_dtype));
+              store32_if(live, at, odd ? pack_out(other, v[i + 1], p.out_dtype) : pack_out(v[i], other, p.out_dtype));
             }
           } else {
 #pragma unroll
@@ -551,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
               bool live;
               char* at = place(i, live);
               if (F32) store32_if(live, at, __float_as_uint(v[i]));
-              else store16_if(live, at, pack2(v[i], v[i], p.out_dtype));
+              else store16_if(live, at, pack_out(v[i], v[i], p.out_dtype));
             }
           }
         }
@@ -642,7 +634,8 @@ bool grouped_maps(const GroupedProblem& p, bool wgrad, GroupedMaps* m) {
     const uint32_t tile[] = {64, 16u << i};
     ok = tensor_map(&m->b[i], p.a, 2, 2, dx, &lda, tile);
   }
-  return ok;
+  const uint32_t one[] = {64, 1};
+  return ok && tensor_map(&m->b_row, p.a, 2, 2, dx, &lda, one);
 }
 
 bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, uint32_t* status, cudaStream_t s,

@@ -32,7 +32,8 @@ def matmul_args(M, **over):
     dict(layout=2), dict(act=2), dict(act=1, n=33, ldo=33), dict(act=1, layout=1), dict(ldx=63), dict(ldw=63),
     dict(layout=1, ldw=31), dict(ldo=31), dict(m=11), dict(x_rows=9), dict(out_rows_n=9), dict(x=P + 1), dict(w=P + 1),
     dict(out_dtype=2, out=P + 2), dict(offsets=P + 2), dict(rows=P + 1), dict(out_rows=P + 3), dict(w_stride=-1),
-    dict(x_rows=-1, rows=P), dict(ldx=2 ** 61)], ids=str)
+    dict(x_rows=-1, rows=P), dict(ldx=2 ** 61),
+    dict(rows=P, workspace=P + 8, workspace_bytes=1), dict(rows=P, workspace_bytes=64)], ids=str)
 def test_grouped_matmul_refuses(M, over):
     assert M.lib().moe_grouped_matmul(ctypes.byref(matmul_args(M, **over)), None) == M.EINVAL
 
@@ -64,6 +65,23 @@ def test_group_route_refuses(M, over):
     assert M.group_route_workspace(1000, 8, 2) > 0
     assert M.lib().moe_group_route(*[a[n] for n in ("logits", "ld", "dtype", "T", "E", "k", "router", "idx", "weights", "offsets",
                                                     "rows", "pairs", "ws", "ws_bytes")], None) == M.EINVAL
+
+
+def test_packed_arguments_are_the_structures(M):
+    """The packed form that the binding passes has the structures' layout."""
+    from routed_expert_ffn_03_gb300 import batch
+    for cls, pack in ((M.GroupedArgs, batch._pack_matmul), (M.GroupedWgradArgs, batch._pack_wgrad), (M.VerifyArgs, batch._pack_verify)):
+        v = list(range(1, len(cls._fields_) + 1))
+        assert ctypes.string_at(ctypes.byref(cls(*v)), ctypes.sizeof(cls)).startswith(pack(*v))
+        assert len(pack(*v)) >= max(getattr(cls, n).offset + getattr(cls, n).size for n, _ in cls._fields_)
+
+
+def test_grouped_workspaces(M):
+    assert M.grouped_workspace(100, 64, 1) == 100 * 64 * 2 and M.grouped_workspace(100, 65, 1) == 100 * 72 * 2
+    assert M.grouped_workspace(8, 64, 256) == 0          # few rows are read where they are
+    assert M.grouped_wgrad_workspace(8, 64) == 8 * 64 * 2
+    for bad in ((-1, 64, 1), (2 ** 30 + 1, 64, 1), (100, 0, 1), (100, 64, 0), (100, 64, 1025)):
+        assert M.grouped_workspace(*bad) == 0
 
 
 def test_group_route_workspace_of_bad_sizes(M):
