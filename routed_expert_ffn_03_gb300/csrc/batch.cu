@@ -136,9 +136,9 @@ moe_status run_product(moe::GroupedProblem p, bool wgrad, void* workspace, size_
   if (!wgrad && few_rows(p, d->num_sms, &nt, &cluster) &&
       moe::launch_grouped_few(p, nt, cluster, d->status, s, &e))
     return done(e);
-  // the maps are made once without the copies, which lie no worse, to see that the fast kernel takes the product
+  // before copies are made for it: whether the pair kernel takes the product (the copies lie no worse than the operands)
   moe::GroupedMaps maps;
-  if (p.m > 0 && workspace_bytes >= need_a + need_b && moe::grouped_maps(p, wgrad, &maps)) {
+  if (p.m > 0 && workspace_bytes >= need_a + need_b && (need_a + need_b == 0 || moe::grouped_maps(p, wgrad, false, &maps))) {
     uint16_t* ws = static_cast<uint16_t*>(workspace);
     if (need_a) e = copy_operand(a, p, ws, d->num_sms, s);
     if (need_b && e == cudaSuccess) e = copy_operand(b, p, ws + need_a / 2, d->num_sms, s);

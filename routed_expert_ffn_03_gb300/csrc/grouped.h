@@ -47,15 +47,14 @@ cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, cudaStream_t
 // size it does not take).
 bool tensor_map(CUtensorMap* m, const void* base, size_t elem, int rank, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box);
-// The maps of a product, 64 elements wide: a: the first factor in tiles; b: the second, forward in boxes of 16, 32,
-// 64 and 128 rows, weight gradient [0] in tiles of 64 rows.
+// The maps of a product, 64 elements wide.  a: the first factor in tiles.  b: the second, forward in boxes of 16, 32, 64
+// and 128 rows, weight gradient [0] in tiles of 64 rows; for the few-rows kernel only [0], of one row where rows are named
+// by number.  d: weight gradient: the result, in boxes of 32 rows of 128 bytes (made by the launcher).
 struct GroupedMaps {
-  CUtensorMap a, b[4];
-  CUtensorMap b_row;   // forward: one row
-  CUtensorMap d;   // weight gradient: the result, in boxes of 32 rows of 128 bytes (made by the launcher)
+  CUtensorMap a, b[4], d;
 };
 // False where TMA cannot take the operands as they lie.
-bool grouped_maps(const GroupedProblem& p, bool wgrad, GroupedMaps* m);
+bool grouped_maps(const GroupedProblem& p, bool wgrad, bool few, GroupedMaps* m);
 
 // Copy of the rows named by number: dst[i][0 .. ld_dst) = src[rows[i]][0 .. len), zeros behind len and for a number
 // outside [0, nrows), for the sorted rows i that offsets cover.  src and dst 16-byte aligned, ld_src and ld_dst

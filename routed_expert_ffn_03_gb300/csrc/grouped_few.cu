@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
     *s_abort = 0;
     mbar_fence_init();
     tma_prefetch_map(&maps.a);
-    tma_prefetch_map(p.a_rows ? &maps.b_row : &maps.b[0]);
+    tma_prefetch_map(&maps.b[0]);
   }
   if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), COLS);
   pdl_launch_dependents();
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
       }
       __syncwarp();
       if (p.a_rows) {
-        if (lane < n / 4) tma_gather4(db + lane * 512, &maps.b_row, kb * 64, gr, bar);
+        if (lane < n / 4) tma_gather4(db + lane * 512, &maps.b[0], kb * 64, gr, bar);
       } else if (lane < n / 16) {
         tma_2d<1>(db + lane * 2048, &maps.b[0], kb * 64, r0 + lane * 16, bar);
       }
@@ -367,7 +367,7 @@ cudaError_t grouped_few_set_attributes() {
 
 bool launch_grouped_few(const GroupedProblem& p, int nt, int cluster, uint32_t* status, cudaStream_t s, cudaError_t* err) {
   GroupedMaps m;
-  if (!grouped_maps(p, false, &m)) return false;
+  if (!grouped_maps(p, false, true, &m)) return false;
   FewArgs a;
   a.p = p;
   a.status = status;

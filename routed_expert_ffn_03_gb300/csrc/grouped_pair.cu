@@ -606,7 +606,7 @@ cudaError_t grouped_pair_set_attributes() {
   return e;
 }
 
-bool grouped_maps(const GroupedProblem& p, bool wgrad, GroupedMaps* m) {
+bool grouped_maps(const GroupedProblem& p, bool wgrad, bool few, GroupedMaps* m) {
   const uint64_t lda = p.lda * 2, ldb = p.ldb * 2;
   if (p.a_nrows < 1 || p.a_nrows > 0x7fffffffLL) return false;
   if (wgrad) {
@@ -630,18 +630,21 @@ bool grouped_maps(const GroupedProblem& p, bool wgrad, GroupedMaps* m) {
     ok = tensor_map(&m->a, p.b, 2, 3, d, st, box);
   }
   const uint64_t dx[] = {k, (uint64_t)p.a_nrows};
-  for (int i = 0; i < 4 && ok; ++i) {
+  if (few && p.a_rows) {
+    const uint32_t one[] = {64, 1};
+    return ok && tensor_map(&m->b[0], p.a, 2, 2, dx, &lda, one);
+  }
+  for (int i = 0; i < (few ? 1 : 4) && ok; ++i) {
     const uint32_t tile[] = {64, 16u << i};
     ok = tensor_map(&m->b[i], p.a, 2, 2, dx, &lda, tile);
   }
-  const uint32_t one[] = {64, 1};
-  return ok && tensor_map(&m->b_row, p.a, 2, 2, dx, &lda, one);
+  return ok;
 }
 
 bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, uint32_t* status, cudaStream_t s,
                          cudaError_t* err) {
   GroupedMaps m;
-  if (p.a_rows || p.b_rows || !grouped_maps(p, wgrad, &m)) return false;
+  if (p.a_rows || p.b_rows || !grouped_maps(p, wgrad, false, &m)) return false;
   PairArgs a;
   a.p = p;
   a.status = status;
