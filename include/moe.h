@@ -370,9 +370,10 @@ size_t moe_grouped_wgrad_workspace(long long m, int len);
  *   tokens[b] = the r drafts, the drawn token, then -1 up to D + 1 entries.
  * p [B][D+1][V], q [B][D][V]: probabilities of `dtype` (any moe_dtype), each row summing to about one (8 at
  * most); rows p_row / q_row and sequences p_seq / q_seq elements apart.  q NULL: the drafts came
- * without probabilities (one-hot).  Probabilities and u (meant in [0, 1)) are read as clamped to [0, 1],
- * NaN as 0; u = 1 draws the last v that has any weight.  Products and sums are exact (running sums in 2^-60 steps), so the
- * order of summation decides nothing.  Where the residual is all zero the token is drawn from
+ * without probabilities (one-hot).  u (meant in [0, 1)), a draft's own p and q, and the weights are read as clamped
+ * to [0, 1], NaN as 0; u = 1 draws the last v that has any weight.  The comparison is exact; a weight p - q is rounded
+ * to fp32; running sums are exact in steps of 2^-60, so the order of summation decides nothing.  Where the
+ * residual is all zero the token is drawn from
  * p[b][r]; where that is too, it is -1.  lengths outside [0, D] are taken as the nearer end; a token
  * outside [0, V) is rejected.  draft [B][D] int32, u [B][D+1] fp32, tokens [B][D+1] int32, all
  * contiguous; rows and drafts past a sequence's length are not read.  B >= 1, D 0..31, V 1..2^30. */

@@ -29,6 +29,7 @@ moe_status device_setup(int dev, Device** out) {
   void* word = nullptr;
   if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       moe::grouped_pair_set_attributes() != cudaSuccess || moe::grouped_few_set_attributes() != cudaSuccess ||
+      moe::verify_set_attributes() != cudaSuccess ||
       cudaHostAlloc(&word, sizeof(uint32_t), cudaHostAllocMapped | cudaHostAllocPortable) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ECUDA;
@@ -273,5 +274,5 @@ extern "C" moe_status moe_verify_draft(const moe_verify_args* a, void* stream) {
   Device* d;
   const moe_status st = current_device(&d);
   if (st != MOE_OK) return st;
-  return done(moe::launch_verify(v, (cudaStream_t)stream));
+  return done(moe::launch_verify(v, d->num_sms, (cudaStream_t)stream));
 }

@@ -12,6 +12,7 @@ struct VerifyArgs {
   long long p_seq, p_row, q_seq, q_row;
   int B, D, V, dtype;
 };
-cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
+cudaError_t verify_set_attributes();
+cudaError_t launch_verify(const VerifyArgs& a, int num_sms, cudaStream_t s);
 
 }  // namespace moe

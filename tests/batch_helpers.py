@@ -104,7 +104,8 @@ def route_ref(logits, k, kind):
 
 
 def verify_ref(p, draft, u, q=None, lengths=None):
-    """(accepted, tokens) in exact integers (2^-60 steps, Python's own)."""
+    """(accepted, tokens): comparisons of drafts in fractions; weights are fp32 differences, clamped, summed in
+    exact integers of 2^-60 (Python's own)."""
     from fractions import Fraction
     B, D1, V = p.shape
     D = D1 - 1
@@ -133,7 +134,8 @@ def verify_ref(p, draft, u, q=None, lengths=None):
             if q is None:
                 w = [0 if v == draft[b, r] else a for v, a in enumerate(base)]
             else:
-                w = [max(a - c, 0) for a, c in zip(base, ints(q[b, r]))]
+                with np.errstate(invalid="ignore"):
+                    w = ints((p[b, r].astype(np.float32) - q[b, r].astype(np.float32)).astype(np.float64))
             if sum(w) == 0:
                 w = base
         total = sum(w)
