@@ -29,7 +29,7 @@ moe_status device_setup(int dev, Device** out) {
   void* word = nullptr;
   if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       moe::grouped_pair_set_attributes() != cudaSuccess || moe::grouped_few_set_attributes() != cudaSuccess ||
-      moe::verify_set_attributes() != cudaSuccess ||
+      moe::verify_set_attributes() != cudaSuccess || moe::group_route_set_attributes() != cudaSuccess ||
       cudaHostAlloc(&word, sizeof(uint32_t), cudaHostAllocMapped | cudaHostAllocPortable) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ECUDA;

@@ -1,11 +1,11 @@
 // group_route.cu - router selection of a batch from its logits, pairs grouped by expert.
 //
-// Two kernels.  The first takes a slice of the tokens per block: each warp selects one
-// token's k experts (k rounds of two warp reductions over order-preserving keys of the
-// logits) and writes ids and weights, and the block counts its pairs by expert.  The second
-// takes the same slices: a block sums the counts of the blocks before it, scans the
-// experts' totals into offsets, and places its pairs in order (a stable counting sort: no
-// atomic decides a position, so the same logits give the same arrays).
+// A block takes a slice of the tokens; each warp selects one token's k experts at a time (k rounds of two warp
+// reductions over order-preserving keys of the logits), writes ids and weights, and the block counts its
+// pairs by expert.  Then a block sums the counts of the blocks before it, scans the experts' totals into offsets,
+// and places its pairs in order: a stable counting sort, in which no atomic decides a position, so the same logits give
+// the same arrays.  Up to 64 tokens are one block of one launch; more are two launches over one block of 32 warps an SM, the
+// second waiting for the first on the device.  Bound: latency (the rounds of a selection depend on one another): ROUTE_LATENCY
 #include "common.cuh"
 #include "group_route.h"
 #include "grouped.h"
@@ -15,9 +15,10 @@ namespace moe {
 
 namespace {
 
-constexpr int GR_THREADS = 256;
+constexpr int GR_THREADS = 1024;
 constexpr int GR_WARPS = GR_THREADS / 32;
-constexpr int GR_MAX_BLOCKS = 128;
+constexpr int GR_ONE_BLOCK = 64;      // tokens of the one-launch form: two a warp
+constexpr int GR_COUNTS = 16384;      // counts by warp and expert that a block holds
 
 __device__ __forceinline__ float load_logit(const void* p, long long i, int dtype) {
   if (dtype == GT_FP32) return __ldg(static_cast<const float*>(p) + i);
@@ -78,13 +79,11 @@ __device__ __forceinline__ void token_topk(const GroupRouteArgs& a, long long t,
 }
 
 // one token by one warp: its ids and weights
+template <int NV>
 __device__ __forceinline__ int route_token(const GroupRouteArgs& a, long long t, int lane) {
   int e;
   uint32_t key;
-  if (a.E <= 128) token_topk<4>(a, t, lane, e, key);
-  else if (a.E <= 256) token_topk<8>(a, t, lane, e, key);
-  else if (a.E <= 512) token_topk<16>(a, t, lane, e, key);
-  else token_topk<32>(a, t, lane, e, key);
+  token_topk<NV>(a, t, lane, e, key);
   // softmax over the selected logits, or over their log sigmoids: exp(z_j - z_0) / sum, the
   // first being the largest of both
   const float l = key_logit(key);
@@ -102,38 +101,28 @@ __device__ __forceinline__ int route_token(const GroupRouteArgs& a, long long t,
   return e;
 }
 
-__global__ void __launch_bounds__(GR_THREADS) group_select_kernel(GroupRouteArgs a) {
-  __shared__ int hist[1024];
+// this block's tokens; and its pairs by expert into hist (shared)
+template <int NV>
+__device__ __forceinline__ void select_tokens(const GroupRouteArgs& a, int* hist) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int e = threadIdx.x; e < a.E; e += GR_THREADS) hist[e] = 0;
   __syncthreads();
   const long long t0 = (long long)blockIdx.x * a.per_block, t1 = min(t0 + a.per_block, (long long)a.T);
   for (long long t = t0 + warp; t < t1; t += GR_WARPS) {
-    const int e = route_token(a, t, lane);
+    const int e = route_token<NV>(a, t, lane);
     if (lane < a.k && e >= 0) atomicAdd(&hist[e], 1);   // a count: its order does not matter
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += GR_THREADS) a.hist[(long long)blockIdx.x * a.E + e] = hist[e];
 }
 
-__global__ void __launch_bounds__(GR_THREADS) group_place_kernel(GroupRouteArgs a) {
-  __shared__ int next[GR_WARPS][1024];   // per warp: count by expert, then the next position
-  __shared__ int wsum[GR_WARPS + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
-  for (int i = tid; i < GR_WARPS * 1024; i += GR_THREADS) (&next[0][0])[i] = 0;
-  // expert 4 tid + q: its pairs in earlier blocks and in all of them
-  int before[4] = {0, 0, 0, 0}, all[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int e = 4 * tid + q;
-    if (e < a.E)
-      for (int b = 0; b < a.blocks; ++b) {
-        const int c = __ldcg(a.hist + (long long)b * a.E + e);
-        all[q] += c;
-        if (b < (int)blockIdx.x) before[q] += c;
-      }
-  }
-  const int mine = all[0] + all[1] + all[2] + all[3];
+// Places this block's pairs.  before, all (shared, [E]): an expert's pairs in earlier blocks and in all of them.
+// counts (shared): [W][E], W warps each with a run of the pairs.
+__device__ __forceinline__ void place_pairs(const GroupRouteArgs& a, const int* before, int* all, int* counts) {
+  __shared__ int wsum[GR_WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.E;
+  const int W = min(GR_WARPS, GR_COUNTS / E);
+  // offsets: an exclusive scan of all over the experts, thread e its own
+  const int mine = tid < E ? all[tid] : 0;
   int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -141,50 +130,50 @@ __global__ void __launch_bounds__(GR_THREADS) group_place_kernel(GroupRouteArgs 
     if (lane >= o) inc += v;
   }
   if (lane == 31) wsum[warp] = inc;
+  for (int i = tid; i < W * E; i += GR_THREADS) counts[i] = 0;
   __syncthreads();
-  int off = inc - mine;
-  for (int w = 0; w < warp; ++w) off += wsum[w];
-  int total = 0;
-  for (int w = 0; w < GR_WARPS; ++w) total += wsum[w];
-
-  // this warp's share of the block's pairs
+  int off = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < GR_WARPS; ++w) {
+    if (w < warp) off += wsum[w];
+    total += wsum[w];
+  }
+  if (tid < E) {
+    all[tid] = off;
+    if (blockIdx.x == 0) a.offsets[tid] = off;
+  }
+  if (blockIdx.x == 0 && tid == 0) a.offsets[E] = total;
   const long long P = (long long)a.T * a.k;
   const long long p0 = min((long long)blockIdx.x * a.per_block * a.k, P), p1 = min(p0 + (long long)a.per_block * a.k, P);
-  const long long share = ((p1 - p0 + GR_WARPS - 1) / GR_WARPS + 31) / 32 * 32;
-  const long long q0 = min(p0 + warp * share, p1), q1 = min(q0 + share, p1);
+  const long long share = ((p1 - p0 + W - 1) / W + 31) / 32 * 32;
+  const long long q0 = min(p0 + warp * share, p1), q1 = warp < W ? min(q0 + share, p1) : q0;
+  int* next = counts + warp * E;
   for (long long i = q0 + lane; i < q1; i += 32) {
     const int e = __ldcg(a.idx + i);
-    if (e >= 0) atomicAdd(&next[warp][e], 1);
+    if (e >= 0) atomicAdd(&next[e], 1);
   }
   __syncthreads();
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int e = 4 * tid + q;
-    if (e < a.E) {
-      int pos = off + before[q];
-      for (int w = 0; w < GR_WARPS; ++w) {
-        const int c = next[w][e];
-        next[w][e] = pos;
-        pos += c;
-      }
-      if (blockIdx.x == 0) a.offsets[e] = off;
+  if (tid < E) {   // counts become first positions
+    int pos = all[tid] + before[tid];
+    for (int w = 0; w < W; ++w) {
+      const int c = counts[w * E + tid];
+      counts[w * E + tid] = pos;
+      pos += c;
     }
-    off += all[q];
   }
-  if (blockIdx.x == 0 && tid == 0) a.offsets[a.E] = total;
   __syncthreads();
   for (long long i0 = q0; i0 < q1; i0 += 32) {
     const long long i = i0 + lane;
     const int e = i < q1 ? __ldcg(a.idx + i) : -1;
     const unsigned same = __match_any_sync(0xffffffffu, e);
+    int pos = 0;
+    if (e >= 0) pos = next[e] + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
     if (e >= 0) {
-      const int r = __popc(same & ((1u << lane) - 1u));
-      const int pos = next[warp][e] + r;
       a.pairs[pos] = (int)i;
       a.rows[pos] = (int)(i / a.k);
+      if (lane == 31 - __clz(same)) next[e] = pos + 1;
     }
-    __syncwarp();
-    if (e >= 0 && lane == 31 - __clz(same)) next[warp][e] += __popc(same);
     __syncwarp();
   }
   // no pair stands behind the last group
@@ -194,23 +183,104 @@ __global__ void __launch_bounds__(GR_THREADS) group_place_kernel(GroupRouteArgs 
   }
 }
 
+template <int NV>
+__global__ void __launch_bounds__(GR_THREADS, 1) group_one_kernel(GroupRouteArgs a) {
+  extern __shared__ int counts[];
+  __shared__ int all[1024], before[1024];
+  pdl_wait();
+  select_tokens<NV>(a, all);
+  for (int e = threadIdx.x; e < a.E; e += GR_THREADS) before[e] = 0;
+  __syncthreads();
+  place_pairs(a, before, all, counts);
+}
+
+template <int NV>
+__global__ void __launch_bounds__(GR_THREADS, 1) group_select_kernel(GroupRouteArgs a) {
+  __shared__ int hist[1024];
+  pdl_launch_dependents();
+  pdl_wait();
+  select_tokens<NV>(a, hist);
+  for (int e = threadIdx.x; e < a.E; e += GR_THREADS) a.hist[(long long)blockIdx.x * a.E + e] = hist[e];
+}
+
+__global__ void __launch_bounds__(GR_THREADS, 1) group_place_kernel(GroupRouteArgs a) {
+  extern __shared__ int counts[];
+  __shared__ int all[1024], before[1024];
+  all[threadIdx.x] = before[threadIdx.x] = 0;
+  __syncthreads();
+  pdl_wait();
+  // thread (part, e): an expert's counts of every parts-th block
+  const int Ep = (a.E + 31) & ~31, parts = GR_THREADS / Ep, part = threadIdx.x / Ep, e = threadIdx.x % Ep;
+  if (part < parts && e < a.E) {
+    int s = 0, p = 0;
+#pragma unroll 8
+    for (int b = part; b < a.blocks; b += parts) {
+      const int c = __ldcg(a.hist + (long long)b * a.E + e);
+      s += c;
+      if (b < (int)blockIdx.x) p += c;
+    }
+    atomicAdd(&all[e], s);
+    atomicAdd(&before[e], p);
+  }
+  __syncthreads();
+  place_pairs(a, before, all, counts);
+}
+
+template <typename... A>
+cudaError_t launch(void (*kernel)(A...), int blocks, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(blocks);
+  c.blockDim = dim3(GR_THREADS);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
+template <int NV>
+cudaError_t launch_as(const GroupRouteArgs& a, cudaStream_t s) {
+  const int warps = GR_COUNTS / a.E < GR_WARPS ? GR_COUNTS / a.E : GR_WARPS;
+  const size_t smem = (size_t)warps * a.E * sizeof(int);
+  if (a.blocks == 1) return launch(group_one_kernel<NV>, 1, smem, s, a);
+  cudaError_t e = launch(group_select_kernel<NV>, a.blocks, 0, s, a);
+  return e != cudaSuccess ? e : launch(group_place_kernel, a.blocks, smem, s, a);
+}
+
+template <int NV>
+cudaError_t set_attribute() {
+  return cudaFuncSetAttribute(group_one_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
+}
+
 }  // namespace
 
+cudaError_t group_route_set_attributes() {
+  cudaError_t e = set_attribute<4>();
+  if (e == cudaSuccess) e = set_attribute<8>();
+  if (e == cudaSuccess) e = set_attribute<16>();
+  if (e == cudaSuccess) e = set_attribute<32>();
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(group_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
+  return e;
+}
+
 GroupRoutePlan group_route_plan(int T, int E, int k) {
+  constexpr int kBlocks = 152;   // one an SM; a constant, so that the workspace's size does not depend on the device
   GroupRoutePlan p;
-  p.per_block = (T + GR_MAX_BLOCKS - 1) / GR_MAX_BLOCKS;
-  if (p.per_block < 32) p.per_block = 32;
+  p.per_block = T <= GR_ONE_BLOCK ? T : (T + kBlocks - 1) / kBlocks;
+  if (T > GR_ONE_BLOCK && p.per_block < GR_WARPS) p.per_block = GR_WARPS;
   p.blocks = (T + p.per_block - 1) / p.per_block;
-  p.workspace = (size_t)p.blocks * E * sizeof(int);
+  p.workspace = p.blocks > 1 ? (size_t)p.blocks * E * sizeof(int) : 0;
   return p;
 }
 
-cudaError_t launch_group_route(GroupRouteArgs a, cudaStream_t s) {
-  group_select_kernel<<<a.blocks, GR_THREADS, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  group_place_kernel<<<a.blocks, GR_THREADS, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s) {
+  if (a.E <= 128) return launch_as<4>(a, s);
+  if (a.E <= 256) return launch_as<8>(a, s);
+  return a.E <= 512 ? launch_as<16>(a, s) : launch_as<32>(a, s);
 }
 
 }  // namespace moe

@@ -21,6 +21,7 @@ struct GroupRoutePlan {
   size_t workspace;        // bytes of hist
 };
 GroupRoutePlan group_route_plan(int T, int E, int k);
-cudaError_t launch_group_route(GroupRouteArgs a, cudaStream_t s);
+cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s);
+cudaError_t group_route_set_attributes();
 
 }  // namespace moe

@@ -2,7 +2,7 @@
 //
 // Draft i with token t stands iff u_i q_i(t) < p_i(t); the token after the last that stands
 // is drawn by inverting the running sum of max(p - q, 0) (or of p, when every draft stands).
-// A weight x (p - q rounded to fp32, which changes a weight by 2^-25 of itself at most) is carried as the integer
+// A weight x (p - q rounded to fp32, by 2^-24 of itself at most) is carried as the integer
 // floor(x 2^60) in 64 bits, so sums are exact and the same in any order, and the token is the least v with
 // cum(v) > floor(u total): an integer comparison, with u a 64-bit fraction.
 //
