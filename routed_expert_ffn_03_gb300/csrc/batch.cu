@@ -28,7 +28,7 @@ moe_status device_setup(int dev, Device** out) {
   Device d{0, nullptr};
   void* word = nullptr;
   if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      moe::grouped_pair_set_attributes() != cudaSuccess || moe::grouped_few_set_attributes() != cudaSuccess ||
+      moe::grouped_any_set_attributes() != cudaSuccess || moe::grouped_pair_set_attributes() != cudaSuccess || moe::grouped_few_set_attributes() != cudaSuccess ||
       moe::verify_set_attributes() != cudaSuccess || moe::group_route_set_attributes() != cudaSuccess ||
       cudaHostAlloc(&word, sizeof(uint32_t), cudaHostAllocMapped | cudaHostAllocPortable) != cudaSuccess) {
     cudaGetLastError();
@@ -146,7 +146,7 @@ moe_status run_product(moe::GroupedProblem p, bool wgrad, void* workspace, size_
     if (e != cudaSuccess) return done(e);
     if (moe::launch_grouped_pair(p, wgrad, d->num_sms, d->status, s, &e)) return done(e);
   }
-  return done(moe::launch_grouped_any(p, wgrad, s));
+  return done(moe::launch_grouped_any(p, wgrad, d->status, s));
 }
 
 }  // namespace

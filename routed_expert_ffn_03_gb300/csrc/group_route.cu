@@ -26,67 +26,91 @@ __device__ __forceinline__ float load_logit(const void* p, long long i, int dtyp
   return dtype == GT_BF16 ? bf16_bits_to_float(b) : __half2float(__ushort_as_half(b));
 }
 
-// k rounds: the largest key not yet taken, then the least id holding it (ids ascend with
-// the register index inside a lane, and a lane keeps the first of its equal keys).  Keys at
-// or below `none` are never selected.  Lane j < k receives the j-th id (-1: none left) and key.
-template <int NV>
-__device__ __forceinline__ void select_keys(const uint32_t (&key)[NV], uint32_t none, int k, int lane, int& my_e,
-                                            uint32_t& my_key) {
-  uint32_t taken = 0u, lk = none;
-  int le = 0x7fffffff;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (key[i] > lk) {
-      lk = key[i];
-      le = lane + 32 * i;
-    }
-  my_e = -1;
-  my_key = none;
-  for (int j = 0; j < k; ++j) {
-    const uint32_t bk = __reduce_max_sync(0xffffffffu, lk);
-    if (bk == none) break;   // uniform
-    const int be = (int)__reduce_min_sync(0xffffffffu, lk == bk ? (uint32_t)le : 0xffffffffu);
-    if (lane == j) {
-      my_e = be;
-      my_key = bk;
-    }
-    if (le == be) {
-      taken |= 1u << ((be - lane) >> 5);
-      lk = none;
-      le = 0x7fffffff;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (!((taken >> i) & 1u) && key[i] > lk) {
-          lk = key[i];
-          le = lane + 32 * i;
-        }
-    }
-  }
+__device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : fminf(x, 3.402823466e38f); }
+__device__ __forceinline__ float logit_of(const GroupRouteArgs& a, long long t, int e) {
+  return clean(load_logit(a.logits, t * a.ld + e, a.dtype));
 }
 
+// The k best of one token, by one warp (lane l holds experts l + 32 i): lane j < k receives the j-th id (-1: none left).
+// Keys carry the expert in their low 10 bits, a lower one larger, so each is unique and one warp maximum a round finds the
+// next: only the lane that held it looks for its next best.  16-bit logits fit the 22 bits above; of fp32 logits
+// those are the leading ones, so one more round shows whether two neighbours in the order share them, and such a token
+// (1 or 2 in 100 of random ones) is selected again from whole keys, with a second maximum for the id.
 template <int NV>
-__device__ __forceinline__ void token_topk(const GroupRouteArgs& a, long long t, int lane, int& my_e, uint32_t& my_key) {
+__device__ __forceinline__ int token_topk(const GroupRouteArgs& a, long long t, int lane) {
   uint32_t key[NV];
-  const uint32_t none = logit_key(-INFINITY);
+  uint32_t best = 0;   // 0: below every expert's
+  float l[NV];   // the loads of each type together: a branch around each would run them one after another
+  if (a.dtype == GT_FP32) {
+    const float* src = static_cast<const float*>(a.logits) + t * a.ld;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] = lane + 32 * i < a.E ? __ldg(src + lane + 32 * i) : -INFINITY;
+  } else {
+    const uint16_t* src = static_cast<const uint16_t*>(a.logits) + t * a.ld;
+    uint16_t raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) raw[i] = lane + 32 * i < a.E ? __ldg(src + lane + 32 * i) : 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] = a.dtype == GT_BF16 ? bf16_bits_to_float(raw[i]) : __half2float(__ushort_as_half(raw[i]));
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = lane + 32 * i;
-    float x = e < a.E ? load_logit(a.logits, t * a.ld + e, a.dtype) : -INFINITY;
-    x = x != x ? -INFINITY : fminf(x, 3.402823466e38f);
-    key[i] = logit_key(x);
+    const float x = e < a.E ? clean(l[i]) : -INFINITY;
+    key[i] = x > -INFINITY ? (logit_key(x) & ~1023u) | (uint32_t)(1023 - e) : 0u;
+    best = max(best, key[i]);
   }
-  select_keys<NV>(key, none, a.k, lane, my_e, my_key);
+  uint32_t mine = 0, last = ~0u;
+  bool same = false;
+  const int rounds = a.dtype == GT_FP32 ? min(a.k + 1, a.E) : a.k;
+  for (int j = 0; j < rounds; ++j) {
+    const uint32_t b = __reduce_max_sync(0xffffffffu, best);
+    if (b == 0) break;   // uniform
+    same |= (b ^ last) < 1024u;
+    last = b;
+    if (lane == j && j < a.k) mine = b;
+    if (best == b) {
+      best = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (key[i] == b) key[i] = 0;
+        best = max(best, key[i]);
+      }
+    }
+  }
+  int e = mine ? 1023 - (int)(mine & 1023u) : -1;
+  if (a.dtype == GT_FP32 && same) {   // uniform
+    uint32_t taken = 0;
+    e = -1;
+    for (int j = 0; j < a.k; ++j) {
+      uint32_t lk = 0;
+      int le = 0x7fffffff;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int ee = lane + 32 * i;
+        const float x = ee < a.E && !((taken >> i) & 1u) ? logit_of(a, t, ee) : -INFINITY;
+        if (x > -INFINITY && logit_key(x) > lk) {   // ascending ids: the first of equal keys stays
+          lk = logit_key(x);
+          le = ee;
+        }
+      }
+      const uint32_t bk = __reduce_max_sync(0xffffffffu, lk);
+      if (bk == 0) break;
+      const int be = (int)__reduce_min_sync(0xffffffffu, lk == bk ? (uint32_t)le : 0xffffffffu);
+      if (lane == j) e = be;
+      if (le == be && lk == bk) taken |= 1u << ((be - lane) >> 5);
+    }
+  }
+  return e;
 }
 
 // one token by one warp: its ids and weights
 template <int NV>
 __device__ __forceinline__ int route_token(const GroupRouteArgs& a, long long t, int lane) {
-  int e;
-  uint32_t key;
-  token_topk<NV>(a, t, lane, e, key);
+  const int e = token_topk<NV>(a, t, lane);
   // softmax over the selected logits, or over their log sigmoids: exp(z_j - z_0) / sum, the
   // first being the largest of both
-  const float l = key_logit(key);
+  const float l = e >= 0 ? logit_of(a, t, e) : 0.f;
   float z = l;
   if (a.kind == 1) z = fminf(l, 0.f) - log1pf(expf(-fabsf(l)));
   const float z0 = __shfl_sync(0xffffffffu, z, 0);
@@ -213,8 +237,11 @@ __global__ void __launch_bounds__(GR_THREADS, 1) group_place_kernel(GroupRouteAr
   const int Ep = (a.E + 31) & ~31, parts = GR_THREADS / Ep, part = threadIdx.x / Ep, e = threadIdx.x % Ep;
   if (part < parts && e < a.E) {
     int s = 0, p = 0;
-#pragma unroll 8
-    for (int b = part; b < a.blocks; b += parts) {
+    // each block starts at another row, so that they do not all read the same lines at once
+    const int n = (a.blocks - part + parts - 1) / parts, start = n > 0 ? (int)(blockIdx.x % n) : 0;
+#pragma unroll 16
+    for (int i = 0; i < n; ++i) {
+      const int r = i + start < n ? i + start : i + start - n, b = part + r * parts;
       const int c = __ldcg(a.hist + (long long)b * a.E + e);
       s += c;
       if (b < (int)blockIdx.x) p += c;

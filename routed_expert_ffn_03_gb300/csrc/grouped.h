@@ -40,7 +40,9 @@ __device__ __forceinline__ void group_range(const int* offsets, int g, long long
 }
 #endif
 
-cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, cudaStream_t s);
+// For any strides and alignment.  status: host-visible word that a wait which ran out sets.
+cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, uint32_t* status, cudaStream_t s);
+cudaError_t grouped_any_set_attributes();
 
 // A tensor map over elements of 2 or 4 bytes, 128-byte swizzled, zeros outside: dims and box in elements, innermost
 // first; strides (of dims 1 ..) in bytes.  False where the hardware cannot address the tensor so (a base, stride or
@@ -69,7 +71,6 @@ struct RowCopy {
 cudaError_t launch_copy_rows(const RowCopy& c, int num_sms, cudaStream_t s);
 
 // The tensor-core kernel over pairs of SMs; false (nothing launched) where TMA cannot take the operands.
-// status: host-visible word that a wait which ran out sets.
 bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, uint32_t* status, cudaStream_t s,
                          cudaError_t* err);
 cudaError_t grouped_pair_set_attributes();

@@ -1,34 +1,99 @@
 // grouped_any.cu - grouped 16-bit products for any stride, alignment and size.
 //
-// D_e = A_e B_e^T for every group e (see GroupedProblem): a block takes one 64 x 64 tile of
-// one group and walks the contracted dimension in steps of 32 with plain loads, so nothing
-// is asked of strides or addresses.  Elements are read along whichever dimension is
-// contiguous and stored in shared memory with the contracted dimension contiguous; rows
-// and columns outside the group, and row numbers outside their array, are stored as zeros.
-// Each of 4 warps multiplies a 32 x 32 quarter with mma m16n8k16 (fp32 sums).
-#include "common.cuh"
+// What the TMA kernels refuse (rows whose pitch or start is not a multiple of 16 bytes, odd widths, several experts
+// on one matrix) is staged here by warps with plain loads, into the same swizzled shared-memory tiles,
+// so the products still run on the tensor core.  A block takes one tile of 128 x 64 of a group and steps of 64
+// contracted elements.  An operand word of 16 bytes that does not start on a 16-byte boundary is put together from the
+// two aligned words around it (one of the two comes from L1: the neighbour lane's), unless those reach past the
+// tensor's first or last byte: then it is read by elements.  Words behind the contracted length, rows of no group and row
+// numbers outside their tensor are stored as zeros.  Warps:
+//   warps 0..7   load (one step ahead in registers) and store into a ring of 4 stages;
+//   warp 8       issues the products, in parts of 512 elements in alternating results;
+//   warps 9..12  add the parts up in fp32 registers, then store the tile by elements.
+// Bound: the loads and shared-memory stores of the staging, ANY_RATE
 #include "grouped.h"
+#include "grouped_mma.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int GA_T = 64;        // tile rows and columns
-constexpr int GA_K = 32;        // contracted elements per step
-constexpr int GA_LD = GA_K + 8; // shared row: 20 words, so a fragment's 8 rows x 4 words hit 32 banks
-constexpr int GA_THREADS = 128;
-
 enum : int { GA_NK = 0, GA_KN = 1, GA_SWIGLU = 2, GA_WGRAD = 3 };
+constexpr int GA_M = 128, GA_N = 64;             // tile: rows of the first factor and of the second
+constexpr int GA_A = GA_M * 128, GA_B = GA_N * 128, GA_STAGE = GA_A + GA_B;   // bytes of a stage: 64 elements a row
+constexpr int GA_STAGES = 4;
+constexpr int GA_COPY_WARPS = 8, GA_EPI_WARPS = 4;
+constexpr int GA_THREADS = (GA_COPY_WARPS + 1 + GA_EPI_WARPS) * 32;
+// 16-byte words of the factors that a thread stages
+constexpr int GA_AW = GA_M * 8 / (GA_COPY_WARPS * 32), GA_BW = GA_N * 8 / (GA_COPY_WARPS * 32);
+constexpr int GA_PART = 8;                      // stages of a part
+constexpr int GA_SMEM = GA_STAGES * GA_STAGE + 256 + 1024;
 
-template <bool BF>
-__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (BF)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    mma_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+struct AnyArgs {
+  GroupedProblem p;
+  uint32_t* status;
+};
+
+// 8 elements at s (null: zeros), zeros from `left` on, as the two aligned words around them, or finished in the first
+struct Word8 {
+  uint4 a, b;
+  int shift;   // bytes from a's first to the first wanted
+};
+__device__ __forceinline__ uint4 by_elements(const uint16_t* s, int n) {
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) w[i >> 1] |= (uint32_t)__ldg(s + i) << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 load_if(bool live, uintptr_t at) {
+  uint4 v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
+      " @p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "l"(at), "r"((uint32_t)live));
+  return v;
+}
+// N words of one factor.  lo, hi: the tensor's first byte and the one behind its last.  Where all of the warp's words are whole
+// and both aligned words of each inside the tensor, the loads stand side by side without a branch.
+template <int N>
+__device__ __forceinline__ void load_words(const uint16_t* const (&s)[N], int left, uintptr_t lo, uintptr_t hi, Word8 (&w)[N]) {
+  bool whole = true;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uintptr_t at = (uintptr_t)s[i] & ~(uintptr_t)15;
+    whole = whole && (!s[i] || (left >= 8 && at >= lo && at + 32 <= hi));
+  }
+  if (__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uintptr_t at = (uintptr_t)s[i] & ~(uintptr_t)15;
+      w[i].shift = (int)((uintptr_t)s[i] & 15);
+      w[i].a = load_if(s[i] != nullptr, at);
+      w[i].b = load_if(s[i] != nullptr, at + 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      w[i].shift = 0;
+      w[i].a = w[i].b = make_uint4(0, 0, 0, 0);
+      if (s[i] && left > 0) w[i].a = by_elements(s[i], min(left, 8));
+    }
+  }
+}
+__device__ __forceinline__ uint4 finish8(const Word8& w) {
+  const uint32_t v[8] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b.x, w.b.y, w.b.z, w.b.w};
+  const int by = 8 * (w.shift & 3);
+  const bool two = w.shift & 8, one = w.shift & 4;   // by halves: 8 bytes, then 4
+  uint32_t x[6], y[5], r[4];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) x[i] = two ? v[i + 2] : v[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) y[i] = one ? x[i + 1] : x[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = __funnelshift_r(y[i], y[i + 1], by);
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 __device__ __forceinline__ void store_out(void* d, long long at, float v, int t) {
@@ -37,193 +102,290 @@ __device__ __forceinline__ void store_out(void* d, long long at, float v, int t)
   else static_cast<__half*>(d)[at] = __float2half_rn(v);
 }
 
-template <int MODE, bool BF>
-__global__ void __launch_bounds__(GA_THREADS) grouped_any_kernel(GroupedProblem p) {
+template <int MODE>
+__global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid_constant__ AnyArgs args) {
   constexpr bool WG = MODE == GA_WGRAD, SW = MODE == GA_SWIGLU;
-  constexpr int NB = SW ? 2 : 1;
-  __shared__ __align__(16) uint16_t as[GA_T * GA_LD];
-  __shared__ __align__(16) uint16_t bs[NB][GA_T * GA_LD];
-  __shared__ int s_tile[4];
+  // factor A: dw's n (weight gradient) or W_e's features; factor B: dw's k, or the group's rows.  MN-major: the contracted
+  // dimension is not the contiguous one.
+  constexpr bool a_mn = WG || MODE == GA_KN, b_mn = WG;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const GroupedProblem& p = args.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_out = SW ? p.n / 2 : p.n;
 
-  // the tile: forward (group, row tile) x column tile; weight gradient group x row tile x column tile
-  int r0, r1, e, a0, b0;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + GA_STAGES * GA_STAGE);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * GA_STAGES + 4);
+  int* s_tile = reinterpret_cast<int*>(tmem_slot + 1);
+  volatile int* s_abort = s_tile + 3;
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * GA_STAGES, tfull0 = empty0 + 8 * GA_STAGES, tempty0 = tfull0 + 16;
+  if (tid == 0) {
+    for (int s = 0; s < GA_STAGES; ++s) {
+      mbar_init(full0 + 8 * s, GA_COPY_WARPS);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tempty0 + 8 * b, GA_EPI_WARPS);
+    }
+    *s_abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == GA_COPY_WARPS) tmem_alloc<1>(smem_u32(tmem_slot), 2 * GA_N);
+
+  // the tile: forward (group, row tile) x feature tile; weight gradient group x n tile x k tile
+  int e, r0, r1, a0, b0 = 0;
   if (WG) {
-    const int ta = (p.n + GA_T - 1) / GA_T, tb = (p.k + GA_T - 1) / GA_T;
-    const int per = ta * tb;
+    const int tb = (p.k + GA_N - 1) / GA_N, per = (p.n + GA_M - 1) / GA_M * tb;
     e = blockIdx.x / per;
-    a0 = (blockIdx.x % per) / tb * GA_T;
-    b0 = (blockIdx.x % per) % tb * GA_T;
+    a0 = blockIdx.x % per / tb * GA_M;
+    b0 = blockIdx.x % per % tb * GA_N;
     group_range(p.offsets, e, p.m, r0, r1);
   } else {
-    const int tb = (n_out + GA_T - 1) / GA_T;
-    const int want = blockIdx.x / tb;
-    b0 = blockIdx.x % tb * GA_T;
-    if (warp == 0) {   // the want-th row tile over the groups
-      int before = 0, found = -1, fr0 = 0, fr1 = 0;
-      for (int g0 = 0; g0 < p.groups && found < 0; g0 += 32) {
-        int gr0 = 0, gr1 = 0;
-        if (g0 + lane < p.groups) group_range(p.offsets, g0 + lane, p.m, gr0, gr1);
-        const int nt = (gr1 - gr0) / GA_T + ((gr1 - gr0) % GA_T != 0);
-        int inc = nt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += v;
-        }
-        const bool mine = want >= before + inc - nt && want < before + inc;
-        const unsigned who = __ballot_sync(0xffffffffu, mine);
-        if (who) {
-          const int l = __ffs(who) - 1;
-          found = g0 + l;
-          fr0 = __shfl_sync(0xffffffffu, gr0 + (want - before - inc + nt) * GA_T, l);
-          fr1 = __shfl_sync(0xffffffffu, gr1, l);
-        }
-        before += __shfl_sync(0xffffffffu, inc, 31);
-      }
+    constexpr int F = SW ? GA_M / 2 : GA_M;
+    const int ta = (n_out + F - 1) / F;
+    a0 = blockIdx.x % ta * F;
+    if (warp == 0) {
+      find_tile(p, GA_N, blockIdx.x / ta, lane, e, r0, r1);
       if (lane == 0) {
-        s_tile[0] = found;
-        s_tile[1] = fr0;
-        s_tile[2] = fr1;
+        s_tile[0] = e;
+        s_tile[1] = r0;
+        s_tile[2] = r1;
       }
     }
-    __syncthreads();
+  }
+  umma_fence_before();
+  __syncthreads();
+  umma_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (!WG) {
     e = s_tile[0];
-    if (e < 0) return;
     r0 = s_tile[1];
-    r1 = min(s_tile[2], r0 + GA_T);
-    a0 = 0;
+    r1 = s_tile[2];
   }
+  const int rows = r1 - r0;
+  const int kdim = e < 0 ? 0 : WG ? rows : p.k, nkb = (kdim + 63) / 64;
+  const int cols = WG ? GA_N : (rows + 15) & ~15;   // columns of the product
 
-  const int kdim = WG ? r1 - r0 : p.k;   // contracted length
-  const int am = WG ? p.n - a0 : r1 - r0;   // rows of A left from the tile's first
-  const int bm = (WG ? p.k : n_out) - b0;   // rows of B left
-  float acc[NB][2][4][4];
+  if (warp < GA_COPY_WARPS) {
+    // ---------------------------------------------------------------- staging
+    // K-major: thread: word c of rows r + 32 i.  MN-major: word c (in slabs of 8) of contracted rows r + step i.
+    const uintptr_t a_lo = (uintptr_t)(WG ? p.a : p.b), b_lo = (uintptr_t)(WG ? p.b : p.a);
+    const uintptr_t a_hi = a_lo + 2 * (WG ? (p.a_nrows - 1) * p.lda + p.n
+                                          : (p.groups - 1) * p.b_stride + ((p.kn ? p.k : p.n) - 1) * p.ldb + (p.kn ? p.n : p.k));
+    const uintptr_t b_hi = b_lo + 2 * (WG ? (p.b_nrows - 1) * p.ldb + p.k : (p.a_nrows - 1) * p.lda + p.k);
+    const int ca = a_mn ? tid & 15 : tid & 7, ra = a_mn ? tid >> 4 : tid >> 3;
+    const int cb = tid & 7, rb = tid >> 3;
+    constexpr int step_a = a_mn ? 16 : 32, step_b = 32;
+    const uint16_t* a_row[GA_AW];   // K-major: the rows' starts, null for a row of zeros
+    const uint16_t* b_row[GA_BW];
+    const uint16_t* w = p.b + (WG ? 0 : (long long)e * p.b_stride);
+    auto row_at = [&](const uint16_t* base, const int* list, long long i, long long n, long long ld) -> const uint16_t* {
+      const long long row = list ? __ldg(list + i) : i;
+      return row >= 0 && row < n ? base + row * ld : nullptr;
+    };
 #pragma unroll
-  for (int x = 0; x < NB; ++x)
+    for (int i = 0; i < GA_AW; ++i) {
+      const int r = ra + step_a * i, f = SW ? a0 + (r >> 5) * 16 + (r & 15) : a0 + r;   // swiglu: 16 rows of gate, then 16 of up
+      a_row[i] = !a_mn && f < n_out ? w + (long long)(SW && (r & 16) ? f + n_out : f) * p.ldb : nullptr;
+    }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < GA_BW; ++i) {
+      const int r = rb + step_b * i;
+      b_row[i] = !b_mn && r < rows ? row_at(p.a, p.a_rows, r0 + r, p.a_nrows, p.lda) : nullptr;
+    }
+    Word8 va[GA_AW], vb[GA_BW];
+    auto load = [&](int kb) {
+      const uint16_t* s[GA_AW];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[x][i][j][q] = 0.f;
-
-  const long long wbase = WG ? 0 : (long long)e * p.b_stride;
-  for (int k0 = 0; k0 < kdim; k0 += GA_K) {
-    uint16_t va[GA_T * GA_K / GA_THREADS], vb[NB][GA_T * GA_K / GA_THREADS];
-#pragma unroll
-    for (int i = 0; i < GA_T * GA_K / GA_THREADS; ++i) {
-      const int kc = tid & 31, rc = (tid >> 5) + 4 * i;   // contracted dimension contiguous
-      const int mm = tid & 63, km = (tid >> 6) + 2 * i;   // the other one contiguous
-      uint16_t v = 0;
-      if (WG) {
-        if (mm < am && k0 + km < kdim) {
-          const long long row = p.a_rows ? __ldg(p.a_rows + r0 + k0 + km) : r0 + k0 + km;
-          if (row >= 0 && row < p.a_nrows) v = __ldg(p.a + row * p.lda + a0 + mm);
+      for (int i = 0; i < GA_AW; ++i) {
+        if (a_mn) {
+          const int k = kb * 64 + ra + step_a * i;
+          const uint16_t* row = nullptr;
+          if (k < kdim) row = WG ? row_at(p.a, p.a_rows, r0 + k, p.a_nrows, p.lda) : w + (long long)k * p.ldb;
+          s[i] = row ? row + a0 + ca * 8 : nullptr;
+        } else {
+          s[i] = a_row[i] ? a_row[i] + kb * 64 + ca * 8 : nullptr;
         }
-      } else if (rc < am && k0 + kc < kdim) {
-        const long long row = p.a_rows ? __ldg(p.a_rows + r0 + rc) : r0 + rc;
-        if (row >= 0 && row < p.a_nrows) v = __ldg(p.a + row * p.lda + k0 + kc);
       }
-      va[i] = v;
+      load_words(s, a_mn ? (WG ? p.n : n_out) - a0 - ca * 8 : kdim - kb * 64 - ca * 8, a_lo, a_hi, va);
+      const uint16_t* t[GA_BW];
 #pragma unroll
-      for (int x = 0; x < NB; ++x) {
-        v = 0;
-        if (WG) {
-          if (mm < bm && k0 + km < kdim) {
-            const long long row = p.b_rows ? __ldg(p.b_rows + r0 + k0 + km) : r0 + k0 + km;
-            if (row >= 0 && row < p.b_nrows) v = __ldg(p.b + row * p.ldb + b0 + mm);
-          }
-        } else if (MODE == GA_KN) {
-          if (mm < bm && k0 + km < kdim) v = __ldg(p.b + wbase + (long long)(k0 + km) * p.ldb + b0 + mm);
-        } else if (rc < bm && k0 + kc < kdim) {
-          v = __ldg(p.b + wbase + (long long)(b0 + rc + x * n_out) * p.ldb + k0 + kc);
+      for (int i = 0; i < GA_BW; ++i) {
+        if (b_mn) {
+          const int k = kb * 64 + rb + step_b * i;
+          const uint16_t* row = k < kdim ? row_at(p.b, p.b_rows, r0 + k, p.b_nrows, p.ldb) : nullptr;
+          t[i] = row ? row + b0 + cb * 8 : nullptr;
+        } else {
+          t[i] = b_row[i] ? b_row[i] + kb * 64 + cb * 8 : nullptr;
         }
-        vb[x][i] = v;
+      }
+      load_words(t, b_mn ? p.k - b0 - cb * 8 : kdim - kb * 64 - cb * 8, b_lo, b_hi, vb);
+    };
+    const uint32_t at_a = (a_mn ? (ca >> 3) * SLAB_BYTES : 0) + ra * 128 + (((ca & 7) ^ (ra & 7)) << 4);
+    const uint32_t at_b = rb * 128 + ((cb ^ (rb & 7)) << 4);
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    if (nkb > 0) load(0);
+    for (int kb = 0; kb < nkb; ++kb) {
+      ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1));
+      if (!ok) break;
+      uint8_t* st = smem + s * GA_STAGE;
+#pragma unroll
+      for (int i = 0; i < GA_AW; ++i) *reinterpret_cast<uint4*>(st + at_a + i * step_a * 128) = finish8(va[i]);
+#pragma unroll
+      for (int i = 0; i < GA_BW; ++i) *reinterpret_cast<uint4*>(st + GA_A + at_b + i * step_b * 128) = finish8(vb[i]);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full0 + 8 * s);
+      if (kb + 1 < nkb) load(kb + 1);
+      if (++s == GA_STAGES) {
+        s = 0;
+        ph ^= 1;
       }
     }
-    __syncthreads();   // the step before has been multiplied
+    if (!ok && lane == 0) *s_abort = 1;
+  } else if (warp == GA_COPY_WARPS) {
+    // ---------------------------------------------------------------- products
+    const bool leader = elect_one();
+    constexpr uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+    const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t da0 = sw128_desc(base, a_mn), db0 = sw128_desc(base + GA_A, b_mn);
+    const uint32_t idesc = idesc_16(p.dtype == GT_BF16, a_mn, b_mn, GA_M, __shfl_sync(0xffffffffu, cols, 0));
+    int s = 0, acc = 0;
+    uint32_t ph = 0, aph = 0;
+    bool ok = true;
+    for (int k0 = 0; k0 < nkb && ok; k0 += GA_PART) {
+      const int k1 = min(k0 + GA_PART, nkb);
+      ok = __all_sync(0xffffffffu, wait_bar(tempty0 + 8 * acc, aph ^ 1));
+      umma_fence_after();
+      for (int kb = k0; kb < k1 && ok; ++kb) {
+        ok = __all_sync(0xffffffffu, wait_bar(full0 + 8 * s, ph));
+        if (!ok) break;
+        umma_fence_after();
+        const uint32_t off = s * (GA_STAGE >> 4);
+        if (leader) {
 #pragma unroll
-    for (int i = 0; i < GA_T * GA_K / GA_THREADS; ++i) {
-      const int kc = tid & 31, rc = (tid >> 5) + 4 * i;
-      const int mm = tid & 63, km = (tid >> 6) + 2 * i;
-      as[WG ? mm * GA_LD + km : rc * GA_LD + kc] = va[i];
-#pragma unroll
-      for (int x = 0; x < NB; ++x) bs[x][WG || MODE == GA_KN ? mm * GA_LD + km : rc * GA_LD + kc] = vb[x][i];
-    }
-    __syncthreads();
-    const int g = lane >> 2, t = lane & 3, m0 = (warp >> 1) * 32, n0 = (warp & 1) * 32;
-#pragma unroll
-    for (int kk = 0; kk < GA_K; kk += 16) {
-      uint32_t af[2][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          af[i][q] = *reinterpret_cast<const uint32_t*>(as + (m0 + i * 16 + g + (q & 1) * 8) * GA_LD + kk + 2 * t +
-                                                        (q >> 1) * 8);
-#pragma unroll
-      for (int x = 0; x < NB; ++x)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint16_t* br = bs[x] + (n0 + j * 8 + g) * GA_LD + kk + 2 * t;
-          const uint32_t bf0 = *reinterpret_cast<const uint32_t*>(br);
-          const uint32_t bf1 = *reinterpret_cast<const uint32_t*>(br + 8);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) mma16<BF>(acc[x][i][j], af[i], bf0, bf1);
+          for (int kk = 0; kk < 4; ++kk)
+            umma<1>(tm + acc * GA_N, da0 + off + kk * a_step, db0 + off + kk * b_step, idesc, kb > k0 || kk > 0);
+          umma_commit(empty0 + 8 * s);
         }
+        __syncwarp();
+        if (++s == GA_STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (leader) umma_commit(tfull0 + 8 * acc);
+      __syncwarp();
+      if (++acc == 2) {
+        acc = 0;
+        aph ^= 1;
+      }
+    }
+    if (!ok && lane == 0) *s_abort = 1;
+  } else if (e >= 0) {
+    // ---------------------------------------------------------------- results
+    const int quarter = warp & 3;   // of the TMEM lanes
+    const uint32_t td = tmem + ((uint32_t)(quarter * 32) << 16);
+    float sum[GA_N];
+#pragma unroll
+    for (int i = 0; i < GA_N; ++i) sum[i] = 0.f;
+    int acc = 0;
+    uint32_t aph = 0;
+    bool ok = true;
+    for (int k0 = 0; k0 < nkb; k0 += GA_PART) {
+      ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, aph));
+      if (!ok) break;
+      umma_fence_after();
+#pragma unroll
+      for (int c = 0; c < GA_N; c += 16) {
+        if (c < cols) {
+          float v[16];
+          tmem_ld16(td + acc * GA_N + c, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[c + i] += v[i];
+        }
+      }
+      umma_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty0 + 8 * acc);
+      if (++acc == 2) {
+        acc = 0;
+        aph ^= 1;
+      }
+    }
+    if (!ok && lane == 0) *s_abort = 1;
+    if (ok && WG) {
+      const int n = a0 + quarter * 32 + lane, k = b0;
+      const long long at = (long long)e * p.d_stride + (long long)n * p.ldd + k;
+#pragma unroll
+      for (int i = 0; i < GA_N; ++i)
+        if (n < p.n && k + i < p.k) store_out(p.d, at + i, sum[i], p.out_dtype);
+    } else if (ok) {
+      const int f = SW ? a0 + quarter * 16 + (lane & 15) : a0 + quarter * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < GA_N; ++i) {
+        float v = sum[i];
+        if (SW) {   // lanes 0..15 hold gate, 16..31 up
+          const float u = __shfl_down_sync(0xffffffffu, v, 16);
+          v = __fdividef(v, 1.f + expf(-v)) * u;
+        }
+        if (i < rows && f < n_out && !(SW && lane >= 16)) {
+          const long long row = p.d_rows ? __ldg(p.d_rows + r0 + i) : r0 + i;
+          if (row >= 0 && row < p.d_nrows) store_out(p.d, row * p.ldd + f, v, p.out_dtype);
+        }
+      }
     }
   }
-
-  const int g = lane >> 2, t = lane & 3, m0 = (warp >> 1) * 32, n0 = (warp & 1) * 32;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = m0 + i * 16 + g + h * 8;
-      if (r >= am) continue;
-      long long at;
-      if (WG) {
-        at = (long long)e * p.d_stride + (long long)(a0 + r) * p.ldd;
-      } else {
-        const long long row = p.d_rows ? __ldg(p.d_rows + r0 + r) : r0 + r;
-        if (row < 0 || row >= p.d_nrows) continue;
-        at = row * p.ldd;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int c = n0 + j * 8 + 2 * t + q;
-          if (c >= bm) continue;
-          float v = acc[0][i][j][2 * h + q];
-          if (SW) v = v / (1.f + expf(-v)) * acc[NB - 1][i][j][2 * h + q];
-          store_out(p.d, at + b0 + c, v, p.out_dtype);
-        }
+  umma_fence_before();
+  __syncthreads();
+  if (*s_abort) {   // a wait ran out: report, and let what is in flight end before the memory goes
+    if (tid == 0) {
+      *reinterpret_cast<volatile uint32_t*>(args.status) = ST_TIMEOUT;
+      __threadfence_system();
     }
+    drain_time();
+  }
+  umma_fence_after();
+  if (warp == GA_COPY_WARPS) tmem_dealloc<1>(tmem, 2 * GA_N);
 }
 
 template <int MODE>
-cudaError_t launch_mode(const GroupedProblem& p, unsigned blocks, cudaStream_t s) {
-  if (p.dtype == GT_BF16) grouped_any_kernel<MODE, true><<<blocks, GA_THREADS, 0, s>>>(p);
-  else grouped_any_kernel<MODE, false><<<blocks, GA_THREADS, 0, s>>>(p);
+cudaError_t launch_mode(const AnyArgs& a, unsigned blocks, cudaStream_t s) {
+  grouped_any_kernel<MODE><<<blocks, GA_THREADS, GA_SMEM, s>>>(a);
   return cudaGetLastError();
 }
+template <int MODE>
+cudaError_t set_attribute() {
+  return cudaFuncSetAttribute(grouped_any_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, GA_SMEM);
+}
 
-long long tiles(long long v) { return (v + GA_T - 1) / GA_T; }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, cudaStream_t s) {
-  // forward: every group can end inside a tile, so there are at most m / 64 + min(groups, m) row tiles
-  const long long blocks = wgrad ? (long long)p.groups * tiles(p.n) * tiles(p.k)
-                                 : (p.m / GA_T + (p.m < p.groups ? p.m : p.groups)) * tiles(p.swiglu ? p.n / 2 : p.n);
+cudaError_t grouped_any_set_attributes() {
+  cudaError_t e = set_attribute<GA_NK>();
+  if (e == cudaSuccess) e = set_attribute<GA_KN>();
+  if (e == cudaSuccess) e = set_attribute<GA_SWIGLU>();
+  if (e == cudaSuccess) e = set_attribute<GA_WGRAD>();
+  return e;
+}
+
+cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, uint32_t* status, cudaStream_t s) {
+  // forward: every group can end inside a tile, so m rows make at most m / 64 + min(groups, m) row tiles
+  const long long blocks =
+      wgrad ? (long long)p.groups * ceil_div(p.n, GA_M) * ceil_div(p.k, GA_N)
+            : (p.m / GA_N + (p.m < p.groups ? p.m : p.groups)) * ceil_div(p.swiglu ? p.n / 2 : p.n, p.swiglu ? GA_M / 2 : GA_M);
   if (blocks <= 0) return cudaSuccess;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (wgrad) return launch_mode<GA_WGRAD>(p, (unsigned)blocks, s);
-  if (p.swiglu) return launch_mode<GA_SWIGLU>(p, (unsigned)blocks, s);
-  return p.kn ? launch_mode<GA_KN>(p, (unsigned)blocks, s) : launch_mode<GA_NK>(p, (unsigned)blocks, s);
+  const AnyArgs a{p, status};
+  if (wgrad) return launch_mode<GA_WGRAD>(a, (unsigned)blocks, s);
+  if (p.swiglu) return launch_mode<GA_SWIGLU>(a, (unsigned)blocks, s);
+  return p.kn ? launch_mode<GA_KN>(a, (unsigned)blocks, s) : launch_mode<GA_NK>(a, (unsigned)blocks, s);
 }
 
 }  // namespace moe

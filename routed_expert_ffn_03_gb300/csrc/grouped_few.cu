@@ -37,50 +37,6 @@ struct FewArgs {
   bool wide;            // 16-bit results can be stored in pairs
 };
 
-// The want-th tile of up to NT rows over the groups, by one warp: its group and rows (e = -1: there is none).  Each lane
-// counts a run of consecutive groups.
-template <int NT>
-__device__ __forceinline__ void find_tile(const GroupedProblem& p, int want, int lane, int& e, int& r0, int& r1) {
-  const int run = (p.groups + 31) / 32, g0 = lane * run, g1 = min(g0 + run, p.groups);
-  int mine = 0;
-#pragma unroll 8
-  for (int g = g0; g < g1; ++g) {
-    int a, b;
-    group_range(p.offsets, g, p.m, a, b);
-    mine += (b - a + NT - 1) / NT;
-  }
-  int inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  const int before = inc - mine;
-  const unsigned who = __ballot_sync(0xffffffffu, want >= before && want < inc);
-  e = -1;
-  r0 = r1 = 0;
-  if (!who) return;
-  const int l = __ffs(who) - 1;
-  if (lane == l) {
-    int left = want - before;
-    for (int g = g0; g < g1; ++g) {
-      int a, b;
-      group_range(p.offsets, g, p.m, a, b);
-      const int nt = (b - a + NT - 1) / NT;
-      if (left < nt) {
-        e = g;
-        r0 = a + left * NT;
-        r1 = min(b, r0 + NT);
-        break;
-      }
-      left -= nt;
-    }
-  }
-  e = __shfl_sync(0xffffffffu, e, l);
-  r0 = __shfl_sync(0xffffffffu, r0, l);
-  r1 = __shfl_sync(0xffffffffu, r1, l);
-}
-
 __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
   float2 v;
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
@@ -124,7 +80,7 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
   const int tile = blockIdx.x / C;
   if (warp == 0) {
     int e, r0, r1;
-    find_tile<NT>(p, tile / a.nft, lane, e, r0, r1);
+    find_tile(p, NT, tile / a.nft, lane, e, r0, r1);
     if (lane == 0) {
       s_tile[0] = e;
       s_tile[1] = r0;

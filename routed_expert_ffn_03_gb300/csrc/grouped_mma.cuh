@@ -121,6 +121,50 @@ __device__ __forceinline__ uint32_t pack_out(float lo, float hi, int dtype) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// ---------------------------------------------------------------- tiles
+// The want-th tile of up to nt_rows rows over the groups, by one warp: its group and rows (e = -1: there is none).  Each lane
+// counts a run of consecutive groups.
+__device__ __forceinline__ void find_tile(const GroupedProblem& p, int nt_rows, int want, int lane, int& e, int& r0, int& r1) {
+  const int run = (p.groups + 31) / 32, g0 = lane * run, g1 = min(g0 + run, p.groups);
+  int mine = 0;
+#pragma unroll 8
+  for (int g = g0; g < g1; ++g) {
+    int a, b;
+    group_range(p.offsets, g, p.m, a, b);
+    mine += (b - a + nt_rows - 1) / nt_rows;
+  }
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  const int before = inc - mine;
+  const unsigned who = __ballot_sync(0xffffffffu, want >= before && want < inc);
+  e = -1;
+  r0 = r1 = 0;
+  if (!who) return;
+  const int l = __ffs(who) - 1;
+  if (lane == l) {
+    int left = want - before;
+    for (int g = g0; g < g1; ++g) {
+      int a, b;
+      group_range(p.offsets, g, p.m, a, b);
+      const int nt = (b - a + nt_rows - 1) / nt_rows;
+      if (left < nt) {
+        e = g;
+        r0 = a + left * nt_rows;
+        r1 = min(b, r0 + nt_rows);
+        break;
+      }
+      left -= nt;
+    }
+  }
+  e = __shfl_sync(0xffffffffu, e, l);
+  r0 = __shfl_sync(0xffffffffu, r0, l);
+  r1 = __shfl_sync(0xffffffffu, r1, l);
+}
+
 // ---------------------------------------------------------------- cluster
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
