@@ -105,8 +105,8 @@ __device__ __forceinline__ void store_out(void* d, long long at, float v, int t)
 template <int MODE>
 __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid_constant__ AnyArgs args) {
   constexpr bool WG = MODE == GA_WGRAD, SW = MODE == GA_SWIGLU;
-  // factor A: dw's n (weight gradient) or W_e's features; factor B: dw's k, or the group's rows.  MN-major: the contracted
-  // dimension is not the contiguous one.
+  // factor A: W_e's features, or dw's k (weight gradient), so that a lane's neighbour is its neighbour in the result; factor
+  // B: the group's rows, or dw's n.  MN-major: the contracted dimension is not the contiguous one.
   constexpr bool a_mn = WG || MODE == GA_KN, b_mn = WG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -133,10 +133,10 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
   }
   if (warp == GA_COPY_WARPS) tmem_alloc<1>(smem_u32(tmem_slot), 2 * GA_N);
 
-  // the tile: forward (group, row tile) x feature tile; weight gradient group x n tile x k tile
+  // the tile: forward (group, row tile) x feature tile; weight gradient group x k tile x n tile
   int e, r0, r1, a0, b0 = 0;
   if (WG) {
-    const int tb = (p.k + GA_N - 1) / GA_N, per = (p.n + GA_M - 1) / GA_M * tb;
+    const int tb = (p.n + GA_N - 1) / GA_N, per = (p.k + GA_M - 1) / GA_M * tb;
     e = blockIdx.x / per;
     a0 = blockIdx.x % per / tb * GA_M;
     b0 = blockIdx.x % per % tb * GA_N;
@@ -170,10 +170,10 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
   if (warp < GA_COPY_WARPS) {
     // ---------------------------------------------------------------- staging
     // K-major: thread: word c of rows r + 32 i.  MN-major: word c (in slabs of 8) of contracted rows r + step i.
-    const uintptr_t a_lo = (uintptr_t)(WG ? p.a : p.b), b_lo = (uintptr_t)(WG ? p.b : p.a);
-    const uintptr_t a_hi = a_lo + 2 * (WG ? (p.a_nrows - 1) * p.lda + p.n
+    const uintptr_t a_lo = (uintptr_t)p.b, b_lo = (uintptr_t)p.a;
+    const uintptr_t a_hi = a_lo + 2 * (WG ? (p.b_nrows - 1) * p.ldb + p.k
                                           : (p.groups - 1) * p.b_stride + ((p.kn ? p.k : p.n) - 1) * p.ldb + (p.kn ? p.n : p.k));
-    const uintptr_t b_hi = b_lo + 2 * (WG ? (p.b_nrows - 1) * p.ldb + p.k : (p.a_nrows - 1) * p.lda + p.k);
+    const uintptr_t b_hi = b_lo + 2 * ((p.a_nrows - 1) * p.lda + (WG ? p.n : p.k));
     const int ca = a_mn ? tid & 15 : tid & 7, ra = a_mn ? tid >> 4 : tid >> 3;
     const int cb = tid & 7, rb = tid >> 3;
     constexpr int step_a = a_mn ? 16 : 32, step_b = 32;
@@ -202,25 +202,25 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
         if (a_mn) {
           const int k = kb * 64 + ra + step_a * i;
           const uint16_t* row = nullptr;
-          if (k < kdim) row = WG ? row_at(p.a, p.a_rows, r0 + k, p.a_nrows, p.lda) : w + (long long)k * p.ldb;
+          if (k < kdim) row = WG ? row_at(p.b, p.b_rows, r0 + k, p.b_nrows, p.ldb) : w + (long long)k * p.ldb;
           s[i] = row ? row + a0 + ca * 8 : nullptr;
         } else {
           s[i] = a_row[i] ? a_row[i] + kb * 64 + ca * 8 : nullptr;
         }
       }
-      load_words(s, a_mn ? (WG ? p.n : n_out) - a0 - ca * 8 : kdim - kb * 64 - ca * 8, a_lo, a_hi, va);
+      load_words(s, a_mn ? (WG ? p.k : n_out) - a0 - ca * 8 : kdim - kb * 64 - ca * 8, a_lo, a_hi, va);
       const uint16_t* t[GA_BW];
 #pragma unroll
       for (int i = 0; i < GA_BW; ++i) {
         if (b_mn) {
           const int k = kb * 64 + rb + step_b * i;
-          const uint16_t* row = k < kdim ? row_at(p.b, p.b_rows, r0 + k, p.b_nrows, p.ldb) : nullptr;
+          const uint16_t* row = k < kdim ? row_at(p.a, p.a_rows, r0 + k, p.a_nrows, p.lda) : nullptr;
           t[i] = row ? row + b0 + cb * 8 : nullptr;
         } else {
           t[i] = b_row[i] ? b_row[i] + kb * 64 + cb * 8 : nullptr;
         }
       }
-      load_words(t, b_mn ? p.k - b0 - cb * 8 : kdim - kb * 64 - cb * 8, b_lo, b_hi, vb);
+      load_words(t, b_mn ? p.n - b0 - cb * 8 : kdim - kb * 64 - cb * 8, b_lo, b_hi, vb);
     };
     const uint32_t at_a = (a_mn ? (ca >> 3) * SLAB_BYTES : 0) + ra * 128 + (((ca & 7) ^ (ra & 7)) << 4);
     const uint32_t at_b = rb * 128 + ((cb ^ (rb & 7)) << 4);
@@ -319,11 +319,11 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
     }
     if (!ok && lane == 0) *s_abort = 1;
     if (ok && WG) {
-      const int n = a0 + quarter * 32 + lane, k = b0;
-      const long long at = (long long)e * p.d_stride + (long long)n * p.ldd + k;
+      const int k = a0 + quarter * 32 + lane;
+      const long long at = (long long)e * p.d_stride + (long long)b0 * p.ldd + k;
 #pragma unroll
       for (int i = 0; i < GA_N; ++i)
-        if (n < p.n && k + i < p.k) store_out(p.d, at + i, sum[i], p.out_dtype);
+        if (k < p.k && b0 + i < p.n) store_out(p.d, at + i * p.ldd, sum[i], p.out_dtype);
     } else if (ok) {
       const int f = SW ? a0 + quarter * 16 + (lane & 15) : a0 + quarter * 32 + lane;
 #pragma unroll
@@ -378,7 +378,7 @@ cudaError_t grouped_any_set_attributes() {
 cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, uint32_t* status, cudaStream_t s) {
   // forward: every group can end inside a tile, so m rows make at most m / 64 + min(groups, m) row tiles
   const long long blocks =
-      wgrad ? (long long)p.groups * ceil_div(p.n, GA_M) * ceil_div(p.k, GA_N)
+      wgrad ? (long long)p.groups * ceil_div(p.k, GA_M) * ceil_div(p.n, GA_N)
             : (p.m / GA_N + (p.m < p.groups ? p.m : p.groups)) * ceil_div(p.swiglu ? p.n / 2 : p.n, p.swiglu ? GA_M / 2 : GA_M);
   if (blocks <= 0) return cudaSuccess;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
