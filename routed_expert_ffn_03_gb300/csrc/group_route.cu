@@ -9,6 +9,7 @@
 #include "common.cuh"
 #include "group_route.h"
 #include "grouped.h"
+#include "grouped_mma.cuh"
 #include "route.cuh"
 
 namespace moe {
@@ -18,6 +19,7 @@ namespace {
 constexpr int GR_THREADS = 1024;
 constexpr int GR_WARPS = GR_THREADS / 32;
 constexpr int GR_ONE_BLOCK = 64;      // tokens of the one-launch form: two a warp
+constexpr int GR_CLUSTER = 2;         // blocks that add up their counts before they leave (4 do not fill every SM: 33 us, not 20)
 constexpr int GR_COUNTS = 16384;      // counts by warp and expert that a block holds
 
 __device__ __forceinline__ float load_logit(const void* p, long long i, int dtype) {
@@ -31,44 +33,81 @@ __device__ __forceinline__ float logit_of(const GroupRouteArgs& a, long long t, 
   return clean(load_logit(a.logits, t * a.ld + e, a.dtype));
 }
 
-// The k best of one token, by one warp (lane l holds experts l + 32 i): lane j < k receives the j-th id (-1: none left).
-// Keys carry the expert in their low 10 bits, a lower one larger, so each is unique and one warp maximum a round finds the
-// next: only the lane that held it looks for its next best.  16-bit logits fit the 22 bits above; of fp32 logits
-// those are the leading ones, so one more round shows whether two neighbours in the order share them, and such a token
-// (1 or 2 in 100 of random ones) is selected again from whole keys, with a second maximum for the id.
+// Lane l's logits of token t: experts l + 32 i.  The loads of each type stand together: a branch around each would run them
+// one after another.
 template <int NV>
-__device__ __forceinline__ int token_topk(const GroupRouteArgs& a, long long t, int lane) {
-  uint32_t key[NV];
-  uint32_t best = 0;   // 0: below every expert's
-  float l[NV];   // the loads of each type together: a branch around each would run them one after another
+__device__ __forceinline__ void load_token(const GroupRouteArgs& a, long long t, int lane, float (&l)[NV]) {
   if (a.dtype == GT_FP32) {
     const float* src = static_cast<const float*>(a.logits) + t * a.ld;
 #pragma unroll
     for (int i = 0; i < NV; ++i) l[i] = lane + 32 * i < a.E ? __ldg(src + lane + 32 * i) : -INFINITY;
   } else {
     const uint16_t* src = static_cast<const uint16_t*>(a.logits) + t * a.ld;
-    uint16_t raw[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) raw[i] = lane + 32 * i < a.E ? __ldg(src + lane + 32 * i) : 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = a.dtype == GT_BF16 ? bf16_bits_to_float(raw[i]) : __half2float(__ushort_as_half(raw[i]));
+    for (int i = 0; i < NV; ++i) l[i] = __uint_as_float(lane + 32 * i < a.E ? __ldg(src + lane + 32 * i) : 0u);   // raw
   }
+}
+
+// Keys carry the expert in their low 10 bits, a lower one larger, so each is unique and none is 0 but the masked ones.  16-bit
+// logits fit the 22 bits above whole; of fp32 logits those are the leading ones.
+template <int NV>
+__device__ __forceinline__ void token_keys(const GroupRouteArgs& a, int lane, const float (&l)[NV], uint32_t (&key)[NV]) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = lane + 32 * i;
-    const float x = e < a.E ? clean(l[i]) : -INFINITY;
+    float x = l[i];
+    if (a.dtype == GT_BF16) x = __uint_as_float(__float_as_uint(x) << 16);
+    if (a.dtype == GT_FP16) x = __half2float(__ushort_as_half((unsigned short)__float_as_uint(x)));
+    x = e < a.E ? clean(x) : -INFINITY;
     key[i] = x > -INFINITY ? (logit_key(x) & ~1023u) | (uint32_t)(1023 - e) : 0u;
-    best = max(best, key[i]);
   }
-  uint32_t mine = 0, last = ~0u;
-  bool same = false;
-  const int rounds = a.dtype == GT_FP32 ? min(a.k + 1, a.E) : a.k;
-  for (int j = 0; j < rounds; ++j) {
+}
+
+// one comparator of a sorting network over the warp: of the pair (lane, lane ^ j) the lower lane keeps the larger key where
+// `down`, the smaller one otherwise
+__device__ __forceinline__ uint32_t comparator(uint32_t v, int j, bool down, int lane) {
+  const uint32_t o = __shfl_xor_sync(0xffffffffu, v, j);
+  return (((lane & j) == 0) == down) ? max(v, o) : min(v, o);
+}
+
+// The first n of the keys in descending order, lane j the j-th (0: none), for n <= SORTED: the lanes' largest and second
+// keys are sorted over the warp (descending and ascending) and merged, 35 comparators in all, which is right unless some
+// lane's third belongs to the n (one token in 20 for 8 of 256).  Returns false then.
+constexpr int SORTED = 10;
+template <int NV>
+__device__ __forceinline__ bool sorted_keys(const uint32_t (&key)[NV], int n, int lane, uint32_t& mine) {
+  uint32_t b1 = 0, b2 = 0, b3 = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const uint32_t x = min(b1, key[i]), y = min(b2, x);
+    b1 = max(b1, key[i]);
+    b2 = max(b2, x);
+    b3 = max(b3, y);
+  }
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+    for (int j = k >> 1; j; j >>= 1) {
+      b1 = comparator(b1, j, (lane & k) == 0 || k == 32, lane);
+      b2 = comparator(b2, j, !((lane & k) == 0 || k == 32), lane);
+    }
+  uint32_t v = max(b1, b2);   // one falling, one rising: the 32 largest of both, as a bitonic sequence
+#pragma unroll
+  for (int j = 16; j; j >>= 1) v = comparator(v, j, true, lane);
+  mine = v;
+  return !__any_sync(0xffffffffu, b3 > __shfl_sync(0xffffffffu, v, n - 1));
+}
+
+// The same for any n <= 32 by rounds: the warp's largest key is the next, and the lane that held it looks for its next.
+template <int NV>
+__device__ __forceinline__ uint32_t rounds_of_keys(uint32_t (&key)[NV], int n, int lane) {
+  uint32_t best = 0, mine = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) best = max(best, key[i]);
+  for (int j = 0; j < n; ++j) {
     const uint32_t b = __reduce_max_sync(0xffffffffu, best);
     if (b == 0) break;   // uniform
-    same |= (b ^ last) < 1024u;
-    last = b;
-    if (lane == j && j < a.k) mine = b;
+    if (lane == j) mine = b;
     if (best == b) {
       best = 0;
 #pragma unroll
@@ -78,27 +117,56 @@ __device__ __forceinline__ int token_topk(const GroupRouteArgs& a, long long t, 
       }
     }
   }
-  int e = mine ? 1023 - (int)(mine & 1023u) : -1;
-  if (a.dtype == GT_FP32 && same) {   // uniform
-    uint32_t taken = 0;
-    e = -1;
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t lk = 0;
-      int le = 0x7fffffff;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int ee = lane + 32 * i;
-        const float x = ee < a.E && !((taken >> i) & 1u) ? logit_of(a, t, ee) : -INFINITY;
-        if (x > -INFINITY && logit_key(x) > lk) {   // ascending ids: the first of equal keys stays
-          lk = logit_key(x);
-          le = ee;
-        }
+  return mine;
+}
+
+// The k best of one token, by one warp: lane j < k receives the j-th id (-1: none left).  Of fp32 logits one more key than k
+// shows whether two neighbours in the order share their leading bits (1 or 2 tokens in 100 of random ones).  Among the
+// k they are then ordered by their whole keys; if the k-th and the one behind it share them, or the latter is not
+// known (k = 32), the token is selected again from whole keys, with a second maximum for the id.
+template <int NV>
+__device__ __forceinline__ int token_topk(const GroupRouteArgs& a, long long t, int lane, const float (&l)[NV]) {
+  uint32_t key[NV], mine = 0;
+  token_keys<NV>(a, lane, l, key);
+  const int n = a.dtype == GT_FP32 ? min(a.k + 1, 32) : a.k;
+  if (n > SORTED || !sorted_keys<NV>(key, n, lane, mine)) mine = rounds_of_keys<NV>(key, n, lane);
+  int e = lane < a.k && mine ? 1023 - (int)(mine & 1023u) : -1;
+  if (a.dtype == GT_FP32) {
+    const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
+    const unsigned doubt = __ballot_sync(0xffffffffu, lane < a.k && mine && (lane < 31 ? (mine ^ next) < 1024u : a.E > 32));
+    if (doubt && !(doubt >> (a.k - 1))) {
+      const uint32_t whole = e >= 0 ? logit_key(logit_of(a, t, e)) : 0u;
+      int rank = 0;
+      for (int i = 0; i < a.k; ++i) {
+        const uint32_t o = __shfl_sync(0xffffffffu, whole, i);
+        const int oe = __shfl_sync(0xffffffffu, e, i);
+        rank += o > whole || (o == whole && (oe < e || (oe == e && i < lane)));   // (the last: places left empty keep theirs)
       }
-      const uint32_t bk = __reduce_max_sync(0xffffffffu, lk);
-      if (bk == 0) break;
-      const int be = (int)__reduce_min_sync(0xffffffffu, lk == bk ? (uint32_t)le : 0xffffffffu);
-      if (lane == j) e = be;
-      if (le == be && lk == bk) taken |= 1u << ((be - lane) >> 5);
+      int from = lane;
+      for (int i = 0; i < a.k; ++i)
+        if (__shfl_sync(0xffffffffu, rank, i) == lane) from = i;
+      e = __shfl_sync(0xffffffffu, e, from);
+    } else if (doubt) {
+      uint32_t taken = 0;
+      e = -1;
+      for (int j = 0; j < a.k; ++j) {
+        uint32_t lk = 0;
+        int le = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int ee = lane + 32 * i;
+          const float x = ee < a.E && !((taken >> i) & 1u) ? logit_of(a, t, ee) : -INFINITY;
+          if (x > -INFINITY && logit_key(x) > lk) {   // ascending ids: the first of equal keys stays
+            lk = logit_key(x);
+            le = ee;
+          }
+        }
+        const uint32_t bk = __reduce_max_sync(0xffffffffu, lk);
+        if (bk == 0) break;
+        const int be = (int)__reduce_min_sync(0xffffffffu, lk == bk ? (uint32_t)le : 0xffffffffu);
+        if (lane == j) e = be;
+        if (le == be && lk == bk) taken |= 1u << ((be - lane) >> 5);
+      }
     }
   }
   return e;
@@ -106,8 +174,8 @@ __device__ __forceinline__ int token_topk(const GroupRouteArgs& a, long long t, 
 
 // one token by one warp: its ids and weights
 template <int NV>
-__device__ __forceinline__ int route_token(const GroupRouteArgs& a, long long t, int lane) {
-  const int e = token_topk<NV>(a, t, lane);
+__device__ __forceinline__ int route_token(const GroupRouteArgs& a, long long t, int lane, const float (&logits)[NV]) {
+  const int e = token_topk<NV>(a, t, lane, logits);
   // softmax over the selected logits, or over their log sigmoids: exp(z_j - z_0) / sum, the
   // first being the largest of both
   const float l = e >= 0 ? logit_of(a, t, e) : 0.f;
@@ -131,9 +199,15 @@ __device__ __forceinline__ void select_tokens(const GroupRouteArgs& a, int* hist
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int e = threadIdx.x; e < a.E; e += GR_THREADS) hist[e] = 0;
   __syncthreads();
-  const long long t0 = (long long)blockIdx.x * a.per_block, t1 = min(t0 + a.per_block, (long long)a.T);
+  const long long t0 = min((long long)blockIdx.x * a.per_block, (long long)a.T), t1 = min(t0 + a.per_block, (long long)a.T);
+  float l[NV], ahead[NV];
+  if (t0 + warp < t1) load_token<NV>(a, t0 + warp, lane, ahead);
   for (long long t = t0 + warp; t < t1; t += GR_WARPS) {
-    const int e = route_token<NV>(a, t, lane);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] = ahead[i];
+    if (NV <= 8 && t + GR_WARPS < t1) load_token<NV>(a, t + GR_WARPS, lane, ahead);   // while this token is selected
+    const int e = route_token<NV>(a, t, lane, l);
+    if (NV > 8 && t + GR_WARPS < t1) load_token<NV>(a, t + GR_WARPS, lane, ahead);
     if (lane < a.k && e >= 0) atomicAdd(&hist[e], 1);   // a count: its order does not matter
   }
   __syncthreads();
@@ -156,12 +230,14 @@ __device__ __forceinline__ void place_pairs(const GroupRouteArgs& a, const int* 
   if (lane == 31) wsum[warp] = inc;
   for (int i = tid; i < W * E; i += GR_THREADS) counts[i] = 0;
   __syncthreads();
-  int off = inc - mine, total = 0;
+  int sums = wsum[lane];   // GR_WARPS == 32: every warp scans the warps' sums for itself
+  const int own = sums;
 #pragma unroll
-  for (int w = 0; w < GR_WARPS; ++w) {
-    if (w < warp) off += wsum[w];
-    total += wsum[w];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sums, o);
+    if (lane >= o) sums += v;
   }
+  const int off = inc - mine + __shfl_sync(0xffffffffu, sums - own, warp), total = __shfl_sync(0xffffffffu, sums, 31);
   if (tid < E) {
     all[tid] = off;
     if (blockIdx.x == 0) a.offsets[tid] = off;
@@ -218,13 +294,29 @@ __global__ void __launch_bounds__(GR_THREADS, 1) group_one_kernel(GroupRouteArgs
   place_pairs(a, before, all, counts);
 }
 
+// The counts leave by clusters, hist [clusters][E], with each block's share of its cluster's before it, [blocks][E] behind:
+// the next kernel's blocks then read half of the rows (read one by one, they took half of that kernel's time).
 template <int NV>
-__global__ void __launch_bounds__(GR_THREADS, 1) group_select_kernel(GroupRouteArgs a) {
+__global__ void __cluster_dims__(GR_CLUSTER, 1, 1) __launch_bounds__(GR_THREADS, 1) group_select_kernel(GroupRouteArgs a) {
   __shared__ int hist[1024];
   pdl_launch_dependents();
   pdl_wait();
   select_tokens<NV>(a, hist);
-  for (int e = threadIdx.x; e < a.E; e += GR_THREADS) a.hist[(long long)blockIdx.x * a.E + e] = hist[e];
+  cluster_sync_all();
+  const int rank = (int)cluster_rank(), clusters = a.blocks / GR_CLUSTER;
+  for (int e = threadIdx.x; e < a.E; e += GR_THREADS) {
+    int before = 0, all = 0;
+#pragma unroll
+    for (int r = 0; r < GR_CLUSTER; ++r) {
+      int c;
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(c) : "r"(map_rank(smem_u32(&hist[e]), r)) : "memory");
+      if (r < rank) before += c;
+      all += c;
+    }
+    a.hist[(long long)(clusters + blockIdx.x) * a.E + e] = before;
+    if (rank == 0) a.hist[(long long)(blockIdx.x / GR_CLUSTER) * a.E + e] = all;
+  }
+  cluster_sync_all();   // the others read this block's counts until here
 }
 
 __global__ void __launch_bounds__(GR_THREADS, 1) group_place_kernel(GroupRouteArgs a) {
@@ -233,18 +325,16 @@ __global__ void __launch_bounds__(GR_THREADS, 1) group_place_kernel(GroupRouteAr
   all[threadIdx.x] = before[threadIdx.x] = 0;
   __syncthreads();
   pdl_wait();
-  // thread (part, e): an expert's counts of every parts-th block
+  // thread (part, e): an expert's counts of every parts-th cluster
   const int Ep = (a.E + 31) & ~31, parts = GR_THREADS / Ep, part = threadIdx.x / Ep, e = threadIdx.x % Ep;
+  const int clusters = a.blocks / GR_CLUSTER, mine = blockIdx.x / GR_CLUSTER;
   if (part < parts && e < a.E) {
-    int s = 0, p = 0;
-    // each block starts at another row, so that they do not all read the same lines at once
-    const int n = (a.blocks - part + parts - 1) / parts, start = n > 0 ? (int)(blockIdx.x % n) : 0;
-#pragma unroll 16
-    for (int i = 0; i < n; ++i) {
-      const int r = i + start < n ? i + start : i + start - n, b = part + r * parts;
-      const int c = __ldcg(a.hist + (long long)b * a.E + e);
-      s += c;
-      if (b < (int)blockIdx.x) p += c;
+    int s = 0, p = part == 0 ? __ldcg(a.hist + (long long)(clusters + blockIdx.x) * a.E + e) : 0;
+#pragma unroll 20
+    for (int c = part; c < clusters; c += parts) {
+      const int n = __ldcg(a.hist + (long long)c * a.E + e);
+      s += n;
+      if (c < mine) p += n;
     }
     atomicAdd(&all[e], s);
     atomicAdd(&before[e], p);
@@ -300,7 +390,8 @@ GroupRoutePlan group_route_plan(int T, int E, int k) {
   p.per_block = T <= GR_ONE_BLOCK ? T : (T + kBlocks - 1) / kBlocks;
   if (T > GR_ONE_BLOCK && p.per_block < GR_WARPS) p.per_block = GR_WARPS;
   p.blocks = (T + p.per_block - 1) / p.per_block;
-  p.workspace = p.blocks > 1 ? (size_t)p.blocks * E * sizeof(int) : 0;
+  if (T > GR_ONE_BLOCK) p.blocks = (p.blocks + GR_CLUSTER - 1) / GR_CLUSTER * GR_CLUSTER;   // some without tokens
+  p.workspace = T > GR_ONE_BLOCK ? (size_t)(p.blocks + p.blocks / GR_CLUSTER) * E * sizeof(int) : 0;
   return p;
 }
 

@@ -13,7 +13,7 @@ struct GroupRouteArgs {
   int* idx;
   float* weights;
   int *offsets, *rows, *pairs;
-  int* hist;               // [blocks][E]: pairs by expert of each block's tokens
+  int* hist;               // pairs by expert: of each cluster of blocks, then of a cluster's blocks before each
   int blocks, per_block;   // tokens per block
 };
 struct GroupRoutePlan {

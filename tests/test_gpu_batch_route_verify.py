@@ -57,6 +57,18 @@ def test_route_ties_masks_and_extremes(M, T, E, k, kind):
     check_route(M, torch.from_numpy(l).cuda(), k, kind)
 
 
+@pytest.mark.parametrize("T,E,k", [(300, 64, 8), (300, 200, 9), (40, 1000, 12), (300, 300, 32), (300, 32, 32), (50, 33, 32)])
+def test_route_fp32_neighbours_a_few_bits_apart(M, T, E, k):
+    """fp32 logits that share their leading bits: within the selection, across its end, and equal ones."""
+    import torch
+    rng = np.random.default_rng(E)
+    base = rng.choice(np.array([1.0, 1.0 + 2.0 ** -13, 2.5, -0.75], np.float32), (T, E))
+    l = base + (rng.integers(0, 6, (T, E)) * 2.0 ** -22).astype(np.float32)
+    l[::7, : E // 2] = 0.0
+    l[::11] = rng.normal(size=l[::11].shape)
+    check_route(M, torch.from_numpy(l.astype(np.float32)).cuda(), k, 0)
+
+
 def test_route_everything_masked(M):
     import torch
     g = check_route(M, torch.full((50, 16), -np.inf, device="cuda"), 3, 0)
