@@ -95,7 +95,7 @@ struct moe_ctx {
   // pool file: the records in a file behind a pinned RAM cache of ft->slots() records
   FileTier* ft = nullptr;
   std::string pool_path;
-  uint8_t* h_ram = nullptr;                  // pinned RAM slots
+  uint8_t* h_ram = nullptr;                  // pinned RAM slots (as allocated)
   uint8_t* h_wstage = nullptr;               // pinned staging of a registered record
   std::vector<cudaEvent_t> ram_ev;           // [RAM slot] after the last copy that read it
   std::vector<char> ram_used;                // that event was recorded
@@ -437,7 +437,9 @@ moe_status moe_create(const moe_config* cfg, int device, moe_ctx** out) {
     if (cfg->pool_file) {
       const size_t stride = (c->rec_bytes + FT_ALIGN - 1) / FT_ALIGN * FT_ALIGN;
       const size_t ram = std::min<size_t>(cfg->host_cache_bytes / stride, (size_t)L * E);
-      if (cudaHostAlloc((void**)&c->h_ram, ram * stride, cudaHostAllocDefault) != cudaSuccess ||
+      // the slots start on an FT_ALIGN boundary (direct reads), which a pinned allocation need not: small ones share a block
+      // with the process's other small ones
+      if (cudaHostAlloc((void**)&c->h_ram, ram * stride + FT_ALIGN, cudaHostAllocDefault) != cudaSuccess ||
           cudaHostAlloc((void**)&c->h_wstage, stride, cudaHostAllocDefault) != cudaSuccess) {
         cudaGetLastError();
         free_all(c);
@@ -449,7 +451,8 @@ moe_status moe_create(const moe_config* cfg, int device, moe_ctx** out) {
       // reader threads: MOE_FILE_READERS (1..64) where set, else 8
       int readers = 8;
       if (const char* env = getenv("MOE_FILE_READERS")) readers = std::min(64, std::max(1, atoi(env)));
-      const int fe = c->ft ? c->ft->open(cfg->pool_file, c->rec_bytes, (long long)L * E, c->h_ram, ram * stride,
+      uint8_t* slots = reinterpret_cast<uint8_t*>(((uintptr_t)c->h_ram + FT_ALIGN - 1) / FT_ALIGN * FT_ALIGN);
+      const int fe = c->ft ? c->ft->open(cfg->pool_file, c->rec_bytes, (long long)L * E, slots, ram * stride,
                                          readers)
                            : ENOMEM;
       if (fe != 0) {
