@@ -5,8 +5,12 @@
 #include "grouped.h"
 #include "verify.h"
 
+#include <unistd.h>
+
 #include <atomic>
 #include <cmath>
+#include <cstdlib>
+#include <cstring>
 #include <mutex>
 #include <new>
 
@@ -16,7 +20,8 @@ namespace {
 // out sets.  Made by the first call on the device, kept for the life of the process.
 struct Device {
   int num_sms;
-  uint32_t* status;
+  uint32_t* status;                 // as the device sees it
+  volatile uint32_t* host_status;
 };
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
@@ -25,22 +30,33 @@ std::atomic<Device*> g_device[kMaxDevices];
 moe_status device_setup(int dev, Device** out) {
   std::lock_guard<std::mutex> lk(g_mu);
   if ((*out = g_device[dev].load())) return MOE_OK;
-  Device d{0, nullptr};
-  void* word = nullptr;
+  Device d{0, nullptr, nullptr};
   if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      moe::grouped_any_set_attributes() != cudaSuccess || moe::grouped_pair_set_attributes() != cudaSuccess || moe::grouped_few_set_attributes() != cudaSuccess ||
-      moe::verify_set_attributes() != cudaSuccess || moe::group_route_set_attributes() != cudaSuccess ||
-      cudaHostAlloc(&word, sizeof(uint32_t), cudaHostAllocMapped | cudaHostAllocPortable) != cudaSuccess) {
+      moe::grouped_any_set_attributes() != cudaSuccess || moe::grouped_pair_set_attributes() != cudaSuccess ||
+      moe::grouped_few_set_attributes() != cudaSuccess || moe::verify_set_attributes() != cudaSuccess ||
+      moe::group_route_set_attributes() != cudaSuccess) {
     cudaGetLastError();
     return MOE_ECUDA;
   }
-  d.status = static_cast<uint32_t*>(word);   // unified addressing: the same address on the device
-  *d.status = 0;
+  // the word stands in a page of its own, registered
+  const size_t page = (size_t)sysconf(_SC_PAGESIZE);
+  void* word = nullptr;
   *out = new (std::nothrow) Device(d);
-  if (!*out) {
-    cudaFreeHost(word);
+  if (!*out || posix_memalign(&word, page, page) != 0) {
+    delete *out;
     return MOE_ENOMEM;
   }
+  memset(word, 0, page);
+  void* on_device = nullptr;
+  if (cudaHostRegister(word, page, cudaHostRegisterMapped | cudaHostRegisterPortable) != cudaSuccess ||
+      cudaHostGetDevicePointer(&on_device, word, 0) != cudaSuccess) {
+    cudaGetLastError();
+    free(word);
+    delete *out;
+    return MOE_ECUDA;
+  }
+  (*out)->host_status = static_cast<volatile uint32_t*>(word);
+  (*out)->status = static_cast<uint32_t*>(on_device);
   g_device[dev].store(*out);
   return MOE_OK;
 }
@@ -57,7 +73,7 @@ moe_status current_device(Device** out) {
     const moe_status st = device_setup(dev, out);
     if (st != MOE_OK) return st;
   }
-  return *static_cast<volatile uint32_t*>((*out)->status) ? MOE_ETIMEOUT : MOE_OK;
+  return *(*out)->host_status ? MOE_ETIMEOUT : MOE_OK;
 }
 
 bool is_dtype(int t, bool fp32) { return t == MOE_T_BF16 || t == MOE_T_FP16 || (fp32 && t == MOE_T_FP32); }
