@@ -303,7 +303,7 @@ size_t moe_group_route_workspace(int T, int E, int k);
  * dx = grouped(dy, w as [k'][n']), n' = k, k' = n.
  * offsets [groups + 1] int32, non-decreasing, offsets[0] >= 0, offsets[groups] <= m: groups may be empty, and
  * out rows that no sorted row writes are left as they were.  Offsets outside [0, m] are taken
- * as the nearer end and a group that ends before it starts as empty; a rows[i] outside [0, x_rows) is a row
+ * as the nearer end (where they decrease, which rows are computed is not said); a rows[i] outside [0, x_rows) is a row
  * of zeros; an out_rows[i] outside [0, out_rows_n) writes nothing.  Two sorted rows must not name one
  * out row.  groups 1..1024; m 0..2^30 (0: nothing to do); n, k 1..2^24.  Any strides that keep
  * rows apart (ldx >= k, ldw >= the row's length, ldo >= n_out; w_stride any) and any

@@ -54,15 +54,16 @@ constexpr int GP_BAND = 8;                       // row tiles of a band
 constexpr int GP_OUT = 4096;                     // a warp's box of results: 32 rows of 128 bytes
 constexpr int GP_OFF_OUT = GP_STAGES * GP_STAGE;      // weight gradient
 constexpr int GP_OFF_TAB = GP_OFF_OUT;           // forward: first tile of each group [groups + 1]
-constexpr int GP_OFF_SCAN = GP_OFF_TAB + (GP_MAX_GROUPS + 1) * 4 + 12;
+constexpr int GP_OFF_SCAN = GP_OFF_TAB + (GP_MAX_GROUPS + 2) * 4;
 constexpr int GP_OFF_BAR = GP_OFF_OUT + GP_EPI_WARPS * GP_OUT;
 constexpr int GP_BARS = 4 * GP_STAGES + 4;
 constexpr int GP_SMEM = GP_OFF_BAR + GP_BARS * 8 + 16 + 1024;   // and 1024 to align the stages
-static_assert(GP_OFF_SCAN + 64 <= GP_OFF_BAR && GP_SMEM <= 227 * 1024, "shared memory");
+static_assert(GP_OFF_SCAN % 8 == 0 && GP_OFF_SCAN + GP_THREADS / 32 * 8 <= GP_OFF_BAR && GP_SMEM <= 227 * 1024, "shared memory");
 
 struct PairArgs {
   GroupedProblem p;
   int nft, nkt;        // forward: feature tiles; weight gradient: n tiles and k tiles
+  int max_tiles;       // the most that m rows can make
   uint32_t* status;
   bool wide;           // results can be stored as 4-byte pairs (forward) or by TMA (weight gradient)
 };
@@ -151,7 +152,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + GP_OFF_BAR + GP_BARS * 8);
   volatile int* s_abort = reinterpret_cast<int*>(smem + GP_OFF_BAR + GP_BARS * 8 + 4);
   int* first = reinterpret_cast<int*>(smem + GP_OFF_TAB);
-  int* scan = reinterpret_cast<int*>(smem + GP_OFF_SCAN);
+  long long* scan = reinterpret_cast<long long*>(smem + GP_OFF_SCAN);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * GP_STAGES;
   const uint32_t land0 = empty0 + 8 * GP_STAGES, ready0 = land0 + 8 * GP_STAGES;
   const uint32_t tfull0 = ready0 + 8 * GP_STAGES, tempty0 = tfull0 + 16;
@@ -181,35 +182,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   if (WG) {
     total = p.groups * a.nft * a.nkt;
   } else {
-    int nt[4], mine = 0;
+    long long nt[4], mine = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int g = 4 * tid + q;
       int r0 = 0, r1 = 0;
       if (g < p.groups) group_range(p.offsets, g, p.m, r0, r1);
-      nt[q] = (r1 - r0 + 255) / 256 * a.nft;
+      nt[q] = (r1 - r0 + 255ll) / 256 * a.nft;
       mine += nt[q];
     }
-    int inc = mine;
+    long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
     if (lane == 31) scan[warp] = inc;
     __syncthreads();
-    int off = inc - mine;
-    total = 0;
+    long long off = inc - mine, all = 0;
 #pragma unroll
     for (int w = 0; w < GP_THREADS / 32; ++w) {
       if (w < warp) off += scan[w];
-      total += scan[w];
+      all += scan[w];
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (4 * tid + q < p.groups) first[4 * tid + q] = off;
+      if (4 * tid + q < p.groups) first[4 * tid + q] = (int)off;
       off += nt[q];
     }
+    // more than m rows can make: the offsets are not non-decreasing, and nothing is done
+    total = all <= a.max_tiles ? (int)all : 0;
   }
   umma_fence_before();
   __syncthreads();
@@ -662,10 +664,11 @@ bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, uint3
   } else {
     a.nft = (int)ceil_div(n_out, p.swiglu ? 128 : 256);
     a.nkt = 1;
-    tiles = (p.m / 256 + (p.m < p.groups ? p.m : p.groups)) * a.nft;   // the most that m rows in groups can make
+    tiles = (p.m / 256 + (p.m < p.groups ? p.m : p.groups)) * a.nft;
     a.wide = (uintptr_t)p.d % 4 == 0 && p.ldd % 2 == 0 && n_out % 2 == 0;
   }
   if (tiles > 0x3fffffff) return false;
+  a.max_tiles = (int)tiles;
   const unsigned pairs = (unsigned)(tiles < num_sms / 2 ? tiles : num_sms / 2);
   if (wgrad) *err = launch_mode<GP_WGRAD>(a, m, pairs, s);
   else if (p.swiglu) *err = launch_mode<GP_SWIGLU>(a, m, pairs, s);

@@ -126,6 +126,25 @@ def test_bad_offsets_and_row_numbers_stay_inside(M):
             assert bool((full[[0, 3, 5]] == 7).all())
 
 
+def test_decreasing_offsets_stay_inside(M):
+    """Offsets that go back and forth make more tiles than m rows can; nothing outside out is written, and the next call
+    is right."""
+    import torch
+    for n, k in ((264, 64), (33, 17)):
+        for m in (40, 700):
+            E = 64
+            off = np.array([0, m] * (E // 2) + [0], np.int32)
+            x, _ = values((m, k), 1, "bf16")
+            w, _ = values((E, n, k), 2, "bf16")
+            full = torch.full((m + 2, n + 4), 7.0, device="cuda")
+            M.grouped_matmul(x, w, dev(off), out=full[1:m + 1, :n])
+            d = M.grouped_wgrad(x, x, dev(off))
+            assert d.shape == (E, k, k)
+            torch.cuda.synchronize()
+            assert bool((full[0] == 7).all()) and bool((full[m + 1] == 7).all()) and bool((full[:, n:] == 7).all())
+    run_matmul(M, [40, 0, 300], 264, 64, "bf16")
+
+
 @pytest.mark.parametrize("pad", [0, 3, 8])
 def test_strides_and_alignment(M, pad):
     """x, w and out as parts of larger tensors: rows and matrices further apart, odd starts."""
