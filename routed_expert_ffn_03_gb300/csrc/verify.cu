@@ -3,7 +3,7 @@
 // Draft i with token t stands iff u_i q_i(t) < p_i(t); the token after the last that stands
 // is drawn by inverting the running sum of max(p - q, 0) (or of p, when every draft stands).
 // A weight x (p - q rounded to fp32, by 2^-24 of itself at most) is carried as the integer
-// floor(x 2^60) in 64 bits, so sums are exact and the same in any order, and the token is the least v with
+// x 2^60, rounded, in 64 bits, so sums are exact and the same in any order, and the token is the least v with
 // cum(v) > floor(u total): an integer comparison, with u a 64-bit fraction.
 //
 // Only the row that decides is read, once: a cluster of S blocks takes a sequence, each warp a contiguous run of
@@ -65,14 +65,6 @@ __device__ __forceinline__ float sub_sat(float a, float b) {
   asm("sub.sat.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// floor(x 2^60) for x in [0, 1], by shifts
-__device__ __forceinline__ u64 fixed60(float x) {
-  const uint32_t b = __float_as_uint(x);
-  const u64 m = (u64)((b << 5 & 0x0fffffe0u) | 0x10000000u) << 32;
-  u64 r;   // shr clamps its amount: far small values shift out, and so do 0 and -0 (whose sign makes the amount large)
-  asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(m), "r"(127u - (b >> 23)));
-  return r;
-}
 __device__ __forceinline__ void copy16(uint4* dst, const uint4* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -88,45 +80,40 @@ __device__ __forceinline__ u64 pair_add(u64 a, u64 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ u64 pair_add_rz(u64 a, u64 b) {
-  u64 r;
-  asm("add.rz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ u64 pair_fma(u64 a, u64 b, u64 c) {
   u64 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ u64 pair_fma_rz(u64 a, u64 b, u64 c) {
-  u64 r;
-  asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 
-// The sum of floor(x 2^60) over several x: 1 + x, rounded to zero, has floor(x 2^23) in its low bits, and the same of what is
-// left over gives the next 23 bits and the last 14.  7 instructions a pair and 3 additions an element.  (The
-// conversion instruction to 64 bits runs at the FP64 rate, low on this part, and shifts take 9 instructions of the
-// integer pipe, at half the rate.)
+// The sum of x 2^60, each rounded to an integer, over several x in [0, 1]: 1 + x has x 2^23 rounded in its low bits, and what
+// is left over, signed, gives the next 23 bits in the same way, and the last 14.  7 instructions a pair and 3
+// additions an element.  (The conversion instruction to 64 bits runs at the FP64 rate, low on this part, shifts take 9
+// instructions of the integer pipe, at half the rate, and additions rounded to zero do not come in pairs.)
 struct Sum60 {
   uint32_t a = 0, b = 0, c = 0;
   __device__ __forceinline__ void add(float x0, float x1) {
-    const u64 one = pair(1.f, 1.f), minus = pair(-1.f, -1.f), x = pair(x0, x1);
-    const u64 h = pair_add_rz(x, one);
-    const u64 r = pair_fma(pair_add(h, minus), minus, x);                                    // exact, below 2^-23
-    const u64 m = pair_fma_rz(r, pair(8388608.f, 8388608.f), one);
-    const u64 l = pair_fma(pair_add(m, minus), pair(-1.1920928955078125e-7f, -1.1920928955078125e-7f), r);   // below 2^-46
-    const u64 n = pair_fma_rz(l, pair(137438953472.f, 137438953472.f), one);
+    const u64 one = pair(1.f, 1.f), minus = pair(-1.f, -1.f), mid = pair(1.5f, 1.5f), x = pair(x0, x1);
+    const u64 h = pair_add(x, one);
+    const u64 r = pair_fma(pair_add(h, minus), minus, x);                                    // exact, 2^-24 at most
+    const u64 m = pair_fma(r, pair(8388608.f, 8388608.f), mid);
+    const u64 l = pair_fma(pair_add(m, pair(-1.5f, -1.5f)), pair(-1.1920928955078125e-7f, -1.1920928955078125e-7f), r);   // 2^-47
+    const u64 n = pair_fma(l, pair(137438953472.f, 137438953472.f), mid);
     a += (uint32_t)h + (uint32_t)(h >> 32);
     b += (uint32_t)m + (uint32_t)(m >> 32);
     c += (uint32_t)n + (uint32_t)(n >> 32);
   }
-  // of n elements (up to 256: the middle parts fill 32 bits)
+  // of n elements (up to 256: the signed middle parts fill 32 bits)
   __device__ __forceinline__ u64 total(uint32_t n) const {
-    const uint32_t base = n * 0x3f800000u;
-    return ((u64)(a - base) << 37) + ((u64)(b - base) << 14) + (c - base);
+    return ((u64)(a - n * 0x3f800000u) << 37) + (u64)((long long)(int)(b - n * 0x3fc00000u) << 14) +
+           (u64)(long long)(int)(c - n * 0x3fc00000u);
   }
 };
+__device__ __forceinline__ u64 fixed60(float x) {
+  Sum60 s;
+  s.add(x, 0.f);
+  return s.total(2);
+}
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll

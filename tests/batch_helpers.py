@@ -113,8 +113,8 @@ def verify_ref(p, draft, u, q=None, lengths=None):
     def clean(v):
         return np.clip(np.nan_to_num(v, nan=0.0, posinf=1.0, neginf=0.0), 0.0, 1.0)
 
-    def ints(v):   # floor(v 2^60) as Python integers: v 2^60 is exact in fp64
-        return [int(a) for a in clean(v) * 2.0 ** 60]
+    def ints(v):   # v 2^60, rounded (half to even), as Python integers: the product is exact in fp64
+        return [int(a) for a in np.rint(clean(v) * 2.0 ** 60)]
 
     acc, tok = np.zeros(B, int), np.full((B, D1), -1)
     for b in range(B):
