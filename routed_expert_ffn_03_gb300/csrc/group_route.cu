@@ -52,14 +52,14 @@ __device__ __forceinline__ void load_token(const GroupRouteArgs& a, long long t,
 // logits fit the 22 bits above whole; of fp32 logits those are the leading ones.
 template <int NV>
 __device__ __forceinline__ void token_keys(const GroupRouteArgs& a, int lane, const float (&l)[NV], uint32_t (&key)[NV]) {
+  constexpr uint32_t inf = 0xff800000u;   // key of +inf, which counts as the one below
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = lane + 32 * i;
     float x = l[i];
     if (a.dtype == GT_BF16) x = __uint_as_float(__float_as_uint(x) << 16);
     if (a.dtype == GT_FP16) x = __half2float(__ushort_as_half((unsigned short)__float_as_uint(x)));
-    x = e < a.E ? clean(x) : -INFINITY;
-    key[i] = x > -INFINITY ? (logit_key(x) & ~1023u) | (uint32_t)(1023 - e) : 0u;
+    const bool live = x > -INFINITY && lane + 32 * i < a.E;   // NaN is not
+    key[i] = live ? (min(logit_key(x), inf - 1u) & ~1023u) | (uint32_t)(1023 - lane - 32 * i) : 0u;
   }
 }
 
@@ -213,12 +213,36 @@ __device__ __forceinline__ void select_tokens(const GroupRouteArgs& a, int* hist
   __syncthreads();
 }
 
+// A block's pairs, shared out to W warps in runs of whole 32s; counts (shared) [W][E].
+struct Pairs {
+  int W;
+  long long p0, p1, q0, q1;   // the block's, this warp's
+  int* next;                  // this warp's row of counts
+};
+__device__ __forceinline__ Pairs block_pairs(const GroupRouteArgs& a, int* counts) {
+  Pairs s;
+  const int warp = threadIdx.x >> 5;
+  s.W = min(GR_WARPS, GR_COUNTS / a.E);
+  const long long P = (long long)a.T * a.k;
+  s.p0 = min((long long)blockIdx.x * a.per_block * a.k, P);
+  s.p1 = min(s.p0 + (long long)a.per_block * a.k, P);
+  const long long share = ((s.p1 - s.p0 + s.W - 1) / s.W + 31) / 32 * 32;
+  s.q0 = min(s.p0 + warp * share, s.p1);
+  s.q1 = warp < s.W ? min(s.q0 + share, s.p1) : s.q0;
+  s.next = counts + warp * a.E;
+  return s;
+}
+// counts (zeros before) by warp and expert
+__device__ __forceinline__ void count_pairs(const GroupRouteArgs& a, const Pairs& s) {
+  for (long long i = s.q0 + (threadIdx.x & 31); i < s.q1; i += 32) {
+    const int e = __ldcg(a.idx + i);
+    if (e >= 0) atomicAdd(&s.next[e], 1);
+  }
+}
 // Places this block's pairs.  before, all (shared, [E]): an expert's pairs in earlier blocks and in all of them.
-// counts (shared): [W][E], W warps each with a run of the pairs.
-__device__ __forceinline__ void place_pairs(const GroupRouteArgs& a, const int* before, int* all, int* counts) {
+__device__ __forceinline__ void place_pairs(const GroupRouteArgs& a, const Pairs& s, const int* before, const int* all, int* counts) {
   __shared__ int wsum[GR_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.E;
-  const int W = min(GR_WARPS, GR_COUNTS / E);
   // offsets: an exclusive scan of all over the experts, thread e its own
   const int mine = tid < E ? all[tid] : 0;
   int inc = mine;
@@ -228,7 +252,6 @@ __device__ __forceinline__ void place_pairs(const GroupRouteArgs& a, const int* 
     if (lane >= o) inc += v;
   }
   if (lane == 31) wsum[warp] = inc;
-  for (int i = tid; i < W * E; i += GR_THREADS) counts[i] = 0;
   __syncthreads();
   int sums = wsum[lane];   // GR_WARPS == 32: every warp scans the warps' sums for itself
   const int own = sums;
@@ -238,46 +261,34 @@ __device__ __forceinline__ void place_pairs(const GroupRouteArgs& a, const int* 
     if (lane >= o) sums += v;
   }
   const int off = inc - mine + __shfl_sync(0xffffffffu, sums - own, warp), total = __shfl_sync(0xffffffffu, sums, 31);
-  if (tid < E) {
-    all[tid] = off;
-    if (blockIdx.x == 0) a.offsets[tid] = off;
-  }
-  if (blockIdx.x == 0 && tid == 0) a.offsets[E] = total;
-  const long long P = (long long)a.T * a.k;
-  const long long p0 = min((long long)blockIdx.x * a.per_block * a.k, P), p1 = min(p0 + (long long)a.per_block * a.k, P);
-  const long long share = ((p1 - p0 + W - 1) / W + 31) / 32 * 32;
-  const long long q0 = min(p0 + warp * share, p1), q1 = warp < W ? min(q0 + share, p1) : q0;
-  int* next = counts + warp * E;
-  for (long long i = q0 + lane; i < q1; i += 32) {
-    const int e = __ldcg(a.idx + i);
-    if (e >= 0) atomicAdd(&next[e], 1);
-  }
-  __syncthreads();
   if (tid < E) {   // counts become first positions
-    int pos = all[tid] + before[tid];
-    for (int w = 0; w < W; ++w) {
+    if (blockIdx.x == 0) a.offsets[tid] = off;
+    int pos = off + before[tid];
+#pragma unroll 8
+    for (int w = 0; w < s.W; ++w) {
       const int c = counts[w * E + tid];
       counts[w * E + tid] = pos;
       pos += c;
     }
   }
+  if (blockIdx.x == 0 && tid == 0) a.offsets[E] = total;
   __syncthreads();
-  for (long long i0 = q0; i0 < q1; i0 += 32) {
+  for (long long i0 = s.q0; i0 < s.q1; i0 += 32) {
     const long long i = i0 + lane;
-    const int e = i < q1 ? __ldcg(a.idx + i) : -1;
+    const int e = i < s.q1 ? __ldcg(a.idx + i) : -1;
     const unsigned same = __match_any_sync(0xffffffffu, e);
     int pos = 0;
-    if (e >= 0) pos = next[e] + __popc(same & ((1u << lane) - 1u));
+    if (e >= 0) pos = s.next[e] + __popc(same & ((1u << lane) - 1u));
     __syncwarp();
     if (e >= 0) {
       a.pairs[pos] = (int)i;
-      a.rows[pos] = (int)(i / a.k);
-      if (lane == 31 - __clz(same)) next[e] = pos + 1;
+      a.rows[pos] = (int)((unsigned)i / (unsigned)a.k);
+      if (lane == 31 - __clz(same)) s.next[e] = pos + 1;
     }
     __syncwarp();
   }
   // no pair stands behind the last group
-  for (long long i = max(p0, (long long)total) + tid; i < p1; i += GR_THREADS) {
+  for (long long i = max(s.p0, (long long)total) + tid; i < s.p1; i += GR_THREADS) {
     a.pairs[i] = -1;
     a.rows[i] = -1;
   }
@@ -287,11 +298,14 @@ template <int NV>
 __global__ void __launch_bounds__(GR_THREADS, 1) group_one_kernel(GroupRouteArgs a) {
   extern __shared__ int counts[];
   __shared__ int all[1024], before[1024];
+  const Pairs s = block_pairs(a, counts);
+  for (int i = threadIdx.x; i < s.W * a.E; i += GR_THREADS) counts[i] = 0;
+  before[threadIdx.x] = 0;
   pdl_wait();
   select_tokens<NV>(a, all);
-  for (int e = threadIdx.x; e < a.E; e += GR_THREADS) before[e] = 0;
+  count_pairs(a, s);
   __syncthreads();
-  place_pairs(a, before, all, counts);
+  place_pairs(a, s, before, all, counts);
 }
 
 // The counts leave by clusters, hist [clusters][E], with each block's share of its cluster's before it, [blocks][E] behind:
@@ -322,9 +336,12 @@ __global__ void __cluster_dims__(GR_CLUSTER, 1, 1) __launch_bounds__(GR_THREADS,
 __global__ void __launch_bounds__(GR_THREADS, 1) group_place_kernel(GroupRouteArgs a) {
   extern __shared__ int counts[];
   __shared__ int all[1024], before[1024];
+  const Pairs pairs = block_pairs(a, counts);
+  for (int i = threadIdx.x; i < pairs.W * a.E; i += GR_THREADS) counts[i] = 0;
   all[threadIdx.x] = before[threadIdx.x] = 0;
   __syncthreads();
   pdl_wait();
+  count_pairs(a, pairs);
   // thread (part, e): an expert's counts of every parts-th cluster
   const int Ep = (a.E + 31) & ~31, parts = GR_THREADS / Ep, part = threadIdx.x / Ep, e = threadIdx.x % Ep;
   const int clusters = a.blocks / GR_CLUSTER, mine = blockIdx.x / GR_CLUSTER;
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(GR_THREADS, 1) group_place_kernel(GroupRouteAr
     atomicAdd(&before[e], p);
   }
   __syncthreads();
-  place_pairs(a, before, all, counts);
+  place_pairs(a, pairs, before, all, counts);
 }
 
 template <typename... A>
