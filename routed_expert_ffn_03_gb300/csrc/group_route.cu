@@ -5,7 +5,9 @@
 // pairs by expert.  Then a block sums the counts of the blocks before it, scans the experts' totals into offsets,
 // and places its pairs in order: a stable counting sort, in which no atomic decides a position, so the same logits give
 // the same arrays.  Up to 64 tokens are one block of one launch; more are two launches over one block of 32 warps an SM, the
-// second waiting for the first on the device.  Bound: latency (the rounds of a selection depend on one another): ROUTE_LATENCY
+// second waiting for the first on the device.  Bound: the
+// integer pipe while selecting (about 300 instructions a token), latency while placing: 16384 tokens of 256 bf16 logits,
+// k = 8, take 21 us (13 selecting; 10 MB, 1.5 us at the memory's rate), one token 5.7 us.
 #include "common.cuh"
 #include "group_route.h"
 #include "grouped.h"

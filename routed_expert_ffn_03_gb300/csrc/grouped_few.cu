@@ -13,6 +13,8 @@
 //   warps 2..5  add the parts up in fp32 registers (the tensor core's own running sum truncates at each step).
 // Then the cluster adds its blocks' sums in rank order through distributed shared memory (no workspace, no
 // atomics, the same bits every time) and each block stores its share.
+// DeepSeek-V3-shaped layer: gate/up of one token (470 MB) 73 us, 0.95 of the memory's rate; down of four tokens (0.9 GB)
+// 126 us (the pair kernel: 86 and 148).
 #include "grouped.h"
 #include "grouped_mma.cuh"
 
