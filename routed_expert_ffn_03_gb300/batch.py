@@ -93,38 +93,40 @@ def _type(t, what, fp32=True):
     return c
 
 
-def _dense(t, what, dims, device):
-    """The shape of a tensor of `dims` dimensions on `device`, its last dimension contiguous."""
-    shape = t.shape
-    if len(shape) != dims or t.device != device or (shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError("%s: a %d-dimensional tensor on %s with a contiguous last dimension is wanted, got %s on %s" %
-                         (what, dims, device, tuple(shape), t.device))
-    return shape
+def _cuda(t, what):
+    """The index of the tensor's CUDA device."""
+    index = t.get_device()
+    if index < 0 or not t.is_cuda:
+        raise ValueError("%s: the tensors must be on a CUDA device, got %s" % (what, t.device))
+    return index
 
 
-def _flat(t, what, dtype, shape, device):
+def _dense(t, what, dims, index):
+    """(shape, strides) of a tensor of `dims` dimensions on the device, its last dimension contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != dims or t.get_device() != index or (stride[-1] != 1 and shape[-1] > 1):
+        raise ValueError("%s: a %d-dimensional tensor on cuda:%d with a contiguous last dimension is wanted, got %s on %s" %
+                         (what, dims, index, tuple(shape), t.device))
+    return shape, stride
+
+
+def _flat(t, what, dtype, shape, index):
     """The address of a contiguous tensor of that type and shape on the device."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError("%s: a contiguous %s tensor of shape %s on %s is wanted, got %s %s on %s" %
-                         (what, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError("%s: a contiguous %s tensor of shape %s on cuda:%d is wanted, got %s %s on %s" %
+                         (what, dtype, tuple(shape), index, t.dtype, tuple(t.shape), t.device))
     return t.data_ptr()
 
 
-def _pitch(t, dim, least):
-    """Elements between neighbours along `dim`; at least `least` where there is only one."""
-    return t.stride(dim) if t.shape[dim] > 1 else max(t.stride(dim), least)
+def _pitch(stride, size, least):
+    """Elements between neighbours along a dimension; at least `least` where there is only one."""
+    return stride if size > 1 or stride > least else least
 
 
-def _device(t):
-    dev = t.device
-    if dev.type != "cuda":
-        raise ValueError("the tensors must be on a CUDA device, got %s" % dev)
-    return dev
-
-
-def _new(stream, dev, *wanted):
+def _new(stream, index, *wanted):
     """New tensors of the given (shape, dtype), belonging to the stream that will use them."""
     torch = _torch
+    dev = torch.device("cuda", index)
     if stream is None:
         return [torch.empty(s, dtype=t, device=dev) for s, t in wanted]
     s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
@@ -132,29 +134,29 @@ def _new(stream, dev, *wanted):
         return [torch.empty(s, dtype=t, device=dev) for s, t in wanted]
 
 
-def _space(workspace, need, stream, dev):
+def _space(workspace, need, stream, index):
     """(address, bytes) of a call's workspace: what is given, or new memory; and the tensor, to be held until the
     launch."""
     if workspace is None:
         if not need:
             return 0, 0, None
-        workspace, = _new(stream, dev, ((need,), _torch.uint8))
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace: a contiguous tensor on %s is wanted, got one on %s" % (dev, workspace.device))
+        workspace, = _new(stream, index, ((need,), _torch.uint8))
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on cuda:%d is wanted, got one on %s" % (index, workspace.device))
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _run(what, call, dev, stream, *args):
+def _run(what, call, index, stream, *args):
     """The call on the tensors' device, on `stream` or that device's current one."""
-    torch = _torch
     if stream is None:
-        stream = _raw_stream(dev.index)
+        stream = _raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if dev.index == torch.cuda.current_device():
+    cuda = _torch.cuda
+    if index == cuda.current_device():
         st = call(*args, stream)
     else:
-        with torch.cuda.device(dev):
+        with cuda.device(index):
             st = call(*args, stream)
     if st != OK:
         raise MoeError(st, what)
@@ -169,21 +171,20 @@ def group_route(logits, k, router=ROUTER_SOFTMAX, out=None, workspace=None, stre
     weight 0, in no group.  out: the five tensors to write instead of new ones.  workspace: uint8 device
     memory of group_route_workspace(T, E, k) bytes; calls that may overlap on the GPU need one each."""
     torch, L = _start()
-    dev = _device(logits)
-    T, E = _dense(logits, "logits", 2, dev)
+    dev = _cuda(logits, "logits")
+    (T, E), stride = _dense(logits, "logits", 2, dev)
     dt = _type(logits, "logits")
-    i32, P = torch.int32, T * k
+    i32, P, TK = torch.int32, (T * k,), (T, k)
     if out is None:
-        idx, weights, offsets, rows, pairs = out = _new(
-            stream, dev, ((T, max(k, 0)), i32), ((T, max(k, 0)), torch.float32), ((E + 1,), i32), ((max(P, 0),), i32), ((max(P, 0),), i32))
-        out = tuple(out)
-    else:
-        idx, weights, offsets, rows, pairs = out
+        if k < 1:
+            raise ValueError("k: at least 1, got %d" % k)
+        out = tuple(_new(stream, dev, (TK, i32), (TK, torch.float32), ((E + 1,), i32), (P, i32), (P, i32)))
+    idx, weights, offsets, rows, pairs = out
     ws, ws_bytes, _held = _space(workspace, L.moe_group_route_workspace(T, E, k), stream, dev)
-    _run("moe_group_route", L.moe_group_route, dev, stream, logits.data_ptr(), _pitch(logits, 0, E), dt, T, E, k, router,
-         _flat(idx, "out: idx", i32, (T, k), dev), _flat(weights, "out: weights", torch.float32, (T, k), dev),
-         _flat(offsets, "out: offsets", i32, (E + 1,), dev), _flat(rows, "out: rows", i32, (P,), dev),
-         _flat(pairs, "out: pairs", i32, (P,), dev), ws, ws_bytes)
+    _run("moe_group_route", L.moe_group_route, dev, stream, logits.data_ptr(), _pitch(stride[0], T, E), dt, T, E, k, router,
+         _flat(idx, "out: idx", i32, TK, dev), _flat(weights, "out: weights", torch.float32, TK, dev),
+         _flat(offsets, "out: offsets", i32, (E + 1,), dev), _flat(rows, "out: rows", i32, P, dev),
+         _flat(pairs, "out: pairs", i32, P, dev), ws, ws_bytes)
     return out
 
 
@@ -213,12 +214,13 @@ def grouped_matmul(x, w, offsets, rows=None, out_rows=None, w_layout="nk", act=N
     were (undefined in a new tensor).  The gradient of x is the same call on dy with the other w_layout.
     workspace (with rows): uint8 device memory of grouped_workspace(m, k, E) bytes; new memory without it."""
     torch, L = _start()
-    dev = _device(x)
-    R, k = _dense(x, "x", 2, dev)
+    dev = _cuda(x, "x")
+    (R, k), x_stride = _dense(x, "x", 2, dev)
     dt = _type(x, "x", fp32=False)
-    E, n, kw = _dense(w, "w", 3, dev)
-    if w.dtype != x.dtype:
+    (E, n, kw), w_stride = _dense(w, "w", 3, dev)
+    if w.dtype is not x.dtype:
         raise ValueError("w: dtype %s, x has %s" % (w.dtype, x.dtype))
+    ldw = _pitch(w_stride[1], n, kw)
     if w_layout == "nk":
         layout = GROUP_NK
     elif w_layout == "kn":
@@ -237,19 +239,19 @@ def grouped_matmul(x, w, offsets, rows=None, out_rows=None, w_layout="nk", act=N
     m = rows.shape[0] if rows is not None else out_rows.shape[0] if out_rows is not None else R
     if out is None:
         out, = _new(stream, dev, ((m, n_out), out_dtype or x.dtype))
-    N, cols = _dense(out, "out", 2, dev)
+    (N, cols), o_stride = _dense(out, "out", 2, dev)
     if cols != n_out or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out: %s %s, wanted %d columns" % (tuple(out.shape), out.dtype, n_out))
     ws = ws_bytes = rows_at = 0
     if rows is not None:
         rows_at = _flat(rows, "rows", i32, (m,), dev)
-        ws, ws_bytes, _held = _space(workspace, L.moe_grouped_workspace(m, k, E), stream, dev)
+        ws, ws_bytes, _held = _space(workspace, 0 if workspace is not None else L.moe_grouped_workspace(m, k, E), stream, dev)
     if m:
         a = _pack_matmul(
             x.data_ptr(), w.data_ptr(), _flat(offsets, "offsets", i32, (E + 1,), dev), rows_at,
-            0 if out_rows is None else _flat(out_rows, "out_rows", i32, (m,), dev), out.data_ptr(), R, _pitch(x, 0, k),
-            _pitch(w, 1, w.shape[2]), w.stride(0) if E > 1 else 0, N, _pitch(out, 0, n_out), m, E, n, k, dt, _type(out, "out"), layout,
-            act, ws, ws_bytes)
+            0 if out_rows is None else _flat(out_rows, "out_rows", i32, (m,), dev), out.data_ptr(), R, _pitch(x_stride[0], R, k),
+            ldw, w_stride[0] if E > 1 else 0, N, _pitch(o_stride[0], N, n_out), m, E, n, k, dt, _type(out, "out"), layout, act, ws,
+            ws_bytes)
         _run("moe_grouped_matmul", L.moe_grouped_matmul, dev, stream, a)
     return out
 
@@ -262,19 +264,20 @@ def grouped_wgrad(dy, x, offsets, dy_rows=None, x_rows=None, out=None, out_dtype
     workspace (with row numbers): uint8 device memory of grouped_wgrad_workspace(m, n) bytes for dy_rows and
     grouped_wgrad_workspace(m, k) for x_rows; new memory without it."""
     torch, L = _start()
-    dev = _device(dy)
-    R, n = _dense(dy, "dy", 2, dev)
+    dev = _cuda(dy, "dy")
+    (R, n), dy_stride = _dense(dy, "dy", 2, dev)
     dt = _type(dy, "dy", fp32=False)
-    S, k = _dense(x, "x", 2, dev)
-    if x.dtype != dy.dtype:
+    (S, k), x_stride = _dense(x, "x", 2, dev)
+    if x.dtype is not dy.dtype:
         raise ValueError("x: dtype %s, dy has %s" % (x.dtype, dy.dtype))
     E, i32 = offsets.shape[0] - 1, torch.int32
     m = dy_rows.shape[0] if dy_rows is not None else x_rows.shape[0] if x_rows is not None else min(R, S)
     if out is None:
         out, = _new(stream, dev, ((E, n, k), out_dtype or dy.dtype))
-    if _dense(out, "out", 3, dev) != (E, n, k) or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError("out: %s %s, wanted %s" % (tuple(out.shape), out.dtype, (E, n, k)))
-    ldw = _pitch(out, 1, k)
+    shape, o_stride = _dense(out, "out", 3, dev)
+    if shape != (E, n, k) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out: %s %s, wanted %s" % (tuple(shape), out.dtype, (E, n, k)))
+    ldw = _pitch(o_stride[1], n, k)
     dy_at = x_at = need = 0
     if dy_rows is not None:
         dy_at = _flat(dy_rows, "dy_rows", i32, (m,), dev)
@@ -284,9 +287,9 @@ def grouped_wgrad(dy, x, offsets, dy_rows=None, x_rows=None, out=None, out_dtype
         need += L.moe_grouped_wgrad_workspace(m, k)
     ws, ws_bytes, _held = _space(workspace, need, stream, dev) if need else (0, 0, None)
     a = _pack_wgrad(
-        dy.data_ptr(), x.data_ptr(), _flat(offsets, "offsets", i32, (E + 1,), dev), dy_at, x_at, out.data_ptr(), R, _pitch(dy, 0, n),
-        S, _pitch(x, 0, k), ldw, out.stride(0) if E > 1 else max(out.stride(0), (n - 1) * ldw + k), m, E, n, k, dt, _type(out, "out"),
-        ws, ws_bytes)
+        dy.data_ptr(), x.data_ptr(), _flat(offsets, "offsets", i32, (E + 1,), dev), dy_at, x_at, out.data_ptr(), R,
+        _pitch(dy_stride[0], R, n), S, _pitch(x_stride[0], S, k), ldw, _pitch(o_stride[0], E, (n - 1) * ldw + k), m, E, n, k, dt,
+        _type(out, "out"), ws, ws_bytes)
     _run("moe_grouped_wgrad", L.moe_grouped_wgrad, dev, stream, a)
     return out
 
@@ -299,22 +302,24 @@ def verify_draft(p, draft, u, q=None, lengths=None, out=None, stream=None):
     drafts per sequence (D without it).  Returns (accepted [B] int32, tokens [B, D + 1] int32): the accepted drafts,
     the drawn token, then -1."""
     torch, L = _start()
-    dev = _device(p)
-    B, D1, V = _dense(p, "p", 3, dev)
+    dev = _cuda(p, "p")
+    (B, D1, V), p_stride = _dense(p, "p", 3, dev)
     dt = _type(p, "p")
     D, i32 = D1 - 1, torch.int32
     q_at = q_seq = q_row = 0
     if q is not None:
-        if _dense(q, "q", 3, dev) != (B, D, V) or q.dtype != p.dtype:
-            raise ValueError("q: %s %s, wanted %s %s" % (tuple(q.shape), q.dtype, (B, D, V), p.dtype))
+        shape, stride = _dense(q, "q", 3, dev)
+        if shape != (B, D, V) or q.dtype is not p.dtype:
+            raise ValueError("q: %s %s, wanted %s %s" % (tuple(shape), q.dtype, (B, D, V), p.dtype))
         if D:
-            q_at, q_seq, q_row = q.data_ptr(), _pitch(q, 0, D * V), _pitch(q, 1, V)
+            q_at, q_seq, q_row = q.data_ptr(), _pitch(stride[0], B, D * V), _pitch(stride[1], D, V)
+    out_shape = (B, D1)
     if out is None:
-        out = tuple(_new(stream, dev, ((B,), i32), ((B, D1), i32)))
+        out = tuple(_new(stream, dev, ((B,), i32), (out_shape, i32)))
     a = _pack_verify(
         p.data_ptr(), q_at, _flat(draft, "draft", i32, (B, D), dev) if D else 0,
-        0 if lengths is None else _flat(lengths, "lengths", i32, (B,), dev), _flat(u, "u", torch.float32, (B, D1), dev),
-        _flat(out[0], "out: accepted", i32, (B,), dev), _flat(out[1], "out: tokens", i32, (B, D1), dev),
-        _pitch(p, 0, D1 * V), _pitch(p, 1, V), q_seq, q_row, B, D, V, dt)
+        0 if lengths is None else _flat(lengths, "lengths", i32, (B,), dev), _flat(u, "u", torch.float32, out_shape, dev),
+        _flat(out[0], "out: accepted", i32, (B,), dev), _flat(out[1], "out: tokens", i32, out_shape, dev),
+        _pitch(p_stride[0], B, D1 * V), _pitch(p_stride[1], D1, V), q_seq, q_row, B, D, V, dt)
     _run("moe_verify_draft", L.moe_verify_draft, dev, stream, a)
     return out
