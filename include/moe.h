@@ -373,10 +373,9 @@ size_t moe_grouped_wgrad_workspace(long long m, int len);
  * without probabilities (one-hot).  u (meant in [0, 1)), a draft's own p and q, and the weights are read as clamped
  * to [0, 1], NaN as 0; u = 1 draws the last v that has any weight.  The comparison is exact; a weight p - q is rounded
  * to fp32; running sums are exact in steps of 2^-60, so the order of summation decides nothing.  Where the
- * residual is all zero the token is drawn from
- * p[b][r]; where that is too, it is -1.  lengths outside [0, D] are taken as the nearer end; a token
+ * residual is all zero the token is drawn from p[b][r]; where that is too, it is -1.  lengths outside [0, D] are taken as the nearer end; a token
  * outside [0, V) is rejected.  draft [B][D] int32, u [B][D+1] fp32, tokens [B][D+1] int32, all
- * contiguous; rows and drafts past a sequence's length are not read.  B >= 1, D 0..31, V 1..2^30. */
+ * contiguous; rows of p and q past a sequence's length are not read and drafts past it do not matter.  B >= 1, D 0..31, V 1..2^30. */
 typedef struct {
     const void* p;
     const void* q;        /* NULL: one-hot drafts */

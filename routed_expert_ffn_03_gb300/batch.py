@@ -270,6 +270,8 @@ def grouped_wgrad(dy, x, offsets, dy_rows=None, x_rows=None, out=None, out_dtype
     (S, k), x_stride = _dense(x, "x", 2, dev)
     if x.dtype is not dy.dtype:
         raise ValueError("x: dtype %s, dy has %s" % (x.dtype, dy.dtype))
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets: one more than the groups, got %s" % (tuple(offsets.shape),))
     E, i32 = offsets.shape[0] - 1, torch.int32
     m = dy_rows.shape[0] if dy_rows is not None else x_rows.shape[0] if x_rows is not None else min(R, S)
     if out is None:

@@ -80,7 +80,7 @@ bool is_dtype(int t, bool fp32) { return t == MOE_T_BF16 || t == MOE_T_FP16 || (
 size_t dtype_bytes(int t) { return t == MOE_T_FP32 ? 4 : 2; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// rows of `len` elements `ld` apart; at most 2^24 long, and `rows` of them within 2^62 bytes
+// rows of `len` elements `ld` apart that do not overlap, all of them within 2^62 bytes
 bool rows_fit(long long rows, long long ld, long long len) {
   return rows >= 0 && ld >= len && ld < (1ll << 40) && (rows == 0 || ld <= (1ll << 60) / rows);
 }

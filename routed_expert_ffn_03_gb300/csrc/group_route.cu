@@ -406,9 +406,9 @@ cudaError_t group_route_set_attributes() {
 GroupRoutePlan group_route_plan(int T, int E, int k) {
   constexpr int kBlocks = 152;   // one an SM; a constant, so that the workspace's size does not depend on the device
   GroupRoutePlan p;
-  p.per_block = T <= GR_ONE_BLOCK ? T : (T + kBlocks - 1) / kBlocks;
+  p.per_block = T <= GR_ONE_BLOCK ? T : (T - 1) / kBlocks + 1;
   if (T > GR_ONE_BLOCK && p.per_block < GR_WARPS) p.per_block = GR_WARPS;
-  p.blocks = (T + p.per_block - 1) / p.per_block;
+  p.blocks = (T - 1) / p.per_block + 1;
   if (T > GR_ONE_BLOCK) p.blocks = (p.blocks + GR_CLUSTER - 1) / GR_CLUSTER * GR_CLUSTER;   // some without tokens
   p.workspace = T > GR_ONE_BLOCK ? (size_t)(p.blocks + p.blocks / GR_CLUSTER) * E * sizeof(int) : 0;
   return p;

@@ -37,6 +37,7 @@ CASES = [
     (RAGGED, 256, 64), (RAGGED, 136, 72), (RAGGED, 520, 1032), ([5, 0, 3], 8, 8), ([1], 1, 1), ([33, 64, 65], 33, 7),
     ([0, 0, 4], 1000, 264), ([130, 129], 48, 100), ([1, 1, 0, 1], 2048, 2056), ([700, 0, 31], 64, 512),
     ([1] * 40, 96, 160), ([17, 16, 15, 32, 33, 31, 48, 64, 63], 272, 200), ([2, 0] * 300, 40, 48),
+    ([1, 0, 0, 2] * 256, 24, 40), ([40, 0, 3, 20] * 256, 24, 40), ([19, 2] * 512, 9, 15),
 ]
 
 
@@ -224,7 +225,8 @@ def test_long_offsets_pass_32_bits(M):
 
 
 WCASES = [(RAGGED, 256, 64), (RAGGED, 136, 72), ([5, 0, 3], 8, 8), ([1], 1, 1), ([33, 64, 65], 33, 7), ([0, 0, 4], 520, 264),
-          ([130, 129, 128], 48, 104), ([700, 0, 31], 64, 512), ([63, 64, 1], 264, 392), ([2, 0] * 200, 40, 48)]
+          ([130, 129, 128], 48, 104), ([700, 0, 31], 64, 512), ([63, 64, 1], 264, 392), ([2, 0] * 200, 40, 48),
+          ([3, 0, 130], 20, 12), ([65, 1, 40], 33, 7)]
 
 
 @pytest.mark.parametrize("out", ["same", "fp32"])
@@ -320,6 +322,18 @@ def test_other_stream_capture_and_two_at_once(M):
         torch.cuda.synchronize()
         for y in outs:
             B.check_close(y, val, tol, "bf16")
+        idx = np.random.default_rng(0).permutation(m).astype(np.int32)
+        gathered = dev(idx)
+        torch.cuda.synchronize()
+        outs = [M.grouped_matmul(x, w, o, rows=gathered, stream=s) for s in side for _ in range(3)]
+        dws = [M.grouped_wgrad(x, x, o, x_rows=gathered, stream=s) for s in side for _ in range(2)]
+        torch.cuda.synchronize()
+        v2, t2 = B.grouped_ref(xd, wd, off, idx)
+        for g in outs:
+            B.check_close(g, v2, t2, "bf16")
+        v2, t2 = B.wgrad_ref(xd, xd, off, None, idx)
+        for g in dws:
+            B.check_close(g, v2, t2, "bf16")
         y = torch.zeros_like(outs[0])
         d = torch.zeros(len(sizes), n, k, dtype=torch.bfloat16, device="cuda")
         M.grouped_wgrad(y, x, o, out=d)
