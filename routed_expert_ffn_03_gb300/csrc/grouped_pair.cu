@@ -124,17 +124,19 @@ __device__ __forceinline__ Tile decode(const PairArgs& a, const int* first, int 
   int r1;
   group_range(p.offsets, lo, p.m, T.r0, r1);
   const int R = r1 - T.r0, nt = (R + 255) / 256;
-  const int each = ((R + nt - 1) / nt + 31) & ~31;      // rows of a tile: the group in even parts
   const int i = t - first[lo];
   const int band = i / (GP_BAND * a.nft), in = i - band * GP_BAND * a.nft;
   const int h = min(GP_BAND, nt - band * GP_BAND);
   const int rt = band * GP_BAND + in % h;
   T.f0 = in / h * (MODE == GP_SWIGLU ? 128 : 256);
-  T.r0 += rt * each;
-  T.rows = min(R - rt * each, each);                    // 0 or less where the even parts end early
-  T.n = (max(T.rows, 0) + 31) & ~31;
+  // the group's 32s of rows in even parts: a tile of few rows would wait for its weights
+  const int units = (R + 31) / 32, base = units / nt, more = units - base * nt;
+  const int at = (rt * base + min(rt, more)) * 32;
+  T.rows = min(R - at, (base + (rt < more)) * 32);
+  T.r0 += at;
+  T.n = (T.rows + 31) & ~31;
   T.c0 = 0;
-  T.nkb = T.rows > 0 ? (p.k + 63) / 64 : 0;
+  T.nkb = (p.k + 63) / 64;
   return T;
 }
 
