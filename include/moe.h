@@ -308,7 +308,7 @@ size_t moe_group_route_workspace(int T, int E, int k);
  * out row.  groups 1..1024; m 0..2^30 (0: nothing to do); n, k 1..2^24.  Any strides that keep
  * rows apart (ldx >= k, ldw >= the row's length, ldo >= n_out; w_stride any) and any
  * 2-byte (fp32: 4-byte) alignment; pointers and strides of x and w that are multiples of 16 bytes
- * (and for SwiGLU n/2 a multiple of 16) take the fast kernels.
+ * take the fast kernels.
  * Rows named by `rows` are copied side by side into the workspace first, as the fast kernel for many rows takes
  * them; with a workspace that is NULL or too small a slower kernel reads them where they are.  Calls that can overlap,
  * replays of graphs among them, need a workspace each.

@@ -7,11 +7,11 @@
 // two aligned words around it (one of the two comes from L1: the neighbour lane's), unless those reach past the
 // tensor's first or last byte: then it is read by elements.  Words behind the contracted length, rows of no group and row
 // numbers outside their tensor are stored as zeros.  Warps:
-//   warps 0..7   load (one step ahead in registers) and store into a ring of 4 stages;
-//   warp 8       issues the products, in parts of 512 elements in alternating results;
-//   warps 9..12  add the parts up in fp32 registers, then store the tile by elements.
-// Bound: the loads' latency and the shared-memory stores of the staging: 115 TFLOP/s at 4096 rows, n = k = 4095, 8 groups
-// (23 with 64 x 64 tiles of the warp-level mma and element loads).
+//   warps 0..15  load (two steps ahead in registers) and store into a ring of 4 stages;
+//   warp 16      issues the products, in parts of 512 elements in alternating results;
+//   warps 17..20 add the parts up in fp32 registers, then store the tile by elements.
+// Bound: the loads' latency and the shared-memory stores of the staging: 133 TFLOP/s at 4096 rows, n = k = 4095, 8 groups (23
+// with 64 x 64 tiles of the warp-level mma and element loads; 115 with 8 loading warps one step ahead).
 #include "grouped.h"
 #include "grouped_mma.cuh"
 
@@ -23,7 +23,7 @@ enum : int { GA_NK = 0, GA_KN = 1, GA_SWIGLU = 2, GA_WGRAD = 3 };
 constexpr int GA_M = 128, GA_N = 64;             // tile: rows of the first factor and of the second
 constexpr int GA_A = GA_M * 128, GA_B = GA_N * 128, GA_STAGE = GA_A + GA_B;   // bytes of a stage: 64 elements a row
 constexpr int GA_STAGES = 4;
-constexpr int GA_COPY_WARPS = 8, GA_EPI_WARPS = 4;
+constexpr int GA_COPY_WARPS = 16, GA_EPI_WARPS = 4;
 constexpr int GA_THREADS = (GA_COPY_WARPS + 1 + GA_EPI_WARPS) * 32;
 // 16-byte words of the factors that a thread stages
 constexpr int GA_AW = GA_M * 8 / (GA_COPY_WARPS * 32), GA_BW = GA_N * 8 / (GA_COPY_WARPS * 32);
@@ -170,14 +170,14 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
 
   if (warp < GA_COPY_WARPS) {
     // ---------------------------------------------------------------- staging
-    // K-major: thread: word c of rows r + 32 i.  MN-major: word c (in slabs of 8) of contracted rows r + step i.
+    // K-major: thread: word c of rows r + step i.  MN-major: word c (in slabs of 8) of contracted rows r + step i.
     const uintptr_t a_lo = (uintptr_t)p.b, b_lo = (uintptr_t)p.a;
     const uintptr_t a_hi = a_lo + 2 * (WG ? (p.b_nrows - 1) * p.ldb + p.k
                                           : (p.groups - 1) * p.b_stride + ((p.kn ? p.k : p.n) - 1) * p.ldb + (p.kn ? p.n : p.k));
     const uintptr_t b_hi = b_lo + 2 * ((p.a_nrows - 1) * p.lda + (WG ? p.n : p.k));
     const int ca = a_mn ? tid & 15 : tid & 7, ra = a_mn ? tid >> 4 : tid >> 3;
     const int cb = tid & 7, rb = tid >> 3;
-    constexpr int step_a = a_mn ? 16 : 32, step_b = 32;
+    constexpr int step_a = GA_COPY_WARPS * 32 / (a_mn ? 16 : 8), step_b = GA_COPY_WARPS * 32 / 8;
     const uint16_t* a_row[GA_AW];   // K-major: the rows' starts, null for a row of zeros
     const uint16_t* b_row[GA_BW];
     const uint16_t* w = p.b + (WG ? 0 : (long long)e * p.b_stride);
@@ -195,8 +195,7 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
       const int r = rb + step_b * i;
       b_row[i] = !b_mn && r < rows ? row_at(p.a, p.a_rows, r0 + r, p.a_nrows, p.lda) : nullptr;
     }
-    Word8 va[GA_AW], vb[GA_BW];
-    auto load = [&](int kb) {
+    auto load = [&](int kb, Word8 (&va)[GA_AW], Word8 (&vb)[GA_BW]) {
       const uint16_t* s[GA_AW];
 #pragma unroll
       for (int i = 0; i < GA_AW; ++i) {
@@ -228,10 +227,10 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    if (nkb > 0) load(0);
-    for (int kb = 0; kb < nkb; ++kb) {
+    // step kb's words, and then those of step kb + 2 in the same registers
+    auto step = [&](int kb, Word8 (&va)[GA_AW], Word8 (&vb)[GA_BW]) {
       ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1));
-      if (!ok) break;
+      if (!ok) return;
       uint8_t* st = smem + s * GA_STAGE;
 #pragma unroll
       for (int i = 0; i < GA_AW; ++i) *reinterpret_cast<uint4*>(st + at_a + i * step_a * 128) = finish8(va[i]);
@@ -240,11 +239,18 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(full0 + 8 * s);
-      if (kb + 1 < nkb) load(kb + 1);
+      if (kb + 2 < nkb) load(kb + 2, va, vb);
       if (++s == GA_STAGES) {
         s = 0;
         ph ^= 1;
       }
+    };
+    Word8 va0[GA_AW], vb0[GA_BW], va1[GA_AW], vb1[GA_BW];
+    if (nkb > 0) load(0, va0, vb0);
+    if (nkb > 1) load(1, va1, vb1);
+    for (int kb = 0; kb < nkb && ok; kb += 2) {
+      step(kb, va0, vb0);
+      if (ok && kb + 1 < nkb) step(kb + 1, va1, vb1);
     }
     if (!ok && lane == 0) *s_abort = 1;
   } else if (warp == GA_COPY_WARPS) {

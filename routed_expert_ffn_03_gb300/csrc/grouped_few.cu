@@ -37,6 +37,7 @@ struct FewArgs {
   int cluster;
   uint32_t* status;
   bool wide;            // 16-bit results can be stored in pairs
+  bool by_16;           // swiglu: W_e in boxes of 16 rows
 };
 
 __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
@@ -125,13 +126,17 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
       if (lane == 0) {
         mbar_arrive_expect_tx(bar, GF_A + n * 128);
         if (MODE == GF_NK) tma_3d<1>(da, &maps.a, kb * 64, f0, e, bar);
-        if (SW) tma_5d<1>(da, &maps.a, kb * 64, 0, 0, f0 / 16, e, bar);
+        if (SW && !a.by_16) tma_5d<1>(da, &maps.a, kb * 64, 0, 0, f0 / 16, e, bar);
         if (MODE == GF_KN) {
           tma_3d<1>(da, &maps.a, f0, kb * 64, e, bar);
           tma_3d<1>(da + SLAB_BYTES, &maps.a, f0 + 64, kb * 64, e, bar);
         }
       }
       __syncwarp();
+      if (SW && a.by_16 && lane < 8) {   // gate and up in turn, 16 rows each
+        const int f = f0 + (lane >> 1) * 16 + (lane & 1) * (p.n / 2);
+        tma_3d<1>(da + lane * 2048, &maps.a, kb * 64, f, e, bar);
+      }
       if (p.a_rows) {
         if (lane < n / 4) tma_gather4(db + lane * 512, &maps.b[0], kb * 64, gr, bar);
       } else if (lane < n / 16) {
@@ -332,6 +337,7 @@ bool launch_grouped_few(const GroupedProblem& p, int nt, int cluster, uint32_t* 
   const int n_out = p.swiglu ? p.n / 2 : p.n;
   a.nft = (int)ceil_div(n_out, p.swiglu ? 64 : 128);
   a.cluster = cluster;
+  a.by_16 = p.swiglu && p.n / 2 % 16 != 0;
   a.wide = (uintptr_t)p.d % 4 == 0 && p.ldd % 2 == 0 && n_out % 2 == 0;
   const long long tiles = (p.m / nt + (p.m < p.groups ? p.m : p.groups)) * a.nft;   // the most that m rows can make
   if (tiles * cluster > 0x3fffffff) return false;

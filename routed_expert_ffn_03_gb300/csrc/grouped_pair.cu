@@ -66,6 +66,7 @@ struct PairArgs {
   int max_tiles;       // the most that m rows can make
   uint32_t* status;
   bool wide;           // results can be stored as 4-byte pairs (forward) or by TMA (weight gradient)
+  bool by_16;          // swiglu: W_e in boxes of 16 rows
 };
 
 struct Tile {
@@ -254,11 +255,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
           if (lane == 0) {
             const int f = T.f0 + (int)rank * (SW ? 64 : 128);
             if (MODE == GP_NK) tma_3d<2>(da, &maps.a, kb * 64, f, T.e, bar);
-            if (SW) tma_5d<2>(da, &maps.a, kb * 64, 0, 0, f / 16, T.e, bar);
+            if (SW && !a.by_16) tma_5d<2>(da, &maps.a, kb * 64, 0, 0, f / 16, T.e, bar);
             if (MODE == GP_KN) {
               tma_3d<2>(da, &maps.a, f, kb * 64, T.e, bar);
               tma_3d<2>(da + SLAB_BYTES, &maps.a, f + 64, kb * 64, T.e, bar);
             }
+          }
+          if (SW && a.by_16 && lane < 8) {   // gate and up in turn, 16 rows each
+            const int f = T.f0 + (int)rank * 64 + (lane >> 1) * 16 + (lane & 1) * (p.n / 2);
+            tma_3d<2>(da + lane * 2048, &maps.a, kb * 64, f, T.e, bar);
           }
           // the half's rows, a multiple of 16, in boxes of 128, 64, 32 and 16: lane i those of bit i
           const int box = 16 << lane;
@@ -624,13 +629,13 @@ bool grouped_maps(const GroupedProblem& p, bool wgrad, bool few, GroupedMaps* m)
   const uint64_t rows = p.kn ? k : n, step = p.groups > 1 ? p.b_stride * 2 : rows * ldb;
   if (step == 0) return false;
   bool ok;
-  if (p.swiglu) {
+  if (p.swiglu && n / 2 % 16 == 0) {   // a tile's alternating runs of 16 rows of gate and up in one box
     const uint64_t h = n / 2, d[] = {k, 16, 2, h / 16, E}, st[] = {ldb, h * ldb, 16 * ldb, step};
     const uint32_t box[] = {64, 16, 2, 4, 1};
-    ok = h % 16 == 0 && tensor_map(&m->a, p.b, 2, 5, d, st, box);
+    ok = tensor_map(&m->a, p.b, 2, 5, d, st, box);
   } else {
     const uint64_t d[] = {p.kn ? n : k, p.kn ? k : n, E}, st[] = {ldb, step};
-    const uint32_t box[] = {64, p.kn ? 64u : 128u, 1};
+    const uint32_t box[] = {64, p.swiglu ? 16u : p.kn ? 64u : 128u, 1};
     ok = tensor_map(&m->a, p.b, 2, 3, d, st, box);
   }
   const uint64_t dx[] = {k, (uint64_t)p.a_nrows};
@@ -652,6 +657,7 @@ bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, uint3
   PairArgs a;
   a.p = p;
   a.status = status;
+  a.by_16 = p.swiglu && p.n / 2 % 16 != 0;
   const int n_out = p.swiglu ? p.n / 2 : p.n;
   const size_t el = p.out_dtype == GT_FP32 ? 4 : 2;
   long long tiles;

@@ -37,7 +37,7 @@ CASES = [
     (RAGGED, 256, 64), (RAGGED, 136, 72), (RAGGED, 520, 1032), ([5, 0, 3], 8, 8), ([1], 1, 1), ([33, 64, 65], 33, 7),
     ([0, 0, 4], 1000, 264), ([130, 129], 48, 100), ([1, 1, 0, 1], 2048, 2056), ([700, 0, 31], 64, 512),
     ([1] * 40, 96, 160), ([17, 16, 15, 32, 33, 31, 48, 64, 63], 272, 200), ([2, 0] * 300, 40, 48),
-    ([1, 0, 0, 2] * 256, 24, 40), ([40, 0, 3, 20] * 256, 24, 40), ([19, 2] * 512, 9, 15),
+    ([1, 0, 0, 2] * 256, 24, 40), (RAGGED, 200, 64), ([5, 2, 0, 1], 200, 136), ([300, 3], 1000, 2064), ([40, 0, 3, 20] * 256, 24, 40), ([19, 2] * 512, 9, 15),
 ]
 
 
