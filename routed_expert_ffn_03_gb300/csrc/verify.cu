@@ -8,9 +8,10 @@
 //
 // Only the row that decides is read, once: a cluster of S blocks takes a sequence, each warp a contiguous run of
 // the vocabulary in 16-byte words of p (q starts at another offset in its 16 bytes when V is odd, so its words are
-// put together from two loads).  The warps' sums are scanned over the cluster through distributed
-// shared memory, and the one warp whose run holds the threshold walks it again (from L2).  Bound: memory, with the
-// arithmetic close behind (about 14 instructions an element).
+// put together from two).  The blocks' sums are scanned over the cluster through distributed
+// shared memory, and the block whose share holds the threshold searches the run of the warp that does, all threads at
+// once (from L2; by that warp alone it took a quarter of the kernel's time).  Bound: 256 sequences of 129281 in bf16 with q
+// take 33 us, of which reading the rows is 17 at the memory's rate (116 MB); the rest is a block's chain of waits.
 #include "common.cuh"
 #include "grouped.h"
 #include "grouped_mma.cuh"
@@ -20,12 +21,10 @@ namespace moe {
 
 namespace {
 
-constexpr int VF_THREADS = 256;
-constexpr int VF_WARPS = VF_THREADS / 32;
 constexpr int VF_MAX_CLUSTER = 8;
-constexpr int VF_DEPTH = 4;
-constexpr int VF_STEP = 32 + 34;                       // 16-byte words of a step (33 of q, and one to keep 32 bytes)
-constexpr int VF_SMEM = VF_WARPS * VF_DEPTH * VF_STEP * 16;
+constexpr int VF_DEPTH = 3;
+constexpr int VF_STEP = 64;                            // 16-byte words of p in a step, two a lane
+constexpr int VF_SLOT = VF_STEP + VF_STEP + 2;         // with q's (one more where q is off a boundary, one to keep 32 bytes)
 typedef unsigned long long u64;
 
 // clamped to [0, 1]; max with NaN gives the other operand, 0
@@ -156,16 +155,19 @@ struct Row {
     const float a = load_prob<DT>(p, v);
     return v == hot ? 0 : fixed60(sub_sat(a, q ? load_prob<DT>(q, v) : 0.f));
   }
-  // 16 bytes from `shift` on of two neighbouring words (the branch is the same for the whole row)
+  // 16 bytes from `shift` on of two neighbouring words; SH: shift / 4
+  template <int SH>
   __device__ __forceinline__ uint4 align(const uint4& lo, const uint4& hi) const {
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (W::EL == 4) return make_uint4(w[SH], w[SH + 1], w[SH + 2], w[SH + 3]);
     const int by = 8 * (shift & 3);
-    auto cut = [&](uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e) {
-      return make_uint4(__funnelshift_r(a, b, by), __funnelshift_r(b, c, by), __funnelshift_r(c, d, by), __funnelshift_r(d, e, by));
-    };
-    if (shift < 4) return cut(lo.x, lo.y, lo.z, lo.w, hi.x);
-    if (shift < 8) return cut(lo.y, lo.z, lo.w, hi.x, hi.y);
-    if (shift < 12) return cut(lo.z, lo.w, hi.x, hi.y, hi.z);
-    return cut(lo.w, hi.x, hi.y, hi.z, hi.w);
+    return make_uint4(__funnelshift_r(w[SH], w[SH + 1], by), __funnelshift_r(w[SH + 1], w[SH + 2], by),
+                      __funnelshift_r(w[SH + 2], w[SH + 3], by), __funnelshift_r(w[SH + 3], w[SH + 4], by));
+  }
+  __device__ __forceinline__ uint4 align(const uint4& lo, const uint4& hi) const {
+    if (shift < 4) return align<0>(lo, hi);
+    if (shift < 8) return align<1>(lo, hi);
+    return shift < 12 ? align<2>(lo, hi) : align<3>(lo, hi);
   }
   __device__ __forceinline__ const uint4* p_at(int c) const {
     return reinterpret_cast<const uint4*>(p + (size_t)head * W::EL) + c;
@@ -173,22 +175,26 @@ struct Row {
   __device__ __forceinline__ const uint4* q_at(int c) const {   // its first word, `shift` bytes early
     return reinterpret_cast<const uint4*>(q + (size_t)head * W::EL - shift) + c;
   }
-  // the weights of word c from its 16 bytes of p and of q
+  // the weights of a word from its 16 bytes of p and of q
   template <bool Q>
-  __device__ __forceinline__ W weights(int c, const uint4& pw, const uint4& qw) const {
+  static __device__ __forceinline__ W weights(const uint4& pw, const uint4& qw) {
     W a, b;
     a.decode(pw);
     if (Q) b.decode(qw);
-    const int skip = hot - head - c * W::N;
 #pragma unroll
-    for (int i = 0; i < W::N; ++i) a.x[i] = Q ? sub_sat(a.x[i], b.x[i]) : i == skip ? 0.f : sub_sat(a.x[i], 0.f);
+    for (int i = 0; i < W::N; ++i) a.x[i] = sub_sat(a.x[i], Q ? b.x[i] : 0.f);
     return a;
   }
   template <bool Q>
   __device__ __forceinline__ W word(int c) const {
     uint4 qw = make_uint4(0, 0, 0, 0);
     if (Q) qw = shift ? align(__ldg(q_at(c)), __ldg(q_at(c) + 1)) : __ldg(q_at(c));
-    return weights<Q>(c, __ldg(p_at(c)), qw);
+    W a = weights<Q>(__ldg(p_at(c)), qw);
+    const int skip = hot - head - c * W::N;
+#pragma unroll
+    for (int i = 0; i < W::N; ++i)
+      if (!Q && i == skip) a.x[i] = 0.f;
+    return a;
   }
   static __device__ __forceinline__ u64 sum_of(const W& w) {
     Sum60 s;
@@ -196,40 +202,90 @@ struct Row {
     for (int i = 0; i < W::N; i += 2) s.add(w.x[i], w.x[i + 1]);
     return s.total(W::N);
   }
-  // Words [c0, c1) by one warp, through its ring of VF_DEPTH steps of 32 words of p and 33 of q: the copies in flight need no
-  // registers.
-  template <bool Q>
+  // Words [c0, c1) by one warp, through its ring of VF_DEPTH steps: the copies in flight need no registers.  Q: with q, SH:
+  // shift / 4, -1 where q stands on a boundary too.  `hot` is left in.
+  template <bool Q, int SH>
   __device__ __forceinline__ u64 sum_words(int c0, int c1, int lane, uint4* ring) const {
-    const int steps = (c1 - c0 + 31) / 32;
-    auto issue = [&](int i) {
-      const int c = c0 + i * 32 + lane;
-      uint4* at = ring + (i % VF_DEPTH) * VF_STEP + lane;
-      if (i < steps && c < c1) {
-        copy16(at, p_at(c));
+    const int n = c1 - c0, full = n / VF_STEP, rest = n % VF_STEP, steps = full + (rest != 0);
+    const uint4 *ps = p_at(c0) + lane, *qs = Q ? q_at(c0) + lane : nullptr;
+    ring += lane;
+    auto issue = [&](int i, int slot) {
+      uint4* at = ring + slot * VF_SLOT;
+      if (i < full) {
+        copy16(at, ps);
+        copy16(at + 32, ps + 32);
         if (Q) {
-          copy16(at + 32, q_at(c));
-          if (shift && (lane == 31 || c == c1 - 1)) copy16(at + 33, q_at(c) + 1);
+          copy16(at + VF_STEP, qs);
+          copy16(at + VF_STEP + 32, qs + 32);
+          if (SH >= 0 && lane == 31) copy16(at + VF_STEP + 33, qs + 33);
         }
+        ps += VF_STEP;
+        if (Q) qs += VF_STEP;
+      } else if (i < steps) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (lane + 32 * j < rest) {
+            copy16(at + 32 * j, ps + 32 * j);
+            if (Q) copy16(at + VF_STEP + 32 * j, qs + 32 * j);
+            if (SH >= 0 && (lane == 31 || lane + 32 * j == rest - 1)) copy16(at + VF_STEP + 32 * j + 1, qs + 32 * j + 1);
+          }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    auto add_word = [&](const uint4* at, Sum60& s) {
+      uint4 qw = make_uint4(0, 0, 0, 0);
+      if (Q) qw = SH >= 0 ? align<SH < 0 ? 0 : SH>(at[VF_STEP], at[VF_STEP + 1]) : at[VF_STEP];
+      const W x = weights<Q>(at[0], qw);
 #pragma unroll
-    for (int i = 0; i < VF_DEPTH - 1; ++i) issue(i);
+      for (int i = 0; i < W::N; i += 2) s.add(x.x[i], x.x[i + 1]);
+    };
+    issue(0, 0);
+    issue(1, 1);
     u64 sum = 0;
-    for (int i = 0; i < steps; ++i) {
-      issue(i + VF_DEPTH - 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(VF_DEPTH - 1) : "memory");
-      __syncwarp();
-      const int c = c0 + i * 32 + lane;
-      const uint4* at = ring + (i % VF_DEPTH) * VF_STEP + lane;
-      if (c < c1) {
-        uint4 qw = make_uint4(0, 0, 0, 0);
-        if (Q) qw = shift ? align(at[32], at[33]) : at[32];
-        sum += sum_of(weights<Q>(c, at[0], qw));
+    Sum60 s;
+    constexpr int RUN = 256 / (2 * W::N);   // steps whose sums fit 32 bits
+    int slot = 0;
+    for (int i = 0; i < full; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(VF_DEPTH - 2) : "memory");
+      __syncwarp();   // every lane's copies are there, and the slot written next has been read
+      issue(i + 2, slot ? slot - 1 : 2);
+      const uint4* at = ring + slot * VF_SLOT;
+      add_word(at, s);
+      add_word(at + 32, s);
+      if (i % RUN == RUN - 1) {
+        sum += s.total(256);
+        s = Sum60();
       }
-      __syncwarp();   // the step's slot is written again from the next round on
+      slot = slot == 2 ? 0 : slot + 1;
     }
+    sum += s.total((uint32_t)(full % RUN) * 2 * W::N);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (lane + 32 * j < rest) {
+        Sum60 t;
+        add_word(ring + slot * VF_SLOT + 32 * j, t);
+        sum += t.total(W::N);
+      }
+    __syncwarp();   // the ring may be written again
     return sum;
+  }
+  // one warp's sum of its words
+  __device__ __forceinline__ u64 sum_of_run(int c0, int c1, int lane, uint4* ring) const {
+    if (!q) {
+      u64 sum = sum_words<false, -1>(c0, c1, lane, ring);
+      const int at = hot - head;
+      if (hot >= 0 && at >= c0 * W::N && at < c1 * W::N && lane == 0) sum -= fixed60(sub_sat(load_prob<DT>(p, hot), 0.f));
+      return sum;
+    }
+    switch (shift ? shift >> 2 : -1) {
+      case 0: return sum_words<true, DT == GT_FP32 ? -1 : 0>(c0, c1, lane, ring);
+      case 1: return sum_words<true, 1>(c0, c1, lane, ring);
+      case 2: return sum_words<true, 2>(c0, c1, lane, ring);
+      case 3: return sum_words<true, 3>(c0, c1, lane, ring);
+      default: return sum_words<true, -1>(c0, c1, lane, ring);
+    }
   }
   // A warp's walk to the least element with run + cumulative weight > thr.  One step of up to 32 elements, or words, from
   // `at`: advances run, returns the element or -1 (the same in every lane).
@@ -263,22 +319,52 @@ struct Row {
     run = __shfl_sync(0xffffffffu, cum, 31);
     return found;
   }
-  // Words [c0, c1): first the sums of AHEAD steps whose loads are all in flight, then the one step that holds it.
-  template <bool Q>
-  __device__ __forceinline__ int walk_words(int c0, int c1, u64 thr, u64& run, int lane) const {
-    constexpr int AHEAD = 4;
-    for (int c = c0; c < c1; c += 32 * AHEAD) {
-      u64 s[AHEAD];
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) s[i] = c + 32 * i + lane < c1 ? sum_of(word<Q>(c + 32 * i + lane)) : 0;
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        const u64 sum = warp_sum(s[i]);
-        if (run + sum > thr) return step(true, c + 32 * i, c1, thr, run, lane);
-        run += sum;
-      }
+  // The least element of words [c0, c1) with run + cumulative weight > thr, by the whole block: each thread sums a few
+  // neighbouring words, and the warp of the one that holds it steps through those.  -1 in the other warps; run advances to
+  // the sum behind the words, and is > thr in all of them if the element is among the words.  A run of more than 8 words
+  // a thread is first cut down to the warp's share that holds it.
+  template <bool Q, int WARPS>
+  __device__ __forceinline__ int search(int c0, int c1, u64 thr, u64& run, int lane, u64* part) const {
+    const int warp = threadIdx.x >> 5;
+    while (c1 - c0 > 8 * 32 * WARPS) {
+      const int len = c1 - c0, a0 = c0 + (int)((long long)len * warp / WARPS), a1 = c0 + (int)((long long)len * (warp + 1) / WARPS);
+      u64 mine = 0;
+#pragma unroll 4
+      for (int w = a0 + lane; w < a1; w += 32) mine += sum_of(word<Q>(w));
+      mine = warp_sum(mine);
+      if (lane == 0) part[warp] = mine;
+      __syncthreads();
+      int hit = 0;
+      while (hit < WARPS && run + part[hit] <= thr) run += part[hit++];
+      __syncthreads();   // part has been read
+      if (hit == WARPS) return -1;
+      c1 = c0 + (int)((long long)len * (hit + 1) / WARPS);
+      c0 += (int)((long long)len * hit / WARPS);
     }
-    return -1;
+    const int n = c1 - c0, per = (n + WARPS * 32 - 1) / (WARPS * 32);
+    const int w0 = c0 + min((int)threadIdx.x * per, n), w1 = min(w0 + per, c1);
+    u64 mine = 0;
+#pragma unroll 4
+    for (int w = w0; w < w1; ++w) mine += sum_of(word<Q>(w));
+    const u64 inc = warp_scan(mine, lane);
+    if (lane == 31) part[warp] = inc;
+    __syncthreads();
+    u64 before = run;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w == warp) before = run;
+      run += part[w];
+    }
+    before += inc - mine;
+    const unsigned hit = __ballot_sync(0xffffffffu, before <= thr && thr < before + mine);
+    int found = -1;
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      u64 at = __shfl_sync(0xffffffffu, before, l);
+      const int end = __shfl_sync(0xffffffffu, w1, l);
+      for (int w = __shfl_sync(0xffffffffu, w0, l); w < end && found < 0; w += 32) found = step(true, w, end, thr, at, lane);
+    }
+    return found;
   }
 };
 
@@ -286,9 +372,10 @@ __device__ __forceinline__ void st_cluster64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-template <int DT>
-__global__ void __launch_bounds__(VF_THREADS, 4) verify_kernel(VerifyArgs a, int S) {
-  __shared__ u64 part[VF_WARPS];
+template <int DT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(VerifyArgs a, int S) {
+  constexpr int VF_WARPS = THREADS / 32;
+  __shared__ u64 part[VF_WARPS], found_part[VF_WARPS];
   __shared__ u64 block_sum[2][VF_MAX_CLUSTER];   // by attempt and rank: every block writes its sum to all
   extern __shared__ uint4 rings[];
   constexpr int EL = Word<DT>::EL;
@@ -299,6 +386,7 @@ __global__ void __launch_bounds__(VF_THREADS, 4) verify_kernel(VerifyArgs a, int
 
   if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this block has started
 
+  pdl_wait();   // (the next kernel is not let in early: its blocks would crowd on the SMs that have room)
   // lane i: draft i (every warp alike, so nothing is passed between them)
   const int L = a.lengths ? min(max(__ldg(a.lengths + b), 0), a.D) : a.D;
   int tok = -1;
@@ -325,41 +413,44 @@ __global__ void __launch_bounds__(VF_THREADS, 4) verify_kernel(VerifyArgs a, int
   const int W = S * VF_WARPS, me = rank * VF_WARPS + warp;
   const int c0 = (int)((long long)row.words * me / W), c1 = (int)((long long)row.words * (me + 1) / W);
   const int tail = row.head + row.words * Word<DT>::N;   // the first element behind the words
-  uint4* ring = rings + warp * VF_DEPTH * VF_STEP;
+  uint4* ring = rings + warp * VF_DEPTH * VF_SLOT;
   bool drawn = false;
   for (int attempt = 0; attempt < 2; ++attempt) {
-    u64 sum = row.q ? row.template sum_words<true>(c0, c1, lane, ring) : row.template sum_words<false>(c0, c1, lane, ring);
+    u64 sum = row.sum_of_run(c0, c1, lane, ring);
     if (me == 0 && lane < row.head) sum += row.one(lane);
     if (me == W - 1 && tail + lane < a.V) sum += row.one(tail + lane);
     sum = warp_sum(sum);
     if (attempt) __syncthreads();   // part has been read
     if (lane == 0) part[warp] = sum;
     __syncthreads();
-    u64 before = 0, total = 0;
+    u64 block = 0, before = 0;   // the block's sum, and the blocks' before it
 #pragma unroll
-    for (int w = 0; w < VF_WARPS; ++w) {
-      if (w == warp) before = total;
-      total += part[w];
-    }
+    for (int w = 0; w < VF_WARPS; ++w) block += part[w];
+    u64 total = block;
     if (S > 1) {
       if (attempt == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // and so have the others
-      if ((int)threadIdx.x < S) st_cluster64(map_rank(smem_u32(&block_sum[attempt][rank]), threadIdx.x), total);
+      if ((int)threadIdx.x < S) st_cluster64(map_rank(smem_u32(&block_sum[attempt][rank]), threadIdx.x), block);
       cluster_sync_all();   // after it nothing is read from another block: a block may end when it has no more to do
       const u64 s = lane < S ? block_sum[attempt][lane] : 0;
       const u64 inc = warp_scan(s, lane);
       total = __shfl_sync(0xffffffffu, inc, 31);
-      before += __shfl_sync(0xffffffffu, inc - s, rank);
+      before = __shfl_sync(0xffffffffu, inc - s, rank);
     }
     if (total) {
       const u64 thr = __umul64hi(U, total);   // floor(u total) < total
-      if (before <= thr && thr < before + sum) {
+      if (before <= thr && thr < before + block) {   // the same in the whole block
         u64 run = before;
+        int hit = 0;   // the warp whose run holds it
+        while (hit < VF_WARPS - 1 && run + part[hit] <= thr) run += part[hit++];
+        const int h = rank * VF_WARPS + hit, h0 = (int)((long long)row.words * h / W), h1 = (int)((long long)row.words * (h + 1) / W);
         int v = -1;
-        if (me == 0) v = row.step(false, 0, row.head, thr, run, lane);
-        if (v < 0)
-          v = row.q ? row.template walk_words<true>(c0, c1, thr, run, lane) : row.template walk_words<false>(c0, c1, thr, run, lane);
-        if (v < 0) v = row.step(false, tail, a.V, thr, run, lane);
-        if (lane == 0) a.tokens[(long long)b * (a.D + 1) + r] = v;
+        if (h == 0) v = row.step(false, 0, row.head, thr, run, lane);
+        if (v < 0) {
+          v = row.q ? row.template search<true, VF_WARPS>(h0, h1, thr, run, lane, found_part)
+                    : row.template search<false, VF_WARPS>(h0, h1, thr, run, lane, found_part);
+          if (run <= thr) v = row.step(false, tail, a.V, thr, run, lane);
+        }
+        if (lane == 0 && v >= 0) a.tokens[(long long)b * (a.D + 1) + r] = v;   // (each warp that has it has the same)
       }
       drawn = true;
       break;
@@ -376,39 +467,54 @@ __global__ void __launch_bounds__(VF_THREADS, 4) verify_kernel(VerifyArgs a, int
   }
 }
 
-template <int DT>
+constexpr int verify_smem(int threads) { return threads / 32 * VF_DEPTH * VF_SLOT * 16; }
+
+template <int DT, int THREADS>
 cudaError_t launch_as(const VerifyArgs& a, int S, cudaStream_t s) {
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)a.B * S);
-  c.blockDim = dim3(VF_THREADS);
-  c.dynamicSmemBytes = VF_SMEM;
+  c.blockDim = dim3(THREADS);
+  c.dynamicSmemBytes = verify_smem(THREADS);
   c.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = S;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, verify_kernel<DT>, a, S);
+  c.numAttrs = 2;
+  return cudaLaunchKernelEx(&c, verify_kernel<DT, THREADS>, a, S);
+}
+template <int THREADS>
+cudaError_t launch_type(const VerifyArgs& a, int S, cudaStream_t s) {
+  if (a.dtype == GT_FP32) return launch_as<GT_FP32, THREADS>(a, S, s);
+  return a.dtype == GT_BF16 ? launch_as<GT_BF16, THREADS>(a, S, s) : launch_as<GT_FP16, THREADS>(a, S, s);
 }
 
 }  // namespace
 
 cudaError_t verify_set_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(verify_kernel<GT_FP32>, cudaFuncAttributeMaxDynamicSharedMemorySize, VF_SMEM);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(verify_kernel<GT_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, VF_SMEM);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(verify_kernel<GT_FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, VF_SMEM);
+  auto set = [](void (*kernel)(VerifyArgs, int)) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, verify_smem(256));
+  };
+  cudaError_t e = set(verify_kernel<GT_FP32, 256>);
+  if (e == cudaSuccess) e = set(verify_kernel<GT_BF16, 256>);
+  if (e == cudaSuccess) e = set(verify_kernel<GT_FP16, 256>);
   return e;
 }
 
 cudaError_t launch_verify(const VerifyArgs& a, int num_sms, cudaStream_t s) {
-  // Blocks to a sequence: four to an SM in all, so that one streams while others wait (a block is a chain of waits: drafts,
-  // sums, scan, walk), with a few words for every lane.  256 sequences of 129281 in 1 / 2 / 4 / 8 blocks each:
-  // 77 / 51 / 43 / 44 us; 64 sequences: 58 / 33 / 22 / 19 us; blocks of 512 threads: 53 / 48 / 50 / 66 us.
-  int S = 1;
-  while (S < VF_MAX_CLUSTER && (long long)a.B * S < 4 * num_sms && a.V >= 2048 * S) S *= 2;
-  if (a.dtype == GT_FP32) return launch_as<GT_FP32>(a, S, s);
-  return a.dtype == GT_BF16 ? launch_as<GT_BF16>(a, S, s) : launch_as<GT_FP16>(a, S, s);
+  // Blocks to a sequence: 8, while that makes no more than two blocks an SM, or leaves each 60000 bytes of p: small shares
+  // have more waits (drafts, sums, scan, search) to an element, large ones end less evenly.  In 1 / 2 / 4 / 8 blocks each,
+  // us: 64 sequences of 129281 in bf16 21 / 14 / 12.1 / 12.3; 256 35 / 36 / 33 / 37; 512 65 / 54 / 54 / 66; 256 of 32000 10.4 / 12.0 / 14.9 / 21.2.
+  const int el = a.dtype == GT_FP32 ? 4 : 2;
+  int S = VF_MAX_CLUSTER;
+  while (S > 1 && (a.V < 1024 * S || ((long long)a.B * S > 2 * num_sms && (long long)a.V * el < 60000ll * S))) S /= 2;
+  // Many short sequences: of blocks of 128 threads twice as many stand on an SM.  2048 of 3000 in bf16 15 and 23 us, of 12000
+  // 29 and 35, of 24000 49 and 46; 608 of 12000 14 and 11.
+  if (a.B > 4 * num_sms && (long long)a.V * el < 40000) return launch_type<128>(a, 1, s);
+  return launch_type<256>(a, S, s);
 }
 
 }  // namespace moe

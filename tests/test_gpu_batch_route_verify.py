@@ -155,6 +155,15 @@ def test_verify_large_vocabulary(M, dtype):
     check_verify(M, p, draft, u)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("Bn,D,V", [(640, 1, 5001), (320, 1, 20001), (160, 1, 65001), (80, 1, 121001), (2, 1, 1100003)])
+def test_verify_shares(M, Bn, D, V, dtype):
+    """Many sequences of short rows, few of long ones, and what lies between: other numbers of blocks to a sequence."""
+    p, draft, u, q = make(Bn, D, V, dtype, V, sharp=1.0)
+    check_verify(M, p, draft, u, q)
+    check_verify(M, p, draft, u)
+
+
 @pytest.mark.parametrize("V", [10, 999, 5000])
 def test_verify_borders(M, V):
     """Random numbers at the borders: 0, the last below 1, 1, and sums that fall on a border exactly."""
