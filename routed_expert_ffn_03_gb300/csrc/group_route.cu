@@ -1,13 +1,13 @@
 // group_route.cu - router selection of a batch from its logits, pairs grouped by expert.
 //
-// A block takes a slice of the tokens; each warp selects one token's k experts at a time (k rounds of two warp
-// reductions over order-preserving keys of the logits), writes ids and weights, and the block counts its
+// A block takes a slice of the tokens; each warp selects two tokens' experts at a time over order-preserving keys of the
+// logits, writes ids and weights, and the block counts its
 // pairs by expert.  Then a block sums the counts of the blocks before it, scans the experts' totals into offsets,
 // and places its pairs in order: a stable counting sort, in which no atomic decides a position, so the same logits give
-// the same arrays.  Up to 64 tokens are one block of one launch; more are two launches over one block of 32 warps an SM, the
-// second waiting for the first on the device.  Bound: the
-// integer pipe while selecting (about 300 instructions a token), latency while placing: 16384 tokens of 256 bf16 logits,
-// k = 8, take 21 us (13 selecting; 10 MB, 1.5 us at the memory's rate), one token 5.7 us.
+// the same arrays.  Up to 512 tokens are one cluster of one launch; more are two launches over one block of 32 warps an SM,
+// the second waiting for the first on the device.  Bound: issue while selecting (about 350 instructions a token, 2.4 us for
+// 32 tokens an SM), latency while placing: 16384 tokens of 256 bf16 logits, k = 8, take 19.6 us (10 MB, 1.5 us at the
+// memory's rate), of which 8 are two launches' of any size; one token 4.8 us.
 #include "common.cuh"
 #include "group_route.h"
 #include "grouped.h"
@@ -20,7 +20,9 @@ namespace {
 
 constexpr int GR_THREADS = 1024;
 constexpr int GR_WARPS = GR_THREADS / 32;
-constexpr int GR_ONE_BLOCK = 64;      // tokens of the one-launch form: two a warp
+// Tokens of the one-launch form, a cluster of up to 8 blocks: one or two a warp.  512 of 256 experts: 10.2 us, in two launches
+// 10.4, and 16 with the host's part; 1000: 15.0 and 10.4.  256 of 1000 experts, k = 32: 33 us, 1000 111 and 36.
+constexpr int one_launch(int E) { return E <= 512 ? 512 : 256; }
 constexpr int GR_CLUSTER = 2;         // blocks that add up their counts before they leave (4 do not fill every SM: 33 us, not 20)
 constexpr int GR_COUNTS = 16384;      // counts by warp and expert that a block holds
 
@@ -55,49 +57,56 @@ __device__ __forceinline__ void load_token(const GroupRouteArgs& a, long long t,
 template <int NV>
 __device__ __forceinline__ void token_keys(const GroupRouteArgs& a, int lane, const float (&l)[NV], uint32_t (&key)[NV]) {
   constexpr uint32_t inf = 0xff800000u;   // key of +inf, which counts as the one below
+  auto keys = [&](auto value) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float x = l[i];
-    if (a.dtype == GT_BF16) x = __uint_as_float(__float_as_uint(x) << 16);
-    if (a.dtype == GT_FP16) x = __half2float(__ushort_as_half((unsigned short)__float_as_uint(x)));
-    const bool live = x > -INFINITY && lane + 32 * i < a.E;   // NaN is not
-    key[i] = live ? (min(logit_key(x), inf - 1u) & ~1023u) | (uint32_t)(1023 - lane - 32 * i) : 0u;
-  }
-}
-
-// one comparator of a sorting network over the warp: of the pair (lane, lane ^ j) the lower lane keeps the larger key where
-// `down`, the smaller one otherwise
-__device__ __forceinline__ uint32_t comparator(uint32_t v, int j, bool down, int lane) {
-  const uint32_t o = __shfl_xor_sync(0xffffffffu, v, j);
-  return (((lane & j) == 0) == down) ? max(v, o) : min(v, o);
-}
-
-// The first n of the keys in descending order, lane j the j-th (0: none), for n <= SORTED: the lanes' largest and second
-// keys are sorted over the warp (descending and ascending) and merged, 35 comparators in all, which is right unless some
-// lane's third belongs to the n (one token in 20 for 8 of 256).  Returns false then.
-constexpr int SORTED = 10;
-template <int NV>
-__device__ __forceinline__ bool sorted_keys(const uint32_t (&key)[NV], int n, int lane, uint32_t& mine) {
-  uint32_t b1 = 0, b2 = 0, b3 = 0;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const uint32_t x = min(b1, key[i]), y = min(b2, x);
-    b1 = max(b1, key[i]);
-    b2 = max(b2, x);
-    b3 = max(b3, y);
-  }
-#pragma unroll
-  for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll
-    for (int j = k >> 1; j; j >>= 1) {
-      b1 = comparator(b1, j, (lane & k) == 0 || k == 32, lane);
-      b2 = comparator(b2, j, !((lane & k) == 0 || k == 32), lane);
+    for (int i = 0; i < NV; ++i) {
+      const float x = value(l[i]);
+      const bool live = x > -INFINITY && lane + 32 * i < a.E;   // NaN is not
+      key[i] = live ? (min(logit_key(x), inf - 1u) & ~1023u) | (uint32_t)(1023 - lane - 32 * i) : 0u;
     }
-  uint32_t v = max(b1, b2);   // one falling, one rising: the 32 largest of both, as a bitonic sequence
+  };
+  if (a.dtype == GT_BF16) keys([](float x) { return __uint_as_float(__float_as_uint(x) << 16); });
+  else if (a.dtype == GT_FP16) keys([](float x) { return __half2float(__ushort_as_half((unsigned short)__float_as_uint(x))); });
+  else keys([](float x) { return x; });
+}
+
+// The first n of the keys in descending order, lane j the j-th (0: none), for n <= FEW: each round takes the largest of the
+// lanes' firsts, and the lane that held it steps to its second and third.  ok is false where a lane gave all three (one
+// token in 20 for 8 of 256).  U tokens side by side, as each round waits for the one before.  (A sorting network over the
+// warp takes twice the instructions: 20.8 and 19.6 us for 16384 tokens.)
+constexpr int FEW = 10;
+template <int NV, int U>
+__device__ __forceinline__ void few_keys(const uint32_t (&key)[U][NV], int n, int lane, uint32_t (&mine)[U], bool (&ok)[U]) {
+  uint32_t b1[U], b2[U], b3[U];
+  bool three[U];
 #pragma unroll
-  for (int j = 16; j; j >>= 1) v = comparator(v, j, true, lane);
-  mine = v;
-  return !__any_sync(0xffffffffu, b3 > __shfl_sync(0xffffffffu, v, n - 1));
+  for (int u = 0; u < U; ++u) {
+    b1[u] = b2[u] = b3[u] = mine[u] = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t x = min(b1[u], key[u][i]), y = min(b2[u], x);
+      b1[u] = max(b1[u], key[u][i]);
+      b2[u] = max(b2[u], x);
+      b3[u] = max(b3[u], y);
+    }
+    three[u] = b3[u] != 0;
+  }
+#pragma unroll
+  for (int j = 0; j < FEW; ++j) {
+    if (j >= n) break;   // uniform
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t b = __reduce_max_sync(0xffffffffu, b1[u]);
+      if (lane == j) mine[u] = b;
+      if (b1[u] == b) {
+        b1[u] = b2[u];
+        b2[u] = b3[u];
+        b3[u] = 0;
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) ok[u] = !__any_sync(0xffffffffu, three[u] && b1[u] == 0);
 }
 
 // The same for any n <= 32 by rounds: the warp's largest key is the next, and the lane that held it looks for its next.
@@ -122,16 +131,12 @@ __device__ __forceinline__ uint32_t rounds_of_keys(uint32_t (&key)[NV], int n, i
   return mine;
 }
 
-// The k best of one token, by one warp: lane j < k receives the j-th id (-1: none left).  Of fp32 logits one more key than k
-// shows whether two neighbours in the order share their leading bits (1 or 2 tokens in 100 of random ones).  Among the
-// k they are then ordered by their whole keys; if the k-th and the one behind it share them, or the latter is not
+// The k best of one token from its sorted keys: lane j < k receives the j-th id (-1: none left).  Of fp32 logits one more
+// key than k shows whether two neighbours in the order share their leading bits (1 or 2 tokens in 100 of random ones).  Among
+// the k they are then ordered by their whole keys; if the k-th and the one behind it share them, or the latter is not
 // known (k = 32), the token is selected again from whole keys, with a second maximum for the id.
 template <int NV>
-__device__ __forceinline__ int token_topk(const GroupRouteArgs& a, long long t, int lane, const float (&l)[NV]) {
-  uint32_t key[NV], mine = 0;
-  token_keys<NV>(a, lane, l, key);
-  const int n = a.dtype == GT_FP32 ? min(a.k + 1, 32) : a.k;
-  if (n > SORTED || !sorted_keys<NV>(key, n, lane, mine)) mine = rounds_of_keys<NV>(key, n, lane);
+__device__ __forceinline__ int token_topk(const GroupRouteArgs& a, long long t, int lane, uint32_t mine) {
   int e = lane < a.k && mine ? 1023 - (int)(mine & 1023u) : -1;
   if (a.dtype == GT_FP32) {
     const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
@@ -174,43 +179,66 @@ __device__ __forceinline__ int token_topk(const GroupRouteArgs& a, long long t, 
   return e;
 }
 
-// one token by one warp: its ids and weights
-template <int NV>
-__device__ __forceinline__ int route_token(const GroupRouteArgs& a, long long t, int lane, const float (&logits)[NV]) {
-  const int e = token_topk<NV>(a, t, lane, logits);
-  // softmax over the selected logits, or over their log sigmoids: exp(z_j - z_0) / sum, the
-  // first being the largest of both
-  const float l = e >= 0 ? logit_of(a, t, e) : 0.f;
-  float z = l;
-  if (a.kind == 1) z = fminf(l, 0.f) - log1pf(expf(-fabsf(l)));
-  const float z0 = __shfl_sync(0xffffffffu, z, 0);
-  const float num = lane < a.k && e >= 0 ? expf(z - z0) : 0.f;
-  float den = num;
+// U tokens by one warp, t and every GR_WARPS-th behind it up to t1: their ids and weights, and their pairs by expert into hist
+template <int NV, int U>
+__device__ __forceinline__ void route_tokens(const GroupRouteArgs& a, long long t, long long t1, int lane, float (&l)[U][NV],
+                                             int* hist) {
+  uint32_t key[U][NV], mine[U];
+  bool ok[U];
+  const int n = a.dtype == GT_FP32 ? min(a.k + 1, 32) : a.k;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-  if (lane < a.k) {
-    a.idx[t * a.k + lane] = e;
-    a.weights[t * a.k + lane] = e >= 0 ? num / den : 0.f;
+  for (int u = 0; u < U; ++u) token_keys<NV>(a, lane, l[u], key[u]);
+  if (n <= FEW) few_keys<NV, U>(key, n, lane, mine, ok);
+  float z[U], num[U], den[U];
+  int e[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long tt = t + u * GR_WARPS;
+    e[u] = -1;
+    z[u] = 0.f;
+    if (tt >= t1) continue;
+    if (n > FEW || !ok[u]) mine[u] = rounds_of_keys<NV>(key[u], n, lane);
+    e[u] = token_topk<NV>(a, tt, lane, mine[u]);
+    // softmax over the selected logits, or over their log sigmoids: exp(z_j - z_0) / sum, the first being the largest
+    // of both; a 16-bit logit stands in its key whole (+inf as a large value)
+    float l = 0.f;
+    if (e[u] >= 0)
+      l = a.dtype == GT_FP32 ? logit_of(a, tt, e[u]) : key_logit(mine[u] >> 31 ? mine[u] & ~1023u : mine[u] | 1023u);
+    z[u] = a.kind == 1 ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : l;
   }
-  return e;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float z0 = __shfl_sync(0xffffffffu, z[u], 0);
+    den[u] = num[u] = lane < a.k && e[u] >= 0 ? expf(z[u] - z0) : 0.f;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int u = 0; u < U; ++u) den[u] += __shfl_xor_sync(0xffffffffu, den[u], o);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long tt = t + u * GR_WARPS;
+    if (lane < a.k && tt < t1) {
+      a.idx[tt * a.k + lane] = e[u];
+      a.weights[tt * a.k + lane] = e[u] >= 0 ? num[u] / den[u] : 0.f;
+      if (e[u] >= 0) atomicAdd(&hist[e[u]], 1);   // a count: its order does not matter
+    }
+  }
 }
 
 // this block's tokens; and its pairs by expert into hist (shared)
 template <int NV>
 __device__ __forceinline__ void select_tokens(const GroupRouteArgs& a, int* hist) {
+  constexpr int U = NV <= 8 ? 2 : 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int e = threadIdx.x; e < a.E; e += GR_THREADS) hist[e] = 0;
   __syncthreads();
   const long long t0 = min((long long)blockIdx.x * a.per_block, (long long)a.T), t1 = min(t0 + a.per_block, (long long)a.T);
-  float l[NV], ahead[NV];
-  if (t0 + warp < t1) load_token<NV>(a, t0 + warp, lane, ahead);
-  for (long long t = t0 + warp; t < t1; t += GR_WARPS) {
+  for (long long t = t0 + warp; t < t1; t += U * GR_WARPS) {
+    float l[U][NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = ahead[i];
-    if (NV <= 8 && t + GR_WARPS < t1) load_token<NV>(a, t + GR_WARPS, lane, ahead);   // while this token is selected
-    const int e = route_token<NV>(a, t, lane, l);
-    if (NV > 8 && t + GR_WARPS < t1) load_token<NV>(a, t + GR_WARPS, lane, ahead);
-    if (lane < a.k && e >= 0) atomicAdd(&hist[e], 1);   // a count: its order does not matter
+    for (int u = 0; u < U; ++u) load_token<NV>(a, min(t + u * GR_WARPS, t1 - 1), lane, l[u]);
+    route_tokens<NV, U>(a, t, t1, lane, l, hist);
   }
   __syncthreads();
 }
@@ -296,24 +324,39 @@ __device__ __forceinline__ void place_pairs(const GroupRouteArgs& a, const Pairs
   }
 }
 
+// One launch: the blocks are one cluster, and read each other's counts.
 template <int NV>
 __global__ void __launch_bounds__(GR_THREADS, 1) group_one_kernel(GroupRouteArgs a) {
   extern __shared__ int counts[];
-  __shared__ int all[1024], before[1024];
+  __shared__ int hist[1024], all[1024], before[1024];
   const Pairs s = block_pairs(a, counts);
   for (int i = threadIdx.x; i < s.W * a.E; i += GR_THREADS) counts[i] = 0;
-  before[threadIdx.x] = 0;
   pdl_wait();
-  select_tokens<NV>(a, all);
-  count_pairs(a, s);
-  __syncthreads();
+  select_tokens<NV>(a, hist);
+  if (a.blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  count_pairs(a, s);   // while the others arrive
+  if (a.blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const int e = threadIdx.x, rank = a.blocks > 1 ? (int)cluster_rank() : 0;
+  int sum = 0, mine = 0;
+  if (e < a.E)
+    for (int r = 0; r < a.blocks; ++r) {
+      int c = hist[e];
+      if (a.blocks > 1)
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(c) : "r"(map_rank(smem_u32(&hist[e]), r)) : "memory");
+      if (r < rank) mine += c;
+      sum += c;
+    }
+  all[e] = sum;
+  before[e] = mine;
+  if (a.blocks > 1) cluster_sync_all();   // the others read this block's counts until here
+  else __syncthreads();
   place_pairs(a, s, before, all, counts);
 }
 
 // The counts leave by clusters, hist [clusters][E], with each block's share of its cluster's before it, [blocks][E] behind:
 // the next kernel's blocks then read half of the rows (read one by one, they took half of that kernel's time).
 template <int NV>
-__global__ void __cluster_dims__(GR_CLUSTER, 1, 1) __launch_bounds__(GR_THREADS, 1) group_select_kernel(GroupRouteArgs a) {
+__global__ void __launch_bounds__(GR_THREADS, 1) group_select_kernel(GroupRouteArgs a) {
   __shared__ int hist[1024];
   pdl_launch_dependents();
   pdl_wait();
@@ -363,17 +406,20 @@ __global__ void __launch_bounds__(GR_THREADS, 1) group_place_kernel(GroupRouteAr
 }
 
 template <typename... A>
-cudaError_t launch(void (*kernel)(A...), int blocks, size_t smem, cudaStream_t s, A... args) {
+cudaError_t launch(void (*kernel)(A...), int blocks, int cluster, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(blocks);
   c.blockDim = dim3(GR_THREADS);
   c.dynamicSmemBytes = smem;
   c.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   c.attrs = at;
-  c.numAttrs = 1;
+  c.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
@@ -381,9 +427,9 @@ template <int NV>
 cudaError_t launch_as(const GroupRouteArgs& a, cudaStream_t s) {
   const int warps = GR_COUNTS / a.E < GR_WARPS ? GR_COUNTS / a.E : GR_WARPS;
   const size_t smem = (size_t)warps * a.E * sizeof(int);
-  if (a.blocks == 1) return launch(group_one_kernel<NV>, 1, smem, s, a);
-  cudaError_t e = launch(group_select_kernel<NV>, a.blocks, 0, s, a);
-  return e != cudaSuccess ? e : launch(group_place_kernel, a.blocks, smem, s, a);
+  if (a.T <= one_launch(a.E)) return launch(group_one_kernel<NV>, a.blocks, a.blocks, smem, s, a);
+  cudaError_t e = launch(group_select_kernel<NV>, a.blocks, GR_CLUSTER, 0, s, a);
+  return e != cudaSuccess ? e : launch(group_place_kernel, a.blocks, 1, smem, s, a);
 }
 
 template <int NV>
@@ -406,11 +452,17 @@ cudaError_t group_route_set_attributes() {
 GroupRoutePlan group_route_plan(int T, int E, int k) {
   constexpr int kBlocks = 152;   // one an SM; a constant, so that the workspace's size does not depend on the device
   GroupRoutePlan p;
-  p.per_block = T <= GR_ONE_BLOCK ? T : (T - 1) / kBlocks + 1;
-  if (T > GR_ONE_BLOCK && p.per_block < GR_WARPS) p.per_block = GR_WARPS;
-  p.blocks = (T - 1) / p.per_block + 1;
-  if (T > GR_ONE_BLOCK) p.blocks = (p.blocks + GR_CLUSTER - 1) / GR_CLUSTER * GR_CLUSTER;   // some without tokens
-  p.workspace = T > GR_ONE_BLOCK ? (size_t)(p.blocks + p.blocks / GR_CLUSTER) * E * sizeof(int) : 0;
+  if (T <= one_launch(E)) {   // a token a warp, from eight blocks on more
+    p.blocks = 1;
+    while (p.blocks < 8 && p.blocks * GR_WARPS < T) p.blocks *= 2;   // (some may have no tokens)
+    p.per_block = (T - 1) / p.blocks + 1;
+    p.workspace = 0;
+  } else {
+    p.per_block = (T - 1) / kBlocks + 1;
+    if (p.per_block < GR_WARPS) p.per_block = GR_WARPS;
+    p.blocks = ((T - 1) / p.per_block + GR_CLUSTER) / GR_CLUSTER * GR_CLUSTER;   // (one may have none)
+    p.workspace = (size_t)(p.blocks + p.blocks / GR_CLUSTER) * E * sizeof(int);
+  }
   return p;
 }
 

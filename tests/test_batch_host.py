@@ -62,7 +62,7 @@ def test_group_route_refuses(M, over):
     a = dict(logits=P, ld=8, dtype=2, T=1000, E=8, k=2, router=0, idx=P, weights=P, offsets=P, rows=P, pairs=P, ws=P,
              ws_bytes=1 << 30)
     a.update(over)
-    assert M.group_route_workspace(1000, 8, 2) > 0
+    assert M.group_route_workspace(2000, 8, 2) > 0
     assert M.lib().moe_group_route(*[a[n] for n in ("logits", "ld", "dtype", "T", "E", "k", "router", "idx", "weights", "offsets",
                                                     "rows", "pairs", "ws", "ws_bytes")], None) == M.EINVAL
 

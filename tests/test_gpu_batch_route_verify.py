@@ -32,7 +32,8 @@ def check_route(M, logits, k, kind, **kw):
 @pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("kind", [0, 1])
 @pytest.mark.parametrize("T,E,k", [(1, 256, 8), (1, 1, 1), (3, 8, 2), (4, 5, 5), (31, 33, 4), (257, 384, 16), (1000, 64, 6),
-                                   (33, 1024, 32), (5000, 17, 3), (700, 1000, 10), (64, 40, 32)])
+                                   (33, 1024, 32), (5000, 17, 3), (700, 1000, 10), (64, 40, 32), (65, 256, 8), (200, 96, 10),
+                                   (512, 512, 4), (513, 40, 8), (256, 1000, 8), (1111, 256, 9)])
 def test_route(M, T, E, k, kind, dtype):
     import torch
     g = torch.Generator(device="cuda").manual_seed(T + E)
@@ -41,8 +42,9 @@ def test_route(M, T, E, k, kind, dtype):
 
 
 @pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("T,E,k", [(40, 64, 4), (1, 64, 4), (3000, 12, 6)])
-def test_route_ties_masks_and_extremes(M, T, E, k, kind):
+def test_route_ties_masks_and_extremes(M, T, E, k, kind, dtype):
     import torch
     rng = np.random.default_rng(T)
     l = rng.choice(np.array([0.0, -0.0, 1.0, -1.0, 2.0], np.float32), (T, E))          # ties everywhere
@@ -54,7 +56,7 @@ def test_route_ties_masks_and_extremes(M, T, E, k, kind):
     if T > 2:
         l[1] = np.finfo(np.float32).min
         l[2] = -2000.0                                                                   # every sigmoid underflows
-    check_route(M, torch.from_numpy(l).cuda(), k, kind)
+    check_route(M, torch.from_numpy(l).cuda().to(B.torch_type(dtype)), k, kind)
 
 
 @pytest.mark.parametrize("T,E,k", [(300, 64, 8), (300, 200, 9), (40, 1000, 12), (300, 300, 32), (300, 32, 32), (50, 33, 32)])
@@ -78,8 +80,8 @@ def test_route_everything_masked(M):
 def test_route_rows_apart_and_workspace(M):
     import torch
     g = torch.Generator(device="cuda").manual_seed(1)
-    big = torch.randn(300, 50, generator=g, device="cuda").bfloat16()
-    ws = torch.empty(M.group_route_workspace(300, 37, 4) + 64, dtype=torch.uint8, device="cuda")
+    big = torch.randn(1300, 50, generator=g, device="cuda").bfloat16()
+    ws = torch.empty(M.group_route_workspace(1300, 37, 4) + 64, dtype=torch.uint8, device="cuda")
     check_route(M, big[:, 3:40], 4, 0, workspace=ws)
     with pytest.raises(M.MoeError):
         M.group_route(big, 4, workspace=ws[:16])
