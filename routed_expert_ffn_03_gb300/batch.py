@@ -10,6 +10,7 @@ products take, so the checks are kept lean.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 from .moe import OK, ROUTER_SOFTMAX, MoeError, lib
@@ -72,18 +73,36 @@ def _lib():
 _torch = None
 _types = {}
 _raw_stream = None    # torch's current stream of a device as an address, without a Stream object (2 us less)
+_current = None       # the current device's index
 
 
 def _start():
     """(torch, the library)"""
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current
     if _torch is None:
         import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _types.update({torch.bfloat16: T_BF16, torch.float16: T_FP16, torch.float32: T_FP32})
         _torch = torch
     return _torch, _calls or _lib()
+
+
+# The workspaces' sizes depend on the numbers alone; remembered, as a call through ctypes takes 0.5 us.
+@functools.lru_cache(4096)
+def _route_space(T, E, k):
+    return _lib().moe_group_route_workspace(T, E, k)
+
+
+@functools.lru_cache(4096)
+def _matmul_space(m, k, groups):
+    return _lib().moe_grouped_workspace(m, k, groups)
+
+
+@functools.lru_cache(4096)
+def _wgrad_space(m, length):
+    return _lib().moe_grouped_wgrad_workspace(m, length)
 
 
 def _type(t, what, fp32=True):
@@ -152,11 +171,10 @@ def _run(what, call, index, stream, *args):
         stream = _raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    cuda = _torch.cuda
-    if index == cuda.current_device():
+    if index == _current():
         st = call(*args, stream)
     else:
-        with cuda.device(index):
+        with _torch.cuda.device(index):
             st = call(*args, stream)
     if st != OK:
         raise MoeError(st, what)
@@ -180,7 +198,7 @@ def group_route(logits, k, router=ROUTER_SOFTMAX, out=None, workspace=None, stre
             raise ValueError("k: at least 1, got %d" % k)
         out = tuple(_new(stream, dev, (TK, i32), (TK, torch.float32), ((E + 1,), i32), (P, i32), (P, i32)))
     idx, weights, offsets, rows, pairs = out
-    ws, ws_bytes, _held = _space(workspace, L.moe_group_route_workspace(T, E, k), stream, dev)
+    ws, ws_bytes, _held = _space(workspace, _route_space(T, E, k), stream, dev)
     _run("moe_group_route", L.moe_group_route, dev, stream, logits.data_ptr(), _pitch(stride[0], T, E), dt, T, E, k, router,
          _flat(idx, "out: idx", i32, TK, dev), _flat(weights, "out: weights", torch.float32, TK, dev),
          _flat(offsets, "out: offsets", i32, (E + 1,), dev), _flat(rows, "out: rows", i32, P, dev),
@@ -245,7 +263,7 @@ def grouped_matmul(x, w, offsets, rows=None, out_rows=None, w_layout="nk", act=N
     ws = ws_bytes = rows_at = 0
     if rows is not None:
         rows_at = _flat(rows, "rows", i32, (m,), dev)
-        ws, ws_bytes, _held = _space(workspace, 0 if workspace is not None else L.moe_grouped_workspace(m, k, E), stream, dev)
+        ws, ws_bytes, _held = _space(workspace, 0 if workspace is not None else _matmul_space(m, k, E), stream, dev)
     if m:
         a = _pack_matmul(
             x.data_ptr(), w.data_ptr(), _flat(offsets, "offsets", i32, (E + 1,), dev), rows_at,
@@ -283,10 +301,10 @@ def grouped_wgrad(dy, x, offsets, dy_rows=None, x_rows=None, out=None, out_dtype
     dy_at = x_at = need = 0
     if dy_rows is not None:
         dy_at = _flat(dy_rows, "dy_rows", i32, (m,), dev)
-        need = L.moe_grouped_wgrad_workspace(m, n)
+        need = _wgrad_space(m, n)
     if x_rows is not None:
         x_at = _flat(x_rows, "x_rows", i32, (m,), dev)
-        need += L.moe_grouped_wgrad_workspace(m, k)
+        need += _wgrad_space(m, k)
     ws, ws_bytes, _held = _space(workspace, need, stream, dev) if need else (0, 0, None)
     a = _pack_wgrad(
         dy.data_ptr(), x.data_ptr(), _flat(offsets, "offsets", i32, (E + 1,), dev), dy_at, x_at, out.data_ptr(), R,
