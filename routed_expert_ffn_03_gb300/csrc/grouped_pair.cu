@@ -42,7 +42,7 @@ constexpr int GP_STAGES = 6;
 constexpr int GP_OP = 128 * 128;                 // bytes of one factor's half stage: 128 rows x 64 elements
 constexpr int GP_STAGE = 2 * GP_OP;
 constexpr int GP_EPI_WARPS = 8;
-constexpr int GP_CLEAR_WARP = 2 + GP_EPI_WARPS;
+constexpr int GP_CLEAR_WARP = 2 + GP_EPI_WARPS, GP_ROW_WARP = GP_CLEAR_WARP;   // weight gradient; forward
 constexpr int GP_THREADS = (GP_CLEAR_WARP + 1) * 32;
 constexpr int GP_MAX_GROUPS = 1024;
 // The tensor core's running sum drops bits at every step (K = 16) instead of rounding, which costs about
@@ -226,56 +226,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   const int pair = blockIdx.x >> 1, npair = gridDim.x >> 1;
   const uint32_t s0 = smem_u32(smem);
 
-  if (warp == 0) {
+  if (warp == 0 || (!WG && warp == GP_ROW_WARP)) {
     // ---------------------------------------------------------------- copies
-    const uint32_t pair_full0 = map_rank(full0, 0);
+    // As with the products below, the warp walks the loop together and one elected thread issues.  Forward: warp 0 the weights,
+    // warp 10 the rows.
+    const bool leader = elect_one(), weights = warp == 0;
+    const uint32_t pair_full0 = __shfl_sync(0xffffffffu, map_rank(full0, 0), 0), base = __shfl_sync(0xffffffffu, s0, 0);
+    const int side = __shfl_sync(0xffffffffu, (int)rank, 0);
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
     for (int t = pair; t < total && ok; t += npair) {
       const Tile T = decode<MODE>(a, first, t);
-      const int half = T.n / 2;                            // rows of the second factor in each block
-      for (int kb = 0; kb < T.nkb; ++kb) {
+      const int nkb = __shfl_sync(0xffffffffu, T.nkb, 0), half = __shfl_sync(0xffffffffu, T.n, 0) / 2;   // rows of B in each block
+      const int e = __shfl_sync(0xffffffffu, T.e, 0), r0 = __shfl_sync(0xffffffffu, T.r0, 0);
+      const int f0 = __shfl_sync(0xffffffffu, T.f0, 0), c0 = __shfl_sync(0xffffffffu, T.c0, 0);
+      const int f = f0 + side * (SW ? 64 : 128), fb = c0 + side * 128, rb = r0 + side * half;
+      const uint32_t bytes = GP_OP + (WG ? GP_OP : half * 128);   // of a step, in each block
+      for (int kb = 0; kb < nkb; ++kb) {
         ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1));
         if (!ok) break;
-        const uint32_t bytes = GP_OP + (WG ? GP_OP : half * 128);   // in each block
         // a step whose rows behind the group are to be cleared is announced to the block's own warp 10
         const bool clear = clears(T, kb);
         const uint32_t bar = (clear ? land0 : pair_full0) + 8 * s;
-        if (lane == 0) {
-          if (clear) mbar_arrive_expect_tx(bar, bytes);
-          if (rank == 0) {
-            if (clear) mbar_arrive(full0 + 8 * s);
-            else mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
+        const uint32_t da = base + s * GP_STAGE, db = da + GP_OP;
+        if (leader) {
+          if (weights) {
+            if (clear) mbar_arrive_expect_tx(bar, bytes);
+            if (side == 0) {
+              if (clear) mbar_arrive(full0 + 8 * s);
+              else mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
+            }
+          }
+          if (WG) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              tma_2d<2>(da + h * SLAB_BYTES, &maps.a, f + h * 64, r0 + kb * 64, bar);
+              tma_2d<2>(db + h * SLAB_BYTES, &maps.b[0], fb + h * 64, r0 + kb * 64, bar);
+            }
+          } else if (weights) {
+            if (MODE == GP_NK) tma_3d<2>(da, &maps.a, kb * 64, f, e, bar);
+            if (SW && !a.by_16) tma_5d<2>(da, &maps.a, kb * 64, 0, 0, f / 16, e, bar);
+            if (SW && a.by_16)   // gate and up in turn, 16 rows each
+              for (int i = 0; i < 8; ++i) tma_3d<2>(da + i * 2048, &maps.a, kb * 64, f + (i >> 1) * 16 + (i & 1) * (p.n / 2), e, bar);
+            if (MODE == GP_KN) {
+              tma_3d<2>(da, &maps.a, f, kb * 64, e, bar);
+              tma_3d<2>(da + SLAB_BYTES, &maps.a, f + 64, kb * 64, e, bar);
+            }
+          } else {
+            // the half's rows, a multiple of 16, in boxes of 128, 64, 32 and 16
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int box = 16 << i, before = half & ~(2 * box - 1);
+              if (half & box) tma_2d<2>(db + before * 128, &maps.b[i], kb * 64, rb + before, bar);
+            }
           }
         }
         __syncwarp();
-        const uint32_t da = s0 + s * GP_STAGE, db = da + GP_OP;
-        if (!WG) {
-          if (lane == 0) {
-            const int f = T.f0 + (int)rank * (SW ? 64 : 128);
-            if (MODE == GP_NK) tma_3d<2>(da, &maps.a, kb * 64, f, T.e, bar);
-            if (SW && !a.by_16) tma_5d<2>(da, &maps.a, kb * 64, 0, 0, f / 16, T.e, bar);
-            if (MODE == GP_KN) {
-              tma_3d<2>(da, &maps.a, f, kb * 64, T.e, bar);
-              tma_3d<2>(da + SLAB_BYTES, &maps.a, f + 64, kb * 64, T.e, bar);
-            }
-          }
-          if (SW && a.by_16 && lane < 8) {   // gate and up in turn, 16 rows each
-            const int f = T.f0 + (int)rank * 64 + (lane >> 1) * 16 + (lane & 1) * (p.n / 2);
-            tma_3d<2>(da + lane * 2048, &maps.a, kb * 64, f, T.e, bar);
-          }
-          // the half's rows, a multiple of 16, in boxes of 128, 64, 32 and 16: lane i those of bit i
-          const int box = 16 << lane;
-          if (lane < 4 && (half & box)) {
-            const int before = half & ~(2 * box - 1);
-            tma_2d<2>(db + before * 128, &maps.b[lane], kb * 64, T.r0 + (int)rank * half + before, bar);
-          }
-        } else if (lane < 2) {
-          const int fa = T.f0 + (int)rank * 128, fb = T.c0 + (int)rank * 128;
-          tma_2d<2>(da + lane * SLAB_BYTES, &maps.a, fa + lane * 64, T.r0 + kb * 64, bar);
-          tma_2d<2>(db + lane * SLAB_BYTES, &maps.b[0], fb + lane * 64, T.r0 + kb * 64, bar);
-        }
         if (++s == GP_STAGES) {
           s = 0;
           ph ^= 1;
