@@ -7,13 +7,13 @@
 // (M = 128, the rows as N: 16 columns cost next to nothing), and a cluster of C blocks shares the contracted dimension
 // of a tile, so that few tiles still make several blocks an SM.  Two blocks share an SM: one computes
 // its start (finding its group takes two memory round trips) while the other streams.  Warps:
-//   warp 0      copies W_e tiles and the rows by TMA into a ring (rows named by number: gather, 4 rows an
-//               instruction, cheap at 16 rows and not for many);
+//   warp 0      copies W_e tiles by TMA into a ring;
+//   warp 6      the rows (named by number: gather, 4 rows an instruction, cheap at 16 rows and not for many);
 //   warp 1      issues the products, in parts of 512 elements in alternating results;
 //   warps 2..5  add the parts up in fp32 registers (the tensor core's own running sum truncates at each step).
 // Then the cluster adds its blocks' sums in rank order through distributed shared memory (no workspace, no
 // atomics, the same bits every time) and each block stores its share.
-// DeepSeek-V3-shaped layer: gate/up of one token (470 MB) 73 us, 0.95 of the memory's rate; down of four tokens (0.9 GB)
+// DeepSeek-V3-shaped layer: gate/up of one token (470 MB) 74 us, 0.93 of the memory's rate; down of four tokens (0.9 GB)
 // 126 us (the pair kernel: 86 and 148).
 #include "grouped.h"
 #include "grouped_mma.cuh"
@@ -23,7 +23,8 @@ namespace moe {
 namespace {
 
 enum : int { GF_NK = 0, GF_KN = 1, GF_SWIGLU = 2 };
-constexpr int GF_THREADS = 192;
+constexpr int GF_ROW_WARP = 6;
+constexpr int GF_THREADS = (GF_ROW_WARP + 1) * 32;
 constexpr int GF_A = 128 * 128;       // bytes of a W_e tile: 128 features x 64 elements
 constexpr int GF_PART = 8;            // stages of a part
 
@@ -105,6 +106,36 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
 #pragma unroll
   for (int i = 0; i < NT; ++i) sum[i] = 0.f;
   if (work && warp == 0) {
+    // the warp walks the loop together and one elected thread issues: the operands sit in uniform registers
+    const bool leader = elect_one();
+    const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), bar0 = __shfl_sync(0xffffffffu, full0, 0);
+    const int ue = __shfl_sync(0xffffffffu, e, 0), uf = __shfl_sync(0xffffffffu, f0, 0), un = __shfl_sync(0xffffffffu, n, 0);
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1));
+      if (!ok) break;
+      const uint32_t bar = bar0 + 8 * s, da = base + s * STAGE;
+      if (leader) {
+        mbar_arrive_expect_tx(bar, GF_A + un * 128);
+        if (MODE == GF_NK) tma_3d<1>(da, &maps.a, kb * 64, uf, ue, bar);
+        if (SW && !a.by_16) tma_5d<1>(da, &maps.a, kb * 64, 0, 0, uf / 16, ue, bar);
+        if (SW && a.by_16)   // gate and up in turn, 16 rows each
+          for (int i = 0; i < 8; ++i) tma_3d<1>(da + i * 2048, &maps.a, kb * 64, uf + (i >> 1) * 16 + (i & 1) * (p.n / 2), ue, bar);
+        if (MODE == GF_KN) {
+          tma_3d<1>(da, &maps.a, uf, kb * 64, ue, bar);
+          tma_3d<1>(da + SLAB_BYTES, &maps.a, uf + 64, kb * 64, ue, bar);
+        }
+      }
+      __syncwarp();
+      if (++s == STAGES) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+    if (!ok && lane == 0) *s_abort = 1;
+  } else if (work && warp == GF_ROW_WARP) {
     int4 gr = make_int4(0, 0, 0, 0);
     if (p.a_rows && lane < n / 4) {   // lane i gathers rows 4 i .. 4 i + 3; a number outside x gives zeros
       int r[4];
@@ -122,26 +153,13 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
     for (int kb = kb0; kb < kb1; ++kb) {
       ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1));
       if (!ok) break;
-      const uint32_t bar = full0 + 8 * s, da = smem_u32(smem) + s * STAGE, db = da + GF_A;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar, GF_A + n * 128);
-        if (MODE == GF_NK) tma_3d<1>(da, &maps.a, kb * 64, f0, e, bar);
-        if (SW && !a.by_16) tma_5d<1>(da, &maps.a, kb * 64, 0, 0, f0 / 16, e, bar);
-        if (MODE == GF_KN) {
-          tma_3d<1>(da, &maps.a, f0, kb * 64, e, bar);
-          tma_3d<1>(da + SLAB_BYTES, &maps.a, f0 + 64, kb * 64, e, bar);
-        }
-      }
-      __syncwarp();
-      if (SW && a.by_16 && lane < 8) {   // gate and up in turn, 16 rows each
-        const int f = f0 + (lane >> 1) * 16 + (lane & 1) * (p.n / 2);
-        tma_3d<1>(da + lane * 2048, &maps.a, kb * 64, f, e, bar);
-      }
+      const uint32_t bar = full0 + 8 * s, db = smem_u32(smem) + s * STAGE + GF_A;
       if (p.a_rows) {
         if (lane < n / 4) tma_gather4(db + lane * 512, &maps.b[0], kb * 64, gr, bar);
       } else if (lane < n / 16) {
         tma_2d<1>(db + lane * 2048, &maps.b[0], kb * 64, r0 + lane * 16, bar);
       }
+      __syncwarp();
       if (++s == STAGES) {
         s = 0;
         ph ^= 1;
