@@ -109,22 +109,26 @@ int few_rows_tile(long long m, int groups) {
 }
 // And the blocks that share a tile's k: as many as bring 1.5 blocks an SM from the tiles that m rows spread evenly make,
 // 512 elements each at least.  Measured (down product, k = 14336, 64 tiles, cluster 1 / 2 / 4 / 8): 57 / 42 / 39 / 42 us;
-// 450 tiles of k = 2048: 40 / 45 / 53 / 82 us.
+// 450 tiles of k = 2048: 40 / 45 / 53 / 82 us.  Tiles full of rows gain less: one block an SM (192 tiles, k = 2048: 13 / 18 us).
 // It also takes products of which the pair kernel would keep a third of its pairs busy or fewer (4096 rows in 4 groups, n =
-// 128: k = 512 14 and 9 us, k = 4096 34 and 21 us; n = 512, k = 4096 36 and 71 us), and up to half
-// of them where a tile of 64 rows covers a group and k is long enough to share out (308 rows in 7 groups, n = 928,
-// k = 14280: 57 and 39 us; n = 1024, k = 1024: 9.2 and 10.4; at n = 2048, k = 4096, 64 tiles, 26 and 27).
+// 128: k = 512 14 and 9 us, k = 4096 34 and 21 us; n = 512, k = 4096 36 and 71 us), or whose tiles of 32 rows stand on the SMs
+// all at once, while k is not long (768 rows in 32 groups, n = 768, k = 512: 10.4 and 7.6 us; in 8 groups, k = 2048: 15.7 and
+// 12.7; 1536 in 32, n = 768: 12.0 and 12.7, 504 tiles), and up to half of the pairs where a tile of 64 rows covers a group
+// and k is long enough to share out (308 rows in 7 groups, n = 928, k = 14280: 57 and 39 us; n = 1024, k = 1024: 9.2 and 10.4;
+// at n = 2048, k = 4096, 64 tiles, 26 and 27).
 bool few_rows(const moe::GroupedProblem& p, int num_sms, int* nt, int* cluster) {
   *nt = few_rows_tile(p.m, p.groups);
   const int n_out = p.swiglu ? p.n / 2 : p.n, width = p.swiglu ? 128 : 256;
   const long long pair_tiles = (p.m / 256 + (p.m < p.groups ? p.m : p.groups)) * ((n_out + width - 1) / width);
-  if (!*nt && pair_tiles <= num_sms / 6) *nt = 32;
+  const double reached = p.groups * (1 - std::pow(1 - 1.0 / p.groups, (double)p.m));
+  auto tiles_of = [&](int rows) { return (reached + p.m / rows) * std::ceil(n_out / (width / 2.0)); };
+  if (!*nt && (pair_tiles <= num_sms / 6 || (p.k <= 2048 && tiles_of(32) <= 2 * num_sms))) *nt = 32;
   if (!*nt && pair_tiles <= num_sms / 4 && p.k >= 4096 && p.m <= 48ll * p.groups) *nt = 64;
   if (!*nt) return false;
-  const double reached = p.groups * (1 - std::pow(1 - 1.0 / p.groups, (double)p.m));
-  const double tiles = (reached + p.m / *nt) * ((p.swiglu ? p.n / 2 : p.n) / (p.swiglu ? 64.0 : 128.0));
+  const double tiles = tiles_of(*nt);
   *cluster = 1;
-  while (*cluster < 8 && tiles * *cluster < 1.5 * num_sms && p.k / (2 * *cluster) >= 512) *cluster *= 2;
+  const double most = (few_rows_tile(p.m, p.groups) ? 1.5 : 1.0) * num_sms;
+  while (*cluster < 8 && tiles * *cluster < most && p.k / (2 * *cluster) >= 512) *cluster *= 2;
   return true;
 }
 

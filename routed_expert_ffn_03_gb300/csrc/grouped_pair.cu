@@ -268,7 +268,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
             if (MODE == GP_NK) tma_3d<2>(da, &maps.a, kb * 64, f, e, bar);
             if (SW && !a.by_16) tma_5d<2>(da, &maps.a, kb * 64, 0, 0, f / 16, e, bar);
             if (SW && a.by_16)   // gate and up in turn, 16 rows each
-              for (int i = 0; i < 8; ++i) tma_3d<2>(da + i * 2048, &maps.a, kb * 64, f + (i >> 1) * 16 + (i & 1) * (p.n / 2), e, bar);
+              for (int i = 0; i < 8; ++i)
+                tma_3d<2>(da + i * 2048, &maps.a, kb * 64, f + (i >> 1) * 16 + (i & 1) * (p.n / 2), e, bar);
             if (MODE == GP_KN) {
               tma_3d<2>(da, &maps.a, f, kb * 64, e, bar);
               tma_3d<2>(da + SLAB_BYTES, &maps.a, f + 64, kb * 64, e, bar);
