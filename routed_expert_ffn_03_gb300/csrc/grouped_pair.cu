@@ -12,19 +12,22 @@
 // tensor cycles, where single blocks of 128 x 256 would take 48 KB.
 //
 // Persistent pairs walk the tiles; the warps of a block have fixed roles:
-//   warp 0      copies operands by TMA into a ring of 6 stages (64 contracted elements each);
+//   warp 0      copies operands by TMA into a ring of 6 stages (64 contracted elements each), in forward products the weights;
 //   warp 1      of the first block issues the products for both;
 //   warps 2..9  read finished results from tensor memory and store them, while the next
 //               tile's products run into the other half of the 512 columns;
-//   warp 10     where a weight gradient's group ends inside a step, clears the rows behind it in both
-//               factors, so that nothing of a neighbour enters a sum (zeros in one factor alone
-//               would let the other's NaN through).
-// Rows named by number are copied side by side by a kernel of their own first (memory bound; 2% of a
+//   warp 10     in forward products copies the rows.  Where a weight gradient's group ends inside a step, it clears the rows
+//               behind it in both factors, so that nothing of a neighbour enters a sum (zeros in one factor
+//               alone would let the other's NaN through).
+// Copies are issued by an elected thread of a warp that walks its loop together, and by two warps, as each instruction counts:
+// from a branch of single lanes of one warp the Mixtral-shaped gate/up product takes 440 us for 1001 tokens and 682 for 2048
+// instead of 385 and 587, the fp32 weight gradient 716 instead of 663.
+// Rows named by number are copied side by side by a kernel of their own first (memory bound; 1% of a
 // Mixtral-shaped gate/up product's time) and then come as tiles.  Measured against that, for the Mixtral-shaped down
 // product of 8192 tokens (1160 us from tiles): TMA gather 4014 us (~76 cycles an instruction of 4 rows), cp.async by
 // 4 warps into the same stages 1379 to 2072 us (its shared-memory writes wait behind the tensor core's reads).
-// 16384 rows over 8 groups, k = 14336, n = 4096: 513 cycles a step, the tensor core's own; 1070 us and 1800 TFLOP/s for a
-// call, 1250 us in a row of them, where the card's power limit holds the clock down.
+// 16384 rows over 8 groups, k = 14336, n = 4096: 513 cycles a step, the tensor core's own; 1100 us, 1750 TFLOP/s, and up to
+// 1250 in a long row of them, where the card's power limit holds the clock down.
 // Tiles of a group go rows first within bands of 8 row tiles, so the pairs at work share
 // weights and rows in L2.
 #include "grouped.h"
