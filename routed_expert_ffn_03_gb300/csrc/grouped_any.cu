@@ -9,8 +9,9 @@
 // numbers outside their tensor are stored as zeros.  Warps:
 //   warps 0..15  load (two steps ahead in registers) and store into a ring of 4 stages;
 //   warp 16      issues the products, in parts of 512 elements in alternating results;
-//   warps 17..20 add the parts up in fp32 registers, then store the tile by elements.
-// Bound: the loads' latency and the shared-memory stores of the staging: 133 TFLOP/s at 4096 rows, n = k = 4095, 8 groups (23
+//   warps 16..19 add the parts up in fp32 registers.
+// Then all warps store the tile by elements.
+// Bound: the loads' latency and the staging's instructions: 141 TFLOP/s at 4096 rows, n = k = 4095, 8 groups (23
 // with 64 x 64 tiles of the warp-level mma and element loads; 115 with 8 loading warps one step ahead).
 #include "grouped.h"
 #include "grouped_mma.cuh"
@@ -24,7 +25,7 @@ constexpr int GA_M = 128, GA_N = 64;             // tile: rows of the first fact
 constexpr int GA_A = GA_M * 128, GA_B = GA_N * 128, GA_STAGE = GA_A + GA_B;   // bytes of a stage: 64 elements a row
 constexpr int GA_STAGES = 4;
 constexpr int GA_COPY_WARPS = 16, GA_EPI_WARPS = 4;
-constexpr int GA_THREADS = (GA_COPY_WARPS + 1 + GA_EPI_WARPS) * 32;
+constexpr int GA_THREADS = (GA_COPY_WARPS + GA_EPI_WARPS) * 32;   // 20 warps have 96 registers a thread, 21 only 80
 // 16-byte words of the factors that a thread stages
 constexpr int GA_AW = GA_M * 8 / (GA_COPY_WARPS * 32), GA_BW = GA_N * 8 / (GA_COPY_WARPS * 32);
 constexpr int GA_PART = 8;                      // stages of a part
@@ -56,23 +57,25 @@ __device__ __forceinline__ uint4 load_if(bool live, uintptr_t at) {
       : "l"(at), "r"((uint32_t)live));
   return v;
 }
-// N words of one factor.  lo, hi: the tensor's first byte and the one behind its last.  Where all of the warp's words are whole
-// and both aligned words of each inside the tensor, the loads stand side by side without a branch.
-template <int N>
+// N words of one factor.  lo, hi: the tensor's first byte and the one behind its last.  Where both aligned words of each of
+// the warp's are inside the tensor, the loads stand side by side without a branch; else the words are read by elements.  PART:
+// finish8 clears what is not wanted of a word, so such words load in the same way (a warp of an MN-major tile at the
+// edge has one in every step; K-major ones meet them in the last step alone, and clearing costs the others 3%).
+template <bool PART, int N>
 __device__ __forceinline__ void load_words(const uint16_t* const (&s)[N], int left, uintptr_t lo, uintptr_t hi, Word8 (&w)[N]) {
   bool whole = true;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const uintptr_t at = (uintptr_t)s[i] & ~(uintptr_t)15;
-    whole = whole && (!s[i] || (left >= 8 && at >= lo && at + 32 <= hi));
+    whole = whole && (!s[i] || (PART && left <= 0) || ((PART || left >= 8) && at >= lo && at + 32 <= hi));
   }
   if (__all_sync(0xffffffffu, whole)) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const uintptr_t at = (uintptr_t)s[i] & ~(uintptr_t)15;
       w[i].shift = (int)((uintptr_t)s[i] & 15);
-      w[i].a = load_if(s[i] != nullptr, at);
-      w[i].b = load_if(s[i] != nullptr, at + 16);
+      w[i].a = load_if(s[i] != nullptr && (!PART || left > 0), at);
+      w[i].b = load_if(s[i] != nullptr && (!PART || left > 0), at + 16);
     }
   } else {
 #pragma unroll
@@ -83,7 +86,8 @@ __device__ __forceinline__ void load_words(const uint16_t* const (&s)[N], int le
     }
   }
 }
-__device__ __forceinline__ uint4 finish8(const Word8& w) {
+template <bool PART>
+__device__ __forceinline__ uint4 finish8(const Word8& w, int left) {
   const uint32_t v[8] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b.x, w.b.y, w.b.z, w.b.w};
   const int by = 8 * (w.shift & 3);
   const bool two = w.shift & 8, one = w.shift & 4;   // by halves: 8 bytes, then 4
@@ -94,6 +98,10 @@ __device__ __forceinline__ uint4 finish8(const Word8& w) {
   for (int i = 0; i < 5; ++i) y[i] = one ? x[i + 1] : x[i];
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = __funnelshift_r(y[i], y[i + 1], by);
+  if (PART && left < 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = left >= 2 * i + 2 ? r[i] : left > 2 * i ? r[i] & 0xffffu : 0u;
+  }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
@@ -195,6 +203,8 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
       const int r = rb + step_b * i;
       b_row[i] = !b_mn && r < rows ? row_at(p.a, p.a_rows, r0 + r, p.a_nrows, p.lda) : nullptr;
     }
+    auto left_a = [&](int kb) { return a_mn ? (WG ? p.k : n_out) - a0 - ca * 8 : kdim - kb * 64 - ca * 8; };
+    auto left_b = [&](int kb) { return b_mn ? p.n - b0 - cb * 8 : kdim - kb * 64 - cb * 8; };
     auto load = [&](int kb, Word8 (&va)[GA_AW], Word8 (&vb)[GA_BW]) {
       const uint16_t* s[GA_AW];
 #pragma unroll
@@ -208,7 +218,7 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
           s[i] = a_row[i] ? a_row[i] + kb * 64 + ca * 8 : nullptr;
         }
       }
-      load_words(s, a_mn ? (WG ? p.k : n_out) - a0 - ca * 8 : kdim - kb * 64 - ca * 8, a_lo, a_hi, va);
+      load_words<a_mn>(s, left_a(kb), a_lo, a_hi, va);
       const uint16_t* t[GA_BW];
 #pragma unroll
       for (int i = 0; i < GA_BW; ++i) {
@@ -220,7 +230,7 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
           t[i] = b_row[i] ? b_row[i] + kb * 64 + cb * 8 : nullptr;
         }
       }
-      load_words(t, b_mn ? p.n - b0 - cb * 8 : kdim - kb * 64 - cb * 8, b_lo, b_hi, vb);
+      load_words<b_mn>(t, left_b(kb), b_lo, b_hi, vb);
     };
     const uint32_t at_a = (a_mn ? (ca >> 3) * SLAB_BYTES : 0) + ra * 128 + (((ca & 7) ^ (ra & 7)) << 4);
     const uint32_t at_b = rb * 128 + ((cb ^ (rb & 7)) << 4);
@@ -233,9 +243,9 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
       if (!ok) return;
       uint8_t* st = smem + s * GA_STAGE;
 #pragma unroll
-      for (int i = 0; i < GA_AW; ++i) *reinterpret_cast<uint4*>(st + at_a + i * step_a * 128) = finish8(va[i]);
+      for (int i = 0; i < GA_AW; ++i) *reinterpret_cast<uint4*>(st + at_a + i * step_a * 128) = finish8<a_mn>(va[i], left_a(kb));
 #pragma unroll
-      for (int i = 0; i < GA_BW; ++i) *reinterpret_cast<uint4*>(st + GA_A + at_b + i * step_b * 128) = finish8(vb[i]);
+      for (int i = 0; i < GA_BW; ++i) *reinterpret_cast<uint4*>(st + GA_A + at_b + i * step_b * 128) = finish8<b_mn>(vb[i], left_b(kb));
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(full0 + 8 * s);
@@ -253,99 +263,85 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
       if (ok && kb + 1 < nkb) step(kb + 1, va1, vb1);
     }
     if (!ok && lane == 0) *s_abort = 1;
-  } else if (warp == GA_COPY_WARPS) {
-    // ---------------------------------------------------------------- products
-    const bool leader = elect_one();
-    constexpr uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
-    const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t da0 = sw128_desc(base, a_mn), db0 = sw128_desc(base + GA_A, b_mn);
-    const uint32_t idesc = idesc_16(p.dtype == GT_BF16, a_mn, b_mn, GA_M, __shfl_sync(0xffffffffu, cols, 0));
-    int s = 0, acc = 0;
-    uint32_t ph = 0, aph = 0;
-    bool ok = true;
-    for (int k0 = 0; k0 < nkb && ok; k0 += GA_PART) {
-      const int k1 = min(k0 + GA_PART, nkb);
-      ok = __all_sync(0xffffffffu, wait_bar(tempty0 + 8 * acc, aph ^ 1));
-      umma_fence_after();
-      for (int kb = k0; kb < k1 && ok; ++kb) {
-        ok = __all_sync(0xffffffffu, wait_bar(full0 + 8 * s, ph));
-        if (!ok) break;
-        umma_fence_after();
-        const uint32_t off = s * (GA_STAGE >> 4);
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma<1>(tm + acc * GA_N, da0 + off + kk * a_step, db0 + off + kk * b_step, idesc, kb > k0 || kk > 0);
-          umma_commit(empty0 + 8 * s);
-        }
-        __syncwarp();
-        if (++s == GA_STAGES) {
-          s = 0;
-          ph ^= 1;
-        }
-      }
-      if (!ok) break;
-      if (leader) umma_commit(tfull0 + 8 * acc);
-      __syncwarp();
-      if (++acc == 2) {
-        acc = 0;
-        aph ^= 1;
-      }
-    }
-    if (!ok && lane == 0) *s_abort = 1;
-  } else if (e >= 0) {
-    // ---------------------------------------------------------------- results
+  } else {
+    // ---------------------------------------------------------------- products and results
     const int quarter = warp & 3;   // of the TMEM lanes
     const uint32_t td = tmem + ((uint32_t)(quarter * 32) << 16);
     float sum[GA_N];
 #pragma unroll
     for (int i = 0; i < GA_N; ++i) sum[i] = 0.f;
-    int acc = 0;
-    uint32_t aph = 0;
+    int racc = 0;
+    uint32_t raph = 0;
     bool ok = true;
-    for (int k0 = 0; k0 < nkb; k0 += GA_PART) {
-      ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, aph));
-      if (!ok) break;
+    auto add_part = [&]() {
+      ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * racc, raph));
+      if (!ok) return;
       umma_fence_after();
 #pragma unroll
       for (int c = 0; c < GA_N; c += 16) {
         if (c < cols) {
           float v[16];
-          tmem_ld16(td + acc * GA_N + c, v);
+          tmem_ld16(td + racc * GA_N + c, v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) sum[c + i] += v[i];
         }
       }
       umma_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(tempty0 + 8 * acc);
-      if (++acc == 2) {
-        acc = 0;
-        aph ^= 1;
+      if (lane == 0) mbar_arrive(tempty0 + 8 * racc);
+      if (++racc == 2) {
+        racc = 0;
+        raph ^= 1;
       }
+    };
+    if (warp == GA_COPY_WARPS) {   // issues a part's products, then adds up the part before
+      const bool leader = elect_one();
+      constexpr uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+      const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t da0 = sw128_desc(base, a_mn), db0 = sw128_desc(base + GA_A, b_mn);
+      const uint32_t idesc = idesc_16(p.dtype == GT_BF16, a_mn, b_mn, GA_M, __shfl_sync(0xffffffffu, cols, 0));
+      int s = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      for (int k0 = 0; k0 < nkb && ok; k0 += GA_PART) {
+        const int k1 = min(k0 + GA_PART, nkb);
+        ok = __all_sync(0xffffffffu, wait_bar(tempty0 + 8 * acc, aph ^ 1));
+        umma_fence_after();
+        for (int kb = k0; kb < k1 && ok; ++kb) {
+          ok = __all_sync(0xffffffffu, wait_bar(full0 + 8 * s, ph));
+          if (!ok) break;
+          umma_fence_after();
+          const uint32_t off = s * (GA_STAGE >> 4);
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma<1>(tm + acc * GA_N, da0 + off + kk * a_step, db0 + off + kk * b_step, idesc, kb > k0 || kk > 0);
+            umma_commit(empty0 + 8 * s);
+          }
+          __syncwarp();
+          if (++s == GA_STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (leader) umma_commit(tfull0 + 8 * acc);
+        __syncwarp();
+        if (++acc == 2) {
+          acc = 0;
+          aph ^= 1;
+        }
+        if (k0 > 0) add_part();
+      }
+      if (ok && nkb > 0) add_part();
+    } else {
+      for (int k0 = 0; k0 < nkb && ok; k0 += GA_PART) add_part();
     }
     if (!ok && lane == 0) *s_abort = 1;
-    if (ok && WG) {
-      const int k = a0 + quarter * 32 + lane;
-      const long long at = (long long)e * p.d_stride + (long long)b0 * p.ldd + k;
+    // the sums, [column][feature], over the stages: all products have ended
+    float* part = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
 #pragma unroll
-      for (int i = 0; i < GA_N; ++i)
-        if (k < p.k && b0 + i < p.n) store_out(p.d, at + i * p.ldd, sum[i], p.out_dtype);
-    } else if (ok) {
-      const int f = SW ? a0 + quarter * 16 + (lane & 15) : a0 + quarter * 32 + lane;
-#pragma unroll
-      for (int i = 0; i < GA_N; ++i) {
-        float v = sum[i];
-        if (SW) {   // lanes 0..15 hold gate, 16..31 up
-          const float u = __shfl_down_sync(0xffffffffu, v, 16);
-          v = __fdividef(v, 1.f + expf(-v)) * u;
-        }
-        if (i < rows && f < n_out && !(SW && lane >= 16)) {
-          const long long row = p.d_rows ? __ldg(p.d_rows + r0 + i) : r0 + i;
-          if (row >= 0 && row < p.d_nrows) store_out(p.d, row * p.ldd + f, v, p.out_dtype);
-        }
-      }
-    }
+    for (int i = 0; i < GA_N; ++i)
+      if (i < cols) part[i * GA_M] = sum[i];
   }
   umma_fence_before();
   __syncthreads();
@@ -355,6 +351,24 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
       __threadfence_system();
     }
     drain_time();
+  } else if (e >= 0) {
+    // stored by all warps in a short loop, neighbours along a row: unrolled over the columns in registers the code
+    // runs once a tile and is fetched that often (124 rows in 19 groups, 1699 columns with swiglu, k = 103: 46 and 23 us)
+    const float* part = reinterpret_cast<const float*>(smem);
+    constexpr int F = SW ? GA_M / 2 : GA_M;
+    const int columns = WG ? min(GA_N, p.n - b0) : rows, left = (WG ? p.k : n_out) - a0;
+    for (int i = tid; i < columns * F; i += GA_THREADS) {
+      const int c = i / F, f = i % F;
+      if (f >= left) continue;
+      if (WG) {
+        store_out(p.d, (long long)e * p.d_stride + (long long)(b0 + c) * p.ldd + a0 + f, part[c * GA_M + f], p.out_dtype);
+      } else {
+        const long long row = p.d_rows ? __ldg(p.d_rows + r0 + c) : r0 + c;
+        float v = part[c * GA_M + (SW ? (f >> 4) * 32 + (f & 15) : f)];
+        if (SW) v = __fdividef(v, 1.f + expf(-v)) * part[c * GA_M + (f >> 4) * 32 + (f & 15) + 16];
+        if (row >= 0 && row < p.d_nrows) store_out(p.d, row * p.ldd + a0 + f, v, p.out_dtype);
+      }
+    }
   }
   umma_fence_after();
   if (warp == GA_COPY_WARPS) tmem_dealloc<1>(tmem, 2 * GA_N);

@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(VerifyA
         u64 run = before;
         int hit = 0;   // the warp whose run holds it
         while (hit < VF_WARPS - 1 && run + part[hit] <= thr) run += part[hit++];
-        const int h = rank * VF_WARPS + hit, h0 = (int)((long long)row.words * h / W), h1 = (int)((long long)row.words * (h + 1) / W);
+        const int h = rank * VF_WARPS + hit;
+        const int h0 = (int)((long long)row.words * h / W), h1 = (int)((long long)row.words * (h + 1) / W);
         int v = -1;
         if (h == 0) v = row.step(false, 0, row.head, thr, run, lane);
         if (v < 0) {
