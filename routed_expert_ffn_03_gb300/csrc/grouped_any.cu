@@ -8,7 +8,7 @@
 // tensor's first or last byte: then it is read by elements.  Words behind the contracted length, rows of no group and row
 // numbers outside their tensor are stored as zeros.  Warps:
 //   warps 0..15  load (two steps ahead in registers) and store into a ring of 4 stages;
-//   warp 16      issues the products, in parts of 512 elements in alternating results;
+//   warp 16      issues the products, in parts of 256 elements in alternating results;
 //   warps 16..19 add the parts up in fp32 registers.
 // Then all warps store the tile by elements.
 // Bound: the loads' latency and the staging's instructions: 141 TFLOP/s at 4096 rows, n = k = 4095, 8 groups (23
@@ -28,7 +28,7 @@ constexpr int GA_COPY_WARPS = 16, GA_EPI_WARPS = 4;
 constexpr int GA_THREADS = (GA_COPY_WARPS + GA_EPI_WARPS) * 32;   // 20 warps have 96 registers a thread, 21 only 80
 // 16-byte words of the factors that a thread stages
 constexpr int GA_AW = GA_M * 8 / (GA_COPY_WARPS * 32), GA_BW = GA_N * 8 / (GA_COPY_WARPS * 32);
-constexpr int GA_PART = 8;                      // stages of a part
+constexpr int GA_PART = 4;                      // stages of a part
 constexpr int GA_SMEM = GA_STAGES * GA_STAGE + 256 + 1024;
 
 struct AnyArgs {

@@ -9,7 +9,7 @@
 // its start (finding its group takes two memory round trips) while the other streams.  Warps:
 //   warp 0      copies W_e tiles by TMA into a ring;
 //   warp 6      the rows (named by number: gather, 4 rows an instruction, cheap at 16 rows and not for many);
-//   warp 1      issues the products, in parts of 512 elements in alternating results;
+//   warp 1      issues the products, in parts of 256 elements in alternating results;
 //   warps 2..5  add the parts up in fp32 registers (the tensor core's own running sum truncates at each step).
 // Then the cluster adds its blocks' sums in rank order through distributed shared memory (no workspace, no
 // atomics, the same bits every time) and each block stores its share.
@@ -26,7 +26,7 @@ enum : int { GF_NK = 0, GF_KN = 1, GF_SWIGLU = 2 };
 constexpr int GF_ROW_WARP = 6;
 constexpr int GF_THREADS = (GF_ROW_WARP + 1) * 32;
 constexpr int GF_A = 128 * 128;       // bytes of a W_e tile: 128 features x 64 elements
-constexpr int GF_PART = 8;            // stages of a part
+constexpr int GF_PART = 4;            // stages of a part (8 are no faster)
 
 constexpr int gf_stages(int nt) { return nt == 16 ? 6 : nt == 32 ? 5 : 4; }   // two blocks an SM
 constexpr int gf_stage_bytes(int nt) { return GF_A + nt * 128; }

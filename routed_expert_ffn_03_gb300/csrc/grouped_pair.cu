@@ -51,8 +51,11 @@ constexpr int GP_MAX_GROUPS = 1024;
 // The tensor core's running sum drops bits at every step (K = 16) instead of rounding, which costs about
 // 2e-8 of the result a step: nothing in a 16-bit result, but 1.3e-6 after 1024 elements, where fp32 sums rounded
 // at every step are off by 3e-7.  fp32 results are therefore summed in parts of 8 stages (512 elements), which
-// the storing warps add up in registers, rounding to nearest, while the next part's products run.
-constexpr int GP_PART = 8;
+// the storing warps add up in registers, rounding to nearest, while the next part's products run: 4 to 6e-7.  With swiglu the
+// errors of gate and up add up, and parts are 4 stages: 6.9e-7 instead of 1.3e-6, for 7% more time (415 and 445 us for
+// 1001 Mixtral-shaped tokens; in a weight gradient 4 stages would cost 8%).
+template <int MODE>
+constexpr int GP_PART = MODE == GP_SWIGLU ? 4 : 8;
 constexpr int GP_BAND = 8;                       // row tiles of a band
 constexpr int GP_OUT = 4096;                     // a warp's box of results: 32 rows of 128 bytes
 constexpr int GP_OFF_OUT = GP_STAGES * GP_STAGE;      // weight gradient
@@ -324,8 +327,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         const int last_rows = __shfl_sync(0xffffffffu, T.rows, 0) - (nkb - 1) * 64;
         const uint32_t idesc = idesc0 | ((uint32_t)(n >> 3) << 17);
         if (t + npair < total) T = decode<MODE>(a, first, t + npair);   // while this tile's products are queued
-        for (int kb0 = 0; kb0 < nkb && ok; kb0 += F32 ? GP_PART : nkb) {
-          const int kb1 = F32 ? min(kb0 + GP_PART, nkb) : nkb;
+        for (int kb0 = 0; kb0 < nkb && ok; kb0 += F32 ? GP_PART<MODE> : nkb) {
+          const int kb1 = F32 ? min(kb0 + GP_PART<MODE>, nkb) : nkb;
           ok = __all_sync(0xffffffffu, wait_bar(tempty0 + 8 * acc, aph ^ 1));
           umma_fence_after();
           const uint32_t dst = tm + acc * 256;
@@ -417,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         for (int q = 0; q < (F32 ? 4 : 1); ++q)
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[q][i] = 0.f;
-        for (int kb = 0; kb < T.nkb && ok; kb += GP_PART) {
+        for (int kb = 0; kb < T.nkb && ok; kb += GP_PART<MODE>) {
           ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, aph));
           if (!ok) break;
           umma_fence_after();

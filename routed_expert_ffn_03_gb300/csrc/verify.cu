@@ -508,7 +508,8 @@ cudaError_t verify_set_attributes() {
 cudaError_t launch_verify(const VerifyArgs& a, int num_sms, cudaStream_t s) {
   // Blocks to a sequence: 8, while that makes no more than two blocks an SM, or leaves each 60000 bytes of p: small shares
   // have more waits (drafts, sums, scan, search) to an element, large ones end less evenly.  In 1 / 2 / 4 / 8 blocks each,
-  // us: 64 sequences of 129281 in bf16 21 / 14 / 12.1 / 12.3; 256 35 / 36 / 33 / 37; 512 65 / 54 / 54 / 66; 256 of 32000 10.4 / 12.0 / 14.9 / 21.2.
+  // us: 64 sequences of 129281 in bf16 21 / 14 / 12.1 / 12.3; 256 35 / 36 / 33 / 37; 512 65 / 54 / 54 / 66; 256 of 32000
+  // 10.4 / 12.0 / 14.9 / 21.2.
   const int el = a.dtype == GT_FP32 ? 4 : 2;
   int S = VF_MAX_CLUSTER;
   while (S > 1 && (a.V < 1024 * S || ((long long)a.B * S > 2 * num_sms && (long long)a.V * el < 60000ll * S))) S /= 2;
