@@ -305,6 +305,42 @@ def test_gradients_against_differences(M):
         assert abs((f(xd, wd + d) - f(xd, wd - d)) / (2 * h) - dw[i]) < B.sum_bound(3, 3 * 16.0) + 1e-9
 
 
+@pytest.mark.parametrize("T,n,k", [(700, 264, 1024), (9, 264, 1024), (300, 263, 77)])
+def test_calls_in_a_row_give_what_calls_apart_give(M, T, n, k):
+    """Routing, gathered products, their gradients and a workspace used again, launched without a pause and captured:
+    each launch may start before the one in front has ended, and must not read early."""
+    import torch
+    E, top = 12, 3
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, k, generator=gen, device="cuda").bfloat16()
+    w = (torch.randn(E, n, k, generator=gen, device="cuda") * k ** -0.5).bfloat16()
+    logits = torch.randn(8, T, E, generator=gen, device="cuda")
+    ws = torch.empty(max(16, M.grouped_workspace(T * top, k, E), M.grouped_wgrad_workspace(T * top, k)), dtype=torch.uint8, device="cuda")
+
+    def chain(l, pause):
+        idx, _, off, rows, pairs = M.group_route(l, top)
+        pause()
+        y = M.grouped_matmul(x, w, off, rows=rows, workspace=ws)
+        pause()
+        dw = M.grouped_wgrad(y, x, off, x_rows=rows, workspace=ws)
+        pause()
+        dx = M.grouped_matmul(y, w, off, w_layout="kn", out_rows=pairs, out=torch.zeros(T * top, k, dtype=x.dtype, device="cuda"))
+        pause()
+        return idx, off, rows, y, dw, dx
+
+    apart = [chain(l, torch.cuda.synchronize) for l in logits]
+    run = [chain(l, lambda: None) for l in logits]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = [chain(l, lambda: None) for l in logits]
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b, c in zip(apart, run, captured):
+        for p, q, r in zip(a, b, c):
+            assert torch.equal(p, q) and torch.equal(p, r)
+
+
 def test_other_stream_capture_and_two_at_once(M):
     """A call on a side stream, a captured call replayed on new data, and calls on two streams at once."""
     import torch
