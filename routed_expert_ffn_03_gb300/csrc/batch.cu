@@ -101,8 +101,8 @@ bool product_ok(int groups, long long m, int n, int k, int dtype, int out_dtype)
 
 // Whether the kernel for few rows a group takes a forward product, by the mean over the groups that m rows can reach, as
 // the groups' sizes are not known here: tiles of nt rows, four times the mean, so that uneven groups fit too.  Measured
-// (DeepSeek-V3- and Mixtral-shaped layers, us for nt 16 / 32 / 64 / the pair kernel): mean 1: 75 / 74 / 75 / 83; mean 8:
-// 2038 / 2016 / 2054 / 2144; mean 16: 386 / 284 / 274 / 281; mean 32: 610 / 410 / 310 / 285.
+// (DeepSeek-V3- and Mixtral-shaped layers, us for nt 16 / 32 / 64 / the pair kernel): mean 1: 73 / 73 / 75 / 79; mean 8:
+// 2102 / 2076 / 2096 / 2189; mean 16: 390 / 284 / 275 / 281; mean 24: 499 / 319 / 278 / 282; mean 32: 622 / 417 / 308 / 284.
 int few_rows_tile(long long m, int groups) {
   const long long reach = m < groups ? m : groups;
   return m < 1 ? 0 : m <= 4 * reach ? 16 : m <= 8 * reach ? 32 : m <= 16 * reach ? 64 : 0;

@@ -14,7 +14,7 @@
 // Then the cluster adds its blocks' sums in rank order through distributed shared memory (no workspace, no
 // atomics, the same bits every time) and each block stores its share.
 // DeepSeek-V3-shaped layer: gate/up of one token (470 MB) 74 us, 0.93 of the memory's rate; down of four tokens (0.9 GB)
-// 126 us (the pair kernel: 86 and 148).
+// 129 us (the pair kernel: 79 and 138).
 #include "grouped.h"
 #include "grouped_mma.cuh"
 
