@@ -312,7 +312,11 @@ size_t moe_group_route_workspace(int T, int E, int k);
  * Rows named by `rows` are copied side by side into the workspace first, as the fast kernel for many rows takes
  * them; with a workspace that is NULL or too small a slower kernel reads them where they are.  Calls that can overlap,
  * replays of graphs among them, need a workspace each.
- * Sums are fp32, rounded once at the store. */
+ * Sums are fp32, rounded once to the result's type at the store.  The tensor core adds 16 products at a time to its
+ * running sum and cuts the result off where fp32 would round it (about 2e-8 of it), so it runs over a part of the contracted
+ * dimension only, and the parts are added with rounding to nearest: parts of 512 elements or fewer for fp32 results, of
+ * 16384 or fewer for 16-bit ones.  So an element is off by 1e-6 (fp32) or 2e-5 (16 bits) of the sum of its products'
+ * absolute values before it is rounded to its type, whatever the length. */
 typedef struct {
     const void* x;
     const void* w;
@@ -340,7 +344,7 @@ size_t moe_grouped_workspace(long long m, int k, int groups);
  *   dy [dy_rows_n][n] and x [x_rows_n][k] bf16 or fp16, rows lddy and ldx apart; row i reads
  *   dy row dy_rows[i] and x row x_rows[i], or row i where that is NULL;
  *   dw [groups] matrices [n][k] bf16, fp16 or fp32, dw_stride elements apart, rows lddw apart.
- * Offsets, row numbers, limits and alignment as moe_grouped_matmul; with m = 0 (dy and x may be
+ * Offsets, row numbers, limits, alignment and sums as moe_grouped_matmul; with m = 0 (dy and x may be
  * NULL then) dw is all zeros. */
 typedef struct {
     const void* dy;

@@ -48,14 +48,19 @@ constexpr int GP_EPI_WARPS = 8;
 constexpr int GP_CLEAR_WARP = 2 + GP_EPI_WARPS, GP_ROW_WARP = GP_CLEAR_WARP;   // weight gradient; forward
 constexpr int GP_THREADS = (GP_CLEAR_WARP + 1) * 32;
 constexpr int GP_MAX_GROUPS = 1024;
-// The tensor core's running sum drops bits at every step (K = 16) instead of rounding, which costs about
-// 2e-8 of the result a step: nothing in a 16-bit result, but 1.3e-6 after 1024 elements, where fp32 sums rounded
+// The tensor core's running sum drops bits at every step (K = 16) instead of rounding, always towards zero, which costs about
+// 2e-8 of the result a step: 1.3e-6 after 1024 elements, where fp32 sums rounded
 // at every step are off by 3e-7.  fp32 results are therefore summed in parts of 8 stages (512 elements), which
 // the storing warps add up in registers, rounding to nearest, while the next part's products run: 4 to 6e-7.  With swiglu the
 // errors of gate and up add up, and parts are 4 stages: 6.9e-7 instead of 1.3e-6, for 7% more time (415 and 445 us for
 // 1001 Mixtral-shaped tokens; in a weight gradient 4 stages would cost 8%).
+// 16-bit results are summed in one go up to GP_LONG stages (16384 elements: 2e-5, a 24th of an fp16 half step) and in
+// parts beyond, where the error would go on growing: an fp16 half step at 400 thousand elements.  Parts cost a forward product
+// 3% there (4096 rows in 4 groups, n = 4096, k = 16448: 326 and 338 us; with swiglu 6%), a weight gradient 1%.
 template <int MODE>
 constexpr int GP_PART = MODE == GP_SWIGLU ? 4 : 8;
+constexpr int GP_LONG = 256;
+enum : int { GP_OUT_16 = 0, GP_OUT_16_LONG = 1, GP_OUT_32 = 2 };   // results, and whether contractions past GP_LONG may come
 constexpr int GP_BAND = 8;                       // row tiles of a band
 constexpr int GP_OUT = 4096;                     // a warp's box of results: 32 rows of 128 bytes
 constexpr int GP_OFF_OUT = GP_STAGES * GP_STAGE;      // weight gradient
@@ -147,7 +152,7 @@ __device__ __forceinline__ Tile decode(const PairArgs& a, const int* first, int 
   return T;
 }
 
-template <int MODE, bool F32>
+template <int MODE, int OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
     grouped_pair_kernel(const __grid_constant__ PairArgs a, const __grid_constant__ GroupedMaps maps) {
   extern __shared__ uint8_t smem_raw[];
@@ -155,7 +160,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const GroupedProblem& p = a.p;
-  constexpr bool WG = MODE == GP_WGRAD, SW = MODE == GP_SWIGLU;
+  constexpr bool WG = MODE == GP_WGRAD, SW = MODE == GP_SWIGLU, F32 = OUT == GP_OUT_32;
+  constexpr bool PARTS = OUT != GP_OUT_16;   // sums in registers
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + GP_OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + GP_OFF_BAR + GP_BARS * 8);
@@ -227,6 +233,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   cluster_sync_all();   // barriers of both blocks exist before either signals the other
   umma_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // steps of a part of a tile's sum
+  auto part_steps = [](int nkb) { return F32 || (PARTS && nkb > GP_LONG) ? GP_PART<MODE> : max(nkb, 1); };
   // whether the group ends inside step kb
   auto clears = [&](const Tile& T, int kb) { return WG && T.rows - kb * 64 < 64; };
   const int pair = blockIdx.x >> 1, npair = gridDim.x >> 1;
@@ -327,8 +335,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         const int last_rows = __shfl_sync(0xffffffffu, T.rows, 0) - (nkb - 1) * 64;
         const uint32_t idesc = idesc0 | ((uint32_t)(n >> 3) << 17);
         if (t + npair < total) T = decode<MODE>(a, first, t + npair);   // while this tile's products are queued
-        for (int kb0 = 0; kb0 < nkb && ok; kb0 += F32 ? GP_PART<MODE> : nkb) {
-          const int kb1 = F32 ? min(kb0 + GP_PART<MODE>, nkb) : nkb;
+        const int steps = part_steps(nkb);
+        for (int kb0 = 0; kb0 < nkb && ok; kb0 += steps) {
+          const int kb1 = min(kb0 + steps, nkb);
           ok = __all_sync(0xffffffffu, wait_bar(tempty0 + 8 * acc, aph ^ 1));
           umma_fence_after();
           const uint32_t dst = tm + acc * 256;
@@ -412,21 +421,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
     for (int t = pair; t < total; t += npair) {
       const Tile T = decode<MODE>(a, first, t);
       if (T.nkb == 0 && !WG) continue;
-      // column c of this warp's q-th run of 32: its runs alternate with the other warp's of the same lanes
-      float sum[F32 ? 4 : 1][32];
+      // this warp's q-th run of 32 columns: its runs alternate with the other warp's of the same lanes, by twos where a
+      // box of 16-bit results is made of two
+      auto run_at = [&](int q) { return WG && PARTS && !F32 ? (q >> 1) * 128 + part * 64 + (q & 1) * 32 : part * 32 + 64 * q; };
+      float sum[PARTS ? 4 : 1][32];
       uint32_t td = 0;
-      if (F32) {
+      if (PARTS) {
 #pragma unroll
-        for (int q = 0; q < (F32 ? 4 : 1); ++q)
+        for (int q = 0; q < (PARTS ? 4 : 1); ++q)
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[q][i] = 0.f;
-        for (int kb = 0; kb < T.nkb && ok; kb += GP_PART<MODE>) {
+        for (int kb = 0; kb < T.nkb && ok; kb += part_steps(T.nkb)) {
           ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, aph));
           if (!ok) break;
           umma_fence_after();
 #pragma unroll
-          for (int q = 0; q < (F32 ? 4 : 1); ++q) {
-            const int c = part * 32 + 64 * q;
+          for (int q = 0; q < (PARTS ? 4 : 1); ++q) {
+            const int c = run_at(q);
             if (c < T.n) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {   // by 16: the sums fill the registers
@@ -470,7 +481,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float v[32];
-              if (T.nkb > 0) {
+              if (PARTS) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = sum[PARTS ? 2 * q + h : 0][i];
+              } else if (T.nkb > 0) {
                 tmem_ld32(td + c + 32 * h, v);
               } else {
 #pragma unroll
@@ -490,12 +504,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
       } else
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int c = part * 32 + 64 * q;
+        const int c = run_at(q);
         if (c >= T.n) break;
         float v[32];
-        if (F32) {
+        if (PARTS) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = sum[F32 ? q : 0][i];
+          for (int i = 0; i < 32; ++i) v[i] = sum[PARTS ? q : 0][i];
         } else if (WG && T.nkb == 0) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -571,7 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
           }
         }
       }
-      if (!F32 && T.nkb > 0) release();
+      if (!PARTS && T.nkb > 0) release();
     }
     if (WG && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok && lane == 0) *s_abort = 1;
@@ -590,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   if (warp == 1) tmem_dealloc<2>(tmem, 512);
 }
 
-template <int MODE, bool F32>
+template <int MODE, int OUT>
 cudaError_t launch_as(const PairArgs& a, const GroupedMaps& m, unsigned pairs, cudaStream_t s) {
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(2 * pairs);
@@ -602,19 +616,26 @@ cudaError_t launch_as(const PairArgs& a, const GroupedMaps& m, unsigned pairs, c
   at[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, grouped_pair_kernel<MODE, F32>, a, m);
+  return cudaLaunchKernelEx(&c, grouped_pair_kernel<MODE, OUT>, a, m);
 }
 
 template <int MODE>
 cudaError_t launch_mode(const PairArgs& a, const GroupedMaps& m, unsigned pairs, cudaStream_t s) {
-  return a.p.out_dtype == GT_FP32 ? launch_as<MODE, true>(a, m, pairs, s) : launch_as<MODE, false>(a, m, pairs, s);
+  if (a.p.out_dtype == GT_FP32) return launch_as<MODE, GP_OUT_32>(a, m, pairs, s);
+  // (of a weight gradient the longest that a group can be: shorter ones are summed in one go there too)
+  const long long longest = MODE == GP_WGRAD ? a.p.m : a.p.k;
+  return longest > GP_LONG * 64 ? launch_as<MODE, GP_OUT_16_LONG>(a, m, pairs, s) : launch_as<MODE, GP_OUT_16>(a, m, pairs, s);
 }
 
+template <int MODE, int OUT>
+cudaError_t set_attribute() {
+  return cudaFuncSetAttribute(grouped_pair_kernel<MODE, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
+}
 template <int MODE>
 cudaError_t set_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(grouped_pair_kernel<MODE, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(grouped_pair_kernel<MODE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
+  cudaError_t e = set_attribute<MODE, GP_OUT_16>();
+  if (e == cudaSuccess) e = set_attribute<MODE, GP_OUT_16_LONG>();
+  return e == cudaSuccess ? set_attribute<MODE, GP_OUT_32>() : e;
 }
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
