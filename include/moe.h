@@ -315,8 +315,8 @@ size_t moe_group_route_workspace(int T, int E, int k);
  * Sums are fp32, rounded once to the result's type at the store.  The tensor core adds 16 products at a time to its
  * running sum and cuts the result off where fp32 would round it (about 2e-8 of it), so it runs over a part of the contracted
  * dimension only, and the parts are added with rounding to nearest: parts of 512 elements or fewer for fp32 results, of
- * 16384 or fewer for 16-bit ones.  So an element is off by 1e-6 (fp32) or 2e-5 (16 bits) of the sum of its products'
- * absolute values before it is rounded to its type, whatever the length. */
+ * 16384 or fewer for 16-bit ones.  So a sum of up to a million products is off by about 1e-6 (fp32) or 2e-5 (16 bits) of the
+ * sum of their absolute values before it is rounded to its type. */
 typedef struct {
     const void* x;
     const void* w;
@@ -363,6 +363,13 @@ typedef struct {
 moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* stream);
 /* Bytes of workspace for m rows of length `len` named by number (the sum of both for dy_rows and x_rows). */
 size_t moe_grouped_wgrad_workspace(long long m, int len);
+
+/* Which kernel a product with these arguments takes on a device of num_sms SMs (host code, no device; addresses count by their
+ * alignment only): that for few rows a group, that for pairs of SMs, or the one for any stride and alignment.
+ * MOE_GROUPED_NONE where the call would launch nothing or be refused. */
+typedef enum { MOE_GROUPED_NONE = 0, MOE_GROUPED_FEW = 1, MOE_GROUPED_PAIR = 2, MOE_GROUPED_ANY = 3 } moe_grouped_kernel_id;
+int moe_grouped_kernel(const moe_grouped_args* a, int num_sms);
+int moe_grouped_wgrad_kernel(const moe_grouped_wgrad_args* a, int num_sms);
 
 /* Which of a sequence's drafted tokens stand, and the token after them, so that what comes
  * out is distributed as the target's own samples.  For sequence b with L = lengths[b] drafts

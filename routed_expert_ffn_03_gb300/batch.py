@@ -18,6 +18,7 @@ from .moe import OK, ROUTER_SOFTMAX, MoeError, lib
 T_BF16, T_FP16, T_FP32 = 0, 1, 2
 GROUP_NK, GROUP_KN = 0, 1
 ACT_NONE, ACT_SWIGLU = 0, 1
+GROUPED_NONE, GROUPED_FEW, GROUPED_PAIR, GROUPED_ANY = range(4)
 
 _vp, _i, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
 
@@ -64,6 +65,9 @@ def _lib():
             getattr(L, n).restype = ctypes.c_size_t
         for n in ("moe_grouped_matmul", "moe_grouped_wgrad", "moe_verify_draft"):
             getattr(L, n).argtypes = [_vp, _vp]
+        for n in ("moe_grouped_kernel", "moe_grouped_wgrad_kernel"):
+            getattr(L, n).argtypes = [_vp, _i]
+            getattr(L, n).restype = _i
         for n in ("moe_group_route", "moe_grouped_matmul", "moe_grouped_wgrad", "moe_verify_draft"):
             getattr(L, n).restype = _i
         _calls = L
@@ -219,6 +223,13 @@ def grouped_workspace(m, k, groups):
 def grouped_wgrad_workspace(m, length):
     """Bytes of workspace that grouped_wgrad needs for m rows of that length named by number."""
     return int(_lib().moe_grouped_wgrad_workspace(m, length))
+
+
+def grouped_kernel(args, num_sms):
+    """The kernel (GROUPED_FEW, GROUPED_PAIR or GROUPED_ANY; GROUPED_NONE) that a call with these GroupedArgs or
+    GroupedWgradArgs takes on a device of that many SMs; host code, no device."""
+    call = _lib().moe_grouped_kernel if isinstance(args, GroupedArgs) else _lib().moe_grouped_wgrad_kernel
+    return call(ctypes.byref(args), num_sms)
 
 
 def grouped_matmul(x, w, offsets, rows=None, out_rows=None, w_layout="nk", act=None, out=None, out_dtype=None, stream=None,

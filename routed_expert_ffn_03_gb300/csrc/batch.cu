@@ -151,26 +151,36 @@ cudaError_t copy_operand(const Operand& o, const moe::GroupedProblem& p, uint16_
   return moe::launch_copy_rows(c, num_sms, s);
 }
 
-// The kernels of a product, by what the operands allow: TMA wants 16-byte aligned addresses and strides, and rows side
-// by side, so named rows are copied into the workspace first.
+// The kernel of a product.  TMA wants 16-byte aligned addresses and strides, and many rows side by side, so those named by
+// number are copied into the workspace first.
+struct Plan {
+  int kernel;              // moe_grouped_kernel_id
+  int nt, cluster;         // of the few-rows kernel
+  size_t need_a, need_b;   // bytes of the copies that the pair kernel takes
+};
+Plan plan_product(const moe::GroupedProblem& p, bool wgrad, int num_sms, size_t workspace_bytes) {
+  Plan pl{MOE_GROUPED_ANY, 0, 0, p.a_rows ? row_copy_bytes(p.m, wgrad ? p.n : p.k) : 0, p.b_rows ? row_copy_bytes(p.m, p.k) : 0};
+  if (!wgrad && few_rows(p, num_sms, &pl.nt, &pl.cluster) && moe::grouped_maps(p, false, true, nullptr))
+    pl.kernel = MOE_GROUPED_FEW;
+  // (the copies lie no worse than the operands)
+  else if (p.m > 0 && workspace_bytes >= pl.need_a + pl.need_b && moe::grouped_maps(p, wgrad, false, nullptr))
+    pl.kernel = MOE_GROUPED_PAIR;
+  return pl;
+}
+
 moe_status run_product(moe::GroupedProblem p, bool wgrad, void* workspace, size_t workspace_bytes, cudaStream_t s) {
   Device* d;
   const moe_status st = current_device(&d);
   if (st != MOE_OK) return st;
   const Operand a{&p.a, &p.a_rows, &p.a_nrows, &p.lda, wgrad ? p.n : p.k};
   const Operand b{&p.b, &p.b_rows, &p.b_nrows, &p.ldb, p.k};
-  const size_t need_a = p.a_rows ? row_copy_bytes(p.m, a.len) : 0, need_b = p.b_rows ? row_copy_bytes(p.m, b.len) : 0;
+  const Plan pl = plan_product(p, wgrad, d->num_sms, workspace_bytes);
   cudaError_t e = cudaSuccess;
-  int nt, cluster;
-  if (!wgrad && few_rows(p, d->num_sms, &nt, &cluster) &&
-      moe::launch_grouped_few(p, nt, cluster, d->status, s, &e))
-    return done(e);
-  // before copies are made for it: whether the pair kernel takes the product (the copies lie no worse than the operands)
-  moe::GroupedMaps maps;
-  if (p.m > 0 && workspace_bytes >= need_a + need_b && (need_a + need_b == 0 || moe::grouped_maps(p, wgrad, false, &maps))) {
+  if (pl.kernel == MOE_GROUPED_FEW && moe::launch_grouped_few(p, pl.nt, pl.cluster, d->status, s, &e)) return done(e);
+  if (pl.kernel == MOE_GROUPED_PAIR) {
     uint16_t* ws = static_cast<uint16_t*>(workspace);
-    if (need_a) e = copy_operand(a, p, ws, d->num_sms, s);
-    if (need_b && e == cudaSuccess) e = copy_operand(b, p, ws + need_a / 2, d->num_sms, s);
+    if (pl.need_a) e = copy_operand(a, p, ws, d->num_sms, s);
+    if (pl.need_b && e == cudaSuccess) e = copy_operand(b, p, ws + pl.need_a / 2, d->num_sms, s);
     if (e != cudaSuccess) return done(e);
     if (moe::launch_grouped_pair(p, wgrad, d->num_sms, d->status, s, &e)) return done(e);
   }
@@ -213,7 +223,10 @@ extern "C" size_t moe_grouped_wgrad_workspace(long long m, int len) {
   return m < 0 || m > kMaxRows || len < 1 || len > kMaxDim ? 0 : row_copy_bytes(m, len);
 }
 
-extern "C" moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream) {
+namespace {
+
+// the arguments checked, and as the kernels take them
+moe_status matmul_problem(const moe_grouped_args* a, moe::GroupedProblem* out) {
   if (!a || !a->x || !a->w || !a->offsets || !a->out) return MOE_EINVAL;
   if (!product_ok(a->groups, a->m, a->n, a->k, a->dtype, a->out_dtype)) return MOE_EINVAL;
   if (a->layout != MOE_GROUP_NK && a->layout != MOE_GROUP_KN) return MOE_EINVAL;
@@ -228,8 +241,8 @@ extern "C" moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream
       !aligned(a->rows, 4) || !aligned(a->out_rows, 4) || !aligned(a->workspace, 16) ||
       (!a->workspace && a->workspace_bytes))
     return MOE_EINVAL;
-  if (a->m == 0) return MOE_OK;
-  moe::GroupedProblem p{};
+  moe::GroupedProblem& p = *out;
+  p = {};
   p.a = static_cast<const uint16_t*>(a->x);
   p.b = static_cast<const uint16_t*>(a->w);
   p.d = a->out;
@@ -250,10 +263,10 @@ extern "C" moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream
   p.out_dtype = a->out_dtype;
   p.kn = kn;
   p.swiglu = sw;
-  return run_product(p, false, a->workspace, a->workspace_bytes, (cudaStream_t)stream);
+  return MOE_OK;
 }
 
-extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* stream) {
+moe_status wgrad_problem(const moe_grouped_wgrad_args* a, moe::GroupedProblem* out) {
   if (!a || !a->offsets || !a->dw || (a->m != 0 && (!a->dy || !a->x))) return MOE_EINVAL;
   if (!product_ok(a->groups, a->m, a->n, a->k, a->dtype, a->out_dtype)) return MOE_EINVAL;
   if (!rows_fit(a->dy_rows_n, a->lddy, a->n) || !rows_fit(a->x_rows_n, a->ldx, a->k) || !rows_fit(a->n, a->lddw, a->k) ||
@@ -264,7 +277,8 @@ extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* s
       !aligned(a->dy_rows, 4) || !aligned(a->x_rows, 4) || !aligned(a->workspace, 16) ||
       (!a->workspace && a->workspace_bytes))
     return MOE_EINVAL;
-  moe::GroupedProblem p{};
+  moe::GroupedProblem& p = *out;
+  p = {};
   p.a = static_cast<const uint16_t*>(a->dy);
   p.b = static_cast<const uint16_t*>(a->x);
   p.d = a->dw;
@@ -283,7 +297,35 @@ extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* s
   p.k = a->k;
   p.dtype = a->dtype;
   p.out_dtype = a->out_dtype;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream) {
+  moe::GroupedProblem p;
+  const moe_status st = matmul_problem(a, &p);
+  if (st != MOE_OK || p.m == 0) return st;
+  return run_product(p, false, a->workspace, a->workspace_bytes, (cudaStream_t)stream);
+}
+
+extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* stream) {
+  moe::GroupedProblem p;
+  const moe_status st = wgrad_problem(a, &p);
+  if (st != MOE_OK) return st;
   return run_product(p, true, a->workspace, a->workspace_bytes, (cudaStream_t)stream);
+}
+
+extern "C" int moe_grouped_kernel(const moe_grouped_args* a, int num_sms) {
+  moe::GroupedProblem p;
+  return matmul_problem(a, &p) != MOE_OK || p.m == 0 || num_sms < 1 ? MOE_GROUPED_NONE
+                                                                    : plan_product(p, false, num_sms, a->workspace_bytes).kernel;
+}
+
+extern "C" int moe_grouped_wgrad_kernel(const moe_grouped_wgrad_args* a, int num_sms) {
+  moe::GroupedProblem p;
+  return wgrad_problem(a, &p) != MOE_OK || num_sms < 1 ? MOE_GROUPED_NONE
+                                                       : plan_product(p, true, num_sms, a->workspace_bytes).kernel;
 }
 
 extern "C" moe_status moe_verify_draft(const moe_verify_args* a, void* stream) {

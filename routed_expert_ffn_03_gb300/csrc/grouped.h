@@ -46,7 +46,7 @@ cudaError_t grouped_any_set_attributes();
 
 // A tensor map over elements of 2 or 4 bytes, 128-byte swizzled, zeros outside: dims and box in elements, innermost
 // first; strides (of dims 1 ..) in bytes.  False where the hardware cannot address the tensor so (a base, stride or
-// size it does not take).
+// size it does not take).  m null: that alone is looked at, without the driver.
 bool tensor_map(CUtensorMap* m, const void* base, size_t elem, int rank, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box);
 // The maps of a product, 64 elements wide.  a: the first factor in tiles.  b: the second, forward in boxes of 16, 32, 64
@@ -55,7 +55,7 @@ bool tensor_map(CUtensorMap* m, const void* base, size_t elem, int rank, const u
 struct GroupedMaps {
   CUtensorMap a, b[4], d;
 };
-// False where TMA cannot take the operands as they lie.
+// False where TMA cannot take the operands as they lie.  m null: that alone is looked at, without the driver.
 bool grouped_maps(const GroupedProblem& p, bool wgrad, bool few, GroupedMaps* m);
 
 // Copy of the rows named by number: dst[i][0 .. ld_dst) = src[rows[i]][0 .. len), zeros behind len and for a number

@@ -652,12 +652,14 @@ cudaError_t grouped_pair_set_attributes() {
 
 bool grouped_maps(const GroupedProblem& p, bool wgrad, bool few, GroupedMaps* m) {
   const uint64_t lda = p.lda * 2, ldb = p.ldb * 2;
+  CUtensorMap *ma = m ? &m->a : nullptr, *mb = m ? m->b : nullptr;
+  auto map_b = [&](int i) { return mb ? mb + i : nullptr; };
   if (p.a_nrows < 1 || p.a_nrows > 0x7fffffffLL) return false;
   if (wgrad) {
     if (p.b_nrows < 1 || p.b_nrows > 0x7fffffffLL) return false;
     const uint64_t da[] = {(uint64_t)p.n, (uint64_t)p.a_nrows}, db[] = {(uint64_t)p.k, (uint64_t)p.b_nrows};
     const uint32_t tile[] = {64, 64};
-    return tensor_map(&m->a, p.a, 2, 2, da, &lda, tile) && tensor_map(&m->b[0], p.b, 2, 2, db, &ldb, tile);
+    return tensor_map(ma, p.a, 2, 2, da, &lda, tile) && tensor_map(map_b(0), p.b, 2, 2, db, &ldb, tile);
   }
   const uint64_t n = p.n, k = p.k, E = p.groups;
   // one expert: any step to the next; several on top of one another are not a tensor
@@ -667,20 +669,20 @@ bool grouped_maps(const GroupedProblem& p, bool wgrad, bool few, GroupedMaps* m)
   if (p.swiglu && n / 2 % 16 == 0) {   // a tile's alternating runs of 16 rows of gate and up in one box
     const uint64_t h = n / 2, d[] = {k, 16, 2, h / 16, E}, st[] = {ldb, h * ldb, 16 * ldb, step};
     const uint32_t box[] = {64, 16, 2, 4, 1};
-    ok = tensor_map(&m->a, p.b, 2, 5, d, st, box);
+    ok = tensor_map(ma, p.b, 2, 5, d, st, box);
   } else {
     const uint64_t d[] = {p.kn ? n : k, p.kn ? k : n, E}, st[] = {ldb, step};
     const uint32_t box[] = {64, p.swiglu ? 16u : p.kn ? 64u : 128u, 1};
-    ok = tensor_map(&m->a, p.b, 2, 3, d, st, box);
+    ok = tensor_map(ma, p.b, 2, 3, d, st, box);
   }
   const uint64_t dx[] = {k, (uint64_t)p.a_nrows};
   if (few && p.a_rows) {
     const uint32_t one[] = {64, 1};
-    return ok && tensor_map(&m->b[0], p.a, 2, 2, dx, &lda, one);
+    return ok && tensor_map(map_b(0), p.a, 2, 2, dx, &lda, one);
   }
   for (int i = 0; i < (few ? 1 : 4) && ok; ++i) {
     const uint32_t tile[] = {64, 16u << i};
-    ok = tensor_map(&m->b[i], p.a, 2, 2, dx, &lda, tile);
+    ok = tensor_map(map_b(i), p.a, 2, 2, dx, &lda, tile);
   }
   return ok;
 }
