@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
       } else {
         const long long row = p.d_rows ? __ldg(p.d_rows + r0 + c) : r0 + c;
         float v = part[c * GA_M + (SW ? (f >> 4) * 32 + (f & 15) : f)];
-        if (SW) v = __fdividef(v, 1.f + expf(-v)) * part[c * GA_M + (f >> 4) * 32 + (f & 15) + 16];
+        if (SW) v = silu(v) * part[c * GA_M + (f >> 4) * 32 + (f & 15) + 16];
         if (row >= 0 && row < p.d_nrows) store_out(p.d, row * p.ldd + a0 + f, v, p.out_dtype);
       }
     }

@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
         }
       }
       if (SW) {
-        v.x = __fdividef(v.x, 1.f + expf(-v.x)) * u.x;
-        v.y = __fdividef(v.y, 1.f + expf(-v.y)) * u.y;
+        v.x = silu(v.x) * u.x;
+        v.y = silu(v.y) * u.y;
       }
       const long long row = p.d_rows ? __ldg(p.d_rows + r0 + t) : r0 + t;
       const int fo = f0 + 2 * j;

@@ -111,6 +111,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// g sigma(g), by e^-|g|: the quick division gives 0 where 1 + e^-g is past 2^126, and e^-g is infinite past that, where the
+// result is still a number of its type.  The exact division costs 0.6% of the Mixtral-shaped gate/up product of 1001 tokens (372
+// and 374 us).
+__device__ __forceinline__ float silu(float g) {
+  const float e = expf(-fabsf(g));
+  return g * ((g < 0.f ? e : 1.f) / (1.f + e));
+}
+
 // two results rounded to a 16-bit type
 __device__ __forceinline__ uint32_t pack_out(float lo, float hi, int dtype) {
   if (dtype == GT_BF16) {

@@ -557,7 +557,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
               const float mine = lane < 16 ? v[i] : v[i + 1];
               const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? v[i + 1] : v[i], 16);
               const float g = lane < 16 ? mine : other, u = lane < 16 ? other : mine;
-              const float h = __fdividef(g, 1.f + expf(-g)) * u;
+              const float h = silu(g) * u;
               bool live;
               char* at = place(i, live);
               if (F32) store32_if(live, at, __float_as_uint(h));

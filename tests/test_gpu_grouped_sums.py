@@ -102,3 +102,25 @@ def test_long_groups_of_a_weight_gradient_lose_nothing(M, n, k, out):
     g = M.grouped_wgrad(dy, x, dev(B.make_groups(sizes, None)), out_dtype=B.torch_type(out)).double().cpu().numpy()
     tol = (B.HALF_STEP[out] if out != "fp32" else 0) * want
     assert (np.abs(g - want[:, None, None]) <= tol[:, None, None]).all(), (g.min((1, 2)), g.max((1, 2)), want)
+
+
+@pytest.mark.parametrize("sizes,n,k", [([3, 2], 1024, 64), ([512, 700, 33, 800], 1536, 192), ([70, 2], 999, 65)])
+def test_swiglu_over_the_range_of_its_gate(M, sizes, n, k):
+    """Gates from deep in the exponential's underflow to past its overflow, with factors that bring the product back."""
+    import torch
+    E, m = len(sizes), sum(sizes)
+    g = np.concatenate([np.linspace(-104, 104, n - 8), [-87.5, -88, -88.5, -0.0, 0.0, -1e-30, 30000.0, -30000.0]])
+    u = np.where(np.arange(n) % 2 == 0, 2.0 ** 60, -1.5)
+    w = torch.zeros(E, 2 * n, k, dtype=torch.bfloat16, device="cuda")
+    w[:, :n, 0], w[:, n:, 0] = dev(g, torch.bfloat16), dev(u, torch.bfloat16)
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1
+    y = M.grouped_matmul(x, w, dev(B.make_groups(sizes, None)), act="swiglu", out_dtype=torch.float32).double().cpu().numpy()
+    g, u = w[0, :n, 0].double().cpu().numpy(), w[0, n:, 0].double().cpu().numpy()
+    with np.errstate(over="ignore"):
+        want = g / (1 + np.exp(-g)) * u
+    # the exponential, two products, a sum and a division, each within a step or two; below 2^-126 the exponential and the
+    # quotient have steps of 2^-149 each, which the gate and the factor multiply, and so has the result
+    tol = 8 * 2.0 ** -23 * np.abs(want) + 2 * 2.0 ** -149 * (np.abs(g * u) + 1)
+    bad = np.argwhere(~(np.abs(y - want) <= tol))
+    assert not len(bad), [(g[c], u[c], y[r, c], want[c]) for r, c in bad[:3]]
