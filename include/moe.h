@@ -380,7 +380,8 @@ int moe_grouped_wgrad_kernel(const moe_grouped_wgrad_args* a, int num_sms);
  *   rejected), else p[b][L]: the least v whose running sum exceeds u[b][D] times the total;
  *   tokens[b] = the r drafts, the drawn token, then -1 up to D + 1 entries.
  * p [B][D+1][V], q [B][D][V]: probabilities of `dtype` (any moe_dtype), each row summing to about one (8 at
- * most); rows p_row / q_row and sequences p_seq / q_seq elements apart.  q NULL: the drafts came
+ * most); rows p_row / q_row and sequences p_seq / q_seq elements apart, no two rows on one another: sequence behind
+ * sequence, or all sequences' first rows, then their second ones (with one sequence p_seq and q_seq do not matter).  q NULL: the drafts came
  * without probabilities (one-hot).  u (meant in [0, 1)), a draft's own p and q, and the weights are read as clamped
  * to [0, 1], NaN as 0; u = 1 draws the last v that has any weight.  The comparison is exact; a weight p - q is rounded
  * to fp32; running sums are exact in steps of 2^-60, so the order of summation decides nothing.  Where the

@@ -85,6 +85,13 @@ bool rows_fit(long long rows, long long ld, long long len) {
   return rows >= 0 && ld >= len && ld < (1ll << 40) && (rows == 0 || ld <= (1ll << 60) / rows);
 }
 
+// `rows` rows of `len` elements in each of B sequences, none on another: one sequence behind the other, or the sequences' first
+// rows, then their second ones, and so on
+bool sequences_fit(int B, long long seq, int rows, long long row, int len) {
+  if (!rows_fit(rows, row, len)) return false;
+  return B == 1 || rows_fit(B, seq, (rows - 1) * row + len) || (rows_fit(B, seq, len) && rows_fit(rows, row, (B - 1) * seq + len));
+}
+
 moe_status done(cudaError_t e) {
   if (e == cudaSuccess) return MOE_OK;
   cudaGetLastError();
@@ -332,9 +339,8 @@ extern "C" moe_status moe_verify_draft(const moe_verify_args* a, void* stream) {
   if (!a || !a->p || !a->u || !a->accepted || !a->tokens) return MOE_EINVAL;
   if (a->B < 1 || a->D < 0 || a->D > 31 || (a->D && !a->draft) || a->V < 1 || a->V > (1 << 30) || !is_dtype(a->dtype, true))
     return MOE_EINVAL;
-  if (!rows_fit(a->D + 1, a->p_row, a->V) || !rows_fit(a->B, a->p_seq, a->D * a->p_row + a->V)) return MOE_EINVAL;
-  if (a->q && a->D && (!rows_fit(a->D, a->q_row, a->V) || !rows_fit(a->B, a->q_seq, (a->D - 1) * a->q_row + a->V)))
-    return MOE_EINVAL;
+  if (!sequences_fit(a->B, a->p_seq, a->D + 1, a->p_row, a->V)) return MOE_EINVAL;
+  if (a->q && a->D && !sequences_fit(a->B, a->q_seq, a->D, a->q_row, a->V)) return MOE_EINVAL;
   const size_t el = dtype_bytes(a->dtype);
   if (!aligned(a->p, el) || !aligned(a->q, el) || !aligned(a->draft, 4) || !aligned(a->lengths, 4) || !aligned(a->u, 4) ||
       !aligned(a->accepted, 4) || !aligned(a->tokens, 4))
