@@ -398,8 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(VerifyA
     if (tok >= 0 && tok < a.V) {
       const float pv = clamp01(load_prob<DT>(p + lane * a.p_row * EL, tok));
       const float qv = q ? clamp01(load_prob<DT>(q + lane * a.q_row * EL, tok)) : 1.f;
-      const float uq = u * qv;   // and what its rounding left: the comparison is exact
-      stands = uq < pv || (uq == pv && __fmaf_rn(u, qv, -uq) < 0.f);
+      stands = (double)u * (double)qv < (double)pv;   // exact: 48 bits, and no product below fp64's range
     }
   }
   const unsigned no = __ballot_sync(0xffffffffu, !stands);

@@ -1,4 +1,6 @@
-"""verify_draft on views: one sequence of a larger tensor, and sequences row by row."""
+"""verify_draft on views (one sequence of a larger tensor, sequences row by row), and on drafts whose probabilities are at the
+bottom of fp32's range."""
+import numpy as np
 import pytest
 
 from tests.test_gpu_batch_route_verify import check_verify, make
@@ -34,3 +36,21 @@ def test_sequences_of_time_major_tensors(M, dtype):
         check_verify(M, step(p), draft, u, q)
         check_verify(M, p, draft, u, step(q))
         check_verify(M, step(p), draft, u)
+
+
+def test_drafts_of_the_least_probabilities(M):
+    """u q below fp32's least step, where it rounds up to p or down to 0: the comparison is exact."""
+    import torch
+    V, tiny = 64, 2.0 ** -149
+    cases = [(u, q, p) for u in (2.0 ** -24, 0.25, 0.5, 0.75, 1 - 2.0 ** -24, 1e-40, tiny, 0.0) for q in (tiny, 2 * tiny, 3 * tiny, 1e-38, 0.5, 1.0)
+             for p in (0.0, tiny, 2 * tiny, 3 * tiny, 1e-39)]
+    n = len(cases)
+    uu = np.zeros((n, 2), np.float32)
+    P, Q = np.zeros((n, 2, V), np.float32), np.zeros((n, 1, V), np.float32)
+    P[:, :, 5], Q[:, :, 6] = 0.5, 0.5
+    for i, (u, q, p) in enumerate(cases):
+        uu[i, 0], P[i, 0, 9], Q[i, 0, 9] = u, p, q
+    uu[:, 1] = 0.3
+    d = np.full((n, 1), 9)
+    acc, _ = check_verify(M, torch.from_numpy(P).cuda(), d, uu, torch.from_numpy(Q).cuda())
+    assert 0 < acc.sum() < n
