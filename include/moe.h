@@ -291,7 +291,7 @@ moe_status moe_group_route(const void* logits, long long ld, int dtype, int T, i
 size_t moe_group_route_workspace(int T, int E, int k);
 
 /* out row of i = act(W_e x_i) for every sorted row i of [offsets[e], offsets[e+1]), e < groups.
- *   x [x_rows][k] bf16 or fp16, rows ldx apart; row i reads x row rows[i], or x row i with
+ *   x [x_rows][k] bf16 or fp16 (NULL with x_rows 0), rows ldx apart; row i reads x row rows[i], or x row i with
  *   rows NULL (then m <= x_rows);
  *   w [groups] matrices of the same type, w_stride elements apart, rows ldw apart:
  *   [n][k] (MOE_GROUP_NK) or [k][n] (MOE_GROUP_KN);
@@ -344,7 +344,7 @@ size_t moe_grouped_workspace(long long m, int k, int groups);
  *   dy [dy_rows_n][n] and x [x_rows_n][k] bf16 or fp16, rows lddy and ldx apart; row i reads
  *   dy row dy_rows[i] and x row x_rows[i], or row i where that is NULL;
  *   dw [groups] matrices [n][k] bf16, fp16 or fp32, dw_stride elements apart, rows lddw apart.
- * Offsets, row numbers, limits, alignment and sums as moe_grouped_matmul; with m = 0 (dy and x may be
+ * Offsets, row numbers, limits, alignment and sums as moe_grouped_matmul (dy and x NULL with no rows); with m = 0 (dy and x may be
  * NULL then) dw is all zeros. */
 typedef struct {
     const void* dy;

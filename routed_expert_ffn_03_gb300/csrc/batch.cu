@@ -234,7 +234,7 @@ namespace {
 
 // the arguments checked, and as the kernels take them
 moe_status matmul_problem(const moe_grouped_args* a, moe::GroupedProblem* out) {
-  if (!a || !a->x || !a->w || !a->offsets || !a->out) return MOE_EINVAL;
+  if (!a || (!a->x && a->x_rows != 0) || !a->w || !a->offsets || !a->out) return MOE_EINVAL;
   if (!product_ok(a->groups, a->m, a->n, a->k, a->dtype, a->out_dtype)) return MOE_EINVAL;
   if (a->layout != MOE_GROUP_NK && a->layout != MOE_GROUP_KN) return MOE_EINVAL;
   if (a->act != MOE_ACT_NONE && a->act != MOE_ACT_SWIGLU) return MOE_EINVAL;
@@ -274,7 +274,8 @@ moe_status matmul_problem(const moe_grouped_args* a, moe::GroupedProblem* out) {
 }
 
 moe_status wgrad_problem(const moe_grouped_wgrad_args* a, moe::GroupedProblem* out) {
-  if (!a || !a->offsets || !a->dw || (a->m != 0 && (!a->dy || !a->x))) return MOE_EINVAL;
+  if (!a || !a->offsets || !a->dw) return MOE_EINVAL;
+  if (a->m != 0 && ((!a->dy && a->dy_rows_n != 0) || (!a->x && a->x_rows_n != 0))) return MOE_EINVAL;
   if (!product_ok(a->groups, a->m, a->n, a->k, a->dtype, a->out_dtype)) return MOE_EINVAL;
   if (!rows_fit(a->dy_rows_n, a->lddy, a->n) || !rows_fit(a->x_rows_n, a->ldx, a->k) || !rows_fit(a->n, a->lddw, a->k) ||
       a->dw_stride < (a->n - 1) * a->lddw + a->k || a->dw_stride >= (1ll << 50))

@@ -68,3 +68,19 @@ def test_calls_that_launch_nothing(M):
     w = G.wgrad_args(M, [1, 2], 64, 64)
     w.groups = 0
     assert M.grouped_kernel(w, 152) == M.GROUPED_NONE
+
+
+def test_an_empty_x_may_have_no_address(M):
+    """Rows named by number of an x without rows are rows of zeros."""
+    a = G.args(M, [4, 3], 64, 64, gather=True)
+    a.x, a.x_rows = None, 0
+    assert M.grouped_kernel(a, 152) == M.GROUPED_ANY
+    a.x_rows = 1
+    assert M.grouped_kernel(a, 152) == M.GROUPED_NONE
+    a.x_rows, a.rows = 0, None       # rows by their place would stand outside it
+    assert M.grouped_kernel(a, 152) == M.GROUPED_NONE
+    w = G.wgrad_args(M, [4, 3], 64, 64, dy_rows=True)
+    w.dy, w.dy_rows_n = None, 0
+    assert M.grouped_kernel(w, 152) == M.GROUPED_ANY
+    w.dy_rows = None
+    assert M.grouped_kernel(w, 152) == M.GROUPED_NONE
