@@ -289,7 +289,7 @@ def grouped_wgrad(dy, x, offsets, dy_rows=None, x_rows=None, out=None, out_dtype
     """The weights' gradient of grouped_matmul (moe_grouped_wgrad): out[e] = sum over the sorted rows i of
     expert e of dy[dy_rows[i]]^T x[x_rows[i]], [E, n, k] (zeros where a group is empty).
 
-    dy [R, n] and x [S, k] bf16 or fp16 of one type; offsets [E + 1] int32.  For "kn" weights exchange dy and x.
+    dy [R, n] and x [S, k] bf16 or fp16 of one type (R = S without row numbers); offsets [E + 1] int32.  For "kn" weights exchange dy and x.
     workspace (with row numbers): uint8 device memory of grouped_wgrad_workspace(m, n) bytes for dy_rows and
     grouped_wgrad_workspace(m, k) for x_rows; new memory without it."""
     torch, L = _start()
@@ -302,7 +302,9 @@ def grouped_wgrad(dy, x, offsets, dy_rows=None, x_rows=None, out=None, out_dtype
     if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError("offsets: one more than the groups, got %s" % (tuple(offsets.shape),))
     E, i32 = offsets.shape[0] - 1, torch.int32
-    m = dy_rows.shape[0] if dy_rows is not None else x_rows.shape[0] if x_rows is not None else min(R, S)
+    if dy_rows is None and x_rows is None and R != S:
+        raise ValueError("dy has %d rows, x %d, and neither's are named by number" % (R, S))
+    m = dy_rows.shape[0] if dy_rows is not None else x_rows.shape[0] if x_rows is not None else R
     if out is None:
         out, = _new(stream, dev, ((E, n, k), out_dtype or dy.dtype))
     shape, o_stride = _dense(out, "out", 3, dev)
