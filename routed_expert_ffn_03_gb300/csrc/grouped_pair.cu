@@ -378,13 +378,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
     if (WG) {
       int s = 0;
       uint32_t land_ph = 0;
+      unsigned long long steps = 0;   // that the ring may still have to take until the next one that is cleared
       bool ok = true;
       for (int t = pair; t < total && ok; t += npair) {
         const Tile T = decode<MODE>(a, first, t);
         if (T.nkb == 0) continue;
         s = (s + T.nkb - 1) % GP_STAGES;   // the tile's last step
+        steps += T.nkb;
         if (clears(T, T.nkb - 1)) {
-          ok = __all_sync(0xffffffffu, wait_bar(land0 + 8 * s, (land_ph >> s) & 1));
+          ok = __all_sync(0xffffffffu, wait_bar(land0 + 8 * s, (land_ph >> s) & 1, steps));
+          steps = 0;
           land_ph ^= 1u << s;
           if (!ok) break;
           uint8_t* st = smem + s * GP_STAGE;

@@ -124,3 +124,21 @@ def test_swiglu_over_the_range_of_its_gate(M, sizes, n, k):
     tol = 8 * 2.0 ** -23 * np.abs(want) + 2 * 2.0 ** -149 * (np.abs(g * u) + 1)
     bad = np.argwhere(~(np.abs(y - want) <= tol))
     assert not len(bad), [(g[c], u[c], y[r, c], want[c]) for r, c in bad[:3]]
+
+
+def test_a_group_that_takes_longer_than_a_wait(M):
+    """300 million rows in one group of one tile: more than a second of steps in front of the one that ends the group.  They
+    are summed, and the next call finds nothing wrong."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    m = 300_000_037
+    t = torch.ones(m, 8, dtype=torch.bfloat16, device="cuda")
+    o = torch.tensor([0, m - 3, m], dtype=torch.int32, device="cuda")
+    for out in (torch.bfloat16, torch.float32):
+        g = M.grouped_wgrad(t, t, o, out_dtype=out)
+        torch.cuda.synchronize()
+        # parts of 512 ones are exact, and so is their sum up to the last one (below 2^29 fp32 has steps of 32)
+        assert float((g[0].double() - (m - 3)).abs().max()) <= 32 + (B.HALF_STEP["bf16"] * m if out == torch.bfloat16 else 0)
+        assert bool((g[1] == 3).all())
+    assert float(M.grouped_wgrad(t[:70], t[:70], torch.tensor([0, 70], dtype=torch.int32, device="cuda")).max()) == 70
