@@ -261,7 +261,7 @@ moe_status moe_route_noalloc(const uint16_t* x_bf16, const float* W, int T, int 
  * checked on the host (MOE_EINVAL); what stands in device memory (offsets, row numbers,
  * lengths, token ids) cannot be, so the kernels check it: each call says what a bad value
  * does, and none reads or writes outside the arrays.  A device wait that runs out makes
- * the next call on that device return MOE_ETIMEOUT (sticky).
+ * later calls on that device return MOE_ETIMEOUT (sticky; see moe_debug_batch_wait).
  * Same inputs, same bits: no atomics order a sum. */
 typedef enum { MOE_T_BF16 = 0, MOE_T_FP16 = 1, MOE_T_FP32 = 2 } moe_dtype;
 typedef enum {
@@ -433,6 +433,12 @@ moe_status moe_debug_fail_copies(moe_ctx* ctx, int n);
  * the expected answer.  The time-out is recorded in *status only; it does not make the
  * context sticky. */
 moe_status moe_debug_wait_timeout(moe_ctx* ctx, unsigned long long cycles, void* stream, int* status);
+
+/* Bound the device waits of the batch calls made on the current device from now on to `cycles` SM clock cycles (0: their
+ * products wait for a flag that nothing sets; below 0: the usual bound, about a second), and forget a wait that ran out, with
+ * none of those calls in flight.  A product whose wait runs out ends early, its result undefined, and the calls after it return
+ * MOE_ETIMEOUT. */
+moe_status moe_debug_batch_wait(long long cycles);
 
 /* ---------------------------------------------------------------- the file tier alone
  * The RAM + file part of the streamed store on its own ("WISP - streaming what can't run",

@@ -65,6 +65,8 @@ def _lib():
             getattr(L, n).restype = ctypes.c_size_t
         for n in ("moe_grouped_matmul", "moe_grouped_wgrad", "moe_verify_draft"):
             getattr(L, n).argtypes = [_vp, _vp]
+        L.moe_debug_batch_wait.argtypes = [_ll]
+        L.moe_debug_batch_wait.restype = _i
         for n in ("moe_grouped_kernel", "moe_grouped_wgrad_kernel"):
             getattr(L, n).argtypes = [_vp, _i]
             getattr(L, n).restype = _i
@@ -223,6 +225,14 @@ def grouped_workspace(m, k, groups):
 def grouped_wgrad_workspace(m, length):
     """Bytes of workspace that grouped_wgrad needs for m rows of that length named by number."""
     return int(_lib().moe_grouped_wgrad_workspace(m, length))
+
+
+def debug_batch_wait(cycles=-1):
+    """Bound the batch operators' device waits on the current device in SM cycles (0: their
+    products wait for a flag that nothing sets, -1: the usual bound), and forget one that ran out (moe_debug_batch_wait)."""
+    st = _lib().moe_debug_batch_wait(cycles)
+    if st != OK:
+        raise MoeError(st, "moe_debug_batch_wait")
 
 
 def grouped_kernel(args, num_sms):

@@ -22,7 +22,11 @@ struct Device {
   int num_sms;
   uint32_t* status;                 // as the device sees it
   volatile uint32_t* host_status;
+  std::atomic<unsigned long long> wait_cycles;   // bound of the kernels' waits
+
+  moe::WaitLimit wait() const { return {status, wait_cycles.load(std::memory_order_relaxed)}; }
 };
+constexpr unsigned long long kWaitCycles = 2000000000ull;   // about a second
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 std::atomic<Device*> g_device[kMaxDevices];
@@ -30,8 +34,8 @@ std::atomic<Device*> g_device[kMaxDevices];
 moe_status device_setup(int dev, Device** out) {
   std::lock_guard<std::mutex> lk(g_mu);
   if ((*out = g_device[dev].load())) return MOE_OK;
-  Device d{0, nullptr, nullptr};
-  if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+  int num_sms = 0;
+  if (cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       moe::grouped_any_set_attributes() != cudaSuccess || moe::grouped_pair_set_attributes() != cudaSuccess ||
       moe::grouped_few_set_attributes() != cudaSuccess || moe::verify_set_attributes() != cudaSuccess ||
       moe::group_route_set_attributes() != cudaSuccess) {
@@ -41,7 +45,7 @@ moe_status device_setup(int dev, Device** out) {
   // the word stands in a page of its own, registered
   const size_t page = (size_t)sysconf(_SC_PAGESIZE);
   void* word = nullptr;
-  *out = new (std::nothrow) Device(d);
+  *out = new (std::nothrow) Device{num_sms, nullptr, nullptr, {kWaitCycles}};
   if (!*out || posix_memalign(&word, page, page) != 0) {
     delete *out;
     return MOE_ENOMEM;
@@ -183,15 +187,15 @@ moe_status run_product(moe::GroupedProblem p, bool wgrad, void* workspace, size_
   const Operand b{&p.b, &p.b_rows, &p.b_nrows, &p.ldb, p.k};
   const Plan pl = plan_product(p, wgrad, d->num_sms, workspace_bytes);
   cudaError_t e = cudaSuccess;
-  if (pl.kernel == MOE_GROUPED_FEW && moe::launch_grouped_few(p, pl.nt, pl.cluster, d->status, s, &e)) return done(e);
+  if (pl.kernel == MOE_GROUPED_FEW && moe::launch_grouped_few(p, pl.nt, pl.cluster, d->wait(), s, &e)) return done(e);
   if (pl.kernel == MOE_GROUPED_PAIR) {
     uint16_t* ws = static_cast<uint16_t*>(workspace);
     if (pl.need_a) e = copy_operand(a, p, ws, d->num_sms, s);
     if (pl.need_b && e == cudaSuccess) e = copy_operand(b, p, ws + pl.need_a / 2, d->num_sms, s);
     if (e != cudaSuccess) return done(e);
-    if (moe::launch_grouped_pair(p, wgrad, d->num_sms, d->status, s, &e)) return done(e);
+    if (moe::launch_grouped_pair(p, wgrad, d->num_sms, d->wait(), s, &e)) return done(e);
   }
-  return done(moe::launch_grouped_any(p, wgrad, d->status, s));
+  return done(moe::launch_grouped_any(p, wgrad, d->wait(), s));
 }
 
 }  // namespace
@@ -322,6 +326,15 @@ extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* s
   const moe_status st = wgrad_problem(a, &p);
   if (st != MOE_OK) return st;
   return run_product(p, true, a->workspace, a->workspace_bytes, (cudaStream_t)stream);
+}
+
+extern "C" moe_status moe_debug_batch_wait(long long cycles) {
+  Device* d;
+  const moe_status st = current_device(&d);
+  if (st != MOE_OK && st != MOE_ETIMEOUT) return st;
+  d->wait_cycles.store(cycles < 0 ? kWaitCycles : (unsigned long long)cycles);
+  *d->host_status = 0;
+  return MOE_OK;
 }
 
 extern "C" int moe_grouped_kernel(const moe_grouped_args* a, int num_sms) {

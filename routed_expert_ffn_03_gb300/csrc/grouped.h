@@ -40,8 +40,14 @@ __device__ __forceinline__ void group_range(const int* offsets, int g, long long
 }
 #endif
 
-// For any strides and alignment.  status: host-visible word that a wait which ran out sets.
-cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, uint32_t* status, cudaStream_t s);
+// The bound of a kernel's waits, in SM cycles, and the host-visible word that one which runs out sets.
+struct WaitLimit {
+  uint32_t* status;
+  unsigned long long cycles;
+};
+
+// For any strides and alignment.
+cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, const WaitLimit& wait, cudaStream_t s);
 cudaError_t grouped_any_set_attributes();
 
 // A tensor map over elements of 2 or 4 bytes, 128-byte swizzled, zeros outside: dims and box in elements, innermost
@@ -71,13 +77,13 @@ struct RowCopy {
 cudaError_t launch_copy_rows(const RowCopy& c, int num_sms, cudaStream_t s);
 
 // The tensor-core kernel over pairs of SMs; false (nothing launched) where TMA cannot take the operands.
-bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, uint32_t* status, cudaStream_t s,
+bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, const WaitLimit& wait, cudaStream_t s,
                          cudaError_t* err);
 cudaError_t grouped_pair_set_attributes();
 
 // The kernel for few rows a group, in tiles of nt = 16, 32 or 64 rows, `cluster` (1, 2, 4, 8) blocks to a tile; forward
 // products only; reads rows by number where they are.  Otherwise as launch_grouped_pair.
-bool launch_grouped_few(const GroupedProblem& p, int nt, int cluster, uint32_t* status, cudaStream_t s, cudaError_t* err);
+bool launch_grouped_few(const GroupedProblem& p, int nt, int cluster, const WaitLimit& wait, cudaStream_t s, cudaError_t* err);
 cudaError_t grouped_few_set_attributes();
 
 }  // namespace moe

@@ -33,7 +33,7 @@ constexpr int GA_SMEM = GA_STAGES * GA_STAGE + 256 + 1024;
 
 struct AnyArgs {
   GroupedProblem p;
-  uint32_t* status;
+  WaitLimit wait;
 };
 
 // 8 elements at s (null: zeros), zeros from `left` on, as the two aligned words around them, or finished in the first
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * GA_STAGES, tfull0 = empty0 + 8 * GA_STAGES, tempty0 = tfull0 + 16;
   if (tid == 0) {
     for (int s = 0; s < GA_STAGES; ++s) {
-      mbar_init(full0 + 8 * s, GA_COPY_WARPS);
+      mbar_init(full0 + 8 * s, stage_arrivals(args.wait, GA_COPY_WARPS));
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
     bool ok = true;
     // step kb's words, and then those of step kb + 2 in the same registers
     auto step = [&](int kb, Word8 (&va)[GA_AW], Word8 (&vb)[GA_BW]) {
-      ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1));
+      ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1, args.wait));
       if (!ok) return;
       uint8_t* st = smem + s * GA_STAGE;
 #pragma unroll
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
     uint32_t raph = 0;
     bool ok = true;
     auto add_part = [&]() {
-      ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * racc, raph));
+      ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * racc, raph, args.wait));
       if (!ok) return;
       umma_fence_after();
 #pragma unroll
@@ -304,10 +304,10 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
       uint32_t ph = 0, aph = 0;
       for (int k0 = 0; k0 < nkb && ok; k0 += GA_PART) {
         const int k1 = min(k0 + GA_PART, nkb);
-        ok = __all_sync(0xffffffffu, wait_bar(tempty0 + 8 * acc, aph ^ 1));
+        ok = __all_sync(0xffffffffu, wait_bar(tempty0 + 8 * acc, aph ^ 1, args.wait));
         umma_fence_after();
         for (int kb = k0; kb < k1 && ok; ++kb) {
-          ok = __all_sync(0xffffffffu, wait_bar(full0 + 8 * s, ph));
+          ok = __all_sync(0xffffffffu, wait_bar(full0 + 8 * s, ph, args.wait));
           if (!ok) break;
           umma_fence_after();
           const uint32_t off = s * (GA_STAGE >> 4);
@@ -346,10 +346,7 @@ __global__ void __launch_bounds__(GA_THREADS, 1) grouped_any_kernel(const __grid
   umma_fence_before();
   __syncthreads();
   if (*s_abort) {   // a wait ran out: report, and let what is in flight end before the memory goes
-    if (tid == 0) {
-      *reinterpret_cast<volatile uint32_t*>(args.status) = ST_TIMEOUT;
-      __threadfence_system();
-    }
+    if (tid == 0) report_wait(args.wait);
     drain_time();
   } else if (e >= 0) {
     // stored by all warps in a short loop, neighbours along a row: unrolled over the columns in registers the code
@@ -396,14 +393,14 @@ cudaError_t grouped_any_set_attributes() {
   return e;
 }
 
-cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, uint32_t* status, cudaStream_t s) {
+cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, const WaitLimit& wait, cudaStream_t s) {
   // forward: every group can end inside a tile, so m rows make at most m / 64 + min(groups, m) row tiles
   const long long blocks =
       wgrad ? (long long)p.groups * ceil_div(p.k, GA_M) * ceil_div(p.n, GA_N)
             : (p.m / GA_N + (p.m < p.groups ? p.m : p.groups)) * ceil_div(p.swiglu ? p.n / 2 : p.n, p.swiglu ? GA_M / 2 : GA_M);
   if (blocks <= 0) return cudaSuccess;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const AnyArgs a{p, status};
+  const AnyArgs a{p, wait};
   if (wgrad) return launch_mode<GA_WGRAD>(a, (unsigned)blocks, s);
   if (p.swiglu) return launch_mode<GA_SWIGLU>(a, (unsigned)blocks, s);
   return p.kn ? launch_mode<GA_KN>(a, (unsigned)blocks, s) : launch_mode<GA_NK>(a, (unsigned)blocks, s);

@@ -36,7 +36,7 @@ struct FewArgs {
   GroupedProblem p;
   int nft;              // feature tiles
   int cluster;
-  uint32_t* status;
+  WaitLimit wait;
   bool wide;            // 16-bit results can be stored in pairs
   bool by_16;           // swiglu: W_e in boxes of 16 rows
 };
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, tfull0 = empty0 + 8 * STAGES, tempty0 = tfull0 + 16;
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full0 + 8 * s, 1);
+      mbar_init(full0 + 8 * s, stage_arrivals(a.wait, 1));
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
     uint32_t ph = 0;
     bool ok = true;
     for (int kb = kb0; kb < kb1; ++kb) {
-      ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1));
+      ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1, a.wait));
       if (!ok) break;
       const uint32_t bar = bar0 + 8 * s, da = base + s * STAGE;
       if (leader) {
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
     uint32_t ph = 0;
     bool ok = true;
     for (int kb = kb0; kb < kb1; ++kb) {
-      ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1));
+      ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1, a.wait));
       if (!ok) break;
       const uint32_t bar = full0 + 8 * s, db = smem_u32(smem) + s * STAGE + GF_A;
       if (p.a_rows) {
@@ -178,10 +178,10 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
     bool ok = true;
     for (int k0 = kb0; k0 < kb1 && ok; k0 += GF_PART) {
       const int k1 = min(k0 + GF_PART, kb1);
-      ok = __all_sync(0xffffffffu, wait_bar(tempty0 + 8 * acc, aph ^ 1));
+      ok = __all_sync(0xffffffffu, wait_bar(tempty0 + 8 * acc, aph ^ 1, a.wait));
       umma_fence_after();
       for (int kb = k0; kb < k1 && ok; ++kb) {
-        ok = __all_sync(0xffffffffu, wait_bar(full0 + 8 * s, ph));
+        ok = __all_sync(0xffffffffu, wait_bar(full0 + 8 * s, ph, a.wait));
         if (!ok) break;
         umma_fence_after();
         const uint64_t da = da0 + (uint32_t)(s * (STAGE >> 4)), db = db0 + (uint32_t)(s * (STAGE >> 4));
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
     uint32_t aph = 0;
     bool ok = true;
     for (int k0 = kb0; k0 < kb1; k0 += GF_PART) {
-      ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, aph));
+      ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, aph, a.wait));
       if (!ok) break;
       umma_fence_after();
 #pragma unroll
@@ -244,10 +244,7 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
   umma_fence_before();
   __syncthreads();
   if (*s_abort) {   // a wait ran out: report, and let what is in flight end before the memory goes
-    if (tid == 0) {
-      *reinterpret_cast<volatile uint32_t*>(a.status) = ST_TIMEOUT;
-      __threadfence_system();
-    }
+    if (tid == 0) report_wait(a.wait);
     drain_time();
   }
   if (C > 1) cluster_sync_all();
@@ -346,12 +343,12 @@ cudaError_t grouped_few_set_attributes() {
   return e == cudaSuccess ? set_attributes<GF_SWIGLU>() : e;
 }
 
-bool launch_grouped_few(const GroupedProblem& p, int nt, int cluster, uint32_t* status, cudaStream_t s, cudaError_t* err) {
+bool launch_grouped_few(const GroupedProblem& p, int nt, int cluster, const WaitLimit& wait, cudaStream_t s, cudaError_t* err) {
   GroupedMaps m;
   if (!grouped_maps(p, false, true, &m)) return false;
   FewArgs a;
   a.p = p;
-  a.status = status;
+  a.wait = wait;
   const int n_out = p.swiglu ? p.n / 2 : p.n;
   a.nft = (int)ceil_div(n_out, p.swiglu ? 64 : 128);
   a.cluster = cluster;

@@ -195,14 +195,20 @@ __device__ __forceinline__ void cluster_sync_all() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// Every wait of the grouped kernels is bounded: about a second of SM cycles, far beyond any part of a tile, and where a warp
-// waits across more steps of 64 elements, 30 times what one takes for each of them.
-constexpr unsigned long long WAIT_CYCLES = 2000000000ull;
+// Every wait of the grouped kernels is bounded: by WaitLimit, as a rule about a second, far beyond any part of a tile, and where
+// a warp waits across more steps of 64 elements, by 30 times what one takes for each of them on top.
 constexpr unsigned long long WAIT_STEP = 16384;
 // after a wait ran out: long enough for every copy and product in flight to end
 constexpr long long DRAIN_CYCLES = 100000000ll;
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, unsigned long long steps = 0) {
-  return mbar_wait_bounded(bar, parity, WAIT_CYCLES + steps * WAIT_STEP);
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const WaitLimit& limit, unsigned long long steps = 0) {
+  return mbar_wait_bounded(bar, parity, limit.cycles + steps * WAIT_STEP);
+}
+// Arrivals on the barrier of a stage's operands, n of them.  Under a bound of no cycles it is one more, which never comes: the
+// hardware suspends a waiting thread for longer than the operands take, so a short bound alone would not run out.
+__device__ __forceinline__ uint32_t stage_arrivals(const WaitLimit& limit, uint32_t n) { return n + (limit.cycles == 0); }
+__device__ __forceinline__ void report_wait(const WaitLimit& limit) {
+  *reinterpret_cast<volatile uint32_t*>(limit.status) = ST_TIMEOUT;
+  __threadfence_system();
 }
 __device__ __forceinline__ void drain_time() {
   const long long t0 = clock64();

@@ -75,7 +75,7 @@ struct PairArgs {
   GroupedProblem p;
   int nft, nkt;        // forward: feature tiles; weight gradient: n tiles and k tiles
   int max_tiles;       // the most that m rows can make
-  uint32_t* status;
+  WaitLimit wait;
   bool wide;           // results can be stored as 4-byte pairs (forward) or by TMA (weight gradient)
   bool by_16;          // swiglu: W_e in boxes of 16 rows
 };
@@ -174,7 +174,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < GP_STAGES; ++s) {
-      mbar_init(full0 + 8 * s, 1);     // first block's: its own arrival, both blocks' bytes
+      mbar_init(full0 + 8 * s, stage_arrivals(a.wait, 1));   // first block's: its own arrival, both blocks' bytes
       mbar_init(empty0 + 8 * s, 1);    // the products that read the stage
       mbar_init(land0 + 8 * s, 1);     // this block's tiles of a step that has rows to clear
       mbar_init(ready0 + 8 * s, 2);    // first block's: both blocks have cleared theirs
@@ -258,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
       const int f = f0 + side * (SW ? 64 : 128), fb = c0 + side * 128, rb = r0 + side * half;
       const uint32_t bytes = GP_OP + (WG ? GP_OP : half * 128);   // of a step, in each block
       for (int kb = 0; kb < nkb; ++kb) {
-        ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1));
+        ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1, a.wait));
         if (!ok) break;
         // a step whose rows behind the group are to be cleared is announced to the block's own warp 10
         const bool clear = clears(T, kb);
@@ -306,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
     }
     // the first block's products signal this block's barriers: they have all done so before it may exit
     for (int i = 0; i < GP_STAGES && ok; ++i) {
-      ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1));
+      ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ph ^ 1, a.wait));
       if (++s == GP_STAGES) {
         s = 0;
         ph ^= 1;
@@ -338,13 +338,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         const int steps = part_steps(nkb);
         for (int kb0 = 0; kb0 < nkb && ok; kb0 += steps) {
           const int kb1 = min(kb0 + steps, nkb);
-          ok = __all_sync(0xffffffffu, wait_bar(tempty0 + 8 * acc, aph ^ 1));
+          ok = __all_sync(0xffffffffu, wait_bar(tempty0 + 8 * acc, aph ^ 1, a.wait));
           umma_fence_after();
           const uint32_t dst = tm + acc * 256;
           for (int kb = kb0; kb < kb1 && ok; ++kb) {
-            ok = __all_sync(0xffffffffu, wait_bar(full0 + 8 * s, ph));
+            ok = __all_sync(0xffffffffu, wait_bar(full0 + 8 * s, ph, a.wait));
             if (WG && kb == nkb - 1 && last_rows < 64) {   // rows behind the group are being cleared
-              ok = __all_sync(0xffffffffu, ok && wait_bar(ready0 + 8 * s, (ready_ph >> s) & 1));
+              ok = __all_sync(0xffffffffu, ok && wait_bar(ready0 + 8 * s, (ready_ph >> s) & 1, a.wait));
               ready_ph ^= 1u << s;
             }
             if (!ok) break;
@@ -386,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         s = (s + T.nkb - 1) % GP_STAGES;   // the tile's last step
         steps += T.nkb;
         if (clears(T, T.nkb - 1)) {
-          ok = __all_sync(0xffffffffu, wait_bar(land0 + 8 * s, (land_ph >> s) & 1, steps));
+          ok = __all_sync(0xffffffffu, wait_bar(land0 + 8 * s, (land_ph >> s) & 1, a.wait, steps));
           steps = 0;
           land_ph ^= 1u << s;
           if (!ok) break;
@@ -435,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[q][i] = 0.f;
         for (int kb = 0; kb < T.nkb && ok; kb += part_steps(T.nkb)) {
-          ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, aph));
+          ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, aph, a.wait));
           if (!ok) break;
           umma_fence_after();
 #pragma unroll
@@ -455,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         }
         if (!ok) break;
       } else if (T.nkb > 0) {
-        ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, aph));
+        ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, aph, a.wait));
         if (!ok) break;
         umma_fence_after();
         td = tmem + acc * 256 + ((uint32_t)(quarter * 32) << 16);
@@ -596,10 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   umma_fence_before();
   __syncthreads();
   if (*s_abort) {   // a wait ran out: report, and let what is in flight end before the memory goes
-    if (tid == 0) {
-      *reinterpret_cast<volatile uint32_t*>(a.status) = ST_TIMEOUT;
-      __threadfence_system();
-    }
+    if (tid == 0) report_wait(a.wait);
     drain_time();
   }
   cluster_sync_all();   // the peer reads and signals this block's memory until here
@@ -690,13 +687,13 @@ bool grouped_maps(const GroupedProblem& p, bool wgrad, bool few, GroupedMaps* m)
   return ok;
 }
 
-bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, uint32_t* status, cudaStream_t s,
+bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, const WaitLimit& wait, cudaStream_t s,
                          cudaError_t* err) {
   GroupedMaps m;
   if (p.a_rows || p.b_rows || !grouped_maps(p, wgrad, false, &m)) return false;
   PairArgs a;
   a.p = p;
-  a.status = status;
+  a.wait = wait;
   a.by_16 = p.swiglu && p.n / 2 % 16 != 0;
   const int n_out = p.swiglu ? p.n / 2 : p.n;
   const size_t el = p.out_dtype == GT_FP32 ? 4 : 2;
