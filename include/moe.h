@@ -435,9 +435,9 @@ moe_status moe_debug_fail_copies(moe_ctx* ctx, int n);
 moe_status moe_debug_wait_timeout(moe_ctx* ctx, unsigned long long cycles, void* stream, int* status);
 
 /* Bound the device waits of the batch calls made on the current device from now on to `cycles` SM clock cycles (0: their
- * products wait for a flag that nothing sets; below 0: the usual bound, about a second), and forget a wait that ran out, with
- * none of those calls in flight.  A product whose wait runs out ends early, its result undefined, and the calls after it return
- * MOE_ETIMEOUT. */
+ * products wait for a flag that nothing sets; below 0: the usual bound, about a second; 2^36 at most), and forget a wait that
+ * ran out, with none of those calls in flight.  A product whose wait runs out ends early, its result undefined, and the calls
+ * after it return MOE_ETIMEOUT. */
 moe_status moe_debug_batch_wait(long long cycles);
 
 /* ---------------------------------------------------------------- the file tier alone

@@ -329,6 +329,7 @@ extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* s
 }
 
 extern "C" moe_status moe_debug_batch_wait(long long cycles) {
+  if (cycles > 1ll << 36) return MOE_EINVAL;
   Device* d;
   const moe_status st = current_device(&d);
   if (st != MOE_OK && st != MOE_ETIMEOUT) return st;

@@ -84,3 +84,9 @@ def test_an_empty_x_may_have_no_address(M):
     assert M.grouped_kernel(w, 152) == M.GROUPED_ANY
     w.dy_rows = None
     assert M.grouped_kernel(w, 152) == M.GROUPED_NONE
+
+
+def test_waits_stay_bounded(M):
+    with pytest.raises(M.MoeError) as e:
+        M.debug_batch_wait(2 ** 36 + 1)
+    assert e.value.status == M.EINVAL
