@@ -142,3 +142,23 @@ def test_a_group_that_takes_longer_than_a_wait(M):
         assert float((g[0].double() - (m - 3)).abs().max()) <= 32 + (B.HALF_STEP["bf16"] * m if out == torch.bfloat16 else 0)
         assert bool((g[1] == 3).all())
     assert float(M.grouped_wgrad(t[:70], t[:70], torch.tensor([0, 70], dtype=torch.int32, device="cuda")).max()) == 70
+
+
+@pytest.mark.parametrize("out", ["fp16", "bf16", "fp32"])
+def test_long_group_into_rows_of_an_odd_pitch(M, out):
+    """The same in a result that leaves the kernel element by element."""
+    import torch
+    sizes, n, k = [20485, 40], 264, 520
+    a, b, ones = far_sum(sizes[0])
+    t = B.torch_type(out if out != "fp32" else "bf16")
+    dy = torch.ones(sum(sizes), n, dtype=t, device="cuda")
+    x = torch.ones(sum(sizes), k, dtype=t, device="cuda")
+    scale = 1 + np.arange(n) % 4             # each row of the gradient its own multiple
+    dy[:sizes[0]] = dev(a[:, None] * np.where(a[:, None] == 1, scale, 1), t)
+    x[:sizes[0]] = dev(b, t)[:, None]
+    full = torch.full((2, n + 1, k + 3), 7.0, dtype=B.torch_type(out), device="cuda")
+    M.grouped_wgrad(dy, x, dev(B.make_groups(sizes, None)), out=full[:, :n, :k])
+    want = np.stack([ones * scale, np.full(n, 40)])[:, :, None]
+    g = full[:, :n, :k].double().cpu().numpy()
+    assert (np.abs(g - want) <= (B.HALF_STEP[out] * want if out != "fp32" else 0)).all(), (g.min((1, 2)), g.max((1, 2)))
+    assert bool((full[:, n:] == 7).all()) and bool((full[:, :, k:] == 7).all())
