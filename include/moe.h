@@ -335,7 +335,8 @@ typedef struct {
 } moe_grouped_args;
 moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream);
 /* Bytes of workspace for m rows of length k named by number, over that many groups (0 where the rows are so few that the
- * kernel for them reads them where they are, and for sizes that are refused). */
+ * kernel for them reads them where they are whatever n is, and for sizes that are refused; moe_grouped_kernel says
+ * MOE_GROUPED_FEW of the other calls that leave the workspace alone). */
 size_t moe_grouped_workspace(long long m, int k, int groups);
 
 /* dw[e][n][k] = sum over the sorted rows i of expert e of dy_i[n] x_i[k]: the weights' gradient

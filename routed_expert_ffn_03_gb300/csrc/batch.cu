@@ -113,7 +113,9 @@ bool product_ok(int groups, long long m, int n, int k, int dtype, int out_dtype)
 // Whether the kernel for few rows a group takes a forward product, by the mean over the groups that m rows can reach, as
 // the groups' sizes are not known here: tiles of nt rows, four times the mean, so that uneven groups fit too.  Measured
 // (DeepSeek-V3- and Mixtral-shaped layers, us for nt 16 / 32 / 64 / the pair kernel): mean 1: 73 / 73 / 75 / 79; mean 8:
-// 2102 / 2076 / 2096 / 2189; mean 16: 390 / 284 / 275 / 281; mean 24: 499 / 319 / 278 / 282; mean 32: 622 / 417 / 308 / 284.
+// 2102 / 2076 / 2096 / 2189; mean 16: 390 / 284 / 275 / 281; mean 24: 499 / 319 / 278 / 282; mean 32: 622 / 417 / 308 / 284.  Uneven groups at mean 16 (64 experts, n =
+// 4096, k = 14336): half of the rows in one group 1118 and 1125 us by the pair kernel, all of them in four groups 153 and 91, in one
+// 145 and 72; 256 experts 539 and 275: an expert's weights are then read by more tiles than the pair kernel makes.
 int few_rows_tile(long long m, int groups) {
   const long long reach = m < groups ? m : groups;
   return m < 1 ? 0 : m <= 4 * reach ? 16 : m <= 8 * reach ? 32 : m <= 16 * reach ? 64 : 0;
@@ -123,8 +125,8 @@ int few_rows_tile(long long m, int groups) {
 // 450 tiles of k = 2048: 40 / 45 / 53 / 82 us.  Tiles full of rows gain less: one block an SM (192 tiles, k = 2048: 13 / 18 us).
 // It also takes products of which the pair kernel would keep a third of its pairs busy or fewer (4096 rows in 4 groups, n =
 // 128: k = 512 14 and 9 us, k = 4096 34 and 21 us; n = 512, k = 4096 36 and 71 us), or whose tiles of 32 rows stand on the SMs
-// all at once, while k is not long (768 rows in 32 groups, n = 768, k = 512: 10.4 and 7.6 us; in 8 groups, k = 2048: 15.7 and
-// 12.7; 1536 in 32, n = 768: 12.0 and 12.7, 504 tiles), and up to half of the pairs where a tile of 64 rows covers a group
+// all at once, taken as the most that m rows make, while k is not long (pair kernel and this one: 768 rows in 32 groups, n = 512,
+// k = 512 7.3 and 7.1 us; in 8 groups, k = 2048 13.2 and 10.4, n = 768 13.2 and 13.4, 192 tiles), and up to half of the pairs where a tile of 64 rows covers a group
 // and k is long enough to share out (308 rows in 7 groups, n = 928, k = 14280: 57 and 39 us; n = 1024, k = 1024: 9.2 and 10.4;
 // at n = 2048, k = 4096, 64 tiles, 26 and 27).
 bool few_rows(const moe::GroupedProblem& p, int num_sms, int* nt, int* cluster) {
