@@ -290,6 +290,53 @@ moe_status moe_group_route(const void* logits, long long ld, int dtype, int T, i
                            size_t workspace_bytes, void* stream);
 size_t moe_group_route_workspace(int T, int E, int k);
 
+/* Router selection as moe_group_route, with a bias for balance, experts in groups, weights that need not be renormalised, and
+ * a factor.  For each token, with s = softmax of its logits over all E experts, or their sigmoid (`router`):
+ *   c_e = s_e + bias_e (bias [E] fp32, or NULL: none); the experts stand in `groups` equal groups, one behind the other;
+ *   a group's score is its largest c (MOE_GROUP_MAX) or the sum of its two largest (MOE_GROUP_TOP2; with one expert left, that
+ *   one's); the `keep` groups of the largest scores stay (equal ones: the lower first), and of their experts the k of the largest c
+ *   (equal ones: the lower first) are selected, in that order;
+ *   w_j = scale s_j / sum over the selected of s (renormalize), or scale s_j.  The bias chooses, it is in no weight.
+ * Comparisons are made as in 64 bits, whatever fp32 would round.  Logits of -inf and NaN, and biases of -inf and NaN, mask: such an
+ * expert is never selected and counts in no group (a masked logit not in the softmax either); +inf counts as the largest finite float.
+ * idx, weights, offsets, rows, pairs, T, E, k, ld and the workspace as moe_group_route; places [T][k] int32: where each pair stands
+ * in the sorted order (pairs[places[t][j]] = t k + j), -1 where nothing was selected; moe_combine_rows reads results by it.
+ * groups 1..32, a divisor of E; keep 1..groups; k at most keep E / groups; scale finite. */
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+typedef struct {
+    const void* logits;
+    const float* bias;
+    int *idx;
+    float* weights;
+    int *offsets, *rows, *pairs, *places;
+    long long ld;
+    int T, E, k, dtype;
+    int router;           /* moe_router: which scores */
+    int groups, keep;
+    int group_score;      /* moe_group_score */
+    int renormalize;
+    float scale;
+    void* workspace;      /* moe_group_route_workspace(T, E, k) bytes, 16-byte aligned (NULL where that is 0) */
+    size_t workspace_bytes;
+} moe_balanced_route_args;
+moe_status moe_balanced_route(const moe_balanced_route_args* a, void* stream);
+
+/* The gradient of its weights by the logits: dlogits [T][E] of out_dtype, rows ldd apart, from dweights [T][k] fp32, the logits
+ * and idx [T][k] of the call.  router, renormalize and scale as there; the choice of experts passes no gradient on, and none
+ * goes to the bias.  Every element of a row is written (0 for an expert that has no part in the weights, and for masked ones).
+ * idx outside [0, E) is no expert (its dweights is not used); a token's idx must differ from one another. */
+typedef struct {
+    const float* dweights;
+    const void* logits;
+    const int* idx;
+    void* dlogits;
+    long long ld, ldd;
+    int T, E, k, dtype, out_dtype;
+    int router, renormalize;
+    float scale;
+} moe_balanced_route_grad_args;
+moe_status moe_balanced_route_backward(const moe_balanced_route_grad_args* a, void* stream);
+
 /* out row of i = act(W_e x_i) for every sorted row i of [offsets[e], offsets[e+1]), e < groups.
  *   x [x_rows][k] bf16 or fp16 (NULL with x_rows 0), rows ldx apart; row i reads x row rows[i], or x row i with
  *   rows NULL (then m <= x_rows);
@@ -339,6 +386,33 @@ moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream);
  * MOE_GROUPED_FEW of the other calls that leave the workspace alone). */
 size_t moe_grouped_workspace(long long m, int k, int groups);
 
+/* moe_grouped_matmul of MOE_GROUP_NK weights in 8 bits: x and w hold e4m3 numbers (1 sign, 4 exponent, 3 mantissa bits, 448 at
+ * most), x_scale [x_rows] and w_scale [groups][n] fp32 what one of them stands for in each row, as moe_quantize_rows makes them:
+ *   out row of i = act(x_scale[r] w_scale[e][f] sum_k w[e][f][k] x[r][k])  for features f, r = rows[i] (or i).
+ * Sums as there, of exact products; each is multiplied by its two scales in fp32 before the activation.
+ * k, ldx, ldw and w_stride are multiples of 16, x and w 16-byte aligned, w_stride at least a matrix's extent (with one group it does not
+ * matter); other limits, offsets, row numbers and out as there.  Rows named by number need the workspace, moe_grouped8_workspace bytes
+ * (MOE_EINVAL without; 0 where the rows are so few that they are read where they are). */
+typedef struct {
+    const void* x;
+    const float* x_scale;
+    const void* w;
+    const float* w_scale;
+    const int* offsets;
+    const int* rows;      /* [m] or NULL */
+    const int* out_rows;  /* [m] or NULL */
+    void* out;
+    long long x_rows, ldx, ldw, w_stride, out_rows_n, ldo;
+    long long m;
+    int groups, n, k;
+    int out_dtype;        /* moe_dtype */
+    int act;              /* moe_group_act */
+    void* workspace;
+    size_t workspace_bytes;
+} moe_grouped8_args;
+moe_status moe_grouped_matmul8(const moe_grouped8_args* a, void* stream);
+size_t moe_grouped8_workspace(long long m, int k, int groups);
+
 /* dw[e][n][k] = sum over the sorted rows i of expert e of dy_i[n] x_i[k]: the weights' gradient
  * of moe_grouped_matmul (MOE_GROUP_NK; for MOE_GROUP_KN exchange dy and x).  Every element of dw is written,
  * zeros where a group is empty.
@@ -371,6 +445,95 @@ size_t moe_grouped_wgrad_workspace(long long m, int len);
 typedef enum { MOE_GROUPED_NONE = 0, MOE_GROUPED_FEW = 1, MOE_GROUPED_PAIR = 2, MOE_GROUPED_ANY = 3 } moe_grouped_kernel_id;
 int moe_grouped_kernel(const moe_grouped_args* a, int num_sms);
 int moe_grouped_wgrad_kernel(const moe_grouped_wgrad_args* a, int num_sms);
+int moe_grouped8_kernel(const moe_grouped8_args* a, int num_sms);
+
+/* Root-mean-square norm of T rows of H, with the residual's addition in front of it and outputs in 16 (32) and 8 bits:
+ *   h = x + residual, rounded to residual_dtype and written to sum (without a residual h = x);
+ *   rstd = 1 / sqrt(mean over the row of h^2 + eps);  y = h rstd gain (gain [H], NULL: ones);
+ *   out = y in out_dtype (or NULL);  scale[t] = max(max |y| / 448, 2^-100), out8 = y / scale[t] to the nearest e4m3 (or NULL);
+ *   rstd [T], which the gradient reads (or NULL).
+ * What is stored is what is normalised.  x, residual, gain and out each any moe_dtype; rows ldx, ld_residual, ld_sum, ldo, ldo8 apart.
+ * sum may be the residual's own memory, out x's own, in the same layout and type.  Sums are fp32, each output is rounded once; h^2 has
+ * to stay within fp32, and a row of zeros needs an eps above 0.  A NaN or infinity of x or the residual makes its row NaN (or 0 and
+ * NaN), one of the gain its column.  T >= 0, H 1..32768; 8 elements at a time where H is a multiple of 8 and rows are 16-byte
+ * aligned (out8: 8), one by one otherwise. */
+typedef struct {
+    const void* x;
+    const void* residual;
+    const void* gain;
+    void* sum;            /* with residual */
+    void* out;
+    void* out8;
+    float* scale;         /* with out8 */
+    float* rstd;
+    long long ldx, ld_residual, ld_sum, ldo, ldo8;
+    int T, H;
+    int dtype, residual_dtype, gain_dtype, out_dtype;
+    float eps;
+} moe_rms_norm_args;
+moe_status moe_rms_norm(const moe_rms_norm_args* a, void* stream);
+
+/* Its gradient: with n = h rstd, d = dy gain:
+ *   dh = rstd (d - n mean(d n)) + dsum   (dsum: what reaches the sum from behind it, or NULL), for x and the residual both;
+ *   dgain [H] = sum over the rows of dy n, fp32 (or NULL).
+ * h is the stored sum (x where there was no residual), rstd [T] the forward's.  All matrices any moe_dtype; dh may be dy's, h's or dsum's own
+ * memory in the same layout and type.  workspace: moe_rms_norm_backward_workspace(T, H) bytes with dgain, 16-byte aligned; calls
+ * that can overlap, replays of graphs among them, need one each.  With T = 0 dgain is zeros. */
+typedef struct {
+    const void* dy;
+    const void* h;
+    const float* rstd;
+    const void* gain;
+    const void* dsum;
+    void* dh;
+    float* dgain;
+    long long ld_dy, ld_h, ld_dsum, ld_dh;
+    int T, H;
+    int dy_dtype, h_dtype, gain_dtype, dsum_dtype, dh_dtype;
+    void* workspace;
+    size_t workspace_bytes;
+} moe_rms_norm_grad_args;
+moe_status moe_rms_norm_backward(const moe_rms_norm_grad_args* a, void* stream);
+size_t moe_rms_norm_backward_workspace(int T, int H);
+
+/* T rows of H in 8 bits, as moe_rms_norm makes them of y: scale[t] = max(max |x_t| / 448, 2^-100), out8 = x_t / scale[t] to the
+ * nearest e4m3.  NaN stays NaN; a row with an infinity has scale infinity and is 0, NaN where the infinity stands.  Types, limits and
+ * alignment as there. */
+moe_status moe_quantize_rows(const void* x, long long ldx, int dtype, int T, int H, void* out8, long long ldo8, float* scale, void* stream);
+
+/* The weighted sum of a token's k rows of y, where the grouped products left them:
+ *   out[t] = sum_j weights[t][j] y[places[t][j]] (+ residual[t]),   in rank order, fp32, rounded once.
+ * y [y_rows][H] of dtype; weights [T][k] fp32; places [T][k] int32 (moe_balanced_route), or NULL: row t k + j (products scattered by
+ * out_rows = pairs); residual (a shared expert's result, the residual stream; or NULL) and out [T][H] of out_dtype, out may be the
+ * residual's own memory in the same layout.  A place outside [0, y_rows) and a weight of 0 add nothing, whatever y holds there, so rows
+ * of pairs that were masked need not have been written.  T >= 0, k 1..32, T k < 2^31, H 1..2^24; any strides that keep rows apart. */
+typedef struct {
+    const void* y;
+    const float* weights;
+    const int* places;
+    const void* residual;
+    void* out;
+    long long y_rows, ldy, ld_residual, ldo;
+    int T, k, H;
+    int dtype, out_dtype;
+} moe_combine_args;
+moe_status moe_combine_rows(const moe_combine_args* a, void* stream);
+
+/* Its gradient (the residual's is dout itself): dy[places[t][j]] = weights[t][j] dout[t] in y's dtype, dweights[t][j] = <dout[t],
+ * y[places[t][j]]> fp32, 0 for a place outside y.  No two pairs may name one row; rows of dy that none names are left as they were.  dy may be
+ * y's own memory in the same layout. */
+typedef struct {
+    const void* dout;
+    const void* y;
+    const float* weights;
+    const int* places;
+    void* dy;
+    float* dweights;
+    long long y_rows, ld_dout, ldy, ld_dy;
+    int T, k, H;
+    int dout_dtype, dtype;
+} moe_combine_grad_args;
+moe_status moe_combine_rows_backward(const moe_combine_grad_args* a, void* stream);
 
 /* Which of a sequence's drafted tokens stand, and the token after them, so that what comes
  * out is distributed as the target's own samples.  For sequence b with L = lengths[b] drafts

@@ -1,5 +1,6 @@
 """Python binding of the batch operators in include/moe.h: the router's selection with rows grouped by
-expert, the 16-bit grouped products and their gradients, the verification of drafted tokens.
+expert and its gradient, the grouped products in 16 and 8 bits and their gradients, the verification of drafted tokens
+(those on rows, the norm and the weighted sum of experts' results, are in ``batch_rows``).
 
 Argument marshalling only: shapes, types and devices of the tensors are checked here (ValueError),
 everything else by the library (MoeError).  Outputs and workspaces are allocated where they are not
@@ -19,8 +20,9 @@ T_BF16, T_FP16, T_FP32 = 0, 1, 2
 GROUP_NK, GROUP_KN = 0, 1
 ACT_NONE, ACT_SWIGLU = 0, 1
 GROUPED_NONE, GROUPED_FEW, GROUPED_PAIR, GROUPED_ANY = range(4)
+GROUP_MAX, GROUP_TOP2 = 0, 1
 
-_vp, _i, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
+_vp, _i, _ll, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
 
 
 class GroupedArgs(ctypes.Structure):
@@ -37,6 +39,24 @@ class GroupedWgradArgs(ctypes.Structure):
         [("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class Grouped8Args(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("x", "x_scale", "w", "w_scale", "offsets", "rows", "out_rows", "out")] + \
+        [(n, _ll) for n in ("x_rows", "ldx", "ldw", "w_stride", "out_rows_n", "ldo", "m")] + \
+        [(n, _i) for n in ("groups", "n", "k", "out_dtype", "act")] + \
+        [("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class BalancedRouteArgs(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("logits", "bias", "idx", "weights", "offsets", "rows", "pairs", "places")] + \
+        [("ld", _ll)] + [(n, _i) for n in ("T", "E", "k", "dtype", "router", "groups", "keep", "group_score", "renormalize")] + \
+        [("scale", _f), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class BalancedRouteGradArgs(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("dweights", "logits", "idx", "dlogits")] + [("ld", _ll), ("ldd", _ll)] + \
+        [(n, _i) for n in ("T", "E", "k", "dtype", "out_dtype", "router", "renormalize")] + [("scale", _f)]
+
+
 class VerifyArgs(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("p", "q", "draft", "lengths", "u", "accepted", "tokens")] + \
         [(n, _ll) for n in ("p_seq", "p_row", "q_seq", "q_row")] + [(n, _i) for n in ("B", "D", "V", "dtype")]
@@ -45,11 +65,12 @@ class VerifyArgs(ctypes.Structure):
 def _packer(cls):
     """The structure's packed form: the same bytes as the ctypes structure, made in one call (pointers and sizes as
     unsigned numbers)."""
-    code = {_vp: "Q", _ll: "q", _i: "i", ctypes.c_size_t: "Q"}
+    code = {_vp: "Q", _ll: "q", _i: "i", _f: "f", ctypes.c_size_t: "Q"}
     return struct.Struct("@" + "".join(code[t] for _, t in cls._fields_)).pack
 
 
 _pack_matmul, _pack_wgrad, _pack_verify = _packer(GroupedArgs), _packer(GroupedWgradArgs), _packer(VerifyArgs)
+_pack_matmul8, _pack_balanced, _pack_balanced_grad = _packer(Grouped8Args), _packer(BalancedRouteArgs), _packer(BalancedRouteGradArgs)
 _calls = None
 
 
@@ -59,18 +80,25 @@ def _lib():
         L = lib()
         L.moe_group_route.argtypes = [_vp, _ll, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
         L.moe_group_route_workspace.argtypes = [_i, _i, _i]
-        L.moe_grouped_workspace.argtypes = [_ll, _i, _i]
+        L.moe_grouped_workspace.argtypes = L.moe_grouped8_workspace.argtypes = [_ll, _i, _i]
+        L.moe_rms_norm_backward_workspace.argtypes = [_i, _i]
         L.moe_grouped_wgrad_workspace.argtypes = [_ll, _i]
-        for n in ("moe_group_route_workspace", "moe_grouped_workspace", "moe_grouped_wgrad_workspace"):
+        for n in ("moe_group_route_workspace", "moe_grouped_workspace", "moe_grouped8_workspace", "moe_grouped_wgrad_workspace",
+                  "moe_rms_norm_backward_workspace"):
             getattr(L, n).restype = ctypes.c_size_t
-        for n in ("moe_grouped_matmul", "moe_grouped_wgrad", "moe_verify_draft"):
+        L.moe_quantize_rows.argtypes = [_vp, _ll, _i, _i, _i, _vp, _ll, _vp, _vp]
+        for n in ("moe_grouped_matmul", "moe_grouped_matmul8", "moe_grouped_wgrad", "moe_verify_draft", "moe_balanced_route",
+                  "moe_balanced_route_backward", "moe_rms_norm", "moe_rms_norm_backward", "moe_combine_rows",
+                  "moe_combine_rows_backward"):
             getattr(L, n).argtypes = [_vp, _vp]
         L.moe_debug_batch_wait.argtypes = [_ll]
         L.moe_debug_batch_wait.restype = _i
-        for n in ("moe_grouped_kernel", "moe_grouped_wgrad_kernel"):
+        for n in ("moe_grouped_kernel", "moe_grouped8_kernel", "moe_grouped_wgrad_kernel"):
             getattr(L, n).argtypes = [_vp, _i]
             getattr(L, n).restype = _i
-        for n in ("moe_group_route", "moe_grouped_matmul", "moe_grouped_wgrad", "moe_verify_draft"):
+        for n in ("moe_group_route", "moe_grouped_matmul", "moe_grouped_matmul8", "moe_grouped_wgrad", "moe_verify_draft",
+                  "moe_balanced_route", "moe_balanced_route_backward", "moe_rms_norm", "moe_rms_norm_backward", "moe_quantize_rows",
+                  "moe_combine_rows", "moe_combine_rows_backward"):
             getattr(L, n).restype = _i
         _calls = L
     return _calls
@@ -104,6 +132,11 @@ def _route_space(T, E, k):
 @functools.lru_cache(4096)
 def _matmul_space(m, k, groups):
     return _lib().moe_grouped_workspace(m, k, groups)
+
+
+@functools.lru_cache(4096)
+def _matmul8_space(m, k, groups):
+    return _lib().moe_grouped8_workspace(m, k, groups)
 
 
 @functools.lru_cache(4096)
@@ -212,14 +245,79 @@ def group_route(logits, k, router=ROUTER_SOFTMAX, out=None, workspace=None, stre
     return out
 
 
+def balanced_route(logits, k, bias=None, router=ROUTER_SOFTMAX, groups=1, keep=1, group_score="top2", renormalize=True, scale=1.0,
+                   out=None, workspace=None, stream=None):
+    """Router selection with a bias for balance and experts in groups (moe_balanced_route).
+
+    logits [T, E] bf16, fp16 or fp32; bias [E] fp32.  Of the `groups` equal groups of experts the `keep` best stay, by their largest
+    biased score (group_score="max") or the sum of their two largest ("top2"); of their experts the k of the largest biased
+    scores are selected.  Weights are the scores without the bias (softmax over all experts, or sigmoid), divided by their sum over the
+    selected with renormalize, times scale.  Returns (idx, weights, offsets, rows, pairs) as group_route and places [T, k] int32, each
+    pair's row in the sorted order (-1: masked), which ``combine_rows`` reads by.  out: the six tensors to write instead of new
+    ones.  workspace: as for group_route."""
+    torch, L = _start()
+    dev = _cuda(logits, "logits")
+    (T, E), stride = _dense(logits, "logits", 2, dev)
+    dt = _type(logits, "logits")
+    i32, P, TK = torch.int32, (T * k,), (T, k)
+    score = _GROUP_SCORES.get(group_score)
+    if score is None:
+        raise ValueError("group_score: 'top2' or 'max', got %r" % (group_score,))
+    if out is None:
+        if k < 1:
+            raise ValueError("k: at least 1, got %d" % k)
+        out = tuple(_new(stream, dev, (TK, i32), (TK, torch.float32), ((E + 1,), i32), (P, i32), (P, i32), (TK, i32)))
+    idx, weights, offsets, rows, pairs, places = out
+    ws, ws_bytes, _held = _space(workspace, _route_space(T, E, k), stream, dev)
+    a = _pack_balanced(
+        logits.data_ptr(), 0 if bias is None else _flat(bias, "bias", torch.float32, (E,), dev), _flat(idx, "out: idx", i32, TK, dev),
+        _flat(weights, "out: weights", torch.float32, TK, dev), _flat(offsets, "out: offsets", i32, (E + 1,), dev),
+        _flat(rows, "out: rows", i32, P, dev), _flat(pairs, "out: pairs", i32, P, dev), _flat(places, "out: places", i32, TK, dev),
+        _pitch(stride[0], T, E), T, E, k, dt, router, groups, keep, score, bool(renormalize), scale, ws, ws_bytes)
+    _run("moe_balanced_route", L.moe_balanced_route, dev, stream, a)
+    return out
+
+
+def balanced_route_backward(dweights, logits, idx, router=ROUTER_SOFTMAX, renormalize=True, scale=1.0, out=None, out_dtype=None,
+                            stream=None):
+    """The gradient of balanced_route's weights by the logits (moe_balanced_route_backward): [T, E] of the logits' type, zero
+    where an expert has no part in the weights.  dweights [T, k] fp32; idx [T, k] int32 and the rest as of that call (of
+    group_route's weights: renormalize, scale 1)."""
+    torch, L = _start()
+    dev = _cuda(logits, "logits")
+    (T, E), stride = _dense(logits, "logits", 2, dev)
+    dt = _type(logits, "logits")
+    if idx.dim() != 2:
+        raise ValueError("idx: [T, k], got %s" % (tuple(idx.shape),))
+    TK = (T, idx.shape[1])
+    if out is None:
+        out, = _new(stream, dev, ((T, E), out_dtype or logits.dtype))
+    shape, o_stride = _dense(out, "out", 2, dev)
+    if shape != (T, E) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out: %s %s, wanted %s" % (tuple(shape), out.dtype, (T, E)))
+    a = _pack_balanced_grad(
+        _flat(dweights, "dweights", torch.float32, TK, dev), logits.data_ptr(), _flat(idx, "idx", torch.int32, TK, dev), out.data_ptr(),
+        _pitch(stride[0], T, E), _pitch(o_stride[0], T, E), T, E, TK[1], dt, _type(out, "out"), router, bool(renormalize), scale)
+    _run("moe_balanced_route_backward", L.moe_balanced_route_backward, dev, stream, a)
+    return out
+
+
+_GROUP_SCORES = {"max": GROUP_MAX, "top2": GROUP_TOP2}
+
+
 def group_route_workspace(T, E, k):
-    """Bytes of workspace that group_route needs at these sizes (0 for sizes it refuses)."""
+    """Bytes of workspace that group_route and balanced_route need at these sizes (0 for sizes it refuses)."""
     return int(_lib().moe_group_route_workspace(T, E, k))
 
 
 def grouped_workspace(m, k, groups):
     """Bytes of workspace that grouped_matmul needs for m rows of length k named by number (0 where it needs none)."""
     return int(_lib().moe_grouped_workspace(m, k, groups))
+
+
+def grouped8_workspace(m, k, groups):
+    """Bytes of workspace that grouped_matmul8 needs for m rows of length k named by number (0 where it needs none)."""
+    return int(_lib().moe_grouped8_workspace(m, k, groups))
 
 
 def grouped_wgrad_workspace(m, length):
@@ -236,9 +334,11 @@ def debug_batch_wait(cycles=-1):
 
 
 def grouped_kernel(args, num_sms):
-    """The kernel (GROUPED_FEW, GROUPED_PAIR or GROUPED_ANY; GROUPED_NONE) that a call with these GroupedArgs or
+    """The kernel (GROUPED_FEW, GROUPED_PAIR or GROUPED_ANY; GROUPED_NONE) that a call with these GroupedArgs, Grouped8Args or
     GroupedWgradArgs takes on a device of that many SMs; host code, no device."""
-    call = _lib().moe_grouped_kernel if isinstance(args, GroupedArgs) else _lib().moe_grouped_wgrad_kernel
+    L = _lib()
+    call = L.moe_grouped_kernel if isinstance(args, GroupedArgs) else \
+        L.moe_grouped8_kernel if isinstance(args, Grouped8Args) else L.moe_grouped_wgrad_kernel
     return call(ctypes.byref(args), num_sms)
 
 
@@ -292,6 +392,48 @@ def grouped_matmul(x, w, offsets, rows=None, out_rows=None, w_layout="nk", act=N
             ldw, w_stride[0] if E > 1 else 0, N, _pitch(o_stride[0], N, n_out), m, E, n, k, dt, _type(out, "out"), layout, act, ws,
             ws_bytes)
         _run("moe_grouped_matmul", L.moe_grouped_matmul, dev, stream, a)
+    return out
+
+
+def grouped_matmul8(x, x_scale, w, w_scale, offsets, rows=None, out_rows=None, act=None, out=None, out_dtype=None, stream=None,
+                    workspace=None):
+    """The products of ragged groups of rows with their experts' weights, both in 8 bits (moe_grouped_matmul8).
+
+    x [R, k] and w [E, n, k] float8_e4m3fn, k a multiple of 16; x_scale [R] and w_scale [E, n] fp32: what a number of the row stands
+    for (``rms_norm``, ``quantize_rows``).  The rest as grouped_matmul with w_layout "nk"; out_dtype is bf16 unless given.
+    workspace (with rows): uint8 device memory of grouped8_workspace(m, k, E) bytes; new memory without it."""
+    torch, L = _start()
+    dev = _cuda(x, "x")
+    (R, k), x_stride = _dense(x, "x", 2, dev)
+    (E, n, kw), w_stride = _dense(w, "w", 3, dev)
+    if x.dtype is not torch.float8_e4m3fn or w.dtype is not torch.float8_e4m3fn:
+        raise ValueError("x, w: float8_e4m3fn is wanted, got %s and %s" % (x.dtype, w.dtype))
+    if kw != k:
+        raise ValueError("x has %d columns, w takes %d" % (k, kw))
+    if act is None:
+        n_out, act = n, ACT_NONE
+    elif act == "swiglu":
+        n_out, act = n // 2, ACT_SWIGLU
+    else:
+        raise ValueError("act: None or 'swiglu', got %r" % (act,))
+    i32, f32 = torch.int32, torch.float32
+    m = rows.shape[0] if rows is not None else out_rows.shape[0] if out_rows is not None else R
+    if out is None:
+        out, = _new(stream, dev, ((m, n_out), out_dtype or torch.bfloat16))
+    (N, cols), o_stride = _dense(out, "out", 2, dev)
+    if cols != n_out or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out: %s %s, wanted %d columns" % (tuple(out.shape), out.dtype, n_out))
+    ws = ws_bytes = rows_at = 0
+    if rows is not None:
+        rows_at = _flat(rows, "rows", i32, (m,), dev)
+        ws, ws_bytes, _held = _space(workspace, 0 if workspace is not None else _matmul8_space(m, k, E), stream, dev)
+    if m:
+        a = _pack_matmul8(
+            x.data_ptr(), _flat(x_scale, "x_scale", f32, (R,), dev), w.data_ptr(), _flat(w_scale, "w_scale", f32, (E, n), dev),
+            _flat(offsets, "offsets", i32, (E + 1,), dev), rows_at, 0 if out_rows is None else _flat(out_rows, "out_rows", i32, (m,), dev),
+            out.data_ptr(), R, _pitch(x_stride[0], R, k), _pitch(w_stride[1], n, k), w_stride[0] if E > 1 else 0, N,
+            _pitch(o_stride[0], N, n_out), m, E, n, k, _type(out, "out"), act, ws, ws_bytes)
+        _run("moe_grouped_matmul8", L.moe_grouped_matmul8, dev, stream, a)
     return out
 
 

@@ -1,6 +1,6 @@
-// batch.cu - entry points of the batch operators (moe_group_route, moe_grouped_matmul,
-// moe_grouped_wgrad, moe_verify_draft): argument checks, then one launcher each.
-#include "../../include/moe.h"
+// batch.cu - entry points of the batch operators' routing, products and verification (moe_group_route, moe_balanced_route,
+// moe_grouped_matmul, moe_grouped_matmul8, moe_grouped_wgrad, moe_verify_draft): argument checks, then one launcher each.
+#include "batch.h"
 #include "group_route.h"
 #include "grouped.h"
 #include "verify.h"
@@ -16,8 +16,6 @@
 
 namespace {
 
-// What a device needs once: kernel attributes, its SM count, and the host-visible word that a kernel whose wait ran
-// out sets.  Made by the first call on the device, kept for the life of the process.
 struct Device {
   int num_sms;
   uint32_t* status;                 // as the device sees it
@@ -80,26 +78,17 @@ moe_status current_device(Device** out) {
   return *(*out)->host_status ? MOE_ETIMEOUT : MOE_OK;
 }
 
-bool is_dtype(int t, bool fp32) { return t == MOE_T_BF16 || t == MOE_T_FP16 || (fp32 && t == MOE_T_FP32); }
-size_t dtype_bytes(int t) { return t == MOE_T_FP32 ? 4 : 2; }
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-// rows of `len` elements `ld` apart that do not overlap, all of them within 2^62 bytes
-bool rows_fit(long long rows, long long ld, long long len) {
-  return rows >= 0 && ld >= len && ld < (1ll << 40) && (rows == 0 || ld <= (1ll << 60) / rows);
-}
+using moe::aligned;
+using moe::done;
+using moe::dtype_bytes;
+using moe::is_dtype;
+using moe::rows_fit;
 
 // `rows` rows of `len` elements in each of B sequences, none on another: one sequence behind the other, or the sequences' first
 // rows, then their second ones, and so on
 bool sequences_fit(int B, long long seq, int rows, long long row, int len) {
   if (!rows_fit(rows, row, len)) return false;
   return B == 1 || rows_fit(B, seq, (rows - 1) * row + len) || (rows_fit(B, seq, len) && rows_fit(rows, row, (B - 1) * seq + len));
-}
-
-moe_status done(cudaError_t e) {
-  if (e == cudaSuccess) return MOE_OK;
-  cudaGetLastError();
-  return MOE_ECUDA;
 }
 
 constexpr long long kMaxRows = 1ll << 30;
@@ -132,20 +121,23 @@ int few_rows_tile(long long m, int groups) {
 bool few_rows(const moe::GroupedProblem& p, int num_sms, int* nt, int* cluster) {
   *nt = few_rows_tile(p.m, p.groups);
   const int n_out = p.swiglu ? p.n / 2 : p.n, width = p.swiglu ? 128 : 256;
+  const int k = p.eight ? p.k / 2 : p.k;   // the rules count a row's bytes
   const long long pair_tiles = (p.m / 256 + (p.m < p.groups ? p.m : p.groups)) * ((n_out + width - 1) / width);
   const double reached = p.groups * (1 - std::pow(1 - 1.0 / p.groups, (double)p.m));
   auto tiles_of = [&](int rows) { return (reached + p.m / rows) * std::ceil(n_out / (width / 2.0)); };
-  if (!*nt && (pair_tiles <= num_sms / 6 || (p.k <= 2048 && tiles_of(32) <= 2 * num_sms))) *nt = 32;
-  if (!*nt && pair_tiles <= num_sms / 4 && p.k >= 4096 && p.m <= 48ll * p.groups) *nt = 64;
+  if (!*nt && (pair_tiles <= num_sms / 6 || (k <= 2048 && tiles_of(32) <= 2 * num_sms))) *nt = 32;
+  if (!*nt && pair_tiles <= num_sms / 4 && k >= 4096 && p.m <= 48ll * p.groups) *nt = 64;
   if (!*nt) return false;
   const double tiles = tiles_of(*nt);
   *cluster = 1;
   const double most = (few_rows_tile(p.m, p.groups) ? 1.5 : 1.0) * num_sms;
-  while (*cluster < 8 && tiles * *cluster < most && p.k / (2 * *cluster) >= 512) *cluster *= 2;
+  while (*cluster < 8 && tiles * *cluster < most && k / (2 * *cluster) >= 512) *cluster *= 2;
   return true;
 }
 
 size_t row_copy_bytes(long long m, int len) { return (size_t)m * ((len + 7) / 8 * 8) * 2; }
+// rows of 8 bits, a multiple of 16, as half as many elements of 16
+size_t row_copy_bytes_8(long long m, int k) { return row_copy_bytes(m, k / 2); }
 
 // Where an operand's rows are named by number: copies them into ws (m rows), and makes the operand the copy.
 struct Operand {
@@ -153,14 +145,15 @@ struct Operand {
   const int** rows;
   long long *nrows, *ld;
   int len;
+  int per;   // elements in 16 bits
 };
 cudaError_t copy_operand(const Operand& o, const moe::GroupedProblem& p, uint16_t* ws, int num_sms, cudaStream_t s) {
-  const int ld = (o.len + 7) / 8 * 8;
-  const moe::RowCopy c{*o.base, ws, *o.rows, p.offsets, *o.nrows, *o.ld, p.m, p.groups, o.len, ld};
+  const int len = o.len / o.per, ld = (len + 7) / 8 * 8;
+  const moe::RowCopy c{*o.base, ws, *o.rows, p.offsets, *o.nrows, *o.ld / o.per, p.m, p.groups, len, ld};
   *o.base = ws;
   *o.rows = nullptr;
   *o.nrows = p.m;
-  *o.ld = ld;
+  *o.ld = (long long)ld * o.per;
   return moe::launch_copy_rows(c, num_sms, s);
 }
 
@@ -172,7 +165,8 @@ struct Plan {
   size_t need_a, need_b;   // bytes of the copies that the pair kernel takes
 };
 Plan plan_product(const moe::GroupedProblem& p, bool wgrad, int num_sms, size_t workspace_bytes) {
-  Plan pl{MOE_GROUPED_ANY, 0, 0, p.a_rows ? row_copy_bytes(p.m, wgrad ? p.n : p.k) : 0, p.b_rows ? row_copy_bytes(p.m, p.k) : 0};
+  Plan pl{p.eight ? MOE_GROUPED_NONE : MOE_GROUPED_ANY, 0, 0, 0, p.b_rows ? row_copy_bytes(p.m, p.k) : 0};
+  if (p.a_rows) pl.need_a = p.eight ? row_copy_bytes_8(p.m, p.k) : row_copy_bytes(p.m, wgrad ? p.n : p.k);
   if (!wgrad && few_rows(p, num_sms, &pl.nt, &pl.cluster) && moe::grouped_maps(p, false, true, nullptr))
     pl.kernel = MOE_GROUPED_FEW;
   // (the copies lie no worse than the operands)
@@ -185,8 +179,8 @@ moe_status run_product(moe::GroupedProblem p, bool wgrad, void* workspace, size_
   Device* d;
   const moe_status st = current_device(&d);
   if (st != MOE_OK) return st;
-  const Operand a{&p.a, &p.a_rows, &p.a_nrows, &p.lda, wgrad ? p.n : p.k};
-  const Operand b{&p.b, &p.b_rows, &p.b_nrows, &p.ldb, p.k};
+  const Operand a{&p.a, &p.a_rows, &p.a_nrows, &p.lda, wgrad ? p.n : p.k, p.eight ? 2 : 1};
+  const Operand b{&p.b, &p.b_rows, &p.b_nrows, &p.ldb, p.k, 1};
   const Plan pl = plan_product(p, wgrad, d->num_sms, workspace_bytes);
   cudaError_t e = cudaSuccess;
   if (pl.kernel == MOE_GROUPED_FEW && moe::launch_grouped_few(p, pl.nt, pl.cluster, d->wait(), s, &e)) return done(e);
@@ -197,10 +191,18 @@ moe_status run_product(moe::GroupedProblem p, bool wgrad, void* workspace, size_
     if (e != cudaSuccess) return done(e);
     if (moe::launch_grouped_pair(p, wgrad, d->num_sms, d->wait(), s, &e)) return done(e);
   }
-  return done(moe::launch_grouped_any(p, wgrad, d->wait(), s));
+  // (8 bits: rows that the tensor maps cannot address, or named by number without a workspace)
+  return p.eight ? MOE_EINVAL : done(moe::launch_grouped_any(p, wgrad, d->wait(), s));
 }
 
 }  // namespace
+
+moe_status moe::batch_device(BatchDevice* out) {
+  Device* d;
+  const moe_status st = current_device(&d);
+  if (st == MOE_OK) *out = {d->num_sms, d->wait()};
+  return st;
+}
 
 extern "C" size_t moe_group_route_workspace(int T, int E, int k) {
   if (T < 1 || E < 1 || E > 1024 || k < 1 || k > E || k > 32 || (long long)T * k > 0x7fffffffLL) return 0;
@@ -219,17 +221,71 @@ extern "C" moe_status moe_group_route(const void* logits, long long ld, int dtyp
     return MOE_EINVAL;
   const moe::GroupRoutePlan plan = moe::group_route_plan(T, E, k);
   if (plan.workspace && (!workspace || workspace_bytes < plan.workspace)) return MOE_EINVAL;
-  moe::GroupRouteArgs a{logits, ld, dtype, T, E, k, router, idx, weights, offsets, rows, pairs,
-                        static_cast<int*>(workspace), plan.blocks, plan.per_block};
+  const moe::GroupRouteArgs a{logits, ld, dtype, T, E, k, router, idx, weights, offsets, rows, pairs,
+                              static_cast<int*>(workspace), plan.blocks, plan.per_block};
   Device* d;
   const moe_status st = current_device(&d);
   if (st != MOE_OK) return st;
   return done(moe::launch_group_route(a, (cudaStream_t)stream));
 }
 
+extern "C" moe_status moe_balanced_route(const moe_balanced_route_args* a, void* stream) {
+  if (!a || !a->logits || !a->idx || !a->weights || !a->offsets || !a->rows || !a->pairs || !a->places) return MOE_EINVAL;
+  const int T = a->T, E = a->E, k = a->k;
+  if (!is_dtype(a->dtype, true) || T < 1 || E < 1 || E > 1024 || k < 1 || k > E || k > 32) return MOE_EINVAL;
+  if ((long long)T * k > 0x7fffffffLL || !rows_fit(T, a->ld, E)) return MOE_EINVAL;
+  if (a->router != MOE_ROUTER_SOFTMAX_TOPK_RENORM && a->router != MOE_ROUTER_SIGMOID_TOPK_NORM) return MOE_EINVAL;
+  if (a->groups < 1 || a->groups > 32 || E % a->groups || a->keep < 1 || a->keep > a->groups || k > a->keep * (E / a->groups) ||
+      (a->group_score != MOE_GROUP_MAX && a->group_score != MOE_GROUP_TOP2) || !(std::fabs(a->scale) <= 3e38f))
+    return MOE_EINVAL;
+  if (!aligned(a->logits, dtype_bytes(a->dtype)) || !aligned(a->bias, 4) || !aligned(a->idx, 4) || !aligned(a->weights, 4) ||
+      !aligned(a->offsets, 4) || !aligned(a->rows, 4) || !aligned(a->pairs, 4) || !aligned(a->places, 4) || !aligned(a->workspace, 16))
+    return MOE_EINVAL;
+  const moe::GroupRoutePlan plan = moe::group_route_plan(T, E, k);
+  if (plan.workspace && (!a->workspace || a->workspace_bytes < plan.workspace)) return MOE_EINVAL;
+  moe::GroupRouteArgs r{a->logits, a->ld, a->dtype, T, E, k, a->router, a->idx, a->weights, a->offsets, a->rows, a->pairs,
+                        static_cast<int*>(a->workspace), plan.blocks, plan.per_block};
+  r.balanced = true;
+  r.top2 = a->group_score == MOE_GROUP_TOP2;
+  r.renorm = a->renormalize != 0;
+  r.bias = a->bias;
+  r.groups = a->groups;
+  r.keep = a->keep;
+  r.factor = a->scale;
+  r.places = a->places;
+  Device* d;
+  const moe_status st = current_device(&d);
+  if (st != MOE_OK) return st;
+  return done(moe::launch_group_route(r, (cudaStream_t)stream));
+}
+
+extern "C" moe_status moe_balanced_route_backward(const moe_balanced_route_grad_args* a, void* stream) {
+  if (!a || !a->dweights || !a->logits || !a->idx || !a->dlogits) return MOE_EINVAL;
+  const int T = a->T, E = a->E, k = a->k;
+  if (!is_dtype(a->dtype, true) || !is_dtype(a->out_dtype, true) || T < 1 || E < 1 || E > 1024 || k < 1 || k > E || k > 32)
+    return MOE_EINVAL;
+  if ((long long)T * k > 0x7fffffffLL || !rows_fit(T, a->ld, E) || !rows_fit(T, a->ldd, E)) return MOE_EINVAL;
+  if ((a->router != MOE_ROUTER_SOFTMAX_TOPK_RENORM && a->router != MOE_ROUTER_SIGMOID_TOPK_NORM) || !(std::fabs(a->scale) <= 3e38f))
+    return MOE_EINVAL;
+  if (!aligned(a->logits, dtype_bytes(a->dtype)) || !aligned(a->dlogits, dtype_bytes(a->out_dtype)) || !aligned(a->dweights, 4) ||
+      !aligned(a->idx, 4))
+    return MOE_EINVAL;
+  const moe::RouteGradArgs r{a->dweights, a->logits, a->idx, a->dlogits, a->ld, a->ldd, a->dtype, a->out_dtype, T, E, k, a->router,
+                             a->renormalize != 0, a->scale};
+  Device* d;
+  const moe_status st = current_device(&d);
+  if (st != MOE_OK) return st;
+  return done(moe::launch_route_grad(r, (cudaStream_t)stream));
+}
+
 extern "C" size_t moe_grouped_workspace(long long m, int k, int groups) {
   if (m < 0 || m > kMaxRows || k < 1 || k > kMaxDim || groups < 1 || groups > 1024) return 0;
   return few_rows_tile(m, groups) ? 0 : row_copy_bytes(m, k);
+}
+
+extern "C" size_t moe_grouped8_workspace(long long m, int k, int groups) {
+  if (m < 0 || m > kMaxRows || k < 1 || k > kMaxDim || k % 16 || groups < 1 || groups > 1024) return 0;
+  return few_rows_tile(m, groups) ? 0 : row_copy_bytes_8(m, k);
 }
 
 extern "C" size_t moe_grouped_wgrad_workspace(long long m, int len) {
@@ -279,6 +335,50 @@ moe_status matmul_problem(const moe_grouped_args* a, moe::GroupedProblem* out) {
   return MOE_OK;
 }
 
+moe_status matmul8_problem(const moe_grouped8_args* a, moe::GroupedProblem* out) {
+  if (!a || (!a->x && a->x_rows != 0) || (!a->x_scale && a->x_rows != 0) || !a->w || !a->w_scale || !a->offsets || !a->out)
+    return MOE_EINVAL;
+  if (!product_ok(a->groups, a->m, a->n, a->k, MOE_T_BF16, a->out_dtype)) return MOE_EINVAL;
+  if (a->act != MOE_ACT_NONE && a->act != MOE_ACT_SWIGLU) return MOE_EINVAL;
+  const bool sw = a->act == MOE_ACT_SWIGLU;
+  if (sw && a->n % 2) return MOE_EINVAL;
+  if (a->k % 16 || a->ldx % 16 || a->ldw % 16 || !rows_fit(a->x_rows, a->ldx, a->k) || !rows_fit(a->n, a->ldw, a->k) ||
+      !rows_fit(a->out_rows_n, a->ldo, sw ? a->n / 2 : a->n))
+    return MOE_EINVAL;
+  if (a->groups > 1 && (a->w_stride % 16 || a->w_stride < (a->n - 1) * a->ldw + a->k || a->w_stride >= (1ll << 40))) return MOE_EINVAL;
+  if ((!a->rows && a->m > a->x_rows) || (!a->out_rows && a->m > a->out_rows_n)) return MOE_EINVAL;
+  if (!aligned(a->x, 16) || !aligned(a->w, 16) || !aligned(a->x_scale, 4) || !aligned(a->w_scale, 4) ||
+      !aligned(a->out, dtype_bytes(a->out_dtype)) || !aligned(a->offsets, 4) || !aligned(a->rows, 4) || !aligned(a->out_rows, 4) ||
+      !aligned(a->workspace, 16) || (!a->workspace && a->workspace_bytes))
+    return MOE_EINVAL;
+  moe::GroupedProblem& p = *out;
+  p = {};
+  p.a = static_cast<const uint16_t*>(a->x);
+  p.b = static_cast<const uint16_t*>(a->w);
+  p.d = a->out;
+  p.offsets = a->offsets;
+  p.a_rows = a->rows;
+  p.d_rows = a->out_rows;
+  p.a_nrows = a->x_rows;
+  p.lda = a->ldx;
+  p.ldb = a->ldw;
+  p.b_stride = a->w_stride;
+  p.d_nrows = a->out_rows_n;
+  p.ldd = a->ldo;
+  p.m = a->m;
+  p.groups = a->groups;
+  p.n = a->n;
+  p.k = a->k;
+  p.out_dtype = a->out_dtype;
+  p.swiglu = sw;
+  p.eight = 1;
+  p.a_scale = a->x_scale;
+  p.b_scale = a->w_scale;
+  p.scale_rows = a->rows;
+  p.scale_nrows = a->x_rows;
+  return MOE_OK;
+}
+
 moe_status wgrad_problem(const moe_grouped_wgrad_args* a, moe::GroupedProblem* out) {
   if (!a || !a->offsets || !a->dw) return MOE_EINVAL;
   if (a->m != 0 && ((!a->dy && a->dy_rows_n != 0) || (!a->x && a->x_rows_n != 0))) return MOE_EINVAL;
@@ -321,6 +421,19 @@ extern "C" moe_status moe_grouped_matmul(const moe_grouped_args* a, void* stream
   const moe_status st = matmul_problem(a, &p);
   if (st != MOE_OK || p.m == 0) return st;
   return run_product(p, false, a->workspace, a->workspace_bytes, (cudaStream_t)stream);
+}
+
+extern "C" moe_status moe_grouped_matmul8(const moe_grouped8_args* a, void* stream) {
+  moe::GroupedProblem p;
+  const moe_status st = matmul8_problem(a, &p);
+  if (st != MOE_OK || p.m == 0) return st;
+  return run_product(p, false, a->workspace, a->workspace_bytes, (cudaStream_t)stream);
+}
+
+extern "C" int moe_grouped8_kernel(const moe_grouped8_args* a, int num_sms) {
+  moe::GroupedProblem p;
+  return matmul8_problem(a, &p) != MOE_OK || p.m == 0 || num_sms < 1 ? MOE_GROUPED_NONE
+                                                                     : plan_product(p, false, num_sms, a->workspace_bytes).kernel;
 }
 
 extern "C" moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, void* stream) {

@@ -1,0 +1,217 @@
+// combine_rows.cu - the weighted sum of a token's expert results, where the grouped products left them, and its gradient.
+//
+//   out[t] = sum_j weights[t][j] y[places[t][j]]  (+ residual[t])      in rank order, fp32, rounded once
+//   dy[places[t][j]] = weights[t][j] dout[t],   dweights[t][j] = <dout[t], y[places[t][j]]>
+//
+// The rows are named by where they stand, so the products can leave them by expert (a scattering product takes up to 15% longer)
+// and no copy puts them in order.  A place outside y is no row: it adds nothing, and its weight's gradient is 0; a weight of 0
+// reads no row, as that of a masked pair was never written.  Bound: memory; a
+// thread has eight rows' words in flight.
+#include "combine_rows.h"
+#include "rows_io.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int CR_THREADS = 256;
+constexpr int CR_RANKS = 8;    // rows in flight
+constexpr int CR_MAX_K = 32;
+
+// The token's rows and weights into shared memory: offsets in elements, -1 for none.
+__device__ __forceinline__ void token_rows(const float* weights, const int* places, long long t, int k, long long y_rows, long long ld,
+                                           bool skip_zero, long long* off, float* w) {
+  if (threadIdx.x < k) {
+    const long long i = t * k + threadIdx.x, r = places ? __ldg(places + i) : i;
+    const float weight = __ldg(weights + i);
+    const bool in = r >= 0 && r < y_rows && (weight != 0.f || !skip_zero);
+    off[threadIdx.x] = in ? r * ld : -1;
+    w[threadIdx.x] = weight;
+  }
+  __syncthreads();
+}
+
+// chunk c (VEC) or element c of a row at `off` elements, as fp32
+template <bool VEC>
+__device__ __forceinline__ void load_word(const void* p, long long off, int c, int type, float (&v)[VEC ? CHUNK : 1]) {
+  if (!VEC) {
+    v[0] = one_value(p, off + c, type);
+  } else if (type == GT_FP32) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + off) + 2 * c;
+    const float4 a = __ldcs(s), b = __ldcs(s + 1);
+    const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < (VEC ? CHUNK : 1); ++i) v[i] = f[i];
+  } else {
+    const uint4 r = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + off) + c);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < (VEC ? CHUNK : 1); ++i) {
+      const float2 f = two_16(w[i / 2], type);
+      v[i] = i % 2 ? f.y : f.x;
+    }
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_word(void* p, long long off, int c, int type, const float (&v)[VEC ? CHUNK : 1]) {
+  if constexpr (!VEC) {
+    put_value(p, off + c, type, v[0]);
+  } else if (type == GT_FP32) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + off) + 2 * c;
+    d[0] = make_float4(v[0], v[1], v[2], v[3]);
+    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + off)[c] =
+        make_uint4(pack_16(v[0], v[1], type), pack_16(v[2], v[3], type), pack_16(v[4], v[5], type), pack_16(v[6], v[7], type));
+  }
+}
+
+// A block: a token, and one of gridDim.y runs of its columns.
+template <bool VEC, int YT>
+__global__ void __launch_bounds__(CR_THREADS) combine_rows_kernel(const CombineRowsArgs a) {
+  constexpr int N = VEC ? CHUNK : 1;
+  __shared__ long long off[CR_MAX_K];
+  __shared__ float weight[CR_MAX_K];
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long t = blockIdx.x;
+  token_rows(a.weights, a.places, t, a.k, a.y_rows, a.ldy, true, off, weight);
+  const int words = a.H / N;
+  for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < words; c += gridDim.y * blockDim.x) {
+    float sum[N], r[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum[i] = r[i] = 0.f;
+    if (a.residual) load_word<VEC>(a.residual, t * a.ld_res, c, a.out_type, r);
+    for (int j0 = 0; j0 < a.k; j0 += CR_RANKS) {
+      float v[CR_RANKS][N];
+#pragma unroll
+      for (int j = 0; j < CR_RANKS; ++j) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[j][i] = 0.f;
+        if (j0 + j < a.k && off[j0 + j] >= 0) load_word<VEC>(a.y, off[j0 + j], c, YT, v[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < CR_RANKS; ++j) {
+        const float w = j0 + j < a.k && off[j0 + j] >= 0 ? weight[j0 + j] : 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum[i] = fmaf(w, v[j][i], sum[i]);
+      }
+    }
+    if (a.residual) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum[i] += r[i];
+    }
+    store_word<VEC>(a.out, t * a.ldo, c, a.out_type, sum);
+  }
+}
+
+// A block: a token, as the weights' gradients are sums over all of its columns.
+template <bool VEC, int YT>
+__global__ void __launch_bounds__(1024) combine_grad_kernel(const CombineGradArgs a) {
+  constexpr int N = VEC ? CHUNK : 1;
+  __shared__ long long off[CR_MAX_K];
+  __shared__ float weight[CR_MAX_K];
+  __shared__ float part[32][CR_MAX_K];
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long t = blockIdx.x;
+  token_rows(a.weights, a.places, t, a.k, a.y_rows, 1, false, off, weight);
+  const int words = a.H / N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int j0 = 0; j0 < a.k; j0 += CR_RANKS) {
+    float dot[CR_RANKS];
+#pragma unroll
+    for (int j = 0; j < CR_RANKS; ++j) dot[j] = 0.f;
+    for (int c = threadIdx.x; c < words; c += blockDim.x) {
+      float d[N], v[CR_RANKS][N];
+      load_word<VEC>(a.dout, t * a.ld_dout, c, a.dout_type, d);
+#pragma unroll
+      for (int j = 0; j < CR_RANKS; ++j) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[j][i] = 0.f;
+        if (j0 + j < a.k && off[j0 + j] >= 0) load_word<VEC>(a.y, off[j0 + j] * a.ldy, c, YT, v[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < CR_RANKS; ++j) {
+        if (j0 + j < a.k && off[j0 + j] >= 0) {
+          const float w = weight[j0 + j];
+          float o[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            dot[j] = fmaf(d[i], v[j][i], dot[j]);
+            o[i] = w * d[i];
+          }
+          store_word<VEC>(a.dy, off[j0 + j] * a.ld_dy, c, a.dy_type, o);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < CR_RANKS; ++j) {
+      if (j0 + j >= a.k) break;
+      const float s = warp_sum(dot[j]);
+      if (lane == 0) part[warp][j0 + j] = s;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < a.k) {   // the warps' sums in order
+    float s = 0.f;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += part[w][threadIdx.x];
+    a.dweights[t * a.k + threadIdx.x] = s;
+  }
+}
+
+template <typename A>
+cudaError_t launch(void (*kernel)(A), dim3 grid, int threads, cudaStream_t s, const A& a) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, a);
+}
+
+bool chunks(const void* p, long long ld, int type) {
+  return !p || ((uintptr_t)p % 16 == 0 && ld * (type == GT_FP32 ? 4 : 2) % 16 == 0);
+}
+int warps_of(long long words, int most) {
+  const long long t = (words + 31) / 32 * 32;
+  return t < most ? (int)t : most;
+}
+
+}  // namespace
+
+cudaError_t launch_combine_rows(const CombineRowsArgs& a, cudaStream_t s) {
+  const bool vec = a.H % CHUNK == 0 && chunks(a.y, a.ldy, a.y_type) && chunks(a.residual, a.ld_res, a.out_type) &&
+                   chunks(a.out, a.ldo, a.out_type);
+  const long long words = vec ? a.H / CHUNK : a.H;
+  long long runs = (words + CR_THREADS - 1) / CR_THREADS;
+  const int threads = warps_of((words + runs - 1) / runs, CR_THREADS);   // even runs
+  if (runs > 65535) runs = 65535;
+  const dim3 grid((unsigned)a.T, (unsigned)runs);
+  auto go = [&](auto v) {
+    constexpr bool V = decltype(v)::value;
+    if (a.y_type == GT_FP32) return launch(combine_rows_kernel<V, GT_FP32>, grid, threads, s, a);
+    return a.y_type == GT_BF16 ? launch(combine_rows_kernel<V, GT_BF16>, grid, threads, s, a)
+                               : launch(combine_rows_kernel<V, GT_FP16>, grid, threads, s, a);
+  };
+  return vec ? go(std::true_type{}) : go(std::false_type{});
+}
+
+cudaError_t launch_combine_rows_grad(const CombineGradArgs& a, cudaStream_t s) {
+  const bool vec = a.H % CHUNK == 0 && chunks(a.dout, a.ld_dout, a.dout_type) && chunks(a.y, a.ldy, a.y_type) &&
+                   chunks(a.dy, a.ld_dy, a.dy_type);
+  const int threads = warps_of(vec ? a.H / CHUNK : a.H, a.T <= 304 ? 1024 : 512);
+  const dim3 grid((unsigned)a.T);
+  auto go = [&](auto v) {
+    constexpr bool V = decltype(v)::value;
+    if (a.y_type == GT_FP32) return launch(combine_grad_kernel<V, GT_FP32>, grid, threads, s, a);
+    return a.y_type == GT_BF16 ? launch(combine_grad_kernel<V, GT_BF16>, grid, threads, s, a)
+                               : launch(combine_grad_kernel<V, GT_FP16>, grid, threads, s, a);
+  };
+  return vec ? go(std::true_type{}) : go(std::false_type{});
+}
+
+}  // namespace moe

@@ -8,6 +8,7 @@
 // the second waiting for the first on the device.  Bound: issue while selecting (about 350 instructions a token, 2.4 us for
 // 32 tokens an SM), latency while placing: 16384 tokens of 256 bf16 logits, k = 8, take 19.6 us (10 MB, 1.5 us at the
 // memory's rate), of which 8 are two launches' of any size; one token 4.8 us.
+#include "balanced_select.cuh"
 #include "common.cuh"
 #include "group_route.h"
 #include "grouped.h"
@@ -25,17 +26,6 @@ constexpr int GR_WARPS = GR_THREADS / 32;
 constexpr int one_launch(int E) { return E <= 512 ? 512 : 256; }
 constexpr int GR_CLUSTER = 2;         // blocks that add up their counts before they leave (4 do not fill every SM: 33 us, not 20)
 constexpr int GR_COUNTS = 16384;      // counts by warp and expert that a block holds
-
-__device__ __forceinline__ float load_logit(const void* p, long long i, int dtype) {
-  if (dtype == GT_FP32) return __ldg(static_cast<const float*>(p) + i);
-  const uint16_t b = __ldg(static_cast<const uint16_t*>(p) + i);
-  return dtype == GT_BF16 ? bf16_bits_to_float(b) : __half2float(__ushort_as_half(b));
-}
-
-__device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : fminf(x, 3.402823466e38f); }
-__device__ __forceinline__ float logit_of(const GroupRouteArgs& a, long long t, int e) {
-  return clean(load_logit(a.logits, t * a.ld + e, a.dtype));
-}
 
 // Lane l's logits of token t: experts l + 32 i.  The loads of each type stand together: a branch around each would run them
 // one after another.
@@ -226,19 +216,52 @@ __device__ __forceinline__ void route_tokens(const GroupRouteArgs& a, long long 
   }
 }
 
-// this block's tokens; and its pairs by expert into hist (shared)
+// the same of one token for the balanced selection
 template <int NV>
+__device__ __forceinline__ void route_balanced(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane, int* hist) {
+  float l[NV];
+  load_token<NV>(a, t, lane, l);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const uint32_t raw = __float_as_uint(l[i]);
+    if (a.dtype == GT_BF16) l[i] = __uint_as_float(raw << 16);
+    else if (a.dtype == GT_FP16) l[i] = __half2float(__ushort_as_half((unsigned short)raw));
+    l[i] = lane + 32 * i < a.E ? clean(l[i]) : -INFINITY;
+  }
+  int e;
+  float w;
+  balanced_token<NV>(a, tab, t, lane, l, e, w);
+  if (lane < a.k) {
+    a.idx[t * a.k + lane] = e;
+    a.weights[t * a.k + lane] = e >= 0 ? w : 0.f;
+    if (e >= 0) atomicAdd(&hist[e], 1);   // a count: its order does not matter
+  }
+}
+
+// in kernels of the balanced selection alone
+__device__ __forceinline__ BalancedTables& tables() {
+  __shared__ BalancedTables t;
+  return t;
+}
+
+// this block's tokens; and its pairs by expert into hist (shared)
+template <int NV, bool BAL>
 __device__ __forceinline__ void select_tokens(const GroupRouteArgs& a, int* hist) {
-  constexpr int U = NV <= 8 ? 2 : 1;
+  constexpr int U = !BAL && NV <= 8 ? 2 : 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int e = threadIdx.x; e < a.E; e += GR_THREADS) hist[e] = 0;
+  if constexpr (BAL) balanced_tables(a, tables());
   __syncthreads();
   const long long t0 = min((long long)blockIdx.x * a.per_block, (long long)a.T), t1 = min(t0 + a.per_block, (long long)a.T);
-  for (long long t = t0 + warp; t < t1; t += U * GR_WARPS) {
-    float l[U][NV];
+  if constexpr (BAL) {
+    for (long long t = t0 + warp; t < t1; t += GR_WARPS) route_balanced<NV>(a, tables(), t, lane, hist);
+  } else {
+    for (long long t = t0 + warp; t < t1; t += U * GR_WARPS) {
+      float l[U][NV];
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_token<NV>(a, min(t + u * GR_WARPS, t1 - 1), lane, l[u]);
-    route_tokens<NV, U>(a, t, t1, lane, l, hist);
+      for (int u = 0; u < U; ++u) load_token<NV>(a, min(t + u * GR_WARPS, t1 - 1), lane, l[u]);
+      route_tokens<NV, U>(a, t, t1, lane, l, hist);
+    }
   }
   __syncthreads();
 }
@@ -270,6 +293,7 @@ __device__ __forceinline__ void count_pairs(const GroupRouteArgs& a, const Pairs
   }
 }
 // Places this block's pairs.  before, all (shared, [E]): an expert's pairs in earlier blocks and in all of them.
+template <bool BAL>
 __device__ __forceinline__ void place_pairs(const GroupRouteArgs& a, const Pairs& s, const int* before, const int* all, int* counts) {
   __shared__ int wsum[GR_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.E;
@@ -310,6 +334,7 @@ __device__ __forceinline__ void place_pairs(const GroupRouteArgs& a, const Pairs
     int pos = 0;
     if (e >= 0) pos = s.next[e] + __popc(same & ((1u << lane) - 1u));
     __syncwarp();
+    if (BAL && i < s.q1) a.places[i] = e >= 0 ? pos : -1;
     if (e >= 0) {
       a.pairs[pos] = (int)i;
       a.rows[pos] = (int)((unsigned)i / (unsigned)a.k);
@@ -325,14 +350,14 @@ __device__ __forceinline__ void place_pairs(const GroupRouteArgs& a, const Pairs
 }
 
 // One launch: the blocks are one cluster, and read each other's counts.
-template <int NV>
+template <int NV, bool BAL>
 __global__ void __launch_bounds__(GR_THREADS, 1) group_one_kernel(GroupRouteArgs a) {
   extern __shared__ int counts[];
   __shared__ int hist[1024], all[1024], before[1024];
   const Pairs s = block_pairs(a, counts);
   for (int i = threadIdx.x; i < s.W * a.E; i += GR_THREADS) counts[i] = 0;
   pdl_wait();
-  select_tokens<NV>(a, hist);
+  select_tokens<NV, BAL>(a, hist);
   if (a.blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   count_pairs(a, s);   // while the others arrive
   if (a.blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -350,17 +375,17 @@ __global__ void __launch_bounds__(GR_THREADS, 1) group_one_kernel(GroupRouteArgs
   before[e] = mine;
   if (a.blocks > 1) cluster_sync_all();   // the others read this block's counts until here
   else __syncthreads();
-  place_pairs(a, s, before, all, counts);
+  place_pairs<BAL>(a, s, before, all, counts);
 }
 
 // The counts leave by clusters, hist [clusters][E], with each block's share of its cluster's before it, [blocks][E] behind:
 // the next kernel's blocks then read half of the rows (read one by one, they took half of that kernel's time).
-template <int NV>
+template <int NV, bool BAL>
 __global__ void __launch_bounds__(GR_THREADS, 1) group_select_kernel(GroupRouteArgs a) {
   __shared__ int hist[1024];
   pdl_launch_dependents();
   pdl_wait();
-  select_tokens<NV>(a, hist);
+  select_tokens<NV, BAL>(a, hist);
   cluster_sync_all();
   const int rank = (int)cluster_rank(), clusters = a.blocks / GR_CLUSTER;
   for (int e = threadIdx.x; e < a.E; e += GR_THREADS) {
@@ -378,6 +403,7 @@ __global__ void __launch_bounds__(GR_THREADS, 1) group_select_kernel(GroupRouteA
   cluster_sync_all();   // the others read this block's counts until here
 }
 
+template <bool BAL>
 __global__ void __launch_bounds__(GR_THREADS, 1) group_place_kernel(GroupRouteArgs a) {
   extern __shared__ int counts[];
   __shared__ int all[1024], before[1024];
@@ -402,7 +428,7 @@ __global__ void __launch_bounds__(GR_THREADS, 1) group_place_kernel(GroupRouteAr
     atomicAdd(&before[e], p);
   }
   __syncthreads();
-  place_pairs(a, pairs, before, all, counts);
+  place_pairs<BAL>(a, pairs, before, all, counts);
 }
 
 template <typename... A>
@@ -423,18 +449,24 @@ cudaError_t launch(void (*kernel)(A...), int blocks, int cluster, size_t smem, c
   return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
-template <int NV>
+template <int NV, bool BAL>
 cudaError_t launch_as(const GroupRouteArgs& a, cudaStream_t s) {
   const int warps = GR_COUNTS / a.E < GR_WARPS ? GR_COUNTS / a.E : GR_WARPS;
   const size_t smem = (size_t)warps * a.E * sizeof(int);
-  if (a.T <= one_launch(a.E)) return launch(group_one_kernel<NV>, a.blocks, a.blocks, smem, s, a);
-  cudaError_t e = launch(group_select_kernel<NV>, a.blocks, GR_CLUSTER, 0, s, a);
-  return e != cudaSuccess ? e : launch(group_place_kernel, a.blocks, 1, smem, s, a);
+  if (a.T <= one_launch(a.E)) return launch(group_one_kernel<NV, BAL>, a.blocks, a.blocks, smem, s, a);
+  cudaError_t e = launch(group_select_kernel<NV, BAL>, a.blocks, GR_CLUSTER, 0, s, a);
+  return e != cudaSuccess ? e : launch(group_place_kernel<BAL>, a.blocks, 1, smem, s, a);
 }
 
 template <int NV>
 cudaError_t set_attribute() {
-  return cudaFuncSetAttribute(group_one_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
+  const cudaError_t e = cudaFuncSetAttribute(group_one_kernel<NV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(group_one_kernel<NV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
+}
+template <int NV>
+cudaError_t launch_of(const GroupRouteArgs& a, cudaStream_t s) {
+  return a.balanced ? launch_as<NV, true>(a, s) : launch_as<NV, false>(a, s);
 }
 
 }  // namespace
@@ -445,7 +477,9 @@ cudaError_t group_route_set_attributes() {
   if (e == cudaSuccess) e = set_attribute<16>();
   if (e == cudaSuccess) e = set_attribute<32>();
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(group_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
+    e = cudaFuncSetAttribute(group_place_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(group_place_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
   return e;
 }
 
@@ -467,9 +501,9 @@ GroupRoutePlan group_route_plan(int T, int E, int k) {
 }
 
 cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s) {
-  if (a.E <= 128) return launch_as<4>(a, s);
-  if (a.E <= 256) return launch_as<8>(a, s);
-  return a.E <= 512 ? launch_as<16>(a, s) : launch_as<32>(a, s);
+  if (a.E <= 128) return launch_of<4>(a, s);
+  if (a.E <= 256) return launch_of<8>(a, s);
+  return a.E <= 512 ? launch_of<16>(a, s) : launch_of<32>(a, s);
 }
 
 }  // namespace moe

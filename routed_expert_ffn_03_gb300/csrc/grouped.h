@@ -1,4 +1,4 @@
-// grouped.h - device arguments and launchers of the 16-bit grouped products (internal).
+// grouped.h - device arguments and launchers of the grouped products in 16 and 8 bits (internal).
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -13,7 +13,7 @@ enum : int { GT_BF16 = 0, GT_FP16 = 1, GT_FP32 = 2 };
 //   forward: A = sorted rows of x [m][k], B = W_e as n rows of k; D rows go to out rows
 //   weight gradient: A = dy^T (n rows), B = x^T (k rows), contracted over the group's rows
 struct GroupedProblem {
-  const uint16_t* a;         // x, or dy
+  const uint16_t* a;         // x, or dy; bytes with `eight`
   const uint16_t* b;         // w, or x
   void* d;                   // out, or dw
   const int* offsets;        // [groups + 1]
@@ -28,6 +28,12 @@ struct GroupedProblem {
   int dtype, out_dtype;
   int kn;                    // forward: W_e stored [k][n]
   int swiglu;
+  // forward products in 8 bits (e4m3, MOE_GROUP_NK): the sums are multiplied by a scale for each row of x and each row of W_e
+  int eight;
+  const float* a_scale;      // [scale_nrows], by x row
+  const float* b_scale;      // [groups][n]
+  const int* scale_rows;     // x rows by sorted row, or null (a_rows, which goes where rows are copied side by side)
+  long long scale_nrows;
 };
 
 #ifdef __CUDACC__
@@ -37,6 +43,11 @@ __device__ __forceinline__ void group_range(const int* offsets, int g, long long
   const int hi = (int)m;
   r0 = min(max(__ldg(offsets + g), 0), hi);
   r1 = min(max(__ldg(offsets + g + 1), r0), hi);
+}
+// the scale of sorted row i (0, as its values are, for a number outside x)
+__device__ __forceinline__ float row_scale(const GroupedProblem& p, int i) {
+  const long long r = p.scale_rows ? __ldg(p.scale_rows + i) : i;
+  return r >= 0 && r < p.scale_nrows ? __ldg(p.a_scale + r) : 0.f;
 }
 #endif
 
@@ -50,12 +61,12 @@ struct WaitLimit {
 cudaError_t launch_grouped_any(const GroupedProblem& p, bool wgrad, const WaitLimit& wait, cudaStream_t s);
 cudaError_t grouped_any_set_attributes();
 
-// A tensor map over elements of 2 or 4 bytes, 128-byte swizzled, zeros outside: dims and box in elements, innermost
+// A tensor map over elements of 1, 2 or 4 bytes, 128-byte swizzled, zeros outside: dims and box in elements, innermost
 // first; strides (of dims 1 ..) in bytes.  False where the hardware cannot address the tensor so (a base, stride or
 // size it does not take).  m null: that alone is looked at, without the driver.
 bool tensor_map(CUtensorMap* m, const void* base, size_t elem, int rank, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box);
-// The maps of a product, 64 elements wide.  a: the first factor in tiles.  b: the second, forward in boxes of 16, 32, 64
+// The maps of a product, 128 bytes (64 elements of 16 bits) wide.  a: the first factor in tiles.  b: the second, forward in boxes of 16, 32, 64
 // and 128 rows, weight gradient [0] in tiles of 64 rows; for the few-rows kernel only [0], of one row where rows are named
 // by number.  d: weight gradient: the result, in boxes of 32 rows of 128 bytes (made by the launcher).
 struct GroupedMaps {

@@ -22,7 +22,7 @@ namespace moe {
 
 namespace {
 
-enum : int { GF_NK = 0, GF_KN = 1, GF_SWIGLU = 2 };
+enum : int { GF_NK = 0, GF_KN = 1, GF_SWIGLU = 2, GF_NK8 = 3, GF_SWIGLU8 = 4 };
 constexpr int GF_ROW_WARP = 6;
 constexpr int GF_THREADS = (GF_ROW_WARP + 1) * 32;
 constexpr int GF_A = 128 * 128;       // bytes of a W_e tile: 128 features x 64 elements
@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : 4, STAGE = GF_A + NT * 128;
   constexpr int COLS = NT == 16 ? 32 : 2 * NT;      // two results
-  constexpr bool SW = MODE == GF_SWIGLU;
+  constexpr bool SW = MODE == GF_SWIGLU || MODE == GF_SWIGLU8, F8 = MODE == GF_NK8 || MODE == GF_SWIGLU8;
+  constexpr int STEP = F8 ? 128 : 64;               // contracted elements of a stage: 128 bytes
   const GroupedProblem& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = a.cluster, rank = C > 1 ? (int)cluster_rank() : 0;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
   const bool work = e >= 0;                       // the same in every block of the cluster
   const int f0 = tile % a.nft * (SW ? 64 : 128);  // first feature (with swiglu: of gate and of up)
   const int n = (rows + 15) & ~15;                // columns of the product
-  const int nkb = (p.k + 63) / 64, kb0 = (int)((long long)nkb * rank / C), kb1 = (int)((long long)nkb * (rank + 1) / C);
+  const int nkb = (p.k + STEP - 1) / STEP, kb0 = (int)((long long)nkb * rank / C), kb1 = (int)((long long)nkb * (rank + 1) / C);
   const int n_out = SW ? p.n / 2 : p.n;
 
   float sum[NT];
@@ -119,10 +120,10 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
       const uint32_t bar = bar0 + 8 * s, da = base + s * STAGE;
       if (leader) {
         mbar_arrive_expect_tx(bar, GF_A + un * 128);
-        if (MODE == GF_NK) tma_3d<1>(da, &maps.a, kb * 64, uf, ue, bar);
-        if (SW && !a.by_16) tma_5d<1>(da, &maps.a, kb * 64, 0, 0, uf / 16, ue, bar);
+        if (MODE == GF_NK || MODE == GF_NK8) tma_3d<1>(da, &maps.a, kb * STEP, uf, ue, bar);
+        if (SW && !a.by_16) tma_5d<1>(da, &maps.a, kb * STEP, 0, 0, uf / 16, ue, bar);
         if (SW && a.by_16)   // gate and up in turn, 16 rows each
-          for (int i = 0; i < 8; ++i) tma_3d<1>(da + i * 2048, &maps.a, kb * 64, uf + (i >> 1) * 16 + (i & 1) * (p.n / 2), ue, bar);
+          for (int i = 0; i < 8; ++i) tma_3d<1>(da + i * 2048, &maps.a, kb * STEP, uf + (i >> 1) * 16 + (i & 1) * (p.n / 2), ue, bar);
         if (MODE == GF_KN) {
           tma_3d<1>(da, &maps.a, uf, kb * 64, ue, bar);
           tma_3d<1>(da + SLAB_BYTES, &maps.a, uf + 64, kb * 64, ue, bar);
@@ -155,9 +156,9 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
       if (!ok) break;
       const uint32_t bar = full0 + 8 * s, db = smem_u32(smem) + s * STAGE + GF_A;
       if (p.a_rows) {
-        if (lane < n / 4) tma_gather4(db + lane * 512, &maps.b[0], kb * 64, gr, bar);
+        if (lane < n / 4) tma_gather4(db + lane * 512, &maps.b[0], kb * STEP, gr, bar);
       } else if (lane < n / 16) {
-        tma_2d<1>(db + lane * 2048, &maps.b[0], kb * 64, r0 + lane * 16, bar);
+        tma_2d<1>(db + lane * 2048, &maps.b[0], kb * STEP, r0 + lane * 16, bar);
       }
       __syncwarp();
       if (++s == STAGES) {
@@ -172,7 +173,8 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
     constexpr uint32_t a_step = (a_mn ? 2048 : 32) >> 4;
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t da0 = sw128_desc(base, a_mn), db0 = sw128_desc(base + GF_A, false);
-    const uint32_t idesc = idesc_16(p.dtype == GT_BF16, a_mn, false, 128, __shfl_sync(0xffffffffu, n, 0));
+    const int un = __shfl_sync(0xffffffffu, n, 0);
+    const uint32_t idesc = F8 ? idesc_8(128, un) : idesc_16(p.dtype == GT_BF16, a_mn, false, 128, un);
     int s = 0, acc = 0;
     uint32_t ph = 0, aph = 0;
     bool ok = true;
@@ -187,7 +189,10 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
         const uint64_t da = da0 + (uint32_t)(s * (STAGE >> 4)), db = db0 + (uint32_t)(s * (STAGE >> 4));
         if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) umma<1>(tm + acc * NT, da + kk * a_step, db + kk * 2, idesc, kb > k0 || kk > 0);
+          for (int kk = 0; kk < 4; ++kk) {
+            if (F8) umma_8<1>(tm + acc * NT, da + kk * a_step, db + kk * 2, idesc, kb > k0 || kk > 0);
+            else umma<1>(tm + acc * NT, da + kk * a_step, db + kk * 2, idesc, kb > k0 || kk > 0);
+          }
           umma_commit(empty0 + 8 * s);
         }
         __syncwarp();
@@ -268,6 +273,19 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
           u.y += x.y;
         }
       }
+      if (F8) {
+        const float xs = row_scale(p, r0 + t);
+        const float* ws = p.b_scale + (long long)e * p.n;
+        const int g = f0 + 2 * j, h = min(g + 1, n_out - 1);   // (a feature past the last is not stored)
+        if (g < n_out) {
+          v.x *= xs * __ldg(ws + g);
+          v.y *= xs * __ldg(ws + h);
+          if (SW) {
+            u.x *= xs * __ldg(ws + n_out + g);
+            u.y *= xs * __ldg(ws + n_out + h);
+          }
+        }
+      }
       if (SW) {
         v.x = silu(v.x) * u.x;
         v.y = silu(v.y) * u.y;
@@ -340,6 +358,8 @@ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 cudaError_t grouped_few_set_attributes() {
   cudaError_t e = set_attributes<GF_NK>();
   if (e == cudaSuccess) e = set_attributes<GF_KN>();
+  if (e == cudaSuccess) e = set_attributes<GF_NK8>();
+  if (e == cudaSuccess) e = set_attributes<GF_SWIGLU8>();
   return e == cudaSuccess ? set_attributes<GF_SWIGLU>() : e;
 }
 
@@ -356,9 +376,10 @@ bool launch_grouped_few(const GroupedProblem& p, int nt, int cluster, const Wait
   a.wide = (uintptr_t)p.d % 4 == 0 && p.ldd % 2 == 0 && n_out % 2 == 0;
   const long long tiles = (p.m / nt + (p.m < p.groups ? p.m : p.groups)) * a.nft;   // the most that m rows can make
   if (tiles * cluster > 0x3fffffff) return false;
-  *err = p.swiglu ? launch_mode<GF_SWIGLU>(a, m, nt, (unsigned)tiles, s)
-         : p.kn   ? launch_mode<GF_KN>(a, m, nt, (unsigned)tiles, s)
-                  : launch_mode<GF_NK>(a, m, nt, (unsigned)tiles, s);
+  *err = p.eight    ? (p.swiglu ? launch_mode<GF_SWIGLU8>(a, m, nt, (unsigned)tiles, s) : launch_mode<GF_NK8>(a, m, nt, (unsigned)tiles, s))
+         : p.swiglu ? launch_mode<GF_SWIGLU>(a, m, nt, (unsigned)tiles, s)
+         : p.kn     ? launch_mode<GF_KN>(a, m, nt, (unsigned)tiles, s)
+                    : launch_mode<GF_NK>(a, m, nt, (unsigned)tiles, s);
   return true;
 }
 

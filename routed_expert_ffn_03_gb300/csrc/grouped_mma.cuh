@@ -28,6 +28,11 @@ __host__ __device__ __forceinline__ uint32_t idesc_16(bool bf16, bool a_mn, bool
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// kind::f8f6f4 with fp32 sums, A and B e4m3, both K-major; a step is K = 32, the same 32 B
+__host__ __device__ __forceinline__ uint32_t idesc_8(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
 // true in one lane of the warp (all of it calls)
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -46,6 +51,21 @@ __device__ __forceinline__ void umma(uint32_t dtmem, uint64_t adesc, uint64_t bd
   else
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+            dtmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void umma_8(uint32_t dtmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool acc) {
+  if (CG == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+            dtmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(
             dtmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)acc)
         : "memory");

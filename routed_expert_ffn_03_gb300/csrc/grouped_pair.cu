@@ -37,7 +37,13 @@ namespace moe {
 
 namespace {
 
-enum : int { GP_NK = 0, GP_KN = 1, GP_SWIGLU = 2, GP_WGRAD = 3 };
+enum : int { GP_NK = 0, GP_KN = 1, GP_SWIGLU = 2, GP_WGRAD = 3, GP_NK8 = 4, GP_SWIGLU8 = 5 };
+template <int MODE>
+constexpr bool GP_IS_8 = MODE == GP_NK8 || MODE == GP_SWIGLU8;
+template <int MODE>
+constexpr bool GP_IS_SWIGLU = MODE == GP_SWIGLU || MODE == GP_SWIGLU8;
+template <int MODE>
+constexpr int GP_STEP = GP_IS_8<MODE> ? 128 : 64;   // contracted elements of a stage: 128 bytes
 
 // stages of the ring, and per storing warp one box of results on its way out (weight gradient).  5 stages and two boxes
 // were 8% slower (Mixtral-shaped, fp32 results: 765 and 711 us).
@@ -58,7 +64,7 @@ constexpr int GP_MAX_GROUPS = 1024;
 // parts beyond, where the error would go on growing: an fp16 half step at 400 thousand elements.  Parts cost a forward product
 // 3% there (4096 rows in 4 groups, n = 4096, k = 16448: 326 and 338 us; with swiglu 6%), a weight gradient 1%.
 template <int MODE>
-constexpr int GP_PART = MODE == GP_SWIGLU ? 4 : 8;
+constexpr int GP_PART = GP_IS_SWIGLU<MODE> ? 4 : 8;
 constexpr int GP_LONG = 256;
 enum : int { GP_OUT_16 = 0, GP_OUT_16_LONG = 1, GP_OUT_32 = 2 };   // results, and whether contractions past GP_LONG may come
 constexpr int GP_BAND = 8;                       // row tiles of a band
@@ -140,7 +146,7 @@ __device__ __forceinline__ Tile decode(const PairArgs& a, const int* first, int 
   const int band = i / (GP_BAND * a.nft), in = i - band * GP_BAND * a.nft;
   const int h = min(GP_BAND, nt - band * GP_BAND);
   const int rt = band * GP_BAND + in % h;
-  T.f0 = in / h * (MODE == GP_SWIGLU ? 128 : 256);
+  T.f0 = in / h * (GP_IS_SWIGLU<MODE> ? 128 : 256);
   // the group's 32s of rows in even parts: a tile of few rows would wait for its weights
   const int units = (R + 31) / 32, base = units / nt, more = units - base * nt;
   const int at = (rt * base + min(rt, more)) * 32;
@@ -148,7 +154,7 @@ __device__ __forceinline__ Tile decode(const PairArgs& a, const int* first, int 
   T.r0 += at;
   T.n = (T.rows + 31) & ~31;
   T.c0 = 0;
-  T.nkb = (p.k + 63) / 64;
+  T.nkb = (p.k + GP_STEP<MODE> - 1) / GP_STEP<MODE>;
   return T;
 }
 
@@ -160,7 +166,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const GroupedProblem& p = a.p;
-  constexpr bool WG = MODE == GP_WGRAD, SW = MODE == GP_SWIGLU, F32 = OUT == GP_OUT_32;
+  constexpr bool WG = MODE == GP_WGRAD, SW = GP_IS_SWIGLU<MODE>, F32 = OUT == GP_OUT_32, F8 = GP_IS_8<MODE>;
+  constexpr int STEP = GP_STEP<MODE>;
   constexpr bool PARTS = OUT != GP_OUT_16;   // sums in registers
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + GP_OFF_BAR);
@@ -279,11 +286,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
               tma_2d<2>(db + h * SLAB_BYTES, &maps.b[0], fb + h * 64, r0 + kb * 64, bar);
             }
           } else if (weights) {
-            if (MODE == GP_NK) tma_3d<2>(da, &maps.a, kb * 64, f, e, bar);
-            if (SW && !a.by_16) tma_5d<2>(da, &maps.a, kb * 64, 0, 0, f / 16, e, bar);
+            if (MODE == GP_NK || MODE == GP_NK8) tma_3d<2>(da, &maps.a, kb * STEP, f, e, bar);
+            if (SW && !a.by_16) tma_5d<2>(da, &maps.a, kb * STEP, 0, 0, f / 16, e, bar);
             if (SW && a.by_16)   // gate and up in turn, 16 rows each
               for (int i = 0; i < 8; ++i)
-                tma_3d<2>(da + i * 2048, &maps.a, kb * 64, f + (i >> 1) * 16 + (i & 1) * (p.n / 2), e, bar);
+                tma_3d<2>(da + i * 2048, &maps.a, kb * STEP, f + (i >> 1) * 16 + (i & 1) * (p.n / 2), e, bar);
             if (MODE == GP_KN) {
               tma_3d<2>(da, &maps.a, f, kb * 64, e, bar);
               tma_3d<2>(da + SLAB_BYTES, &maps.a, f + 64, kb * 64, e, bar);
@@ -293,7 +300,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int box = 16 << i, before = half & ~(2 * box - 1);
-              if (half & box) tma_2d<2>(db + before * 128, &maps.b[i], kb * 64, rb + before, bar);
+              if (half & box) tma_2d<2>(db + before * 128, &maps.b[i], kb * STEP, rb + before, bar);
             }
           }
         }
@@ -327,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
       constexpr uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
       const uint32_t base = __shfl_sync(0xffffffffu, s0, 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint64_t da0 = sw128_desc(base, a_mn), db0 = sw128_desc(base + GP_OP, b_mn);
-      const uint32_t idesc0 = idesc_16(p.dtype == GT_BF16, a_mn, b_mn, 256, 0);
+      const uint32_t idesc0 = F8 ? idesc_8(256, 0) : idesc_16(p.dtype == GT_BF16, a_mn, b_mn, 256, 0);
       Tile T{};
       if (pair < total) T = decode<MODE>(a, first, pair);
       for (int t = pair; t < total && ok; t += npair) {
@@ -352,8 +359,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
             const uint64_t da = da0 + (uint32_t)(s * (GP_STAGE >> 4)), db = db0 + (uint32_t)(s * (GP_STAGE >> 4));
             if (leader) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma<2>(dst, da + kk * a_step, db + kk * b_step, idesc, kb > kb0 || kk > 0);
+              for (int kk = 0; kk < 4; ++kk) {
+                if (F8) umma_8<2>(dst, da + kk * a_step, db + kk * b_step, idesc, kb > kb0 || kk > 0);
+                else umma<2>(dst, da + kk * a_step, db + kk * b_step, idesc, kb > kb0 || kk > 0);
+              }
               umma_commit_pair(empty0 + 8 * s);
             }
             __syncwarp();
@@ -519,6 +528,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         } else {
           tmem_ld32(td + c, v);
         }
+        if (F8) {   // lane: a row of W_e; columns: rows of x
+          const int f = SW ? T.f0 + (int)rank * 64 + quarter * 16 + (lane & 15) : T.f0 + (int)rank * 128 + quarter * 32 + lane;
+          const float ws = f < n_out ? __ldg(p.b_scale + (long long)T.e * p.n + (SW && lane >= 16 ? n_out : 0) + f) : 0.f;
+          const float xs = c + lane < T.rows ? row_scale(p, T.r0 + c + lane) : 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= ws * __shfl_sync(0xffffffffu, xs, i);
+        }
         if (WG) {
           // lane: row n of dw; columns: k
           const int n = T.f0 + (int)rank * 128 + quarter * 32 + lane, k = T.c0 + c;
@@ -624,7 +640,7 @@ cudaError_t launch_mode(const PairArgs& a, const GroupedMaps& m, unsigned pairs,
   if (a.p.out_dtype == GT_FP32) return launch_as<MODE, GP_OUT_32>(a, m, pairs, s);
   // (of a weight gradient the longest that a group can be: shorter ones are summed in one go there too)
   const long long longest = MODE == GP_WGRAD ? a.p.m : a.p.k;
-  return longest > GP_LONG * 64 ? launch_as<MODE, GP_OUT_16_LONG>(a, m, pairs, s) : launch_as<MODE, GP_OUT_16>(a, m, pairs, s);
+  return longest > GP_LONG * GP_STEP<MODE> ? launch_as<MODE, GP_OUT_16_LONG>(a, m, pairs, s) : launch_as<MODE, GP_OUT_16>(a, m, pairs, s);
 }
 
 template <int MODE, int OUT>
@@ -647,11 +663,15 @@ cudaError_t grouped_pair_set_attributes() {
   if (e == cudaSuccess) e = set_attributes<GP_KN>();
   if (e == cudaSuccess) e = set_attributes<GP_SWIGLU>();
   if (e == cudaSuccess) e = set_attributes<GP_WGRAD>();
+  if (e == cudaSuccess) e = set_attributes<GP_NK8>();
+  if (e == cudaSuccess) e = set_attributes<GP_SWIGLU8>();
   return e;
 }
 
 bool grouped_maps(const GroupedProblem& p, bool wgrad, bool few, GroupedMaps* m) {
-  const uint64_t lda = p.lda * 2, ldb = p.ldb * 2;
+  const size_t el = p.eight ? 1 : 2;
+  const uint32_t wide = 128 / (uint32_t)el;   // elements of a box
+  const uint64_t lda = p.lda * el, ldb = p.ldb * el;
   CUtensorMap *ma = m ? &m->a : nullptr, *mb = m ? m->b : nullptr;
   auto map_b = [&](int i) { return mb ? mb + i : nullptr; };
   if (p.a_nrows < 1 || p.a_nrows > 0x7fffffffLL) return false;
@@ -663,26 +683,26 @@ bool grouped_maps(const GroupedProblem& p, bool wgrad, bool few, GroupedMaps* m)
   }
   const uint64_t n = p.n, k = p.k, E = p.groups;
   // one expert: any step to the next; several on top of one another are not a tensor
-  const uint64_t rows = p.kn ? k : n, step = p.groups > 1 ? p.b_stride * 2 : rows * ldb;
+  const uint64_t rows = p.kn ? k : n, step = p.groups > 1 ? p.b_stride * el : rows * ldb;
   if (step == 0) return false;
   bool ok;
   if (p.swiglu && n / 2 % 16 == 0) {   // a tile's alternating runs of 16 rows of gate and up in one box
     const uint64_t h = n / 2, d[] = {k, 16, 2, h / 16, E}, st[] = {ldb, h * ldb, 16 * ldb, step};
-    const uint32_t box[] = {64, 16, 2, 4, 1};
-    ok = tensor_map(ma, p.b, 2, 5, d, st, box);
+    const uint32_t box[] = {wide, 16, 2, 4, 1};
+    ok = tensor_map(ma, p.b, el, 5, d, st, box);
   } else {
     const uint64_t d[] = {p.kn ? n : k, p.kn ? k : n, E}, st[] = {ldb, step};
-    const uint32_t box[] = {64, p.swiglu ? 16u : p.kn ? 64u : 128u, 1};
-    ok = tensor_map(ma, p.b, 2, 3, d, st, box);
+    const uint32_t box[] = {wide, p.swiglu ? 16u : p.kn ? 64u : 128u, 1};
+    ok = tensor_map(ma, p.b, el, 3, d, st, box);
   }
   const uint64_t dx[] = {k, (uint64_t)p.a_nrows};
   if (few && p.a_rows) {
-    const uint32_t one[] = {64, 1};
-    return ok && tensor_map(map_b(0), p.a, 2, 2, dx, &lda, one);
+    const uint32_t one[] = {wide, 1};
+    return ok && tensor_map(map_b(0), p.a, el, 2, dx, &lda, one);
   }
   for (int i = 0; i < (few ? 1 : 4) && ok; ++i) {
-    const uint32_t tile[] = {64, 16u << i};
-    ok = tensor_map(map_b(i), p.a, 2, 2, dx, &lda, tile);
+    const uint32_t tile[] = {wide, 16u << i};
+    ok = tensor_map(map_b(i), p.a, el, 2, dx, &lda, tile);
   }
   return ok;
 }
@@ -716,6 +736,7 @@ bool launch_grouped_pair(const GroupedProblem& p, bool wgrad, int num_sms, const
   a.max_tiles = (int)tiles;
   const unsigned pairs = (unsigned)(tiles < num_sms / 2 ? tiles : num_sms / 2);
   if (wgrad) *err = launch_mode<GP_WGRAD>(a, m, pairs, s);
+  else if (p.eight) *err = p.swiglu ? launch_mode<GP_SWIGLU8>(a, m, pairs, s) : launch_mode<GP_NK8>(a, m, pairs, s);
   else if (p.swiglu) *err = launch_mode<GP_SWIGLU>(a, m, pairs, s);
   else *err = p.kn ? launch_mode<GP_KN>(a, m, pairs, s) : launch_mode<GP_NK>(a, m, pairs, s);
   return true;

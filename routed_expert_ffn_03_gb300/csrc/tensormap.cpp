@@ -32,7 +32,9 @@ bool tensor_map(CUtensorMap* m, const void* base, size_t elem, int rank, const u
     es[i] = 1;
   }
   for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
-  return encode(m, elem == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), d, st, b, es,
+  return encode(m, elem == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                   : elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                               : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), d, st, b, es,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

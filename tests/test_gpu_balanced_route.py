@@ -1,0 +1,209 @@
+"""balanced_route and its gradient against the plain 64-bit forms."""
+import numpy as np
+import pytest
+
+from tests import batch_helpers as B
+from tests import rows_helpers as R
+from tests.test_gpu_grouped import M  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def check(M, logits, k, bias=None, router=0, groups=1, keep=1, group_score="top2", renormalize=True, scale=1.0, **kw):  # noqa: F811
+    l = logits.double().cpu().numpy()
+    ref = R.balanced_ref(l, k, router, None if bias is None else bias.double().cpu().numpy(), groups, keep, group_score == "top2",
+                         renormalize, scale)
+    got = [t.cpu().numpy() for t in M.balanced_route(logits, k, bias=bias, router=router, groups=groups, keep=keep, group_score=group_score,
+                                                     renormalize=renormalize, scale=scale, **kw)]
+    for i in (0, 2, 3, 4, 5):
+        np.testing.assert_array_equal(got[i], ref[i])
+    assert (np.abs(got[1] - ref[1]) <= R.weights_tol(l, ref[0], ref[1], scale)).all()
+    assert (got[1][ref[0] < 0] == 0).all()
+    return got
+
+
+def random_logits(T, E, dtype, scale=1.5, seed=0):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed + T + E)
+    return (scale * torch.randn(T, E, generator=g, device="cuda")).to(B.torch_type(dtype))
+
+
+def random_bias(E, scale=0.05):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(E)
+    return scale * torch.randn(E, generator=g, device="cuda")
+
+
+CASES = [  # T, E, k, groups, keep
+    (1, 256, 8, 8, 4), (1, 1, 1, 1, 1), (3, 8, 2, 1, 1), (5, 12, 3, 4, 2), (257, 160, 6, 8, 3), (1000, 64, 6, 32, 5), (33, 1024, 32, 32, 8),
+    (700, 1000, 10, 8, 3), (64, 40, 32, 5, 4), (513, 256, 8, 8, 4), (2000, 256, 8, 8, 4), (200, 96, 10, 3, 2), (260, 384, 16, 1, 1),
+    (100, 512, 8, 8, 8), (40, 30, 30, 30, 30), (300, 31, 5, 31, 7), (600, 768, 4, 12, 2)]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("router", [0, 1])
+@pytest.mark.parametrize("T,E,k,groups,keep", CASES)
+def test_balanced_route(M, T, E, k, groups, keep, router, dtype):  # noqa: F811
+    logits = random_logits(T, E, dtype)
+    check(M, logits, k, random_bias(E), router, groups, keep, "top2", True, 2.5)
+    check(M, logits, k, None, router, groups, keep, "max", False, 1.0)
+
+
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("with_bias", [True, False])
+@pytest.mark.parametrize("router", [0, 1])
+def test_balanced_route_options(M, router, with_bias, renormalize, group_score):  # noqa: F811
+    for groups, keep in ((1, 1), (6, 2), (6, 6)):
+        check(M, random_logits(70, 48, "fp32"), 5, random_bias(48) if with_bias else None, router, groups, keep, group_score, renormalize, -1.5)
+
+
+def test_balanced_route_without_bias_or_groups_is_group_route(M):  # noqa: F811
+    for router in (0, 1):
+        l = random_logits(600, 200, "bf16")
+        a, b = M.balanced_route(l, 7, router=router), M.group_route(l, 7, router=router)
+        for i in (0, 2, 3, 4):
+            assert (a[i] == b[i]).all()
+        assert (a[1] - b[1]).abs().max() < 1e-6
+        p, places = a[4].cpu().numpy(), a[5].cpu().numpy().reshape(-1)
+        np.testing.assert_array_equal(p[places], np.arange(len(p)))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("router", [0, 1])
+@pytest.mark.parametrize("T,E,k,groups,keep", [(40, 64, 4, 8, 3), (1, 64, 4, 8, 3), (3000, 12, 6, 3, 2), (600, 12, 6, 1, 1)])
+def test_balanced_route_ties_masks_and_extremes(M, T, E, k, groups, keep, router, dtype):  # noqa: F811
+    import torch
+    rng = np.random.default_rng(T)
+    # ties everywhere, but no two sums of scores that are equal in the reals alone (as sigmoid(1) + sigmoid(-1) = 2 sigmoid(0))
+    l = rng.choice(np.array([0.0, -0.0, 1.0, -1.5, 2.0], np.float32), (T, E))
+    l[rng.random((T, E)) < 0.3] = -np.inf
+    l[rng.random((T, E)) < 0.05] = np.nan
+    l[rng.random((T, E)) < 0.02] = np.inf
+    l[rng.random((T, E)) < 0.05] = np.finfo(np.float32).min
+    l[:: 5] = -np.inf                                                                 # padding
+    if T > 2:
+        l[1] = np.finfo(np.float32).min
+        l[2] = -2000.0                                                                # every sigmoid underflows
+    logits = torch.from_numpy(l).cuda().to(B.torch_type(dtype))
+    bias = torch.from_numpy(rng.choice(np.array([0.0, 0.25, -0.25, 0.25, 1.0, -3.0], np.float32), E)).cuda()
+    for b in (None, torch.zeros(E, device="cuda")):
+        check(M, logits, k, b, router, groups, keep, "top2")
+        check(M, logits, k, b, router, groups, keep, "max", renormalize=False)
+    check(M, logits, k, bias, router, groups, keep, "max")
+    bias = bias + torch.from_numpy((0.01 * rng.normal(size=E)).astype(np.float32)).cuda()   # (with shared ones such sums occur)
+    check(M, logits, k, bias, router, groups, keep, "top2")
+    bias[3], bias[4], bias[5] = -np.inf, np.nan, np.inf
+    check(M, logits, k, bias, router, groups, keep, "top2")
+
+
+@pytest.mark.parametrize("router", [0, 1])
+@pytest.mark.parametrize("E,k,groups,keep", [(64, 8, 1, 1), (64, 8, 8, 4), (300, 32, 1, 1), (1000, 6, 8, 2), (40, 5, 5, 2)])
+def test_balanced_route_scores_a_rounding_apart(M, router, E, k, groups, keep):  # noqa: F811
+    """Scores with the bias that differ by less than fp32 can tell, and some that are equal: the order of 64 bits decides."""
+    import torch
+    rng = np.random.default_rng(E + k)
+    T = 200
+    l = rng.choice(np.array([0.5, 1.0, 2.0], np.float32), (T, E)) + (rng.integers(0, 4, (T, E)) * 2.0 ** -22).astype(np.float32)
+    bias = (rng.choice(np.array([0.0, 2.0 ** -24, 0.1]), E) + np.arange(E) * 2.0 ** -26).astype(np.float32)
+    l[::9] = rng.normal(size=l[::9].shape)
+    l[::7] -= 12.0                                  # small scores, where a bias of 2^-24 counts
+    check(M, torch.from_numpy(l.astype(np.float32)).cuda(), k, torch.from_numpy(bias).cuda(), router, groups, keep, "top2")
+    check(M, torch.from_numpy(l.astype(np.float32)).cuda(), k, torch.zeros(E, device="cuda"), router, groups, keep, "max")
+    check(M, torch.from_numpy((l + 20).astype(np.float32)).cuda(), k, torch.from_numpy(bias).cuda(), router, groups, keep, "top2")
+
+
+def test_balanced_route_rows_apart_workspace_and_refusals(M):  # noqa: F811
+    import torch
+    big = random_logits(1300, 50, "bf16")
+    ws = torch.empty(M.group_route_workspace(1300, 36, 4) + 64, dtype=torch.uint8, device="cuda")
+    check(M, big[:, 3:39], 4, random_bias(36), 0, 4, 2, workspace=ws)
+    with pytest.raises(M.MoeError):
+        M.balanced_route(big, 4, workspace=ws[:16])
+    with pytest.raises(M.MoeError):
+        M.balanced_route(big, 4, groups=3)
+    with pytest.raises(M.MoeError):
+        M.balanced_route(big, 11, groups=5, keep=1)
+    for bad in (dict(bias=random_bias(49)), dict(bias=random_bias(50).double()), dict(group_score="sum")):
+        with pytest.raises(ValueError):
+            M.balanced_route(big, 4, **bad)
+
+
+def test_balanced_route_streams_and_capture(M):  # noqa: F811
+    import torch
+    a, bias = random_logits(2000, 96, "fp32"), random_bias(96)
+    torch.cuda.synchronize()
+    call = lambda **kw: M.balanced_route(a, 5, bias=bias, router=1, groups=4, keep=2, **kw)  # noqa: E731
+    outs = [call(stream=s) for s in [torch.cuda.Stream() for _ in range(3)] for _ in range(2)]
+    out = call()
+    ws = torch.empty(M.group_route_workspace(2000, 96, 5), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all((x == y).all() for x, y in zip(o, out))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out=out, workspace=ws)
+    a.copy_(random_logits(2000, 96, "fp32", seed=5))
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in out]
+    assert all((x == y).all() for x, y in zip(got, call()))
+
+
+def check_grad(M, logits, idx, dweights, router, renormalize, scale, out_type=None, **kw):  # noqa: F811
+    got = M.balanced_route_backward(dweights, logits, idx, router=router, renormalize=renormalize, scale=scale,
+                                    out_dtype=None if out_type is None else B.torch_type(out_type), **kw)
+    ref = R.balanced_grad_ref(dweights.double().cpu().numpy(), logits.double().cpu().numpy(), idx.cpu().numpy(), router, renormalize, scale)
+    name = {B.torch_type(n): n for n in ("bf16", "fp16", "fp32")}[got.dtype]
+    B.check_close(got, *ref, name)
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("router", [0, 1])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 256, 8), (37, 8, 2), (100, 160, 6), (9, 1000, 32), (300, 65, 5), (20, 512, 16), (4, 1024, 3)])
+def test_balanced_route_backward(M, T, E, k, renormalize, router, dtype):  # noqa: F811
+    import torch
+    logits = random_logits(T, E, dtype)
+    idx = M.balanced_route(logits, k, bias=random_bias(E), router=router)[0]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    check_grad(M, logits, idx, torch.randn(T, k, generator=g, device="cuda"), router, renormalize, 2.5)
+
+
+@pytest.mark.parametrize("router", [0, 1])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_balanced_route_backward_masks_and_extremes(M, router, renormalize):  # noqa: F811
+    import torch
+    rng = np.random.default_rng(1)
+    l = rng.normal(size=(40, 24)).astype(np.float32)
+    l[rng.random(l.shape) < 0.4] = -np.inf
+    l[3], l[4], l[5] = -np.inf, np.nan, -90.0
+    l[6, :20] = -np.inf
+    l[7] = 80.0
+    logits = torch.from_numpy(l).cuda()
+    idx = M.balanced_route(logits, 6, router=router, renormalize=renormalize)[0]
+    dw = torch.from_numpy(rng.normal(size=(40, 6)).astype(np.float32)).cuda()
+    dw[(idx < 0)] = float("nan")                   # of pairs that were masked: not used
+    clean = torch.where(idx < 0, torch.zeros_like(dw), dw)
+    got = M.balanced_route_backward(dw, logits, idx, router=router, renormalize=renormalize)
+    assert (got == check_grad(M, logits, idx, clean, router, renormalize, 1.0)).all()
+    assert (got[torch.isinf(logits) | torch.isnan(logits)] == 0).all()
+    wild = idx.clone()
+    wild[:, 0] = 24
+    wild[:, 1] = 2 ** 31 - 1
+    check_grad(M, logits, wild, clean, router, renormalize, 1.0)
+
+
+def test_balanced_route_backward_rows_apart(M):  # noqa: F811
+    import torch
+    big = random_logits(30, 64, "bf16")
+    logits = big[:, 3:50]
+    idx = M.balanced_route(logits, 4)[0]
+    out = torch.zeros(30, 60, device="cuda")
+    check_grad(M, logits, idx, torch.randn(30, 4, device="cuda"), 0, False, 1.0, out=out[:, 5:52])
+    assert (out[:, :5] == 0).all() and (out[:, 52:] == 0).all()
+    with pytest.raises(ValueError):
+        M.balanced_route_backward(torch.zeros(30, 5, device="cuda"), logits, idx)
+    with pytest.raises(ValueError):
+        M.balanced_route_backward(torch.zeros(30, 4, device="cuda"), logits, idx.long())
