@@ -3,6 +3,7 @@
 #include "batch.h"
 #include "group_route.h"
 #include "grouped.h"
+#include "rms_norm.h"
 #include "verify.h"
 
 #include <unistd.h>
@@ -36,7 +37,7 @@ moe_status device_setup(int dev, Device** out) {
   if (cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       moe::grouped_any_set_attributes() != cudaSuccess || moe::grouped_pair_set_attributes() != cudaSuccess ||
       moe::grouped_few_set_attributes() != cudaSuccess || moe::verify_set_attributes() != cudaSuccess ||
-      moe::group_route_set_attributes() != cudaSuccess) {
+      moe::group_route_set_attributes() != cudaSuccess || moe::rms_norm_set_attributes() != cudaSuccess) {
     cudaGetLastError();
     return MOE_ECUDA;
   }

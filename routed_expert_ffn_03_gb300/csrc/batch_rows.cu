@@ -79,7 +79,7 @@ extern "C" moe_status moe_rms_norm_backward(const moe_rms_norm_grad_args* a, voi
   const moe_status st = batch_device(&d);
   if (st != MOE_OK) return st;
   if (a->T == 0) return a->dgain ? done(cudaMemsetAsync(a->dgain, 0, (size_t)a->H * sizeof(float), (cudaStream_t)stream)) : MOE_OK;
-  return done(launch_rms_norm_grad(g, (cudaStream_t)stream));
+  return done(launch_rms_norm_grad(g, d.wait, (cudaStream_t)stream));
 }
 
 extern "C" moe_status moe_combine_rows(const moe_combine_args* a, void* stream) {

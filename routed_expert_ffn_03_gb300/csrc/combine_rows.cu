@@ -31,27 +31,6 @@ __device__ __forceinline__ void token_rows(const float* weights, const int* plac
   __syncthreads();
 }
 
-// chunk c (VEC) or element c of a row at `off` elements, as fp32
-template <bool VEC>
-__device__ __forceinline__ void load_word(const void* p, long long off, int c, int type, float (&v)[VEC ? CHUNK : 1]) {
-  if (!VEC) {
-    v[0] = one_value(p, off + c, type);
-  } else if (type == GT_FP32) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + off) + 2 * c;
-    const float4 a = __ldcs(s), b = __ldcs(s + 1);
-    const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < (VEC ? CHUNK : 1); ++i) v[i] = f[i];
-  } else {
-    const uint4 r = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + off) + c);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < (VEC ? CHUNK : 1); ++i) {
-      const float2 f = two_16(w[i / 2], type);
-      v[i] = i % 2 ? f.y : f.x;
-    }
-  }
-}
 template <bool VEC>
 __device__ __forceinline__ void store_word(void* p, long long off, int c, int type, const float (&v)[VEC ? CHUNK : 1]) {
   if constexpr (!VEC) {
@@ -66,8 +45,8 @@ __device__ __forceinline__ void store_word(void* p, long long off, int c, int ty
   }
 }
 
-// A block: a token, and one of gridDim.y runs of its columns.
-template <bool VEC, int YT>
+// A block: a token, and one of gridDim.y runs of its columns; RANKS rows at a time.
+template <bool VEC, int YT, int OT, int RANKS>
 __global__ void __launch_bounds__(CR_THREADS) combine_rows_kernel(const CombineRowsArgs a) {
   constexpr int N = VEC ? CHUNK : 1;
   __shared__ long long off[CR_MAX_K];
@@ -78,35 +57,33 @@ __global__ void __launch_bounds__(CR_THREADS) combine_rows_kernel(const CombineR
   token_rows(a.weights, a.places, t, a.k, a.y_rows, a.ldy, true, off, weight);
   const int words = a.H / N;
   for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < words; c += gridDim.y * blockDim.x) {
-    float sum[N], r[N];
+    float sum[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) sum[i] = r[i] = 0.f;
-    if (a.residual) load_word<VEC>(a.residual, t * a.ld_res, c, a.out_type, r);
-    for (int j0 = 0; j0 < a.k; j0 += CR_RANKS) {
-      float v[CR_RANKS][N];
+    for (int i = 0; i < N; ++i) sum[i] = 0.f;
+    Word<VEC, OT> res;
+    res.load(a.residual, t * a.ld_res, c, a.residual != nullptr);
+    for (int j0 = 0; j0 < a.k; j0 += RANKS) {
+      Word<VEC, YT> v[RANKS];
 #pragma unroll
-      for (int j = 0; j < CR_RANKS; ++j) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[j][i] = 0.f;
-        if (j0 + j < a.k && off[j0 + j] >= 0) load_word<VEC>(a.y, off[j0 + j], c, YT, v[j]);
+      for (int j = 0; j < RANKS; ++j) {
+        const long long o = j0 + j < a.k ? off[j0 + j] : -1;
+        v[j].load(a.y, o, c, o >= 0);
       }
 #pragma unroll
-      for (int j = 0; j < CR_RANKS; ++j) {
+      for (int j = 0; j < RANKS; ++j) {
         const float w = j0 + j < a.k && off[j0 + j] >= 0 ? weight[j0 + j] : 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum[i] = fmaf(w, v[j][i], sum[i]);
+        for (int i = 0; i < N; ++i) sum[i] = fmaf(w, v[j].get(i), sum[i]);
       }
     }
-    if (a.residual) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) sum[i] += r[i];
-    }
-    store_word<VEC>(a.out, t * a.ldo, c, a.out_type, sum);
+    for (int i = 0; i < N; ++i) sum[i] += res.get(i);
+    store_word<VEC>(a.out, t * a.ldo, c, OT, sum);
   }
 }
 
-// A block: a token, as the weights' gradients are sums over all of its columns.
-template <bool VEC, int YT>
+// A block: a token, as the weights' gradients are sums over all of its columns; RANKS rows at a time.
+template <bool VEC, int DT, int YT, int RANKS>
 __global__ void __launch_bounds__(1024) combine_grad_kernel(const CombineGradArgs a) {
   constexpr int N = VEC ? CHUNK : 1;
   __shared__ long long off[CR_MAX_K];
@@ -117,35 +94,35 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(const CombineGradArg
   const long long t = blockIdx.x;
   token_rows(a.weights, a.places, t, a.k, a.y_rows, 1, false, off, weight);
   const int words = a.H / N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int j0 = 0; j0 < a.k; j0 += CR_RANKS) {
-    float dot[CR_RANKS];
+  for (int j0 = 0; j0 < a.k; j0 += RANKS) {
+    float dot[RANKS];
 #pragma unroll
-    for (int j = 0; j < CR_RANKS; ++j) dot[j] = 0.f;
+    for (int j = 0; j < RANKS; ++j) dot[j] = 0.f;
     for (int c = threadIdx.x; c < words; c += blockDim.x) {
-      float d[N], v[CR_RANKS][N];
-      load_word<VEC>(a.dout, t * a.ld_dout, c, a.dout_type, d);
+      Word<VEC, DT> d;
+      Word<VEC, YT> v[RANKS];
+      d.load(a.dout, t * a.ld_dout, c, true);
 #pragma unroll
-      for (int j = 0; j < CR_RANKS; ++j) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[j][i] = 0.f;
-        if (j0 + j < a.k && off[j0 + j] >= 0) load_word<VEC>(a.y, off[j0 + j] * a.ldy, c, YT, v[j]);
+      for (int j = 0; j < RANKS; ++j) {
+        const long long o = j0 + j < a.k ? off[j0 + j] : -1;
+        v[j].load(a.y, o * a.ldy, c, o >= 0);
       }
 #pragma unroll
-      for (int j = 0; j < CR_RANKS; ++j) {
+      for (int j = 0; j < RANKS; ++j) {
         if (j0 + j < a.k && off[j0 + j] >= 0) {
           const float w = weight[j0 + j];
           float o[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            dot[j] = fmaf(d[i], v[j][i], dot[j]);
-            o[i] = w * d[i];
+            dot[j] = fmaf(d.get(i), v[j].get(i), dot[j]);
+            o[i] = w * d.get(i);
           }
-          store_word<VEC>(a.dy, off[j0 + j] * a.ld_dy, c, a.dy_type, o);
+          store_word<VEC>(a.dy, off[j0 + j] * a.ld_dy, c, YT, o);
         }
       }
     }
 #pragma unroll
-    for (int j = 0; j < CR_RANKS; ++j) {
+    for (int j = 0; j < RANKS; ++j) {
       if (j0 + j >= a.k) break;
       const float s = warp_sum(dot[j]);
       if (lane == 0) part[warp][j0 + j] = s;
@@ -176,6 +153,22 @@ cudaError_t launch(void (*kernel)(A), dim3 grid, int threads, cudaStream_t s, co
 bool chunks(const void* p, long long ld, int type) {
   return !p || ((uintptr_t)p % 16 == 0 && ld * (type == GT_FP32 ? 4 : 2) % 16 == 0);
 }
+// f with vec, two types and the rows at a time (2 where there are no more, for their registers) as constants
+template <typename F>
+cudaError_t by_types(bool vec, int t0, int t1, int k, F f) {
+  auto type = [](int t, auto g) {
+    if (t == GT_FP32) return g(std::integral_constant<int, GT_FP32>{});
+    return t == GT_BF16 ? g(std::integral_constant<int, GT_BF16>{}) : g(std::integral_constant<int, GT_FP16>{});
+  };
+  return type(t0, [&](auto a) {
+    return type(t1, [&](auto b) {
+      auto ranks = [&](auto v) {
+        return k <= 2 ? f(v, a, b, std::integral_constant<int, 2>{}) : f(v, a, b, std::integral_constant<int, CR_RANKS>{});
+      };
+      return vec ? ranks(std::true_type{}) : ranks(std::false_type{});
+    });
+  });
+}
 int warps_of(long long words, int most) {
   const long long t = (words + 31) / 32 * 32;
   return t < most ? (int)t : most;
@@ -191,27 +184,19 @@ cudaError_t launch_combine_rows(const CombineRowsArgs& a, cudaStream_t s) {
   const int threads = warps_of((words + runs - 1) / runs, CR_THREADS);   // even runs
   if (runs > 65535) runs = 65535;
   const dim3 grid((unsigned)a.T, (unsigned)runs);
-  auto go = [&](auto v) {
-    constexpr bool V = decltype(v)::value;
-    if (a.y_type == GT_FP32) return launch(combine_rows_kernel<V, GT_FP32>, grid, threads, s, a);
-    return a.y_type == GT_BF16 ? launch(combine_rows_kernel<V, GT_BF16>, grid, threads, s, a)
-                               : launch(combine_rows_kernel<V, GT_FP16>, grid, threads, s, a);
-  };
-  return vec ? go(std::true_type{}) : go(std::false_type{});
+  return by_types(vec, a.y_type, a.out_type, a.k, [&](auto v, auto yt, auto ot, auto ranks) {
+    return launch(combine_rows_kernel<decltype(v)::value, decltype(yt)::value, decltype(ot)::value, decltype(ranks)::value>, grid, threads, s, a);
+  });
 }
 
 cudaError_t launch_combine_rows_grad(const CombineGradArgs& a, cudaStream_t s) {
   const bool vec = a.H % CHUNK == 0 && chunks(a.dout, a.ld_dout, a.dout_type) && chunks(a.y, a.ldy, a.y_type) &&
                    chunks(a.dy, a.ld_dy, a.dy_type);
-  const int threads = warps_of(vec ? a.H / CHUNK : a.H, a.T <= 304 ? 1024 : 512);
+  const int threads = warps_of(vec ? a.H / CHUNK : a.H, a.T <= 304 ? 1024 : 128);
   const dim3 grid((unsigned)a.T);
-  auto go = [&](auto v) {
-    constexpr bool V = decltype(v)::value;
-    if (a.y_type == GT_FP32) return launch(combine_grad_kernel<V, GT_FP32>, grid, threads, s, a);
-    return a.y_type == GT_BF16 ? launch(combine_grad_kernel<V, GT_BF16>, grid, threads, s, a)
-                               : launch(combine_grad_kernel<V, GT_FP16>, grid, threads, s, a);
-  };
-  return vec ? go(std::true_type{}) : go(std::false_type{});
+  return by_types(vec, a.dout_type, a.y_type, a.k, [&](auto v, auto dt, auto yt, auto ranks) {
+    return launch(combine_grad_kernel<decltype(v)::value, decltype(dt)::value, decltype(yt)::value, decltype(ranks)::value>, grid, threads, s, a);
+  });
 }
 
 }  // namespace moe

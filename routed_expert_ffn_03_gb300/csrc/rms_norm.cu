@@ -33,8 +33,10 @@ __device__ __forceinline__ void row_reduce(float& a, float& b) {
   b = warp_max(p.y);
 }
 
-template <int NC, bool VEC, bool WARP>
+// Rows of any length and alignment, element by element.
+template <int NC, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) rms_norm_kernel(const NormArgs a) {
+  constexpr bool VEC = false;
   pdl_launch_dependents();
   pdl_wait();
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, stride = WARP ? 32 : blockDim.x;
@@ -72,6 +74,92 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) rms_norm_kernel(
     const float scale = fmaxf(top * rstd / E4M3_MAX, LEAST_SCALE);
     store_e4m3<NC, VEC>(a.out8 + t * a.ldo8, a.H, tid, stride, h, scale);
     if (tid == 0) a.scale[t] = scale;
+  }
+}
+
+// Aligned rows, types known: the row stays in registers as it lies (h in the type it was rounded to), half of what fp32 takes, so
+// that more of them are in flight; it is made fp32 twice instead.
+template <int XT, int HT, bool RES, int NC, bool WARP, int MAXT>
+__global__ void __launch_bounds__(MAXT) rms_norm_words_kernel(const NormArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, stride = WARP ? 32 : blockDim.x;
+  const long long t = WARP ? (long long)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5) : blockIdx.x;
+  if (t >= a.T) return;   // whole warps
+  auto row = [&](const void* p, long long ld, int type) { return static_cast<const char*>(p) + t * ld * (type == GT_FP32 ? 4 : 2); };
+  const int n = a.H / CHUNK;
+  Word<true, HT> h[NC];
+  {
+    Word<true, XT> x[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) x[i].load(row(a.x, a.ldx, XT), 0, tid + i * stride, tid + i * stride < n);
+    if constexpr (RES) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) h[i].load(row(a.residual, a.ld_res, HT), 0, tid + i * stride, tid + i * stride < n);
+      char* sum = const_cast<char*>(row(a.sum, a.ld_sum, HT));
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        float v[CHUNK];
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j) v[j] = x[i].get(j) + h[i].get(j);
+        h[i].set(v);
+        if (tid + i * stride < n) h[i].store(sum, tid + i * stride);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int q = 0; q < Word<true, XT>::REGS; ++q) h[i].r[q] = x[i].r[q];
+    }
+  }
+  float ss = 0.f, top = 0.f, rstd = 1.f;
+  // chunk i of y / rstd
+  auto scaled = [&](int i, float (&v)[CHUNK]) {
+#pragma unroll
+    for (int j = 0; j < CHUNK; ++j) v[j] = h[i].get(j);
+    if (a.gain && tid + i * stride < n) {
+      float g[CHUNK];
+      chunk_of<false>(a.gain, tid + i * stride, a.gain_type, g);
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) v[j] *= g[j];
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    if (a.norm) {
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) ss = fmaf(h[i].get(j), h[i].get(j), ss);
+    }
+    if (a.out8) {
+      if (HT != GT_FP32 && !a.gain) {
+        top = fmaxf(top, h[i].largest());
+      } else {
+        float v[CHUNK];
+        scaled(i, v);
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j) top = fmaxf(top, fabsf(v[j]));
+      }
+    }
+  }
+  row_reduce<WARP>(ss, top);
+  if (a.norm) rstd = rsqrtf(ss / (float)a.H + a.eps);
+  if (tid == 0 && a.rstd) a.rstd[t] = rstd;
+  const float scale = fmaxf(top * rstd / E4M3_MAX, LEAST_SCALE);
+  const Divisor by(scale);
+  if (tid == 0 && a.out8) a.scale[t] = scale;
+  char* out = const_cast<char*>(row(a.out, a.ldo, a.out_type));
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = tid + i * stride;
+    if (c >= n) break;
+    float v[CHUNK];
+    scaled(i, v);
+    if (a.norm) {
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) v[j] *= rstd;
+    }
+    if (a.out) put_chunk(out, c, a.out_type, v);
+    if (a.out8) reinterpret_cast<uint2*>(a.out8 + t * a.ldo8)[c] = e4m3_chunk(v, by);
   }
 }
 
@@ -152,6 +240,141 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) rms_norm_grad_ke
   }
 }
 
+// Aligned rows of a block: one block an SM, the rows of dy, h and dsum copied ahead into a ring of `stages` in shared memory, so that
+// they arrive while the row before them waits for its sum.  Everything of a stage is read before the barrier of its row's sum, so
+// behind it the stage is filled again.
+struct GradRing {
+  int stages;
+  uint32_t dy_bytes, h_bytes, dsum_bytes;   // of a row
+  WaitLimit wait;
+};
+constexpr int RING_MAX = 8;
+template <int NC>
+__global__ void __launch_bounds__(512, 1) rms_norm_grad_ring_kernel(const NormGradArgs a, const GradRing ring) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float part[2][32];
+  __shared__ uint64_t bars[RING_MAX];
+  __shared__ int gave_up[2];   // by the row's turn, as the sums
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, stride = blockDim.x, n = a.H / CHUNK;
+  const uint32_t stage = ring.dy_bytes + ring.h_bytes + ring.dsum_bytes, bytes = stage;
+  if (tid == 0) {
+    for (int s = 0; s < ring.stages; ++s) mbar_init(smem_u32(bars + s), 1 + (ring.wait.cycles == 0));
+    gave_up[0] = gave_up[1] = 0;
+    mbar_fence_init();
+  }
+  __syncthreads();
+  pdl_launch_dependents();
+  pdl_wait();
+  auto fill = [&](long long t, int s) {   // thread 0
+    const uint32_t bar = smem_u32(bars + s), at = smem_u32(smem) + s * stage;
+    auto row = [&](const void* p, long long ld, uint32_t row_bytes) {
+      return static_cast<const char*>(p) + t * ld * (row_bytes / (uint32_t)a.H);
+    };
+    mbar_arrive_expect_tx(bar, bytes);
+    bulk_g2s(at, row(a.dy, a.ld_dy, ring.dy_bytes), ring.dy_bytes, bar);
+    bulk_g2s(at + ring.dy_bytes, row(a.h, a.ld_h, ring.h_bytes), ring.h_bytes, bar);
+    if (a.dsum) bulk_g2s(at + ring.dy_bytes + ring.h_bytes, row(a.dsum, a.ld_dsum, ring.dsum_bytes), ring.dsum_bytes, bar);
+  };
+  const long long first = blockIdx.x, step = gridDim.x;
+  if (tid == 0)
+    for (int s = 0; s < ring.stages; ++s)
+      if (first + s * step < a.T) fill(first + s * step, s);
+  float dg[NC * CHUNK], g[NC * CHUNK];
+#pragma unroll
+  for (int j = 0; j < NC * CHUNK; ++j) {
+    dg[j] = 0.f;
+    g[j] = 1.f;
+  }
+  if (a.gain) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (tid + i * stride < n) {
+        float v[CHUNK];
+        chunk_of<false>(a.gain, tid + i * stride, a.gain_type, v);
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j) g[i * CHUNK + j] = v[j];
+      }
+  }
+  int s = 0, turn = 0;
+  uint32_t parity = 0;
+  for (long long t = first; t < a.T; t += step, turn ^= 1) {
+    const float rstd = __ldg(a.rstd + t);
+    if (!mbar_wait_bounded(smem_u32(bars + s), parity, ring.wait.cycles)) gave_up[turn] = 1;
+    const uint8_t* at = smem + s * stage;
+    float nv[NC * CHUNK], d[NC * CHUNK], dot = 0.f;
+    Word<true, GT_FP32> ds[NC];   // as it lies
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = tid + i * stride;
+      if (c < n) {
+        float x[CHUNK], y[CHUNK];
+        chunk_of<true>(at, c, a.dy_type, y);
+        chunk_of<true>(at + ring.dy_bytes, c, a.h_type, x);
+        if (a.dsum) {
+          const uint4* q = reinterpret_cast<const uint4*>(at + ring.dy_bytes + ring.h_bytes) + (a.dsum_type == GT_FP32 ? 2 * c : c);
+          const uint4 lo = q[0], hi = a.dsum_type == GT_FP32 ? q[1] : lo;
+          const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int j = 0; j < CHUNK; ++j) ds[i].r[j] = w[j];
+        }
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j) {
+          const int k = i * CHUNK + j;
+          nv[k] = x[j] * rstd;
+          dg[k] = fmaf(y[j], nv[k], dg[k]);
+          d[k] = y[j] * g[k];
+          dot = fmaf(d[k], nv[k], dot);
+        }
+      }
+    }
+    dot = warp_sum(dot);
+    if (lane == 0) part[turn][warp] = dot;   // (two in turn: the one before may still be read)
+    __syncthreads();
+    if (gave_up[turn]) break;   // the same in all threads
+    if (tid == 0 && t + ring.stages * step < a.T) fill(t + ring.stages * step, s);
+    dot = warp_sum(lane < (stride >> 5) ? part[turn][lane] : 0.f) / (float)a.H;
+    char* out = static_cast<char*>(a.dh) + t * a.ld_dh * (a.dh_type == GT_FP32 ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = tid + i * stride;
+      if (c < n) {
+        float v[CHUNK];
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j) v[j] = rstd * fmaf(-nv[i * CHUNK + j], dot, d[i * CHUNK + j]);
+        if (a.dsum) {
+#pragma unroll
+          for (int j = 0; j < CHUNK; ++j) {
+            const float2 f = two_16(ds[i].r[j / 2], a.dsum_type);
+            v[j] += a.dsum_type == GT_FP32 ? ds[i].get(j) : j % 2 ? f.y : f.x;
+          }
+        }
+        put_chunk(out, c, a.dh_type, v);
+      }
+    }
+    if (++s == ring.stages) {
+      s = 0;
+      parity ^= 1;
+    }
+  }
+  if (gave_up[turn]) {   // a wait ran out: report, and let the copies in flight end before the memory goes
+    if (tid == 0) {
+      *reinterpret_cast<volatile uint32_t*>(ring.wait.status) = ST_TIMEOUT;
+      __threadfence_system();
+    }
+    const long long t0 = clock64();
+    while (clock64() - t0 < 100000000ll) __nanosleep(1000);
+    return;
+  }
+  if (!a.dgain) return;
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+    if (tid + i * stride < n) {
+      float* out = a.partial + (long long)blockIdx.x * a.H + (tid + i * stride) * CHUNK;
+      reinterpret_cast<float4*>(out)[0] = make_float4(dg[i * CHUNK], dg[i * CHUNK + 1], dg[i * CHUNK + 2], dg[i * CHUNK + 3]);
+      reinterpret_cast<float4*>(out)[1] = make_float4(dg[i * CHUNK + 4], dg[i * CHUNK + 5], dg[i * CHUNK + 6], dg[i * CHUNK + 7]);
+    }
+}
+
 // dgain = the blocks' sums: 32 columns a block, 8 parts of the rows, each in order
 constexpr int SUM_PARTS = 8;
 __global__ void __launch_bounds__(32 * SUM_PARTS) sum_blocks_kernel(const float* partial, float* out, int blocks, int H) {
@@ -193,6 +416,7 @@ struct Share {
   int nc, threads;
 };
 constexpr int WARP_H = 1024;   // the longest row of a warp
+constexpr int RING_BLOCKS = 152;   // one an SM; a constant, as norm_grad_blocks
 Share share_of(int H, int most_nc) {
   if (H <= WARP_H) return {true, H <= 256 ? 1 : H <= 512 ? 2 : 4, 32 * ROW_WARPS};
   int nc = 1;
@@ -208,21 +432,49 @@ bool chunks(const void* p, long long ld, int type) { return !p || (multiple(p, 1
 }  // namespace
 
 cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
-  const Share sh = share_of(a.H, a.T <= num_sms ? 1 : 4);
   const bool vec = a.H % CHUNK == 0 && chunks(a.x, a.ldx, a.x_type) && chunks(a.residual, a.ld_res, a.res_type) &&
                    chunks(a.residual ? a.sum : nullptr, a.ld_sum, a.res_type) && chunks(a.gain, 0, a.gain_type) &&
                    chunks(a.out, a.ldo, a.out_type) && (!a.out8 || (multiple(a.out8, 8) && a.ldo8 % 8 == 0));
-  const long long blocks = sh.warp ? ((long long)a.T + ROW_WARPS - 1) / ROW_WARPS : a.T;
-  auto go = [&](auto nc, auto v, auto w) {
-    return launch(rms_norm_kernel<decltype(nc)::value, decltype(v)::value, decltype(w)::value>, blocks, sh.threads, 0, s, a);
+  using std::integral_constant;
+  using True = std::true_type;
+  using False = std::false_type;
+  if (!vec) {
+    const Share sh = share_of(a.H, 4);
+    const long long blocks = sh.warp ? ((long long)a.T + ROW_WARPS - 1) / ROW_WARPS : a.T;
+    auto go = [&](auto nc, auto w) {
+      return launch(rms_norm_kernel<decltype(nc)::value, decltype(w)::value>, blocks, sh.threads, 0, s, a);
+    };
+    auto with = [&](auto nc) { return sh.warp ? go(nc, True{}) : go(nc, False{}); };
+    return sh.nc == 1 ? with(integral_constant<int, 1>{}) : sh.nc == 2 ? with(integral_constant<int, 2>{}) : with(integral_constant<int, 4>{});
+  }
+  // A warp a row up to WARP_H, else a block: of few chunks a thread where there are fewer rows than SMs (latency), four otherwise.
+  const bool warp = a.H <= WARP_H;
+  const int nc = warp ? (a.H <= 256 ? 1 : a.H <= 512 ? 2 : 4) : a.T <= num_sms && a.H <= 8192 ? 1 : 4;
+  const long long blocks = warp ? ((long long)a.T + ROW_WARPS - 1) / ROW_WARPS : a.T;
+  const int threads = warp ? 32 * ROW_WARPS : (a.H / CHUNK + nc * 32 - 1) / (nc * 32) * 32;
+  auto types = [&](auto xt, auto ht, auto res) {
+    auto go = [&](auto c, auto w, auto most) {
+      return launch(rms_norm_words_kernel<decltype(xt)::value, decltype(ht)::value, decltype(res)::value, decltype(c)::value,
+                                          decltype(w)::value, decltype(most)::value>,
+                    blocks, threads, 0, s, a);
+    };
+    using W = integral_constant<int, 32 * ROW_WARPS>;
+    if (warp)
+      return nc == 1   ? go(integral_constant<int, 1>{}, True{}, W{})
+             : nc == 2 ? go(integral_constant<int, 2>{}, True{}, W{})
+                       : go(integral_constant<int, 4>{}, True{}, W{});
+    if (nc == 1) return go(integral_constant<int, 1>{}, False{}, integral_constant<int, 1024>{});
+    return threads <= 512 ? go(integral_constant<int, 4>{}, False{}, integral_constant<int, 512>{})
+                          : go(integral_constant<int, 4>{}, False{}, integral_constant<int, 1024>{});
   };
-  auto with = [&](auto nc) {
-    using T = std::true_type;
-    using F = std::false_type;
-    return sh.warp ? (vec ? go(nc, T{}, T{}) : go(nc, F{}, T{})) : vec ? go(nc, T{}, F{}) : go(nc, F{}, F{});
+  auto of = [](int type, auto f) {
+    if (type == GT_FP32) return f(integral_constant<int, GT_FP32>{});
+    return type == GT_BF16 ? f(integral_constant<int, GT_BF16>{}) : f(integral_constant<int, GT_FP16>{});
   };
-  if (sh.nc == 1) return with(std::integral_constant<int, 1>{});
-  return sh.nc == 2 ? with(std::integral_constant<int, 2>{}) : with(std::integral_constant<int, 4>{});
+  return of(a.x_type, [&](auto xt) {
+    if (!a.residual) return types(xt, xt, False{});
+    return of(a.res_type, [&](auto rt) { return types(xt, rt, True{}); });
+  });
 }
 
 int norm_grad_blocks(int T, int H) {
@@ -231,23 +483,49 @@ int norm_grad_blocks(int T, int H) {
   return need < most ? need : most;
 }
 
-cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
-  const Share sh = share_of(a.H, 1);
+namespace {
+constexpr size_t RING_BYTES = 200 * 1024;
+template <int NC>
+cudaError_t launch_ring(const NormGradArgs& a, const GradRing& r, int blocks, cudaStream_t s) {
+  const int threads = (a.H / CHUNK + NC * 32 - 1) / (NC * 32) * 32;
+  return launch(rms_norm_grad_ring_kernel<NC>, blocks, threads, (size_t)r.stages * (r.dy_bytes + r.h_bytes + r.dsum_bytes), s, a, r);
+}
+}  // namespace
+
+cudaError_t rms_norm_set_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(rms_norm_grad_ring_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(rms_norm_grad_ring_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(rms_norm_grad_ring_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES);
+  return e;
+}
+
+cudaError_t launch_rms_norm_grad(const NormGradArgs& a, const WaitLimit& wait, cudaStream_t s) {
   const bool vec = a.H % CHUNK == 0 && chunks(a.dy, a.ld_dy, a.dy_type) && chunks(a.h, a.ld_h, a.h_type) &&
                    chunks(a.gain, 0, a.gain_type) && chunks(a.dsum, a.ld_dsum, a.dsum_type) && chunks(a.dh, a.ld_dh, a.dh_type);
-  const int blocks = norm_grad_blocks(a.T, a.H);
-  const size_t smem = sh.warp && a.dgain ? (size_t)ROW_WARPS * a.H * sizeof(float) : 0;   // 32 KB at most
-  auto go = [&](auto nc, auto v, auto w) {
-    return launch(rms_norm_grad_kernel<decltype(nc)::value, decltype(v)::value, decltype(w)::value>, blocks, sh.threads, smem, s, a);
-  };
-  auto with = [&](auto nc) {
-    using T = std::true_type;
-    using F = std::false_type;
-    return sh.warp ? (vec ? go(nc, T{}, T{}) : go(nc, F{}, T{})) : vec ? go(nc, T{}, F{}) : go(nc, F{}, F{});
-  };
-  cudaError_t e = sh.nc == 1   ? with(std::integral_constant<int, 1>{})
-                  : sh.nc == 2 ? with(std::integral_constant<int, 2>{})
-                               : with(std::integral_constant<int, 4>{});
+  int blocks = norm_grad_blocks(a.T, a.H);
+  cudaError_t e;
+  GradRing ring{0, (uint32_t)(a.H * bytes_of(a.dy_type)), (uint32_t)(a.H * bytes_of(a.h_type)),
+                a.dsum ? (uint32_t)(a.H * bytes_of(a.dsum_type)) : 0u, wait};
+  const size_t fit = RING_BYTES / (ring.dy_bytes + ring.h_bytes + ring.dsum_bytes);
+  ring.stages = fit < RING_MAX ? (int)fit : RING_MAX;
+  if (vec && a.H > WARP_H && a.H <= 16384 && ring.stages >= 2) {
+    if (blocks > RING_BLOCKS) blocks = RING_BLOCKS;
+    e = a.H <= 4096 ? launch_ring<1>(a, ring, blocks, s) : a.H <= 8192 ? launch_ring<2>(a, ring, blocks, s) : launch_ring<4>(a, ring, blocks, s);
+  } else {
+    const Share sh = share_of(a.H, 1);
+    const size_t smem = sh.warp && a.dgain ? (size_t)ROW_WARPS * a.H * sizeof(float) : 0;   // 32 KB at most
+    auto go = [&](auto nc, auto v, auto w) {
+      return launch(rms_norm_grad_kernel<decltype(nc)::value, decltype(v)::value, decltype(w)::value>, blocks, sh.threads, smem, s, a);
+    };
+    auto with = [&](auto nc) {
+      using T = std::true_type;
+      using F = std::false_type;
+      return sh.warp ? (vec ? go(nc, T{}, T{}) : go(nc, F{}, T{})) : vec ? go(nc, T{}, F{}) : go(nc, F{}, F{});
+    };
+    e = sh.nc == 1   ? with(std::integral_constant<int, 1>{})
+        : sh.nc == 2 ? with(std::integral_constant<int, 2>{})
+                     : with(std::integral_constant<int, 4>{});
+  }
   if (e == cudaSuccess && a.dgain)
     e = launch(sum_blocks_kernel, (a.H + 31) / 32, 32 * SUM_PARTS, 0, s, (const float*)a.partial, a.dgain, blocks, a.H);
   return e;

@@ -2,6 +2,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include "grouped.h"
+
 #include <cstddef>
 #include <cstdint>
 
@@ -32,6 +34,7 @@ struct NormGradArgs {
 // Blocks that the gain's gradient is summed over, a function of the sizes alone, so that neither the workspace nor the bits depend
 // on the device.
 int norm_grad_blocks(int T, int H);
-cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s);
+cudaError_t launch_rms_norm_grad(const NormGradArgs& a, const WaitLimit& wait, cudaStream_t s);
+cudaError_t rms_norm_set_attributes();
 
 }  // namespace moe

@@ -120,21 +120,90 @@ __device__ __forceinline__ void store_row(void* row, int dtype, int H, int tid, 
   }
 }
 
+// Word c of a row at `off` elements, as it lies: 8 elements (VEC) or one.  Predicated, not branched around, so that the loads of
+// several rows are in flight together.
+template <bool VEC, int TYPE>
+struct Word {
+  static constexpr int N = VEC ? CHUNK : 1, REGS = VEC ? (TYPE == GT_FP32 ? 8 : 4) : 1;
+  uint32_t r[REGS];
+  __device__ __forceinline__ void load(const void* p, long long off, int c, bool in) {
+    const char* s = static_cast<const char*>(p) + (off + (long long)c * N) * (TYPE == GT_FP32 ? 4 : 2);
+    if constexpr (VEC) {
+#pragma unroll
+      for (int q = 0; q < REGS; q += 4)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
+            " @p ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
+            : "=&r"(r[q]), "=&r"(r[q + 1]), "=&r"(r[q + 2]), "=&r"(r[q + 3])
+            : "l"(s + 4 * q), "r"((uint32_t)in)
+            : "memory");
+    } else if constexpr (TYPE == GT_FP32) {
+      asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.u32 %0, 0;\n @p ld.global.cs.u32 %0, [%1];\n}\n"
+                   : "=&r"(r[0])
+                   : "l"(s), "r"((uint32_t)in)
+                   : "memory");
+    } else {
+      uint16_t h;
+      asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.u16 %0, 0;\n @p ld.global.cs.u16 %0, [%1];\n}\n"
+                   : "=&h"(h)
+                   : "l"(s), "r"((uint32_t)in)
+                   : "memory");
+      r[0] = h;
+    }
+  }
+  __device__ __forceinline__ void store(void* p, int c) const {   // (VEC)
+    uint4* d = reinterpret_cast<uint4*>(static_cast<char*>(p) + (long long)c * REGS * 4);
+#pragma unroll
+    for (int q = 0; q < REGS; q += 4) d[q / 4] = make_uint4(r[q], r[q + 1], r[q + 2], r[q + 3]);
+  }
+  __device__ __forceinline__ void set(const float (&v)[N]) {   // (VEC) rounded to the type
+#pragma unroll
+    for (int i = 0; i < REGS; ++i) r[i] = TYPE == GT_FP32 ? __float_as_uint(v[i]) : pack_16(v[2 * i % N], v[(2 * i + 1) % N], TYPE);
+  }
+  // the largest magnitude, two at a time (16 bits, VEC); NaN is passed over, as by fmaxf
+  __device__ __forceinline__ float largest() const {
+    auto pair = [&](auto two) {
+      using P = decltype(two);
+      auto at = [&](int q) { return __habs2(*reinterpret_cast<const P*>(&r[q])); };
+      return __hmax2(__hmax2(at(0), at(1 % REGS)), __hmax2(at(2 % REGS), at(3 % REGS)));
+    };
+    if constexpr (TYPE == GT_BF16) {
+      const float2 f = __bfloat1622float2(pair(__nv_bfloat162()));
+      return fmaxf(f.x, f.y);
+    } else {
+      const float2 f = __half22float2(pair(__half2()));
+      return fmaxf(f.x, f.y);
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {   // i: a constant once unrolled
+    if (TYPE == GT_FP32) return __uint_as_float(r[i]);
+    const float2 f = two_16(r[i / 2], TYPE);
+    return i % 2 ? f.y : f.x;
+  }
+};
 // y / scale rounded to nearest, inv = 1 / scale: the product's remainder added (Markstein, IBM J. Res. Dev. 34, 1990).  With the
 // product alone quotients that lie on a border between two e4m3 numbers go either way, which is common for 16-bit rows: 1 value in
 // 700, and an error of 3.8e-3 instead of 1.7e-3 in a bf16 product that reads them.
-__device__ __forceinline__ float quotient(float y, float scale, float inv) {
-  const float q = y * inv;
-  return fmaf(fmaf(-q, scale, y), inv, q);
-}
+// An infinite scale has no remainder: finite values are 0, infinite ones NaN.
+struct Divisor {
+  float inv, scale, back;
+  __device__ __forceinline__ explicit Divisor(float s) : inv(1.f / s), scale(s < INFINITY ? s : 0.f), back(s < INFINITY ? inv : 0.f) {}
+  __device__ __forceinline__ float operator()(float y) const {
+    const float q = y * inv;
+    return fmaf(fmaf(-q, scale, y), back, q);
+  }
+};
 // e4m3, to nearest, at most 448 (NaN stays NaN)
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
+__device__ __forceinline__ uint2 e4m3_chunk(const float* s, const Divisor& by) {
+  auto q = [&](int i) { return by(s[i]); };
+  return make_uint2(e4m3_pair(q(0), q(1)) | e4m3_pair(q(2), q(3)) << 16, e4m3_pair(q(4), q(5)) | e4m3_pair(q(6), q(7)) << 16);
+}
 template <int NC, bool VEC>
 __device__ __forceinline__ void store_e4m3(uint8_t* row, int H, int tid, int stride, const float (&v)[NC * CHUNK], float scale) {
-  const float inv = 1.f / scale;
-  auto q = [&](float y) { return quotient(y, scale, inv); };
+  const Divisor q(scale);
   if (!VEC) {
 #pragma unroll
     for (int j = 0; j < NC * CHUNK; ++j) {
@@ -147,11 +216,37 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, int H, int tid, int str
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = tid + i * stride;
-    const float* s = v + i * CHUNK;
     if (c >= n) break;
-    reinterpret_cast<uint2*>(row)[c] =
-        make_uint2(e4m3_pair(q(s[0]), q(s[1])) | e4m3_pair(q(s[2]), q(s[3])) << 16,
-                   e4m3_pair(q(s[4]), q(s[5])) | e4m3_pair(q(s[6]), q(s[7])) << 16);
+    reinterpret_cast<uint2*>(row)[c] = e4m3_chunk(v + i * CHUNK, q);
+  }
+}
+
+// 8 elements of a type known at run time, from read-only or shared memory
+template <bool SHARED>
+__device__ __forceinline__ void chunk_of(const void* p, int c, int type, float (&v)[CHUNK]) {
+  auto word = [&](int i) { return SHARED ? static_cast<const uint4*>(p)[i] : __ldg(static_cast<const uint4*>(p) + i); };
+  if (type == GT_FP32) {
+    const uint4 a = word(2 * c), b = word(2 * c + 1);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) v[i] = __uint_as_float(w[i]);
+  } else {
+    const uint4 a = word(c);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) {
+      const float2 f = two_16(w[i / 2], type);
+      v[i] = i % 2 ? f.y : f.x;
+    }
+  }
+}
+__device__ __forceinline__ void put_chunk(void* p, int c, int type, const float (&v)[CHUNK]) {
+  if (type == GT_FP32) {
+    static_cast<float4*>(p)[2 * c] = make_float4(v[0], v[1], v[2], v[3]);
+    static_cast<float4*>(p)[2 * c + 1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    static_cast<uint4*>(p)[c] =
+        make_uint4(pack_16(v[0], v[1], type), pack_16(v[2], v[3], type), pack_16(v[4], v[5], type), pack_16(v[6], v[7], type));
   }
 }
 
