@@ -106,6 +106,7 @@ def _lib():
 
 _torch = None
 _types = {}
+_devices = {}
 _raw_stream = None    # torch's current stream of a device as an address, without a Stream object (2 us less)
 _current = None       # the current device's index
 
@@ -184,9 +185,12 @@ def _pitch(stride, size, least):
 def _new(stream, index, *wanted):
     """New tensors of the given (shape, dtype), belonging to the stream that will use them."""
     torch = _torch
-    dev = torch.device("cuda", index)
+    dev = _devices.get(index)
+    if dev is None:
+        dev = _devices[index] = torch.device("cuda", index)
     if stream is None:
-        return [torch.empty(s, dtype=t, device=dev) for s, t in wanted]
+        empty = torch.empty
+        return [empty(s, dtype=t, device=dev) for s, t in wanted]
     s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
     with torch.cuda.stream(s):
         return [torch.empty(s, dtype=t, device=dev) for s, t in wanted]
@@ -267,13 +271,16 @@ def balanced_route(logits, k, bias=None, router=ROUTER_SOFTMAX, groups=1, keep=1
         if k < 1:
             raise ValueError("k: at least 1, got %d" % k)
         out = tuple(_new(stream, dev, (TK, i32), (TK, torch.float32), ((E + 1,), i32), (P, i32), (P, i32), (TK, i32)))
-    idx, weights, offsets, rows, pairs, places = out
+        at = [t.data_ptr() for t in out]
+    else:
+        idx, weights, offsets, rows, pairs, places = out
+        at = (_flat(idx, "out: idx", i32, TK, dev), _flat(weights, "out: weights", torch.float32, TK, dev),
+              _flat(offsets, "out: offsets", i32, (E + 1,), dev), _flat(rows, "out: rows", i32, P, dev),
+              _flat(pairs, "out: pairs", i32, P, dev), _flat(places, "out: places", i32, TK, dev))
     ws, ws_bytes, _held = _space(workspace, _route_space(T, E, k), stream, dev)
     a = _pack_balanced(
-        logits.data_ptr(), 0 if bias is None else _flat(bias, "bias", torch.float32, (E,), dev), _flat(idx, "out: idx", i32, TK, dev),
-        _flat(weights, "out: weights", torch.float32, TK, dev), _flat(offsets, "out: offsets", i32, (E + 1,), dev),
-        _flat(rows, "out: rows", i32, P, dev), _flat(pairs, "out: pairs", i32, P, dev), _flat(places, "out: places", i32, TK, dev),
-        _pitch(stride[0], T, E), T, E, k, dt, router, groups, keep, score, bool(renormalize), scale, ws, ws_bytes)
+        logits.data_ptr(), 0 if bias is None else _flat(bias, "bias", torch.float32, (E,), dev), *at, _pitch(stride[0], T, E), T, E, k,
+        dt, router, groups, keep, score, bool(renormalize), scale, ws, ws_bytes)
     _run("moe_balanced_route", L.moe_balanced_route, dev, stream, a)
     return out
 

@@ -49,6 +49,10 @@ class Norm(NamedTuple):
     scale: Optional[object]   # [T] fp32, with out8
 
 
+_NOTHING = Norm(None, None, None, None, None)
+_WANT = frozenset(("out", "out8", "rstd"))
+
+
 @functools.lru_cache(4096)
 def _norm_grad_space(T, H):
     return B._lib().moe_rms_norm_backward_workspace(T, H)
@@ -92,60 +96,71 @@ def rms_norm(x, gain=None, residual=None, eps=1e-6, want=("out",), out_dtype=Non
     dev = _cuda(x, "x")
     (T, H), stride = _dense(x, "x", 2, dev)
     dt = _type(x, "x")
-    o, total, rstd, out8, scale = out if out is not None else (None,) * 5
     f32 = torch.float32
     for w in want:
-        if w not in ("out", "out8", "rstd"):
+        if w not in _WANT:
             raise ValueError("want: any of 'out', 'out8', 'rstd', got %r" % (w,))
+    old = out if out is not None else _NOTHING
+    # what is new is made as it is passed on, so it needs no check
     new = []
-    if "out" not in want:
-        o = None
-    elif o is None:
-        new.append(((T, H), out_dtype or x.dtype))
-    elif out_dtype is not None and o.dtype != out_dtype:
-        raise ValueError("out: %s, wanted %s" % (o.dtype, out_dtype))
-    if residual is None:
-        total = None
-    elif total is None:
-        new.append(((T, H), residual.dtype))
-    if "rstd" not in want:
-        rstd = None
-    elif rstd is None:
-        new.append(((T,), f32))
-    if "out8" not in want:
-        out8 = scale = None
-    else:
-        if out8 is None:
-            new.append(((T, H), torch.float8_e4m3fn))
-        if scale is None:
-            new.append(((T,), f32))
-    if new:
-        made = iter(_new(stream, dev, *new))
-        if "out" in want and o is None:
-            o = next(made)
-        if residual is not None and total is None:
-            total = next(made)
-        if "rstd" in want and rstd is None:
-            rstd = next(made)
-        if "out8" in want:
-            out8 = next(made) if out8 is None else out8
-            scale = next(made) if scale is None else scale
-    r_at = r_ld = r_dt = s_at = s_ld = o_at = o_ld = o_dt = q_at = q_ld = 0
+    o = total = rstd = out8 = scale = None
+    o_at = o_ld = o_dt = r_at = r_ld = r_dt = s_at = s_ld = d_at = q_at = q_ld = c_at = 0
+    if "out" in want:
+        if old.out is None:
+            new.append(((T, H), out_dtype or x.dtype))
+        else:
+            o = old.out
+            if out_dtype is not None and o.dtype != out_dtype:
+                raise ValueError("out: %s, wanted %s" % (o.dtype, out_dtype))
+            o_at, o_ld, o_dt = _rows(o, "out", T, H, dev)
     if residual is not None:
         r_at, r_ld, r_dt = _rows(residual, "residual", T, H, dev)
-        s_at, s_ld, s_dt = _rows(total, "out: sum", T, H, dev)
-        if s_dt != r_dt:
-            raise ValueError("out: sum: %s, the residual has %s" % (total.dtype, residual.dtype))
-    if o is not None:
-        o_at, o_ld, o_dt = _rows(o, "out", T, H, dev)
-    if out8 is not None:
-        q_at, q_ld = _rows8(out8, "out: out8", T, H, dev)
+        if old.sum is None:
+            new.append(((T, H), residual.dtype))
+        else:
+            total = old.sum
+            s_at, s_ld, s_dt = _rows(total, "out: sum", T, H, dev)
+            if s_dt != r_dt:
+                raise ValueError("out: sum: %s, the residual has %s" % (total.dtype, residual.dtype))
+    if "rstd" in want:
+        if old.rstd is None:
+            new.append(((T,), f32))
+        else:
+            rstd = old.rstd
+            d_at = _flat(rstd, "out: rstd", f32, (T,), dev)
+    if "out8" in want:
+        if old.out8 is None:
+            new.append(((T, H), torch.float8_e4m3fn))
+        else:
+            out8 = old.out8
+            q_at, q_ld = _rows8(out8, "out: out8", T, H, dev)
+        if old.scale is None:
+            new.append(((T,), f32))
+        else:
+            scale = old.scale
+            c_at = _flat(scale, "out: scale", f32, (T,), dev)
+    if new:
+        made = _new(stream, dev, *new)[::-1]
+        if "out" in want and o is None:
+            o = made.pop()
+            o_at, o_ld, o_dt = o.data_ptr(), H, _type(o, "out")
+        if residual is not None and total is None:
+            total = made.pop()
+            s_at, s_ld = total.data_ptr(), H
+        if "rstd" in want and rstd is None:
+            rstd = made.pop()
+            d_at = rstd.data_ptr()
+        if "out8" in want:
+            if out8 is None:
+                out8 = made.pop()
+                q_at, q_ld = out8.data_ptr(), H
+            if scale is None:
+                scale = made.pop()
+                c_at = scale.data_ptr()
     g_at, g_dt = _gain(gain, H, dev)
     if T:
-        a = _pack_norm(
-            x.data_ptr(), r_at, g_at, s_at, o_at, q_at, 0 if scale is None else _flat(scale, "out: scale", f32, (T,), dev),
-            0 if rstd is None else _flat(rstd, "out: rstd", f32, (T,), dev), _pitch(stride[0], T, H), r_ld, s_ld, o_ld, q_ld, T, H, dt,
-            r_dt, g_dt, o_dt, eps)
+        a = _pack_norm(x.data_ptr(), r_at, g_at, s_at, o_at, q_at, c_at, d_at, _pitch(stride[0], T, H), r_ld, s_ld, o_ld, q_ld, T, H, dt,
+                       r_dt, g_dt, o_dt, eps)
         _run("moe_rms_norm", L.moe_rms_norm, dev, stream, a)
     return Norm(o, total, rstd, out8, scale)
 
@@ -194,8 +209,10 @@ def quantize_rows(x, out=None, stream=None):
     dt = _type(x, "x")
     if out is None:
         out = tuple(_new(stream, dev, ((T, H), torch.float8_e4m3fn), ((T,), torch.float32)))
-    q_at, q_ld = _rows8(out[0], "out: x8", T, H, dev)
-    scale = _flat(out[1], "out: scale", torch.float32, (T,), dev)
+        q_at, q_ld, scale = out[0].data_ptr(), H, out[1].data_ptr()
+    else:
+        q_at, q_ld = _rows8(out[0], "out: x8", T, H, dev)
+        scale = _flat(out[1], "out: scale", torch.float32, (T,), dev)
     if T:
         _run("moe_quantize_rows", L.moe_quantize_rows, dev, stream, x.data_ptr(), _pitch(stride[0], T, H), dt, T, H, q_at, q_ld, scale)
     return out
@@ -221,9 +238,11 @@ def combine_rows(y, weights, places=None, residual=None, out=None, out_dtype=Non
     T, k = TK
     if out is None:
         out, = _new(stream, dev, ((T, H), out_dtype or (y.dtype if residual is None else residual.dtype)))
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out: %s, wanted %s" % (out.dtype, out_dtype))
-    o_at, o_ld, o_dt = _rows(out, "out", T, H, dev)
+        o_at, o_ld, o_dt = out.data_ptr(), H, _type(out, "out")
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out: %s, wanted %s" % (out.dtype, out_dtype))
+        o_at, o_ld, o_dt = _rows(out, "out", T, H, dev)
     r_at = r_ld = 0
     if residual is not None:
         r_at, r_ld, r_dt = _rows(residual, "residual", T, H, dev)

@@ -6,7 +6,7 @@
 // Experts are chosen as if scores were compared in 64 bits, so that the choice does not depend on how fp32 rounds an
 // exponential.  Scores are fp32 first, with a bound on their error; only where two neighbours in the order are closer than
 // that are they computed again in fp64: of one token in some thousands, for the candidates alone, one a lane.  (fp64 runs at a
-// 64th of fp32's rate: all of 256 scores take 4 us.)  Where that does not decide it (groups that close, more
+// 64th of fp32's rate: all of 256 scores take 4 us.)  Where that does not decide it (a group's own best that close, more
 // candidates than lanes, scores that underflow) all of the token's scores are.
 #pragma once
 #include "group_route.h"
@@ -44,6 +44,64 @@ __device__ __forceinline__ void balanced_tables(const GroupRouteArgs& a, Balance
 
 __device__ __forceinline__ float key_value(uint32_t k) { return k ? key_logit(k) : -INFINITY; }
 __device__ __forceinline__ float warp_max_f(float v) { return key_value(__reduce_max_sync(0xffffffffu, v > -INFINITY ? logit_key(v) : 0u)); }
+
+// order-preserving key of a number (not NaN; -0 below +0), two instructions
+__device__ __forceinline__ uint32_t quick_key(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+// e^x within 2 + 1.2 |x| steps, and 1 / x within one; results below 2^-126 are 0
+__device__ __forceinline__ float quick_exp(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float quick_inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Each register's two largest keys over the warp, all registers at once: the first steps of the butterfly halve the registers instead
+// of reducing each (NV = 8: 60 instructions, where two reductions a register take 240).  Lane register_lane(r) receives register r's.
+template <int NV>
+__device__ __forceinline__ void two_largest(const uint32_t (&key)[NV], int lane, uint32_t& b1, uint32_t& b2) {
+  uint32_t x1[NV], x2[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    x1[i] = key[i];
+    x2[i] = 0;
+  }
+  int o = 16;
+#pragma unroll
+  for (int n = NV / 2; n >= 1; n /= 2, o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const uint32_t k1 = upper ? x1[i + n] : x1[i], s1 = upper ? x1[i] : x1[i + n];
+      const uint32_t r1 = __shfl_xor_sync(0xffffffffu, s1, o);
+      if (n == NV / 2) {
+        x2[i] = min(k1, r1);
+      } else {
+        const uint32_t k2 = upper ? x2[i + n] : x2[i], s2 = upper ? x2[i] : x2[i + n];
+        x2[i] = max(min(k1, r1), max(k2, __shfl_xor_sync(0xffffffffu, s2, o)));
+      }
+      x1[i] = max(k1, r1);
+    }
+  }
+#pragma unroll
+  for (; o >= 1; o >>= 1) {
+    const uint32_t r1 = __shfl_xor_sync(0xffffffffu, x1[0], o), r2 = __shfl_xor_sync(0xffffffffu, x2[0], o);
+    x2[0] = max(min(x1[0], r1), max(x2[0], r2));
+    x1[0] = max(x1[0], r1);
+  }
+  b1 = x1[0];
+  b2 = x2[0];
+}
+template <int NV>
+__device__ __forceinline__ int register_lane(int r) {   // the s-th step, across lanes 16 >> s, chose by bit log2(NV) - 1 - s
+  return NV == 4 ? r << 3 : NV == 8 ? r << 2 : NV == 16 ? r << 1 : r;
+}
 
 // the kept groups as bits: the best of lane g's score of group g (-inf: none), equal ones the lower first
 template <typename T>
@@ -134,49 +192,237 @@ static __device__ __noinline__ int exact_select(const GroupRouteArgs& a, const B
   return mine;
 }
 
-// The selection of token t: lane j < k receives the j-th expert (-1: none) and its weight.  x: lane l's logits of experts
-// l + 32 i, cleaned (-inf: masked, or past the experts).
-template <int NV>
-__device__ __forceinline__ void balanced_token(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane,
-                                               const float (&x)[NV], int& my_e, float& my_w) {
-  const bool limited = a.keep < a.groups, scores = a.bias || limited || !a.renorm;
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) top = fmaxf(top, x[i]);
-  const float m = warp_max_f(top);   // the largest logit
-  float inv = 1.f, err = 0.f;        // softmax: one over the sum; the scores' absolute error
-  if (scores) {
-    if (a.kind == 0) {
-      float z = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) z += x[i] > -INFINITY ? expf(x[i] - m) : 0.f;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-      inv = 1.f / z;
-      // each of NV + 5 additions, the exponential and two products a step; e^-d is off by d 2^-24 of itself for the rounding of d,
-      // at most 0.37 2^-24
-      err = (NV + 17) * 0x1p-23f * inv;
-    } else {
-      err = 0x1p-21f / (1.f + expf(-m));   // exponential, sum and division: four steps of the largest score at most
+constexpr uint32_t KEY_ID = MAX_EXPERTS - 1;   // the part of a key that names its expert
+constexpr int UNSETTLED = -2;
+
+// The kept groups where fp32 leaves them open, by the 64-bit scores of each group's best one or two experts, lane g looking through
+// group g (2 us; all of the token's scores in 64 bits take 10).  All lanes NO_GROUPS where a group's own best are too close to tell.
+constexpr unsigned NO_GROUPS = 0;
+static __device__ __noinline__ unsigned settle_groups(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane, float m,
+                                                      float inv, float err) {
+  float c[3] = {-INFINITY, -INFINITY, -INFINITY};
+  int e[2] = {0, 0};
+  const int size = a.E / a.groups;
+  if (lane < a.groups)
+    for (int q = lane * size; q < (lane + 1) * size; ++q) {
+      const float l = logit_of(a, t, q);
+      if (!(l > -INFINITY)) continue;
+      const float v = (a.kind == 1 ? quick_inverse(1.f + quick_exp(-l)) : quick_exp(l - m) * inv) + tab.bias[q];
+      if (v > c[0]) {
+        c[2] = c[1], c[1] = c[0], c[0] = v;
+        e[1] = e[0], e[0] = q;
+      } else if (v > c[1]) {
+        c[2] = c[1], c[1] = v;
+        e[1] = q;
+      } else {
+        c[2] = fmaxf(c[2], v);
+      }
+    }
+  const float least = a.top2 ? c[1] : c[0], other = a.top2 ? c[2] : c[1];
+  const bool open = other > -INFINITY && !(least - other > 2.f * err + 0x1p-22f * fmaxf(fabsf(least), fabsf(other)));
+  if (__any_sync(0xffffffffu, open)) return NO_GROUPS;
+  // (without a bias the softmax's sum is common to all)
+  const double z = a.kind == 0 && a.bias ? exact_total(a, t, lane, m) : 1.0;
+  double score = -INFINITY;
+  for (int i = 0; i < (a.top2 ? 2 : 1); ++i)
+    if (c[i] > -INFINITY) {
+      const double v = exact_score(a, logit_of(a, t, e[i]), m, z) + (double)tab.bias[e[i]];
+      score = i ? score + v : v;
+    }
+  return kept_groups(score, a.groups, a.keep, lane);
+}
+
+// The order of a token's selected experts (lane j: the j-th's key `mine` and id e), where keys of 22 bits leave it open.  The
+// candidates, one a lane: the selected, and the others that are not beyond the last of them and its error.  By fp32 values first; where
+// those are closer than their errors, and not of the same logit and bias, by 64 bits.  All lanes UNSETTLED where there are more
+// candidates than lanes.
+static __device__ __noinline__ int settle(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane, uint32_t mine, int e,
+                                          unsigned kept, float m, float inv, float err) {
+  auto score = [&](float l, float b) {
+    return a.bias ? (a.kind == 1 ? quick_inverse(1.f + quick_exp(-l)) : quick_exp(l - m) * inv) + b : l;
+  };
+  const int n = __popc(__ballot_sync(0xffffffffu, mine != 0));
+  const uint32_t k_last = __shfl_sync(0xffffffffu, mine, n - 1);
+  const float c_last = key_value(k_last & ~KEY_ID);   // its value or a little below
+  const float limit = c_last - (a.bias ? 2.f * err + 0x1p-21f * fabsf(c_last) : 0.f);
+  if (!(limit > -INFINITY)) return UNSETTLED;
+  int count = n;
+  for (int i0 = 0; i0 < a.E; i0 += 32) {
+    const int q = i0 + lane;
+    const unsigned selected = __reduce_or_sync(0xffffffffu, lane < n && (e >> 5) == (i0 >> 5) ? 1u << (e & 31) : 0u);
+    bool in = false;
+    if (q < a.E && !((selected >> lane) & 1u) && ((kept >> (tab.group[q] & 31)) & 1u)) {
+      const float l = logit_of(a, t, q), c = score(l, tab.bias[q]);
+      in = l > -INFINITY && c >= limit;
+    }
+    unsigned who = __ballot_sync(0xffffffffu, in);
+    for (; who && count <= 32; who &= who - 1, ++count)
+      if (lane == count) e = i0 + __ffs(who) - 1;
+  }
+  if (count > 32) return UNSETTLED;
+  const bool live = lane < count;
+  const float l = live ? logit_of(a, t, e) : -INFINITY, b = live ? tab.bias[e] : 0.f;
+  double v = live ? score(l, b) : -INFINITY;
+  auto order = [&]() {   // this lane's place among the candidates
+    int rank = 0;
+    for (int q = 0; q < count; ++q) {
+      const double o = __shfl_sync(0xffffffffu, v, q);
+      const int oe = __shfl_sync(0xffffffffu, e, q);
+      rank += o > v || (o == v && oe < e);
+    }
+    return rank;
+  };
+  int rank = order();
+  if (a.bias) {
+    bool close = false;
+    const float f = (float)v;
+    for (int q = 0; q < count; ++q) {
+      const float o = __shfl_sync(0xffffffffu, f, q), ol = __shfl_sync(0xffffffffu, l, q), ob = __shfl_sync(0xffffffffu, b, q);
+      close |= q != lane && !(fabsf(o - f) > 2.f * err + 0x1p-22f * fabsf(o)) && !(ol == l && ob == b);
+    }
+    if (__any_sync(0xffffffffu, live && close)) {
+      const double z = a.kind == 0 ? exact_total(a, t, lane, m) : 1.0;
+      if (live) v = exact_score(a, l, m, z) + (double)b;
+      rank = order();
     }
   }
-  // keys by which experts are compared: scores with the bias, or logits
-  uint32_t key[NV];
-  const bool by_score = a.bias || limited;
+  int from = -1;
+  for (int q = 0; q < count; ++q)
+    if (__shfl_sync(0xffffffffu, rank, q) == lane) from = q;
+  const int sorted = __shfl_sync(0xffffffffu, e, max(from, 0));
+  return from >= 0 && lane < a.k ? sorted : -1;
+}
+
+// kept_groups of fp32 scores by rounds of the warp's maximum (or minimum, where fewer groups go than stay); and the least kept and the
+// largest other score (-inf: none).
+__device__ __forceinline__ unsigned kept_by_rounds(float score, int groups, int keep, int lane, float& last, float& next) {
+  const uint32_t key = lane < groups && score > -INFINITY ? logit_key(score) : 0u;
+  unsigned kept = 0;
+  if (2 * keep <= groups) {
+    uint32_t rest = key, b = 0;
+    for (int j = 0; j < keep; ++j) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, rest);
+      if (best == 0) break;   // uniform
+      b = best;
+      const int who = __ffs(__ballot_sync(0xffffffffu, rest == best)) - 1;
+      kept |= 1u << who;
+      if (lane == who) rest = 0;
+    }
+    last = key_value(b);
+    next = key_value(__reduce_max_sync(0xffffffffu, rest));
+  } else {
+    uint32_t rest = lane < groups ? key : 0xffffffffu, b = 0;
+    unsigned gone = 0;
+    for (int j = keep; j < groups; ++j) {
+      b = __reduce_min_sync(0xffffffffu, rest);
+      const int who = 31 - __clz(__ballot_sync(0xffffffffu, rest == b));   // of equal ones the last goes first
+      gone |= 1u << who;
+      if (lane == who) rest = 0xffffffffu;
+    }
+    kept = __ballot_sync(0xffffffffu, key != 0) & ~gone;
+    last = key_value(__reduce_min_sync(0xffffffffu, key && ((kept >> lane) & 1u) ? key : 0xffffffffu));
+    next = key_value(b);
+  }
+  return kept;
+}
+
+// The first n <= 33 keys in descending order (0: none left), lane j the j-th and `last` the 33rd; each key is unique.  A round takes
+// the largest of the lanes' firsts, and the lane that held it steps to its second and third; where a lane gave all three, the
+// warp starts again with rounds in which that lane looks through its keys.
+template <int NV>
+__device__ __forceinline__ uint32_t ordered_keys(const uint32_t (&key)[NV], int n, int lane, uint32_t& behind) {
+  uint32_t b1 = 0, b2 = 0, b3 = 0, mine = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    key[i] = 0;
-    if (x[i] > -INFINITY) {
-      float c = x[i];
-      if (by_score) {
-        const float s = a.kind == 1 ? __fdividef(1.f, 1.f + expf(-x[i])) : expf(x[i] - m) * inv;
-        c = s + tab.bias[lane + 32 * i];
-      }
-      if (c > -INFINITY) key[i] = logit_key(c);
+    const uint32_t x = min(b1, key[i]), y = min(b2, x);
+    b1 = max(b1, key[i]);
+    b2 = max(b2, x);
+    b3 = max(b3, y);
+  }
+  const bool three = b3 != 0;
+  const uint32_t best0 = b1;
+  behind = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint32_t b = __reduce_max_sync(0xffffffffu, b1);
+    if (lane == j) mine = b;
+    if (j == n - 1) behind = b;
+    if (b1 == b) {
+      b1 = b2;
+      b2 = b3;
+      b3 = 0;
     }
   }
-  // scores below 2^-100 lose bits
+  if (NV > 3 && __any_sync(0xffffffffu, three && b1 == 0)) {
+    uint32_t best = best0, floor = 0xffffffffu;   // this lane's keys from `floor` on are taken
+    mine = 0;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t b = __reduce_max_sync(0xffffffffu, best);
+      if (lane == j) mine = b;
+      if (j == n - 1) behind = b;
+      if (best == b && b) {
+        floor = b;
+        best = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) best = max(best, key[i] < floor ? key[i] : 0u);
+      }
+    }
+  }
+  return mine;
+}
+
+// The selection of token t: lane j < k receives the j-th expert (-1: none) and its weight.  x: lane l's logits of experts
+// l + 32 i (-inf, NaN: masked; -inf past the experts).
+template <int NV>
+__device__ __forceinline__ void balanced_token(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane,
+                                               float (&x)[NV], int& my_e, float& my_w) {
+  const bool limited = a.keep < a.groups, by_score = a.bias || limited;   // else logits are compared
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) top = fmaxf(top, x[i]);   // (NaN is passed over; no comparison below takes it)
+  float m = warp_max_f(top);   // the largest logit
+  if (m == INFINITY) {
+    m = 3.402823466e38f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = x[i] == INFINITY ? m : x[i];
+  }
+  float inv = 1.f, err = 0.f;        // softmax: one over the sum; the scores' absolute error
+  uint32_t key[NV];                  // by which experts are compared
+  if (a.kind == 0 && (by_score || !a.renorm)) {
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float p = x[i] > -INFINITY ? quick_exp(x[i] - m) : 0.f;
+      key[i] = __float_as_uint(p);
+      z += p;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    inv = 1.f / z;
+    // e^-d is within 2 + 1.2 d steps of itself, 2 steps of the largest; so are the sum's terms, and its NV + 5 additions
+    // and two products a step each
+    err = (NV + 20) * 0x1p-23f * inv;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float c = __uint_as_float(key[i]) * inv + tab.bias[lane + 32 * i];
+      key[i] = x[i] > -INFINITY && c > -INFINITY ? quick_key(c) : 0u;
+    }
+  } else if (by_score && a.kind == 1) {
+    // the derivative by e^-l is s (1 - s): 2 + 1.2 |l| steps of it are 0.6 steps of 1 for l >= 0, and 2 + 1.2 |m| of the largest score
+    // where all logits are below 0; the sum and the division two more
+    err = 0x1p-23f * (4.f + 2.f * fmaxf(-m, 0.f)) / (1.f + __expf(-m));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float c = quick_inverse(1.f + quick_exp(-x[i])) + tab.bias[lane + 32 * i];
+      key[i] = x[i] > -INFINITY && c > -INFINITY ? quick_key(c) : 0u;   // (c is never -0)
+    }
+  }
+  if (!by_score) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) key[i] = x[i] > -INFINITY ? logit_key(x[i]) : 0u;
+  }
+  // sigmoids below 2^-100 lose bits
   bool doubt = by_score && a.kind == 1 && m < -69.f && m > -INFINITY;
+  unsigned kept = ~0u;
   if (limited) {
     float score = -INFINITY;
     auto finish = [&](int g, uint32_t b1, uint32_t b2) {   // a group's score from the lanes' two largest
@@ -189,21 +435,20 @@ __device__ __forceinline__ void balanced_token(const GroupRouteArgs& a, const Ba
       }
       if (lane == g) score = v;
     };
-    const int size = a.E / a.groups;
-    if (size % 32 == 0) {   // a group is whole registers
-      uint32_t b1 = 0, b2 = 0;
-      int left = size / 32, g = 0;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (g < a.groups) {
-          b2 = max(b2, min(b1, key[i]));
-          b1 = max(b1, key[i]);
-          if (--left == 0) {
-            finish(g++, b1, b2);
-            b1 = b2 = 0;
-            left = size / 32;
-          }
-        }
+    const int size = a.E / a.groups, per = size / 32;
+    const bool whole = size % 32 == 0;   // a group is whole registers
+    if (whole) {
+      uint32_t r1, r2, b1 = 0, b2 = 0;
+      two_largest<NV>(key, lane, r1, r2);
+      for (int q = 0; q < per; ++q) {
+        const int from = register_lane<NV>((lane * per + q) & (NV - 1));
+        const uint32_t o1 = __shfl_sync(0xffffffffu, r1, from), o2 = __shfl_sync(0xffffffffu, r2, from);
+        b2 = max(min(b1, o1), max(b2, o2));
+        b1 = max(b1, o1);
+      }
+      if (lane < a.groups) {
+        score = key_value(b1);
+        if (a.top2 && b2) score += key_value(b2);
       }
     } else {
       for (int g = 0; g < a.groups; ++g) {
@@ -217,102 +462,66 @@ __device__ __forceinline__ void balanced_token(const GroupRouteArgs& a, const Ba
         finish(g, b1, b2);
       }
     }
-    const unsigned kept = kept_groups(score, a.groups, a.keep, lane);
-    const bool in = (kept >> lane) & 1u;
-    const float last = -warp_max_f(in ? -score : -INFINITY), next = warp_max_f(lane < a.groups && !in ? score : -INFINITY);
+    float last, next;
+    kept = kept_by_rounds(score, a.groups, a.keep, lane, last, next);
     // two scores a group, and the roundings of their sums with the biases and each other
-    doubt |= next > -INFINITY && !(last - next > 4.f * err + 0x1p-21f * fmaxf(fabsf(last), fabsf(next)));
+    if (next > -INFINITY && !(last - next > 4.f * err + 0x1p-21f * fmaxf(fabsf(last), fabsf(next))) && !doubt) {
+      kept = settle_groups(a, tab, t, lane, m, inv, err);
+      doubt = kept == NO_GROUPS;
+    }
+    unsigned stay = kept;   // by register, whole groups
+    if (whole && per > 1) {
+      stay = 0;
+      for (int g = 0; g < a.groups; ++g)
+        if ((kept >> g) & 1u) stay |= ((1u << per) - 1u) << (g * per);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = min(lane + 32 * i, MAX_EXPERTS - 1);
-      if (!((kept >> (tab.group[e] & 31)) & 1u)) key[i] = 0;
-      else if (!a.bias && key[i]) key[i] = logit_key(x[i]);
+      if (whole) {
+        if (!((stay >> i) & 1u)) key[i] = 0;
+      } else if (!((kept >> (tab.group[min(lane + 32 * i, MAX_EXPERTS - 1)] & 31)) & 1u)) {
+        key[i] = 0;
+      }
+      if (!a.bias && key[i]) key[i] = logit_key(x[i]);
     }
   }
   int e = -1;
   if (!doubt) {
-    // the k best and the one behind them
-    uint32_t mine = 0, behind = 0, best = 0;
+    // Keys carry the expert in their low 10 bits, a lower one larger, so each is unique, and a round needs no search for its expert.
+    // 16-bit logits fit the other 22 bits whole; of scores and fp32 logits those are the leading ones, and where two neighbours could
+    // be the other way round, the candidates' values decide.
+    uint32_t behind;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) best = max(best, key[i]);
-    for (int j = 0; j <= a.k; ++j) {
-      const uint32_t b = __reduce_max_sync(0xffffffffu, best);
-      if (b == 0) break;   // uniform
-      if (j == a.k) {
-        behind = b;
-        break;
-      }
-      int id = 0x7fffffff;
-      if (best == b) {
-#pragma unroll
-        for (int i = NV - 1; i >= 0; --i)
-          if (key[i] == b) id = lane + 32 * i;
-      }
-      id = (int)__reduce_min_sync(0xffffffffu, (unsigned)id);
-      if (lane == j) {
-        mine = b;
-        e = id;
-      }
-      if ((id & 31) == lane) {
-        best = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          if (lane + 32 * i == id) key[i] = 0;
-          best = max(best, key[i]);
-        }
-      }
-    }
-    if (a.bias) {
-      // neighbours in the order whose scores are closer than their errors, and not the same logit and bias
-      const float c = key_value(mine), b = e >= 0 ? tab.bias[e] : 0.f, l = e >= 0 ? logit_of(a, t, e) : -INFINITY;
+    for (int i = 0; i < NV; ++i) key[i] = key[i] ? (key[i] & ~KEY_ID) | (KEY_ID - lane - 32 * i) : 0u;
+    uint32_t mine = ordered_keys<NV>(key, a.k + 1, lane, behind);
+    if (lane >= a.k) mine = 0;
+    if (mine) e = (int)(KEY_ID - (mine & KEY_ID));
+    if (a.bias || a.dtype == GT_FP32) {
       uint32_t after = __shfl_down_sync(0xffffffffu, mine, 1);
-      const float la = __shfl_down_sync(0xffffffffu, l, 1), ba = __shfl_down_sync(0xffffffffu, b, 1);
-      const bool inner = lane + 1 < a.k;
-      if (!inner) after = behind;
-      const float ca = key_value(after);
-      const float gap = 2.f * err + 0x1p-23f * fmaxf(fabsf(c), fabsf(ca));
-      const bool close = lane < a.k && mine && after && !(c - ca > gap) && !(inner && l == la && b == ba);
+      if (lane + 1 >= a.k) after = behind;
+      const float lo = key_value(mine & ~KEY_ID), hi = key_value(after | KEY_ID);
+      const bool close = mine && after && !(lo - hi > (a.bias ? 2.f * err + 0x1p-21f * fmaxf(fabsf(lo), fabsf(hi)) : 0.f));
       if (__any_sync(0xffffffffu, close)) {
-        // candidates: the selected, and the others within the error of the last of them, one a lane
-        const int n = __popc(__ballot_sync(0xffffffffu, mine != 0));
-        const float c_last = __shfl_sync(0xffffffffu, c, n - 1);
-        const float limit = c_last - 2.f * err - 0x1p-22f * fabsf(c_last);
-        int count = n;
-        doubt = !(limit > -INFINITY);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          unsigned who = __ballot_sync(0xffffffffu, key[i] != 0 && key_value(key[i]) >= limit);
-          for (; who && count <= 32; who &= who - 1, ++count)
-            if (lane == count) e = 32 * i + __ffs(who) - 1;
-        }
-        doubt |= count > 32;
-        if (!doubt) {
-          const double z = a.kind == 0 ? exact_total(a, t, lane, m) : 1.0;
-          double v = -INFINITY;
-          if (lane < count) v = exact_score(a, logit_of(a, t, e), m, z) + (double)tab.bias[e];
-          int rank = 0, from = -1;
-          for (int q = 0; q < count; ++q) {
-            const double o = __shfl_sync(0xffffffffu, v, q);
-            const int oe = __shfl_sync(0xffffffffu, e, q);
-            rank += o > v || (o == v && oe < e);
-          }
-          for (int q = 0; q < count; ++q)
-            if (__shfl_sync(0xffffffffu, rank, q) == lane) from = q;
-          const int sorted = __shfl_sync(0xffffffffu, e, max(from, 0));
-          e = from >= 0 && lane < a.k ? sorted : -1;
-        }
+        e = settle(a, tab, t, lane, mine, e, kept, m, inv, err);
+        doubt = __any_sync(0xffffffffu, e == UNSETTLED);
       }
     }
   }
   if (doubt) e = exact_select<NV>(a, tab, t, lane, m);
-  // weights: of the selected alone by e^(z - largest z) with z the logit or its log sigmoid, so that scores that would all
-  // underflow still give weights that sum to the factor
+  // weights of the selected alone
   const float l = e >= 0 ? logit_of(a, t, e) : 0.f;
   float w = 0.f;
   if (a.renorm) {
-    const float z = a.kind == 1 ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : l;
-    const float z0 = warp_max_f(e >= 0 ? z : -INFINITY);
-    const float num = e >= 0 ? expf(z - z0) : 0.f;
+    float num;
+    if (a.kind == 1 && !__any_sync(0xffffffffu, e >= 0 && l < -60.f)) {
+      num = e >= 0 ? 1.f / (1.f + expf(-l)) : 0.f;
+    } else {
+      // e^(z - largest z) with z the logit or its log sigmoid, so that scores that would all underflow still give weights that sum
+      // to the factor
+      const float z = a.kind == 1 ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : l;
+      const float z0 = warp_max_f(e >= 0 ? z : -INFINITY);
+      num = e >= 0 ? expf(z - z0) : 0.f;
+    }
     float den = num;
 #pragma unroll
     for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);

@@ -226,7 +226,7 @@ __device__ __forceinline__ void route_balanced(const GroupRouteArgs& a, const Ba
     const uint32_t raw = __float_as_uint(l[i]);
     if (a.dtype == GT_BF16) l[i] = __uint_as_float(raw << 16);
     else if (a.dtype == GT_FP16) l[i] = __half2float(__ushort_as_half((unsigned short)raw));
-    l[i] = lane + 32 * i < a.E ? clean(l[i]) : -INFINITY;
+    if (lane + 32 * i >= a.E) l[i] = -INFINITY;
   }
   int e;
   float w;
