@@ -192,7 +192,6 @@ static __device__ __noinline__ int exact_select(const GroupRouteArgs& a, const B
   return mine;
 }
 
-constexpr uint32_t KEY_ID = MAX_EXPERTS - 1;   // the part of a key that names its expert
 constexpr int UNSETTLED = -2;
 
 // The kept groups where fp32 leaves them open, by the 64-bit scores of each group's best one or two experts, lane g looking through
@@ -200,26 +199,36 @@ constexpr int UNSETTLED = -2;
 constexpr unsigned NO_GROUPS = 0;
 static __device__ __noinline__ unsigned settle_groups(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane, float m,
                                                       float inv, float err) {
-  float c[3] = {-INFINITY, -INFINITY, -INFINITY};
+  // the group's best one or two, and the best of the others; one of the same logit and bias as the least of those does not change the
+  // score, as long as the best is no less than they are
+  const int last = a.top2 ? 1 : 0;
+  float c[2] = {-INFINITY, -INFINITY}, other = -INFINITY;
   int e[2] = {0, 0};
+  bool skipped = false;
+  auto alike = [&](int p, int q) { return logit_of(a, t, p) == logit_of(a, t, q) && tab.bias[p] == tab.bias[q]; };
+  auto apart = [&](float p, float q) { return p - q > 2.f * err + 0x1p-22f * fmaxf(fabsf(p), fabsf(q)); };
   const int size = a.E / a.groups;
   if (lane < a.groups)
     for (int q = lane * size; q < (lane + 1) * size; ++q) {
       const float l = logit_of(a, t, q);
       if (!(l > -INFINITY)) continue;
       const float v = (a.kind == 1 ? quick_inverse(1.f + quick_exp(-l)) : quick_exp(l - m) * inv) + tab.bias[q];
+      float out = v;
+      int out_e = q;
       if (v > c[0]) {
-        c[2] = c[1], c[1] = c[0], c[0] = v;
-        e[1] = e[0], e[0] = q;
-      } else if (v > c[1]) {
-        c[2] = c[1], c[1] = v;
-        e[1] = q;
-      } else {
-        c[2] = fmaxf(c[2], v);
+        out = c[0], out_e = e[0];
+        c[0] = v, e[0] = q;
       }
+      if (last && out > c[1]) {
+        const float x = c[1];
+        const int y = e[1];
+        c[1] = out, e[1] = out_e;
+        out = x, out_e = y;
+      }
+      if (out > -INFINITY && out == c[last] && alike(out_e, e[last])) skipped = true;
+      else other = fmaxf(other, out);
     }
-  const float least = a.top2 ? c[1] : c[0], other = a.top2 ? c[2] : c[1];
-  const bool open = other > -INFINITY && !(least - other > 2.f * err + 0x1p-22f * fmaxf(fabsf(least), fabsf(other)));
+  const bool open = (other > -INFINITY && !apart(c[last], other)) || (last && skipped && !apart(c[0], c[1]) && !alike(e[0], e[1]));
   if (__any_sync(0xffffffffu, open)) return NO_GROUPS;
   // (without a bias the softmax's sum is common to all)
   const double z = a.kind == 0 && a.bias ? exact_total(a, t, lane, m) : 1.0;
@@ -232,20 +241,24 @@ static __device__ __noinline__ unsigned settle_groups(const GroupRouteArgs& a, c
   return kept_groups(score, a.groups, a.keep, lane);
 }
 
-// The order of a token's selected experts (lane j: the j-th's key `mine` and id e), where keys of 22 bits leave it open.  The
-// candidates, one a lane: the selected, and the others that are not beyond the last of them and its error.  By fp32 values first; where
-// those are closer than their errors, and not of the same logit and bias, by 64 bits.  All lanes UNSETTLED where there are more
-// candidates than lanes.
-static __device__ __noinline__ int settle(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane, uint32_t mine, int e,
-                                          unsigned kept, float m, float inv, float err) {
+// The order of a token's selected experts (lane j: the j-th, e; -1 from n on), where their keys leave it open.  The candidates, one a lane:
+// the selected, and the others that are not below the least of them by more than the errors; those of the last one's logit and bias
+// are left out where all the selected are no less than it (of equal ones the lower was taken).  By fp32 values first; where those are closer than their errors, and not of the
+// same logit and bias, by 64 bits.  All lanes UNSETTLED where there are more candidates than lanes.
+static __device__ __noinline__ int settle(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane, int e, unsigned kept,
+                                          float m, float inv, float err) {
   auto score = [&](float l, float b) {
     return a.bias ? (a.kind == 1 ? quick_inverse(1.f + quick_exp(-l)) : quick_exp(l - m) * inv) + b : l;
   };
-  const int n = __popc(__ballot_sync(0xffffffffu, mine != 0));
-  const uint32_t k_last = __shfl_sync(0xffffffffu, mine, n - 1);
-  const float c_last = key_value(k_last & ~KEY_ID);   // its value or a little below
-  const float limit = c_last - (a.bias ? 2.f * err + 0x1p-21f * fabsf(c_last) : 0.f);
+  const int n = __popc(__ballot_sync(0xffffffffu, e >= 0));
+  const float my_l = e >= 0 ? logit_of(a, t, e) : INFINITY, my_b = e >= 0 ? tab.bias[e] : 0.f;
+  const float l_last = __shfl_sync(0xffffffffu, my_l, n - 1), b_last = __shfl_sync(0xffffffffu, my_b, n - 1);
+  const float least = -warp_max_f(e >= 0 ? -score(my_l, my_b) : -INFINITY);
+  const float limit = least - (a.bias ? 2.f * err + 0x1p-21f * fabsf(least) : 0.f);
   if (!(limit > -INFINITY)) return UNSETTLED;
+  const float c_last = score(l_last, b_last);
+  const bool above = __all_sync(0xffffffffu, e < 0 || (my_l == l_last && my_b == b_last) ||
+                                                 score(my_l, my_b) - c_last > (a.bias ? 2.f * err + 0x1p-21f * fmaxf(fabsf(c_last), fabsf(least)) : 0.f));
   int count = n;
   for (int i0 = 0; i0 < a.E; i0 += 32) {
     const int q = i0 + lane;
@@ -253,7 +266,7 @@ static __device__ __noinline__ int settle(const GroupRouteArgs& a, const Balance
     bool in = false;
     if (q < a.E && !((selected >> lane) & 1u) && ((kept >> (tab.group[q] & 31)) & 1u)) {
       const float l = logit_of(a, t, q), c = score(l, tab.bias[q]);
-      in = l > -INFINITY && c >= limit;
+      in = l > -INFINITY && c >= limit && !(above && l == l_last && tab.bias[q] == b_last);
     }
     unsigned who = __ballot_sync(0xffffffffu, in);
     for (; who && count <= 32; who &= who - 1, ++count)
@@ -487,22 +500,45 @@ __device__ __forceinline__ void balanced_token(const GroupRouteArgs& a, const Ba
   }
   int e = -1;
   if (!doubt) {
-    // Keys carry the expert in their low 10 bits, a lower one larger, so each is unique, and a round needs no search for its expert.
-    // 16-bit logits fit the other 22 bits whole; of scores and fp32 logits those are the leading ones, and where two neighbours could
-    // be the other way round, the candidates' values decide.
-    uint32_t behind;
+    // Keys to order by carry the expert in their low bits, a lower one larger, so each is unique, and a round needs no search for its
+    // expert.  Above them stands the biased score in steps of 2^-23 (E > 256: 2^-22, 2^-21) of the scores' range, or the leading bits of the logit,
+    // which hold a 16-bit one whole.  Where two neighbours could be the other way round, the candidates' values decide.
+    constexpr int ID = NV == 4 ? 7 : NV == 8 ? 8 : NV == 16 ? 9 : 10, FIXED = 31 - ID < 23 ? 31 - ID : 23;
+    constexpr uint32_t LOW = (1u << ID) - 1;
+    float steps = 0.f, spread = 0.f;   // steps of one; the largest magnitude, to whose rounding the scores are known
+    if (a.bias) {
+      uint32_t hi = 0, lo = 0xffffffffu;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) key[i] = key[i] ? (key[i] & ~KEY_ID) | (KEY_ID - lane - 32 * i) : 0u;
+      for (int i = 0; i < NV; ++i) {
+        hi = max(hi, key[i]);
+        lo = min(lo, key[i] - 1u);   // (none: the largest)
+      }
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      lo = __reduce_min_sync(0xffffffffu, lo) + 1u;
+      const float base = key_logit(lo), range = key_logit(hi) - base;
+      spread = fmaxf(fabsf(base), fabsf(key_logit(hi)));
+      // (a range beyond fp32, or none: all keys the same)
+      steps = range > 1e-30f && range < 1e30f ? __fdividef((float)((1 << FIXED) - 2), range) : 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const float c = __uint_as_float(key[i] ^ (~(uint32_t)((int)key[i] >> 31) | 0x80000000u));
+        key[i] = key[i] ? 0x80000000u | ((__float_as_uint(fmaf(c - base, steps, 8388608.f)) & 0x7fffffu) << ID) | (LOW - lane - 32 * i) : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) key[i] = key[i] ? (key[i] & ~LOW) | (LOW - lane - 32 * i) : 0u;
+    }
+    uint32_t behind;
     uint32_t mine = ordered_keys<NV>(key, a.k + 1, lane, behind);
     if (lane >= a.k) mine = 0;
-    if (mine) e = (int)(KEY_ID - (mine & KEY_ID));
+    if (mine) e = (int)(LOW - (mine & LOW));
     if (a.bias || a.dtype == GT_FP32) {
       uint32_t after = __shfl_down_sync(0xffffffffu, mine, 1);
       if (lane + 1 >= a.k) after = behind;
-      const float lo = key_value(mine & ~KEY_ID), hi = key_value(after | KEY_ID);
-      const bool close = mine && after && !(lo - hi > (a.bias ? 2.f * err + 0x1p-21f * fmaxf(fabsf(lo), fabsf(hi)) : 0.f));
-      if (__any_sync(0xffffffffu, close)) {
-        e = settle(a, tab, t, lane, mine, e, kept, m, inv, err);
+      // scores: nearer than their errors, and two steps; logits: the same leading bits
+      const float apart = (float)((mine >> ID) - (after >> ID)), least = a.bias ? 2.f + steps * (2.f * err + 0x1p-21f * spread) : 0.f;
+      if (__any_sync(0xffffffffu, mine && after && !(apart > least))) {
+        e = settle(a, tab, t, lane, e, kept, m, inv, err);
         doubt = __any_sync(0xffffffffu, e == UNSETTLED);
       }
     }
@@ -514,7 +550,7 @@ __device__ __forceinline__ void balanced_token(const GroupRouteArgs& a, const Ba
   if (a.renorm) {
     float num;
     if (a.kind == 1 && !__any_sync(0xffffffffu, e >= 0 && l < -60.f)) {
-      num = e >= 0 ? 1.f / (1.f + expf(-l)) : 0.f;
+      num = e >= 0 ? __fdividef(1.f, 1.f + expf(-l)) : 0.f;
     } else {
       // e^(z - largest z) with z the logit or its log sigmoid, so that scores that would all underflow still give weights that sum
       // to the factor
@@ -525,7 +561,7 @@ __device__ __forceinline__ void balanced_token(const GroupRouteArgs& a, const Ba
     float den = num;
 #pragma unroll
     for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    if (e >= 0) w = num / den;
+    if (e >= 0) w = __fdividef(num, den);
   } else if (e >= 0) {
     const float d = expf(-fabsf(l));
     w = a.kind == 1 ? (l >= 0.f ? 1.f : d) / (1.f + d) : expf(l - m) * inv;

@@ -221,13 +221,12 @@ template <int NV>
 __device__ __forceinline__ void route_balanced(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane, int* hist) {
   float l[NV];
   load_token<NV>(a, t, lane, l);
+  auto values = [&](auto value) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const uint32_t raw = __float_as_uint(l[i]);
-    if (a.dtype == GT_BF16) l[i] = __uint_as_float(raw << 16);
-    else if (a.dtype == GT_FP16) l[i] = __half2float(__ushort_as_half((unsigned short)raw));
-    if (lane + 32 * i >= a.E) l[i] = -INFINITY;
-  }
+    for (int i = 0; i < NV; ++i) l[i] = lane + 32 * i < a.E ? value(l[i]) : -INFINITY;
+  };
+  if (a.dtype == GT_BF16) values([](float x) { return __uint_as_float(__float_as_uint(x) << 16); });
+  else if (a.dtype == GT_FP16) values([](float x) { return __half2float(__ushort_as_half((unsigned short)__float_as_uint(x))); });
   int e;
   float w;
   balanced_token<NV>(a, tab, t, lane, l, e, w);

@@ -207,3 +207,39 @@ def test_balanced_route_backward_rows_apart(M):  # noqa: F811
         M.balanced_route_backward(torch.zeros(30, 5, device="cuda"), logits, idx)
     with pytest.raises(ValueError):
         M.balanced_route_backward(torch.zeros(30, 4, device="cuda"), logits, idx.long())
+
+
+@pytest.mark.parametrize("router", [0, 1])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_balanced_route_equal_logits(M, router, dtype):  # noqa: F811
+    """A router that has not learned anything: every logit the same; biases all zero, all different, or of a few values."""
+    import torch
+    logits = torch.zeros(300, 64, device="cuda").to(B.torch_type(dtype))
+    logits[7] = 3.0
+    rng = np.random.default_rng(0)
+    for bias in (None, torch.zeros(64, device="cuda"), random_bias(64),
+                 torch.from_numpy(rng.choice(np.array([0.0, 0.125], np.float32), 64)).cuda()):
+        for groups, keep in ((1, 1), (8, 3), (4, 3)):
+            check(M, logits, 6, bias, router, groups, keep, "top2")
+            check(M, logits, 6, bias, router, groups, keep, "max", renormalize=False)
+
+
+@pytest.mark.parametrize("groups,keep", [(1, 1), (8, 4)])
+@pytest.mark.parametrize("router", [0, 1])
+def test_balanced_route_twins_beside_near_ones(M, router, groups, keep):  # noqa: F811
+    """Experts with the same logit and bias beside one whose score differs by less than fp32 tells, above or below them."""
+    import torch
+    T, E = 400, 64
+    rng = np.random.default_rng(3)
+    l = rng.normal(size=(T, E)).astype(np.float32) - 4
+    bias = np.zeros(E, np.float32)
+    for t in range(T):
+        g = rng.integers(0, groups) * (E // groups)
+        at = g + rng.permutation(E // groups)[:5]
+        l[t, at] = 1.0
+        l[t, at[0]] = np.float32(1.0) + np.float32(2.0 ** -23) * rng.integers(-2, 3)
+        l[t, at[1]] = np.float32(1.0) + np.float32(2.0 ** -23) * rng.integers(-2, 3)
+    logits = torch.from_numpy(l).cuda()
+    for k in (1, 2, 3, 4):
+        check(M, logits, k, torch.from_numpy(bias).cuda(), router, groups, keep, "top2")
+        check(M, logits, k, None, router, groups, keep, "top2")
