@@ -449,7 +449,8 @@ cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
   }
   // A warp a row up to WARP_H, else a block: of few chunks a thread where there are fewer rows than SMs (latency), four otherwise.
   const bool warp = a.H <= WARP_H;
-  const int nc = warp ? (a.H <= 256 ? 1 : a.H <= 512 ? 2 : 4) : a.T <= num_sms && a.H <= 8192 ? 1 : 4;
+  const bool few = a.T <= num_sms, eight = !few && !a.residual && a.x_type != GT_FP32 && a.H >= 4096;
+  const int nc = warp ? (a.H <= 256 ? 1 : a.H <= 512 ? 2 : 4) : few && a.H <= 8192 ? 1 : eight ? 8 : 4;
   const long long blocks = warp ? ((long long)a.T + ROW_WARPS - 1) / ROW_WARPS : a.T;
   const int threads = warp ? 32 * ROW_WARPS : (a.H / CHUNK + nc * 32 - 1) / (nc * 32) * 32;
   auto types = [&](auto xt, auto ht, auto res) {
@@ -464,6 +465,9 @@ cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
              : nc == 2 ? go(integral_constant<int, 2>{}, True{}, W{})
                        : go(integral_constant<int, 4>{}, True{}, W{});
     if (nc == 1) return go(integral_constant<int, 1>{}, False{}, integral_constant<int, 1024>{});
+    if constexpr (!decltype(res)::value && decltype(xt)::value != GT_FP32) {
+      if (nc == 8) return go(integral_constant<int, 8>{}, False{}, integral_constant<int, 512>{});
+    }
     return threads <= 512 ? go(integral_constant<int, 4>{}, False{}, integral_constant<int, 512>{})
                           : go(integral_constant<int, 4>{}, False{}, integral_constant<int, 1024>{});
   };

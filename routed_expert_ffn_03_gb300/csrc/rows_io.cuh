@@ -197,9 +197,15 @@ struct Divisor {
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
+__device__ __forceinline__ uint32_t e4m3_four(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
 __device__ __forceinline__ uint2 e4m3_chunk(const float* s, const Divisor& by) {
-  auto q = [&](int i) { return by(s[i]); };
-  return make_uint2(e4m3_pair(q(0), q(1)) | e4m3_pair(q(2), q(3)) << 16, e4m3_pair(q(4), q(5)) | e4m3_pair(q(6), q(7)) << 16);
+  return make_uint2(e4m3_four(by(s[0]), by(s[1]), by(s[2]), by(s[3])), e4m3_four(by(s[4]), by(s[5]), by(s[6]), by(s[7])));
 }
 template <int NC, bool VEC>
 __device__ __forceinline__ void store_e4m3(uint8_t* row, int H, int tid, int stride, const float (&v)[NC * CHUNK], float scale) {
