@@ -297,8 +297,10 @@ __global__ void __launch_bounds__(512, 1) rms_norm_grad_ring_kernel(const NormGr
   }
   int s = 0, turn = 0;
   uint32_t parity = 0;
+  float next_rstd = first < a.T ? __ldg(a.rstd + first) : 0.f;   // a row ahead, as all of the row waits for it
   for (long long t = first; t < a.T; t += step, turn ^= 1) {
-    const float rstd = __ldg(a.rstd + t);
+    const float rstd = next_rstd;
+    if (t + step < a.T) next_rstd = __ldg(a.rstd + t + step);
     if (!mbar_wait_bounded(smem_u32(bars + s), parity, ring.wait.cycles)) gave_up[turn] = 1;
     const uint8_t* at = smem + s * stage;
     float nv[NC * CHUNK], d[NC * CHUNK], dot = 0.f;
