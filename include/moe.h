@@ -450,7 +450,7 @@ int moe_grouped8_kernel(const moe_grouped8_args* a, int num_sms);
 /* Root-mean-square norm of T rows of H, with the residual's addition in front of it and outputs in 16 (32) and 8 bits:
  *   h = x + residual, rounded to residual_dtype and written to sum (without a residual h = x);
  *   rstd = 1 / sqrt(mean over the row of h^2 + eps);  y = h rstd gain (gain [H], NULL: ones);
- *   out = y in out_dtype (or NULL);  scale[t] = max(max |y| / 448, 2^-100), out8 = y / scale[t] to the nearest e4m3 (or NULL);
+ *   out = y in out_dtype (or NULL);  scale[t] = max(max |y| (1/448 in fp32), 2^-100), out8 = e4m3(y / scale[t]), each rounded to nearest (or NULL);
  *   rstd [T], which the gradient reads (or NULL).
  * What is stored is what is normalised.  x, residual, gain and out each any moe_dtype; rows ldx, ld_residual, ld_sum, ldo, ldo8 apart.
  * sum may be the residual's own memory, out x's own, in the same layout and type.  Sums are fp32, each output is rounded once; h^2 has
@@ -496,8 +496,8 @@ typedef struct {
 moe_status moe_rms_norm_backward(const moe_rms_norm_grad_args* a, void* stream);
 size_t moe_rms_norm_backward_workspace(int T, int H);
 
-/* T rows of H in 8 bits, as moe_rms_norm makes them of y: scale[t] = max(max |x_t| / 448, 2^-100), out8 = x_t / scale[t] to the
- * nearest e4m3.  NaN stays NaN; a row with an infinity has scale infinity and is 0, NaN where the infinity stands.  Types, limits and
+/* T rows of H in 8 bits, as moe_rms_norm makes them of y: scale[t] = max(max |x_t| (1/448 in fp32), 2^-100), out8 = e4m3(x_t / scale[t]).
+ * NaN stays NaN; a row with an infinity has scale infinity and is 0, NaN where the infinity stands.  Types, limits and
  * alignment as there. */
 moe_status moe_quantize_rows(const void* x, long long ldx, int dtype, int T, int H, void* out8, long long ldo8, float* scale, void* stream);
 

@@ -139,6 +139,13 @@ __device__ __forceinline__ float silu(float g) {
   return g * ((g < 0.f ? e : 1.f) / (1.f + e));
 }
 
+// The same with a quick division, whose denominator is 1 to 2 here: within three steps of fp32, and fewer instructions where the
+// products are as quick as their epilogue (8 bits).
+__device__ __forceinline__ float silu_quick(float g) {
+  const float e = expf(-fabsf(g));
+  return g * __fdividef(g < 0.f ? e : 1.f, 1.f + e);
+}
+
 // two results rounded to a 16-bit type
 __device__ __forceinline__ uint32_t pack_out(float lo, float hi, int dtype) {
   if (dtype == GT_BF16) {

@@ -528,12 +528,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         } else {
           tmem_ld32(td + c, v);
         }
+        float col_scale = 0.f;   // 8 bits: of column c + lane
         if (F8) {   // lane: a row of W_e; columns: rows of x
           const int f = SW ? T.f0 + (int)rank * 64 + quarter * 16 + (lane & 15) : T.f0 + (int)rank * 128 + quarter * 32 + lane;
           const float ws = f < n_out ? __ldg(p.b_scale + (long long)T.e * p.n + (SW && lane >= 16 ? n_out : 0) + f) : 0.f;
-          const float xs = c + lane < T.rows ? row_scale(p, T.r0 + c + lane) : 0.f;
+          col_scale = c + lane < T.rows ? row_scale(p, T.r0 + c + lane) : 0.f;
+          // (with swiglu the columns' scales follow where a lane has its column's gate and up)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= ws * __shfl_sync(0xffffffffu, xs, i);
+          for (int i = 0; i < 32; ++i) v[i] *= SW ? ws : ws * __shfl_sync(0xffffffffu, col_scale, i);
         }
         if (WG) {
           // lane: row n of dw; columns: k
@@ -575,8 +577,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
             for (int i = 0; i < 32; i += 2) {
               const float mine = lane < 16 ? v[i] : v[i + 1];
               const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? v[i + 1] : v[i], 16);
-              const float g = lane < 16 ? mine : other, u = lane < 16 ? other : mine;
-              const float h = silu(g) * u;
+              float g = lane < 16 ? mine : other, u = lane < 16 ? other : mine;
+              if (F8) {
+                const float xs = __shfl_sync(0xffffffffu, col_scale, i + sub);
+                g *= xs;
+                u *= xs;
+              }
+              const float h = (F8 ? silu_quick(g) : silu(g)) * u;
               bool live;
               char* at = place(i, live);
               if (F32) store32_if(live, at, __float_as_uint(h));

@@ -1,7 +1,7 @@
 // rms_norm.cu - root-mean-square norm of rows, with the residual's addition and an output in 8 bits, and its gradient.
 //
 //   h = round(x + residual)  (to the residual's type; x without one),  rstd = 1 / sqrt(mean h^2 + eps),  y = h rstd g
-//   8 bits: scale = max(max|y| / 448, 2^-100), q = e4m3(y / scale)
+//   8 bits: scale = max(max|y| / 448, 2^-100) (by the fp32 inverse of 448), q = e4m3(y / scale)
 //   gradient: n = h rstd, d = dy g:  dh = rstd (d - n mean(d n)) + dsum,  dg = sum over rows of dy n
 //
 // What is stored is what is normalised, so that the gradient, which reads the stored sum, is that of what was computed.
@@ -14,7 +14,7 @@ namespace moe {
 
 namespace {
 
-constexpr float E4M3_MAX = 448.f;
+constexpr float E4M3_INVERSE = 1.f / 448.f;   // of the largest e4m3
 constexpr float LEAST_SCALE = 7.888609052210118e-31f;   // 2^-100: its inverse is a number, and a row of zeros stays zeros
 constexpr int ROW_WARPS = 8;                            // rows of a block where a warp takes a row
 
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) rms_norm_kernel(
   if (a.out)
     store_row<NC, VEC>(const_cast<char*>(row(a.out, a.ldo, a.out_type)), a.out_type, a.H, tid, stride, h);
   if (a.out8) {
-    const float scale = fmaxf(top * rstd / E4M3_MAX, LEAST_SCALE);
+    const float scale = fmaxf(top * rstd * E4M3_INVERSE, LEAST_SCALE);
     store_e4m3<NC, VEC>(a.out8 + t * a.ldo8, a.H, tid, stride, h, scale);
     if (tid == 0) a.scale[t] = scale;
   }
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(MAXT) rms_norm_words_kernel(const NormArgs a) 
   row_reduce<WARP>(ss, top);
   if (a.norm) rstd = rsqrtf(ss / (float)a.H + a.eps);
   if (tid == 0 && a.rstd) a.rstd[t] = rstd;
-  const float scale = fmaxf(top * rstd / E4M3_MAX, LEAST_SCALE);
+  const float scale = fmaxf(top * rstd * E4M3_INVERSE, LEAST_SCALE);
   const Divisor by(scale);
   if (tid == 0 && a.out8) a.scale[t] = scale;
   char* out = const_cast<char*>(row(a.out, a.ldo, a.out_type));
@@ -378,6 +378,115 @@ __global__ void __launch_bounds__(512 / PER_SM, PER_SM) rms_norm_grad_ring_kerne
     }
 }
 
+// Aligned rows of up to WARP_H, a warp a row: the three rows' words loaded together, a row ahead.
+struct RawChunk {   // 8 elements of a type known at run time, as they lie
+  uint32_t r[8];
+  __device__ __forceinline__ void load(const void* row, int c, int type, bool in) {
+    const char* p = static_cast<const char*>(row) + (long long)c * (type == GT_FP32 ? 32 : 16);
+    Word<true, GT_BF16> lo, hi;
+    lo.load(p, 0, 0, in);
+    hi.load(p, CHUNK, 0, in && type == GT_FP32);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[i] = lo.r[i];
+      r[4 + i] = hi.r[i];
+    }
+  }
+  __device__ __forceinline__ void values(int type, float (&v)[CHUNK]) const {
+    if (type == GT_FP32) {
+#pragma unroll
+      for (int i = 0; i < CHUNK; ++i) v[i] = __uint_as_float(r[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < CHUNK; ++i) {
+        const float2 f = two_16(r[i / 2], type);
+        v[i] = i % 2 ? f.y : f.x;
+      }
+    }
+  }
+};
+template <int NC>
+__global__ void __launch_bounds__(32 * ROW_WARPS) rms_norm_grad_warp_kernel(const NormGradArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, n = a.H / CHUNK;
+  const long long first = (long long)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5), step = (long long)gridDim.x * ROW_WARPS;
+  float dg[NC * CHUNK], g[NC * CHUNK];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    float v[CHUNK];
+#pragma unroll
+    for (int j = 0; j < CHUNK; ++j) v[j] = 1.f;
+    if (a.gain && lane + 32 * i < n) chunk_of<false>(a.gain, lane + 32 * i, a.gain_type, v);
+#pragma unroll
+    for (int j = 0; j < CHUNK; ++j) {
+      g[i * CHUNK + j] = v[j];
+      dg[i * CHUNK + j] = 0.f;
+    }
+  }
+  RawChunk y[NC], h[NC], ds[NC];
+  float rstd = 0.f;
+  auto load = [&](long long t) {
+    auto row = [&](const void* p, long long ld, int type) { return static_cast<const char*>(p) + t * ld * (type == GT_FP32 ? 4 : 2); };
+    const bool live = t < a.T;
+    rstd = live ? __ldg(a.rstd + t) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = lane + 32 * i;
+      y[i].load(row(a.dy, a.ld_dy, a.dy_type), c, a.dy_type, live && c < n);
+      h[i].load(row(a.h, a.ld_h, a.h_type), c, a.h_type, live && c < n);
+      ds[i].load(row(a.dsum, a.ld_dsum, a.dsum_type), c, a.dsum_type, live && a.dsum && c < n);
+    }
+  };
+  load(first);
+  for (long long t = first; t < a.T; t += step) {
+    float nv[NC * CHUNK], d[NC * CHUNK], s[NC * CHUNK], dot = 0.f;
+    const float r = rstd;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      float yv[CHUNK], hv[CHUNK], sv[CHUNK];
+      y[i].values(a.dy_type, yv);
+      h[i].values(a.h_type, hv);
+      ds[i].values(a.dsum_type, sv);
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) {
+        const int k = i * CHUNK + j;
+        nv[k] = hv[j] * r;
+        dg[k] = fmaf(yv[j], nv[k], dg[k]);
+        d[k] = yv[j] * g[k];
+        dot = fmaf(d[k], nv[k], dot);
+        s[k] = sv[j];
+      }
+    }
+    load(t + step);
+    dot = warp_sum(dot) / (float)a.H;
+    char* out = static_cast<char*>(a.dh) + t * a.ld_dh * (a.dh_type == GT_FP32 ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (lane + 32 * i < n) {
+        float v[CHUNK];
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j) v[j] = r * fmaf(-nv[i * CHUNK + j], dot, d[i * CHUNK + j]) + s[i * CHUNK + j];
+        put_chunk(out, lane + 32 * i, a.dh_type, v);
+      }
+  }
+  if (!a.dgain) return;
+  extern __shared__ float sums[];   // [ROW_WARPS][H], the warps' in order
+  float* mine = sums + (threadIdx.x >> 5) * a.H;
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+    if (lane + 32 * i < n)
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) mine[(lane + 32 * i) * CHUNK + j] = dg[i * CHUNK + j];
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.H; e += blockDim.x) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < ROW_WARPS; ++w) v += sums[w * a.H + e];
+    a.partial[(long long)blockIdx.x * a.H + e] = v;
+  }
+}
+
 // dgain = the blocks' sums: 32 columns a block, a warp every 32nd row (its loads all at once: 7.4 us for 304 rows of 4096, with 8 warps 8.0)
 constexpr int SUM_PARTS = 32;
 __global__ void __launch_bounds__(32 * SUM_PARTS) sum_blocks_kernel(const float* partial, float* out, int blocks, int H) {
@@ -534,6 +643,12 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, const WaitLimit& wait, c
       e = a.H <= 4096   ? launch_ring<1, 1>(a, ring, blocks, s)
           : a.H <= 8192 ? launch_ring<2, 1>(a, ring, blocks, s)
                         : launch_ring<4, 1>(a, ring, blocks, s);
+  } else if (vec && a.H <= WARP_H) {
+    const size_t smem = a.dgain ? (size_t)ROW_WARPS * a.H * sizeof(float) : 0;   // 32 KB at most
+    const int threads = 32 * ROW_WARPS;
+    e = a.H <= 256   ? launch(rms_norm_grad_warp_kernel<1>, blocks, threads, smem, s, a)
+        : a.H <= 512 ? launch(rms_norm_grad_warp_kernel<2>, blocks, threads, smem, s, a)
+                     : launch(rms_norm_grad_warp_kernel<4>, blocks, threads, smem, s, a);
   } else {
     const Share sh = share_of(a.H, 1);
     const size_t smem = sh.warp && a.dgain ? (size_t)ROW_WARPS * a.H * sizeof(float) : 0;   // 32 KB at most
@@ -543,7 +658,7 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, const WaitLimit& wait, c
     auto with = [&](auto nc) {
       using T = std::true_type;
       using F = std::false_type;
-      return sh.warp ? (vec ? go(nc, T{}, T{}) : go(nc, F{}, T{})) : vec ? go(nc, T{}, F{}) : go(nc, F{}, F{});
+      return sh.warp ? go(nc, F{}, T{}) : vec ? go(nc, T{}, F{}) : go(nc, F{}, F{});
     };
     e = sh.nc == 1   ? with(std::integral_constant<int, 1>{})
         : sh.nc == 2 ? with(std::integral_constant<int, 2>{})
