@@ -9,8 +9,7 @@
 // 64th of fp32's rate: all of 256 scores take 4 us.)  Where that does not decide it (a group's own best that close, more
 // candidates than lanes, scores that underflow) all of the token's scores are.
 #pragma once
-#include "group_route.h"
-#include "grouped.h"
+#include "group_sort.cuh"
 #include "route.cuh"
 
 namespace moe {
@@ -24,17 +23,7 @@ struct BalancedTables {
   uint8_t group[MAX_EXPERTS];
 };
 
-__device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : fminf(x, 3.402823466e38f); }
-__device__ __forceinline__ float load_logit(const void* p, long long i, int dtype) {
-  if (dtype == GT_FP32) return __ldg(static_cast<const float*>(p) + i);
-  const uint16_t b = __ldg(static_cast<const uint16_t*>(p) + i);
-  return dtype == GT_BF16 ? bf16_bits_to_float(b) : __half2float(__ushort_as_half(b));
-}
-__device__ __forceinline__ float logit_of(const GroupRouteArgs& a, long long t, int e) {
-  return clean(load_logit(a.logits, t * a.ld + e, a.dtype));
-}
-
-__device__ __forceinline__ void balanced_tables(const GroupRouteArgs& a, BalancedTables& tab) {
+__device__ __forceinline__ void balanced_tables(const BalancedRouteArgs& a, BalancedTables& tab) {
   const int size = a.E / a.groups;
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
     tab.bias[e] = a.bias ? clean(__ldg(a.bias + e)) : 0.f;
@@ -115,7 +104,7 @@ __device__ __forceinline__ unsigned kept_groups(T score, int groups, int keep, i
 }
 
 // sum over the token's experts of e^(l - m), in 64 bits
-static __device__ __noinline__ double exact_total(const GroupRouteArgs& a, long long t, int lane, float m) {
+static __device__ __noinline__ double exact_total(const BalancedRouteArgs& a, long long t, int lane, float m) {
   double z = 0.0;
   for (int e = lane; e < a.E; e += 32) {
     const float l = logit_of(a, t, e);
@@ -124,13 +113,13 @@ static __device__ __noinline__ double exact_total(const GroupRouteArgs& a, long 
   for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   return z;
 }
-__device__ __forceinline__ double exact_score(const GroupRouteArgs& a, float l, float m, double z) {
+__device__ __forceinline__ double exact_score(const BalancedRouteArgs& a, float l, float m, double z) {
   return a.kind == 1 ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m) / z;
 }
 
 // The whole selection in 64 bits: lane j < k receives the j-th expert, or -1.
 template <int NV>
-static __device__ __noinline__ int exact_select(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane, float m) {
+static __device__ __noinline__ int exact_select(const BalancedRouteArgs& a, const BalancedTables& tab, long long t, int lane, float m) {
   double c[NV];
   const double z = a.kind == 0 ? exact_total(a, t, lane, m) : 1.0;
   for (int i = 0; i < NV; ++i) {
@@ -197,7 +186,7 @@ constexpr int UNSETTLED = -2;
 // The kept groups where fp32 leaves them open, by the 64-bit scores of each group's best one or two experts, lane g looking through
 // group g (2 us; all of the token's scores in 64 bits take 10).  All lanes NO_GROUPS where a group's own best are too close to tell.
 constexpr unsigned NO_GROUPS = 0;
-static __device__ __noinline__ unsigned settle_groups(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane, float m,
+static __device__ __noinline__ unsigned settle_groups(const BalancedRouteArgs& a, const BalancedTables& tab, long long t, int lane, float m,
                                                       float inv, float err) {
   // the group's best one or two, and the best of the others; one of the same logit and bias as the least of those does not change the
   // score, as long as the best is no less than they are
@@ -245,7 +234,7 @@ static __device__ __noinline__ unsigned settle_groups(const GroupRouteArgs& a, c
 // the selected, and the others that are not below the least of them by more than the errors; those of the last one's logit and bias
 // are left out where all the selected are no less than it (of equal ones the lower was taken).  By fp32 values first; where those are closer than their errors, and not of the
 // same logit and bias, by 64 bits.  All lanes UNSETTLED where there are more candidates than lanes.
-static __device__ __noinline__ int settle(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane, int e, unsigned kept,
+static __device__ __noinline__ int settle(const BalancedRouteArgs& a, const BalancedTables& tab, long long t, int lane, int e, unsigned kept,
                                           float m, float inv, float err) {
   auto score = [&](float l, float b) {
     return a.bias ? (a.kind == 1 ? quick_inverse(1.f + quick_exp(-l)) : quick_exp(l - m) * inv) + b : l;
@@ -386,7 +375,7 @@ __device__ __forceinline__ uint32_t ordered_keys(const uint32_t (&key)[NV], int 
 // The selection of token t: lane j < k receives the j-th expert (-1: none) and its weight.  x: lane l's logits of experts
 // l + 32 i (-inf, NaN: masked; -inf past the experts).
 template <int NV>
-__device__ __forceinline__ void balanced_token(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane,
+__device__ __forceinline__ void balanced_token(const BalancedRouteArgs& a, const BalancedTables& tab, long long t, int lane,
                                                float (&x)[NV], int& my_e, float& my_w) {
   const bool limited = a.keep < a.groups, by_score = a.bias || limited;   // else logits are compared
   float top = -INFINITY;

@@ -37,7 +37,8 @@ moe_status device_setup(int dev, Device** out) {
   if (cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       moe::grouped_any_set_attributes() != cudaSuccess || moe::grouped_pair_set_attributes() != cudaSuccess ||
       moe::grouped_few_set_attributes() != cudaSuccess || moe::verify_set_attributes() != cudaSuccess ||
-      moe::group_route_set_attributes() != cudaSuccess || moe::rms_norm_set_attributes() != cudaSuccess) {
+      moe::group_route_set_attributes() != cudaSuccess || moe::balanced_route_set_attributes() != cudaSuccess ||
+      moe::rms_norm_set_attributes() != cudaSuccess) {
     cudaGetLastError();
     return MOE_ECUDA;
   }
@@ -244,20 +245,14 @@ extern "C" moe_status moe_balanced_route(const moe_balanced_route_args* a, void*
     return MOE_EINVAL;
   const moe::GroupRoutePlan plan = moe::group_route_plan(T, E, k);
   if (plan.workspace && (!a->workspace || a->workspace_bytes < plan.workspace)) return MOE_EINVAL;
-  moe::GroupRouteArgs r{a->logits, a->ld, a->dtype, T, E, k, a->router, a->idx, a->weights, a->offsets, a->rows, a->pairs,
-                        static_cast<int*>(a->workspace), plan.blocks, plan.per_block};
-  r.balanced = true;
-  r.top2 = a->group_score == MOE_GROUP_TOP2;
-  r.renorm = a->renormalize != 0;
-  r.bias = a->bias;
-  r.groups = a->groups;
-  r.keep = a->keep;
-  r.factor = a->scale;
-  r.places = a->places;
+  const moe::BalancedRouteArgs r{
+      {a->logits, a->ld, a->dtype, T, E, k, a->router, a->idx, a->weights, a->offsets, a->rows, a->pairs, static_cast<int*>(a->workspace),
+       plan.blocks, plan.per_block},
+      a->group_score == MOE_GROUP_TOP2, a->renormalize != 0, a->bias, a->groups, a->keep, a->scale, a->places};
   Device* d;
   const moe_status st = current_device(&d);
   if (st != MOE_OK) return st;
-  return done(moe::launch_group_route(r, (cudaStream_t)stream));
+  return done(moe::launch_balanced_route(r, (cudaStream_t)stream));
 }
 
 extern "C" moe_status moe_balanced_route_backward(const moe_balanced_route_grad_args* a, void* stream) {

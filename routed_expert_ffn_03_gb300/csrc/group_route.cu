@@ -8,39 +8,12 @@
 // the second waiting for the first on the device.  Bound: issue while selecting (about 350 instructions a token, 2.4 us for
 // 32 tokens an SM), latency while placing: 16384 tokens of 256 bf16 logits, k = 8, take 19.6 us (10 MB, 1.5 us at the
 // memory's rate), of which 8 are two launches' of any size; one token 4.8 us.
-#include "balanced_select.cuh"
-#include "common.cuh"
-#include "group_route.h"
-#include "grouped.h"
-#include "grouped_mma.cuh"
+#include "group_sort.cuh"
 #include "route.cuh"
 
 namespace moe {
 
 namespace {
-
-constexpr int GR_THREADS = 1024;
-constexpr int GR_WARPS = GR_THREADS / 32;
-// Tokens of the one-launch form, a cluster of up to 8 blocks: one or two a warp.  512 of 256 experts: 10.2 us, in two launches
-// 10.4, and 16 with the host's part; 1000: 15.0 and 10.4.  256 of 1000 experts, k = 32: 33 us, 1000 111 and 36.
-constexpr int one_launch(int E) { return E <= 512 ? 512 : 256; }
-constexpr int GR_CLUSTER = 2;         // blocks that add up their counts before they leave (4 do not fill every SM: 33 us, not 20)
-constexpr int GR_COUNTS = 16384;      // counts by warp and expert that a block holds
-
-// Lane l's logits of token t: experts l + 32 i.  The loads of each type stand together: a branch around each would run them
-// one after another.
-template <int NV>
-__device__ __forceinline__ void load_token(const GroupRouteArgs& a, long long t, int lane, float (&l)[NV]) {
-  if (a.dtype == GT_FP32) {
-    const float* src = static_cast<const float*>(a.logits) + t * a.ld;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = lane + 32 * i < a.E ? __ldg(src + lane + 32 * i) : -INFINITY;
-  } else {
-    const uint16_t* src = static_cast<const uint16_t*>(a.logits) + t * a.ld;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = __uint_as_float(lane + 32 * i < a.E ? __ldg(src + lane + 32 * i) : 0u);   // raw
-  }
-}
 
 // Keys carry the expert in their low 10 bits, a lower one larger, so each is unique and none is 0 but the masked ones.  16-bit
 // logits fit the 22 bits above whole; of fp32 logits those are the leading ones.
@@ -216,147 +189,32 @@ __device__ __forceinline__ void route_tokens(const GroupRouteArgs& a, long long 
   }
 }
 
-// the same of one token for the balanced selection
-template <int NV>
-__device__ __forceinline__ void route_balanced(const GroupRouteArgs& a, const BalancedTables& tab, long long t, int lane, int* hist) {
-  float l[NV];
-  load_token<NV>(a, t, lane, l);
-  auto values = [&](auto value) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = lane + 32 * i < a.E ? value(l[i]) : -INFINITY;
-  };
-  if (a.dtype == GT_BF16) values([](float x) { return __uint_as_float(__float_as_uint(x) << 16); });
-  else if (a.dtype == GT_FP16) values([](float x) { return __half2float(__ushort_as_half((unsigned short)__float_as_uint(x))); });
-  int e;
-  float w;
-  balanced_token<NV>(a, tab, t, lane, l, e, w);
-  if (lane < a.k) {
-    a.idx[t * a.k + lane] = e;
-    a.weights[t * a.k + lane] = e >= 0 ? w : 0.f;
-    if (e >= 0) atomicAdd(&hist[e], 1);   // a count: its order does not matter
-  }
-}
-
-// in kernels of the balanced selection alone
-__device__ __forceinline__ BalancedTables& tables() {
-  __shared__ BalancedTables t;
-  return t;
-}
-
 // this block's tokens; and its pairs by expert into hist (shared)
-template <int NV, bool BAL>
+template <int NV>
 __device__ __forceinline__ void select_tokens(const GroupRouteArgs& a, int* hist) {
-  constexpr int U = !BAL && NV <= 8 ? 2 : 1;
+  constexpr int U = NV <= 8 ? 2 : 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int e = threadIdx.x; e < a.E; e += GR_THREADS) hist[e] = 0;
-  if constexpr (BAL) balanced_tables(a, tables());
   __syncthreads();
   const long long t0 = min((long long)blockIdx.x * a.per_block, (long long)a.T), t1 = min(t0 + a.per_block, (long long)a.T);
-  if constexpr (BAL) {
-    for (long long t = t0 + warp; t < t1; t += GR_WARPS) route_balanced<NV>(a, tables(), t, lane, hist);
-  } else {
-    for (long long t = t0 + warp; t < t1; t += U * GR_WARPS) {
-      float l[U][NV];
+  for (long long t = t0 + warp; t < t1; t += U * GR_WARPS) {
+    float l[U][NV];
 #pragma unroll
-      for (int u = 0; u < U; ++u) load_token<NV>(a, min(t + u * GR_WARPS, t1 - 1), lane, l[u]);
-      route_tokens<NV, U>(a, t, t1, lane, l, hist);
-    }
+    for (int u = 0; u < U; ++u) load_token<NV>(a, min(t + u * GR_WARPS, t1 - 1), lane, l[u]);
+    route_tokens<NV, U>(a, t, t1, lane, l, hist);
   }
   __syncthreads();
-}
-
-// A block's pairs, shared out to W warps in runs of whole 32s; counts (shared) [W][E].
-struct Pairs {
-  int W;
-  long long p0, p1, q0, q1;   // the block's, this warp's
-  int* next;                  // this warp's row of counts
-};
-__device__ __forceinline__ Pairs block_pairs(const GroupRouteArgs& a, int* counts) {
-  Pairs s;
-  const int warp = threadIdx.x >> 5;
-  s.W = min(GR_WARPS, GR_COUNTS / a.E);
-  const long long P = (long long)a.T * a.k;
-  s.p0 = min((long long)blockIdx.x * a.per_block * a.k, P);
-  s.p1 = min(s.p0 + (long long)a.per_block * a.k, P);
-  const long long share = ((s.p1 - s.p0 + s.W - 1) / s.W + 31) / 32 * 32;
-  s.q0 = min(s.p0 + warp * share, s.p1);
-  s.q1 = warp < s.W ? min(s.q0 + share, s.p1) : s.q0;
-  s.next = counts + warp * a.E;
-  return s;
-}
-// counts (zeros before) by warp and expert
-__device__ __forceinline__ void count_pairs(const GroupRouteArgs& a, const Pairs& s) {
-  for (long long i = s.q0 + (threadIdx.x & 31); i < s.q1; i += 32) {
-    const int e = __ldcg(a.idx + i);
-    if (e >= 0) atomicAdd(&s.next[e], 1);
-  }
-}
-// Places this block's pairs.  before, all (shared, [E]): an expert's pairs in earlier blocks and in all of them.
-template <bool BAL>
-__device__ __forceinline__ void place_pairs(const GroupRouteArgs& a, const Pairs& s, const int* before, const int* all, int* counts) {
-  __shared__ int wsum[GR_WARPS];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.E;
-  // offsets: an exclusive scan of all over the experts, thread e its own
-  const int mine = tid < E ? all[tid] : 0;
-  int inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) wsum[warp] = inc;
-  __syncthreads();
-  int sums = wsum[lane];   // GR_WARPS == 32: every warp scans the warps' sums for itself
-  const int own = sums;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, sums, o);
-    if (lane >= o) sums += v;
-  }
-  const int off = inc - mine + __shfl_sync(0xffffffffu, sums - own, warp), total = __shfl_sync(0xffffffffu, sums, 31);
-  if (tid < E) {   // counts become first positions
-    if (blockIdx.x == 0) a.offsets[tid] = off;
-    int pos = off + before[tid];
-#pragma unroll 8
-    for (int w = 0; w < s.W; ++w) {
-      const int c = counts[w * E + tid];
-      counts[w * E + tid] = pos;
-      pos += c;
-    }
-  }
-  if (blockIdx.x == 0 && tid == 0) a.offsets[E] = total;
-  __syncthreads();
-  for (long long i0 = s.q0; i0 < s.q1; i0 += 32) {
-    const long long i = i0 + lane;
-    const int e = i < s.q1 ? __ldcg(a.idx + i) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    int pos = 0;
-    if (e >= 0) pos = s.next[e] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (BAL && i < s.q1) a.places[i] = e >= 0 ? pos : -1;
-    if (e >= 0) {
-      a.pairs[pos] = (int)i;
-      a.rows[pos] = (int)((unsigned)i / (unsigned)a.k);
-      if (lane == 31 - __clz(same)) s.next[e] = pos + 1;
-    }
-    __syncwarp();
-  }
-  // no pair stands behind the last group
-  for (long long i = max(s.p0, (long long)total) + tid; i < s.p1; i += GR_THREADS) {
-    a.pairs[i] = -1;
-    a.rows[i] = -1;
-  }
 }
 
 // One launch: the blocks are one cluster, and read each other's counts.
-template <int NV, bool BAL>
+template <int NV>
 __global__ void __launch_bounds__(GR_THREADS, 1) group_one_kernel(GroupRouteArgs a) {
   extern __shared__ int counts[];
   __shared__ int hist[1024], all[1024], before[1024];
   const Pairs s = block_pairs(a, counts);
   for (int i = threadIdx.x; i < s.W * a.E; i += GR_THREADS) counts[i] = 0;
   pdl_wait();
-  select_tokens<NV, BAL>(a, hist);
+  select_tokens<NV>(a, hist);
   if (a.blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   count_pairs(a, s);   // while the others arrive
   if (a.blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -374,17 +232,17 @@ __global__ void __launch_bounds__(GR_THREADS, 1) group_one_kernel(GroupRouteArgs
   before[e] = mine;
   if (a.blocks > 1) cluster_sync_all();   // the others read this block's counts until here
   else __syncthreads();
-  place_pairs<BAL>(a, s, before, all, counts);
+  place_pairs<false>(a, s, before, all, counts, nullptr);
 }
 
 // The counts leave by clusters, hist [clusters][E], with each block's share of its cluster's before it, [blocks][E] behind:
 // the next kernel's blocks then read half of the rows (read one by one, they took half of that kernel's time).
-template <int NV, bool BAL>
+template <int NV>
 __global__ void __launch_bounds__(GR_THREADS, 1) group_select_kernel(GroupRouteArgs a) {
   __shared__ int hist[1024];
   pdl_launch_dependents();
   pdl_wait();
-  select_tokens<NV, BAL>(a, hist);
+  select_tokens<NV>(a, hist);
   cluster_sync_all();
   const int rank = (int)cluster_rank(), clusters = a.blocks / GR_CLUSTER;
   for (int e = threadIdx.x; e < a.E; e += GR_THREADS) {
@@ -402,7 +260,6 @@ __global__ void __launch_bounds__(GR_THREADS, 1) group_select_kernel(GroupRouteA
   cluster_sync_all();   // the others read this block's counts until here
 }
 
-template <bool BAL>
 __global__ void __launch_bounds__(GR_THREADS, 1) group_place_kernel(GroupRouteArgs a) {
   extern __shared__ int counts[];
   __shared__ int all[1024], before[1024];
@@ -427,45 +284,21 @@ __global__ void __launch_bounds__(GR_THREADS, 1) group_place_kernel(GroupRouteAr
     atomicAdd(&before[e], p);
   }
   __syncthreads();
-  place_pairs<BAL>(a, pairs, before, all, counts);
+  place_pairs<false>(a, pairs, before, all, counts, nullptr);
 }
 
-template <typename... A>
-cudaError_t launch(void (*kernel)(A...), int blocks, int cluster, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(blocks);
-  c.blockDim = dim3(GR_THREADS);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = cluster;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  c.attrs = at;
-  c.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&c, kernel, args...);
-}
-
-template <int NV, bool BAL>
+template <int NV>
 cudaError_t launch_as(const GroupRouteArgs& a, cudaStream_t s) {
   const int warps = GR_COUNTS / a.E < GR_WARPS ? GR_COUNTS / a.E : GR_WARPS;
   const size_t smem = (size_t)warps * a.E * sizeof(int);
-  if (a.T <= one_launch(a.E)) return launch(group_one_kernel<NV, BAL>, a.blocks, a.blocks, smem, s, a);
-  cudaError_t e = launch(group_select_kernel<NV, BAL>, a.blocks, GR_CLUSTER, 0, s, a);
-  return e != cudaSuccess ? e : launch(group_place_kernel<BAL>, a.blocks, 1, smem, s, a);
+  if (a.T <= one_launch(a.E)) return launch(group_one_kernel<NV>, a.blocks, a.blocks, smem, s, a);
+  cudaError_t e = launch(group_select_kernel<NV>, a.blocks, GR_CLUSTER, 0, s, a);
+  return e != cudaSuccess ? e : launch(group_place_kernel, a.blocks, 1, smem, s, a);
 }
 
 template <int NV>
 cudaError_t set_attribute() {
-  const cudaError_t e = cudaFuncSetAttribute(group_one_kernel<NV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
-  return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(group_one_kernel<NV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
-}
-template <int NV>
-cudaError_t launch_of(const GroupRouteArgs& a, cudaStream_t s) {
-  return a.balanced ? launch_as<NV, true>(a, s) : launch_as<NV, false>(a, s);
+  return cudaFuncSetAttribute(group_one_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
 }
 
 }  // namespace
@@ -476,9 +309,7 @@ cudaError_t group_route_set_attributes() {
   if (e == cudaSuccess) e = set_attribute<16>();
   if (e == cudaSuccess) e = set_attribute<32>();
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(group_place_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(group_place_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
+    e = cudaFuncSetAttribute(group_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_COUNTS * 4);
   return e;
 }
 
@@ -500,9 +331,9 @@ GroupRoutePlan group_route_plan(int T, int E, int k) {
 }
 
 cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s) {
-  if (a.E <= 128) return launch_of<4>(a, s);
-  if (a.E <= 256) return launch_of<8>(a, s);
-  return a.E <= 512 ? launch_of<16>(a, s) : launch_of<32>(a, s);
+  if (a.E <= 128) return launch_as<4>(a, s);
+  if (a.E <= 256) return launch_as<8>(a, s);
+  return a.E <= 512 ? launch_as<16>(a, s) : launch_as<32>(a, s);
 }
 
 }  // namespace moe

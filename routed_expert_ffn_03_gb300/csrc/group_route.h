@@ -15,12 +15,6 @@ struct GroupRouteArgs {
   int *offsets, *rows, *pairs;
   int* hist;               // pairs by expert: of each cluster of blocks, then of a cluster's blocks before each
   int blocks, per_block;   // tokens per block
-  // the balanced selection
-  bool balanced, top2, renorm;   // top2: a group's score is the sum of its two largest, not its largest
-  const float* bias;             // [E] or null
-  int groups, keep;
-  float factor;
-  int* places;                   // [T][k]
 };
 struct GroupRoutePlan {
   int blocks, per_block;
@@ -30,8 +24,18 @@ GroupRoutePlan group_route_plan(int T, int E, int k);
 cudaError_t launch_group_route(const GroupRouteArgs& a, cudaStream_t s);
 cudaError_t group_route_set_attributes();
 
+// The selection with a bias for balance, limited to groups of experts.
+struct BalancedRouteArgs : GroupRouteArgs {
+  bool top2, renorm;   // top2: a group's score is the sum of its two largest, not its largest
+  const float* bias;   // [E] or null
+  int groups, keep;
+  float factor;
+  int* places;         // [T][k]
+};
+cudaError_t launch_balanced_route(const BalancedRouteArgs& a, cudaStream_t s);
+cudaError_t balanced_route_set_attributes();
 
-// Gradient of the balanced selection's weights by the logits.
+// Gradient of its weights by the logits.
 struct RouteGradArgs {
   const float* dweights;   // [T][k]
   const void* logits;

@@ -438,6 +438,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
       auto run_at = [&](int q) { return WG && PARTS && !F32 ? (q >> 1) * 128 + part * 64 + (q & 1) * 32 : part * 32 + 64 * q; };
       float sum[PARTS ? 4 : 1][32];
       uint32_t td = 0;
+      // 8 bits: the scales of this lane's row of W_e and of its column of each run, loaded while the products run (where they are
+      // wanted, a run waits two round trips for them: Mixtral-shaped gate/up of 2002 rows 200 and 195 us, 875 rows, n = 7680, k = 448 20.7 and
+      // 19.4)
+      float ws = 0.f, xs[F8 ? 4 : 1];
+      if (F8) {
+        const int f = SW ? T.f0 + (int)rank * 64 + quarter * 16 + (lane & 15) : T.f0 + (int)rank * 128 + quarter * 32 + lane;
+        if (f < n_out) ws = __ldg(p.b_scale + (long long)T.e * p.n + (SW && lane >= 16 ? n_out : 0) + f);
+#pragma unroll
+        for (int q = 0; q < (F8 ? 4 : 1); ++q) {
+          const int c = run_at(q) + lane;
+          xs[q] = c < T.rows ? row_scale(p, T.r0 + c) : 0.f;
+        }
+      }
       if (PARTS) {
 #pragma unroll
         for (int q = 0; q < (PARTS ? 4 : 1); ++q)
@@ -528,11 +541,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         } else {
           tmem_ld32(td + c, v);
         }
-        float col_scale = 0.f;   // 8 bits: of column c + lane
-        if (F8) {   // lane: a row of W_e; columns: rows of x
-          const int f = SW ? T.f0 + (int)rank * 64 + quarter * 16 + (lane & 15) : T.f0 + (int)rank * 128 + quarter * 32 + lane;
-          const float ws = f < n_out ? __ldg(p.b_scale + (long long)T.e * p.n + (SW && lane >= 16 ? n_out : 0) + f) : 0.f;
-          col_scale = c + lane < T.rows ? row_scale(p, T.r0 + c + lane) : 0.f;
+        const float col_scale = F8 ? xs[F8 ? q : 0] : 0.f;
+        if (F8) {
           // (with swiglu the columns' scales follow where a lane has its column's gate and up)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] *= SW ? ws : ws * __shfl_sync(0xffffffffu, col_scale, i);
@@ -579,9 +589,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
               const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? v[i + 1] : v[i], 16);
               float g = lane < 16 ? mine : other, u = lane < 16 ? other : mine;
               if (F8) {
-                const float xs = __shfl_sync(0xffffffffu, col_scale, i + sub);
-                g *= xs;
-                u *= xs;
+                const float s = __shfl_sync(0xffffffffu, col_scale, i + sub);
+                g *= s;
+                u *= s;
               }
               const float h = (F8 ? silu_quick(g) : silu(g)) * u;
               bool live;

@@ -7,7 +7,7 @@
 //   softmax over all:      dl_e = P_e ([e selected] v_e - sum_j P_j v_j)
 // and 0 for the other experts.  The bias and the groups choose; no gradient passes through them.  A warp takes a token: one pass
 // over its row.  Bound: memory (the result; with softmax over all the logits too).
-#include "balanced_select.cuh"
+#include "group_sort.cuh"
 #include "rows_io.cuh"
 
 namespace moe {
