@@ -21,14 +21,28 @@ constexpr int MAX_EXPERTS = 1024;
 struct BalancedTables {
   float bias[MAX_EXPERTS];
   uint8_t group[MAX_EXPERTS];
+  int set;   // whether any bias is not 0
 };
 
 __device__ __forceinline__ void balanced_tables(const BalancedRouteArgs& a, BalancedTables& tab) {
   const int size = a.E / a.groups;
+  bool set = false;
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    tab.bias[e] = a.bias ? clean(__ldg(a.bias + e)) : 0.f;
+    const float b = a.bias ? clean(__ldg(a.bias + e)) : 0.f;
+    tab.bias[e] = b;
     tab.group[e] = (uint8_t)(e / size);
+    set |= b != 0.f;
   }
+  set = __syncthreads_or(set);
+  if (threadIdx.x == 0) tab.set = set;
+}
+// Whether different logits have different scores (the largest being m): a sigmoid near 1 and a softmax beside an infinite logit have not.
+__device__ __forceinline__ bool scores_tell(const BalancedRouteArgs& a, float m) { return m < (a.kind == 1 ? 20.f : 1e30f); }
+// Whether a token's experts are ordered by their biased scores.  Without a bias, and with biases that are all 0 (as training starts;
+// there 16-bit logits are often equal), they are ordered by their logits, which is the scores' order.  Groups' scores likewise, where
+// they are not sums.
+__device__ __forceinline__ bool by_biased(const BalancedRouteArgs& a, const BalancedTables& tab, float m) {
+  return a.bias && (tab.set || !scores_tell(a, m));
 }
 
 __device__ __forceinline__ float key_value(uint32_t k) { return k ? key_logit(k) : -INFINITY; }
@@ -122,12 +136,13 @@ template <int NV>
 static __device__ __noinline__ int exact_select(const BalancedRouteArgs& a, const BalancedTables& tab, long long t, int lane, float m) {
   double c[NV];
   const double z = a.kind == 0 ? exact_total(a, t, lane, m) : 1.0;
+  const bool by_bias = by_biased(a, tab, m), scores = by_bias || a.top2 || !scores_tell(a, m);
   for (int i = 0; i < NV; ++i) {
     const int e = lane + 32 * i;
     c[i] = -INFINITY;
     if (e < a.E) {
       const float l = logit_of(a, t, e), b = tab.bias[e];
-      if (l > -INFINITY && b > -INFINITY) c[i] = exact_score(a, l, m, z) + (double)b;
+      if (l > -INFINITY && b > -INFINITY) c[i] = scores ? exact_score(a, l, m, z) + (double)b : (double)l;
     }
   }
   unsigned kept = ~0u;
@@ -151,11 +166,10 @@ static __device__ __noinline__ int exact_select(const BalancedRouteArgs& a, cons
     }
     kept = kept_groups(score, a.groups, a.keep, lane);
   }
-  // without a bias logits are compared, as their scores' order is theirs
   for (int i = 0; i < NV; ++i) {
     const int e = lane + 32 * i;
     if (e >= a.E || !((kept >> (tab.group[e] & 31)) & 1u)) c[i] = -INFINITY;
-    else if (!a.bias && c[i] > -INFINITY) c[i] = logit_of(a, t, e);
+    else if (!by_bias && c[i] > -INFINITY) c[i] = logit_of(a, t, e);
   }
   int mine = -1;
   for (int j = 0; j < a.k; ++j) {
@@ -183,51 +197,71 @@ static __device__ __noinline__ int exact_select(const BalancedRouteArgs& a, cons
 
 constexpr int UNSETTLED = -2;
 
-// The kept groups where fp32 leaves them open, by the 64-bit scores of each group's best one or two experts, lane g looking through
-// group g (2 us; all of the token's scores in 64 bits take 10).  All lanes NO_GROUPS where a group's own best are too close to tell.
+// Which `need` of the groups `open` stay, where fp32 leaves it so, by the 64-bit scores of each one's best one or two experts (all of the
+// token's scores in 64 bits take some 10 us).  NO_GROUPS where a group's own best are too close to tell, too.
 constexpr unsigned NO_GROUPS = 0;
-static __device__ __noinline__ unsigned settle_groups(const BalancedRouteArgs& a, const BalancedTables& tab, long long t, int lane, float m,
-                                                      float inv, float err) {
-  // the group's best one or two, and the best of the others; one of the same logit and bias as the least of those does not change the
-  // score, as long as the best is no less than they are
-  const int last = a.top2 ? 1 : 0;
-  float c[2] = {-INFINITY, -INFINITY}, other = -INFINITY;
-  int e[2] = {0, 0};
-  bool skipped = false;
-  auto alike = [&](int p, int q) { return logit_of(a, t, p) == logit_of(a, t, q) && tab.bias[p] == tab.bias[q]; };
+static __device__ __noinline__ unsigned settle_groups(const BalancedRouteArgs& a, const BalancedTables& tab, long long t, int lane, unsigned open,
+                                                      int need, float m, float inv, float err) {
+  const int size = a.E / a.groups, best = a.top2 ? 2 : 1;
   auto apart = [&](float p, float q) { return p - q > 2.f * err + 0x1p-22f * fmaxf(fabsf(p), fabsf(q)); };
-  const int size = a.E / a.groups;
-  if (lane < a.groups)
-    for (int q = lane * size; q < (lane + 1) * size; ++q) {
-      const float l = logit_of(a, t, q);
-      if (!(l > -INFINITY)) continue;
-      const float v = (a.kind == 1 ? quick_inverse(1.f + quick_exp(-l)) : quick_exp(l - m) * inv) + tab.bias[q];
-      float out = v;
-      int out_e = q;
-      if (v > c[0]) {
-        out = c[0], out_e = e[0];
-        c[0] = v, e[0] = q;
+  int my_e[2] = {-1, -1};
+  for (unsigned left = open; left; left &= left - 1) {
+    const int g = __ffs(left) - 1;
+    int e[2] = {-1, -1};
+    float c[3] = {-INFINITY, -INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, b[2] = {0.f, 0.f};
+    bool skipped = false;
+    // the best one or two, and the best of the others; one of the same logit and bias as the least of those does not change the score, as
+    // long as the best is no less than they are
+    for (int r = 0; r <= best; ++r) {
+      uint32_t key = 0;
+      int at = 0x7fffffff;
+      for (int q = g * size + lane; q < (g + 1) * size; q += 32) {
+        const float x = logit_of(a, t, q), y = tab.bias[q];
+        if (!(x > -INFINITY) || !(y > -INFINITY) || q == e[0] || q == e[1]) continue;
+        if (r == best && x == l[best - 1] && y == b[best - 1]) {
+          skipped = true;
+          continue;
+        }
+        const uint32_t k = logit_key((a.kind == 1 ? quick_inverse(1.f + quick_exp(-x)) : quick_exp(x - m) * inv) + y);
+        if (k > key) {
+          key = k;
+          at = q;
+        }
       }
-      if (last && out > c[1]) {
-        const float x = c[1];
-        const int y = e[1];
-        c[1] = out, e[1] = out_e;
-        out = x, out_e = y;
+      const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+      if (top == 0) break;   // uniform
+      at = (int)__reduce_min_sync(0xffffffffu, key == top ? (unsigned)at : 0x7fffffffu);
+      c[r] = key_value(top);
+      if (r < best) {
+        e[r] = at;
+        l[r] = logit_of(a, t, at);
+        b[r] = tab.bias[at];
       }
-      if (out > -INFINITY && out == c[last] && alike(out_e, e[last])) skipped = true;
-      else other = fmaxf(other, out);
     }
-  const bool open = (other > -INFINITY && !apart(c[last], other)) || (last && skipped && !apart(c[0], c[1]) && !alike(e[0], e[1]));
-  if (__any_sync(0xffffffffu, open)) return NO_GROUPS;
+    skipped = __any_sync(0xffffffffu, skipped);
+    if ((c[best] > -INFINITY && !apart(c[best - 1], c[best])) ||
+        (best == 2 && skipped && !apart(c[0], c[1]) && !(l[0] == l[1] && b[0] == b[1])))
+      return NO_GROUPS;
+    if (lane == g) {
+      my_e[0] = e[0];
+      my_e[1] = e[1];
+    }
+  }
   // (without a bias the softmax's sum is common to all)
-  const double z = a.kind == 0 && a.bias ? exact_total(a, t, lane, m) : 1.0;
+  const double z = a.kind == 0 && tab.set ? exact_total(a, t, lane, m) : 1.0;
   double score = -INFINITY;
-  for (int i = 0; i < (a.top2 ? 2 : 1); ++i)
-    if (c[i] > -INFINITY) {
-      const double v = exact_score(a, logit_of(a, t, e[i]), m, z) + (double)tab.bias[e[i]];
+  for (int i = 0; i < best; ++i)
+    if (my_e[i] >= 0) {
+      const double v = exact_score(a, logit_of(a, t, my_e[i]), m, z) + (double)tab.bias[my_e[i]];
       score = i ? score + v : v;
     }
-  return kept_groups(score, a.groups, a.keep, lane);
+  int rank = 0;
+  for (unsigned left = open; left; left &= left - 1) {
+    const int q = __ffs(left) - 1;
+    const double o = __shfl_sync(0xffffffffu, score, q);
+    rank += o > score || (o == score && q < lane);
+  }
+  return __ballot_sync(0xffffffffu, ((open >> lane) & 1u) && rank < need);
 }
 
 // The order of a token's selected experts (lane j: the j-th, e; -1 from n on), where their keys leave it open.  The candidates, one a lane:
@@ -236,18 +270,19 @@ static __device__ __noinline__ unsigned settle_groups(const BalancedRouteArgs& a
 // same logit and bias, by 64 bits.  All lanes UNSETTLED where there are more candidates than lanes.
 static __device__ __noinline__ int settle(const BalancedRouteArgs& a, const BalancedTables& tab, long long t, int lane, int e, unsigned kept,
                                           float m, float inv, float err) {
+  const bool by_bias = by_biased(a, tab, m);
   auto score = [&](float l, float b) {
-    return a.bias ? (a.kind == 1 ? quick_inverse(1.f + quick_exp(-l)) : quick_exp(l - m) * inv) + b : l;
+    return by_bias ? (a.kind == 1 ? quick_inverse(1.f + quick_exp(-l)) : quick_exp(l - m) * inv) + b : l;
   };
   const int n = __popc(__ballot_sync(0xffffffffu, e >= 0));
   const float my_l = e >= 0 ? logit_of(a, t, e) : INFINITY, my_b = e >= 0 ? tab.bias[e] : 0.f;
   const float l_last = __shfl_sync(0xffffffffu, my_l, n - 1), b_last = __shfl_sync(0xffffffffu, my_b, n - 1);
   const float least = -warp_max_f(e >= 0 ? -score(my_l, my_b) : -INFINITY);
-  const float limit = least - (a.bias ? 2.f * err + 0x1p-21f * fabsf(least) : 0.f);
+  const float limit = least - (by_bias ? 2.f * err + 0x1p-21f * fabsf(least) : 0.f);
   if (!(limit > -INFINITY)) return UNSETTLED;
   const float c_last = score(l_last, b_last);
   const bool above = __all_sync(0xffffffffu, e < 0 || (my_l == l_last && my_b == b_last) ||
-                                                 score(my_l, my_b) - c_last > (a.bias ? 2.f * err + 0x1p-21f * fmaxf(fabsf(c_last), fabsf(least)) : 0.f));
+                                                 score(my_l, my_b) - c_last > (by_bias ? 2.f * err + 0x1p-21f * fmaxf(fabsf(c_last), fabsf(least)) : 0.f));
   int count = n;
   for (int i0 = 0; i0 < a.E; i0 += 32) {
     const int q = i0 + lane;
@@ -275,7 +310,7 @@ static __device__ __noinline__ int settle(const BalancedRouteArgs& a, const Bala
     return rank;
   };
   int rank = order();
-  if (a.bias) {
+  if (by_bias) {
     bool close = false;
     const float f = (float)v;
     for (int q = 0; q < count; ++q) {
@@ -377,7 +412,7 @@ __device__ __forceinline__ uint32_t ordered_keys(const uint32_t (&key)[NV], int 
 template <int NV>
 __device__ __forceinline__ void balanced_token(const BalancedRouteArgs& a, const BalancedTables& tab, long long t, int lane,
                                                float (&x)[NV], int& my_e, float& my_w) {
-  const bool limited = a.keep < a.groups, by_score = a.bias || limited;   // else logits are compared
+  const bool limited = a.keep < a.groups;
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NV; ++i) top = fmaxf(top, x[i]);   // (NaN is passed over; no comparison below takes it)
@@ -387,6 +422,7 @@ __device__ __forceinline__ void balanced_token(const BalancedRouteArgs& a, const
 #pragma unroll
     for (int i = 0; i < NV; ++i) x[i] = x[i] == INFINITY ? m : x[i];
   }
+  const bool by_bias = by_biased(a, tab, m), by_score = by_bias || (limited && (a.top2 || !scores_tell(a, m)));   // else logits are compared
   float inv = 1.f, err = 0.f;        // softmax: one over the sum; the scores' absolute error
   uint32_t key[NV];                  // by which experts are compared
   if (a.kind == 0 && (by_score || !a.renorm)) {
@@ -418,7 +454,7 @@ __device__ __forceinline__ void balanced_token(const BalancedRouteArgs& a, const
       key[i] = x[i] > -INFINITY && c > -INFINITY ? quick_key(c) : 0u;   // (c is never -0)
     }
   }
-  if (!by_score) {
+  if (!by_score) {   // (with a bias here it is 0)
 #pragma unroll
     for (int i = 0; i < NV; ++i) key[i] = x[i] > -INFINITY ? logit_key(x[i]) : 0u;
   }
@@ -467,9 +503,14 @@ __device__ __forceinline__ void balanced_token(const BalancedRouteArgs& a, const
     float last, next;
     kept = kept_by_rounds(score, a.groups, a.keep, lane, last, next);
     // two scores a group, and the roundings of their sums with the biases and each other
-    if (next > -INFINITY && !(last - next > 4.f * err + 0x1p-21f * fmaxf(fabsf(last), fabsf(next))) && !doubt) {
-      kept = settle_groups(a, tab, t, lane, m, inv, err);
-      doubt = kept == NO_GROUPS;
+    const float near = 4.f * err + 0x1p-21f * fmaxf(fabsf(last), fabsf(next));
+    if (by_score && next > -INFINITY && !(last - next > near) && !doubt) {
+      const bool in = (kept >> lane) & 1u;
+      const unsigned sure = __ballot_sync(0xffffffffu, in && score - next > near);
+      const unsigned open = __ballot_sync(0xffffffffu, lane < a.groups && score > -INFINITY && (in ? !(score - next > near) : !(last - score > near)));
+      const unsigned more = settle_groups(a, tab, t, lane, open, __popc(kept) - __popc(sure), m, inv, err);
+      doubt = more == NO_GROUPS;
+      kept = sure | more;
     }
     unsigned stay = kept;   // by register, whole groups
     if (whole && per > 1) {
@@ -484,7 +525,7 @@ __device__ __forceinline__ void balanced_token(const BalancedRouteArgs& a, const
       } else if (!((kept >> (tab.group[min(lane + 32 * i, MAX_EXPERTS - 1)] & 31)) & 1u)) {
         key[i] = 0;
       }
-      if (!a.bias && key[i]) key[i] = logit_key(x[i]);
+      if (by_score && !by_bias && key[i]) key[i] = logit_key(x[i]);
     }
   }
   int e = -1;
@@ -495,7 +536,7 @@ __device__ __forceinline__ void balanced_token(const BalancedRouteArgs& a, const
     constexpr int ID = NV == 4 ? 7 : NV == 8 ? 8 : NV == 16 ? 9 : 10, FIXED = 31 - ID < 23 ? 31 - ID : 23;
     constexpr uint32_t LOW = (1u << ID) - 1;
     float steps = 0.f, spread = 0.f;   // steps of one; the largest magnitude, to whose rounding the scores are known
-    if (a.bias) {
+    if (by_bias) {
       uint32_t hi = 0, lo = 0xffffffffu;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -521,11 +562,11 @@ __device__ __forceinline__ void balanced_token(const BalancedRouteArgs& a, const
     uint32_t mine = ordered_keys<NV>(key, a.k + 1, lane, behind);
     if (lane >= a.k) mine = 0;
     if (mine) e = (int)(LOW - (mine & LOW));
-    if (a.bias || a.dtype == GT_FP32) {
+    if (by_bias || a.dtype == GT_FP32) {
       uint32_t after = __shfl_down_sync(0xffffffffu, mine, 1);
       if (lane + 1 >= a.k) after = behind;
       // scores: nearer than their errors, and two steps; logits: the same leading bits
-      const float apart = (float)((mine >> ID) - (after >> ID)), least = a.bias ? 2.f + steps * (2.f * err + 0x1p-21f * spread) : 0.f;
+      const float apart = (float)((mine >> ID) - (after >> ID)), least = by_bias ? 2.f + steps * (2.f * err + 0x1p-21f * spread) : 0.f;
       if (__any_sync(0xffffffffu, mine && after && !(apart > least))) {
         e = settle(a, tab, t, lane, e, kept, m, inv, err);
         doubt = __any_sync(0xffffffffu, e == UNSETTLED);
