@@ -107,14 +107,13 @@ __device__ __forceinline__ int register_lane(int r) {   // the s-th step, across
 }
 
 // the kept groups as bits: the best of lane g's score of group g (-inf: none), equal ones the lower first
-template <typename T>
-__device__ __forceinline__ unsigned kept_groups(T score, int groups, int keep, int lane) {
+__device__ __forceinline__ unsigned kept_groups(double score, int groups, int keep, int lane) {
   int rank = 0;
   for (int q = 0; q < groups; ++q) {
-    const T o = __shfl_sync(0xffffffffu, score, q);
+    const double o = __shfl_sync(0xffffffffu, score, q);
     rank += o > score || (o == score && q < lane);
   }
-  return __ballot_sync(0xffffffffu, lane < groups && rank < keep && score > (T)-INFINITY);
+  return __ballot_sync(0xffffffffu, lane < groups && rank < keep && score > -INFINITY);
 }
 
 // sum over the token's experts of e^(l - m), in 64 bits

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) rms_norm_kernel(
     store_row<NC, VEC>(const_cast<char*>(row(a.out, a.ldo, a.out_type)), a.out_type, a.H, tid, stride, h);
   if (a.out8) {
     const float scale = fmaxf(top * rstd * E4M3_INVERSE, LEAST_SCALE);
-    store_e4m3<NC, VEC>(a.out8 + t * a.ldo8, a.H, tid, stride, h, scale);
+    store_e4m3<NC>(a.out8 + t * a.ldo8, a.H, tid, stride, h, scale);
     if (tid == 0) a.scale[t] = scale;
   }
 }
@@ -241,9 +241,9 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) rms_norm_grad_ke
 }
 
 // Aligned rows of a block: two blocks an SM (one where two rows do not fit twice), the rows of dy, h and dsum copied ahead into a
-// ring of `stages` in shared memory, so that they arrive while the row before them waits for its sum.  8191 rows of 4096 (bf16 dy, fp32 h, dsum
-// and dh): 70 us, 0.98 of the memory's rate; one block of 512 threads an SM 78, rows loaded into registers 86.  Everything of a stage is read before the barrier of its row's sum, so
-// behind it the stage is filled again.
+// ring of `stages` in shared memory, so that they arrive while the row before them waits for its sum.  Everything of a stage is
+// read before the barrier of its row's sum, so behind it the stage is filled again.  8191 rows of 4096 (bf16 dy, fp32 h, dsum and dh): 70 us,
+// 0.98 of the memory's rate; with one block of 512 threads an SM 78, with rows loaded into registers 86.
 struct GradRing {
   int stages;
   uint32_t dy_bytes, h_bytes, dsum_bytes;   // of a row
@@ -378,7 +378,8 @@ __global__ void __launch_bounds__(512 / PER_SM, PER_SM) rms_norm_grad_ring_kerne
     }
 }
 
-// Aligned rows of up to WARP_H, a warp a row: the three rows' words loaded together, a row ahead.
+// Aligned rows of up to WARP_H, a warp a row: the three rows' words loaded together, a row ahead (10182 rows of 64: 24 us a call
+// with loads one after another, 13 so, 7.4 of them on the device).
 struct RawChunk {   // 8 elements of a type known at run time, as they lie
   uint32_t r[8];
   __device__ __forceinline__ void load(const void* row, int c, int type, bool in) {

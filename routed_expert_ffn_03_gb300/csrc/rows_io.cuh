@@ -1,7 +1,5 @@
 // rows_io.cuh - rows of bf16, fp16 or fp32 in registers as fp32, for the operators around the products.
 #pragma once
-#include <cuda_fp8.h>
-
 #include "common.cuh"
 #include "grouped.h"
 
@@ -9,11 +7,6 @@ namespace moe {
 
 constexpr int CHUNK = 8;   // elements of a 16-byte word of 16-bit values, the unit of aligned rows
 
-__device__ __forceinline__ float one_value(const void* p, long long i, int dtype) {
-  if (dtype == GT_FP32) return __ldcs(static_cast<const float*>(p) + i);
-  const uint16_t b = __ldcs(static_cast<const uint16_t*>(p) + i);
-  return dtype == GT_BF16 ? bf16_bits_to_float(b) : __half2float(__ushort_as_half(b));
-}
 __device__ __forceinline__ void put_value(void* p, long long i, int dtype, float v) {
   if (dtype == GT_FP32) static_cast<float*>(p)[i] = v;
   else if (dtype == GT_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
@@ -36,22 +29,21 @@ __device__ __forceinline__ float round_to(float v, int dtype) {
 }
 
 // A thread's values of a row.  Aligned rows: chunks tid + i * stride, 8 elements each; others: elements tid + j * stride.
-// Values past the row are `past`.
+// Values past the row are 0.
 template <int NC, bool VEC>
 __device__ __forceinline__ int element_of(int j, int tid, int stride) {
   return VEC ? (tid + (j / CHUNK) * stride) * CHUNK + j % CHUNK : tid + j * stride;
 }
 
 template <int NC, bool VEC>
-__device__ __forceinline__ void load_row(const void* row, int dtype, int H, int tid, int stride, float (&v)[NC * CHUNK],
-                                         float past = 0.f) {
+__device__ __forceinline__ void load_row(const void* row, int dtype, int H, int tid, int stride, float (&v)[NC * CHUNK]) {
   if (!VEC) {
     // the loads of a type stand together, as a branch around each would run them one after another
     auto all = [&](auto one) {
 #pragma unroll
       for (int j = 0; j < NC * CHUNK; ++j) {
         const int e = tid + j * stride;
-        v[j] = e < H ? one(e) : past;
+        v[j] = e < H ? one(e) : 0.f;
       }
     };
     if (dtype == GT_FP32) all([&](int e) { return __ldcs(static_cast<const float*>(row) + e); });
@@ -64,7 +56,7 @@ __device__ __forceinline__ void load_row(const void* row, int dtype, int H, int 
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = tid + i * stride;
-      float4 a = make_float4(past, past, past, past), b = a;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
       if (c < n) {
         a = __ldcs(static_cast<const float4*>(row) + 2 * c);
         b = __ldcs(static_cast<const float4*>(row) + 2 * c + 1);
@@ -84,12 +76,11 @@ __device__ __forceinline__ void load_row(const void* row, int dtype, int H, int 
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-    const bool in = tid + i * stride < n;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const float2 f = two_16(w[q], dtype);
-      v[i * CHUNK + 2 * q] = in ? f.x : past;
-      v[i * CHUNK + 2 * q + 1] = in ? f.y : past;
+      v[i * CHUNK + 2 * q] = f.x;
+      v[i * CHUNK + 2 * q + 1] = f.y;
     }
   }
 }
@@ -194,9 +185,6 @@ struct Divisor {
   }
 };
 // e4m3, to nearest, at most 448 (NaN stays NaN)
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
 __device__ __forceinline__ uint32_t e4m3_four(float a, float b, float c, float d) {
   uint32_t r;
   asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
@@ -207,23 +195,14 @@ __device__ __forceinline__ uint32_t e4m3_four(float a, float b, float c, float d
 __device__ __forceinline__ uint2 e4m3_chunk(const float* s, const Divisor& by) {
   return make_uint2(e4m3_four(by(s[0]), by(s[1]), by(s[2]), by(s[3])), e4m3_four(by(s[4]), by(s[5]), by(s[6]), by(s[7])));
 }
-template <int NC, bool VEC>
+// (element by element)
+template <int NC>
 __device__ __forceinline__ void store_e4m3(uint8_t* row, int H, int tid, int stride, const float (&v)[NC * CHUNK], float scale) {
   const Divisor q(scale);
-  if (!VEC) {
 #pragma unroll
-    for (int j = 0; j < NC * CHUNK; ++j) {
-      const int e = tid + j * stride;
-      if (e < H) row[e] = (uint8_t)e4m3_pair(q(v[j]), 0.f);
-    }
-    return;
-  }
-  const int n = H / CHUNK;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int c = tid + i * stride;
-    if (c >= n) break;
-    reinterpret_cast<uint2*>(row)[c] = e4m3_chunk(v + i * CHUNK, q);
+  for (int j = 0; j < NC * CHUNK; ++j) {
+    const int e = tid + j * stride;
+    if (e < H) row[e] = (uint8_t)e4m3_four(q(v[j]), 0.f, 0.f, 0.f);
   }
 }
 
