@@ -16,14 +16,19 @@ namespace {
 
 constexpr float E4M3_INVERSE = 1.f / 448.f;   // of the largest e4m3
 constexpr float LEAST_SCALE = 7.888609052210118e-31f;   // 2^-100: its inverse is a number, and a row of zeros stays zeros
+// (a row of zeros, times it, is to stay zeros)
+__device__ __forceinline__ float finite(float x) { return x == INFINITY ? 3.402823466e38f : x; }
 constexpr int ROW_WARPS = 8;                            // rows of a block where a warp takes a row
 
-// Sum of a and maximum of b over the row's threads: a warp, or the block.
-template <bool WARP>
+// Sum of a and maximum of b over the row's threads: LANES of a warp, or the block (0).
+template <int LANES>
 __device__ __forceinline__ void row_reduce(float& a, float& b) {
-  a = warp_sum(a);
-  b = warp_max(b);
-  if (WARP) return;
+#pragma unroll
+  for (int o = LANES ? LANES / 2 : 16; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+  }
+  if (LANES) return;
   __shared__ float2 part[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (lane == 0) part[warp] = make_float2(a, b);
@@ -63,7 +68,7 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) rms_norm_kernel(
   }
 #pragma unroll
   for (int j = 0; j < NC * CHUNK; ++j) top = fmaxf(top, fabsf(h[j]));
-  row_reduce<WARP>(ss, top);
+  row_reduce<WARP ? 32 : 0>(ss, top);
   if (a.norm) rstd = rsqrtf(ss / (float)a.H + a.eps);
   if (tid == 0 && a.rstd) a.rstd[t] = rstd;
 #pragma unroll
@@ -79,13 +84,16 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) rms_norm_kernel(
 
 // Aligned rows, types known: the row stays in registers as it lies (h in the type it was rounded to), half of what fp32 takes, so
 // that more of them are in flight; it is made fp32 twice instead.
-template <int XT, int HT, bool RES, int NC, bool WARP, int MAXT>
-__global__ void __launch_bounds__(MAXT) rms_norm_words_kernel(const NormArgs a) {
+template <int XT, int HT, bool RES, int NC, int LANES, int MAXT>
+__global__ void __launch_bounds__(MAXT, NC == 8 ? 2 : 1) rms_norm_words_kernel(const NormArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, stride = WARP ? 32 : blockDim.x;
-  const long long t = WARP ? (long long)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5) : blockIdx.x;
-  if (t >= a.T) return;   // whole warps
+  const int tid = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x, stride = LANES ? LANES : blockDim.x;
+  const long long at = LANES ? ((long long)blockIdx.x * (32 * ROW_WARPS) + threadIdx.x) / (LANES ? LANES : 1) : blockIdx.x;
+  if (LANES && at - (threadIdx.x & 31) / (LANES ? LANES : 1) >= a.T) return;   // whole warps
+  // (rows behind the last, in a warp that has others before them, are read as the last and not written)
+  const bool live = at < a.T;
+  const long long t = live ? at : a.T - 1;
   auto row = [&](const void* p, long long ld, int type) { return static_cast<const char*>(p) + t * ld * (type == GT_FP32 ? 4 : 2); };
   const int n = a.H / CHUNK;
   Word<true, HT> h[NC];
@@ -103,7 +111,7 @@ __global__ void __launch_bounds__(MAXT) rms_norm_words_kernel(const NormArgs a) 
 #pragma unroll
         for (int j = 0; j < CHUNK; ++j) v[j] = x[i].get(j) + h[i].get(j);
         h[i].set(v);
-        if (tid + i * stride < n) h[i].store(sum, tid + i * stride);
+        if (tid + i * stride < n && live) h[i].store(sum, tid + i * stride);
       }
     } else {
 #pragma unroll
@@ -141,11 +149,14 @@ __global__ void __launch_bounds__(MAXT) rms_norm_words_kernel(const NormArgs a) 
       }
     }
   }
-  row_reduce<WARP>(ss, top);
+  row_reduce<LANES>(ss, top);
+  if (LANES && !live) return;
   if (a.norm) rstd = rsqrtf(ss / (float)a.H + a.eps);
   if (tid == 0 && a.rstd) a.rstd[t] = rstd;
   const float scale = fmaxf(top * rstd * E4M3_INVERSE, LEAST_SCALE);
+  // rows as they are: the exact quotient, as 16-bit values often lie on a border; normalised: rstd and the scale in one factor
   const Divisor by(scale);
+  const float factor = finite(rstd * by.inv);
   if (tid == 0 && a.out8) a.scale[t] = scale;
   char* out = const_cast<char*>(row(a.out, a.ldo, a.out_type));
 #pragma unroll
@@ -154,12 +165,20 @@ __global__ void __launch_bounds__(MAXT) rms_norm_words_kernel(const NormArgs a) 
     if (c >= n) break;
     float v[CHUNK];
     scaled(i, v);
-    if (a.norm) {
+    if (a.out8) {
+      uint2* out8 = reinterpret_cast<uint2*>(a.out8 + t * a.ldo8);
+      if (a.norm) {
+        const float k = factor;
+        out8[c] = make_uint2(e4m3_four(v[0] * k, v[1] * k, v[2] * k, v[3] * k), e4m3_four(v[4] * k, v[5] * k, v[6] * k, v[7] * k));
+      } else {
+        out8[c] = e4m3_chunk(v, by);
+      }
+    }
+    if (a.out) {
 #pragma unroll
       for (int j = 0; j < CHUNK; ++j) v[j] *= rstd;
+      put_chunk(out, c, a.out_type, v);
     }
-    if (a.out) put_chunk(out, c, a.out_type, v);
-    if (a.out8) reinterpret_cast<uint2*>(a.out8 + t * a.ldo8)[c] = e4m3_chunk(v, by);
   }
 }
 
@@ -280,21 +299,23 @@ __global__ void __launch_bounds__(512 / PER_SM, PER_SM) rms_norm_grad_ring_kerne
   if (tid == 0)
     for (int s = 0; s < ring.stages; ++s)
       if (first + s * step < a.T) fill(first + s * step, s);
-  float dg[NC * CHUNK], g[NC * CHUNK];
+  constexpr bool KEEP = NC < 4;   // the gain stays in registers; more columns a thread leave no room for it
+  float dg[NC * CHUNK], kept[KEEP ? NC * CHUNK : 1];
+  auto gain = [&](int i, float (&v)[CHUNK]) {
 #pragma unroll
-  for (int j = 0; j < NC * CHUNK; ++j) {
-    dg[j] = 0.f;
-    g[j] = 1.f;
-  }
-  if (a.gain) {
+    for (int j = 0; j < CHUNK; ++j) v[j] = 1.f;
+    if (a.gain && tid + i * stride < n) chunk_of<false>(a.gain, tid + i * stride, a.gain_type, v);
+  };
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-      if (tid + i * stride < n) {
-        float v[CHUNK];
-        chunk_of<false>(a.gain, tid + i * stride, a.gain_type, v);
+  for (int i = 0; i < NC; ++i) {
+    if constexpr (KEEP) {
+      float v[CHUNK];
+      gain(i, v);
 #pragma unroll
-        for (int j = 0; j < CHUNK; ++j) g[i * CHUNK + j] = v[j];
-      }
+      for (int j = 0; j < CHUNK; ++j) kept[i * CHUNK + j] = v[j];
+    }
+#pragma unroll
+    for (int j = 0; j < CHUNK; ++j) dg[i * CHUNK + j] = 0.f;
   }
   int s = 0, turn = 0;
   uint32_t parity = 0;
@@ -310,9 +331,15 @@ __global__ void __launch_bounds__(512 / PER_SM, PER_SM) rms_norm_grad_ring_kerne
     for (int i = 0; i < NC; ++i) {
       const int c = tid + i * stride;
       if (c < n) {
-        float x[CHUNK], y[CHUNK];
+        float x[CHUNK], y[CHUNK], g[CHUNK];
         chunk_of<true>(at, c, a.dy_type, y);
         chunk_of<true>(at + ring.dy_bytes, c, a.h_type, x);
+        if constexpr (KEEP) {
+#pragma unroll
+          for (int j = 0; j < CHUNK; ++j) g[j] = kept[i * CHUNK + j];
+        } else {
+          gain(i, g);
+        }
         if (a.dsum) {
           const uint4* q = reinterpret_cast<const uint4*>(at + ring.dy_bytes + ring.h_bytes) + (a.dsum_type == GT_FP32 ? 2 * c : c);
           const uint4 lo = q[0], hi = a.dsum_type == GT_FP32 ? q[1] : lo;
@@ -325,7 +352,7 @@ __global__ void __launch_bounds__(512 / PER_SM, PER_SM) rms_norm_grad_ring_kerne
           const int k = i * CHUNK + j;
           nv[k] = x[j] * rstd;
           dg[k] = fmaf(y[j], nv[k], dg[k]);
-          d[k] = y[j] * g[k];
+          d[k] = y[j] * g[j];
           dot = fmaf(d[k], nv[k], dot);
         }
       }
@@ -562,9 +589,11 @@ cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
   }
   // A warp a row up to WARP_H, else a block: of few chunks a thread where there are fewer rows than SMs (latency), four otherwise.
   const bool warp = a.H <= WARP_H;
-  const bool few = a.T <= num_sms, eight = !few && !a.residual && a.x_type != GT_FP32 && a.H >= 4096;
+  const int lanes = a.H <= 64 ? 8 : a.H <= 128 ? 16 : 32;   // of a row, in a warp
+  const bool few = a.T <= num_sms, eight = !few && !a.norm && a.x_type != GT_FP32 && a.H >= 4096;
   const int nc = warp ? (a.H <= 256 ? 1 : a.H <= 512 ? 2 : 4) : few && a.H <= 8192 ? 1 : eight ? 8 : 4;
-  const long long blocks = warp ? ((long long)a.T + ROW_WARPS - 1) / ROW_WARPS : a.T;
+  const int rows = 32 * ROW_WARPS / lanes;
+  const long long blocks = warp ? ((long long)a.T + rows - 1) / rows : a.T;
   const int threads = warp ? 32 * ROW_WARPS : (a.H / CHUNK + nc * 32 - 1) / (nc * 32) * 32;
   auto types = [&](auto xt, auto ht, auto res) {
     auto go = [&](auto c, auto w, auto most) {
@@ -573,16 +602,20 @@ cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
                     blocks, threads, 0, s, a);
     };
     using W = integral_constant<int, 32 * ROW_WARPS>;
-    if (warp)
-      return nc == 1   ? go(integral_constant<int, 1>{}, True{}, W{})
-             : nc == 2 ? go(integral_constant<int, 2>{}, True{}, W{})
-                       : go(integral_constant<int, 4>{}, True{}, W{});
-    if (nc == 1) return go(integral_constant<int, 1>{}, False{}, integral_constant<int, 1024>{});
-    if constexpr (!decltype(res)::value && decltype(xt)::value != GT_FP32) {
-      if (nc == 8) return go(integral_constant<int, 8>{}, False{}, integral_constant<int, 512>{});
+    using Block = integral_constant<int, 0>;
+    if (warp) {
+      if (lanes == 8) return go(integral_constant<int, 1>{}, integral_constant<int, 8>{}, W{});
+      if (lanes == 16) return go(integral_constant<int, 1>{}, integral_constant<int, 16>{}, W{});
+      return nc == 1   ? go(integral_constant<int, 1>{}, integral_constant<int, 32>{}, W{})
+             : nc == 2 ? go(integral_constant<int, 2>{}, integral_constant<int, 32>{}, W{})
+                       : go(integral_constant<int, 4>{}, integral_constant<int, 32>{}, W{});
     }
-    return threads <= 512 ? go(integral_constant<int, 4>{}, False{}, integral_constant<int, 512>{})
-                          : go(integral_constant<int, 4>{}, False{}, integral_constant<int, 1024>{});
+    if (nc == 1) return go(integral_constant<int, 1>{}, Block{}, integral_constant<int, 1024>{});
+    if constexpr (!decltype(res)::value && decltype(xt)::value != GT_FP32) {   // (rows as they are)
+      if (nc == 8) return go(integral_constant<int, 8>{}, Block{}, integral_constant<int, 512>{});
+    }
+    return threads <= 512 ? go(integral_constant<int, 4>{}, Block{}, integral_constant<int, 512>{})
+                          : go(integral_constant<int, 4>{}, Block{}, integral_constant<int, 1024>{});
   };
   auto of = [](int type, auto f) {
     if (type == GT_FP32) return f(integral_constant<int, GT_FP32>{});
@@ -632,7 +665,7 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, const WaitLimit& wait, c
   GradRing ring{0, (uint32_t)(a.H * bytes_of(a.dy_type)), (uint32_t)(a.H * bytes_of(a.h_type)),
                 a.dsum ? (uint32_t)(a.H * bytes_of(a.dsum_type)) : 0u, wait};
   const size_t row = ring.dy_bytes + ring.h_bytes + ring.dsum_bytes;
-  const int per_sm = a.H <= 8192 && 2 * row <= ring_bytes(2) ? 2 : 1;
+  const int per_sm = a.H <= 4096 && 2 * row <= ring_bytes(2) ? 2 : 1;
   const size_t fit = ring_bytes(per_sm) / row;
   ring.stages = fit < RING_MAX ? (int)fit : RING_MAX;
   if (vec && a.H > WARP_H && a.H <= 16384 && ring.stages >= 2) {

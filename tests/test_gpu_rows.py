@@ -300,3 +300,27 @@ def test_rows_streams_and_capture(M):  # noqa: F811
     torch.cuda.synchronize()
     again = step()
     assert all((a == b).all() for a, b in zip(captured, again)) and not (again[0] == ref[0]).all()
+
+
+@pytest.mark.parametrize("T,H", [(1, 8), (5, 16), (33, 64), (4, 64), (17, 72), (31, 120), (1, 128), (35, 128), (600, 128), (3, 136)])
+def test_short_rows(M, T, H):  # noqa: F811
+    """Several rows a warp, whole warps and parts of the last; nothing behind the last row is written."""
+    import torch
+    x, r, g = make((T, H), "bf16", T), make((T, H), "bf16", 2), make((1, H), "bf16", 3)[0]
+    out, total = torch.full((T + 8, H), 7.0, device="cuda").bfloat16(), torch.full((T + 8, H), 7.0, device="cuda").bfloat16()
+    o8, scale = torch.full((T + 8, H), 7, dtype=torch.uint8, device="cuda"), torch.full((T + 8,), 7.0, device="cuda")
+    rstd = torch.full((T + 8,), 7.0, device="cuda")
+    n = M.Norm(out[:T], total[:T], rstd[:T], o8[:T].view(torch.float8_e4m3fn), scale[:T])
+    check_norm_call(M, x, r, g, out=n)
+    for t in (out, total, o8, scale, rstd):
+        assert (t[T:] == 7).all()
+    q, s = M.quantize_rows(x)
+    R.check_eight(f64(q.float()), f64(s), f64(x), 0.0)
+
+
+def test_zero_rows_under_a_small_eps(M):  # noqa: F811
+    import torch
+    for H in (64, 2048, 7168, 100):
+        x = torch.zeros(3, H, device="cuda").bfloat16()
+        n = M.rms_norm(x, eps=1e-30, want=("out", "out8"))
+        assert (n.out == 0).all() and (n.out8.view(torch.uint8) == 0).all() and (n.scale == 2.0 ** -100).all()
