@@ -250,7 +250,9 @@ moe_status moe_route_noalloc(const uint16_t* x_bf16, const float* W, int T, int 
  * pass of drafted tokens, a training step) and experts kept in bf16 or fp16: the router's
  * selection with the rows grouped by expert, the products of those ragged groups with their
  * experts' weights and the products' gradients, and the verification of drafted tokens
- * ("WISP - streaming what can't run", section "Speculative decoding": several drafted
+ * (and what stands around the products in a layer: the norm in front with an 8-bit output, routing with a bias for balance, products
+ * in 8 bits, the weighted sum of the experts' results, each with its gradient where a training step has one;
+ * "WISP - streaming what can't run", section "Speculative decoding": several drafted
  * tokens are verified in one parallel forward).
  *
  * Shared by these calls: no context; device pointers, on the current device; `stream` as
@@ -297,7 +299,8 @@ size_t moe_group_route_workspace(int T, int E, int k);
  *   one's); the `keep` groups of the largest scores stay (equal ones: the lower first), and of their experts the k of the largest c
  *   (equal ones: the lower first) are selected, in that order;
  *   w_j = scale s_j / sum over the selected of s (renormalize), or scale s_j.  The bias chooses, it is in no weight.
- * Comparisons are made as in 64 bits, whatever fp32 would round.  Logits of -inf and NaN, and biases of -inf and NaN, mask: such an
+ * Comparisons are made as in 64 bits, whatever fp32 would round; without a bias (or where all are 0) experts are in the order of their
+ * logits.  Logits of -inf and NaN, and biases of -inf and NaN, mask: such an
  * expert is never selected and counts in no group (a masked logit not in the softmax either); +inf counts as the largest finite float.
  * idx, weights, offsets, rows, pairs, T, E, k, ld and the workspace as moe_group_route; places [T][k] int32: where each pair stands
  * in the sorted order (pairs[places[t][j]] = t k + j), -1 where nothing was selected; moe_combine_rows reads results by it.
@@ -389,9 +392,10 @@ size_t moe_grouped_workspace(long long m, int k, int groups);
 /* moe_grouped_matmul of MOE_GROUP_NK weights in 8 bits: x and w hold e4m3 numbers (1 sign, 4 exponent, 3 mantissa bits, 448 at
  * most), x_scale [x_rows] and w_scale [groups][n] fp32 what one of them stands for in each row, as moe_quantize_rows makes them:
  *   out row of i = act(x_scale[r] w_scale[e][f] sum_k w[e][f][k] x[r][k])  for features f, r = rows[i] (or i).
- * Sums as there, of exact products; each is multiplied by its two scales in fp32 before the activation.
+ * Sums as there, of exact products, 32 at a time, in parts of 1024 elements or fewer for fp32 results, of 32768 or fewer for 16-bit
+ * ones: within 1e-6 of the sum of their absolute values.  Each is multiplied by its two scales in fp32 before the activation.
  * k, ldx, ldw and w_stride are multiples of 16, x and w 16-byte aligned, w_stride at least a matrix's extent (with one group it does not
- * matter); other limits, offsets, row numbers and out as there.  Rows named by number need the workspace, moe_grouped8_workspace bytes
+ * matter), x_rows at least 1 where m is; other limits, offsets, row numbers and out as there.  Rows named by number need the workspace, moe_grouped8_workspace bytes
  * (MOE_EINVAL without; 0 where the rows are so few that they are read where they are). */
 typedef struct {
     const void* x;
