@@ -269,8 +269,34 @@ struct GradRing {
   WaitLimit wait;
 };
 constexpr int RING_MAX = 8;
-template <int NC, int PER_SM>
-__global__ void __launch_bounds__(512 / PER_SM, PER_SM) rms_norm_grad_ring_kernel(const NormGradArgs a, const GradRing ring) {
+template <bool NARROW>
+struct RingWords {   // 8 elements as they lie, of 16 bits (NARROW) or a type known at run time
+  uint32_t r[NARROW ? 4 : 8];
+  __device__ __forceinline__ void load(const uint8_t* row, int c, int type) {
+    const uint4* p = reinterpret_cast<const uint4*>(row);
+    const bool wide = !NARROW && type == GT_FP32;
+    const uint4 lo = p[wide ? 2 * c : c];
+    r[0] = lo.x, r[1] = lo.y, r[2] = lo.z, r[3] = lo.w;
+    if constexpr (!NARROW) {
+      const uint4 hi = wide ? p[2 * c + 1] : lo;
+      r[4] = hi.x, r[5] = hi.y, r[6] = hi.z, r[7] = hi.w;
+    }
+  }
+  __device__ __forceinline__ void values(int type, float (&v)[CHUNK]) const {
+    if (!NARROW && type == GT_FP32) {
+#pragma unroll
+      for (int i = 0; i < CHUNK; ++i) v[i] = __uint_as_float(r[NARROW ? 0 : i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < CHUNK; ++i) {
+        const float2 f = two_16(r[i / 2], type);
+        v[i] = i % 2 ? f.y : f.x;
+      }
+    }
+  }
+};
+template <int NC, int PER_SM, int MAXT, bool NARROW, bool KEEP>
+__global__ void __launch_bounds__(MAXT, PER_SM) rms_norm_grad_ring_kernel(const NormGradArgs a, const GradRing ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float part[2][32];
   __shared__ uint64_t bars[RING_MAX];
@@ -299,24 +325,27 @@ __global__ void __launch_bounds__(512 / PER_SM, PER_SM) rms_norm_grad_ring_kerne
   if (tid == 0)
     for (int s = 0; s < ring.stages; ++s)
       if (first + s * step < a.T) fill(first + s * step, s);
-  constexpr bool KEEP = NC < 4;   // the gain stays in registers; more columns a thread leave no room for it
-  float dg[NC * CHUNK], kept[KEEP ? NC * CHUNK : 1];
-  auto gain = [&](int i, float (&v)[CHUNK]) {
+  // The gain: in registers, or behind the stages (it is read twice a row, and little of L1 is left to read it from).
+  uint4* gains = reinterpret_cast<uint4*>(smem + ring.stages * stage);
+  float kept[KEEP ? NC * CHUNK : 1];
+  if constexpr (KEEP) {
 #pragma unroll
-    for (int j = 0; j < CHUNK; ++j) v[j] = 1.f;
-    if (a.gain && tid + i * stride < n) chunk_of<false>(a.gain, tid + i * stride, a.gain_type, v);
-  };
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    if constexpr (KEEP) {
+    for (int i = 0; i < NC; ++i) {
       float v[CHUNK];
-      gain(i, v);
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) v[j] = 1.f;
+      if (a.gain && tid + i * stride < n) chunk_of<false>(a.gain, tid + i * stride, a.gain_type, v);
 #pragma unroll
       for (int j = 0; j < CHUNK; ++j) kept[i * CHUNK + j] = v[j];
     }
-#pragma unroll
-    for (int j = 0; j < CHUNK; ++j) dg[i * CHUNK + j] = 0.f;
+  } else {
+    if (a.gain)
+      for (int i = tid; i < n * (a.gain_type == GT_FP32 ? 2 : 1); i += stride) gains[i] = __ldg(static_cast<const uint4*>(a.gain) + i);
+    __syncthreads();
   }
+  float dg[NC * CHUNK];
+#pragma unroll
+  for (int j = 0; j < NC * CHUNK; ++j) dg[j] = 0.f;
   int s = 0, turn = 0;
   uint32_t parity = 0;
   float next_rstd = first < a.T ? __ldg(a.rstd + first) : 0.f;   // a row ahead, as all of the row waits for it
@@ -325,35 +354,35 @@ __global__ void __launch_bounds__(512 / PER_SM, PER_SM) rms_norm_grad_ring_kerne
     if (t + step < a.T) next_rstd = __ldg(a.rstd + t + step);
     if (!mbar_wait_bounded(smem_u32(bars + s), parity, ring.wait.cycles)) gave_up[turn] = 1;
     const uint8_t* at = smem + s * stage;
-    float nv[NC * CHUNK], d[NC * CHUNK], dot = 0.f;
-    Word<true, GT_FP32> ds[NC];   // as it lies
+    RingWords<NARROW> y[NC], h[NC], ds[NC];
+    float dot = 0.f;
+    // n and d of chunk i; made twice, as the words take half the registers (16-bit rows)
+    auto values = [&](int i, float (&yv)[CHUNK], float (&nv)[CHUNK], float (&d)[CHUNK]) {
+      y[i].values(a.dy_type, yv);
+      h[i].values(a.h_type, nv);
+      float g[CHUNK];
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) g[j] = KEEP ? kept[KEEP ? i * CHUNK + j : 0] : 1.f;
+      if (!KEEP && a.gain) chunk_of<true>(gains, tid + i * stride, a.gain_type, g);
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) {
+        nv[j] *= rstd;
+        d[j] = yv[j] * g[j];
+      }
+    };
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = tid + i * stride;
       if (c < n) {
-        float x[CHUNK], y[CHUNK], g[CHUNK];
-        chunk_of<true>(at, c, a.dy_type, y);
-        chunk_of<true>(at + ring.dy_bytes, c, a.h_type, x);
-        if constexpr (KEEP) {
-#pragma unroll
-          for (int j = 0; j < CHUNK; ++j) g[j] = kept[i * CHUNK + j];
-        } else {
-          gain(i, g);
-        }
-        if (a.dsum) {
-          const uint4* q = reinterpret_cast<const uint4*>(at + ring.dy_bytes + ring.h_bytes) + (a.dsum_type == GT_FP32 ? 2 * c : c);
-          const uint4 lo = q[0], hi = a.dsum_type == GT_FP32 ? q[1] : lo;
-          const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-          for (int j = 0; j < CHUNK; ++j) ds[i].r[j] = w[j];
-        }
+        y[i].load(at, c, a.dy_type);
+        h[i].load(at + ring.dy_bytes, c, a.h_type);
+        if (a.dsum) ds[i].load(at + ring.dy_bytes + ring.h_bytes, c, a.dsum_type);
+        float yv[CHUNK], nv[CHUNK], d[CHUNK];
+        values(i, yv, nv, d);
 #pragma unroll
         for (int j = 0; j < CHUNK; ++j) {
-          const int k = i * CHUNK + j;
-          nv[k] = x[j] * rstd;
-          dg[k] = fmaf(y[j], nv[k], dg[k]);
-          d[k] = y[j] * g[j];
-          dot = fmaf(d[k], nv[k], dot);
+          dg[i * CHUNK + j] = fmaf(yv[j], nv[j], dg[i * CHUNK + j]);
+          dot = fmaf(d[j], nv[j], dot);
         }
       }
     }
@@ -368,15 +397,14 @@ __global__ void __launch_bounds__(512 / PER_SM, PER_SM) rms_norm_grad_ring_kerne
     for (int i = 0; i < NC; ++i) {
       const int c = tid + i * stride;
       if (c < n) {
-        float v[CHUNK];
+        float v[CHUNK], yv[CHUNK], nv[CHUNK], d[CHUNK];
+        values(i, yv, nv, d);
 #pragma unroll
-        for (int j = 0; j < CHUNK; ++j) v[j] = rstd * fmaf(-nv[i * CHUNK + j], dot, d[i * CHUNK + j]);
+        for (int j = 0; j < CHUNK; ++j) v[j] = rstd * fmaf(-nv[j], dot, d[j]);
         if (a.dsum) {
+          ds[i].values(a.dsum_type, yv);
 #pragma unroll
-          for (int j = 0; j < CHUNK; ++j) {
-            const float2 f = two_16(ds[i].r[j / 2], a.dsum_type);
-            v[j] += a.dsum_type == GT_FP32 ? ds[i].get(j) : j % 2 ? f.y : f.x;
-          }
+          for (int j = 0; j < CHUNK; ++j) v[j] += yv[j];
         }
         put_chunk(out, c, a.dh_type, v);
       }
@@ -634,27 +662,33 @@ int norm_grad_blocks(int T, int H) {
 }
 
 namespace {
-constexpr size_t ring_bytes(int per_sm) { return (per_sm == 2 ? 108 : 216) * 1024; }
-template <int NC, int PER_SM>
-cudaError_t launch_ring(const NormGradArgs& a, GradRing r, int& blocks, cudaStream_t s) {
-  const int threads = (a.H / CHUNK + NC * 32 - 1) / (NC * 32) * 32, most = PER_SM * RING_SMS;
-  if (blocks > most) blocks = most;
-  return launch(rms_norm_grad_ring_kernel<NC, PER_SM>, blocks, threads, (size_t)r.stages * (r.dy_bytes + r.h_bytes + r.dsum_bytes), s, a, r);
-}
-template <int NC, int PER_SM>
-cudaError_t ring_attribute() {
-  return cudaFuncSetAttribute(rms_norm_grad_ring_kernel<NC, PER_SM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring_bytes(PER_SM));
-}
+constexpr size_t ring_bytes(int per_sm) { return (per_sm == 2 ? 110 : 226) * 1024; }
+// The kernels: chunks a thread, blocks an SM, most threads, rows all of 16 bits, the gain in registers.
+template <int NC, int PER_SM, int MAXT, bool NARROW, bool KEEP>
+struct Ring {
+  static cudaError_t attribute() {
+    return cudaFuncSetAttribute(rms_norm_grad_ring_kernel<NC, PER_SM, MAXT, NARROW, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)ring_bytes(PER_SM));
+  }
+  static cudaError_t launch_it(const NormGradArgs& a, const GradRing& r, int& blocks, cudaStream_t s) {
+    const int threads = (a.H / CHUNK + NC * 32 - 1) / (NC * 32) * 32, most = PER_SM * RING_SMS;
+    if (blocks > most) blocks = most;
+    return launch(rms_norm_grad_ring_kernel<NC, PER_SM, MAXT, NARROW, KEEP>, blocks, threads, (size_t)r.stages * (r.dy_bytes + r.h_bytes + r.dsum_bytes) + (a.gain && !KEEP ? a.H * bytes_of(a.gain_type) : 0), s, a, r);
+  }
+};
+using Ring2048 = Ring<1, 2, 256, false, true>;
+using Ring4096 = Ring<2, 2, 256, false, true>;
+using Ring7168Narrow = Ring<2, 2, 448, true, false>;
+using Ring8192 = Ring<2, 1, 512, false, true>;
+using Ring16384 = Ring<4, 1, 512, false, false>;
 }  // namespace
 
 cudaError_t rms_norm_set_attributes() {
-  cudaError_t e = ring_attribute<1, 2>();
-  if (e == cudaSuccess) e = ring_attribute<2, 2>();
-  if (e == cudaSuccess) e = ring_attribute<4, 2>();
-  if (e == cudaSuccess) e = ring_attribute<1, 1>();
-  if (e == cudaSuccess) e = ring_attribute<2, 1>();
-  if (e == cudaSuccess) e = ring_attribute<4, 1>();
-  return e;
+  cudaError_t e = Ring2048::attribute();
+  if (e == cudaSuccess) e = Ring4096::attribute();
+  if (e == cudaSuccess) e = Ring8192::attribute();
+  if (e == cudaSuccess) e = Ring7168Narrow::attribute();
+  return e == cudaSuccess ? Ring16384::attribute() : e;
 }
 
 cudaError_t launch_rms_norm_grad(const NormGradArgs& a, const WaitLimit& wait, cudaStream_t s) {
@@ -665,18 +699,18 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, const WaitLimit& wait, c
   GradRing ring{0, (uint32_t)(a.H * bytes_of(a.dy_type)), (uint32_t)(a.H * bytes_of(a.h_type)),
                 a.dsum ? (uint32_t)(a.H * bytes_of(a.dsum_type)) : 0u, wait};
   const size_t row = ring.dy_bytes + ring.h_bytes + ring.dsum_bytes;
-  const int per_sm = a.H <= 4096 && 2 * row <= ring_bytes(2) ? 2 : 1;
-  const size_t fit = ring_bytes(per_sm) / row;
+  const bool narrow = a.dy_type != GT_FP32 && a.h_type != GT_FP32 && (!a.dsum || a.dsum_type != GT_FP32);
+  const size_t gain = a.gain && a.H > (narrow ? 4096 : 8192) ? a.H * bytes_of(a.gain_type) : 0;   // (in shared memory)
+  const int per_sm = a.H <= (narrow ? 7168 : 4096) && 2 * row + gain <= ring_bytes(2) ? 2 : 1;
+  const size_t fit = (ring_bytes(per_sm) - gain) / row;   // (the gain takes 64 KB at most)
   ring.stages = fit < RING_MAX ? (int)fit : RING_MAX;
   if (vec && a.H > WARP_H && a.H <= 16384 && ring.stages >= 2) {
     if (per_sm == 2)
-      e = a.H <= 2048   ? launch_ring<1, 2>(a, ring, blocks, s)
-          : a.H <= 4096 ? launch_ring<2, 2>(a, ring, blocks, s)
-                        : launch_ring<4, 2>(a, ring, blocks, s);
+      e = a.H <= 2048   ? Ring2048::launch_it(a, ring, blocks, s)
+          : a.H <= 4096 ? Ring4096::launch_it(a, ring, blocks, s)
+                        : Ring7168Narrow::launch_it(a, ring, blocks, s);
     else
-      e = a.H <= 4096   ? launch_ring<1, 1>(a, ring, blocks, s)
-          : a.H <= 8192 ? launch_ring<2, 1>(a, ring, blocks, s)
-                        : launch_ring<4, 1>(a, ring, blocks, s);
+      e = a.H <= 8192 ? Ring8192::launch_it(a, ring, blocks, s) : Ring16384::launch_it(a, ring, blocks, s);
   } else if (vec && a.H <= WARP_H) {
     const size_t smem = a.dgain ? (size_t)ROW_WARPS * a.H * sizeof(float) : 0;   // 32 KB at most
     const int threads = 32 * ROW_WARPS;
