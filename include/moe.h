@@ -299,8 +299,8 @@ size_t moe_group_route_workspace(int T, int E, int k);
  *   one's); the `keep` groups of the largest scores stay (equal ones: the lower first), and of their experts the k of the largest c
  *   (equal ones: the lower first) are selected, in that order;
  *   w_j = scale s_j / sum over the selected of s (renormalize), or scale s_j.  The bias chooses, it is in no weight.
- * Comparisons are made as in 64 bits, whatever fp32 would round; without a bias (or where all are 0) experts are in the order of their
- * logits.  Logits of -inf and NaN, and biases of -inf and NaN, mask: such an
+ * Comparisons are made as in 64 bits, whatever fp32 would round; without a bias experts are in the order of their logits (and with
+ * biases that are all 0, unless scores saturate).  Logits of -inf and NaN, and biases of -inf and NaN, mask: such an
  * expert is never selected and counts in no group (a masked logit not in the softmax either); +inf counts as the largest finite float.
  * idx, weights, offsets, rows, pairs, T, E, k, ld and the workspace as moe_group_route; places [T][k] int32: where each pair stands
  * in the sorted order (pairs[places[t][j]] = t k + j), -1 where nothing was selected; moe_combine_rows reads results by it.

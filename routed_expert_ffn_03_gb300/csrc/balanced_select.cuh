@@ -406,6 +406,13 @@ __device__ __forceinline__ uint32_t ordered_keys(const uint32_t (&key)[NV], int 
   return mine;
 }
 
+// A group's score from its two largest.  Biases near the type's limits (the lowest value as a mask) would leave fp32 with it, and a
+// group at -inf counts as empty; those that meet at the limit are told apart in 64 bits, as any that are close.
+__device__ __forceinline__ float group_sum(float b1, float b2) {
+  constexpr float MOST = 3.402823466e38f;
+  return fminf(fmaxf(b1 + b2, -MOST), MOST);
+}
+
 // The selection of token t: lane j < k receives the j-th expert (-1: none) and its weight.  x: lane l's logits of experts
 // l + 32 i (-inf, NaN: masked; -inf past the experts).
 template <int NV>
@@ -468,7 +475,7 @@ __device__ __forceinline__ void balanced_token(const BalancedRouteArgs& a, const
       if (a.top2 && w1) {
         const int first = __ffs(__ballot_sync(0xffffffffu, b1 == w1)) - 1;
         const uint32_t w2 = __reduce_max_sync(0xffffffffu, lane == first ? b2 : b1);
-        if (w2) v += key_value(w2);
+        if (w2) v = group_sum(v, key_value(w2));
       }
       if (lane == g) score = v;
     };
@@ -485,7 +492,7 @@ __device__ __forceinline__ void balanced_token(const BalancedRouteArgs& a, const
       }
       if (lane < a.groups) {
         score = key_value(b1);
-        if (a.top2 && b2) score += key_value(b2);
+        if (a.top2 && b2) score = group_sum(score, key_value(b2));
       }
     } else {
       for (int g = 0; g < a.groups; ++g) {

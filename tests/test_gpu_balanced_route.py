@@ -113,6 +113,23 @@ def test_balanced_route_scores_a_rounding_apart(M, router, E, k, groups, keep): 
     check(M, torch.from_numpy((l + 20).astype(np.float32)).cuda(), k, torch.from_numpy(bias).cuda(), router, groups, keep, "top2")
 
 
+@pytest.mark.parametrize("router", [0, 1])
+@pytest.mark.parametrize("E,k,groups,keep", [(40, 10, 4, 2), (16, 12, 8, 7), (256, 32, 8, 3), (64, 6, 32, 5)])
+def test_balanced_route_biases_at_the_limits_of_fp32(M, router, E, k, groups, keep):  # noqa: F811
+    """Two such biases together are past fp32; the group counts all the same, behind (or before) the others."""
+    import torch
+    rng = np.random.default_rng(E)
+    lowest, l = float(np.finfo(np.float32).min), random_logits(64, E, "fp32")
+    l[1:, : E // 2][torch.from_numpy(rng.random((63, E // 2)) < 0.8).cuda()] = -np.inf   # few of the unmasked are left
+    bias = torch.zeros(E, device="cuda")
+    bias[E // 2:] = lowest
+    check(M, l, k, bias, router, groups, keep, "top2")
+    check(M, l, k, bias.flip(0), router, groups, keep, "top2")
+    check(M, l, k, -bias, router, groups, keep, "top2")
+    bias[:] = torch.from_numpy((rng.choice([1.0, 0.7, 0.5, -0.4], E) * lowest).astype(np.float32)).cuda()
+    check(M, l, k, bias, router, groups, keep, "top2")
+
+
 def test_balanced_route_rows_apart_workspace_and_refusals(M):  # noqa: F811
     import torch
     big = random_logits(1300, 50, "bf16")
