@@ -1,8 +1,8 @@
 // balanced_route.cu - router selection of a batch with a bias for balance and limits to groups of experts, pairs grouped by expert.
 //
-// As group_route.cu, with balanced_select.cuh's selection, a token a warp at a time.  Bound: issue while selecting, some 1100 instructions a
-// token: 16384 tokens of 256 bf16 logits in 8 groups of which 4 stay, k = 8, take 32 us for it and 11 for placing the pairs (the
-// logits and what is written 11 MB, 1.6 us at the memory's rate); one token 10 us.
+// As group_route.cu, with balanced_select.cuh's selection, a token a warp at a time.  Bound: issue while selecting, some 900 instructions a
+// token: 16384 tokens of 256 bf16 logits in 8 groups of which 4 stay, k = 8, take 26 us for it and 11 for placing the pairs (the
+// logits and what is written 11 MB, 1.6 us at the memory's rate); one token 7.5 us.
 #include "balanced_select.cuh"
 #include "group_sort.cuh"
 
