@@ -16,8 +16,6 @@ namespace {
 
 constexpr float E4M3_INVERSE = 1.f / 448.f;   // of the largest e4m3
 constexpr float LEAST_SCALE = 7.888609052210118e-31f;   // 2^-100: its inverse is a number, and a row of zeros stays zeros
-// (a row of zeros, times it, is to stay zeros)
-__device__ __forceinline__ float finite(float x) { return x == INFINITY ? 3.402823466e38f : x; }
 constexpr int ROW_WARPS = 8;                            // rows of a block where a warp takes a row
 
 // Sum of a and maximum of b over the row's threads: LANES of a warp, or the block (0).
@@ -154,9 +152,9 @@ __global__ void __launch_bounds__(MAXT, NC == 8 ? 2 : 1) rms_norm_words_kernel(c
   if (a.norm) rstd = rsqrtf(ss / (float)a.H + a.eps);
   if (tid == 0 && a.rstd) a.rstd[t] = rstd;
   const float scale = fmaxf(top * rstd * E4M3_INVERSE, LEAST_SCALE);
-  // rows as they are: the exact quotient, as 16-bit values often lie on a border; normalised: rstd and the scale in one factor
+  // the quotient itself: 16-bit values, and products of two, often lie on a border between two e4m3 numbers, where rstd and the scale
+  // in one factor give the wrong one (3 values in 10000 of a bf16 row without a gain)
   const Divisor by(scale);
-  const float factor = finite(rstd * by.inv);
   if (tid == 0 && a.out8) a.scale[t] = scale;
   char* out = const_cast<char*>(row(a.out, a.ldo, a.out_type));
 #pragma unroll
@@ -165,20 +163,12 @@ __global__ void __launch_bounds__(MAXT, NC == 8 ? 2 : 1) rms_norm_words_kernel(c
     if (c >= n) break;
     float v[CHUNK];
     scaled(i, v);
-    if (a.out8) {
-      uint2* out8 = reinterpret_cast<uint2*>(a.out8 + t * a.ldo8);
-      if (a.norm) {
-        const float k = factor;
-        out8[c] = make_uint2(e4m3_four(v[0] * k, v[1] * k, v[2] * k, v[3] * k), e4m3_four(v[4] * k, v[5] * k, v[6] * k, v[7] * k));
-      } else {
-        out8[c] = e4m3_chunk(v, by);
-      }
-    }
-    if (a.out) {
+    if (a.norm) {
 #pragma unroll
       for (int j = 0; j < CHUNK; ++j) v[j] *= rstd;
-      put_chunk(out, c, a.out_type, v);
     }
+    if (a.out8) reinterpret_cast<uint2*>(a.out8 + t * a.ldo8)[c] = e4m3_chunk(v, by);
+    if (a.out) put_chunk(out, c, a.out_type, v);
   }
 }
 
