@@ -393,7 +393,7 @@ size_t moe_grouped_workspace(long long m, int k, int groups);
  * most), x_scale [x_rows] and w_scale [groups][n] fp32 what one of them stands for in each row, as moe_quantize_rows makes them:
  *   out row of i = act(x_scale[r] w_scale[e][f] sum_k w[e][f][k] x[r][k])  for features f, r = rows[i] (or i).
  * Sums as there, of exact products, 32 at a time, in parts of 1024 elements or fewer for fp32 results, of 32768 or fewer for 16-bit
- * ones: within 1e-6 of the sum of their absolute values.  Each is multiplied by its two scales in fp32 before the activation.
+ * ones: within 1e-6 of the sum of their absolute values.  Each is multiplied in fp32 by w_scale, then by x_scale, before the activation.
  * k, ldx, ldw and w_stride are multiples of 16, x and w 16-byte aligned, w_stride at least a matrix's extent (with one group it does not
  * matter), x_rows at least 1 where m is; other limits, offsets, row numbers and out as there.  Rows named by number need the workspace, moe_grouped8_workspace bytes
  * (MOE_EINVAL without; 0 where the rows are so few that they are read where they are). */

@@ -278,11 +278,12 @@ __global__ void __launch_bounds__(GF_THREADS, 2)
         const float* ws = p.b_scale + (long long)e * p.n;
         const int g = f0 + 2 * j, h = min(g + 1, n_out - 1);   // (a feature past the last is not stored)
         if (g < n_out) {
-          v.x *= xs * __ldg(ws + g);
-          v.y *= xs * __ldg(ws + h);
+          // one after the other: the scales' own product may be past fp32 where the result is not
+          v.x = v.x * __ldg(ws + g) * xs;
+          v.y = v.y * __ldg(ws + h) * xs;
           if (SW) {
-            u.x *= xs * __ldg(ws + n_out + g);
-            u.y *= xs * __ldg(ws + n_out + h);
+            u.x = u.x * __ldg(ws + n_out + g) * xs;
+            u.y = u.y * __ldg(ws + n_out + h) * xs;
           }
         }
       }

@@ -543,9 +543,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GP_THREADS, 1)
         }
         const float col_scale = F8 ? xs[F8 ? q : 0] : 0.f;
         if (F8) {
-          // (with swiglu the columns' scales follow where a lane has its column's gate and up)
+          // one after the other, as the scales' own product may be past fp32 where the result is not (with swiglu the columns' follow
+          // where a lane has its column's gate and up)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= SW ? ws : ws * __shfl_sync(0xffffffffu, col_scale, i);
+          for (int i = 0; i < 32; ++i) {
+            v[i] *= ws;
+            if (!SW) v[i] *= __shfl_sync(0xffffffffu, col_scale, i);
+          }
         }
         if (WG) {
           // lane: row n of dw; columns: k
