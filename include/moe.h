@@ -363,10 +363,10 @@ moe_status moe_balanced_route_backward(const moe_balanced_route_grad_args* a, vo
  * them; with a workspace that is NULL or too small a slower kernel reads them where they are.  Calls that can overlap,
  * replays of graphs among them, need a workspace each.
  * Sums are fp32, rounded once to the result's type at the store.  The tensor core adds 16 products at a time to its
- * running sum and cuts the result off where fp32 would round it (about 2e-8 of it), so it runs over a part of the contracted
+ * running sum and cuts the result off where fp32 would round it (about 2e-8 of it, 2^-23 at most), so it runs over a part of the contracted
  * dimension only, and the parts are added with rounding to nearest: parts of 512 elements or fewer for fp32 results, of
  * 16384 or fewer for 16-bit ones.  So a sum of up to a million products is off by about 1e-6 (fp32) or 2e-5 (16 bits) of the
- * sum of their absolute values before it is rounded to its type. */
+ * sum of their absolute values before it is rounded to its type (4e-6 and 1.2e-4 where every step loses all that it can). */
 typedef struct {
     const void* x;
     const void* w;
@@ -393,7 +393,9 @@ size_t moe_grouped_workspace(long long m, int k, int groups);
  * most), x_scale [x_rows] and w_scale [groups][n] fp32 what one of them stands for in each row, as moe_quantize_rows makes them:
  *   out row of i = act(x_scale[r] w_scale[e][f] sum_k w[e][f][k] x[r][k])  for features f, r = rows[i] (or i).
  * Sums as there, of exact products, 32 at a time, in parts of 1024 elements or fewer for fp32 results, of 32768 or fewer for 16-bit
- * ones: within 1e-6 of the sum of their absolute values.  Each is multiplied in fp32 by w_scale, then by x_scale, before the activation.
+ * ones.  A step cuts off at most 2^-23 of the running sum and the addition of a part rounds by 2^-24, so with q parts of k elements a sum is
+ * off by at most (32 + q) 2^-23 (fp32) or (1024 + q) 2^-23 (16 bits: 1.2e-4, a quarter of an fp16 half step) of the sum of the absolute
+ * values, where every step loses all that it can (measured: 2e-6 and 8e-5); of random numbers, of one sign or not, by 1e-7 to 4e-7.  Each is multiplied in fp32 by w_scale, then by x_scale, before the activation.
  * k, ldx, ldw and w_stride are multiples of 16, x and w 16-byte aligned, w_stride at least a matrix's extent (with one group it does not
  * matter), x_rows at least 1 where m is; other limits, offsets, row numbers and out as there.  Rows named by number need the workspace, moe_grouped8_workspace bytes
  * (MOE_EINVAL without; 0 where the rows are so few that they are read where they are). */
