@@ -554,7 +554,9 @@ __device__ __forceinline__ void balanced_token(const BalancedRouteArgs& a, const
       const float base = key_logit(lo), range = key_logit(hi) - base;
       spread = fmaxf(fabsf(base), fabsf(key_logit(hi)));
       // (a range beyond fp32, or none: all keys the same)
-      steps = range > 1e-30f && range < 1e30f ? __fdividef((float)((1 << FIXED) - 2), range) : 0.f;
+      // (8 below the field's end: the quick division may be 2 steps of fp32 above the quotient, which is 2 of the field's, and a key past
+      // its end would be the least of all)
+      steps = range > 1e-30f && range < 1e30f ? __fdividef((float)((1 << FIXED) - 8), range) : 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const float c = __uint_as_float(key[i] ^ (~(uint32_t)((int)key[i] >> 31) | 0x80000000u));

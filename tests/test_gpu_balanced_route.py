@@ -260,3 +260,21 @@ def test_balanced_route_twins_beside_near_ones(M, router, groups, keep):  # noqa
     for k in (1, 2, 3, 4):
         check(M, logits, k, torch.from_numpy(bias).cuda(), router, groups, keep, "top2")
         check(M, logits, k, None, router, groups, keep, "top2")
+
+
+@pytest.mark.parametrize("router", [0, 1])
+@pytest.mark.parametrize("E", [8, 256, 300])
+def test_balanced_route_best_expert_over_many_ranges(M, router, E):  # noqa: F811
+    """The best score stands at the end of the range that keys are made of, another one for each token: it comes first."""
+    import torch
+    T = 1 << 20
+    logits, bias = random_logits(T, E, "fp32"), random_bias(E)
+    idx = M.balanced_route(logits, 2, bias=bias, router=router)[0]
+    for t in range(0, T, 1 << 17):
+        l = logits[t:t + (1 << 17)].double()
+        c = (torch.sigmoid(l) if router else torch.softmax(l, 1)) + bias.double()
+        top = c.topk(2, dim=1)
+        # (where 64-bit scores lie closer than their own rounding, 2^-50, either is right)
+        clear = top.values[:, 0] - top.values[:, 1] > 2.0 ** -45
+        assert torch.equal(idx[t:t + (1 << 17), 0][clear], top.indices[:, 0][clear].int())
+        assert int(clear.sum()) > (1 << 17) - 10
