@@ -182,6 +182,16 @@ def _pitch(stride, size, least):
     return stride if size > 1 or stride > least else least
 
 
+def _clear(t, stream):
+    """Zeros, in the order of the stream."""
+    if stream is None:
+        t.zero_()
+        return
+    s = _torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream
+    with _torch.cuda.stream(s):
+        t.zero_()
+
+
 def _new(stream, index, *wanted):
     """New tensors of the given (shape, dtype), belonging to the stream that will use them."""
     torch = _torch
@@ -258,7 +268,7 @@ def balanced_route(logits, k, bias=None, router=ROUTER_SOFTMAX, groups=1, keep=1
     scores are selected.  Weights are the scores without the bias (softmax over all experts, or sigmoid), divided by their sum over the
     selected with renormalize, times scale.  Returns (idx, weights, offsets, rows, pairs) as group_route and places [T, k] int32, each
     pair's row in the sorted order (-1: masked), which ``combine_rows`` reads by.  out: the six tensors to write instead of new
-    ones.  workspace: as for group_route."""
+    ones.  workspace: as for group_route.  Without tokens offsets is zeros."""
     torch, L = _start()
     dev = _cuda(logits, "logits")
     (T, E), stride = _dense(logits, "logits", 2, dev)
@@ -277,10 +287,13 @@ def balanced_route(logits, k, bias=None, router=ROUTER_SOFTMAX, groups=1, keep=1
         at = (_flat(idx, "out: idx", i32, TK, dev), _flat(weights, "out: weights", torch.float32, TK, dev),
               _flat(offsets, "out: offsets", i32, (E + 1,), dev), _flat(rows, "out: rows", i32, P, dev),
               _flat(pairs, "out: pairs", i32, P, dev), _flat(places, "out: places", i32, TK, dev))
+    bias_at = 0 if bias is None else _flat(bias, "bias", torch.float32, (E,), dev)
+    if T == 0:   # (of the outputs only offsets has elements)
+        _clear(out[2], stream)
+        return out
     ws, ws_bytes, _held = _space(workspace, _route_space(T, E, k), stream, dev)
     a = _pack_balanced(
-        logits.data_ptr(), 0 if bias is None else _flat(bias, "bias", torch.float32, (E,), dev), *at, _pitch(stride[0], T, E), T, E, k,
-        dt, router, groups, keep, score, bool(renormalize), scale, ws, ws_bytes)
+        logits.data_ptr(), bias_at, *at, _pitch(stride[0], T, E), T, E, k, dt, router, groups, keep, score, bool(renormalize), scale, ws, ws_bytes)
     _run("moe_balanced_route", L.moe_balanced_route, dev, stream, a)
     return out
 
@@ -302,10 +315,12 @@ def balanced_route_backward(dweights, logits, idx, router=ROUTER_SOFTMAX, renorm
     shape, o_stride = _dense(out, "out", 2, dev)
     if shape != (T, E) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out: %s %s, wanted %s" % (tuple(shape), out.dtype, (T, E)))
-    a = _pack_balanced_grad(
-        _flat(dweights, "dweights", torch.float32, TK, dev), logits.data_ptr(), _flat(idx, "idx", torch.int32, TK, dev), out.data_ptr(),
-        _pitch(stride[0], T, E), _pitch(o_stride[0], T, E), T, E, TK[1], dt, _type(out, "out"), router, bool(renormalize), scale)
-    _run("moe_balanced_route_backward", L.moe_balanced_route_backward, dev, stream, a)
+    dw_at, idx_at = _flat(dweights, "dweights", torch.float32, TK, dev), _flat(idx, "idx", torch.int32, TK, dev)
+    if T:
+        a = _pack_balanced_grad(
+            dw_at, logits.data_ptr(), idx_at, out.data_ptr(), _pitch(stride[0], T, E), _pitch(o_stride[0], T, E), T, E, TK[1], dt,
+            _type(out, "out"), router, bool(renormalize), scale)
+        _run("moe_balanced_route_backward", L.moe_balanced_route_backward, dev, stream, a)
     return out
 
 

@@ -278,3 +278,31 @@ def test_balanced_route_best_expert_over_many_ranges(M, router, E):  # noqa: F81
         clear = top.values[:, 0] - top.values[:, 1] > 2.0 ** -45
         assert torch.equal(idx[t:t + (1 << 17), 0][clear], top.indices[:, 0][clear].int())
         assert int(clear.sum()) > (1 << 17) - 10
+
+
+def test_balanced_route_without_tokens(M):  # noqa: F811
+    """An empty share of a batch goes through selection, products, sum and gradient as any other."""
+    import torch
+    H, F, E, k = 64, 48, 8, 2
+    x, wr = torch.empty(0, H, dtype=torch.bfloat16, device="cuda"), torch.randn(H, E, device="cuda")
+    w1, w2 = torch.randn(E, F, H, device="cuda").bfloat16(), torch.randn(E, H, F, device="cuda").bfloat16()
+    logits = x.float() @ wr
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, side, side.cuda_stream):
+        out = M.balanced_route(logits, k, bias=torch.zeros(E, device="cuda"), groups=4, keep=2, stream=stream)
+        idx, w, offsets, rows, pairs, places = out
+        torch.cuda.synchronize()
+        assert [tuple(t.shape) for t in out] == [(0, k), (0, k), (E + 1,), (0,), (0,), (0, k)]
+        assert [t.dtype for t in out] == [torch.int32, torch.float32] + [torch.int32] * 4 and (offsets == 0).all()
+    old = tuple(torch.full_like(t, 5) for t in out)
+    assert M.balanced_route(logits, k, out=old) is old and (old[2] == 0).all()
+    y = M.grouped_matmul(M.grouped_matmul(x, w1, offsets, rows=rows), w2, offsets)
+    assert M.combine_rows(y, w, places=places, residual=x).shape == (0, H)
+    dy, dw = M.combine_rows_backward(x, y, w, places=places)
+    dl = M.balanced_route_backward(dw, logits, idx)
+    assert dl.shape == (0, E) and dl.dtype == torch.float32 and dy.shape == (0, H)
+    with pytest.raises(ValueError):
+        M.balanced_route(logits, k, out=old[:5] + (old[5].long(),))
+    with pytest.raises(ValueError):
+        M.balanced_route_backward(dw.double(), logits, idx)
