@@ -461,7 +461,8 @@ int moe_grouped8_kernel(const moe_grouped8_args* a, int num_sms);
  * What is stored is what is normalised.  x, residual, gain and out each any moe_dtype; rows ldx, ld_residual, ld_sum, ldo, ldo8 apart.
  * sum may be the residual's own memory, out x's own, in the same layout and type.  Sums are fp32, each output is rounded once; h^2 has
  * to stay within fp32, and a row of zeros needs an eps above 0.  A NaN or infinity of x or the residual makes its row NaN (or 0 and
- * NaN), one of the gain its column.  T >= 0, H 1..32768; 8 elements at a time where H is a multiple of 8 and rows are 16-byte
+ * NaN), one of the gain its column; with out8 an infinity of the gain also makes scale infinite, and with it the row's out8 0 and NaN,
+ * wherever h is not 0 in that column.  T >= 0, H 1..32768; 8 elements at a time where H is a multiple of 8 and rows are 16-byte
  * aligned (out8: 8), one by one otherwise. */
 typedef struct {
     const void* x;
