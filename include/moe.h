@@ -527,7 +527,9 @@ typedef struct {
 moe_status moe_combine_rows(const moe_combine_args* a, void* stream);
 
 /* Its gradient (the residual's is dout itself): dy[places[t][j]] = weights[t][j] dout[t] in y's dtype, dweights[t][j] = <dout[t],
- * y[places[t][j]]> fp32, 0 for a place outside y.  No two pairs may name one row; rows of dy that none names are left as they were.  dy may be
+ * y[places[t][j]]> fp32, 0 for a place outside y.  A weight of 0 has its gradient as any other, so the row is read: of masked pairs whose
+ * rows were never written the place has to be outside y (moe_balanced_route's is), or, with places NULL, their dweights is whatever
+ * stands there (moe_balanced_route_backward does not use it).  No two pairs may name one row; rows of dy that none names are left as they were.  dy may be
  * y's own memory in the same layout. */
 typedef struct {
     const void* dout;

@@ -33,3 +33,23 @@ def test_gain_that_is_no_number(M, H):  # noqa: F811
     assert np.isinf(s[has]).all() and (q[has][:, rest] == 0).all() and np.isnan(q[has, 7]).all()
     assert np.isfinite(s[3]) and np.isnan(q[3, 7])
     R.check_eight(q[3:4, rest], s[3:4], y[3:4, rest], R.Y_TOL)
+
+
+def test_combine_rows_backward_of_masked_pairs(M):  # noqa: F811
+    """A weight of 0 has its gradient, the product with its row, as any other; a masked pair whose row was never written is named by
+    a place outside y, and has none."""
+    import torch
+    y, w, d = make((12, 72), "bf16", 1), make((4, 3), "fp32", 2), make((4, 72), "bf16", 3)
+    w[0, 1], w[2] = 0, 0
+    dy, dw = M.combine_rows_backward(d, y, w)
+    (rdy, written), dws = R.combine_grad_ref(f64(d), f64(y), f64(w), np.arange(12).reshape(4, 3))
+    B.check_close(dw, *dws, "fp32")
+    assert (f64(dw)[2] != 0).all() and (dy[6:9] == 0).all() and (dy[1] == 0).all()
+    y[6:9] = float("nan")                                             # never written
+    places = np.arange(12).reshape(4, 3)
+    places[2] = -1
+    dy, dw = M.combine_rows_backward(d, y, w, places=torch.from_numpy(places.astype(np.int32)).cuda(),
+                                     out=(torch.full_like(y, 7), torch.empty(4, 3, device="cuda")))
+    (rdy, written), dws = R.combine_grad_ref(f64(d), np.nan_to_num(f64(y)), f64(w), places)
+    B.check_close(dw, *dws, "fp32")
+    assert (dw[2] == 0).all() and (dy[6:9] == 7).all()
