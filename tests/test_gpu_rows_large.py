@@ -80,3 +80,24 @@ def test_products_of_far_rows_and_experts(M):  # noqa: F811
             got = out[i * per: (i + 1) * per].double()
             tol = B.sum_bound(k, wv.abs() @ xv.abs()) + B.HALF_STEP["fp32"] * (wv @ xv).abs()
             assert ((got - wv @ xv).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("H", [64, 1000, 1024, 2047, 4096, 7168, 8192])
+@pytest.mark.parametrize("sign", [False, True], ids=["random", "one sign"])
+def test_gain_gradient_over_many_rows(M, H, sign):  # noqa: F811
+    """Each block adds its rows in fp32, one after another: 921 of them at most (152 blocks), 8 warps' and 32 blocks' sums behind that, with a
+    product's two roundings each: (921 + 8 + 10 + 32 + 2) 2^-24 of the sum of the absolute products."""
+    import torch
+    rows = 140000
+    g = torch.Generator(device="cuda").manual_seed(H)
+    dy, h = (torch.randn(rows, H, generator=g, device="cuda").bfloat16() for _ in range(2))
+    if sign:
+        dy, h = dy.abs(), h.abs()
+    rstd = torch.rsqrt(h.float().square().mean(1) + 1e-6)
+    _, dgain = M.rms_norm_backward(dy, h, rstd, gain=torch.ones(H, device="cuda"))
+    want, absum = torch.zeros(H, dtype=torch.float64, device="cuda"), torch.zeros(H, dtype=torch.float64, device="cuda")
+    for t in range(0, rows, 20000):
+        p = dy[t:t + 20000].double() * h[t:t + 20000].double() * rstd[t:t + 20000, None].double()
+        want += p.sum(0)
+        absum += p.abs().sum(0)
+    assert bool(((dgain.double() - want).abs() <= 973 * R.U * absum + R.U * want.abs()).all())
