@@ -302,6 +302,8 @@ size_t moe_group_route_workspace(int T, int E, int k);
  * Comparisons are made as in 64 bits, whatever fp32 would round; without a bias experts are in the order of their logits (and with
  * biases that are all 0, unless scores saturate).  Logits of -inf and NaN, and biases of -inf and NaN, mask: such an
  * expert is never selected and counts in no group (a masked logit not in the softmax either); +inf counts as the largest finite float.
+ * Mask with -inf: a large negative bias (-1e9, the type's lowest) is ordered after the others too, but leaves the scores beside it so
+ * close together that each token is settled in 64 bits, which takes ten times as long.
  * idx, weights, offsets, rows, pairs, T, E, k, ld and the workspace as moe_group_route; places [T][k] int32: where each pair stands
  * in the sorted order (pairs[places[t][j]] = t k + j), -1 where nothing was selected; moe_combine_rows reads results by it.
  * groups 1..32, a divisor of E; keep 1..groups; k at most keep E / groups; scale finite. */
@@ -393,9 +395,10 @@ size_t moe_grouped_workspace(long long m, int k, int groups);
  * most), x_scale [x_rows] and w_scale [groups][n] fp32 what one of them stands for in each row, as moe_quantize_rows makes them:
  *   out row of i = act(x_scale[r] w_scale[e][f] sum_k w[e][f][k] x[r][k])  for features f, r = rows[i] (or i).
  * Sums as there, of exact products, 32 at a time, in parts of 1024 elements or fewer for fp32 results, of 32768 or fewer for 16-bit
- * ones.  A step cuts off at most 2^-23 of the running sum and the addition of a part rounds by 2^-24, so with q parts of k elements a sum is
- * off by at most (32 + q) 2^-23 (fp32) or (1024 + q) 2^-23 (16 bits: 1.2e-4, a quarter of an fp16 half step) of the sum of the absolute
- * values, where every step loses all that it can (measured: 2e-6 and 8e-5); of random numbers, of one sign or not, by 1e-7 to 4e-7.  Each is multiplied in fp32 by w_scale, then by x_scale, before the activation.
+ * ones.  A step cuts off at most 2^-23 of the running sum and the addition of a part rounds by 2^-24, so with q parts of k elements a sum
+ * is off by at most (32 + q) 2^-23 (fp32) or (1024 + q) 2^-23 (16 bits: 1.2e-4, a quarter of an fp16 half step) of the sum of the
+ * absolute values, where every step loses all that it can (measured: 2e-6 and 8e-5); of random numbers, of one sign or not, by 1e-7 to
+ * 4e-7.  Each is multiplied in fp32 by w_scale, then by x_scale, before the activation.
  * k, ldx, ldw and w_stride are multiples of 16, x and w 16-byte aligned, w_stride at least a matrix's extent (with one group it does not
  * matter), x_rows at least 1 where m is; other limits, offsets, row numbers and out as there.  Rows named by number need the workspace, moe_grouped8_workspace bytes
  * (MOE_EINVAL without; 0 where the rows are so few that they are read where they are). */
@@ -529,7 +532,8 @@ moe_status moe_combine_rows(const moe_combine_args* a, void* stream);
 /* Its gradient (the residual's is dout itself): dy[places[t][j]] = weights[t][j] dout[t] in y's dtype, dweights[t][j] = <dout[t],
  * y[places[t][j]]> fp32, 0 for a place outside y.  A weight of 0 has its gradient as any other, so the row is read: of masked pairs whose
  * rows were never written the place has to be outside y (moe_balanced_route's is), or, with places NULL, their dweights is whatever
- * stands there (moe_balanced_route_backward does not use it).  No two pairs may name one row; rows of dy that none names are left as they were.  dy may be
+ * stands there (moe_balanced_route_backward does not use it).  No two pairs may name one row; rows of dy that none names are left as
+ * they were.  dy may be
  * y's own memory in the same layout. */
 typedef struct {
     const void* dout;

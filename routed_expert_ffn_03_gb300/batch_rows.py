@@ -258,8 +258,8 @@ def combine_rows(y, weights, places=None, residual=None, out=None, out_dtype=Non
 def combine_rows_backward(dout, y, weights, places=None, out=None, stream=None):
     """The gradient of combine_rows (moe_combine_rows_backward): (dy [M, H] of y's type, dweights [T, k] fp32); that of the residual is
     dout itself.  A weight of 0 has its gradient too, so masked pairs whose rows were never written want a place outside y (gradient 0),
-    or their dweights is not to be used.  Rows of dy that no place names are left as they were (undefined in a new tensor).  out: the two tensors to write
-    instead of new ones; dy may be y itself."""
+    or their dweights is not to be used.  Rows of dy that no place names are left as they were (undefined in a new tensor).  out: the
+    two tensors to write instead of new ones; dy may be y itself."""
     torch, L = B._start()
     dev = _cuda(y, "y")
     (M, H), stride = _dense(y, "y", 2, dev)

@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) rms_norm_kernel(
 
 // Aligned rows, types known: the row stays in registers as it lies (h in the type it was rounded to), half of what fp32 takes, so
 // that more of them are in flight; it is made fp32 twice instead.
+// 8192 rows of 7168 (bf16, gain, 8 bits out): with a residual 69.5 us, 0.87 of the memory's rate; without 50, of which 24 instructions an
+// element fill 0.76 of the issue slots.
 template <int XT, int HT, bool RES, int NC, int LANES, int MAXT>
 __global__ void __launch_bounds__(MAXT, NC == 8 ? 2 : 1) rms_norm_words_kernel(const NormArgs a) {
   pdl_launch_dependents();
@@ -691,6 +693,7 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, const WaitLimit& wait, c
   const size_t row = ring.dy_bytes + ring.h_bytes + ring.dsum_bytes;
   const bool narrow = a.dy_type != GT_FP32 && a.h_type != GT_FP32 && (!a.dsum || a.dsum_type != GT_FP32);
   const size_t gain = a.gain && a.H > (narrow ? 4096 : 8192) ? a.H * bytes_of(a.gain_type) : 0;   // (in shared memory)
+  // (16-bit rows of 8192 would fit twice in shared memory, but leave 64 registers a thread of the 72 that 7168 takes: 160 bytes of spills)
   const int per_sm = a.H <= (narrow ? 7168 : 4096) && 2 * row + gain <= ring_bytes(2) ? 2 : 1;
   const size_t fit = (ring_bytes(per_sm) - gain) / row;   // (the gain takes 64 KB at most)
   ring.stages = fit < RING_MAX ? (int)fit : RING_MAX;
